@@ -20,7 +20,7 @@ from . import build as _build
 DTYPES = {"bf16": 0, "fp16": 1, "fp32": 2}
 MODES = {"auto": 0, "direct": 1, "atomic": 2, "deterministic": 3}
 STATUS = {0: "WG_OK", 1: "WG_ERR_INVALID_ARGUMENT", 2: "WG_ERR_NOT_SUPPORTED", 3: "WG_ERR_MISALIGNED",
-          4: "WG_ERR_WORKSPACE", 5: "WG_ERR_CUDA", 6: "WG_ERR_DEVICE_TIMEOUT"}
+          4: "WG_ERR_WORKSPACE", 5: "WG_ERR_CUDA", 6: "WG_ERR_DEVICE_TIMEOUT", 7: "WG_ERR_INVALID_TOKEN"}
 
 
 class WgProblem(ctypes.Structure):
@@ -36,6 +36,22 @@ class WgOptions(ctypes.Structure):
                 ("cluster", ctypes.c_int), ("kernel", ctypes.c_int)]
 
 
+class WgMuonProblem(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("rows", ctypes.c_int), ("cols", ctypes.c_int), ("ld", ctypes.c_longlong),
+                ("batch_stride", ctypes.c_longlong), ("grad_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int),
+                ("weight_dtype", ctypes.c_int), ("steps", ctypes.c_int), ("nesterov", ctypes.c_int),
+                ("coef", ctypes.POINTER(ctypes.c_float)), ("mu", ctypes.c_float), ("dampening", ctypes.c_float),
+                ("eps", ctypes.c_float), ("scale", ctypes.c_float), ("lr", ctypes.c_float),
+                ("weight_decay", ctypes.c_float)]
+
+
+class WgEmbeddingProblem(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_longlong), ("vocab", ctypes.c_int), ("dim", ctypes.c_int),
+                ("ld_table", ctypes.c_longlong), ("ld_out", ctypes.c_longlong), ("table_dtype", ctypes.c_int),
+                ("out_dtype", ctypes.c_int), ("token_bits", ctypes.c_int), ("padding_token", ctypes.c_int),
+                ("scale", ctypes.c_float)]
+
+
 class WgradError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{STATUS.get(status, status)}: {message}")
@@ -45,7 +61,8 @@ class WgradError(RuntimeError):
 EXPORTS = ("wg_problem_normalize", "wg_workspace_size", "wg_conv_bwd_weight", "wg_check_status",
            "wg_plan_string", "wg_status_string", "wg_last_error", "wg_conv_bwd_weight_noalloc",
            "wg_set_mark_event", "wg_conv_bwd_data", "wg_bwd_data_plan_string", "wg_bwd_data_workspace_size",
-           "wg_conv_bwd_weight_host", "wg_selftest_timeout")
+           "wg_conv_bwd_weight_host", "wg_selftest_timeout", "wg_muon_workspace_size", "wg_muon_plan_string",
+           "wg_muon_update", "wg_embedding_lookup", "wg_embedding_workspace_size", "wg_embedding_bwd_weight")
 
 _lib = None
 _lock = threading.Lock()
@@ -81,6 +98,14 @@ def load():
             lib.wg_bwd_data_workspace_size.argtypes = [P, ctypes.POINTER(ctypes.c_size_t)]
             lib.wg_bwd_data_plan_string.argtypes = [P, ctypes.c_char_p, ctypes.c_size_t]
             lib.wg_plan_string.argtypes = [P, O, ctypes.c_char_p, ctypes.c_size_t]
+            MP, EP = ctypes.POINTER(WgMuonProblem), ctypes.POINTER(WgEmbeddingProblem)
+            lib.wg_muon_workspace_size.argtypes = [MP, ctypes.POINTER(ctypes.c_size_t)]
+            lib.wg_muon_plan_string.argtypes = [MP, ctypes.c_char_p, ctypes.c_size_t]
+            lib.wg_muon_update.argtypes = [MP] + [ctypes.c_void_p] * 5 + [ctypes.c_size_t, ctypes.c_void_p]
+            lib.wg_embedding_lookup.argtypes = [EP] + [ctypes.c_void_p] * 4
+            lib.wg_embedding_workspace_size.argtypes = [EP, ctypes.POINTER(ctypes.c_size_t)]
+            lib.wg_embedding_bwd_weight.argtypes = [EP] + [ctypes.c_void_p] * 3 + [ctypes.c_int, ctypes.c_void_p,
+                                                                                   ctypes.c_size_t, ctypes.c_void_p]
             lib.wg_status_string.argtypes = [ctypes.c_int]
             lib.wg_status_string.restype = ctypes.c_char_p
             lib.wg_last_error.restype = ctypes.c_char_p
@@ -329,4 +354,211 @@ def conv_bwd_weight(spec: dict, x, dy, split_k: int = 0, mode: str = "auto", gro
     ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=x.device) if nbytes else None
     wg_conv_bwd_weight(spec, x, dy, out, split_k, mode, group_merge, ws, nbytes, stream, cluster=cluster,
                        kernel=kernel)
+    return out
+
+
+# ---------------------------------------------------------------- weight updates
+
+def make_muon_problem(spec: dict) -> WgMuonProblem:
+    """A spec is a dict: batch (default 1), rows, cols, and optionally ld, batch_stride (elements; 0 = packed),
+    grad_dtype, out_dtype, weight_dtype ('fp32' | 'bf16' | 'fp16'; defaults fp32, bf16, bf16), steps (5), coef (a list
+    of one (a, b, c) per step), eps (1e-7), scale (1), momentum (0.95), dampening (0), nesterov (True), lr (0),
+    weight_decay (0).  See include/wgrad.h for the formula."""
+    p = WgMuonProblem()
+    p.batch, p.rows, p.cols = spec.get("batch", 1), spec["rows"], spec["cols"]
+    p.ld, p.batch_stride = spec.get("ld", 0), spec.get("batch_stride", 0)
+    p.grad_dtype = DTYPES[spec.get("grad_dtype", "fp32")]
+    p.out_dtype = DTYPES[spec.get("out_dtype", "bf16")]
+    p.weight_dtype = DTYPES[spec.get("weight_dtype", "bf16")]
+    p.steps, p.nesterov = spec.get("steps", 5), int(spec.get("nesterov", True))
+    coef = spec.get("coef")
+    if coef is not None:
+        flat = [float(v) for step in coef for v in step]
+        if len(flat) != 3 * max(p.steps, 0):
+            raise ValueError("coef needs one (a, b, c) per step")
+        p.coef = (ctypes.c_float * max(len(flat), 1))(*flat)
+    p.mu, p.dampening = spec.get("momentum", 0.95), spec.get("dampening", 0.0)
+    p.eps, p.scale = spec.get("eps", 1e-7), spec.get("scale", 1.0)
+    p.lr, p.weight_decay = spec.get("lr", 0.0), spec.get("weight_decay", 0.0)
+    return p
+
+
+def _bytes_of(workspace, ws_bytes) -> int:
+    if ws_bytes is not None:
+        return int(ws_bytes)
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def wg_muon_workspace_size(spec: dict) -> int:
+    p, n = make_muon_problem(spec), ctypes.c_size_t(0)
+    _check(load().wg_muon_workspace_size(ctypes.byref(p), ctypes.byref(n)))
+    return int(n.value)
+
+
+def wg_muon_plan_string(spec: dict) -> str:
+    p, buf = make_muon_problem(spec), ctypes.create_string_buffer(1024)
+    _check(load().wg_muon_plan_string(ctypes.byref(p), buf, len(buf)))
+    return buf.value.decode()
+
+
+def wg_muon_update(spec: dict, grad, momentum=None, weight=None, out=None, workspace=None, ws_bytes: int | None = None,
+                   stream=None) -> None:
+    """The orthogonalised update of grad, with the momentum and the weight step where those are given."""
+    p = make_muon_problem(spec)
+    _check(load().wg_muon_update(ctypes.byref(p), _addr(grad), _addr(momentum), _addr(weight), _addr(out),
+                                 _addr(workspace), _bytes_of(workspace, ws_bytes), _stream_handle(stream)))
+
+
+class PreparedMuonUpdate:
+    """wg_muon_update with its arguments marshalled once: calling it makes one ctypes call.  Keeps
+    references to the tensors it was built from."""
+
+    def __init__(self, spec: dict, grad, momentum=None, weight=None, out=None, workspace=None,
+                 ws_bytes: int | None = None):
+        self._keep = (grad, momentum, weight, out, workspace)
+        self.p = make_muon_problem(spec)
+        self.fn = load().wg_muon_update
+        self.args = (ctypes.byref(self.p), *(ctypes.c_void_p(_addr(t)) for t in self._keep),
+                     ctypes.c_size_t(_bytes_of(workspace, ws_bytes)))
+
+    def __call__(self, stream_handle: int | None = None) -> None:
+        st = self.fn(*self.args, stream_handle)
+        if st:
+            _check(st)
+
+
+def _on(stream, *tensors):
+    """Tell torch's allocator that `tensors` (made on the current stream) are used on `stream`, so that their
+    memory is not handed out again while that stream still works on them."""
+    if stream is None:
+        return
+    import torch
+    s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+    for t in tensors:
+        t.record_stream(s)
+
+
+def _packed(**tensors):
+    for name, t in tensors.items():
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def muon_update(spec: dict, grad, momentum=None, weight=None, out=None, stream=None):
+    """Convenience wrapper over wg_muon_update for torch CUDA tensors: allocates the workspace, and `out`
+    (grad's shape) when no weight is given, then calls the library.  Returns out, or the weight."""
+    import torch
+    if out is None and weight is None:
+        tdt = {"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16}[spec.get("out_dtype", "bf16")]
+        out = torch.empty_like(grad, dtype=tdt)
+    if not (spec.get("ld", 0) or spec.get("batch_stride", 0)):
+        _packed(grad=grad, momentum=momentum, weight=weight, out=out)
+    nbytes = wg_muon_workspace_size(spec)
+    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=grad.device)
+    _on(stream, ws)
+    wg_muon_update(spec, grad, momentum, weight, out, ws, nbytes, stream)
+    return out if out is not None else weight
+
+
+def make_embedding_problem(spec: dict) -> WgEmbeddingProblem:
+    """A spec is a dict: tokens, vocab, dim, and optionally ld_table, ld_out (elements; 0 = dim), table_dtype,
+    out_dtype ('fp32' | 'bf16' | 'fp16'; default bf16), token_dtype ('i32' | 'i64'; default i64), scale (1),
+    padding_token (-1 = none)."""
+    p = WgEmbeddingProblem()
+    p.tokens, p.vocab, p.dim = spec["tokens"], spec["vocab"], spec["dim"]
+    p.ld_table, p.ld_out = spec.get("ld_table", 0), spec.get("ld_out", 0)
+    p.table_dtype = DTYPES[spec.get("table_dtype", "bf16")]
+    p.out_dtype = DTYPES[spec.get("out_dtype", "bf16")]
+    p.token_bits = {"i32": 32, "i64": 64}[spec.get("token_dtype", "i64")]
+    p.padding_token, p.scale = spec.get("padding_token", -1), spec.get("scale", 1.0)
+    return p
+
+
+def wg_embedding_lookup(spec: dict, token, table, out, stream=None) -> None:
+    """out[t] = scale * table[token[t]]."""
+    p = make_embedding_problem(spec)
+    _check(load().wg_embedding_lookup(ctypes.byref(p), _addr(token), _addr(table), _addr(out), _stream_handle(stream)))
+
+
+def wg_embedding_workspace_size(spec: dict) -> int:
+    p, n = make_embedding_problem(spec), ctypes.c_size_t(0)
+    _check(load().wg_embedding_workspace_size(ctypes.byref(p), ctypes.byref(n)))
+    return int(n.value)
+
+
+def wg_embedding_bwd_weight(spec: dict, token, dy, dtable, accumulate: bool = False, workspace=None,
+                            ws_bytes: int | None = None, stream=None) -> None:
+    """dtable[v] = (accumulate ? dtable[v] : 0) + scale * sum of dy[t] over the t with token[t] = v."""
+    p = make_embedding_problem(spec)
+    _check(load().wg_embedding_bwd_weight(ctypes.byref(p), _addr(token), _addr(dy), _addr(dtable), int(accumulate),
+                                          _addr(workspace), _bytes_of(workspace, ws_bytes), _stream_handle(stream)))
+
+
+class PreparedEmbeddingLookup:
+    """wg_embedding_lookup with its arguments marshalled once."""
+
+    def __init__(self, spec: dict, token, table, out):
+        self._keep = (token, table, out)
+        self.p = make_embedding_problem(spec)
+        self.fn = load().wg_embedding_lookup
+        self.args = (ctypes.byref(self.p), *(ctypes.c_void_p(_addr(t)) for t in self._keep))
+
+    def __call__(self, stream_handle: int | None = None) -> None:
+        st = self.fn(*self.args, stream_handle)
+        if st:
+            _check(st)
+
+
+class PreparedEmbeddingBwd:
+    """wg_embedding_bwd_weight with its arguments marshalled once."""
+
+    def __init__(self, spec: dict, token, dy, dtable, accumulate: bool = False, workspace=None,
+                 ws_bytes: int | None = None):
+        self._keep = (token, dy, dtable, workspace)
+        self.p = make_embedding_problem(spec)
+        self.fn = load().wg_embedding_bwd_weight
+        self.args = (ctypes.byref(self.p), *(ctypes.c_void_p(_addr(t)) for t in (token, dy, dtable)),
+                     ctypes.c_int(int(accumulate)), ctypes.c_void_p(_addr(workspace)),
+                     ctypes.c_size_t(_bytes_of(workspace, ws_bytes)))
+
+    def __call__(self, stream_handle: int | None = None) -> None:
+        st = self.fn(*self.args, stream_handle)
+        if st:
+            _check(st)
+
+
+def _embedding_spec(token, vocab, dim, table_dtype, out_dtype, scale, padding_token):
+    names = {"torch.float32": "fp32", "torch.bfloat16": "bf16", "torch.float16": "fp16"}
+    return {"tokens": token.numel(), "vocab": vocab, "dim": dim, "table_dtype": names[str(table_dtype)],
+            "out_dtype": names[str(out_dtype)], "token_dtype": {"torch.int32": "i32", "torch.int64": "i64"}[
+                str(token.dtype)], "scale": scale, "padding_token": padding_token}
+
+
+def embedding_lookup(token, table, scale: float = 1.0, out=None, stream=None):
+    """Convenience wrapper over wg_embedding_lookup for torch CUDA tensors: contiguous int32 or int64 tokens of any
+    shape, a contiguous (vocab, dim) table.  Returns (*token.shape, dim) in table's dtype (or `out`)."""
+    import torch
+    if out is None:
+        out = torch.empty((*token.shape, table.shape[1]), dtype=table.dtype, device=table.device)
+    _packed(token=token, table=table, out=out)
+    spec = _embedding_spec(token, table.shape[0], table.shape[1], table.dtype, out.dtype, scale, -1)
+    wg_embedding_lookup(spec, token, table, out, stream)
+    return out
+
+
+def embedding_bwd_weight(token, dy, vocab: int, scale: float = 1.0, padding_token: int = -1, out=None,
+                         accumulate: bool = False, stream=None):
+    """Convenience wrapper over wg_embedding_bwd_weight for torch CUDA tensors: contiguous dy of shape
+    (*token.shape, dim).  Returns the (vocab, dim) gradient in dy's dtype (or `out`, added to when accumulate)."""
+    import torch
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = torch.empty((vocab, dy.shape[-1]), dtype=dy.dtype, device=dy.device)
+    _packed(token=token, dy=dy, out=out)
+    spec = _embedding_spec(token, vocab, dy.shape[-1], out.dtype, dy.dtype, scale, padding_token)
+    nbytes = wg_embedding_workspace_size(spec)
+    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dy.device)
+    _on(stream, ws)
+    wg_embedding_bwd_weight(spec, token, dy, out, accumulate, ws, nbytes, stream)
     return out

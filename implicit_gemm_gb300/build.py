@@ -18,9 +18,10 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIBDIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(LIBDIR, "libwgrad.so")
-SOURCES = [os.path.join(CSRC, "wgrad.cu"), os.path.join(CSRC, "plan.cpp")]
-DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("ptx.cuh", "k_igemm.cuh", "k_depthwise.cuh", "k_dgrad.cuh", "plan.h")] + [
-    os.path.join(ROOT, "include", "wgrad.h")]
+SOURCES = [os.path.join(CSRC, f) for f in ("wgrad.cu", "update.cu", "plan.cpp")]
+DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("ptx.cuh", "vec.cuh", "host.h", "k_igemm.cuh", "k_igemm_pair.cuh",
+                                                  "k_depthwise.cuh", "k_dgrad.cuh", "k_muon.cuh", "k_embedding.cuh",
+                                                  "plan.h")] + [os.path.join(ROOT, "include", "wgrad.h")]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 _lock = threading.Lock()
 
@@ -46,7 +47,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         os.makedirs(LIBDIR, exist_ok=True)
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nvcc(), ARCH, "-lineinfo", "-O3", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
-               "-Xcompiler", "-fvisibility=hidden", "-shared", "-I", os.path.join(ROOT, "include"), "-o", tmp,
+               "-Xcompiler", "-fvisibility=hidden", "-shared", "--threads", "0", "-I", os.path.join(ROOT, "include"), "-o", tmp,
                *SOURCES]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")

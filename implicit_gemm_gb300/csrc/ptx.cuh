@@ -10,10 +10,12 @@ namespace wg {
 
 // Device status word: bit 0 = a bounded wait ran out; bit 1 = a kernel
 // instance was launched for a plan it is not compiled for (an internal
-// error).  Read and cleared by wg_check_status on the host.
-__device__ unsigned int g_status;
+// error); bit 2 = a token outside the embedding table.  Read and cleared by
+// wg_check_status on the host.  One word per translation unit.
+static __device__ unsigned int g_status;
 constexpr unsigned int kStatusTimeout = 1u;
 constexpr unsigned int kStatusBadPlan = 2u;
+constexpr unsigned int kStatusBadToken = 4u;
 
 // Upper bound of any single wait, in nanoseconds of %globaltimer.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;

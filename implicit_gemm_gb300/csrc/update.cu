@@ -1,0 +1,394 @@
+// Weight updates of the C ABI (declared in include/wgrad.h): the orthogonalised
+// update and the embedding table's lookup and gradient.  Validation, workspace
+// layout and launches; no device memory is allocated here.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdio.h>
+#include <string.h>
+
+#include <algorithm>
+#include <string>
+
+#include "../../include/wgrad.h"
+#include "host.h"
+#include "k_embedding.cuh"
+#include "k_muon.cuh"
+
+namespace wg {
+
+cudaError_t take_update_status(unsigned int* v)
+{
+    cudaError_t e = cudaMemcpyFromSymbol(v, g_status, sizeof *v);
+    const unsigned int zero = 0;
+    if (e == cudaSuccess && *v) e = cudaMemcpyToSymbol(g_status, &zero, sizeof zero);
+    return e;
+}
+
+}  // namespace wg
+
+namespace {
+
+using wg::aligned16;
+using wg::cuda_fail;
+using wg::num_sms;
+using wg::set_err;
+
+int esize(int dtype) { return dtype == WG_FP32 ? 4 : 2; }
+bool dtype_ok(int d) { return d == WG_FP32 || d == WG_BF16 || d == WG_FP16; }
+bool aligned_to(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) == 0; }
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+template <typename... P, typename... A>
+int launch(const char* what, void (*k)(P...), dim3 grid, dim3 block, int smem, cudaStream_t stream, A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    unsigned na = 0;
+    wg::pdl_config(&cfg, attr, &na, stream);
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = (size_t)smem;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k, args...);
+    return e == cudaSuccess ? WG_OK : cuda_fail(what, e);
+}
+
+int check_workspace(size_t need, const void* workspace, size_t ws_bytes)
+{
+    if (need == 0) return WG_OK;
+    if (!workspace || ws_bytes < need) {
+        char buf[160];
+        snprintf(buf, sizeof buf, "workspace of %zu bytes needed (got %zu%s)", need, ws_bytes, workspace ? "" : ", NULL");
+        return set_err(WG_ERR_WORKSPACE, buf);
+    }
+    if (!aligned16(workspace)) return set_err(WG_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+    return WG_OK;
+}
+
+// ---------------------------------------------------------------- orthogonalised update
+constexpr int kMuonMaxDim = 32768, kMuonMaxSteps = 16, kMuonMaxParts = 304;
+
+struct MuonPlan {
+    wg_muon_problem p;
+    float coef[kMuonMaxSteps][3];
+    int ldx, m, ldm, nparts;
+    size_t off_x[2], off_xlo, off_a, off_b, off_part, bytes;
+};
+
+// Largest value over s in [0, smax] of what a step (a, b, c) makes of a singular
+// value s, and of |b s^2 + c s^4|, on a grid fine enough for a quintic.
+void step_range(const float* k, double smax, double* grown, double* poly)
+{
+    *grown = *poly = 0.0;
+    for (int i = 0; i <= 4096; ++i) {
+        const double s = smax * i / 4096, l = s * s, q = k[1] * l + k[2] * l * l;
+        *grown = std::max(*grown, fabs(s * (k[0] + q)));
+        *poly = std::max(*poly, fabs(q));
+    }
+}
+
+int muon_plan(const wg_muon_problem* p, MuonPlan* pl)
+{
+    if (!p) return set_err(WG_ERR_INVALID_ARGUMENT, "problem is NULL");
+    if (p->batch < 1 || p->rows < 1 || p->cols < 1)
+        return set_err(WG_ERR_INVALID_ARGUMENT, "batch, rows and cols must be at least 1");
+    if (p->rows > kMuonMaxDim || p->cols > kMuonMaxDim || p->batch > 65535)
+        return set_err(WG_ERR_NOT_SUPPORTED, "rows and cols up to 32768 and batch up to 65535 are supported");
+    if (!dtype_ok(p->grad_dtype) || !dtype_ok(p->out_dtype) || !dtype_ok(p->weight_dtype))
+        return set_err(WG_ERR_INVALID_ARGUMENT, "grad_dtype, out_dtype and weight_dtype must be WG_FP32, WG_BF16 or WG_FP16");
+    if (p->steps < 0 || p->steps > kMuonMaxSteps) return set_err(WG_ERR_INVALID_ARGUMENT, "steps must be 0..16");
+    if (!(p->mu >= 0.f && p->mu < 1.f) || !(p->dampening >= 0.f && p->dampening <= 1.f) || !(p->eps >= 0.f) ||
+        !isfinite(p->eps) || !isfinite(p->scale) || !isfinite(p->lr) || !isfinite(p->weight_decay))
+        return set_err(WG_ERR_INVALID_ARGUMENT, "mu must be in [0, 1), dampening in [0, 1], eps >= 0, and every factor finite");
+    pl->p = *p;
+    wg_muon_problem& q = pl->p;
+    if (q.ld == 0) q.ld = q.cols;
+    if (q.batch_stride == 0) q.batch_stride = (long long)q.rows * q.ld;
+    // Matrices after one another, or side by side (a matrix per head of a fused weight).
+    const bool apart = q.batch_stride >= (long long)(q.rows - 1) * q.ld + q.cols;
+    const bool beside = q.batch_stride >= q.cols && q.ld >= (long long)(q.batch - 1) * q.batch_stride + q.cols;
+    if (q.ld < q.cols || (q.batch > 1 && !apart && !beside))
+        return set_err(WG_ERR_INVALID_ARGUMENT, "ld or batch_stride makes rows overlap");
+    static const float kDefault[3] = {3.4445f, -4.7750f, 2.0315f};
+    double smax = 1.0;
+    for (int i = 0; i < q.steps; ++i) {
+        memcpy(pl->coef[i], q.coef ? q.coef + 3 * i : kDefault, sizeof kDefault);
+        const float* k = pl->coef[i];
+        if (!isfinite(k[0]) || !isfinite(k[1]) || !isfinite(k[2]))
+            return set_err(WG_ERR_INVALID_ARGUMENT, "coef must be finite");
+        double grown, poly;
+        step_range(pl->coef[i], smax, &grown, &poly);
+        if (!(grown <= 4.0) || !(poly <= 48.0))
+            return set_err(WG_ERR_INVALID_ARGUMENT, "coef lets a singular value grow above 4");
+        smax = std::max(grown, 1e-3);
+    }
+    q.coef = nullptr;
+    pl->m = std::min(q.rows, q.cols);
+    pl->ldx = (q.cols + 7) / 8 * 8;
+    pl->ldm = (pl->m + 7) / 8 * 8;
+    const long long n = (long long)q.rows * q.cols;
+    pl->nparts = (int)std::max(1LL, std::min<long long>(kMuonMaxParts, (n + 2047) / 2048));
+    const size_t x = up256((size_t)q.batch * q.rows * pl->ldx * 2), a = up256((size_t)q.batch * pl->m * pl->ldm * 2);
+    size_t o = 0;
+    pl->off_part = o, o += up256((size_t)q.batch * pl->nparts * 4);
+    if (q.steps > 0) {
+        pl->off_x[0] = o, o += x;
+        pl->off_x[1] = o, o += x;
+        pl->off_xlo = o, o += x;
+        pl->off_a = o, o += a;
+        pl->off_b = o, o += a;
+    }
+    pl->bytes = o;
+    return WG_OK;
+}
+
+int muon_run(const MuonPlan& pl, const void* grad, void* momentum, void* weight, void* out, char* ws, cudaStream_t s)
+{
+    const wg_muon_problem& q = pl.p;
+    wg::MuonParams p = {};
+    p.batch = q.batch, p.rows = q.rows, p.cols = q.cols, p.ld = q.ld, p.bs = q.batch_stride;
+    p.grad = grad, p.mom = static_cast<float*>(momentum), p.weight = weight, p.out = out;
+    p.grad_dtype = q.grad_dtype, p.out_dtype = q.out_dtype, p.weight_dtype = q.weight_dtype;
+    p.nesterov = q.nesterov, p.mu = q.mu, p.gain = 1.f - q.dampening, p.eps = q.eps;
+    p.scale = q.scale, p.keep = 1.f - q.lr * q.weight_decay, p.lr = q.lr;
+    p.ldx = pl.ldx, p.m = pl.m, p.ldm = pl.ldm;
+    p.xs = (long long)q.rows * pl.ldx, p.ms = (long long)pl.m * pl.ldm;
+    p.part = reinterpret_cast<float*>(ws + pl.off_part), p.nparts = pl.nparts;
+    if (q.steps > 0) {
+        for (int i = 0; i < 2; ++i) p.x[i] = reinterpret_cast<__half*>(ws + pl.off_x[i]);
+        p.xlo = reinterpret_cast<__half*>(ws + pl.off_xlo);
+        p.a = reinterpret_cast<__half*>(ws + pl.off_a), p.b = reinterpret_cast<__half*>(ws + pl.off_b);
+    }
+    const dim3 egrid(pl.nparts, q.batch);
+    int st = launch("muon_momentum_kernel launch", wg::muon_momentum_kernel, egrid, dim3(256), 0, s, p);
+    if (!st) st = launch("muon_normalize_kernel launch", wg::muon_normalize_kernel, egrid, dim3(256), 0, s, p, (int)(q.steps == 0));
+    const bool wide = q.rows <= q.cols;
+    const unsigned tm = (pl.m + 63) / 64, tr = (q.rows + 63) / 64, tc = (q.cols + 63) / 64;
+    for (int i = 0; i < q.steps && !st; ++i) {
+        const int in = i & 1;
+        wg::MuonGemm g = {};
+        g.a = pl.coef[i][0], g.b = pl.coef[i][1], g.c = pl.coef[i][2];
+        g.xin = in, g.last = i == q.steps - 1;
+        g.stage = 0, g.M = g.N = pl.m, g.K = std::max(q.rows, q.cols);
+        g.P = g.Q = p.x[in], g.pb = g.qb = p.xs;
+        g.pi = g.qj = wide ? pl.ldx : 1, g.pk = g.qk = wide ? 1 : pl.ldx;
+        st = launch("muon_gemm_kernel launch", wg::muon_gemm_kernel, dim3(tm, tm, q.batch), dim3(256), 0, s, p, g);
+        if (st) break;
+        g.stage = 1, g.K = pl.m, g.P = g.Q = p.a, g.pb = g.qb = p.ms;
+        g.pi = g.qk = pl.ldm, g.pk = g.qj = 1;
+        st = launch("muon_gemm_kernel launch", wg::muon_gemm_kernel, dim3(tm, tm, q.batch), dim3(256), 0, s, p, g);
+        if (st) break;
+        g.stage = 2, g.M = q.rows, g.N = q.cols;
+        if (wide) {
+            g.P = p.b, g.pb = p.ms, g.pi = pl.ldm, g.pk = 1;
+            g.Q = p.x[in], g.qb = p.xs, g.qk = pl.ldx, g.qj = 1;
+        } else {
+            g.P = p.x[in], g.pb = p.xs, g.pi = pl.ldx, g.pk = 1;
+            g.Q = p.b, g.qb = p.ms, g.qk = pl.ldm, g.qj = 1;
+        }
+        st = launch("muon_gemm_kernel launch", wg::muon_gemm_kernel, dim3(tc, tr, q.batch), dim3(256), 0, s, p, g);
+    }
+    return st;
+}
+
+// ---------------------------------------------------------------- embedding
+struct EmbPlan {
+    wg_embedding_problem p;
+    size_t off_count, off_offset, off_rank, off_list, off_cursor, bytes;
+};
+
+int emb_plan(const wg_embedding_problem* p, EmbPlan* pl)
+{
+    if (!p) return set_err(WG_ERR_INVALID_ARGUMENT, "problem is NULL");
+    if (p->tokens < 0 || p->tokens > 0x7fffffffLL || p->vocab < 1 || p->dim < 1)
+        return set_err(WG_ERR_INVALID_ARGUMENT, "tokens must be in 0..2^31-1, vocab and dim at least 1");
+    if (!dtype_ok(p->table_dtype) || !dtype_ok(p->out_dtype))
+        return set_err(WG_ERR_INVALID_ARGUMENT, "table_dtype and out_dtype must be WG_FP32, WG_BF16 or WG_FP16");
+    if (p->token_bits != 32 && p->token_bits != 64)
+        return set_err(WG_ERR_INVALID_ARGUMENT, "token_bits must be 32 or 64");
+    if (p->padding_token < -1 || p->padding_token >= p->vocab)
+        return set_err(WG_ERR_INVALID_ARGUMENT, "padding_token must be -1 or a row of the table");
+    if (!isfinite(p->scale)) return set_err(WG_ERR_INVALID_ARGUMENT, "scale must be finite");
+    pl->p = *p;
+    wg_embedding_problem& q = pl->p;
+    if (q.ld_table == 0) q.ld_table = q.dim;
+    if (q.ld_out == 0) q.ld_out = q.dim;
+    if (q.ld_table < q.dim || q.ld_out < q.dim)
+        return set_err(WG_ERR_INVALID_ARGUMENT, "ld_table and ld_out must be 0 or at least dim");
+    size_t o = 0;
+    pl->off_cursor = o, o += 256;
+    pl->off_count = o, o += up256((size_t)q.vocab * 4);
+    pl->off_offset = o, o += up256((size_t)q.vocab * 4);
+    pl->off_rank = o, o += up256((size_t)q.tokens * 4);
+    pl->off_list = o, o += up256((size_t)q.tokens * 4);
+    pl->bytes = o;
+    return WG_OK;
+}
+
+wg::EmbParams emb_params(const EmbPlan& pl, const void* token, const void* in, void* out)
+{
+    const wg_embedding_problem& q = pl.p;
+    wg::EmbParams p = {};
+    p.T = q.tokens, p.V = q.vocab, p.D = q.dim, p.ld_table = q.ld_table, p.ld_out = q.ld_out;
+    p.token = token, p.token64 = q.token_bits == 64, p.padding = q.padding_token, p.scale = q.scale;
+    p.in = in, p.out = out;
+    return p;
+}
+
+int emb_check(const EmbPlan& pl, const void* token, const void* table, const void* out)
+{
+    const wg_embedding_problem& q = pl.p;
+    if ((q.tokens > 0 && (!token || !out)) || !table)
+        return set_err(WG_ERR_INVALID_ARGUMENT, "token, table and out (or dy and dtable) must be non-NULL device pointers");
+    if (!aligned_to(token, q.token_bits / 8) || !aligned_to(table, esize(q.table_dtype)) ||
+        !aligned_to(out, esize(q.out_dtype)))
+        return set_err(WG_ERR_MISALIGNED, "a pointer is not aligned to its elements");
+    return WG_OK;
+}
+
+template <typename TT, typename TO>
+int emb_lookup_t(const EmbPlan& pl, const wg::EmbParams& p, cudaStream_t s)
+{
+    constexpr int V = sizeof(TT) == 4 || sizeof(TO) == 4 ? 4 : 8;
+    const bool vec = p.D % V == 0 && p.ld_table % V == 0 && p.ld_out % V == 0 && aligned_to(p.in, V * sizeof(TT)) &&
+                     aligned_to(p.out, V * sizeof(TO));
+    const long long n = p.T * (p.D / (vec ? V : 1));
+    const unsigned blocks = (unsigned)std::max(1LL, std::min<long long>((n + 255) / 256, 16LL * num_sms()));
+    return launch("emb_lookup_kernel launch", vec ? wg::emb_lookup_kernel<TT, TO, V> : wg::emb_lookup_kernel<TT, TO, 1>,
+                  dim3(blocks), dim3(256), 0, s, p);
+}
+
+template <typename TG, typename TY>
+int emb_bwd_t(const EmbPlan& pl, const wg::EmbParams& p, cudaStream_t s)
+{
+    const unsigned cap = 8u * num_sms();
+    const unsigned vb = std::min<unsigned>((p.V + 255) / 256, cap);
+    const unsigned tb = (unsigned)std::max(1LL, std::min<long long>((p.T + 255) / 256, cap));
+    int st = launch("emb_zero_kernel launch", wg::emb_zero_kernel, dim3(vb), dim3(256), 0, s, p);
+    if (!st) st = launch("emb_count_kernel launch", wg::emb_count_kernel, dim3(tb), dim3(256), 0, s, p);
+    if (!st) st = launch("emb_offset_kernel launch", wg::emb_offset_kernel, dim3(vb), dim3(256), 0, s, p);
+    if (!st) st = launch("emb_fill_kernel launch", wg::emb_fill_kernel, dim3(tb), dim3(256), 0, s, p);
+    if (!st)
+        st = launch("emb_reduce_kernel launch", wg::emb_reduce_kernel<TG, TY>, dim3(std::min<unsigned>((p.V + 7) / 8, cap)),
+                    dim3(256), 0, s, p);
+    return st;
+}
+
+// Call f with the types of two dtypes.
+template <typename A, typename F>
+int with_second(int d, F f)
+{
+    return d == WG_FP32 ? f.template operator()<A, float>()
+           : d == WG_BF16 ? f.template operator()<A, __nv_bfloat16>()
+                          : f.template operator()<A, __half>();
+}
+template <typename F>
+int with_types(int d1, int d2, F f)
+{
+    return d1 == WG_FP32 ? with_second<float>(d2, f)
+           : d1 == WG_BF16 ? with_second<__nv_bfloat16>(d2, f)
+                           : with_second<__half>(d2, f);
+}
+
+struct LookupCall {
+    const EmbPlan& pl;
+    const wg::EmbParams& p;
+    cudaStream_t s;
+    template <typename TT, typename TO>
+    int operator()() const { return emb_lookup_t<TT, TO>(pl, p, s); }
+};
+struct BwdCall {
+    const EmbPlan& pl;
+    const wg::EmbParams& p;
+    cudaStream_t s;
+    template <typename TT, typename TO>
+    int operator()() const { return emb_bwd_t<TT, TO>(pl, p, s); }
+};
+
+}  // namespace
+
+extern "C" {
+
+int wg_muon_workspace_size(const wg_muon_problem* p, size_t* bytes)
+{
+    if (!bytes) return set_err(WG_ERR_INVALID_ARGUMENT, "bytes is NULL");
+    MuonPlan pl;
+    const int st = muon_plan(p, &pl);
+    if (!st) *bytes = pl.bytes;
+    return st;
+}
+
+int wg_muon_plan_string(const wg_muon_problem* p, char* buf, size_t n)
+{
+    if (!buf || n == 0) return set_err(WG_ERR_INVALID_ARGUMENT, "buffer is NULL or empty");
+    MuonPlan pl;
+    const int st = muon_plan(p, &pl);
+    if (st) return st;
+    snprintf(buf, n, "kernel=muon_gemm side=%s m=%d steps=%d ws=%zu", p->rows <= p->cols ? "left" : "right", pl.m,
+             p->steps, pl.bytes);
+    return WG_OK;
+}
+
+int wg_muon_update(const wg_muon_problem* p, const void* grad, void* momentum, void* weight, void* out,
+                   void* workspace, size_t ws_bytes, void* stream)
+{
+    MuonPlan pl;
+    int st = muon_plan(p, &pl);
+    if (st) return st;
+    if (!grad || (!weight && !out))
+        return set_err(WG_ERR_INVALID_ARGUMENT, "grad, and one of weight and out, must be non-NULL device pointers");
+    if (!aligned_to(grad, esize(p->grad_dtype)) || !aligned_to(momentum, 4) ||
+        !aligned_to(weight, esize(p->weight_dtype)) || !aligned_to(out, esize(p->out_dtype)))
+        return set_err(WG_ERR_MISALIGNED, "a pointer is not aligned to its elements");
+    const void* buf[4] = {grad, momentum, weight, out};
+    const int es[4] = {esize(p->grad_dtype), 4, esize(p->weight_dtype), esize(p->out_dtype)};
+    const long long span = (long long)(pl.p.batch - 1) * pl.p.batch_stride + (long long)(pl.p.rows - 1) * pl.p.ld + pl.p.cols;
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < i; ++j) {
+            const uintptr_t a = reinterpret_cast<uintptr_t>(buf[i]), b = reinterpret_cast<uintptr_t>(buf[j]);
+            if (a && b && a < b + (uintptr_t)(span * es[j]) && b < a + (uintptr_t)(span * es[i]))
+                return set_err(WG_ERR_INVALID_ARGUMENT, "grad, momentum, weight and out must not overlap");
+        }
+    if ((st = check_workspace(pl.bytes, workspace, ws_bytes))) return st;
+    return muon_run(pl, grad, momentum, weight, out, static_cast<char*>(workspace), static_cast<cudaStream_t>(stream));
+}
+
+int wg_embedding_lookup(const wg_embedding_problem* p, const void* token, const void* table, void* out, void* stream)
+{
+    EmbPlan pl;
+    int st = emb_plan(p, &pl);
+    if (st) return st;
+    if ((st = emb_check(pl, token, table, out))) return st;
+    if (pl.p.tokens == 0) return WG_OK;
+    const wg::EmbParams e = emb_params(pl, token, table, out);
+    return with_types(pl.p.table_dtype, pl.p.out_dtype, LookupCall{pl, e, static_cast<cudaStream_t>(stream)});
+}
+
+int wg_embedding_workspace_size(const wg_embedding_problem* p, size_t* bytes)
+{
+    if (!bytes) return set_err(WG_ERR_INVALID_ARGUMENT, "bytes is NULL");
+    EmbPlan pl;
+    const int st = emb_plan(p, &pl);
+    if (!st) *bytes = pl.bytes;
+    return st;
+}
+
+int wg_embedding_bwd_weight(const wg_embedding_problem* p, const void* token, const void* dy, void* dtable,
+                            int accumulate, void* workspace, size_t ws_bytes, void* stream)
+{
+    EmbPlan pl;
+    int st = emb_plan(p, &pl);
+    if (st) return st;
+    if ((st = emb_check(pl, token, dtable, dy))) return st;
+    if ((st = check_workspace(pl.bytes, workspace, ws_bytes))) return st;
+    wg::EmbParams e = emb_params(pl, token, dy, dtable);
+    char* ws = static_cast<char*>(workspace);
+    e.accumulate = accumulate != 0;
+    e.count = reinterpret_cast<int*>(ws + pl.off_count), e.offset = reinterpret_cast<int*>(ws + pl.off_offset);
+    e.rank = reinterpret_cast<int*>(ws + pl.off_rank), e.list = reinterpret_cast<int*>(ws + pl.off_list);
+    e.cursor = reinterpret_cast<int*>(ws + pl.off_cursor);
+    return with_types(pl.p.table_dtype, pl.p.out_dtype, BwdCall{pl, e, static_cast<cudaStream_t>(stream)});
+}
+
+}  // extern "C"

@@ -12,6 +12,7 @@
 #include <string>
 
 #include "../../include/wgrad.h"
+#include "host.h"
 #include "k_depthwise.cuh"
 #include "k_dgrad.cuh"
 #include "k_igemm.cuh"
@@ -36,11 +37,9 @@ __global__ void selftest_timeout_kernel()
 
 }  // namespace wg
 
-namespace {
+namespace wg {
 
 thread_local std::string g_err;
-// Event recorded after each call's main kernel (wg_set_mark_event); null = off.
-thread_local cudaEvent_t g_mark = nullptr;
 
 int set_err(int status, const std::string& msg)
 {
@@ -52,10 +51,6 @@ int cuda_fail(const char* what, cudaError_t e)
 {
     return set_err(WG_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
 }
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 EncodeTiledFn encode_fn()
 {
@@ -72,16 +67,13 @@ EncodeTiledFn encode_fn()
     return fn;
 }
 
-// Raise a kernel's dynamic shared-memory limit when a launch needs more than
-// any earlier one (per device).
-template <typename K>
-int ensure_smem(K kernel, int bytes)
+int ensure_smem_ptr(const void* kernel, int bytes)
 {
     static std::mutex mu;
     static std::map<std::pair<const void*, int>, int> done;
     int dev = 0;
     cudaGetDevice(&dev);
-    const auto key = std::make_pair(reinterpret_cast<const void*>(kernel), dev);
+    const auto key = std::make_pair(kernel, dev);
     std::lock_guard<std::mutex> lk(mu);
     auto it = done.find(key);
     if (it != done.end() && it->second >= bytes) return WG_OK;
@@ -106,6 +98,36 @@ int num_sms()
     }
     return n;
 }
+
+// Programmatic stream serialization for a launch (see launch_pre).
+void pdl_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, unsigned* na, cudaStream_t stream)
+{
+    attr[*na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[*na].val.programmaticStreamSerializationAllowed = 1;
+    ++*na;
+    cfg->attrs = attr;
+    cfg->numAttrs = *na;
+    cfg->stream = stream;
+}
+
+bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
+
+}  // namespace wg
+
+namespace {
+
+using wg::aligned16;
+using wg::cuda_fail;
+using wg::encode_fn;
+using wg::EncodeTiledFn;
+using wg::ensure_smem;
+using wg::g_err;
+using wg::num_sms;
+using wg::pdl_config;
+using wg::set_err;
+
+// Event recorded after each call's main kernel (wg_set_mark_event); null = off.
+thread_local cudaEvent_t g_mark = nullptr;
 
 // Device facts for the planner: SM count, and how many CTAs of the
 // tensor-core kernel (at its largest shared-memory size) fit at once in
@@ -183,8 +205,6 @@ int plan_for(const wg_problem* p, const wg_options* opt, wg::Plan* pl, std::stri
     if (key_out) *key_out = key;
     return WG_OK;
 }
-
-bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
 
 int encode(CUtensorMap* tm, int in_dtype, void* base, const cuuint64_t dims[5], const cuuint32_t box[5],
            const cuuint32_t estr[5], CUtensorMapSwizzle swz, const char* what)
@@ -379,17 +399,6 @@ int reduce_regs_ctas_per_sm()
     }
     cache.emplace(dev, n);
     return n;
-}
-
-// Programmatic stream serialization for a launch (see launch_pre).
-void pdl_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, unsigned* na, cudaStream_t stream)
-{
-    attr[*na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[*na].val.programmaticStreamSerializationAllowed = 1;
-    ++*na;
-    cfg->attrs = attr;
-    cfg->numAttrs = *na;
-    cfg->stream = stream;
 }
 
 // Stage 2 of deterministic split-K, launched as a programmatic dependent of the
@@ -677,6 +686,15 @@ int check_buffers(const wg::Plan& pl, const void* x, const void* dy, const void*
     return WG_OK;
 }
 
+// Read and clear this translation unit's device status word.
+cudaError_t take_status(unsigned int* v)
+{
+    cudaError_t e = cudaMemcpyFromSymbol(v, wg::g_status, sizeof *v);
+    const unsigned int zero = 0;
+    if (e == cudaSuccess && *v) e = cudaMemcpyToSymbol(wg::g_status, &zero, sizeof zero);
+    return e;
+}
+
 }  // namespace
 
 extern "C" {
@@ -691,6 +709,7 @@ const char* wg_status_string(int s)
         case WG_ERR_WORKSPACE: return "WG_ERR_WORKSPACE";
         case WG_ERR_CUDA: return "WG_ERR_CUDA";
         case WG_ERR_DEVICE_TIMEOUT: return "WG_ERR_DEVICE_TIMEOUT";
+        case WG_ERR_INVALID_TOKEN: return "WG_ERR_INVALID_TOKEN";
         default: return "WG_ERR_UNKNOWN";
     }
 }
@@ -785,17 +804,17 @@ int wg_check_status(void* stream)
 {
     cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail("cudaStreamSynchronize", e);
-    unsigned int v = 0;
-    e = cudaMemcpyFromSymbol(&v, wg::g_status, sizeof v);
-    if (e != cudaSuccess) return cuda_fail("cudaMemcpyFromSymbol(status)", e);
-    if (v) {
-        const unsigned int zero = 0;
-        e = cudaMemcpyToSymbol(wg::g_status, &zero, sizeof zero);
-        if (e != cudaSuccess) return cuda_fail("cudaMemcpyToSymbol(status)", e);
+    // Each translation unit with kernels has a status word of its own.
+    unsigned int v = 0, u = 0;
+    e = take_status(&v);
+    if (e == cudaSuccess) e = wg::take_update_status(&u);
+    if (e != cudaSuccess) return cuda_fail("reading the device status", e);
+    v |= u;
+    if (v & (wg::kStatusBadPlan | wg::kStatusTimeout))
         return set_err(WG_ERR_DEVICE_TIMEOUT, (v & wg::kStatusBadPlan)
                                                   ? "internal error: a kernel instance got a plan it is not built for"
                                                   : "a kernel's bounded wait ran out");
-    }
+    if (v & wg::kStatusBadToken) return set_err(WG_ERR_INVALID_TOKEN, "an embedding call read a token outside [0, vocab)");
     return WG_OK;
 }
 

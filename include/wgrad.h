@@ -84,8 +84,9 @@ typedef enum {
     WG_ERR_MISALIGNED = 3,       /* a base pointer is not 16-byte aligned */
     WG_ERR_WORKSPACE = 4,        /* workspace missing or smaller than wg_workspace_size */
     WG_ERR_CUDA = 5,             /* a CUDA runtime/driver call failed */
-    WG_ERR_DEVICE_TIMEOUT = 6    /* a kernel's bounded wait ran out, or (an internal error) a kernel
+    WG_ERR_DEVICE_TIMEOUT = 6,   /* a kernel's bounded wait ran out, or (an internal error) a kernel
                                     found its launch inconsistent; reported by wg_check_status */
+    WG_ERR_INVALID_TOKEN = 7     /* an embedding call read a token outside [0, vocab); reported by wg_check_status */
 } wg_status;
 
 /* Problem record (the host arguments of the CK page: G_, N_, C_, K_, spatial
@@ -192,8 +193,8 @@ WG_API int wg_conv_bwd_weight(const wg_problem* p, const void* x, const void* dy
                        void* workspace, size_t ws_bytes, void* stream);
 
 /* Synchronise `stream`, then read and clear the device status word that the
- * kernels set when a bounded wait runs out.  Returns WG_OK,
- * WG_ERR_DEVICE_TIMEOUT or WG_ERR_CUDA. */
+ * kernels set when a bounded wait runs out or a token is out of range.
+ * Returns WG_OK, WG_ERR_DEVICE_TIMEOUT, WG_ERR_INVALID_TOKEN or WG_ERR_CUDA. */
 WG_API int wg_check_status(void* stream);
 
 /* Human-readable plan for (p, opt): kernel, tiles, split degree, mode, grid,
@@ -311,6 +312,116 @@ WG_API int wg_bwd_data_workspace_size(const wg_problem* p, size_t* bytes);
 
 /* Human-readable plan of wg_conv_bwd_data for p.  Host only. */
 WG_API int wg_bwd_data_plan_string(const wg_problem* p, char* buf, size_t n);
+
+/* ------------------------------------------------------------------------
+ * Weight updates: what training does with a weight gradient, and the gradient
+ * of the one weight that is looked up instead of multiplied (no counterparts in
+ * the CK page).  The conventions at the top of this file hold here too. */
+
+/* Orthogonalised update of `batch` matrices (a convolution's dW is G matrices of
+ * K rows and Z*Y*X*C columns, packed), with the momentum before it and the
+ * weight step after it.  Per matrix, g the gradient, m the momentum, w the weight:
+ *
+ *   m <- mu * m + (1 - dampening) * g                 (when m is given)
+ *   u  = nesterov ? (1 - dampening) * g + mu * m : m  (m the new one; u = g without m)
+ *   X  = u / (|u|_F + eps)
+ *   steps times:  A = X X^T,  X <- a X + (b A + c A A) X
+ *   out = scale * X                                   (when out is given)
+ *   w  <- (1 - lr * weight_decay) * w - lr * scale * X  (when w is given)
+ *
+ * The products are the same on the left and on the right of X; the kernels take
+ * the shorter side.  With the default coefficients (3.4445, -4.7750, 2.0315) five
+ * steps bring every singular value that was above about 1e-3 of |u|_F into
+ * [0.7, 1.2].
+ *
+ * Arithmetic: u, the norm and m in fp32.  A matrix whose shorter side is at most
+ * 128 is iterated on its Gram matrix in fp32-like precision; a larger one with
+ * 16-bit operands and fp32 sums (X carried to 22 bits beside its 16-bit operand).
+ * X's relative error (2-norm of all elements) is below 4e-3 in either form on
+ * gradients of rank 1 to full rank; out and w are then rounded to nearest even.
+ * A zero matrix gives zeros; a NaN or an infinity in u makes its matrix's X NaN.
+ * Results are bitwise reproducible from run to run.
+ *
+ *  batch >= 1, rows >= 1, cols >= 1; rows, cols <= 32768; batch <= 65535.
+ *  ld, batch_stride: elements between rows and between matrices of grad,
+ *    momentum, weight and out alike; 0 = packed (cols, rows * ld).  Elements
+ *    between rows are neither read nor written.
+ *  steps: 0..16 products of the iteration; 0 leaves X = u / (|u|_F + eps).
+ *  coef: HOST pointer to steps x (a, b, c), or NULL for the default of every step.
+ *    A step may grow a singular value of at most 1 to at most 4 (checked).
+ *  mu in [0, 1), dampening in [0, 1], eps >= 0; all finite. */
+typedef struct {
+    int batch, rows, cols;
+    long long ld, batch_stride;
+    wg_dtype grad_dtype;   /* grad: WG_FP32, WG_BF16 or WG_FP16 */
+    wg_dtype out_dtype;    /* out */
+    wg_dtype weight_dtype; /* weight */
+    int steps, nesterov;
+    const float* coef;
+    float mu, dampening, eps, scale, lr, weight_decay;
+} wg_muon_problem;
+
+/* Bytes of device workspace wg_muon_update needs for p.  Host only. */
+WG_API int wg_muon_workspace_size(const wg_muon_problem* p, size_t* bytes);
+
+/* Human-readable plan of wg_muon_update for p.  Host only. */
+WG_API int wg_muon_plan_string(const wg_muon_problem* p, char* buf, size_t n);
+
+/* Compute the update of p on `stream`.
+ *  grad: required.  momentum: fp32, read and written, or NULL.  weight: read and
+ *  written, or NULL.  out: written, or NULL.  One of weight and out is required,
+ *  and no two of the four may overlap.
+ *  grad, momentum, weight and out need only their elements' alignment (a layer's
+ *  slice of a larger buffer); workspace is 16-byte aligned.
+ * Returns WG_OK or an error status; nothing is launched on an error. */
+WG_API int wg_muon_update(const wg_muon_problem* p, const void* grad, void* momentum, void* weight, void* out,
+                          void* workspace, size_t ws_bytes, void* stream);
+
+/* Embedding table of `vocab` rows of `dim` elements, looked up by `tokens` tokens.
+ *
+ *   lookup:    out[t, :]    = scale * table[token[t], :]
+ *   gradient:  dtable[v, :] = scale * sum over the t with token[t] = v of dy[t, :]
+ *
+ * Products and sums are fp32, rounded once (to nearest even).  The gradient's
+ * sums run over ascending t, in pieces of 64 for tokens that occur more than
+ * 32 times (pieces added in order): bitwise reproducible.
+ * A token outside [0, vocab) looks up zeros and adds to no row; wg_check_status
+ * then returns WG_ERR_INVALID_TOKEN.
+ *
+ *  tokens in 0..2^31-1 (0: a lookup does nothing, a gradient is zero), vocab and
+ *  dim >= 1.
+ *  ld_table, ld_out: elements between rows of table / dtable and of out / dy;
+ *    0 = dim.  Elements between rows are neither read nor written.
+ *  table_dtype: table and dtable; out_dtype: out and dy (WG_FP32, WG_BF16, WG_FP16).
+ *  token_bits: 32 or 64 (signed integers).
+ *  padding_token: a token whose row takes no gradient; -1 = none.
+ *  table, dtable, out, dy and tokens need only their elements' alignment; 16-byte
+ *  aligned rows are faster. */
+typedef struct {
+    long long tokens;
+    int vocab, dim;
+    long long ld_table, ld_out;
+    wg_dtype table_dtype, out_dtype;
+    int token_bits;
+    int padding_token;
+    float scale;
+} wg_embedding_problem;
+
+/* Look up `tokens` rows of `table` into `out` on `stream`.
+ * Returns WG_OK or an error status; nothing is launched on an error. */
+WG_API int wg_embedding_lookup(const wg_embedding_problem* p, const void* token, const void* table, void* out,
+                               void* stream);
+
+/* Bytes of device workspace wg_embedding_bwd_weight needs for p.  Host only. */
+WG_API int wg_embedding_workspace_size(const wg_embedding_problem* p, size_t* bytes);
+
+/* Gradient of the table on `stream`.  accumulate = 0: every element of dtable is
+ * written once (zeros for rows that no token names).  accumulate = 1: the sums
+ * are added to dtable's rows (in fp32, then rounded), and rows without a token
+ * are not touched.  workspace is 16-byte aligned.
+ * Returns WG_OK or an error status; nothing is launched on an error. */
+WG_API int wg_embedding_bwd_weight(const wg_embedding_problem* p, const void* token, const void* dy, void* dtable,
+                                   int accumulate, void* workspace, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,93 @@
+"""Host-side checks of the weight-update entry points (no GPU needed): sizes, plans and refusals.  Only calls that
+fail validation are made here, so nothing is launched."""
+import math
+
+import pytest
+
+from implicit_gemm_gb300 import binding, build
+
+A = 1 << 20  # stands for a device address; refused before it is used
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build.build()
+    binding.load()
+
+
+def muon(**kw):
+    return {"rows": 24, "cols": 40, **kw}
+
+
+def emb(**kw):
+    return {"tokens": 7, "vocab": 11, "dim": 16, **kw}
+
+
+def refused(status, f, *a, **kw):
+    with pytest.raises(binding.WgradError) as e:
+        f(*a, **kw)
+    assert e.value.status == status, e.value
+    assert binding.wg_last_error()
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(rows=0), 1), (dict(cols=-1), 1), (dict(batch=0), 1), (dict(rows=40000), 2), (dict(batch=70000), 2),
+    (dict(steps=-1), 1), (dict(steps=17), 1), (dict(momentum=1.0), 1), (dict(momentum=-0.1), 1),
+    (dict(momentum=math.nan), 1), (dict(dampening=1.5), 1), (dict(eps=-1e-8), 1), (dict(eps=math.inf), 1),
+    (dict(scale=math.inf), 1), (dict(lr=math.nan), 1), (dict(weight_decay=math.inf), 1), (dict(ld=39), 1),
+    (dict(batch=2, batch_stride=39), 1), (dict(batch=2, ld=79, batch_stride=40), 1),
+    (dict(steps=1, coef=[(8.0, 0.0, 0.0)]), 1), (dict(steps=2, coef=[(2.0, 0.0, 0.0), (math.nan, 0.0, 0.0)]), 1),
+])
+def test_muon_problem_refusals(bad, status):
+    refused(status, binding.wg_muon_workspace_size, muon(**bad))
+    refused(status, binding.wg_muon_update, muon(**bad), A, out=2 * A, workspace=3 * A, ws_bytes=1 << 40, stream=0)
+
+
+def test_muon_layouts_accepted():
+    assert binding.wg_muon_workspace_size(muon(batch=2, ld=80, batch_stride=40)) > 0   # side by side
+    assert binding.wg_muon_workspace_size(muon(batch=2, ld=41, batch_stride=24 * 41 + 5)) > 0
+    assert "muon" in binding.wg_muon_plan_string(muon())
+    with pytest.raises(ValueError):
+        binding.make_muon_problem(muon(steps=2, coef=[(1.0, 0.0, 0.0)]))
+
+
+def test_muon_buffer_refusals():
+    sp, big = muon(), 1 << 30
+    refused(1, binding.wg_muon_update, sp, 0, out=A, workspace=2 * A, ws_bytes=big, stream=0)
+    refused(1, binding.wg_muon_update, sp, A, workspace=2 * A, ws_bytes=big, stream=0)
+    refused(1, binding.wg_muon_update, sp, A, out=A, workspace=4 * A, ws_bytes=big, stream=0)
+    refused(1, binding.wg_muon_update, sp, A, momentum=A + 64, out=2 * A, workspace=4 * A, ws_bytes=big, stream=0)
+    refused(3, binding.wg_muon_update, sp, A + 2, out=2 * A, workspace=4 * A, ws_bytes=big, stream=0)
+    refused(3, binding.wg_muon_update, sp, A, momentum=2 * A + 2, out=4 * A, workspace=8 * A, ws_bytes=big, stream=0)
+    refused(3, binding.wg_muon_update, sp, A, out=2 * A, workspace=4 * A + 8, ws_bytes=big, stream=0)
+    refused(4, binding.wg_muon_update, sp, A, out=2 * A, workspace=4 * A,
+            ws_bytes=binding.wg_muon_workspace_size(sp) - 1, stream=0)
+    refused(4, binding.wg_muon_update, sp, A, out=2 * A, stream=0)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(tokens=-1), 1), (dict(tokens=1 << 31), 1), (dict(vocab=0), 1), (dict(dim=0), 1), (dict(ld_table=15), 1),
+    (dict(ld_out=15), 1), (dict(padding_token=11), 1), (dict(padding_token=-2), 1), (dict(scale=math.nan), 1),
+])
+def test_embedding_problem_refusals(bad, status):
+    refused(status, binding.wg_embedding_workspace_size, emb(**bad))
+    refused(status, binding.wg_embedding_lookup, emb(**bad), A, 2 * A, 3 * A, stream=0)
+    refused(status, binding.wg_embedding_bwd_weight, emb(**bad), A, 2 * A, 3 * A, workspace=4 * A, ws_bytes=1 << 40,
+            stream=0)
+
+
+def test_embedding_buffer_refusals():
+    sp, big = emb(), 1 << 30
+    for args in ((0, A, 2 * A), (A, 0, 2 * A), (A, 2 * A, 0)):
+        refused(1, binding.wg_embedding_lookup, sp, *args, stream=0)
+        refused(1, binding.wg_embedding_bwd_weight, sp, *args, workspace=4 * A, ws_bytes=big, stream=0)
+    refused(3, binding.wg_embedding_lookup, sp, A + 4, 2 * A, 3 * A, stream=0)
+    refused(3, binding.wg_embedding_lookup, sp, A, 2 * A + 1, 3 * A, stream=0)
+    refused(3, binding.wg_embedding_lookup, emb(out_dtype="fp32"), A, 2 * A, 3 * A + 2, stream=0)
+    refused(4, binding.wg_embedding_bwd_weight, sp, A, 2 * A, 3 * A, stream=0)
+    refused(4, binding.wg_embedding_bwd_weight, sp, A, 2 * A, 3 * A, workspace=4 * A, ws_bytes=16, stream=0)
+    refused(3, binding.wg_embedding_bwd_weight, sp, A, 2 * A, 3 * A, workspace=4 * A + 4, ws_bytes=big, stream=0)
+
+
+def test_status_of_a_bad_token_has_a_name():
+    assert binding.wg_status_string(7) == "WG_ERR_INVALID_TOKEN"
