@@ -195,7 +195,9 @@ int muon_run(const MuonPlan& pl, const void* grad, void* momentum, void* weight,
 // ---------------------------------------------------------------- embedding
 struct EmbPlan {
     wg_embedding_problem p;
-    size_t off_count, off_offset, off_rank, off_list, off_cursor, bytes;
+    int R;              // table rows of a CTA of the sort
+    long long windows;  // windows of the sorted list
+    size_t off_meta, off_count, off_list, off_row, off_cross, off_part, bytes;
 };
 
 int emb_plan(const wg_embedding_problem* p, EmbPlan* pl)
@@ -216,12 +218,18 @@ int emb_plan(const wg_embedding_problem* p, EmbPlan* pl)
     if (q.ld_out == 0) q.ld_out = q.dim;
     if (q.ld_table < q.dim || q.ld_out < q.dim)
         return set_err(WG_ERR_INVALID_ARGUMENT, "ld_table and ld_out must be 0 or at least dim");
+    // One CTA of the sort per SM, unless its counters would not fit.
+    pl->R = std::min((q.vocab + num_sms() - 1) / num_sms(), wg::kEmbSortMaxRows);
+    pl->windows = (q.tokens + wg::kEmbWindow - 1) / wg::kEmbWindow;
+    if (pl->windows * ((q.dim + wg::kEmbTile - 1) / wg::kEmbTile) > 8LL * 0x7fffffff)
+        return set_err(WG_ERR_NOT_SUPPORTED, "more tokens by columns than one launch covers");
     size_t o = 0;
-    pl->off_cursor = o, o += 256;
+    pl->off_meta = o, o += 256;
     pl->off_count = o, o += up256((size_t)q.vocab * 4);
-    pl->off_offset = o, o += up256((size_t)q.vocab * 4);
-    pl->off_rank = o, o += up256((size_t)q.tokens * 4);
     pl->off_list = o, o += up256((size_t)q.tokens * 4);
+    pl->off_row = o, o += up256((size_t)q.tokens * 4);
+    pl->off_cross = o, o += up256((size_t)pl->windows * 16);
+    pl->off_part = o, o += up256((size_t)pl->windows * 2 * q.dim * 4);
     pl->bytes = o;
     return WG_OK;
 }
@@ -259,20 +267,32 @@ int emb_lookup_t(const EmbPlan& pl, const wg::EmbParams& p, cudaStream_t s)
                   dim3(blocks), dim3(256), 0, s, p);
 }
 
+template <typename TG, typename TY, int V>
+int emb_bwd_v(const EmbPlan& pl, const wg::EmbParams& p, cudaStream_t s)
+{
+    const int smem = wg::kEmbSortWarps * pl.R * 4;
+    int st = wg::ensure_smem(wg::emb_sort_kernel<TG, V>, smem);
+    if (!st)
+        st = launch("emb_sort_kernel launch", wg::emb_sort_kernel<TG, V>, dim3((p.V + pl.R - 1) / pl.R),
+                    dim3(wg::kEmbSortThreads), smem, s, p);
+    if (st || p.T == 0) return st;
+    const int tiles = (p.D + wg::kEmbTile - 1) / wg::kEmbTile;
+    const long long items = pl.windows * tiles;
+    st = launch("emb_reduce_kernel launch", wg::emb_reduce_kernel<TG, TY, V>, dim3((unsigned)((items + 7) / 8)), dim3(256),
+                0, s, p, tiles);
+    if (!st)
+        st = launch("emb_join_kernel launch", wg::emb_join_kernel<TG, V>,
+                    dim3((unsigned)std::min<long long>(items, 4LL * num_sms())), dim3(256), 0, s, p, tiles);
+    return st;
+}
+
 template <typename TG, typename TY>
 int emb_bwd_t(const EmbPlan& pl, const wg::EmbParams& p, cudaStream_t s)
 {
-    const unsigned cap = 8u * num_sms();
-    const unsigned vb = std::min<unsigned>((p.V + 255) / 256, cap);
-    const unsigned tb = (unsigned)std::max(1LL, std::min<long long>((p.T + 255) / 256, cap));
-    int st = launch("emb_zero_kernel launch", wg::emb_zero_kernel, dim3(vb), dim3(256), 0, s, p);
-    if (!st) st = launch("emb_count_kernel launch", wg::emb_count_kernel, dim3(tb), dim3(256), 0, s, p);
-    if (!st) st = launch("emb_offset_kernel launch", wg::emb_offset_kernel, dim3(vb), dim3(256), 0, s, p);
-    if (!st) st = launch("emb_fill_kernel launch", wg::emb_fill_kernel, dim3(tb), dim3(256), 0, s, p);
-    if (!st)
-        st = launch("emb_reduce_kernel launch", wg::emb_reduce_kernel<TG, TY>, dim3(std::min<unsigned>((p.V + 7) / 8, cap)),
-                    dim3(256), 0, s, p);
-    return st;
+    constexpr int V = sizeof(TG) == 4 || sizeof(TY) == 4 ? 4 : 8;
+    const bool vec = p.D % V == 0 && p.ld_table % V == 0 && p.ld_out % V == 0 && aligned_to(p.in, V * sizeof(TY)) &&
+                     aligned_to(p.out, V * sizeof(TG));
+    return vec ? emb_bwd_v<TG, TY, V>(pl, p, s) : emb_bwd_v<TG, TY, 1>(pl, p, s);
 }
 
 // Call f with the types of two dtypes.
@@ -385,9 +405,10 @@ int wg_embedding_bwd_weight(const wg_embedding_problem* p, const void* token, co
     wg::EmbParams e = emb_params(pl, token, dy, dtable);
     char* ws = static_cast<char*>(workspace);
     e.accumulate = accumulate != 0;
-    e.count = reinterpret_cast<int*>(ws + pl.off_count), e.offset = reinterpret_cast<int*>(ws + pl.off_offset);
-    e.rank = reinterpret_cast<int*>(ws + pl.off_rank), e.list = reinterpret_cast<int*>(ws + pl.off_list);
-    e.cursor = reinterpret_cast<int*>(ws + pl.off_cursor);
+    e.R = pl.R;
+    e.meta = reinterpret_cast<int*>(ws + pl.off_meta), e.count = reinterpret_cast<int*>(ws + pl.off_count);
+    e.list = reinterpret_cast<int*>(ws + pl.off_list), e.row = reinterpret_cast<int*>(ws + pl.off_row);
+    e.cross = reinterpret_cast<int4*>(ws + pl.off_cross), e.part = reinterpret_cast<float*>(ws + pl.off_part);
     return with_types(pl.p.table_dtype, pl.p.out_dtype, BwdCall{pl, e, static_cast<cudaStream_t>(stream)});
 }
 
