@@ -14,11 +14,11 @@
 //                     nothing from each other.  It also writes the zeros of the
 //                     rows that no token names.
 //  emb_reduce_kernel  a segmented sum over the sorted list: a warp takes 32 entries
-//                     (a window) by 256 columns.  Runs of one token inside the
-//                     window are final rows; those that cross its borders leave
-//                     fp32 partial rows.  Every warp has the same work, however
-//                     often a token occurs.
-//  emb_join_kernel    adds the partial rows of the runs that cross windows, in order.
+//                     (a window) by 256 columns.  A run of at most 64 entries is
+//                     summed by the warp of the window it starts in, to its end;
+//                     a longer one leaves an fp32 partial row per window.  So no
+//                     warp has more than 95 entries, however often a token occurs.
+//  emb_join_kernel    adds the partial rows of the long runs, in the windows' order.
 //
 // Windows are fixed places of the sorted list, so every sum has one order.
 #pragma once
@@ -40,12 +40,13 @@ struct EmbParams {
     void* out;       // out (lookup) or dtable (gradient)
     int accumulate;
     int R;        // table rows of a CTA of emb_sort_kernel
-    int* meta;    // [0] entries of the list, [1] runs that cross windows
+    int* meta;    // [0] entries of the list, [1] long runs that cross windows
     int* count;   // [V] occurrences of a row's token
     int* list;    // [T] positions, by (row, position)
     int* row;     // [T] their rows
-    int4* cross;  // [windows] (row, first entry, entries, 0) of the runs that cross windows
+    int4* cross;  // (row, first entry, entries, 0) of the long runs that cross windows
     float* part;  // [windows][2][D] partial rows: of a run from before the window, of a run that goes on after it
+    int token16;  // token is 16-byte aligned
 };
 
 // The token at position t as a table row, or -1 when it is out of range.
@@ -81,8 +82,36 @@ __global__ void __launch_bounds__(256) emb_lookup_kernel(const __grid_constant__
 }
 
 constexpr int kEmbSortThreads = 1024, kEmbSortWarps = kEmbSortThreads / 32;
-constexpr int kEmbSortMaxRows = 1600;  // 32 counters of 4 bytes a row: 205 KB of shared memory
-constexpr int kEmbWindow = 32, kEmbTile = 256;
+constexpr int kEmbSortKept = 64;       // positions of its rows that a warp keeps from the count
+constexpr int kEmbSortMaxRows = 1536;  // 32 counters of 4 bytes a row: 192 KB of shared memory
+constexpr int kEmbWindow = 32, kEmbTile = 256, kEmbShort = 64;
+
+// The tokens at positions t .. t + 3 as table rows; -1: out of range, -2: past the last position.
+__device__ __forceinline__ void emb_tokens4(const EmbParams& p, long long t, int (&v)[4])
+{
+    if (!p.token64 && p.token16 && t + 4 <= p.T) {
+        const int4 x = *reinterpret_cast<const int4*>(static_cast<const int*>(p.token) + t);
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if ((unsigned)v[j] >= (unsigned)p.V) v[j] = -1;
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = t + j < p.T ? emb_token(p, t + j) : -2;
+}
+
+// n elements of zero from any element-aligned address, by one warp.
+template <typename T>
+__device__ __forceinline__ void emb_zero_row(T* row, int n, int lane)
+{
+    const int head = min(n, (int)((16u - ((unsigned)reinterpret_cast<uintptr_t>(row) & 15u)) & 15u) / (int)sizeof(T));
+    const int body = (n - head) * (int)sizeof(T) / 16, tail = head + body * (16 / (int)sizeof(T));
+    if (lane < head) row[lane] = from_f32<T>(0.f);
+    uint4* q = reinterpret_cast<uint4*>(row + head);
+    for (int i = lane; i < body; i += 32) q[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (tail + lane < n) row[tail + lane] = from_f32<T>(0.f);
+}
 
 // Block-wide exclusive sum of one value per thread (1024 threads); *total gets the sum.
 __device__ __forceinline__ int block_exclusive_1024(int v, int* total)
@@ -108,11 +137,12 @@ __device__ __forceinline__ int block_exclusive_1024(int v, int* total)
     return x - v + __shfl_sync(0xffffffffu, s - w, warp);
 }
 
-template <typename TG, int VEC>
+template <typename TG>
 __global__ void __launch_bounds__(kEmbSortThreads, 1) emb_sort_kernel(const __grid_constant__ EmbParams p)
 {
     extern __shared__ int hist[];  // [warps][R]: counts, then each warp's next entry of a row
     __shared__ int first[kEmbSortMaxRows];
+    __shared__ int kept_t[kEmbSortWarps][kEmbSortKept], kept_r[kEmbSortWarps][kEmbSortKept];
     const int R = p.R, lo = blockIdx.x * R, nr = min(R, p.V - lo);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_launch_dependents();
@@ -120,22 +150,54 @@ __global__ void __launch_bounds__(kEmbSortThreads, 1) emb_sort_kernel(const __gr
     __syncthreads();
     pdl_wait();
     int* mine = hist + warp * R;
-    // Each warp's positions: a multiple of 32 * 4 of them.
+    // Each warp's positions: a multiple of 128, four consecutive ones per lane and
+    // load.  Sixteen positions per lane are in flight at a time (one at a time the
+    // loads' latency alone took 30 us for 65,536 tokens).
+    constexpr int kAhead = 4;
     const long long per = ((p.T + kEmbSortThreads * 4 - 1) / (kEmbSortThreads * 4)) * 128;
     const long long t0 = warp * per, t1 = min(p.T, t0 + per);
-    int below = 0;
+    int below = 0, kept = 0;
     bool bad = false;
-    for (long long t = t0 + lane; t < t1; t += 128) {
-        int v[4];
+    for (long long t = t0; t < t1; t += 128 * kAhead) {
+        int v[kAhead][4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = t + 32 * k < t1 ? emb_token(p, t + 32 * k) : -2;
+        for (int k = 0; k < kAhead; ++k) {
+            const long long u = t + 128 * k + 4 * lane;
+            if (u < t1)
+                emb_tokens4(p, u, v[k]);
+            else
+                v[k][0] = v[k][1] = v[k][2] = v[k][3] = -2;
+        }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            bad |= v[k] == -1;
-            if (v[k] >= 0 && v[k] != p.padding) {
-                below += v[k] < lo;
-                if ((unsigned)(v[k] - lo) < (unsigned)nr) atomicAdd(&mine[v[k] - lo], 1);
+        for (int k = 0; k < kAhead; ++k) {
+            unsigned in = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                bad |= v[k][j] == -1;
+                const bool ok = v[k][j] >= 0 && v[k][j] != p.padding;
+                below += ok && v[k][j] < lo;
+                if (ok && (unsigned)(v[k][j] - lo) < (unsigned)nr) in |= 1u << j;
             }
+            if (!__any_sync(0xffffffffu, in)) continue;
+            // Keep the matches in the order of their positions: lane by lane, four in each.
+            const int n = __popc(in);
+            int at = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, at, o);
+                if (lane >= o) at += y;
+            }
+            const int all = __shfl_sync(0xffffffffu, at, 31);
+            at += kept - n;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (in >> j & 1u) {
+                    const int r = v[k][j] - lo;
+                    atomicAdd(&mine[r], 1);
+                    if (at < kEmbSortKept) kept_t[warp][at] = (int)(t + 128 * k + 4 * lane + j), kept_r[warp][at] = r;
+                    ++at;
+                }
+            kept += all;
         }
     }
     if (blockIdx.x == 0 && bad) atomicOr(&g_status, kStatusBadToken);
@@ -145,32 +207,54 @@ __global__ void __launch_bounds__(kEmbSortThreads, 1) emb_sort_kernel(const __gr
     int n[2], own = 0;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const int r = threadIdx.x * 2 + k;
+        const int r = threadIdx.x + k * kEmbSortThreads;
         n[k] = 0;
         if (r < nr)
+#pragma unroll 8
             for (int w = 0; w < kEmbSortWarps; ++w) n[k] += hist[w * R + r];
-        own += n[k];
     }
-    int at = base + block_exclusive_1024(own, &total);
+    int at[2];
+    at[0] = base + block_exclusive_1024(n[0], &own);
+    at[1] = base + own + block_exclusive_1024(n[1], &total);
+    total += own;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const int r = threadIdx.x * 2 + k;
+        const int r = threadIdx.x + k * kEmbSortThreads;
         if (r < nr) {
             p.count[lo + r] = n[k];
             first[r] = n[k];
-            int o = at;
-            for (int w = 0; w < kEmbSortWarps; ++w) {
-                const int c = hist[w * R + r];
-                hist[w * R + r] = o;
-                o += c;
-            }
+            int o = at[k];
+            if (n[k])
+#pragma unroll 8
+                for (int w = 0; w < kEmbSortWarps; ++w) {
+                    const int c = hist[w * R + r];
+                    hist[w * R + r] = o;
+                    o += c;
+                }
         }
-        at += n[k];
     }
     if (threadIdx.x == 0 && blockIdx.x == gridDim.x - 1) p.meta[0] = base + total, p.meta[1] = 0;
     __syncthreads();
-    if (total > 0) {
-        // The positions again, each warp's in order; equal rows of 32 positions take consecutive entries.
+    // The matches in order; equal rows of 32 of them take consecutive entries.
+    auto place = [&](bool in, long long t, int r) {
+        const unsigned who = __ballot_sync(0xffffffffu, in);
+        if (in) {
+            const unsigned same = __match_any_sync(who, r);
+            const int rank = __popc(same & ((1u << lane) - 1u));
+            const int e = mine[r] + rank;
+            p.list[e] = (int)t;
+            p.row[e] = lo + r;
+            __syncwarp(who);
+            if (rank == 0) mine[r] += __popc(same);
+        }
+        __syncwarp();
+    };
+    if (kept <= kEmbSortKept) {
+        for (int i = 0; i < kept; i += 32) {
+            const bool in = i + lane < kept;
+            place(in, in ? kept_t[warp][i + lane] : 0, in ? kept_r[warp][i + lane] : 0);
+        }
+    } else {  // more than were kept (a frequent token, or a small table): the positions again
         for (long long t = t0; t < t1; t += 128) {
             int v[4];
 #pragma unroll
@@ -178,31 +262,15 @@ __global__ void __launch_bounds__(kEmbSortThreads, 1) emb_sort_kernel(const __gr
                 v[k] = t + 32 * k + lane < t1 ? emb_token(p, t + 32 * k + lane) : -1;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const bool in = (unsigned)(v[k] - lo) < (unsigned)nr && v[k] >= 0 && v[k] != p.padding;
-                const unsigned who = __ballot_sync(0xffffffffu, in);
-                if (!who) continue;
-                if (in) {
-                    const unsigned same = __match_any_sync(who, v[k]);
-                    const int rank = __popc(same & ((1u << lane) - 1u));
-                    const int e = mine[v[k] - lo] + rank;
-                    p.list[e] = (int)(t + 32 * k + lane);
-                    p.row[e] = v[k];
-                    __syncwarp(who);
-                    if (rank == 0) mine[v[k] - lo] += __popc(same);
-                }
-                __syncwarp();
+                const bool in = v[k] >= 0 && v[k] != p.padding && (unsigned)(v[k] - lo) < (unsigned)nr;
+                if (__any_sync(0xffffffffu, in)) place(in, t + 32 * k + lane, v[k] - lo);
             }
         }
     }
     // Zeros of the rows without a token: a warp per row.
-    if (!p.accumulate) {
-        const float zero[VEC] = {};
-        for (int r = warp; r < nr; r += kEmbSortWarps) {
-            if (first[r]) continue;
-            TG* out = static_cast<TG*>(p.out) + (long long)(lo + r) * p.ld_table;
-            for (int c = lane * VEC; c < p.D; c += 32 * VEC) store_f32<TG, VEC>(out + c, zero);
-        }
-    }
+    if (!p.accumulate)
+        for (int r = warp; r < nr; r += kEmbSortWarps)
+            if (!first[r]) emb_zero_row(static_cast<TG*>(p.out) + (long long)(lo + r) * p.ld_table, p.D, lane);
 }
 
 // A finished row's 256 columns: scaled, added to what is there when accumulating, rounded.
@@ -239,64 +307,75 @@ __global__ void __launch_bounds__(256) emb_reduce_kernel(const __grid_constant__
     const int n = p.meta[0], e0 = w * kEmbWindow;
     if (e0 >= n) return;
     const int m = min(kEmbWindow, n - e0);
-    int pos = 0, row = -1;
-    if (lane < m) pos = p.list[e0 + lane], row = p.row[e0 + lane];
-    // The run that enters the window, and the one that leaves it.
+    // The window's rows, where runs end in it, and the runs that cross its borders.
+    const int wrow = p.row[min(e0 + lane, e0 + m - 1)];
     const int prev = e0 > 0 ? p.row[e0 - 1] : -1, next = e0 + m < n ? p.row[e0 + m] : -1;
-    const int up = __shfl_down_sync(0xffffffffu, row, 1);
-    const unsigned ends = __ballot_sync(0xffffffffu, lane < m && (lane == m - 1 || up != row));
+    const int head = __shfl_sync(0xffffffffu, wrow, 0), tail = __shfl_sync(0xffffffffu, wrow, m - 1);
+    const int ncut = head == prev ? p.count[head] : 0, ntail = tail == next ? p.count[tail] : 0;
+    const bool entered = ncut > kEmbShort, leaves = ntail > kEmbShort;  // long runs that cross
+    int b = e0, e = e0 + m;
+    if (ncut && !entered) b += __popc(__ballot_sync(0xffffffffu, lane < m && wrow == head));  // an earlier window's run
+    int tail0 = 0;  // first entry in the window of the run that goes on after it
+    if (ntail) tail0 = e0 + m - __popc(__ballot_sync(0xffffffffu, lane < m && wrow == tail));
+    if (ntail && !leaves && b < e) e = tail0 + ntail;  // this window's run, to its end
     const int c0 = tile * kEmbTile + lane * VEC;
+    int col[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) col[j] = min(c0 + j * 32 * VEC, p.D - VEC);  // columns past the row read its last ones
     const TY* dy = static_cast<const TY*>(p.in);
     float s[8] = {};
-    bool entered = __shfl_sync(0xffffffffu, row, 0) == prev;
-    int begin = 0;
-    for (int i0 = 0; i0 < m; i0 += AHEAD) {
-        float f[AHEAD][8];
+    bool from_before = entered;
+    for (int base = b; base < e; base += 32) {
+        const int k = min(32, e - base);
+        const int pos = p.list[min(base + lane, e - 1)], row = p.row[min(base + lane, e - 1)];
+        const int after = base + lane + 1 < e ? p.row[base + lane + 1] : -1;
+        const unsigned ends = __ballot_sync(0xffffffffu, after != row);
+        for (int i0 = 0; i0 < k; i0 += AHEAD) {
+            // Eight rows in flight; entries past the last read its row again.
+            Vec<TY, VEC> f[AHEAD][NV];
 #pragma unroll
-        for (int a = 0; a < AHEAD; ++a) {
-            const long long t = __shfl_sync(0xffffffffu, pos, (i0 + a) & 31);
+            for (int a = 0; a < AHEAD; ++a) {
+                const long long t = __shfl_sync(0xffffffffu, pos, i0 + a);
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int c = c0 + j * 32 * VEC;
-                float g[VEC] = {};
-                if (i0 + a < m && c < p.D) load_f32<TY, VEC>(dy + t * p.ld_out + c, g);
-#pragma unroll
-                for (int k = 0; k < VEC; ++k) f[a][j * VEC + k] = g[k];
+                for (int j = 0; j < NV; ++j)
+                    f[a][j] = *reinterpret_cast<const Vec<TY, VEC>*>(dy + t * p.ld_out + col[j]);
             }
-        }
 #pragma unroll
-        for (int a = 0; a < AHEAD; ++a) {
-            const int i = i0 + a;
-            if (i >= m) break;
+            for (int a = 0; a < AHEAD; ++a) {
+                const int i = i0 + a;
+                if (i >= k) break;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) s[k] += f[a][k];
-            if (!(ends >> i & 1u)) continue;
-            const int v = __shfl_sync(0xffffffffu, row, i);
-            const bool leaves = i == m - 1 && v == next;
-            if (!entered && !leaves) {
-                emb_write<TG, VEC>(p, v, c0, s);
-            } else {
-                float* q = p.part + ((long long)w * 2 + (entered ? 0 : 1)) * p.D;
+                for (int j = 0; j < NV; ++j)
 #pragma unroll
-                for (int j = 0; j < NV; ++j) {
-                    const int c = c0 + j * 32 * VEC;
-                    float g[VEC];
+                    for (int q = 0; q < VEC; ++q) s[j * VEC + q] += to_f32<TY>(f[a][j].v[q]);
+                if (!(ends >> i & 1u)) continue;
+                const int v = __shfl_sync(0xffffffffu, row, i);
+                const bool on = leaves && base + i == e - 1;
+                if (!from_before && !on) {
+                    emb_write<TG, VEC>(p, v, c0, s);
+                } else {
+                    float* q = p.part + ((long long)w * 2 + (from_before ? 0 : 1)) * p.D;
 #pragma unroll
-                    for (int k = 0; k < VEC; ++k) g[k] = s[j * VEC + k];
-                    if (c < p.D) store_f32<float, VEC>(q + c, g);
+                    for (int j = 0; j < NV; ++j) {
+                        const int c = c0 + j * 32 * VEC;
+                        float g[VEC];
+#pragma unroll
+                        for (int x = 0; x < VEC; ++x) g[x] = s[j * VEC + x];
+                        if (c < p.D) store_f32<float, VEC>(q + c, g);
+                    }
+                    if (!from_before && tile == 0 && lane == 0)
+                        p.cross[atomicAdd(&p.meta[1], 1)] = make_int4(v, tail0, ntail, 0);
                 }
-                if (!entered && tile == 0 && lane == 0)
-                    p.cross[atomicAdd(&p.meta[1], 1)] = make_int4(v, e0 + begin, p.count[v], 0);
-            }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) s[k] = 0.f;
-            entered = false;
-            begin = i + 1;
+                for (int x = 0; x < 8; ++x) s[x] = 0.f;
+                from_before = false;
+            }
         }
     }
 }
 
-// The partial rows of a run, in the windows' order: eight warps a contiguous range each, then the eight sums.
+// The partial rows of a long run, in the windows' order: eight warps a contiguous
+// range each, then the eight sums.
 template <typename TG, int VEC>
 __global__ void __launch_bounds__(256) emb_join_kernel(const __grid_constant__ EmbParams p, int tiles)
 {
@@ -307,17 +386,16 @@ __global__ void __launch_bounds__(256) emb_join_kernel(const __grid_constant__ E
     const int runs = p.meta[1];
     for (long long item = blockIdx.x; item < (long long)runs * tiles; item += gridDim.x) {
         const int4 run = p.cross[item / tiles];
-        const int tile = (int)(item % tiles), c0 = tile * kEmbTile;
+        const int tile = (int)(item % tiles), c0 = tile * kEmbTile + lane;
         const int a = run.y / kEmbWindow, b = (run.y + run.z - 1) / kEmbWindow;
         const int per = (b - a + 1 + 7) / 8;
         const int w0 = a + warp * per, w1 = min(b + 1, w0 + per);
         float s[8] = {};
 #pragma unroll 4
         for (int w = w0; w < w1; ++w) {
-            const float* q = p.part + ((long long)w * 2 + (w == a ? 1 : 0)) * p.D + c0;
+            const float* q = p.part + ((long long)w * 2 + (w == a ? 1 : 0)) * p.D;
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (c0 + lane + 32 * k < p.D) s[k] += q[lane + 32 * k];
+            for (int k = 0; k < 8; ++k) s[k] += q[min(c0 + 32 * k, p.D - 1)];
         }
 #pragma unroll
         for (int k = 0; k < 8; ++k) sums[warp][lane + 32 * k] = s[k];
@@ -330,7 +408,7 @@ __global__ void __launch_bounds__(256) emb_join_kernel(const __grid_constant__ E
                 for (int j = 0; j < 8 / VEC; ++j)
 #pragma unroll
                     for (int k = 0; k < VEC; ++k) t[j * VEC + k] += sums[w][l + j * 32 * VEC + k];
-            emb_write<TG, VEC>(p, run.x, c0 + l, t);
+            emb_write<TG, VEC>(p, run.x, tile * kEmbTile + l, t);
         }
         __syncthreads();
     }

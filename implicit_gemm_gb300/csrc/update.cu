@@ -239,7 +239,7 @@ wg::EmbParams emb_params(const EmbPlan& pl, const void* token, const void* in, v
     const wg_embedding_problem& q = pl.p;
     wg::EmbParams p = {};
     p.T = q.tokens, p.V = q.vocab, p.D = q.dim, p.ld_table = q.ld_table, p.ld_out = q.ld_out;
-    p.token = token, p.token64 = q.token_bits == 64, p.padding = q.padding_token, p.scale = q.scale;
+    p.token = token, p.token64 = q.token_bits == 64, p.token16 = aligned16(token), p.padding = q.padding_token, p.scale = q.scale;
     p.in = in, p.out = out;
     return p;
 }
@@ -271,9 +271,9 @@ template <typename TG, typename TY, int V>
 int emb_bwd_v(const EmbPlan& pl, const wg::EmbParams& p, cudaStream_t s)
 {
     const int smem = wg::kEmbSortWarps * pl.R * 4;
-    int st = wg::ensure_smem(wg::emb_sort_kernel<TG, V>, smem);
+    int st = wg::ensure_smem(wg::emb_sort_kernel<TG>, smem);
     if (!st)
-        st = launch("emb_sort_kernel launch", wg::emb_sort_kernel<TG, V>, dim3((p.V + pl.R - 1) / pl.R),
+        st = launch("emb_sort_kernel launch", wg::emb_sort_kernel<TG>, dim3((p.V + pl.R - 1) / pl.R),
                     dim3(wg::kEmbSortThreads), smem, s, p);
     if (st || p.T == 0) return st;
     const int tiles = (p.D + wg::kEmbTile - 1) / wg::kEmbTile;
