@@ -113,13 +113,44 @@ __device__ __forceinline__ float muon_load(const void* in, int dtype, long long 
     return to_f32(static_cast<const __half*>(in)[e]);
 }
 
-// The results of an element of X.
-__device__ __forceinline__ void muon_finish(const MuonParams& p, long long e, float x)
+// The results of an element, o = scale X.
+__device__ __forceinline__ void muon_finish(const MuonParams& p, long long e, float o)
 {
-    const float o = p.scale * x;
     if (p.out) muon_store(p.out, p.out_dtype, e, o);
     if (p.weight)
         muon_store(p.weight, p.weight_dtype, e, fmaf(p.keep, muon_load(p.weight, p.weight_dtype, e), -p.lr * o));
+}
+
+__device__ __forceinline__ void muon_store8(void* out, int dtype, long long e, const float (&v)[8])
+{
+    if (dtype == 2)
+        store_f32<float, 8>(static_cast<float*>(out) + e, v);
+    else if (dtype == 0)
+        store_f32<__nv_bfloat16, 8>(static_cast<__nv_bfloat16*>(out) + e, v);
+    else
+        store_f32<__half, 8>(static_cast<__half*>(out) + e, v);
+}
+__device__ __forceinline__ void muon_load8(const void* in, int dtype, long long e, float (&v)[8])
+{
+    if (dtype == 2)
+        load_f32<float, 8>(static_cast<const float*>(in) + e, v);
+    else if (dtype == 0)
+        load_f32<__nv_bfloat16, 8>(static_cast<const __nv_bfloat16*>(in) + e, v);
+    else
+        load_f32<__half, 8>(static_cast<const __half*>(in) + e, v);
+}
+
+// The results of eight elements along a row (every address 16-byte aligned).
+__device__ __forceinline__ void muon_finish8(const MuonParams& p, long long e, const float (&o)[8])
+{
+    if (p.out) muon_store8(p.out, p.out_dtype, e, o);
+    if (p.weight) {
+        float w[8];
+        muon_load8(p.weight, p.weight_dtype, e, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = fmaf(p.keep, w[i], -p.lr * o[i]);
+        muon_store8(p.weight, p.weight_dtype, e, w);
+    }
 }
 
 // x times 2^8 as two fp16 values.
@@ -149,7 +180,7 @@ __global__ void __launch_bounds__(256) muon_normalize_kernel(const __grid_consta
         }
         const float x = u * inv;
         if (last) {
-            muon_finish(p, e, x);
+            muon_finish(p, e, p.scale * x);
         } else {
             const long long k = blockIdx.y * p.xs + (long long)r * p.ldx + c;
             muon_split(kMuonXScale * x, &p.x[0][k], &p.xlo[k]);
@@ -218,7 +249,7 @@ __global__ void __launch_bounds__(256)
                 const float x = __half2float(p.x[g.xin][e]) + __half2float(p.xlo[e]);
                 const float y = fmaf(g.a, x, d * 0x1p-10f);
                 if (g.last)
-                    muon_finish(p, (long long)b * p.bs + i * p.ld + j, y * (1.f / kMuonXScale));
+                    muon_finish(p, (long long)b * p.bs + i * p.ld + j, p.scale * (y * (1.f / kMuonXScale)));
                 else
                     muon_split(y, &p.x[g.xin ^ 1][e], &p.xlo[e]);
             }

@@ -1,0 +1,568 @@
+// Orthogonalised update of matrices whose shorter side is at most 128, in one
+// launch: the whole iteration runs on the Gram matrix.
+//
+// With A = X X^T and P = a I + b A + c A A a step is X <- P X, so A <- P A P and
+// X_k = Q_k X_0 with Q <- P Q.  All of these are polynomials of one symmetric
+// matrix: they commute, and one shared-memory copy of each serves as either
+// operand of an MMA.  X itself is read twice (A_0 = U U^T and
+// X = Q U) instead of twice a step, and the steps touch m x m matrices only.
+//
+// Precision: errors of A in directions of small singular values grow by a^2 a
+// step, so A, P and Q keep 22 bits: every operand is a pair of fp16 values (what
+// the first rounds away is the second), a product three MMAs, sums fp32 in
+// tensor memory.  (With single fp16 operands gradients of low rank lose every
+// digit.)  U is a pair of bf16 values (16 bits; exact for 16-bit gradients), its
+// range is fp32's.
+//
+// A block of P = 64 or 128 rows of the Gram matrix holds as many whole matrices
+// as fit (the block-diagonal fold of the convolution kernels): entries between
+// different matrices are set to zero after every product.  A matrix that holds a
+// NaN or an infinity enters as zeros and leaves as NaN, so that it cannot reach
+// the others of its block.
+//
+// A cluster of C CTAs takes a block.  Each adds up U U^T over its 64-column
+// chunks of the long side (the momentum's step on the way); the C partial sums
+// are added slice by slice through distributed shared memory into rank 0, which
+// alone runs the steps; Q goes through the workspace, and every CTA multiplies
+// its chunks of U, which it reads again (L2), and writes its part of the results.
+// Bound by latency: three dependent products a step, each MMA -> tensor memory ->
+// registers -> shared memory.
+#pragma once
+
+#include <type_traits>
+
+#include "k_muon.cuh"
+
+namespace wg {
+
+constexpr int kGramThreads = 512;
+constexpr int kGramMaxSteps = 16;
+
+struct GramParams {
+    MuonParams p;
+    int N;           // long side
+    int F;           // matrices per block
+    int wide;        // rows <= cols
+    int chunks;      // 64-column chunks of the long side
+    int C;           // CTAs of a cluster
+    int vec;         // eight elements along memory of grad and momentum are aligned and of one matrix
+    int ovec;        // and of weight and out
+    int split;       // U needs its second bf16 value
+    int steps;
+    float coef[kGramMaxSteps][3];
+    float sa[kGramMaxSteps], sp[kGramMaxSteps], ss[kGramMaxSteps], sq[kGramMaxSteps];  // powers of two of the operands
+    uint8_t* q;      // [blocks][P == 64 ? 16 : 64 KB] operand image of Q, bf16 pairs
+    float* factor;   // [blocks][128] scale / (|u|_F + eps) per row of a block
+};
+
+__host__ __device__ constexpr int gram_mat_bytes(int P) { return P * P * 2; }  // one fp16 image
+// Three pairs of images, and slack for A operands of 128 rows read from images of 64.
+__host__ __device__ constexpr int gram_smem_bytes(int P) { return 6 * gram_mat_bytes(P) + 8192 + 2048; }
+
+// Byte offset of the 16-byte chunk that holds elements 8 c8 .. 8 c8 + 7 of row r of a K-major image of P rows:
+// 64-element (128-byte) columns of P rows, 128-byte swizzle.
+template <int P>
+__device__ __forceinline__ uint32_t gram_off(int r, int c8)
+{
+    return (uint32_t)((c8 >> 3) * (P * 128) + r * 128 + (((c8 & 7) ^ (r & 7)) << 4));
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(__float_as_uint(v[0])),
+        "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
+        "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])),
+        "r"(__float_as_uint(v[7])), "r"(__float_as_uint(v[8])), "r"(__float_as_uint(v[9])),
+        "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])), "r"(__float_as_uint(v[12])),
+        "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])), "r"(__float_as_uint(v[15])), "r"(taddr)
+        : "memory");
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// NC (a multiple of 16) consecutive tensor-memory columns of this warp's lanes.
+template <int NC>
+__device__ __forceinline__ void gram_ld(uint32_t taddr, float (&v)[NC])
+{
+    uint32_t r[NC];
+#pragma unroll
+    for (int i = 0; i < NC; i += 16) tmem_ld16_issue(taddr + i, r + i);
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < NC; i += 16) reg_fence16(r + i);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float a, float b)
+{
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_bf162(float a, float b)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_half2(uint32_t x)
+{
+    return __half22float2(*reinterpret_cast<const __half2*>(&x));
+}
+__device__ __forceinline__ float2 unpack_bf162(uint32_t x)
+{
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x));
+}
+
+// Eight values as a pair of 16-bit chunks (BF: bf16, else fp16): hi, and what hi rounds away.
+template <bool BF>
+__device__ __forceinline__ void split8(const float* v, uint4* hi, uint4* lo)
+{
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        h[i] = BF ? pack_bf162(v[2 * i], v[2 * i + 1]) : pack_half2(v[2 * i], v[2 * i + 1]);
+        const float2 f = BF ? unpack_bf162(h[i]) : unpack_half2(h[i]);
+        l[i] = BF ? pack_bf162(v[2 * i] - f.x, v[2 * i + 1] - f.y) : pack_half2(v[2 * i] - f.x, v[2 * i + 1] - f.y);
+    }
+    *hi = make_uint4(h[0], h[1], h[2], h[3]);
+    *lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+// NC values of row r, columns c0 .., times s, into the image pair at `img` (shared memory).
+template <int P, int NC>
+__device__ __forceinline__ void gram_put(uint8_t* img, int r, int c0, const float (&v)[NC], float s)
+{
+#pragma unroll
+    for (int i = 0; i < NC; i += 8) {
+        float w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = v[i + k] * s;
+        uint4 hi, lo;
+        split8<false>(w, &hi, &lo);
+        uint8_t* o = img + gram_off<P>(r, (c0 + i) >> 3);
+        *reinterpret_cast<uint4*>(o) = hi;
+        *reinterpret_cast<uint4*>(o + gram_mat_bytes(P)) = lo;
+    }
+}
+
+// D[tmem] = X Y for two image pairs: hi hi + hi lo + lo hi.  X is read by rows
+// (K-major) and Y by columns (MN-major) of the same layout.  Reading Y by rows too
+// (symmetric up to roundings) transposes the roundings of Q between a direction
+// the matrix has and one it lacks, which are 482 times larger on one side than on
+// the other: gradients of rank one were 10% off.
+template <int P>
+__device__ __forceinline__ void gram_product(uint32_t d, uint32_t x, uint32_t y)
+{
+    const uint32_t idesc = make_idesc_f16(false, false, true, 128, P);
+    const uint64_t xd = make_sdesc(x, 16u, 1024u, 2u, 0u), yd = make_sdesc(y, P * 128u, 1024u, 2u, 0u);
+    constexpr uint64_t lo = gram_mat_bytes(P) >> 4;
+#pragma unroll
+    for (int ks = 0; ks < P / 16; ++ks) {
+        const uint64_t xo = (uint64_t)((ks >> 2) * (P * 8) + 2 * (ks & 3)), yo = (uint64_t)(128 * ks);
+        umma_f16(d, xd + xo, yd + yo, idesc, ks ? 1u : 0u);
+        umma_f16(d, xd + xo, yd + yo + lo, idesc, 1u);
+        umma_f16(d, xd + xo + lo, yd + yo, idesc, 1u);
+    }
+}
+
+__device__ __forceinline__ void st_dsmem_v4(uint32_t addr, float4 v)
+{
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z),
+                 "f"(v.w)
+                 : "memory");
+}
+
+// The eight values of u at `line`, `seg` .. of chunk `ch` of block `blk` (a line is
+// a row of the block when the matrices are wide and a position of the long side
+// when they are tall; seg runs along memory).  STEP: the momentum's step is taken
+// and written; otherwise it has been.  Outside the matrices: zeros.
+template <bool STEP>
+__device__ __forceinline__ void gram_load8(const GramParams& g, int blk, int ch, int line, int seg, float (&u)[8])
+{
+    const MuonParams& p = g.p;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) u[k] = 0.f;
+    long long e[8];
+    bool ok[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const int i = g.wide ? line : seg + k, n = ch * 64 + (g.wide ? seg + k : line);
+        const int f = i / p.m, b = blk * g.F + f, idx = i - f * p.m;
+        ok[k] = f < g.F && b < p.batch && n < g.N;
+        e[k] = (long long)b * p.bs + (g.wide ? idx * p.ld + n : n * p.ld + idx);
+        if (g.vec && k == 0) break;
+    }
+    if (g.vec) {
+        if (!ok[0]) return;
+        float x[8];
+        muon_load8(p.grad, p.grad_dtype, e[0], x);
+        if (!p.mom) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) u[k] = x[k];
+            return;
+        }
+        float m[8];
+        load_f32<float, 8>(p.mom + e[0], m);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float y = p.gain * x[k];
+            if (STEP) m[k] = fmaf(p.mu, m[k], y);
+            u[k] = p.nesterov ? fmaf(p.mu, m[k], y) : m[k];
+        }
+        if (STEP) store_f32<float, 8>(p.mom + e[0], m);
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        if (!ok[k]) continue;
+        float x = muon_elem(p, e[k]);
+        if (p.mom) {
+            x *= p.gain;
+            float m = p.mom[e[k]];
+            if (STEP) {
+                m = fmaf(p.mu, m, x);
+                p.mom[e[k]] = m;
+            }
+            x = p.nesterov ? fmaf(p.mu, m, x) : m;
+        }
+        u[k] = x;
+    }
+}
+
+template <int P>
+__global__ void __launch_bounds__(kGramThreads, 1) muon_gram_kernel(const __grid_constant__ GramParams g)
+{
+    constexpr int NC = P / 4;                     // columns per thread: four warps share a row
+    constexpr int MAT = gram_mat_bytes(P), PAIR = 2 * MAT;
+    constexpr int IMG = P * 128;                  // one staged image of 64 positions of the long side
+    constexpr uint32_t TA = 0, T2 = P, TQ = 2 * P;  // tensor-memory columns: A, (A A | A P), P Q
+    constexpr int TCOLS = P == 128 ? 512 : 256;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t bar[3];
+    __shared__ uint32_t tslot;
+    __shared__ float diag[128], fac[128];
+    __shared__ int bad[128];
+    uint8_t* smem = align_shared<uint8_t>(smem_raw, 1024);
+    uint8_t *ba = smem, *bp = smem + PAIR, *bq = smem + 2 * PAIR;  // A (and A P), P, Q
+    const MuonParams& p = g.p;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = (int)cluster_ctarank(), blk = blockIdx.x / g.C;
+    // This thread's part of a Gram-sized matrix: row, first column, and the columns of the row's own matrix.
+    const int row = (warp & 3) * 32 + lane, c0 = (warp >> 2) * NC;
+    const bool act = row < P;
+    const int mine = row / p.m, lo = mine * p.m, hi = mine < g.F ? lo + p.m : lo;
+    bool ok = true;
+    uint32_t ph[3] = {0, 0, 0};
+    auto wait = [&](int b) {
+        if (ok) ok = mbar_wait(&bar[b], ph[b]);
+        ph[b] ^= 1u;
+        __syncwarp();
+        tc_fence_after();
+    };
+
+    pdl_launch_dependents();
+    if (tid == 0) {
+        for (int i = 0; i < 3; ++i) mbar_init(&bar[i], 1);
+        fence_mbar_init();
+    }
+    if (tid < 128) bad[tid] = 0;
+    pdl_wait();
+    if (warp == 0) {
+        tmem_alloc(&tslot, TCOLS);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tb = tslot, trow = tb + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)c0;
+
+    // ---------------------------------------------------- A_0 = U U^T over this CTA's chunks
+    // Two staged images (pairs), in A's place.  Wide: rows of the block, 64
+    // positions along; tall: 64 positions, the block's rows along, in 64-wide atoms.
+    const int line = tid >> 3, seg = (tid & 7) * 8;
+    auto stage = [&](uint8_t* img, const float (&u)[P / 64][8]) {
+#pragma unroll
+        for (int j = 0; j < P / 64; ++j) {
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                v[k] = u[j][k];
+                if (!(fabsf(v[k]) < INFINITY)) {
+                    v[k] = 0.f;
+                    bad[(g.wide ? line + 64 * j : seg + 64 * j + k)] = 1;
+                }
+            }
+            uint4 h, l;
+            split8<true>(v, &h, &l);
+            uint8_t* o = img + j * 8192 + line * 128 + ((((tid & 7) ^ (line & 7))) << 4);
+            *reinterpret_cast<uint4*>(o) = h;
+            *reinterpret_cast<uint4*>(o + IMG) = l;
+        }
+    };
+    auto load = [&](int ch, auto step, float (&u)[P / 64][8]) {
+#pragma unroll
+        for (int j = 0; j < P / 64; ++j)
+            gram_load8<decltype(step)::value>(g, blk, ch, g.wide ? line + 64 * j : line, g.wide ? seg : seg + 64 * j, u[j]);
+    };
+    {
+        float u[P / 64][8];
+        int it = 0;
+        if (rank < g.chunks) load(rank, std::true_type{}, u);
+        for (int ch = rank; ch < g.chunks; ch += g.C, ++it) {
+            const int s = it & 1;
+            if (it >= 2) wait(s);
+            uint8_t* img = ba + s * 2 * IMG;
+            stage(img, u);
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncthreads();
+            if (tid == 0) {
+                tc_fence_after();
+                const uint32_t mn = g.wide ? 0u : 1u;
+                const uint32_t idesc = make_idesc_f16(true, mn, mn, 128, P);
+                const uint32_t a = smem_u32(img);
+                // Tall blocks of 64 rows: the second 64 rows of the MMA read the first again.
+                const uint64_t d = g.wide ? make_sdesc(a, 16u, 1024u, 2u, 0u)
+                                          : make_sdesc(a, P == 128 ? 8192u : 0u, 1024u, 2u, 0u);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) {
+                    const uint64_t o = (uint64_t)(ks * (g.wide ? 2 : 128)), l = IMG >> 4;
+                    umma_f16(tb + TA, d + o, d + o, idesc, (it | ks) ? 1u : 0u);
+                    if (g.split) {
+                        umma_f16(tb + TA, d + o, d + o + l, idesc, 1u);
+                        umma_f16(tb + TA, d + o + l, d + o, idesc, 1u);
+                    }
+                }
+                umma_commit(&bar[s]);
+            }
+            if (ch + g.C < g.chunks) load(ch + g.C, std::true_type{}, u);
+        }
+        if (it >= 2) wait(it & 1);
+        if (it >= 1) wait((it - 1) & 1);
+    }
+    // This CTA's partial sum in P's place (fp32 rows, 16-byte chunks swizzled by
+    // the row); NaN on the diagonal of a row that held a NaN or an infinity.
+    __syncthreads();
+    if (act) {
+        float v[NC];
+        gram_ld<NC>(trow + TA, v);
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            if (rank >= g.chunks) v[i] = 0.f;
+            if (c0 + i == row && bad[row]) v[i] = NAN;
+        }
+#pragma unroll
+        for (int i = 0; i < NC; i += 4)
+            *reinterpret_cast<float4*>(bp + row * (P * 4) + (((((c0 + i) >> 2)) ^ (row & 7)) << 4)) =
+                make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    }
+    cluster_sync_all();
+    {
+        // Rows rank * P / C .. of the sum over the cluster, into rank 0's Q.
+        const int chunks16 = P * P / 4 / g.C;  // 16-byte chunks of a slice
+        const uint32_t src = smem_u32(bp), dst = mapa_shared(smem_u32(bq), 0u);
+        for (int i = tid; i < chunks16; i += kGramThreads) {
+            const uint32_t o = (uint32_t)(rank * chunks16 + i) << 4;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int c = 0; c < g.C; ++c) {
+                const float4 x = ld_dsmem_v4(mapa_shared(src + o, (uint32_t)c));
+                s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+            }
+            st_dsmem_v4(dst + o, s);
+        }
+    }
+    cluster_sync_all();
+
+    // ---------------------------------------------------- the steps, on rank 0
+    uint8_t* qimg = g.q + (size_t)blk * PAIR;
+    if (rank == 0) {
+        float v[NC];
+        if (act) {
+#pragma unroll
+            for (int i = 0; i < NC; i += 4) {
+                const float4 x = *reinterpret_cast<const float4*>(bq + row * (P * 4) + (((((c0 + i) >> 2)) ^ (row & 7)) << 4));
+                v[i] = x.x, v[i + 1] = x.y, v[i + 2] = x.z, v[i + 3] = x.w;
+            }
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+                if (c0 + i == row) diag[row] = v[i];
+        }
+        __syncthreads();
+        if (act) {
+            // |u|_F^2 is the trace; A_0 = U U^T / (|u|_F + eps)^2, zero between matrices.
+            float s = 0.f;
+            for (int i = lo; i < hi; ++i) s += diag[i];
+            const float d = sqrtf(s) + p.eps;
+            const bool fin = s < INFINITY;
+            const float inv = fin && d > 0.f ? 1.f / d : 0.f;
+            if (c0 == 0) g.factor[blk * 128 + row] = fin ? p.scale * inv : NAN;
+#pragma unroll
+            for (int i = 0; i < NC; ++i) v[i] = fin && c0 + i >= lo && c0 + i < hi ? v[i] * inv * inv : 0.f;
+#pragma unroll
+            for (int i = 0; i < NC; i += 16) tmem_st16(trow + TA + i, v + i);
+            gram_put<P, NC>(ba, row, c0, v, g.sa[0]);
+        }
+        float ra = 1.f;  // A = ra * (tensor memory)
+        const uint32_t sba = smem_u32(ba), sbp = smem_u32(bp), sbq = smem_u32(bq);
+        auto ready = [&] {
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncthreads();
+        };
+        auto masked = [&](float x, int i) { return c0 + i >= lo && c0 + i < hi ? x : 0.f; };
+        for (int k = 0; k < g.steps; ++k) {
+            const bool last = k == g.steps - 1;
+            const float a = g.coef[k][0], b = g.coef[k][1], c = g.coef[k][2];
+            ready();
+            if (tid == 0) {
+                tc_fence_after();
+                gram_product<P>(tb + T2, sba, sba);
+                umma_commit(&bar[0]);
+            }
+            wait(0);
+            if (act) {
+                // P = a I + b A + c A A
+                float x[NC];
+                gram_ld<NC>(trow + T2, v);
+                gram_ld<NC>(trow + TA, x);
+                const float r2 = c / (g.sa[k] * g.sa[k]), r1 = b * ra;
+#pragma unroll
+                for (int i = 0; i < NC; ++i) v[i] = masked(fmaf(r2, v[i], fmaf(r1, x[i], c0 + i == row ? a : 0.f)), i);
+                gram_put<P, NC>(bp, row, c0, v, g.sp[k]);
+                if (k == 0 && !last) gram_put<P, NC>(bq, row, c0, v, g.sq[0]);
+            }
+            ready();
+            if (tid == 0) {
+                tc_fence_after();
+                if (!last) {
+                    gram_product<P>(tb + T2, sba, sbp);
+                    umma_commit(&bar[0]);
+                }
+                if (k > 0) {
+                    gram_product<P>(tb + TQ, sbp, sbq);
+                    umma_commit(&bar[1]);
+                }
+            }
+            if (!last) {
+                wait(0);
+                if (act) {
+                    // S = A P, in A's place
+                    gram_ld<NC>(trow + T2, v);
+                    const float r = 1.f / (g.sa[k] * g.sp[k]);
+#pragma unroll
+                    for (int i = 0; i < NC; ++i) v[i] = masked(v[i] * r, i);
+                    gram_put<P, NC>(ba, row, c0, v, g.ss[k]);
+                }
+                ready();
+                if (tid == 0) {
+                    tc_fence_after();
+                    gram_product<P>(tb + TA, sba, sbp);  // A <- S P
+                    umma_commit(&bar[2]);
+                }
+            }
+            if (k > 0) {
+                wait(1);
+                if (act) {
+                    gram_ld<NC>(trow + TQ, v);
+                    const float r = 1.f / (g.sp[k] * g.sq[k - 1]);
+#pragma unroll
+                    for (int i = 0; i < NC; ++i) v[i] = masked(v[i] * r, i);
+                    if (!last) gram_put<P, NC>(bq, row, c0, v, g.sq[k]);
+                }
+            }
+            if (!last) {
+                wait(2);
+                ra = 1.f / (g.ss[k] * g.sp[k]);
+                if (act) {
+                    gram_ld<NC>(trow + TA, v);
+#pragma unroll
+                    for (int i = 0; i < NC; ++i) v[i] = masked(v[i] * ra, i);
+                    gram_put<P, NC>(ba, row, c0, v, g.sa[k + 1]);
+                }
+                // What lies between matrices stays out of the next P as well: it is masked there.
+            }
+        }
+        if (act) {
+            // Q (v) as a pair of bf16 operand images, for every CTA of the cluster.
+#pragma unroll
+            for (int i = 0; i < NC; i += 8) {
+                uint4 h, l;
+                split8<true>(v + i, &h, &l);
+                uint8_t* o = qimg + gram_off<P>(row, (c0 + i) >> 3);
+                *reinterpret_cast<uint4*>(o) = h;
+                *reinterpret_cast<uint4*>(o + MAT) = l;
+            }
+        }
+        __threadfence();
+    }
+    cluster_sync_all();
+
+    // ---------------------------------------------------- results: X = Q U over this CTA's chunks
+    for (int i = tid; i < PAIR / 16; i += kGramThreads)
+        reinterpret_cast<uint4*>(bq)[i] = __ldcg(reinterpret_cast<const uint4*>(qimg) + i);
+    if (tid < P) fac[tid] = __ldcg(g.factor + blk * 128 + tid);
+    {
+        float u[P / 64][8];
+        if (rank < g.chunks) load(rank, std::false_type{}, u);
+        for (int ch = rank; ch < g.chunks; ch += g.C) {
+            stage(ba, u);
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncthreads();
+            if (tid == 0) {
+                tc_fence_after();
+                const uint32_t idesc = make_idesc_f16(true, false, g.wide != 0, 128, 64);
+                const uint32_t img = smem_u32(ba);
+                const uint64_t qd = make_sdesc(smem_u32(bq), 16u, 1024u, 2u, 0u);
+                const uint64_t ud = g.wide ? make_sdesc(img, 8192u, 1024u, 2u, 0u) : make_sdesc(img, 16u, 1024u, 2u, 0u);
+                const uint64_t ql = MAT >> 4, ul = IMG >> 4;
+#pragma unroll
+                for (int ks = 0; ks < P / 16; ++ks) {
+                    const uint64_t qo = (uint64_t)((ks >> 2) * (P * 8) + 2 * (ks & 3));
+                    const uint64_t uo = g.wide ? (uint64_t)(128 * ks) : (uint64_t)((ks >> 2) * 512 + 2 * (ks & 3));
+                    umma_f16(tb + T2, qd + qo, ud + uo, idesc, ks ? 1u : 0u);
+                    umma_f16(tb + T2, qd + qo + ql, ud + uo, idesc, 1u);
+                    if (g.split) umma_f16(tb + T2, qd + qo, ud + uo + ul, idesc, 1u);
+                }
+                umma_commit(&bar[0]);
+            }
+            if (ch + g.C < g.chunks) load(ch + g.C, std::false_type{}, u);
+            wait(0);
+            float x[16];
+            const int q0 = (warp >> 2) * 16;
+            if (act) gram_ld<16>(tb + ((uint32_t)((warp & 3) * 32) << 16) + T2 + (uint32_t)q0, x);
+            const int b = blk * g.F + mine;
+            if (act && mine < g.F && b < p.batch) {
+                const float f = fac[row];
+                const long long base = (long long)b * p.bs;
+                const int n0 = ch * 64 + q0;
+                if (g.wide && g.ovec) {
+#pragma unroll
+                    for (int i = 0; i < 16; i += 8) {
+                        float o[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) o[k] = f * x[i + k];
+                        if (n0 + i < g.N) muon_finish8(p, base + (row - lo) * p.ld + n0 + i, o);
+                    }
+                } else
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int n = n0 + i;
+                    if (n < g.N)
+                        muon_finish(p, base + (g.wide ? (row - lo) * p.ld + n : n * p.ld + (row - lo)), f * x[i]);
+                }
+            }
+            tc_fence_before();
+            __syncthreads();  // the staged image and the accumulator are free
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tb, TCOLS);
+    }
+}
+
+}  // namespace wg

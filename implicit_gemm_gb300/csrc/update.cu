@@ -4,16 +4,20 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
+#include <stddef.h>
 #include <stdio.h>
 #include <string.h>
 
 #include <algorithm>
+#include <map>
+#include <mutex>
 #include <string>
 
 #include "../../include/wgrad.h"
 #include "host.h"
 #include "k_embedding.cuh"
 #include "k_muon.cuh"
+#include "k_muon_gram.cuh"
 
 namespace wg {
 
@@ -72,9 +76,50 @@ constexpr int kMuonMaxDim = 32768, kMuonMaxSteps = 16, kMuonMaxParts = 304;
 struct MuonPlan {
     wg_muon_problem p;
     float coef[kMuonMaxSteps][3];
+    bool gram;            // the Gram-matrix kernel
+    wg::GramParams g;     // its problem (pointers are set by the call)
+    int P, blocks;        // rows of a block of the Gram matrix, blocks
     int ldx, m, ldm, nparts;
+    size_t off_q, off_factor;
     size_t off_x[2], off_xlo, off_a, off_b, off_part, bytes;
 };
+
+// The Gram-matrix kernel's problem: blocks of whole matrices, CTAs of a cluster,
+// and the powers of two that bring each operand's largest singular value to at
+// most 2^13 in fp16 (a factor of eight is left to roundings).
+void muon_gram_plan(MuonPlan* pl)
+{
+    const wg_muon_problem& q = pl->p;
+    wg::GramParams& g = pl->g;
+    g = wg::GramParams();
+    pl->P = pl->m <= 64 ? 64 : 128;
+    g.N = std::max(q.rows, q.cols);
+    g.F = std::min(pl->P / pl->m, q.batch);
+    g.wide = q.rows <= q.cols;
+    g.chunks = (g.N + 63) / 64;
+    g.steps = q.steps;
+    pl->blocks = (q.batch + g.F - 1) / g.F;
+    // A CTA per chunk up to the portable cluster size, while every block has its clusters at once.
+    g.C = 1;
+    while (g.C < 8 && 2 * g.C <= g.chunks && 2LL * g.C * pl->blocks <= num_sms()) g.C *= 2;
+    double grid[513], prod[513], smax = 1.0;
+    for (int i = 0; i <= 512; ++i) grid[i] = i / 512.0, prod[i] = 1.0;
+    auto power = [](double bound) { return ldexpf(1.f, (int)floor(log2(8192.0 / std::max(bound, 1e-6)))); };
+    for (int k = 0; k < q.steps; ++k) {
+        const float* c = pl->coef[k];
+        memcpy(g.coef[k], c, sizeof g.coef[k]);
+        double pmax = 0.0, spmax = 0.0, grown = 0.0, qmax = 0.0;
+        for (int i = 0; i <= 512; ++i) {
+            const double s = smax * i / 512, l = s * s, v = c[0] + c[1] * l + c[2] * l * l;
+            pmax = std::max(pmax, fabs(v)), spmax = std::max(spmax, l * fabs(v)), grown = std::max(grown, s * fabs(v));
+            const double t = grid[i] * grid[i], w = c[0] + c[1] * t + c[2] * t * t;
+            prod[i] *= w, grid[i] *= w;
+            qmax = std::max(qmax, fabs(prod[i]));
+        }
+        g.sa[k] = power(smax * smax), g.sp[k] = power(pmax), g.ss[k] = power(spmax), g.sq[k] = power(qmax);
+        smax = std::max(grown, 1e-3);
+    }
+}
 
 // Largest value over s in [0, smax] of what a step (a, b, c) makes of a singular
 // value s, and of |b s^2 + c s^4|, on a grid fine enough for a quintic.
@@ -88,7 +133,7 @@ void step_range(const float* k, double smax, double* grown, double* poly)
     }
 }
 
-int muon_plan(const wg_muon_problem* p, MuonPlan* pl)
+int make_muon_plan(const wg_muon_problem* p, MuonPlan* pl)
 {
     if (!p) return set_err(WG_ERR_INVALID_ARGUMENT, "problem is NULL");
     if (p->batch < 1 || p->rows < 1 || p->cols < 1)
@@ -129,8 +174,16 @@ int muon_plan(const wg_muon_problem* p, MuonPlan* pl)
     pl->ldm = (pl->m + 7) / 8 * 8;
     const long long n = (long long)q.rows * q.cols;
     pl->nparts = (int)std::max(1LL, std::min<long long>(kMuonMaxParts, (n + 2047) / 2048));
-    const size_t x = up256((size_t)q.batch * q.rows * pl->ldx * 2), a = up256((size_t)q.batch * pl->m * pl->ldm * 2);
     size_t o = 0;
+    pl->gram = q.steps > 0 && pl->m <= 128;
+    if (pl->gram) {
+        muon_gram_plan(pl);
+        pl->off_q = o, o += up256((size_t)pl->blocks * 2 * wg::gram_mat_bytes(pl->P));
+        pl->off_factor = o, o += up256((size_t)pl->blocks * 128 * 4);
+        pl->bytes = o;
+        return WG_OK;
+    }
+    const size_t x = up256((size_t)q.batch * q.rows * pl->ldx * 2), a = up256((size_t)q.batch * pl->m * pl->ldm * 2);
     pl->off_part = o, o += up256((size_t)q.batch * pl->nparts * 4);
     if (q.steps > 0) {
         pl->off_x[0] = o, o += x;
@@ -141,6 +194,56 @@ int muon_plan(const wg_muon_problem* p, MuonPlan* pl)
     }
     pl->bytes = o;
     return WG_OK;
+}
+
+// Plans are a pure function of the problem, its coefficients and the SM count;
+// successful ones are cached, so that repeated calls skip the range checks.
+int muon_plan(const wg_muon_problem* p, MuonPlan* pl)
+{
+    static std::mutex mu;
+    static std::map<std::string, MuonPlan> cache;
+    std::string key;
+    if (p && p->steps >= 0 && p->steps <= kMuonMaxSteps) {
+        // (The record without its pointer and its tail padding.)
+        const int sms = num_sms();
+        key.assign(reinterpret_cast<const char*>(p), offsetof(wg_muon_problem, coef));
+        key.append(reinterpret_cast<const char*>(&p->mu), 6 * sizeof(float));
+        key.append(reinterpret_cast<const char*>(&sms), sizeof sms);
+        if (p->coef) key.append(reinterpret_cast<const char*>(p->coef), (size_t)p->steps * 3 * sizeof(float));
+        std::lock_guard<std::mutex> lk(mu);
+        auto it = cache.find(key);
+        if (it != cache.end()) {
+            *pl = it->second;
+            return WG_OK;
+        }
+    }
+    const int st = make_muon_plan(p, pl);
+    if (st) return st;
+    std::lock_guard<std::mutex> lk(mu);
+    if (cache.size() > 1024) cache.clear();
+    cache.emplace(key, *pl);
+    return WG_OK;
+}
+
+template <int P>
+int muon_gram_launch(const MuonPlan& pl, const wg::GramParams& g, cudaStream_t s)
+{
+    const int smem = wg::gram_smem_bytes(P);
+    const int st = wg::ensure_smem(wg::muon_gram_kernel<P>, smem);
+    if (st) return st;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    unsigned na = 0;
+    attr[na].id = cudaLaunchAttributeClusterDimension;
+    attr[na].val.clusterDim.x = (unsigned)g.C;
+    attr[na].val.clusterDim.y = attr[na].val.clusterDim.z = 1;
+    ++na;
+    wg::pdl_config(&cfg, attr, &na, s);
+    cfg.gridDim = dim3((unsigned)(pl.blocks * g.C));
+    cfg.blockDim = dim3(wg::kGramThreads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, wg::muon_gram_kernel<P>, g);
+    return e == cudaSuccess ? WG_OK : cuda_fail("muon_gram_kernel launch", e);
 }
 
 int muon_run(const MuonPlan& pl, const void* grad, void* momentum, void* weight, void* out, char* ws, cudaStream_t s)
@@ -154,6 +257,16 @@ int muon_run(const MuonPlan& pl, const void* grad, void* momentum, void* weight,
     p.scale = q.scale, p.keep = 1.f - q.lr * q.weight_decay, p.lr = q.lr;
     p.ldx = pl.ldx, p.m = pl.m, p.ldm = pl.ldm;
     p.xs = (long long)q.rows * pl.ldx, p.ms = (long long)pl.m * pl.ldm;
+    if (pl.gram) {
+        wg::GramParams g = pl.g;
+        g.p = p;
+        const bool al = q.cols % 8 == 0 && q.ld % 8 == 0 && q.batch_stride % 8 == 0;
+        g.vec = al && aligned16(grad) && aligned16(momentum);
+        g.ovec = al && aligned16(weight) && aligned16(out);
+        g.split = momentum || q.grad_dtype != WG_BF16;
+        g.q = reinterpret_cast<uint8_t*>(ws + pl.off_q), g.factor = reinterpret_cast<float*>(ws + pl.off_factor);
+        return pl.P == 64 ? muon_gram_launch<64>(pl, g, s) : muon_gram_launch<128>(pl, g, s);
+    }
     p.part = reinterpret_cast<float*>(ws + pl.off_part), p.nparts = pl.nparts;
     if (q.steps > 0) {
         for (int i = 0; i < 2; ++i) p.x[i] = reinterpret_cast<__half*>(ws + pl.off_x[i]);
@@ -345,7 +458,12 @@ int wg_muon_plan_string(const wg_muon_problem* p, char* buf, size_t n)
     MuonPlan pl;
     const int st = muon_plan(p, &pl);
     if (st) return st;
-    snprintf(buf, n, "kernel=muon_gemm side=%s m=%d steps=%d ws=%zu", p->rows <= p->cols ? "left" : "right", pl.m,
+    if (pl.gram)
+        snprintf(buf, n, "kernel=muon_gram side=%s m=%d block=%d fold=%d blocks=%d cluster=%d chunks=%d steps=%d ws=%zu",
+                 p->rows <= p->cols ? "left" : "right", pl.m, pl.P, pl.g.F, pl.blocks, pl.g.C, pl.g.chunks, p->steps,
+                 pl.bytes);
+    else
+        snprintf(buf, n, "kernel=muon_gemm side=%s m=%d steps=%d ws=%zu", p->rows <= p->cols ? "left" : "right", pl.m,
              p->steps, pl.bytes);
     return WG_OK;
 }
