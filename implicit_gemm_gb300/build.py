@@ -20,7 +20,7 @@ LIBDIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(LIBDIR, "libwgrad.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("wgrad.cu", "update.cu", "plan.cpp")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("ptx.cuh", "vec.cuh", "host.h", "k_igemm.cuh", "k_igemm_pair.cuh",
-                                                  "k_depthwise.cuh", "k_dgrad.cuh", "k_muon.cuh", "k_muon_gram.cuh",
+                                                  "k_depthwise.cuh", "k_dgrad.cuh", "k_muon.cuh", "k_muon_gram.cuh", "k_muon_gemm.cuh",
                                                   "k_embedding.cuh",
                                                   "plan.h")] + [os.path.join(ROOT, "include", "wgrad.h")]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"

@@ -35,6 +35,7 @@ struct MuonParams {
     __half *x[2], *xlo, *a, *b;
     float* part;          // [batch][nparts] partial sums of squares
     int nparts;
+    int *arrived, narrived;  // counters of the products' parts, zeroed by the first kernel
 };
 
 constexpr float kMuonXScale = 256.f;
@@ -46,54 +47,38 @@ __device__ __forceinline__ float muon_elem(const MuonParams& p, long long i)
     return to_f32(static_cast<const __half*>(p.grad)[i]);
 }
 
-// Block sum in a fixed order; every thread gets it.
-__device__ __forceinline__ float block_sum_256(float s)
+__device__ __forceinline__ uint32_t pack_half2(float a, float b)
 {
-    __shared__ float red[8];
-#pragma unroll
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
-    __syncthreads();
-    s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s += red[i];
-    return s;
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_bf162(float a, float b)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_half2(uint32_t x)
+{
+    return __half22float2(*reinterpret_cast<const __half2*>(&x));
+}
+__device__ __forceinline__ float2 unpack_bf162(uint32_t x)
+{
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x));
 }
 
-// The momentum's step and the partial sums of u's squares.
-__global__ void __launch_bounds__(256) muon_momentum_kernel(const __grid_constant__ MuonParams p)
+// Eight values as a pair of 16-bit chunks (BF: bf16, else fp16): hi, and what hi rounds away.
+template <bool BF>
+__device__ __forceinline__ void split8(const float* v, uint4* hi, uint4* lo)
 {
-    pdl_launch_dependents();
-    pdl_wait();
-    const int n = p.rows * p.cols;
-    const long long base = (long long)blockIdx.y * p.bs;
-    float s = 0.f;
-    for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) {
-        const int r = i / p.cols;
-        const long long e = base + r * p.ld + (i - r * p.cols);
-        float u = muon_elem(p, e);
-        if (p.mom) {
-            u *= p.gain;
-            const float m = fmaf(p.mu, p.mom[e], u);
-            p.mom[e] = m;
-            u = p.nesterov ? fmaf(p.mu, m, u) : m;
-        }
-        s = fmaf(u, u, s);
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        h[i] = BF ? pack_bf162(v[2 * i], v[2 * i + 1]) : pack_half2(v[2 * i], v[2 * i + 1]);
+        const float2 f = BF ? unpack_bf162(h[i]) : unpack_half2(h[i]);
+        l[i] = BF ? pack_bf162(v[2 * i] - f.x, v[2 * i + 1] - f.y) : pack_half2(v[2 * i] - f.x, v[2 * i + 1] - f.y);
     }
-    s = block_sum_256(s);
-    if (threadIdx.x == 0) p.part[blockIdx.y * p.nparts + blockIdx.x] = s;
-}
-
-// 1 / (|u|_F + eps) of matrix b: 0 for a zero matrix, NaN when the sum of
-// squares is not finite.
-__device__ __forceinline__ float muon_inv_norm(const MuonParams& p, int b)
-{
-    float s = 0.f;
-    for (int i = threadIdx.x; i < p.nparts; i += 256) s += p.part[b * p.nparts + i];
-    s = block_sum_256(s);
-    const float d = sqrtf(s) + p.eps;
-    return !(s < INFINITY) ? NAN : d > 0.f ? 1.f / d : 0.f;
+    *hi = make_uint4(h[0], h[1], h[2], h[3]);
+    *lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
 __device__ __forceinline__ void muon_store(void* out, int dtype, long long e, float v)
@@ -153,107 +138,110 @@ __device__ __forceinline__ void muon_finish8(const MuonParams& p, long long e, c
     }
 }
 
-// x times 2^8 as two fp16 values.
-__device__ __forceinline__ void muon_split(float x, __half* hi, __half* lo)
+// Block sum in a fixed order; every thread gets it.
+__device__ __forceinline__ float block_sum_256(float s)
 {
-    *hi = __float2half_rn(x);
-    *lo = __float2half_rn(x - __half2float(*hi));
+    __shared__ float red[8];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+    __syncthreads();
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += red[i];
+    return s;
+}
+
+// u at VEC elements along a row.  STEP: the momentum's step is taken and written;
+// otherwise it has been.
+template <int VEC, bool STEP>
+__device__ __forceinline__ void muon_u(const MuonParams& p, long long e, float (&u)[VEC])
+{
+    if constexpr (VEC == 8)
+        muon_load8(p.grad, p.grad_dtype, e, u);
+    else
+        u[0] = muon_elem(p, e);
+    if (!p.mom) return;
+    float m[VEC];
+    load_f32<float, VEC>(p.mom + e, m);
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+        const float y = p.gain * u[k];
+        if (STEP) m[k] = fmaf(p.mu, m[k], y);
+        u[k] = p.nesterov ? fmaf(p.mu, m[k], y) : m[k];
+    }
+    if (STEP) store_f32<float, VEC>(p.mom + e, m);
+}
+
+// The momentum's step and the partial sums of u's squares.
+template <int VEC>
+__global__ void __launch_bounds__(256) muon_momentum_kernel(const __grid_constant__ MuonParams p)
+{
+    pdl_launch_dependents();
+    pdl_wait();
+    if (blockIdx.x == 0 && blockIdx.y == 0)
+        for (int i = threadIdx.x; i < p.narrived; i += 256) p.arrived[i] = 0;
+    const int nv = p.cols / VEC, n = p.rows * nv;
+    const long long base = (long long)blockIdx.y * p.bs;
+    float s = 0.f;
+#pragma unroll 2
+    for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) {
+        const int r = i / nv;
+        float u[VEC];
+        muon_u<VEC, true>(p, base + r * p.ld + (i - r * nv) * VEC, u);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) s = fmaf(u[k], u[k], s);
+    }
+    s = block_sum_256(s);
+    if (threadIdx.x == 0) p.part[blockIdx.y * p.nparts + blockIdx.x] = s;
+}
+
+// 1 / (|u|_F + eps) of matrix b: 0 for a zero matrix, NaN when the sum of
+// squares is not finite.
+__device__ __forceinline__ float muon_inv_norm(const MuonParams& p, int b)
+{
+    float s = 0.f;
+    for (int i = threadIdx.x; i < p.nparts; i += 256) s += p.part[b * p.nparts + i];
+    s = block_sum_256(s);
+    const float d = sqrtf(s) + p.eps;
+    return !(s < INFINITY) ? NAN : d > 0.f ? 1.f / d : 0.f;
 }
 
 // X = u / (|u|_F + eps) (or the results at once when there are no steps).
+template <int VEC>
 __global__ void __launch_bounds__(256) muon_normalize_kernel(const __grid_constant__ MuonParams p, int last)
 {
     pdl_launch_dependents();
     pdl_wait();
-    const int n = p.rows * p.cols;
+    const int nv = p.cols / VEC, n = p.rows * nv;
     const long long base = (long long)blockIdx.y * p.bs;
     const float inv = muon_inv_norm(p, blockIdx.y);
+#pragma unroll 2
     for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) {
-        const int r = i / p.cols, c = i - r * p.cols;
-        const long long e = base + r * p.ld + c;
-        float u;
-        if (p.mom) {
-            u = p.mom[e];
-            if (p.nesterov) u = fmaf(p.mu, u, p.gain * muon_elem(p, e));
-        } else {
-            u = muon_elem(p, e);
-        }
-        const float x = u * inv;
-        if (last) {
-            muon_finish(p, e, p.scale * x);
-        } else {
-            const long long k = blockIdx.y * p.xs + (long long)r * p.ldx + c;
-            muon_split(kMuonXScale * x, &p.x[0][k], &p.xlo[k]);
-        }
-    }
-}
-
-// One product of the iteration: D[i, j] = sum over k of P[i, k] Q[k, j], a 64 x 64
-// tile per CTA, with the epilogue of its stage:
-//   0: A = D;  1: B = b A + c D;  2: X' = a X + D (the results after the last step).
-struct MuonGemm {
-    const __half *P, *Q;
-    long long pi, pk, qk, qj, pb, qb;  // element strides, and between matrices
-    int M, N, K;
-    int stage, xin, last;
-    float a, b, c;
-};
-
-__global__ void __launch_bounds__(256)
-    muon_gemm_kernel(const __grid_constant__ MuonParams p, const __grid_constant__ MuonGemm g)
-{
-    pdl_launch_dependents();
-    pdl_wait();
-    __shared__ float sp[16][65], sq[16][65];
-    const int b = blockIdx.z, i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;
-    const __half *P = g.P + b * g.pb, *Q = g.Q + b * g.qb;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4] = {};
-    for (int k0 = 0; k0 < g.K; k0 += 16) {
-        for (int e = threadIdx.x; e < 1024; e += 256) {
-            int i = e >> 4, k = e & 15;
-            if (g.pi == 1) i = e & 63, k = e >> 6;
-            sp[k][i] = i0 + i < g.M && k0 + k < g.K ? __half2float(P[(i0 + i) * g.pi + (k0 + k) * g.pk]) : 0.f;
-            int j = e >> 4;
-            k = e & 15;
-            if (g.qj == 1) j = e & 63, k = e >> 6;
-            sq[k][j] = j0 + j < g.N && k0 + k < g.K ? __half2float(Q[(k0 + k) * g.qk + (j0 + j) * g.qj]) : 0.f;
-        }
-        __syncthreads();
+        const int r = i / nv, c = (i - r * nv) * VEC;
+        const long long e = base + r * p.ld + c, k = blockIdx.y * p.xs + (long long)r * p.ldx + c;
+        float u[VEC];
+        muon_u<VEC, false>(p, e, u);
+        if constexpr (VEC == 8) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            float u[4], v[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) u[r] = sp[k][ty * 4 + r], v[r] = sq[k][tx + 16 * r];
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) acc[r][q] = fmaf(u[r], v[q], acc[r][q]);
-        }
-        __syncthreads();
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int i = i0 + ty * 4 + r, j = j0 + tx + 16 * q;
-            if (i >= g.M || j >= g.N) continue;
-            const float d = acc[r][q];
-            if (g.stage == 0) {
-                p.a[b * p.ms + (long long)i * p.ldm + j] = __float2half_rn(d * 0x1p-6f);
-            } else if (g.stage == 1) {
-                const long long e = b * p.ms + (long long)i * p.ldm + j;
-                p.b[e] = __float2half_rn(fmaf(g.c * 0x1p-10f, d, g.b * __half2float(p.a[e])));
+            for (int q = 0; q < 8; ++q) u[q] *= last ? inv * p.scale : kMuonXScale * inv;
+            if (last) {
+                muon_finish8(p, e, u);
             } else {
-                const long long e = b * p.xs + (long long)i * p.ldx + j;
-                const float x = __half2float(p.x[g.xin][e]) + __half2float(p.xlo[e]);
-                const float y = fmaf(g.a, x, d * 0x1p-10f);
-                if (g.last)
-                    muon_finish(p, (long long)b * p.bs + i * p.ld + j, p.scale * (y * (1.f / kMuonXScale)));
-                else
-                    muon_split(y, &p.x[g.xin ^ 1][e], &p.xlo[e]);
+                uint4 h, l;
+                split8<false>(u, &h, &l);
+                *reinterpret_cast<uint4*>(p.x[0] + k) = h;
+                *reinterpret_cast<uint4*>(p.xlo + k) = l;
             }
+        } else if (last) {
+            muon_finish(p, e, u[0] * inv * p.scale);
+        } else {
+            const float x = kMuonXScale * (u[0] * inv);
+            p.x[0][k] = __float2half_rn(x);
+            p.xlo[k] = __float2half_rn(x - __half2float(__float2half_rn(x)));
         }
+    }
 }
 
 }  // namespace wg

@@ -95,40 +95,6 @@ __device__ __forceinline__ void gram_ld(uint32_t taddr, float (&v)[NC])
     for (int i = 0; i < NC; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-__device__ __forceinline__ uint32_t pack_half2(float a, float b)
-{
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t pack_bf162(float a, float b)
-{
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ float2 unpack_half2(uint32_t x)
-{
-    return __half22float2(*reinterpret_cast<const __half2*>(&x));
-}
-__device__ __forceinline__ float2 unpack_bf162(uint32_t x)
-{
-    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x));
-}
-
-// Eight values as a pair of 16-bit chunks (BF: bf16, else fp16): hi, and what hi rounds away.
-template <bool BF>
-__device__ __forceinline__ void split8(const float* v, uint4* hi, uint4* lo)
-{
-    uint32_t h[4], l[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        h[i] = BF ? pack_bf162(v[2 * i], v[2 * i + 1]) : pack_half2(v[2 * i], v[2 * i + 1]);
-        const float2 f = BF ? unpack_bf162(h[i]) : unpack_half2(h[i]);
-        l[i] = BF ? pack_bf162(v[2 * i] - f.x, v[2 * i + 1] - f.y) : pack_half2(v[2 * i] - f.x, v[2 * i + 1] - f.y);
-    }
-    *hi = make_uint4(h[0], h[1], h[2], h[3]);
-    *lo = make_uint4(l[0], l[1], l[2], l[3]);
-}
-
 // NC values of row r, columns c0 .., times s, into the image pair at `img` (shared memory).
 template <int P, int NC>
 __device__ __forceinline__ void gram_put(uint8_t* img, int r, int c0, const float (&v)[NC], float s)
@@ -195,38 +161,15 @@ __device__ __forceinline__ void gram_load8(const GramParams& g, int blk, int ch,
     }
     if (g.vec) {
         if (!ok[0]) return;
-        float x[8];
-        muon_load8(p.grad, p.grad_dtype, e[0], x);
-        if (!p.mom) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) u[k] = x[k];
-            return;
-        }
-        float m[8];
-        load_f32<float, 8>(p.mom + e[0], m);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float y = p.gain * x[k];
-            if (STEP) m[k] = fmaf(p.mu, m[k], y);
-            u[k] = p.nesterov ? fmaf(p.mu, m[k], y) : m[k];
-        }
-        if (STEP) store_f32<float, 8>(p.mom + e[0], m);
+        muon_u<8, STEP>(p, e[0], u);
         return;
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         if (!ok[k]) continue;
-        float x = muon_elem(p, e[k]);
-        if (p.mom) {
-            x *= p.gain;
-            float m = p.mom[e[k]];
-            if (STEP) {
-                m = fmaf(p.mu, m, x);
-                p.mom[e[k]] = m;
-            }
-            x = p.nesterov ? fmaf(p.mu, m, x) : m;
-        }
-        u[k] = x;
+        float x[1];
+        muon_u<1, STEP>(p, e[k], x);
+        u[k] = x[0];
     }
 }
 

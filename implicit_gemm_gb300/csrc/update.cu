@@ -16,8 +16,7 @@
 #include "../../include/wgrad.h"
 #include "host.h"
 #include "k_embedding.cuh"
-#include "k_muon.cuh"
-#include "k_muon_gram.cuh"
+#include "k_muon_gemm.cuh"
 
 namespace wg {
 
@@ -81,7 +80,8 @@ struct MuonPlan {
     int P, blocks;        // rows of a block of the Gram matrix, blocks
     int ldx, m, ldm, nparts;
     size_t off_q, off_factor;
-    size_t off_x[2], off_xlo, off_a, off_b, off_part, bytes;
+    int pairs;
+    size_t off_x[2], off_xlo, off_a, off_b, off_part, off_sums, off_arrived, bytes;
 };
 
 // The Gram-matrix kernel's problem: blocks of whole matrices, CTAs of a cluster,
@@ -191,6 +191,9 @@ int make_muon_plan(const wg_muon_problem* p, MuonPlan* pl)
         pl->off_xlo = o, o += x;
         pl->off_a = o, o += a;
         pl->off_b = o, o += a;
+        pl->pairs = std::max(1, num_sms() / 2);
+        pl->off_sums = o, o += (size_t)pl->pairs * 2 * wg::kMgTile * wg::kMgTile * 4;
+        pl->off_arrived = o, o += up256((size_t)pl->pairs * 16 * 4);
     }
     pl->bytes = o;
     return WG_OK;
@@ -246,6 +249,58 @@ int muon_gram_launch(const MuonPlan& pl, const wg::GramParams& g, cudaStream_t s
     return e == cudaSuccess ? WG_OK : cuda_fail("muon_gram_kernel launch", e);
 }
 
+// fp16 matrices [batch][rows][cols], read in boxes of 64 columns by `box` rows.
+int muon_map(CUtensorMap* tm, void* base, int cols, int rows, int batch, int ld, long long bs, int box)
+{
+    wg::EncodeTiledFn fn = wg::encode_fn();
+    if (!fn) return set_err(WG_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)batch};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)bs * 2};
+    const cuuint32_t bx[3] = {64, (cuuint32_t)box, 1}, es[3] = {1, 1, 1};
+    const CUresult r = fn(tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base, dims, strides, bx, es,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return set_err(WG_ERR_CUDA, "cuTensorMapEncodeTiled failed with CUresult " + std::to_string((int)r));
+    return WG_OK;
+}
+
+// One product over a sum of length K.
+int muon_product(const MuonPlan& pl, const wg::MuonParams& p, wg::MuonProduct& g, const CUtensorMap& ta,
+                 const CUtensorMap& tb, int K, cudaStream_t s)
+{
+    g.kb = (K + 63) / 64;
+    g.tm = (g.M + wg::kMgTile - 1) / wg::kMgTile, g.tn = (g.N + wg::kMgTile - 1) / wg::kMgTile;
+    g.tiles = p.batch * (g.sym ? g.tm * (g.tm + 1) / 2 : g.tm * g.tn);
+    g.pairs = pl.pairs;
+    g.whole = g.tiles / g.pairs * g.pairs;
+    const int rest = g.tiles - g.whole;
+    // The other tiles: cut so that every pair has the same share, of at least four
+    // blocks, where that saves more than the parts' way through memory costs
+    // (about twelve blocks' time); else one to a pair.
+    const long long units = (long long)rest * g.kb;
+    g.cut = std::max(1, rest);
+    if (rest > 0) {
+        const int cut = (int)std::max(1LL, std::min<long long>(g.pairs, units / 4));
+        if (cut > rest && g.kb - (units + cut - 1) / cut > 12) g.cut = cut;
+    }
+    const int used = g.whole ? g.pairs : std::max(g.cut, 1);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    unsigned na = 0;
+    attr[na].id = cudaLaunchAttributeClusterDimension;
+    attr[na].val.clusterDim.x = 2;
+    attr[na].val.clusterDim.y = attr[na].val.clusterDim.z = 1;
+    ++na;
+    wg::pdl_config(&cfg, attr, &na, s);
+    const int st = wg::ensure_smem(wg::muon_product_kernel, wg::kMgSmem);
+    if (st) return st;
+    cfg.gridDim = dim3((unsigned)(2 * used));
+    cfg.blockDim = dim3(wg::kMgThreads);
+    cfg.dynamicSmemBytes = wg::kMgSmem;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, wg::muon_product_kernel, ta, tb, p, g);
+    return e == cudaSuccess ? WG_OK : cuda_fail("muon_product_kernel launch", e);
+}
+
 int muon_run(const MuonPlan& pl, const void* grad, void* momentum, void* weight, void* out, char* ws, cudaStream_t s)
 {
     const wg_muon_problem& q = pl.p;
@@ -273,36 +328,45 @@ int muon_run(const MuonPlan& pl, const void* grad, void* momentum, void* weight,
         p.xlo = reinterpret_cast<__half*>(ws + pl.off_xlo);
         p.a = reinterpret_cast<__half*>(ws + pl.off_a), p.b = reinterpret_cast<__half*>(ws + pl.off_b);
     }
+    if (q.steps > 0)
+        p.arrived = reinterpret_cast<int*>(ws + pl.off_arrived), p.narrived = pl.pairs * 16;
+    const bool al = q.cols % 8 == 0 && q.ld % 8 == 0 && q.batch_stride % 8 == 0;
+    const bool ivec = al && aligned16(grad) && aligned16(momentum), ovec = al && aligned16(weight) && aligned16(out);
     const dim3 egrid(pl.nparts, q.batch);
-    int st = launch("muon_momentum_kernel launch", wg::muon_momentum_kernel, egrid, dim3(256), 0, s, p);
-    if (!st) st = launch("muon_normalize_kernel launch", wg::muon_normalize_kernel, egrid, dim3(256), 0, s, p, (int)(q.steps == 0));
+    int st = launch("muon_momentum_kernel launch", ivec ? wg::muon_momentum_kernel<8> : wg::muon_momentum_kernel<1>,
+                    egrid, dim3(256), 0, s, p);
+    if (!st)
+        st = launch("muon_normalize_kernel launch",
+                    ivec && (q.steps > 0 || ovec) ? wg::muon_normalize_kernel<8> : wg::muon_normalize_kernel<1>, egrid,
+                    dim3(256), 0, s, p, (int)(q.steps == 0));
+    if (st || q.steps == 0) return st;
+    // Tensor maps: X read along and across its rows, A and B along theirs.
     const bool wide = q.rows <= q.cols;
-    const unsigned tm = (pl.m + 63) / 64, tr = (q.rows + 63) / 64, tc = (q.cols + 63) / 64;
-    for (int i = 0; i < q.steps && !st; ++i) {
-        const int in = i & 1;
-        wg::MuonGemm g = {};
-        g.a = pl.coef[i][0], g.b = pl.coef[i][1], g.c = pl.coef[i][2];
-        g.xin = in, g.last = i == q.steps - 1;
-        g.stage = 0, g.M = g.N = pl.m, g.K = std::max(q.rows, q.cols);
-        g.P = g.Q = p.x[in], g.pb = g.qb = p.xs;
-        g.pi = g.qj = wide ? pl.ldx : 1, g.pk = g.qk = wide ? 1 : pl.ldx;
-        st = launch("muon_gemm_kernel launch", wg::muon_gemm_kernel, dim3(tm, tm, q.batch), dim3(256), 0, s, p, g);
-        if (st) break;
-        g.stage = 1, g.K = pl.m, g.P = g.Q = p.a, g.pb = g.qb = p.ms;
-        g.pi = g.qk = pl.ldm, g.pk = g.qj = 1;
-        st = launch("muon_gemm_kernel launch", wg::muon_gemm_kernel, dim3(tm, tm, q.batch), dim3(256), 0, s, p, g);
-        if (st) break;
-        g.stage = 2, g.M = q.rows, g.N = q.cols;
-        if (wide) {
-            g.P = p.b, g.pb = p.ms, g.pi = pl.ldm, g.pk = 1;
-            g.Q = p.x[in], g.qb = p.xs, g.qk = pl.ldx, g.qj = 1;
-        } else {
-            g.P = p.x[in], g.pb = p.xs, g.pi = pl.ldx, g.pk = 1;
-            g.Q = p.b, g.qb = p.ms, g.qk = pl.ldm, g.qj = 1;
-        }
-        st = launch("muon_gemm_kernel launch", wg::muon_gemm_kernel, dim3(tc, tr, q.batch), dim3(256), 0, s, p, g);
+    CUtensorMap along[2], across[2], ma, mb;
+    for (int i = 0; i < 2; ++i) {
+        if ((st = muon_map(&along[i], p.x[i], q.cols, q.rows, q.batch, pl.ldx, p.xs, 128))) return st;
+        if ((st = muon_map(&across[i], p.x[i], q.cols, q.rows, q.batch, pl.ldx, p.xs, 64))) return st;
     }
-    return st;
+    if ((st = muon_map(&ma, p.a, pl.m, pl.m, q.batch, pl.ldm, p.ms, 128))) return st;
+    if ((st = muon_map(&mb, p.b, pl.m, pl.m, q.batch, pl.ldm, p.ms, 128))) return st;
+    for (int i = 0; i < q.steps; ++i) {
+        const int in = i & 1;
+        wg::MuonProduct g = {};
+        g.a = pl.coef[i][0], g.b = pl.coef[i][1], g.c = pl.coef[i][2];
+        g.xin = in, g.last = i == q.steps - 1, g.ovec = ovec;
+        g.part = reinterpret_cast<float*>(ws + pl.off_sums), g.arrived = p.arrived;
+        g.stage = 0, g.M = g.N = pl.m, g.sym = 1;
+        g.a_mn = g.b_mn = !wide;
+        const CUtensorMap& x = wide ? along[in] : across[in];
+        if ((st = muon_product(pl, p, g, x, x, std::max(q.rows, q.cols), s))) return st;
+        g.stage = 1, g.a_mn = g.b_mn = 0;
+        if ((st = muon_product(pl, p, g, ma, ma, pl.m, s))) return st;
+        g.stage = 2, g.M = q.rows, g.N = q.cols, g.sym = 0;
+        g.b_mn = wide;
+        st = wide ? muon_product(pl, p, g, mb, across[in], pl.m, s) : muon_product(pl, p, g, along[in], mb, pl.m, s);
+        if (st) return st;
+    }
+    return WG_OK;
 }
 
 // ---------------------------------------------------------------- embedding
@@ -463,7 +527,7 @@ int wg_muon_plan_string(const wg_muon_problem* p, char* buf, size_t n)
                  p->rows <= p->cols ? "left" : "right", pl.m, pl.P, pl.g.F, pl.blocks, pl.g.C, pl.g.chunks, p->steps,
                  pl.bytes);
     else
-        snprintf(buf, n, "kernel=muon_gemm side=%s m=%d steps=%d ws=%zu", p->rows <= p->cols ? "left" : "right", pl.m,
+        snprintf(buf, n, "kernel=muon_product side=%s m=%d steps=%d ws=%zu", p->rows <= p->cols ? "left" : "right", pl.m,
              p->steps, pl.bytes);
     return WG_OK;
 }
