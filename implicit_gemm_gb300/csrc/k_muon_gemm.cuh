@@ -6,7 +6,7 @@
 //   stage 2:  X' = a X + B X (or X B); after the last step the results
 //
 // Tiles of 256 x 256, 64 of the sum per stage of the ring: each CTA of a pair
-// stages 128 rows of either operand by TMA (32 KB; 6 stages) and holds 128 x 256
+// stages 128 rows of either operand by TMA (32 KB; 5 stages) and holds 128 x 256
 // fp32 sums in tensor memory, twice, so that a tile's epilogue runs beside the
 // next tile's MMAs.  Operands are read as they lie: along the sum (K-major) or
 // across it (MN-major), so nothing is ever transposed.  Tiles above the diagonal
@@ -25,8 +25,9 @@
 namespace wg {
 
 constexpr int kMgThreads = 320;  // warp 0 TMA, warp 1 MMA (rank 0), warps 2..9 epilogue
-constexpr int kMgStages = 6, kMgStageBytes = 32768;
-constexpr int kMgSmem = kMgStages * kMgStageBytes + 1024 + 256;
+constexpr int kMgStages = 5, kMgStageBytes = 32768;
+constexpr int kMgWarpStaging = 8192;  // 32 rows by 64 columns of fp32 per epilogue warp
+constexpr int kMgSmem = kMgStages * kMgStageBytes + 8 * kMgWarpStaging + 1024 + 256;
 constexpr int kMgTile = 256;
 
 struct MuonProduct {
@@ -109,87 +110,132 @@ __device__ __forceinline__ MgTile mg_tile(const MuonProduct& g, int t)
     return r;
 }
 
-// 32 finished sums of row i, columns j .. j + 31 of matrix b.  `mirror`: the tile's
-// mirror image is written too (the lanes of a warp hold 32 consecutive rows).
-__device__ __forceinline__ void mg_epilogue(const MuonParams& p, const MuonProduct& g, int b, int i, int j, bool mirror,
-                                            float (&v)[32])
+// 64 finished sums of row i0 + lane, columns j .. j + 63 of matrix b, by one warp.
+// Global memory is read and written in rows of 128 bytes (eight lanes a row)
+// through the warp's 8 KB of shared memory, whose 16-byte chunks are swizzled by
+// the row: row by row from the lanes, a request touched 32 lines and the epilogue
+// took longer than the MMAs of a 4096-long sum.  `mirror`: the tile's mirror image
+// is written too.
+__device__ __forceinline__ void mg_epilogue(const MuonParams& p, const MuonProduct& g, uint8_t* stg, int b, int i0, int j,
+                                            bool mirror, float (&v)[64])
 {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, sub = lane >> 3, c8 = lane & 7;
+    const int jc = j + 8 * c8;
     if (g.stage < 2) {
-        const bool row = i < g.M;
         __half* base = (g.stage == 0 ? p.a : p.b) + b * p.ms;
-        uint32_t h[16];
+        uint8_t* own = stg + lane * 128;
+        uint32_t h[32];
         if (g.stage == 0) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) h[k] = pack_half2(v[2 * k] * 0x1p-6f, v[2 * k + 1] * 0x1p-6f);
+            for (int k = 0; k < 32; ++k) h[k] = pack_half2(v[2 * k] * 0x1p-6f, v[2 * k + 1] * 0x1p-6f);
         } else {
-            const __half* src = p.a + b * p.ms + (long long)i * p.ldm + j;
+            const __half* src = p.a + b * p.ms + (long long)i0 * p.ldm + jc;
+            uint4 x[8];
+#pragma unroll
+            for (int it = 0; it < 8; ++it) {
+                const int r = 4 * it + sub;
+                x[it] = make_uint4(0u, 0u, 0u, 0u);
+                if (i0 + r < g.M && jc < g.N) x[it] = *reinterpret_cast<const uint4*>(src + (long long)r * p.ldm);
+            }
+#pragma unroll
+            for (int it = 0; it < 8; ++it) {
+                const int r = 4 * it + sub;
+                *reinterpret_cast<uint4*>(stg + r * 128 + ((c8 ^ (r & 7)) << 4)) = x[it];
+            }
+            __syncwarp();
             const float c = g.c * 0x1p-10f;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                if (row && j + 8 * k < g.N) x = *reinterpret_cast<const uint4*>(src + 8 * k);
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            for (int k = 0; k < 8; ++k) {
+                const uint4 y = *reinterpret_cast<const uint4*>(own + ((k ^ c8) << 4));
+                const uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float2 f = unpack_half2(w[e]);
                     h[4 * k + e] = pack_half2(fmaf(g.b, f.x, c * v[8 * k + 2 * e]), fmaf(g.b, f.y, c * v[8 * k + 2 * e + 1]));
                 }
             }
+            __syncwarp();
         }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4*>(own + ((k ^ c8) << 4)) = make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
+        __syncwarp();
         // Rows are padded to eight elements; the padding may be written.
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (row && j + 8 * k < g.N)
-                *reinterpret_cast<uint4*>(base + (long long)i * p.ldm + j + 8 * k) =
-                    make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
+        for (int it = 0; it < 8; ++it) {
+            const int r = 4 * it + sub;
+            const uint4 y = *reinterpret_cast<const uint4*>(stg + r * 128 + ((c8 ^ (r & 7)) << 4));
+            if (i0 + r < g.M && jc < g.N) *reinterpret_cast<uint4*>(base + (long long)(i0 + r) * p.ldm + jc) = y;
+        }
         if (mirror) {
             // Neighbouring lanes exchange so that each has two rows' values of one column.
             const bool odd = lane & 1;
-            const int i2 = i & ~1;
+            const int i2 = i0 + (lane & ~1);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
+            for (int k = 0; k < 32; ++k) {
                 const uint32_t other = __shfl_xor_sync(0xffffffffu, h[k], 1);
                 const uint32_t w = odd ? __byte_perm(other, h[k], 0x7632) : __byte_perm(h[k], other, 0x5410);
                 const int c = j + 2 * k + (odd ? 1 : 0);
                 if (c < g.N && i2 < g.M) *reinterpret_cast<uint32_t*>(base + (long long)c * p.ldm + i2) = w;
             }
         }
+        __syncwarp();
         return;
     }
-    if (i >= g.M) return;
-    const long long e = b * p.xs + (long long)i * p.ldx + j;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        if (j + 8 * k >= g.N) break;
-        const uint4 xh = *reinterpret_cast<const uint4*>(p.x[g.xin] + e + 8 * k);
-        const uint4 xl = *reinterpret_cast<const uint4*>(p.xlo + e + 8 * k);
-        const uint32_t wh[4] = {xh.x, xh.y, xh.z, xh.w}, wl[4] = {xl.x, xl.y, xl.z, xl.w};
-        float y[8];
+    for (int k = 0; k < 16; ++k)
+        *reinterpret_cast<float4*>(stg + lane * 256 + ((k ^ c8) << 4)) =
+            make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+    __syncwarp();
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const float2 h = unpack_half2(wh[q]), l = unpack_half2(wl[q]);
-            y[2 * q] = fmaf(g.a, h.x + l.x, v[8 * k + 2 * q] * 0x1p-10f);
-            y[2 * q + 1] = fmaf(g.a, h.y + l.y, v[8 * k + 2 * q + 1] * 0x1p-10f);
+    for (int h0 = 0; h0 < 8; h0 += 4) {
+        uint4 xh[4], xl[4];
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+            const int i = i0 + 4 * (h0 + it) + sub;
+            xh[it] = xl[it] = make_uint4(0u, 0u, 0u, 0u);
+            if (i < g.M && jc < g.N) {
+                const long long e = b * p.xs + (long long)i * p.ldx + jc;
+                xh[it] = *reinterpret_cast<const uint4*>(p.x[g.xin] + e);
+                xl[it] = *reinterpret_cast<const uint4*>(p.xlo + e);
+            }
         }
-        if (!g.last) {
-            uint4 h, l;
-            split8<false>(y, &h, &l);
-            *reinterpret_cast<uint4*>(p.x[g.xin ^ 1] + e + 8 * k) = h;
-            *reinterpret_cast<uint4*>(p.xlo + e + 8 * k) = l;
-            continue;
-        }
-        const long long o = (long long)b * p.bs + i * p.ld + j + 8 * k;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) y[q] *= p.scale * (1.f / kMuonXScale);
-        if (g.ovec) {
-            muon_finish8(p, o, y);
-        } else {
+        for (int it = 0; it < 4; ++it) {
+            const int r = 4 * (h0 + it) + sub, i = i0 + r;
+            float y[8];
+            const float4 d0 = *reinterpret_cast<const float4*>(stg + r * 256 + (((2 * c8) ^ (r & 7)) << 4));
+            const float4 d1 = *reinterpret_cast<const float4*>(stg + r * 256 + (((2 * c8 + 1) ^ (r & 7)) << 4));
+            const float d[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
+            const uint32_t wh[4] = {xh[it].x, xh[it].y, xh[it].z, xh[it].w}, wl[4] = {xl[it].x, xl[it].y, xl[it].z, xl[it].w};
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-                if (j + 8 * k + q < g.N) muon_finish(p, o + q, y[q]);
+            for (int q = 0; q < 4; ++q) {
+                const float2 h = unpack_half2(wh[q]), l = unpack_half2(wl[q]);
+                y[2 * q] = fmaf(g.a, h.x + l.x, d[2 * q] * 0x1p-10f);
+                y[2 * q + 1] = fmaf(g.a, h.y + l.y, d[2 * q + 1] * 0x1p-10f);
+            }
+            if (i >= g.M || jc >= g.N) continue;
+            if (!g.last) {
+                const long long e = b * p.xs + (long long)i * p.ldx + jc;
+                uint4 h, l;
+                split8<false>(y, &h, &l);
+                *reinterpret_cast<uint4*>(p.x[g.xin ^ 1] + e) = h;
+                *reinterpret_cast<uint4*>(p.xlo + e) = l;
+                continue;
+            }
+            const long long o = (long long)b * p.bs + i * p.ld + jc;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) y[q] *= p.scale * (1.f / kMuonXScale);
+            if (g.ovec) {
+                muon_finish8(p, o, y);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    if (jc + q < g.N) muon_finish(p, o + q, y[q]);
+            }
         }
     }
+    __syncwarp();
 }
 
 __global__ void __launch_bounds__(kMgThreads, 1)
@@ -198,7 +244,8 @@ __global__ void __launch_bounds__(kMgThreads, 1)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align_shared<uint8_t>(smem_raw, 1024);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kMgStages * kMgStageBytes);  // [stages], rank 0's count
+    uint8_t* staging = smem + kMgStages * kMgStageBytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(staging + 8 * kMgWarpStaging);      // [stages], rank 0's count
     uint64_t* empty = full + kMgStages;                                             // [stages]
     uint64_t* accf = empty + kMgStages;                                             // [2] sums complete
     uint64_t* acce = accf + 2;                                                      // [2] sums read (rank 0's count)
@@ -350,21 +397,21 @@ __global__ void __launch_bounds__(kMgThreads, 1)
             }
             if (finish) {
 #pragma unroll 1
-                for (int ch = 0; ch < 4; ++ch) {
-                    float v[32];
+                for (int ch = 0; ch < 2; ++ch) {
+                    float v[64];
                     if (whole) {
-                        gram_ld<32>(trow + (uint32_t)(buf * 256 + ch * 32), v);
+                        gram_ld<64>(trow + (uint32_t)(buf * 256 + ch * 64), v);
                     } else {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) v[k] = 0.f;
+                        for (int k = 0; k < 64; ++k) v[k] = 0.f;
                         for (int c = c0; c <= c1; ++c) {
                             const float* in = g.part + (size_t)(2 * c + (c == c0 ? 1 : 0)) * slot + mine;
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) v[k] += __ldcg(in + (ch * 32 + k) * 128);
+                            for (int k = 0; k < 64; ++k) v[k] += __ldcg(in + (ch * 64 + k) * 128);
                         }
                     }
-                    mg_epilogue(p, g, t.b, t.m * kMgTile + rank * 128 + row, t.n * kMgTile + half * 128 + ch * 32,
-                                g.sym && t.m != t.n, v);
+                    mg_epilogue(p, g, staging + e * kMgWarpStaging, t.b, t.m * kMgTile + rank * 128 + q * 32,
+                                t.n * kMgTile + half * 128 + ch * 64, g.sym && t.m != t.n, v);
                 }
             }
             tc_fence_before();
