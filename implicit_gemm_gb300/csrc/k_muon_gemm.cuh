@@ -5,10 +5,10 @@
 //   stage 1:  B = b A + c A A                  symmetric
 //   stage 2:  X' = a X + B X (or X B); after the last step the results
 //
-// Tiles of 256 x 256, 64 of the sum per stage of the ring: each CTA of a pair
-// stages 128 rows of either operand by TMA (32 KB; 5 stages) and holds 128 x 256
-// fp32 sums in tensor memory, twice, so that a tile's epilogue runs beside the
-// next tile's MMAs.  Operands are read as they lie: along the sum (K-major) or
+// Tiles of 256 x 256 (or 256 x 128, where there are few), 64 of the sum per stage
+// of the ring: each CTA of a pair stages 128 rows of A and half of B's by TMA and
+// holds 128 x 256 fp32 sums in tensor memory, twice, so that a tile's epilogue
+// runs beside the next tile's MMAs.  Operands are read as they lie: along the sum (K-major) or
 // across it (MN-major), so nothing is ever transposed.  Tiles above the diagonal
 // of a symmetric product are written by the epilogue of their mirror image.
 //
@@ -24,11 +24,17 @@
 
 namespace wg {
 
-constexpr int kMgThreads = 320;  // warp 0 TMA, warp 1 MMA (rank 0), warps 2..9 epilogue
-constexpr int kMgStages = 5, kMgStageBytes = 32768;
-constexpr int kMgWarpStaging = 8192;  // 32 rows by 64 columns of fp32 per epilogue warp
-constexpr int kMgSmem = kMgStages * kMgStageBytes + 8 * kMgWarpStaging + 1024 + 256;
-constexpr int kMgTile = 256;
+constexpr int kMgEpiWarps = 16;
+constexpr int kMgThreads = 64 + 32 * kMgEpiWarps;  // warp 0 TMA, warp 1 MMA (rank 0), then the epilogue
+constexpr int kMgWarpStaging = 4096;  // 32 rows by 32 columns of fp32 per epilogue warp
+// Tiles of 256 rows by BN columns, 64 of the sum per stage: a CTA's 128 rows of A and BN / 2 of B.
+template <int BN>
+struct Mg {
+    static constexpr int kStageBytes = 16384 + BN * 64;
+    static constexpr int kStages = BN == 256 ? 5 : 6;
+    static constexpr int kSmem = kStages * kStageBytes + kMgEpiWarps * kMgWarpStaging + 1024 + 256;
+    static constexpr int kTmem = 2 * BN;  // columns: the sums, twice
+};
 
 struct MuonProduct {
     int stage, xin, last;
@@ -36,13 +42,14 @@ struct MuonProduct {
     int a_mn, b_mn;           // operand is read across its rows
     int M, N, kb;             // extents of D, 64-wide blocks of the sum
     int tm, tn, sym;          // tiles along M and N of a matrix
+    int per;                  // tiles of a matrix
     int tiles;                // of all matrices
     int whole;                // tiles taken whole
     int pairs;
     int cut;                  // pairs that share the blocks of sums of the other tiles (at most as many as blocks)
     int ovec;                 // eight elements along a row of weight and out are aligned
-    float* part;              // [pairs][2][2][256][128] sums of parts of tiles
-    int* arrived;             // [pairs][2][8] parts of a tile that are there (zero between launches)
+    float* part;              // [pairs][2][2][BN][128] sums of parts of tiles
+    int* arrived;             // [pairs][2][16] parts of a tile that are there (zero between launches)
 };
 
 __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* tm, uint32_t bar_cluster, int c0, int c1,
@@ -66,87 +73,116 @@ struct MgPiece {
     int t, k0, k1;
 };
 
-// Piece i of pair c, or false.  The tiles after the whole ones are `units` blocks
-// of sums in a row; pair c < cut takes units c * units / cut .. (c + 1) * units / cut.
+// A pair's pieces, one after another.  The tiles after the whole ones are `units`
+// blocks of sums in a row; pair c < cut takes units c * units / cut ..
+// (c + 1) * units / cut, and takes them first: adding up the parts of those tiles
+// then runs beside the MMAs of the whole ones.
 __device__ __forceinline__ long long mg_unit0(const MuonProduct& g, int c)
 {
     return (long long)(g.tiles - g.whole) * g.kb * min(c, g.cut) / g.cut;
 }
-__device__ __forceinline__ bool mg_piece(const MuonProduct& g, int c, int i, long long& u, MgPiece& p)
-{
-    const int own = g.whole / g.pairs;  // whole tiles are whole waves
-    if (i < own) {
-        p.t = c + i * g.pairs, p.k0 = 0, p.k1 = g.kb;
+struct MgWalk {
+    long long u, end;
+    int t;
+    __device__ __forceinline__ MgWalk(const MuonProduct& g, int c) : u(mg_unit0(g, c)), end(mg_unit0(g, c + 1)), t(c) {}
+    __device__ __forceinline__ bool next(const MuonProduct& g, MgPiece& p)
+    {
+        if (u < end) {
+            const int r = (int)(u / g.kb);
+            p.t = g.whole + r;
+            p.k0 = (int)(u - (long long)r * g.kb);
+            p.k1 = (int)min((long long)g.kb, p.k0 + (end - u));
+            u += p.k1 - p.k0;
+            return true;
+        }
+        if (t >= g.whole) return false;
+        p.t = t, p.k0 = 0, p.k1 = g.kb;
+        t += g.pairs;
         return true;
     }
-    if (i == own) u = mg_unit0(g, c);
-    const long long end = mg_unit0(g, c + 1);
-    if (u >= end) return false;
-    const int r = (int)(u / g.kb);
-    p.t = g.whole + r;
-    p.k0 = (int)(u - (long long)r * g.kb);
-    p.k1 = (int)min((long long)g.kb, p.k0 + (end - u));
-    u += p.k1 - p.k0;
-    return true;
-}
+};
 
 struct MgTile {
-    int b, m, n;  // matrix, tile row and column
+    int b, m, n;  // matrix, first row and column
+    bool mirror;  // below the diagonal of a symmetric product
 };
+template <int BN>
 __device__ __forceinline__ MgTile mg_tile(const MuonProduct& g, int t)
 {
+    constexpr int W = 256 / BN;  // tiles that cover a diagonal block
     MgTile r;
-    const int per = g.sym ? g.tm * (g.tm + 1) / 2 : g.tm * g.tn;
-    r.b = t / per;
-    const int i = t - r.b * per;
+    r.b = t / g.per;
+    const int i = t - r.b * g.per;
+    int m, n;
     if (g.sym) {
-        int m = (int)((sqrtf(8.f * i + 1.f) - 1.f) * 0.5f);
-        while (m * (m + 1) / 2 > i) --m;
-        while ((m + 1) * (m + 2) / 2 <= i) ++m;
-        r.m = m, r.n = i - m * (m + 1) / 2;
+        // Rows 0 .. m - 1 of tiles have W m (m + 1) / 2 tiles.
+        m = (int)((sqrtf(8.f * i / W + 1.f) - 1.f) * 0.5f);
+        while (W * (m * (m + 1) / 2) > i) --m;
+        while (W * ((m + 1) * (m + 2) / 2) <= i) ++m;
+        n = i - W * (m * (m + 1) / 2);
+        r.mirror = n < W * m;
     } else {
-        r.n = i / g.tm, r.m = i - r.n * g.tm;
+        n = i / g.tm, m = i - n * g.tm;
+        r.mirror = false;
     }
+    r.m = m * 256, r.n = n * BN;
     return r;
 }
 
-// 64 finished sums of row i0 + lane, columns j .. j + 63 of matrix b, by one warp.
-// Global memory is read and written in rows of 128 bytes (eight lanes a row)
-// through the warp's 8 KB of shared memory, whose 16-byte chunks are swizzled by
-// the row: row by row from the lanes, a request touched 32 lines and the epilogue
-// took longer than the MMAs of a 4096-long sum.  `mirror`: the tile's mirror image
-// is written too.
-__device__ __forceinline__ void mg_epilogue(const MuonParams& p, const MuonProduct& g, uint8_t* stg, int b, int i0, int j,
-                                            bool mirror, float (&v)[64])
+// What a chunk's epilogue reads: A (stage 1), X and what its first value rounds
+// away (stage 2), in rows of 64 bytes (four lanes a row).
+struct MgRead {
+    uint4 x[4], y[4];
+};
+__device__ __forceinline__ void mg_read(const MuonParams& p, const MuonProduct& g, int b, int i0, int j, MgRead& r)
 {
-    const int lane = threadIdx.x & 31, sub = lane >> 3, c8 = lane & 7;
-    const int jc = j + 8 * c8;
+    const int lane = threadIdx.x & 31, sub = lane >> 2, jc = j + 8 * (lane & 3);
+    if (g.stage == 0) return;
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+        const int i = i0 + 8 * it + sub;
+        r.x[it] = r.y[it] = make_uint4(0u, 0u, 0u, 0u);
+        if (i >= g.M || jc >= g.N) continue;
+        if (g.stage == 1) {
+            r.x[it] = *reinterpret_cast<const uint4*>(p.a + b * p.ms + (long long)i * p.ldm + jc);
+        } else {
+            const long long e = b * p.xs + (long long)i * p.ldx + jc;
+            r.x[it] = *reinterpret_cast<const uint4*>(p.x[g.xin] + e);
+            r.y[it] = *reinterpret_cast<const uint4*>(p.xlo + e);
+        }
+    }
+}
+
+// 32 finished sums of row i0 + lane, columns j .. j + 31 of matrix b, by one warp.
+// Global memory is read and written in rows of 64 bytes through the warp's 4 KB of
+// shared memory, whose 16-byte chunks are swizzled by the row: row by row from the
+// lanes, a request touched 32 lines and the epilogue took longer than the MMAs of a
+// 4096-long sum.  `mirror`: the tile's mirror image is written too.
+__device__ __forceinline__ void mg_epilogue(const MuonParams& p, const MuonProduct& g, uint8_t* stg, int b, int i0, int j,
+                                            bool mirror, float (&v)[32], const MgRead& rd)
+{
+    const int lane = threadIdx.x & 31, sub = lane >> 2, c4 = lane & 3;
+    const int jc = j + 8 * c4;
     if (g.stage < 2) {
+        // fp16 rows of 64 bytes: chunk k of row r at k ^ (r / 2) % 4.
         __half* base = (g.stage == 0 ? p.a : p.b) + b * p.ms;
-        uint8_t* own = stg + lane * 128;
-        uint32_t h[32];
+        uint8_t* own = stg + lane * 64;
+        const int osw = (lane >> 1) & 3;
+        uint32_t h[16];
         if (g.stage == 0) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) h[k] = pack_half2(v[2 * k] * 0x1p-6f, v[2 * k + 1] * 0x1p-6f);
+            for (int k = 0; k < 16; ++k) h[k] = pack_half2(v[2 * k] * 0x1p-6f, v[2 * k + 1] * 0x1p-6f);
         } else {
-            const __half* src = p.a + b * p.ms + (long long)i0 * p.ldm + jc;
-            uint4 x[8];
 #pragma unroll
-            for (int it = 0; it < 8; ++it) {
-                const int r = 4 * it + sub;
-                x[it] = make_uint4(0u, 0u, 0u, 0u);
-                if (i0 + r < g.M && jc < g.N) x[it] = *reinterpret_cast<const uint4*>(src + (long long)r * p.ldm);
-            }
-#pragma unroll
-            for (int it = 0; it < 8; ++it) {
-                const int r = 4 * it + sub;
-                *reinterpret_cast<uint4*>(stg + r * 128 + ((c8 ^ (r & 7)) << 4)) = x[it];
+            for (int it = 0; it < 4; ++it) {
+                const int r = 8 * it + sub;
+                *reinterpret_cast<uint4*>(stg + r * 64 + ((c4 ^ ((r >> 1) & 3)) << 4)) = rd.x[it];
             }
             __syncwarp();
             const float c = g.c * 0x1p-10f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const uint4 y = *reinterpret_cast<const uint4*>(own + ((k ^ c8) << 4));
+            for (int k = 0; k < 4; ++k) {
+                const uint4 y = *reinterpret_cast<const uint4*>(own + ((k ^ osw) << 4));
                 const uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -157,95 +193,85 @@ __device__ __forceinline__ void mg_epilogue(const MuonParams& p, const MuonProdu
             __syncwarp();
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<uint4*>(own + ((k ^ c8) << 4)) = make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
+        for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4*>(own + ((k ^ osw) << 4)) = make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
         __syncwarp();
         // Rows are padded to eight elements; the padding may be written.
 #pragma unroll
-        for (int it = 0; it < 8; ++it) {
-            const int r = 4 * it + sub;
-            const uint4 y = *reinterpret_cast<const uint4*>(stg + r * 128 + ((c8 ^ (r & 7)) << 4));
+        for (int it = 0; it < 4; ++it) {
+            const int r = 8 * it + sub;
+            const uint4 y = *reinterpret_cast<const uint4*>(stg + r * 64 + ((c4 ^ ((r >> 1) & 3)) << 4));
             if (i0 + r < g.M && jc < g.N) *reinterpret_cast<uint4*>(base + (long long)(i0 + r) * p.ldm + jc) = y;
         }
         if (mirror) {
             // Neighbouring lanes exchange so that each has two rows' values of one column.
             const bool odd = lane & 1;
             const int i2 = i0 + (lane & ~1);
+            __half* col = base + (long long)(j + (odd ? 1 : 0)) * p.ldm + i2;
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
+            for (int k = 0; k < 16; ++k) {
                 const uint32_t other = __shfl_xor_sync(0xffffffffu, h[k], 1);
                 const uint32_t w = odd ? __byte_perm(other, h[k], 0x7632) : __byte_perm(h[k], other, 0x5410);
-                const int c = j + 2 * k + (odd ? 1 : 0);
-                if (c < g.N && i2 < g.M) *reinterpret_cast<uint32_t*>(base + (long long)c * p.ldm + i2) = w;
+                if (j + 2 * k + (odd ? 1 : 0) < g.N && i2 < g.M) *reinterpret_cast<uint32_t*>(col + 2 * k * p.ldm) = w;
             }
         }
         __syncwarp();
         return;
     }
+    // fp32 rows of 128 bytes: chunk k of row r at k ^ r % 8.
 #pragma unroll
-    for (int k = 0; k < 16; ++k)
-        *reinterpret_cast<float4*>(stg + lane * 256 + ((k ^ c8) << 4)) =
+    for (int k = 0; k < 8; ++k)
+        *reinterpret_cast<float4*>(stg + lane * 128 + ((k ^ (lane & 7)) << 4)) =
             make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
     __syncwarp();
 #pragma unroll
-    for (int h0 = 0; h0 < 8; h0 += 4) {
-        uint4 xh[4], xl[4];
+    for (int it = 0; it < 4; ++it) {
+        const int r = 8 * it + sub, i = i0 + r;
+        float y[8];
+        const float4 d0 = *reinterpret_cast<const float4*>(stg + r * 128 + (((2 * c4) ^ (r & 7)) << 4));
+        const float4 d1 = *reinterpret_cast<const float4*>(stg + r * 128 + (((2 * c4 + 1) ^ (r & 7)) << 4));
+        const float d[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
+        const uint32_t wh[4] = {rd.x[it].x, rd.x[it].y, rd.x[it].z, rd.x[it].w};
+        const uint32_t wl[4] = {rd.y[it].x, rd.y[it].y, rd.y[it].z, rd.y[it].w};
 #pragma unroll
-        for (int it = 0; it < 4; ++it) {
-            const int i = i0 + 4 * (h0 + it) + sub;
-            xh[it] = xl[it] = make_uint4(0u, 0u, 0u, 0u);
-            if (i < g.M && jc < g.N) {
-                const long long e = b * p.xs + (long long)i * p.ldx + jc;
-                xh[it] = *reinterpret_cast<const uint4*>(p.x[g.xin] + e);
-                xl[it] = *reinterpret_cast<const uint4*>(p.xlo + e);
-            }
+        for (int q = 0; q < 4; ++q) {
+            const float2 h = unpack_half2(wh[q]), l = unpack_half2(wl[q]);
+            y[2 * q] = fmaf(g.a, h.x + l.x, d[2 * q] * 0x1p-10f);
+            y[2 * q + 1] = fmaf(g.a, h.y + l.y, d[2 * q + 1] * 0x1p-10f);
         }
+        if (i >= g.M || jc >= g.N) continue;
+        if (!g.last) {
+            const long long e = b * p.xs + (long long)i * p.ldx + jc;
+            uint4 h, l;
+            split8<false>(y, &h, &l);
+            *reinterpret_cast<uint4*>(p.x[g.xin ^ 1] + e) = h;
+            *reinterpret_cast<uint4*>(p.xlo + e) = l;
+            continue;
+        }
+        const long long o = (long long)b * p.bs + i * p.ld + jc;
 #pragma unroll
-        for (int it = 0; it < 4; ++it) {
-            const int r = 4 * (h0 + it) + sub, i = i0 + r;
-            float y[8];
-            const float4 d0 = *reinterpret_cast<const float4*>(stg + r * 256 + (((2 * c8) ^ (r & 7)) << 4));
-            const float4 d1 = *reinterpret_cast<const float4*>(stg + r * 256 + (((2 * c8 + 1) ^ (r & 7)) << 4));
-            const float d[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
-            const uint32_t wh[4] = {xh[it].x, xh[it].y, xh[it].z, xh[it].w}, wl[4] = {xl[it].x, xl[it].y, xl[it].z, xl[it].w};
+        for (int q = 0; q < 8; ++q) y[q] *= p.scale * (1.f / kMuonXScale);
+        if (g.ovec) {
+            muon_finish8(p, o, y);
+        } else {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float2 h = unpack_half2(wh[q]), l = unpack_half2(wl[q]);
-                y[2 * q] = fmaf(g.a, h.x + l.x, d[2 * q] * 0x1p-10f);
-                y[2 * q + 1] = fmaf(g.a, h.y + l.y, d[2 * q + 1] * 0x1p-10f);
-            }
-            if (i >= g.M || jc >= g.N) continue;
-            if (!g.last) {
-                const long long e = b * p.xs + (long long)i * p.ldx + jc;
-                uint4 h, l;
-                split8<false>(y, &h, &l);
-                *reinterpret_cast<uint4*>(p.x[g.xin ^ 1] + e) = h;
-                *reinterpret_cast<uint4*>(p.xlo + e) = l;
-                continue;
-            }
-            const long long o = (long long)b * p.bs + i * p.ld + jc;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) y[q] *= p.scale * (1.f / kMuonXScale);
-            if (g.ovec) {
-                muon_finish8(p, o, y);
-            } else {
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    if (jc + q < g.N) muon_finish(p, o + q, y[q]);
-            }
+            for (int q = 0; q < 8; ++q)
+                if (jc + q < g.N) muon_finish(p, o + q, y[q]);
         }
     }
     __syncwarp();
 }
 
+template <int BN>
 __global__ void __launch_bounds__(kMgThreads, 1)
     muon_product_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                         const __grid_constant__ MuonParams p, const __grid_constant__ MuonProduct g)
 {
+    constexpr int kMgStages = Mg<BN>::kStages, kMgStageBytes = Mg<BN>::kStageBytes;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align_shared<uint8_t>(smem_raw, 1024);
     uint8_t* staging = smem + kMgStages * kMgStageBytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(staging + 8 * kMgWarpStaging);      // [stages], rank 0's count
+    uint64_t* full = reinterpret_cast<uint64_t*>(staging + kMgEpiWarps * kMgWarpStaging);      // [stages], rank 0's count
     uint64_t* empty = full + kMgStages;                                             // [stages]
     uint64_t* accf = empty + kMgStages;                                             // [2] sums complete
     uint64_t* acce = accf + 2;                                                      // [2] sums read (rank 0's count)
@@ -263,13 +289,13 @@ __global__ void __launch_bounds__(kMgThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&accf[i], 1);
-            mbar_init(&acce[i], 16);
+            mbar_init(&acce[i], 2 * kMgEpiWarps);
         }
         fence_mbar_init();
     }
     if (warp == 1) {
         pdl_wait();  // tensor memory may still be held by the kernel before this one
-        tmem_alloc_pair(tslot, 512);
+        tmem_alloc_pair(tslot, Mg<BN>::kTmem);
         tc_fence_before();
     }
     cluster_sync_all();  // both CTAs' barriers are initialised and both hold tensor memory
@@ -283,11 +309,10 @@ __global__ void __launch_bounds__(kMgThreads, 1)
             int st = 0;
             uint32_t ph = 0;
             bool ok = true;
-            long long u = 0;
             MgPiece w;
-            for (int i = 0; ok && mg_piece(g, pair, i, u, w); ++i) {
-                const MgTile t = mg_tile(g, w.t);
-                const int m0 = t.m * kMgTile + rank * 128, n0 = t.n * kMgTile + rank * 128;
+            for (MgWalk walk(g, pair); ok && walk.next(g, w);) {
+                const MgTile t = mg_tile<BN>(g, w.t);
+                const int m0 = t.m + rank * 128, n0 = t.n + rank * (BN / 2);
                 for (int k = w.k0; k < w.k1; ++k) {
                     if (!mbar_wait(&empty[st], ph ^ 1u)) {
                         ok = false;
@@ -304,7 +329,7 @@ __global__ void __launch_bounds__(kMgThreads, 1)
                     }
                     if (g.b_mn) {
                         tma_load_3d_pair(s + 16384, &tb, bar, n0, k * 64, t.b);
-                        tma_load_3d_pair(s + 16384 + 8192, &tb, bar, n0 + 64, k * 64, t.b);
+                        if (BN == 256) tma_load_3d_pair(s + 16384 + 8192, &tb, bar, n0 + 64, k * 64, t.b);
                     } else {
                         tma_load_3d_pair(s + 16384, &tb, bar, k * 64, n0, t.b);
                     }
@@ -315,7 +340,7 @@ __global__ void __launch_bounds__(kMgThreads, 1)
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0) {
-            const uint32_t idesc = make_idesc_f16(false, g.a_mn, g.b_mn, 256, 256);
+            const uint32_t idesc = make_idesc_f16(false, g.a_mn, g.b_mn, 256, BN);
             const uint32_t sbase = smem_u32(smem);
             const uint64_t ad = make_sdesc(sbase, g.a_mn ? 8192u : 16u, 1024u, 2u, 0u);
             const uint64_t bd = make_sdesc(sbase + 16384u, g.b_mn ? 8192u : 16u, 1024u, 2u, 0u);
@@ -323,13 +348,13 @@ __global__ void __launch_bounds__(kMgThreads, 1)
             int st = 0;
             uint32_t ph = 0;
             bool ok = true;
-            long long u = 0;
             MgPiece w;
-            for (int i = 0; ok && mg_piece(g, pair, i, u, w); ++i) {
+            MgWalk walk(g, pair);
+            for (int i = 0; ok && walk.next(g, w); ++i) {
                 const int buf = i & 1;
                 if (!mbar_wait(&acce[buf], ((uint32_t)(i >> 1) & 1u) ^ 1u)) break;
                 tc_fence_after();
-                const uint32_t d = tbase + (uint32_t)(buf * 256);
+                const uint32_t d = tbase + (uint32_t)(buf * BN);
                 for (int k = w.k0; k < w.k1; ++k) {
                     if (!mbar_wait(&full[st], ph)) {
                         ok = false;
@@ -352,31 +377,35 @@ __global__ void __launch_bounds__(kMgThreads, 1)
             }
         }
     } else {
-        // Warp e of the epilogue: 32 rows (its tensor-memory quadrant) by half of the columns.
-        const int e = warp - 2, q = warp & 3, half = e >> 2;
+        // Warp e of the epilogue: 32 rows (its tensor-memory quadrant) by a quarter of the columns.
+        const int e = warp - 2, q = warp & 3, col = (e >> 2) * (BN / 4);
         const uint32_t acce0 = mapa_shared(smem_u32(&acce[0]), 0u);
-        const uint32_t trow = tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * 128);
+        const uint32_t trow = tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)col;
         const int row = q * 32 + lane;
-        long long u = 0;
+        constexpr size_t slot = (size_t)2 * BN * 128;  // floats of a part: both ranks
+        const size_t mine = (size_t)rank * BN * 128 + (size_t)col * 128 + row;
         MgPiece w;
-        for (int i = 0; mg_piece(g, pair, i, u, w); ++i) {
+        MgWalk walk(g, pair);
+        for (int i = 0; walk.next(g, w); ++i) {
             const int buf = i & 1;
-            const MgTile t = mg_tile(g, w.t);
+            const MgTile t = mg_tile<BN>(g, w.t);
+            const int i0 = t.m + rank * 128 + q * 32, j0 = t.n + col;
+            const uint32_t tacc = trow + (uint32_t)(buf * BN);
+            const bool whole = w.k0 == 0 && w.k1 == g.kb;
+            MgRead rd;
+            if (whole) mg_read(p, g, t.b, i0, j0, rd);  // on its way while the sums are made
             if (!mbar_wait_sleep(&accf[buf], (uint32_t)(i >> 1) & 1u)) break;
             __syncwarp();
             tc_fence_after();
-            const bool whole = w.k0 == 0 && w.k1 == g.kb;
             int c0 = pair, c1 = pair;
             bool finish = true;
-            const size_t slot = (size_t)2 * 256 * 128;  // floats of a part: both ranks
-            const size_t mine = (size_t)rank * 256 * 128 + (size_t)(half * 128) * 128 + row;
             if (!whole) {
                 // Leave this part's sums (columns of 128 rows: coalesced), and see whether it is the last.
                 float* out = g.part + (size_t)(2 * pair + (w.k0 ? 0 : 1)) * slot + mine;
 #pragma unroll 1
-                for (int ch = 0; ch < 4; ++ch) {
+                for (int ch = 0; ch < BN / 128; ++ch) {
                     float v[32];
-                    gram_ld<32>(trow + (uint32_t)(buf * 256 + ch * 32), v);
+                    gram_ld<32>(tacc + (uint32_t)(ch * 32), v);
 #pragma unroll
                     for (int k = 0; k < 32; ++k) __stcg(out + (ch * 32 + k) * 128, v[k]);
                 }
@@ -385,7 +414,7 @@ __global__ void __launch_bounds__(kMgThreads, 1)
                 c1 = (int)(((u0 + g.kb) * g.cut + units - 1) / units) - 1;
                 __threadfence();
                 __syncwarp();
-                int* count = g.arrived + ((w.t - g.whole) * 2 + rank) * 8 + e;
+                int* count = g.arrived + ((w.t - g.whole) * 2 + rank) * kMgEpiWarps + e;
                 int n = 0;
                 if (lane == 0) n = atomicAdd(count, 1);
                 n = __shfl_sync(0xffffffffu, n, 0);
@@ -397,21 +426,28 @@ __global__ void __launch_bounds__(kMgThreads, 1)
             }
             if (finish) {
 #pragma unroll 1
-                for (int ch = 0; ch < 2; ++ch) {
-                    float v[64];
+                for (int ch = 0; ch < BN / 128; ++ch) {
+                    float v[32];
                     if (whole) {
-                        gram_ld<64>(trow + (uint32_t)(buf * 256 + ch * 64), v);
+                        if (ch) mg_read(p, g, t.b, i0, j0 + ch * 32, rd);
+                        gram_ld<32>(tacc + (uint32_t)(ch * 32), v);
                     } else {
+                        // 32 loads in flight at a time (left to the compiler, one after another).
 #pragma unroll
-                        for (int k = 0; k < 64; ++k) v[k] = 0.f;
+                        for (int k = 0; k < 32; ++k) v[k] = 0.f;
+#pragma unroll 1
                         for (int c = c0; c <= c1; ++c) {
-                            const float* in = g.part + (size_t)(2 * c + (c == c0 ? 1 : 0)) * slot + mine;
+                            const float* in = g.part + (size_t)(2 * c + (c == c0 ? 1 : 0)) * slot + mine + ch * 32 * 128;
+                            float x[32];
 #pragma unroll
-                            for (int k = 0; k < 64; ++k) v[k] += __ldcg(in + (ch * 64 + k) * 128);
+                            for (int k = 0; k < 32; ++k)
+                                asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(x[k]) : "l"(in + k * 128));
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) v[k] += x[k];
                         }
+                        mg_read(p, g, t.b, i0, j0 + ch * 32, rd);
                     }
-                    mg_epilogue(p, g, staging + e * kMgWarpStaging, t.b, t.m * kMgTile + rank * 128 + q * 32,
-                                t.n * kMgTile + half * 128 + ch * 64, g.sym && t.m != t.n, v);
+                    mg_epilogue(p, g, staging + e * kMgWarpStaging, t.b, i0, j0 + ch * 32, t.mirror, v, rd);
                 }
             }
             tc_fence_before();
@@ -424,7 +460,7 @@ __global__ void __launch_bounds__(kMgThreads, 1)
     cluster_sync_all();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc_pair(tbase, 512);
+        tmem_dealloc_pair(tbase, Mg<BN>::kTmem);
     }
 }
 

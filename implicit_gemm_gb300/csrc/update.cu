@@ -192,8 +192,8 @@ int make_muon_plan(const wg_muon_problem* p, MuonPlan* pl)
         pl->off_a = o, o += a;
         pl->off_b = o, o += a;
         pl->pairs = std::max(1, num_sms() / 2);
-        pl->off_sums = o, o += (size_t)pl->pairs * 2 * wg::kMgTile * wg::kMgTile * 4;
-        pl->off_arrived = o, o += up256((size_t)pl->pairs * 16 * 4);
+        pl->off_sums = o, o += (size_t)pl->pairs * 2 * 256 * 256 * 4;
+        pl->off_arrived = o, o += up256((size_t)pl->pairs * 2 * wg::kMgEpiWarps * 4);
     }
     pl->bytes = o;
     return WG_OK;
@@ -264,26 +264,23 @@ int muon_map(CUtensorMap* tm, void* base, int cols, int rows, int batch, int ld,
     return WG_OK;
 }
 
-// One product over a sum of length K.
-int muon_product(const MuonPlan& pl, const wg::MuonParams& p, wg::MuonProduct& g, const CUtensorMap& ta,
-                 const CUtensorMap& tb, int K, cudaStream_t s)
+// A matrix of the workspace as an operand.
+struct MuonOperand {
+    void* base;
+    int cols, rows, ld;
+    long long bs;
+};
+
+template <int BN>
+int muon_product_bn(const MuonPlan& pl, const wg::MuonParams& p, wg::MuonProduct& g, const MuonOperand& oa,
+                    const MuonOperand& ob, cudaStream_t s)
 {
-    g.kb = (K + 63) / 64;
-    g.tm = (g.M + wg::kMgTile - 1) / wg::kMgTile, g.tn = (g.N + wg::kMgTile - 1) / wg::kMgTile;
-    g.tiles = p.batch * (g.sym ? g.tm * (g.tm + 1) / 2 : g.tm * g.tn);
-    g.pairs = pl.pairs;
-    g.whole = g.tiles / g.pairs * g.pairs;
-    const int rest = g.tiles - g.whole;
-    // The other tiles: cut so that every pair has the same share, of at least four
-    // blocks, where that saves more than the parts' way through memory costs
-    // (about twelve blocks' time); else one to a pair.
-    const long long units = (long long)rest * g.kb;
-    g.cut = std::max(1, rest);
-    if (rest > 0) {
-        const int cut = (int)std::max(1LL, std::min<long long>(g.pairs, units / 4));
-        if (cut > rest && g.kb - (units + cut - 1) / cut > 12) g.cut = cut;
-    }
     const int used = g.whole ? g.pairs : std::max(g.cut, 1);
+    CUtensorMap ta, tb;
+    int st = muon_map(&ta, oa.base, oa.cols, oa.rows, p.batch, oa.ld, oa.bs, g.a_mn ? 64 : 128);
+    if (!st) st = muon_map(&tb, ob.base, ob.cols, ob.rows, p.batch, ob.ld, ob.bs, g.b_mn ? 64 : BN / 2);
+    if (!st) st = wg::ensure_smem(wg::muon_product_kernel<BN>, wg::Mg<BN>::kSmem);
+    if (st) return st;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     unsigned na = 0;
@@ -292,13 +289,45 @@ int muon_product(const MuonPlan& pl, const wg::MuonParams& p, wg::MuonProduct& g
     attr[na].val.clusterDim.y = attr[na].val.clusterDim.z = 1;
     ++na;
     wg::pdl_config(&cfg, attr, &na, s);
-    const int st = wg::ensure_smem(wg::muon_product_kernel, wg::kMgSmem);
-    if (st) return st;
     cfg.gridDim = dim3((unsigned)(2 * used));
     cfg.blockDim = dim3(wg::kMgThreads);
-    cfg.dynamicSmemBytes = wg::kMgSmem;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, wg::muon_product_kernel, ta, tb, p, g);
+    cfg.dynamicSmemBytes = wg::Mg<BN>::kSmem;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, wg::muon_product_kernel<BN>, ta, tb, p, g);
     return e == cudaSuccess ? WG_OK : cuda_fail("muon_product_kernel launch", e);
+}
+
+// One product over a sum of length K.
+int muon_product(const MuonPlan& pl, const wg::MuonParams& p, wg::MuonProduct& g, const MuonOperand& oa,
+                 const MuonOperand& ob, int K, cudaStream_t s)
+{
+    g.kb = (K + 63) / 64;
+    g.pairs = pl.pairs;
+    // The tiles' width, whether a symmetric product takes only the tiles on and
+    // below the diagonal, and the parts that the leftover tiles are cut into, by
+    // the time of the longest pair in us: a 64-long block of sums takes 0.33 for
+    // 256 columns (the rate of cuBLAS) and 0.18 for 128 (0.27 when all pairs are
+    // busy: their operands are twice the bytes per MMA); a tile's mirror image 1;
+    // parts that meet in memory 6 and 2.5 each.
+    const int tm = (g.M + 255) / 256, sym = g.sym;
+    double best = 1e30;
+    int bn = 256, parts = 1;
+    for (int w = 1; w <= 2; ++w)
+        for (int half = 0; half <= sym; ++half) {
+            const int tn = (g.N * w + 255) / 256;
+            const long long per = half ? (long long)w * (tm * (tm + 1) / 2) - (w * tm - tn) : (long long)tm * tn;
+            const long long tiles = p.batch * per, full = tiles / g.pairs, rest = tiles % g.pairs;
+            const double unit = w == 1 ? 0.33 : full ? 0.27 : 0.18;
+            for (int n = 1; n <= 8; ++n) {
+                if (n > 1 && (rest == 0 || rest * n > g.pairs || g.kb < 4 * n || full)) continue;
+                const double t = (full + (rest ? 1.0 / n : 0.0)) * g.kb * unit + half + (n > 1 ? 6 + 2.5 * n : 0);
+                if (t < best) best = t, bn = 256 / w, parts = n, g.sym = half, g.per = (int)per, g.tn = tn;
+            }
+        }
+    g.tm = tm;
+    g.tiles = p.batch * g.per;
+    g.whole = g.tiles / g.pairs * g.pairs;
+    g.cut = std::max(1, (g.tiles - g.whole) * parts);
+    return bn == 256 ? muon_product_bn<256>(pl, p, g, oa, ob, s) : muon_product_bn<128>(pl, p, g, oa, ob, s);
 }
 
 int muon_run(const MuonPlan& pl, const void* grad, void* momentum, void* weight, void* out, char* ws, cudaStream_t s)
@@ -329,7 +358,7 @@ int muon_run(const MuonPlan& pl, const void* grad, void* momentum, void* weight,
         p.a = reinterpret_cast<__half*>(ws + pl.off_a), p.b = reinterpret_cast<__half*>(ws + pl.off_b);
     }
     if (q.steps > 0)
-        p.arrived = reinterpret_cast<int*>(ws + pl.off_arrived), p.narrived = pl.pairs * 16;
+        p.arrived = reinterpret_cast<int*>(ws + pl.off_arrived), p.narrived = pl.pairs * 2 * wg::kMgEpiWarps;
     const bool al = q.cols % 8 == 0 && q.ld % 8 == 0 && q.batch_stride % 8 == 0;
     const bool ivec = al && aligned16(grad) && aligned16(momentum), ovec = al && aligned16(weight) && aligned16(out);
     const dim3 egrid(pl.nparts, q.batch);
@@ -340,15 +369,9 @@ int muon_run(const MuonPlan& pl, const void* grad, void* momentum, void* weight,
                     ivec && (q.steps > 0 || ovec) ? wg::muon_normalize_kernel<8> : wg::muon_normalize_kernel<1>, egrid,
                     dim3(256), 0, s, p, (int)(q.steps == 0));
     if (st || q.steps == 0) return st;
-    // Tensor maps: X read along and across its rows, A and B along theirs.
     const bool wide = q.rows <= q.cols;
-    CUtensorMap along[2], across[2], ma, mb;
-    for (int i = 0; i < 2; ++i) {
-        if ((st = muon_map(&along[i], p.x[i], q.cols, q.rows, q.batch, pl.ldx, p.xs, 128))) return st;
-        if ((st = muon_map(&across[i], p.x[i], q.cols, q.rows, q.batch, pl.ldx, p.xs, 64))) return st;
-    }
-    if ((st = muon_map(&ma, p.a, pl.m, pl.m, q.batch, pl.ldm, p.ms, 128))) return st;
-    if ((st = muon_map(&mb, p.b, pl.m, pl.m, q.batch, pl.ldm, p.ms, 128))) return st;
+    const MuonOperand x[2] = {{p.x[0], q.cols, q.rows, pl.ldx, p.xs}, {p.x[1], q.cols, q.rows, pl.ldx, p.xs}};
+    const MuonOperand ma = {p.a, pl.m, pl.m, pl.ldm, p.ms}, mb = {p.b, pl.m, pl.m, pl.ldm, p.ms};
     for (int i = 0; i < q.steps; ++i) {
         const int in = i & 1;
         wg::MuonProduct g = {};
@@ -357,13 +380,12 @@ int muon_run(const MuonPlan& pl, const void* grad, void* momentum, void* weight,
         g.part = reinterpret_cast<float*>(ws + pl.off_sums), g.arrived = p.arrived;
         g.stage = 0, g.M = g.N = pl.m, g.sym = 1;
         g.a_mn = g.b_mn = !wide;
-        const CUtensorMap& x = wide ? along[in] : across[in];
-        if ((st = muon_product(pl, p, g, x, x, std::max(q.rows, q.cols), s))) return st;
+        if ((st = muon_product(pl, p, g, x[in], x[in], std::max(q.rows, q.cols), s))) return st;
         g.stage = 1, g.a_mn = g.b_mn = 0;
         if ((st = muon_product(pl, p, g, ma, ma, pl.m, s))) return st;
         g.stage = 2, g.M = q.rows, g.N = q.cols, g.sym = 0;
         g.b_mn = wide;
-        st = wide ? muon_product(pl, p, g, mb, across[in], pl.m, s) : muon_product(pl, p, g, along[in], mb, pl.m, s);
+        st = wide ? muon_product(pl, p, g, mb, x[in], pl.m, s) : muon_product(pl, p, g, x[in], mb, pl.m, s);
         if (st) return st;
     }
     return WG_OK;
