@@ -35,6 +35,9 @@ struct MuonParams {
     __half *x[2], *xlo, *a, *b;
     float* part;          // [batch][nparts] partial sums of squares
     int nparts;
+    int nv;  // vectors of a row (the elementwise kernels), and i / nv = i * nv_mul >> nv_shift
+    unsigned nv_mul;
+    int nv_shift;
     int *arrived, narrived;  // counters of the products' parts, zeroed by the first kernel
 };
 
@@ -153,45 +156,76 @@ __device__ __forceinline__ float block_sum_256(float s)
     return s;
 }
 
-// u at VEC elements along a row.  STEP: the momentum's step is taken and written;
-// otherwise it has been.
-template <int VEC, bool STEP>
-__device__ __forceinline__ void muon_u(const MuonParams& p, long long e, float (&u)[VEC])
+// What u at VEC elements along a row is made of, and u.  STEP: the momentum's step
+// is taken (m is then the new momentum); otherwise it has been.
+template <int VEC>
+__device__ __forceinline__ void muon_read(const MuonParams& p, long long e, float (&g)[VEC], float (&m)[VEC])
 {
     if constexpr (VEC == 8)
-        muon_load8(p.grad, p.grad_dtype, e, u);
+        muon_load8(p.grad, p.grad_dtype, e, g);
     else
-        u[0] = muon_elem(p, e);
+        g[0] = muon_elem(p, e);
+    if (p.mom) load_f32<float, VEC>(p.mom + e, m);
+}
+template <int VEC, bool STEP>
+__device__ __forceinline__ void muon_make(const MuonParams& p, float (&u)[VEC], float (&m)[VEC])
+{
     if (!p.mom) return;
-    float m[VEC];
-    load_f32<float, VEC>(p.mom + e, m);
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
         const float y = p.gain * u[k];
         if (STEP) m[k] = fmaf(p.mu, m[k], y);
         u[k] = p.nesterov ? fmaf(p.mu, m[k], y) : m[k];
     }
-    if (STEP) store_f32<float, VEC>(p.mom + e, m);
 }
+template <int VEC, bool STEP>
+__device__ __forceinline__ void muon_u(const MuonParams& p, long long e, float (&u)[VEC])
+{
+    float m[VEC];
+    muon_read<VEC>(p, e, u, m);
+    muon_make<VEC, STEP>(p, u, m);
+    if (STEP && p.mom) store_f32<float, VEC>(p.mom + e, m);
+}
+
+// The row of vector i of a matrix of p.nv vectors a row (i < 2^31).
+__device__ __forceinline__ int muon_row(const MuonParams& p, int i)
+{
+    return (int)(((unsigned long long)(unsigned)i * p.nv_mul) >> p.nv_shift);
+}
+
+// Vectors in flight per thread: the kernels below are bound by HBM.
+template <int VEC>
+constexpr int kMuonAhead = VEC == 8 ? 2 : 8;
 
 // The momentum's step and the partial sums of u's squares.
 template <int VEC>
 __global__ void __launch_bounds__(256) muon_momentum_kernel(const __grid_constant__ MuonParams p)
 {
+    constexpr int U = kMuonAhead<VEC>;
     pdl_launch_dependents();
     pdl_wait();
     if (blockIdx.x == 0 && blockIdx.y == 0)
         for (int i = threadIdx.x; i < p.narrived; i += 256) p.arrived[i] = 0;
-    const int nv = p.cols / VEC, n = p.rows * nv;
+    const int n = p.rows * p.nv, step = gridDim.x * 256;
     const long long base = (long long)blockIdx.y * p.bs;
     float s = 0.f;
-#pragma unroll 2
-    for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) {
-        const int r = i / nv;
-        float u[VEC];
-        muon_u<VEC, true>(p, base + r * p.ld + (i - r * nv) * VEC, u);
+    for (int i0 = blockIdx.x * 256 + threadIdx.x; i0 < n; i0 += U * step) {
+        float g[U][VEC], m[U][VEC];
+        long long e[U];
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) s = fmaf(u[k], u[k], s);
+        for (int q = 0; q < U; ++q) {
+            const int i = min(i0 + q * step, n - 1), r = muon_row(p, i);
+            e[q] = base + r * p.ld + (i - r * p.nv) * VEC;
+            muon_read<VEC>(p, e[q], g[q], m[q]);
+        }
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+            if (i0 + q * step >= n) break;
+            muon_make<VEC, true>(p, g[q], m[q]);
+            if (p.mom) store_f32<float, VEC>(p.mom + e[q], m[q]);
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) s = fmaf(g[q][k], g[q][k], s);
+        }
     }
     s = block_sum_256(s);
     if (threadIdx.x == 0) p.part[blockIdx.y * p.nparts + blockIdx.x] = s;
@@ -212,34 +246,45 @@ __device__ __forceinline__ float muon_inv_norm(const MuonParams& p, int b)
 template <int VEC>
 __global__ void __launch_bounds__(256) muon_normalize_kernel(const __grid_constant__ MuonParams p, int last)
 {
+    constexpr int U = kMuonAhead<VEC>;
     pdl_launch_dependents();
     pdl_wait();
-    const int nv = p.cols / VEC, n = p.rows * nv;
+    const int n = p.rows * p.nv, step = gridDim.x * 256;
     const long long base = (long long)blockIdx.y * p.bs;
     const float inv = muon_inv_norm(p, blockIdx.y);
-#pragma unroll 2
-    for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) {
-        const int r = i / nv, c = (i - r * nv) * VEC;
-        const long long e = base + r * p.ld + c, k = blockIdx.y * p.xs + (long long)r * p.ldx + c;
-        float u[VEC];
-        muon_u<VEC, false>(p, e, u);
-        if constexpr (VEC == 8) {
+    const float f = last ? inv * p.scale : kMuonXScale * inv;
+    for (int i0 = blockIdx.x * 256 + threadIdx.x; i0 < n; i0 += U * step) {
+        float u[U][VEC], m[U][VEC];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) u[q] *= last ? inv * p.scale : kMuonXScale * inv;
-            if (last) {
-                muon_finish8(p, e, u);
+        for (int q = 0; q < U; ++q) {
+            const int i = min(i0 + q * step, n - 1), r = muon_row(p, i);
+            muon_read<VEC>(p, base + r * p.ld + (i - r * p.nv) * VEC, u[q], m[q]);
+        }
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+            const int i = i0 + q * step;
+            if (i >= n) break;
+            const int r = muon_row(p, i), c = (i - r * p.nv) * VEC;
+            const long long k = blockIdx.y * p.xs + (long long)r * p.ldx + c;
+            muon_make<VEC, false>(p, u[q], m[q]);
+#pragma unroll
+            for (int x = 0; x < VEC; ++x) u[q][x] *= f;
+            if constexpr (VEC == 8) {
+                if (last) {
+                    muon_finish8(p, base + r * p.ld + c, u[q]);
+                } else {
+                    uint4 h, l;
+                    split8<false>(u[q], &h, &l);
+                    *reinterpret_cast<uint4*>(p.x[0] + k) = h;
+                    *reinterpret_cast<uint4*>(p.xlo + k) = l;
+                }
+            } else if (last) {
+                muon_finish(p, base + r * p.ld + c, u[q][0]);
             } else {
-                uint4 h, l;
-                split8<false>(u, &h, &l);
-                *reinterpret_cast<uint4*>(p.x[0] + k) = h;
-                *reinterpret_cast<uint4*>(p.xlo + k) = l;
+                const __half h = __float2half_rn(u[q][0]);
+                p.x[0][k] = h;
+                p.xlo[k] = __float2half_rn(u[q][0] - __half2float(h));
             }
-        } else if (last) {
-            muon_finish(p, e, u[0] * inv * p.scale);
-        } else {
-            const float x = kMuonXScale * (u[0] * inv);
-            p.x[0][k] = __float2half_rn(x);
-            p.xlo[k] = __float2half_rn(x - __half2float(__float2half_rn(x)));
         }
     }
 }

@@ -70,7 +70,7 @@ int check_workspace(size_t need, const void* workspace, size_t ws_bytes)
 }
 
 // ---------------------------------------------------------------- orthogonalised update
-constexpr int kMuonMaxDim = 32768, kMuonMaxSteps = 16, kMuonMaxParts = 304;
+constexpr int kMuonMaxDim = 32768, kMuonMaxSteps = 16, kMuonMaxParts = 1216;
 
 struct MuonPlan {
     wg_muon_problem p;
@@ -173,7 +173,8 @@ int make_muon_plan(const wg_muon_problem* p, MuonPlan* pl)
     pl->ldx = (q.cols + 7) / 8 * 8;
     pl->ldm = (pl->m + 7) / 8 * 8;
     const long long n = (long long)q.rows * q.cols;
-    pl->nparts = (int)std::max(1LL, std::min<long long>(kMuonMaxParts, (n + 2047) / 2048));
+    // Eight CTAs of the elementwise kernels per SM, of 2048 elements at least.
+    pl->nparts = (int)std::max(1LL, std::min<long long>(std::max(1, kMuonMaxParts / q.batch), (n + 2047) / 2048));
     size_t o = 0;
     pl->gram = q.steps > 0 && pl->m <= 128;
     if (pl->gram) {
@@ -362,11 +363,22 @@ int muon_run(const MuonPlan& pl, const void* grad, void* momentum, void* weight,
     const bool al = q.cols % 8 == 0 && q.ld % 8 == 0 && q.batch_stride % 8 == 0;
     const bool ivec = al && aligned16(grad) && aligned16(momentum), ovec = al && aligned16(weight) && aligned16(out);
     const dim3 egrid(pl.nparts, q.batch);
+    // Division of vector indexes (below 2^31) by the vectors of a row.
+    const auto rows_of = [&](bool vec) {
+        p.nv = vec ? q.cols / 8 : q.cols;
+        int bits = 0;
+        while ((1LL << bits) < p.nv) ++bits;
+        p.nv_shift = 31 + bits;
+        p.nv_mul = (unsigned)(((1ULL << p.nv_shift) + p.nv - 1) / p.nv);
+    };
+    const bool nvec = ivec && (q.steps > 0 || ovec);
+    rows_of(ivec);
     int st = launch("muon_momentum_kernel launch", ivec ? wg::muon_momentum_kernel<8> : wg::muon_momentum_kernel<1>,
                     egrid, dim3(256), 0, s, p);
+    rows_of(nvec);
     if (!st)
         st = launch("muon_normalize_kernel launch",
-                    ivec && (q.steps > 0 || ovec) ? wg::muon_normalize_kernel<8> : wg::muon_normalize_kernel<1>, egrid,
+                    nvec ? wg::muon_normalize_kernel<8> : wg::muon_normalize_kernel<1>, egrid,
                     dim3(256), 0, s, p, (int)(q.steps == 0));
     if (st || q.steps == 0) return st;
     const bool wide = q.rows <= q.cols;
