@@ -26,7 +26,8 @@
 // alone runs the steps; Q goes through the workspace, and every CTA multiplies
 // its chunks of U, which it reads again (L2), and writes its part of the results.
 // Bound by latency: three dependent products a step, each MMA -> tensor memory ->
-// registers -> shared memory.
+// registers -> shared memory.  One warp does nothing but issue MMAs, so that A P
+// is on its way through the other sixteen while P Q runs.
 #pragma once
 
 #include <type_traits>
@@ -35,7 +36,8 @@
 
 namespace wg {
 
-constexpr int kGramThreads = 512;
+constexpr int kGramThreads = 512;            // the warps that move and convert
+constexpr int kGramBlock = kGramThreads + 32;  // and the one that issues MMAs
 constexpr int kGramMaxSteps = 16;
 
 struct GramParams {
@@ -48,9 +50,13 @@ struct GramParams {
     int vec;         // eight elements along memory of grad and momentum are aligned and of one matrix
     int ovec;        // and of weight and out
     int split;       // U needs its second bf16 value
+    int kn;          // 16-wide parts of a block's rows that are used
     int steps;
-    float coef[kGramMaxSteps][3];
-    float sa[kGramMaxSteps], sp[kGramMaxSteps], ss[kGramMaxSteps], sq[kGramMaxSteps];  // powers of two of the operands
+    // Per step: P = pa I + pb (TA) + pc (T2); S = rs (T2); Q = rq (TQ); A = ra (TA), the
+    // tensor-memory sums holding products of operands scaled by sa, sp, ss and sq (powers of two).
+    struct Step {
+        float pa, pb, pc, rs, rq, ra, sa, sp, ss, sq;
+    } step[kGramMaxSteps];
     uint8_t* q;      // [blocks][P == 64 ? 16 : 64 KB] operand image of Q, bf16 pairs
     float* factor;   // [blocks][128] scale / (|u|_F + eps) per row of a block
 };
@@ -117,18 +123,44 @@ __device__ __forceinline__ void gram_put(uint8_t* img, int r, int c0, const floa
 // (symmetric up to roundings) transposes the roundings of Q between a direction
 // the matrix has and one it lacks, which are 482 times larger on one side than on
 // the other: gradients of rank one were 10% off.
+// P = 64: the two images of Y lie one after the other, and one MMA of 128 columns
+// multiplies both: hi hi + lo hi in columns 0 .. 63, hi lo in columns 64 .. 127 (an
+// MMA takes some 66 cycles whatever its columns up to 128: 2 instead of 3).
 template <int P>
-__device__ __forceinline__ void gram_product(uint32_t d, uint32_t x, uint32_t y)
+__device__ __forceinline__ void gram_product(uint32_t d, uint32_t x, uint32_t y, int kn)
 {
-    const uint32_t idesc = make_idesc_f16(false, false, true, 128, P);
+    const uint32_t idesc = make_idesc_f16(false, false, true, 128, P == 64 ? 64 : 16 * kn);
+    const uint32_t idesc2 = make_idesc_f16(false, false, true, 128, 128);
     const uint64_t xd = make_sdesc(x, 16u, 1024u, 2u, 0u), yd = make_sdesc(y, P * 128u, 1024u, 2u, 0u);
     constexpr uint64_t lo = gram_mat_bytes(P) >> 4;
-#pragma unroll
-    for (int ks = 0; ks < P / 16; ++ks) {
+#pragma unroll 1
+    for (int ks = 0; ks < kn; ++ks) {
         const uint64_t xo = (uint64_t)((ks >> 2) * (P * 8) + 2 * (ks & 3)), yo = (uint64_t)(128 * ks);
-        umma_f16(d, xd + xo, yd + yo, idesc, ks ? 1u : 0u);
-        umma_f16(d, xd + xo, yd + yo + lo, idesc, 1u);
+        if (P == 64) {
+            umma_f16(d, xd + xo, yd + yo, idesc2, ks ? 1u : 0u);
+        } else {
+            umma_f16(d, xd + xo, yd + yo, idesc, ks ? 1u : 0u);
+            umma_f16(d, xd + xo, yd + yo + lo, idesc, 1u);
+        }
         umma_f16(d, xd + xo + lo, yd + yo, idesc, 1u);
+    }
+}
+
+// NC columns of a product, from column c0 (and of its second half).
+template <int P, int NC>
+__device__ __forceinline__ void gram_sums(uint32_t taddr, float (&v)[NC])
+{
+    if (P == 64) {
+        uint32_t r[2 * NC];
+#pragma unroll
+        for (int i = 0; i < NC; i += 16) tmem_ld16_issue(taddr + i, r + i), tmem_ld16_issue(taddr + 64 + i, r + NC + i);
+        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < 2 * NC; i += 16) reg_fence16(r + i);
+#pragma unroll
+        for (int i = 0; i < NC; ++i) v[i] = __uint_as_float(r[i]) + __uint_as_float(r[NC + i]);
+    } else {
+        gram_ld<NC>(taddr, v);
     }
 }
 
@@ -174,13 +206,13 @@ __device__ __forceinline__ void gram_load8(const GramParams& g, int blk, int ch,
 }
 
 template <int P>
-__global__ void __launch_bounds__(kGramThreads, 1) muon_gram_kernel(const __grid_constant__ GramParams g)
+__global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_constant__ GramParams g)
 {
     constexpr int NC = P / 4;                     // columns per thread: four warps share a row
     constexpr int MAT = gram_mat_bytes(P), PAIR = 2 * MAT;
     constexpr int IMG = P * 128;                  // one staged image of 64 positions of the long side
-    constexpr uint32_t TA = 0, T2 = P, TQ = 2 * P;  // tensor-memory columns: A, (A A | A P), P Q
-    constexpr int TCOLS = P == 128 ? 512 : 256;
+    constexpr uint32_t TA = 0, T2 = 128, TQ = 256;  // tensor-memory columns: A, (A A | A P), P Q
+    constexpr int TCOLS = 512;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bar[3];
     __shared__ uint32_t tslot;
@@ -190,17 +222,29 @@ __global__ void __launch_bounds__(kGramThreads, 1) muon_gram_kernel(const __grid
     uint8_t *ba = smem, *bp = smem + PAIR, *bq = smem + 2 * PAIR;  // A (and A P), P, Q
     const MuonParams& p = g.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const bool issuer = warp == kGramThreads / 32;  // the warp that issues MMAs
     const int rank = (int)cluster_ctarank(), blk = blockIdx.x / g.C;
-    // This thread's part of a Gram-sized matrix: row, first column, and the columns of the row's own matrix.
+    // This thread's part of a Gram-sized matrix: row, first column, and which of
+    // its columns are of the row's own matrix.
     const int row = (warp & 3) * 32 + lane, c0 = (warp >> 2) * NC;
-    const bool act = row < P;
+    const bool act = row < P && !issuer;
     const int mine = row / p.m, lo = mine * p.m, hi = mine < g.F ? lo + p.m : lo;
+    uint32_t own = 0;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) own |= (c0 + i >= lo && c0 + i < hi ? 1u : 0u) << i;
     bool ok = true;
     uint32_t ph[3] = {0, 0, 0};
     auto wait = [&](int b) {
         if (ok) ok = mbar_wait(&bar[b], ph[b]);
         ph[b] ^= 1u;
         __syncwarp();
+        tc_fence_after();
+    };
+    // What this thread has written to shared memory and read from tensor memory is done, for the next MMAs.
+    auto ready = [&] {
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncthreads();
         tc_fence_after();
     };
 
@@ -244,31 +288,35 @@ __global__ void __launch_bounds__(kGramThreads, 1) muon_gram_kernel(const __grid
         }
     };
     auto load = [&](int ch, auto step, float (&u)[P / 64][8]) {
+        if (ch >= g.chunks) return;
 #pragma unroll
         for (int j = 0; j < P / 64; ++j)
             gram_load8<decltype(step)::value>(g, blk, ch, g.wide ? line + 64 * j : line, g.wide ? seg : seg + 64 * j, u[j]);
     };
-    {
+    const int nch = (g.chunks - rank + g.C - 1) / g.C;  // this CTA's chunks: rank, rank + C, ...
+    if (!issuer) {
         float u[P / 64][8];
-        int it = 0;
-        if (rank < g.chunks) load(rank, std::true_type{}, u);
-        for (int ch = rank; ch < g.chunks; ch += g.C, ++it) {
-            const int s = it & 1;
-            if (it >= 2) wait(s);
-            uint8_t* img = ba + s * 2 * IMG;
-            stage(img, u);
-            fence_proxy_async_smem();
-            tc_fence_before();
+        load(rank, std::true_type{}, u);
+        for (int it = 0; it < nch; ++it) {
+            if (it >= 2) wait(it & 1);
+            stage(ba + (it & 1) * 2 * IMG, u);
+            ready();
+            load(rank + (it + 1) * g.C, std::true_type{}, u);
+        }
+        if (nch >= 2) wait(nch & 1);
+        if (nch >= 1) wait((nch - 1) & 1);
+    } else {
+        const uint32_t mn = g.wide ? 0u : 1u;
+        const uint32_t idesc = make_idesc_f16(true, mn, mn, 128, P);
+        for (int it = 0; it < nch; ++it) {
             __syncthreads();
-            if (tid == 0) {
-                tc_fence_after();
-                const uint32_t mn = g.wide ? 0u : 1u;
-                const uint32_t idesc = make_idesc_f16(true, mn, mn, 128, P);
-                const uint32_t a = smem_u32(img);
+            tc_fence_after();
+            if (elect_one()) {
+                const uint32_t a = smem_u32(ba + (it & 1) * 2 * IMG);
                 // Tall blocks of 64 rows: the second 64 rows of the MMA read the first again.
                 const uint64_t d = g.wide ? make_sdesc(a, 16u, 1024u, 2u, 0u)
                                           : make_sdesc(a, P == 128 ? 8192u : 0u, 1024u, 2u, 0u);
-#pragma unroll
+#pragma unroll 1
                 for (int ks = 0; ks < 4; ++ks) {
                     const uint64_t o = (uint64_t)(ks * (g.wide ? 2 : 128)), l = IMG >> 4;
                     umma_f16(tb + TA, d + o, d + o, idesc, (it | ks) ? 1u : 0u);
@@ -277,12 +325,10 @@ __global__ void __launch_bounds__(kGramThreads, 1) muon_gram_kernel(const __grid
                         umma_f16(tb + TA, d + o + l, d + o, idesc, 1u);
                     }
                 }
-                umma_commit(&bar[s]);
+                umma_commit(&bar[it & 1]);
             }
-            if (ch + g.C < g.chunks) load(ch + g.C, std::true_type{}, u);
+            __syncwarp();
         }
-        if (it >= 2) wait(it & 1);
-        if (it >= 1) wait((it - 1) & 1);
     }
     // This CTA's partial sum in P's place (fp32 rows, 16-byte chunks swizzled by
     // the row); NaN on the diagonal of a row that held a NaN or an infinity.
@@ -292,7 +338,7 @@ __global__ void __launch_bounds__(kGramThreads, 1) muon_gram_kernel(const __grid
         gram_ld<NC>(trow + TA, v);
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            if (rank >= g.chunks) v[i] = 0.f;
+            if (nch <= 0) v[i] = 0.f;
             if (c0 + i == row && bad[row]) v[i] = NAN;
         }
 #pragma unroll
@@ -301,13 +347,14 @@ __global__ void __launch_bounds__(kGramThreads, 1) muon_gram_kernel(const __grid
                 make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
     }
     cluster_sync_all();
-    {
+    if (!issuer) {
         // Rows rank * P / C .. of the sum over the cluster, into rank 0's Q.
         const int chunks16 = P * P / 4 / g.C;  // 16-byte chunks of a slice
         const uint32_t src = smem_u32(bp), dst = mapa_shared(smem_u32(bq), 0u);
         for (int i = tid; i < chunks16; i += kGramThreads) {
             const uint32_t o = (uint32_t)(rank * chunks16 + i) << 4;
             float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
             for (int c = 0; c < g.C; ++c) {
                 const float4 x = ld_dsmem_v4(mapa_shared(src + o, (uint32_t)c));
                 s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
@@ -319,7 +366,42 @@ __global__ void __launch_bounds__(kGramThreads, 1) muon_gram_kernel(const __grid
 
     // ---------------------------------------------------- the steps, on rank 0
     uint8_t* qimg = g.q + (size_t)blk * PAIR;
-    if (rank == 0) {
+    if (rank == 0 && issuer) {
+        const uint32_t sba = smem_u32(ba), sbp = smem_u32(bp), sbq = smem_u32(bq);
+        __syncthreads();  // the diagonal
+        for (int k = 0; k < g.steps; ++k) {
+            const bool last = k == g.steps - 1;
+            __syncthreads();
+            tc_fence_after();
+            if (elect_one()) {
+                gram_product<P>(tb + T2, sba, sba, g.kn);
+                umma_commit(&bar[0]);
+            }
+            __syncwarp();
+            if (last && k == 0) break;
+            __syncthreads();
+            tc_fence_after();
+            if (elect_one()) {
+                if (!last) {
+                    gram_product<P>(tb + T2, sba, sbp, g.kn);
+                    umma_commit(&bar[0]);
+                }
+                if (k > 0) {
+                    gram_product<P>(tb + TQ, sbp, sbq, g.kn);
+                    umma_commit(&bar[1]);
+                }
+            }
+            __syncwarp();
+            if (last) break;
+            __syncthreads();
+            tc_fence_after();
+            if (elect_one()) {
+                gram_product<P>(tb + TA, sba, sbp, g.kn);  // A <- S P
+                umma_commit(&bar[2]);
+            }
+            __syncwarp();
+        }
+    } else if (rank == 0) {
         float v[NC];
         if (act) {
 #pragma unroll
@@ -341,89 +423,55 @@ __global__ void __launch_bounds__(kGramThreads, 1) muon_gram_kernel(const __grid
             const float inv = fin && d > 0.f ? 1.f / d : 0.f;
             if (c0 == 0) g.factor[blk * 128 + row] = fin ? p.scale * inv : NAN;
 #pragma unroll
-            for (int i = 0; i < NC; ++i) v[i] = fin && c0 + i >= lo && c0 + i < hi ? v[i] * inv * inv : 0.f;
+            for (int i = 0; i < NC; ++i) v[i] = fin && (own >> i & 1u) ? v[i] * inv * inv : 0.f;
 #pragma unroll
             for (int i = 0; i < NC; i += 16) tmem_st16(trow + TA + i, v + i);
-            gram_put<P, NC>(ba, row, c0, v, g.sa[0]);
+            gram_put<P, NC>(ba, row, c0, v, g.step[0].sa);
+            if (P == 64) {
+                float z[NC] = {};
+#pragma unroll
+                for (int i = 0; i < NC; i += 16) tmem_st16(trow + TA + 64 + i, z + i);
+            }
         }
-        float ra = 1.f;  // A = ra * (tensor memory)
-        const uint32_t sba = smem_u32(ba), sbp = smem_u32(bp), sbq = smem_u32(bq);
-        auto ready = [&] {
-            fence_proxy_async_smem();
-            tc_fence_before();
-            __syncthreads();
+        // v = f (sums at t), zero between matrices, times s into the pair at img.
+        auto convert = [&](uint32_t t, float f, uint8_t* img, float s) {
+            gram_sums<P, NC>(trow + t, v);
+#pragma unroll
+            for (int i = 0; i < NC; ++i) v[i] = own >> i & 1u ? v[i] * f : 0.f;
+            if (img) gram_put<P, NC>(img, row, c0, v, s);
         };
-        auto masked = [&](float x, int i) { return c0 + i >= lo && c0 + i < hi ? x : 0.f; };
         for (int k = 0; k < g.steps; ++k) {
             const bool last = k == g.steps - 1;
-            const float a = g.coef[k][0], b = g.coef[k][1], c = g.coef[k][2];
+            const GramParams::Step w = g.step[k];
             ready();
-            if (tid == 0) {
-                tc_fence_after();
-                gram_product<P>(tb + T2, sba, sba);
-                umma_commit(&bar[0]);
-            }
             wait(0);
             if (act) {
                 // P = a I + b A + c A A
                 float x[NC];
-                gram_ld<NC>(trow + T2, v);
-                gram_ld<NC>(trow + TA, x);
-                const float r2 = c / (g.sa[k] * g.sa[k]), r1 = b * ra;
+                gram_sums<P, NC>(trow + T2, v);
+                gram_sums<P, NC>(trow + TA, x);
 #pragma unroll
-                for (int i = 0; i < NC; ++i) v[i] = masked(fmaf(r2, v[i], fmaf(r1, x[i], c0 + i == row ? a : 0.f)), i);
-                gram_put<P, NC>(bp, row, c0, v, g.sp[k]);
-                if (k == 0 && !last) gram_put<P, NC>(bq, row, c0, v, g.sq[0]);
+                for (int i = 0; i < NC; ++i) {
+                    v[i] = fmaf(w.pc, v[i], w.pb * x[i]) + (c0 + i == row ? w.pa : 0.f);
+                    v[i] = own >> i & 1u ? v[i] : 0.f;
+                }
+                gram_put<P, NC>(bp, row, c0, v, w.sp);
+                if (k == 0 && !last) gram_put<P, NC>(bq, row, c0, v, w.sq);
             }
+            if (last && k == 0) break;
             ready();
-            if (tid == 0) {
-                tc_fence_after();
-                if (!last) {
-                    gram_product<P>(tb + T2, sba, sbp);
-                    umma_commit(&bar[0]);
-                }
-                if (k > 0) {
-                    gram_product<P>(tb + TQ, sbp, sbq);
-                    umma_commit(&bar[1]);
-                }
-            }
             if (!last) {
                 wait(0);
-                if (act) {
-                    // S = A P, in A's place
-                    gram_ld<NC>(trow + T2, v);
-                    const float r = 1.f / (g.sa[k] * g.sp[k]);
-#pragma unroll
-                    for (int i = 0; i < NC; ++i) v[i] = masked(v[i] * r, i);
-                    gram_put<P, NC>(ba, row, c0, v, g.ss[k]);
-                }
+                if (act) convert(T2, w.rs, ba, w.ss);  // S = A P, in A's place
                 ready();
-                if (tid == 0) {
-                    tc_fence_after();
-                    gram_product<P>(tb + TA, sba, sbp);  // A <- S P
-                    umma_commit(&bar[2]);
-                }
             }
             if (k > 0) {
                 wait(1);
-                if (act) {
-                    gram_ld<NC>(trow + TQ, v);
-                    const float r = 1.f / (g.sp[k] * g.sq[k - 1]);
-#pragma unroll
-                    for (int i = 0; i < NC; ++i) v[i] = masked(v[i] * r, i);
-                    if (!last) gram_put<P, NC>(bq, row, c0, v, g.sq[k]);
-                }
+                if (act) convert(TQ, w.rq, last ? nullptr : bq, w.sq);
             }
             if (!last) {
                 wait(2);
-                ra = 1.f / (g.ss[k] * g.sp[k]);
-                if (act) {
-                    gram_ld<NC>(trow + TA, v);
-#pragma unroll
-                    for (int i = 0; i < NC; ++i) v[i] = masked(v[i] * ra, i);
-                    gram_put<P, NC>(ba, row, c0, v, g.sa[k + 1]);
-                }
-                // What lies between matrices stays out of the next P as well: it is masked there.
+                if (act) convert(TA, w.ra, ba, g.step[k + 1].sa);
             }
         }
         if (act) {
@@ -439,42 +487,26 @@ __global__ void __launch_bounds__(kGramThreads, 1) muon_gram_kernel(const __grid
         }
         __threadfence();
     }
+    // The first chunk of U comes back while Q is on its way.
+    float u[P / 64][8];
+    if (!issuer) load(rank, std::false_type{}, u);
     cluster_sync_all();
 
     // ---------------------------------------------------- results: X = Q U over this CTA's chunks
-    for (int i = tid; i < PAIR / 16; i += kGramThreads)
-        reinterpret_cast<uint4*>(bq)[i] = __ldcg(reinterpret_cast<const uint4*>(qimg) + i);
-    if (tid < P) fac[tid] = __ldcg(g.factor + blk * 128 + tid);
-    {
-        float u[P / 64][8];
-        if (rank < g.chunks) load(rank, std::false_type{}, u);
-        for (int ch = rank; ch < g.chunks; ch += g.C) {
-            stage(ba, u);
-            fence_proxy_async_smem();
-            tc_fence_before();
-            __syncthreads();
-            if (tid == 0) {
-                tc_fence_after();
-                const uint32_t idesc = make_idesc_f16(true, false, g.wide != 0, 128, 64);
-                const uint32_t img = smem_u32(ba);
-                const uint64_t qd = make_sdesc(smem_u32(bq), 16u, 1024u, 2u, 0u);
-                const uint64_t ud = g.wide ? make_sdesc(img, 8192u, 1024u, 2u, 0u) : make_sdesc(img, 16u, 1024u, 2u, 0u);
-                const uint64_t ql = MAT >> 4, ul = IMG >> 4;
-#pragma unroll
-                for (int ks = 0; ks < P / 16; ++ks) {
-                    const uint64_t qo = (uint64_t)((ks >> 2) * (P * 8) + 2 * (ks & 3));
-                    const uint64_t uo = g.wide ? (uint64_t)(128 * ks) : (uint64_t)((ks >> 2) * 512 + 2 * (ks & 3));
-                    umma_f16(tb + T2, qd + qo, ud + uo, idesc, ks ? 1u : 0u);
-                    umma_f16(tb + T2, qd + qo + ql, ud + uo, idesc, 1u);
-                    if (g.split) umma_f16(tb + T2, qd + qo, ud + uo + ul, idesc, 1u);
-                }
-                umma_commit(&bar[0]);
-            }
-            if (ch + g.C < g.chunks) load(ch + g.C, std::false_type{}, u);
-            wait(0);
+    if (!issuer) {
+        for (int i = tid; i < PAIR / 16; i += kGramThreads)
+            reinterpret_cast<uint4*>(bq)[i] = __ldcg(reinterpret_cast<const uint4*>(qimg) + i);
+        if (tid < P) fac[tid] = __ldcg(g.factor + blk * 128 + tid);
+        for (int it = 0; it < nch; ++it) {
+            const int ch = rank + it * g.C;
+            // (The MMAs that read this image two chunks ago are done: their sums have been read.)
+            stage((it & 1 ? bp : ba), u);
+            ready();
+            load(ch + g.C, std::false_type{}, u);
+            wait(it & 1);
             float x[16];
             const int q0 = (warp >> 2) * 16;
-            if (act) gram_ld<16>(tb + ((uint32_t)((warp & 3) * 32) << 16) + T2 + (uint32_t)q0, x);
+            if (act) gram_ld<16>(tb + ((uint32_t)((warp & 3) * 32) << 16) + (it & 1 ? T2 : TA) + (uint32_t)q0, x);
             const int b = blk * g.F + mine;
             if (act && mine < g.F && b < p.batch) {
                 const float f = fac[row];
@@ -488,16 +520,37 @@ __global__ void __launch_bounds__(kGramThreads, 1) muon_gram_kernel(const __grid
                         for (int k = 0; k < 8; ++k) o[k] = f * x[i + k];
                         if (n0 + i < g.N) muon_finish8(p, base + (row - lo) * p.ld + n0 + i, o);
                     }
-                } else
+                } else {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int n = n0 + i;
-                    if (n < g.N)
-                        muon_finish(p, base + (g.wide ? (row - lo) * p.ld + n : n * p.ld + (row - lo)), f * x[i]);
+                    for (int i = 0; i < 16; ++i) {
+                        const int n = n0 + i;
+                        if (n < g.N)
+                            muon_finish(p, base + (g.wide ? (row - lo) * p.ld + n : n * p.ld + (row - lo)), f * x[i]);
+                    }
                 }
             }
-            tc_fence_before();
-            __syncthreads();  // the staged image and the accumulator are free
+        }
+    } else {
+        const uint32_t idesc = make_idesc_f16(true, false, g.wide != 0, 128, 64);
+        const uint64_t qd = make_sdesc(smem_u32(bq), 16u, 1024u, 2u, 0u);
+        for (int it = 0; it < nch; ++it) {
+            __syncthreads();
+            tc_fence_after();
+            if (elect_one()) {
+                const uint32_t img = smem_u32(it & 1 ? bp : ba), d = tb + (it & 1 ? T2 : TA);
+                const uint64_t ud = g.wide ? make_sdesc(img, 8192u, 1024u, 2u, 0u) : make_sdesc(img, 16u, 1024u, 2u, 0u);
+                const uint64_t ql = MAT >> 4, ul = IMG >> 4;
+#pragma unroll 1
+                for (int ks = 0; ks < g.kn; ++ks) {
+                    const uint64_t qo = (uint64_t)((ks >> 2) * (P * 8) + 2 * (ks & 3));
+                    const uint64_t uo = g.wide ? (uint64_t)(128 * ks) : (uint64_t)((ks >> 2) * 512 + 2 * (ks & 3));
+                    umma_f16(d, qd + qo, ud + uo, idesc, ks ? 1u : 0u);
+                    umma_f16(d, qd + qo + ql, ud + uo, idesc, 1u);
+                    if (g.split) umma_f16(d, qd + qo, ud + uo + ul, idesc, 1u);
+                }
+                umma_commit(&bar[it & 1]);
+            }
+            __syncwarp();
         }
     }
     tc_fence_before();

@@ -102,21 +102,27 @@ void muon_gram_plan(MuonPlan* pl)
     // A CTA per chunk up to the portable cluster size, while every block has its clusters at once.
     g.C = 1;
     while (g.C < 8 && 2 * g.C <= g.chunks && 2LL * g.C * pl->blocks <= num_sms()) g.C *= 2;
+    g.kn = (g.F * pl->m + 15) / 16;
     double grid[513], prod[513], smax = 1.0;
     for (int i = 0; i <= 512; ++i) grid[i] = i / 512.0, prod[i] = 1.0;
     auto power = [](double bound) { return ldexpf(1.f, (int)floor(log2(8192.0 / std::max(bound, 1e-6)))); };
+    float ra = 1.f;  // A = ra * (its sums in tensor memory)
     for (int k = 0; k < q.steps; ++k) {
         const float* c = pl->coef[k];
-        memcpy(g.coef[k], c, sizeof g.coef[k]);
+        wg::GramParams::Step& w = g.step[k];
         double pmax = 0.0, spmax = 0.0, grown = 0.0, qmax = 0.0;
         for (int i = 0; i <= 512; ++i) {
             const double s = smax * i / 512, l = s * s, v = c[0] + c[1] * l + c[2] * l * l;
             pmax = std::max(pmax, fabs(v)), spmax = std::max(spmax, l * fabs(v)), grown = std::max(grown, s * fabs(v));
-            const double t = grid[i] * grid[i], w = c[0] + c[1] * t + c[2] * t * t;
-            prod[i] *= w, grid[i] *= w;
+            const double t = grid[i] * grid[i], u = c[0] + c[1] * t + c[2] * t * t;
+            prod[i] *= u, grid[i] *= u;
             qmax = std::max(qmax, fabs(prod[i]));
         }
-        g.sa[k] = power(smax * smax), g.sp[k] = power(pmax), g.ss[k] = power(spmax), g.sq[k] = power(qmax);
+        w.sa = power(smax * smax), w.sp = power(pmax), w.ss = power(spmax), w.sq = power(qmax);
+        w.pa = c[0], w.pb = c[1] * ra, w.pc = c[2] / (w.sa * w.sa);
+        w.rs = 1.f / (w.sa * w.sp);
+        w.rq = k ? 1.f / (w.sp * g.step[k - 1].sq) : 1.f;
+        w.ra = ra = 1.f / (w.ss * w.sp);
         smax = std::max(grown, 1e-3);
     }
 }
@@ -244,7 +250,7 @@ int muon_gram_launch(const MuonPlan& pl, const wg::GramParams& g, cudaStream_t s
     ++na;
     wg::pdl_config(&cfg, attr, &na, s);
     cfg.gridDim = dim3((unsigned)(pl.blocks * g.C));
-    cfg.blockDim = dim3(wg::kGramThreads);
+    cfg.blockDim = dim3(wg::kGramBlock);
     cfg.dynamicSmemBytes = (size_t)smem;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, wg::muon_gram_kernel<P>, g);
     return e == cudaSuccess ? WG_OK : cuda_fail("muon_gram_kernel launch", e);
