@@ -15,10 +15,10 @@
 // range is fp32's.
 //
 // A block of P = 64 or 128 rows of the Gram matrix holds as many whole matrices
-// as fit (the block-diagonal fold of the convolution kernels): entries between
-// different matrices are set to zero after every product.  A matrix that holds a
-// NaN or an infinity enters as zeros and leaves as NaN, so that it cannot reach
-// the others of its block.
+// as fit (the block-diagonal fold of the convolution kernels): entries of A_0
+// between different matrices are set to zero, and products keep them so.  A matrix
+// that holds a NaN or an infinity enters as zeros and leaves as NaN, so that it
+// cannot reach the others of its block.
 //
 // A cluster of C CTAs takes a block.  Each adds up U U^T over its 64-column
 // chunks of the long side (the momentum's step on the way); the C partial sums
@@ -433,13 +433,18 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
                 for (int i = 0; i < NC; i += 16) tmem_st16(trow + TA + 64 + i, z + i);
             }
         }
-        // v = f (sums at t), zero between matrices, times s into the pair at img.
+        // v = f (sums at t), times s into the pair at img.  (What A_0 has zero between
+        // matrices stays zero: every product adds zeros there.)
         auto convert = [&](uint32_t t, float f, uint8_t* img, float s) {
             gram_sums<P, NC>(trow + t, v);
+            if (img) {
+                gram_put<P, NC>(img, row, c0, v, f * s);
+            } else {
 #pragma unroll
-            for (int i = 0; i < NC; ++i) v[i] = own >> i & 1u ? v[i] * f : 0.f;
-            if (img) gram_put<P, NC>(img, row, c0, v, s);
+                for (int i = 0; i < NC; ++i) v[i] *= f;
+            }
         };
+        const uint32_t diagonal = row >= c0 && row < c0 + NC ? 1u << (row - c0) : 0u;
         for (int k = 0; k < g.steps; ++k) {
             const bool last = k == g.steps - 1;
             const GramParams::Step w = g.step[k];
@@ -452,8 +457,8 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
                 gram_sums<P, NC>(trow + TA, x);
 #pragma unroll
                 for (int i = 0; i < NC; ++i) {
-                    v[i] = fmaf(w.pc, v[i], w.pb * x[i]) + (c0 + i == row ? w.pa : 0.f);
-                    v[i] = own >> i & 1u ? v[i] : 0.f;
+                    v[i] = fmaf(w.pc, v[i], w.pb * x[i]);
+                    if (diagonal >> i & 1u) v[i] += w.pa;
                 }
                 gram_put<P, NC>(bp, row, c0, v, w.sp);
                 if (k == 0 && !last) gram_put<P, NC>(bq, row, c0, v, w.sq);
