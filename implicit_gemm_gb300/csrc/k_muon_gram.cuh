@@ -171,37 +171,82 @@ __device__ __forceinline__ void st_dsmem_v4(uint32_t addr, float4 v)
                  : "memory");
 }
 
-// The eight values of u at `line`, `seg` .. of chunk `ch` of block `blk` (a line is
-// a row of the block when the matrices are wide and a position of the long side
-// when they are tall; seg runs along memory).  STEP: the momentum's step is taken
-// and written; otherwise it has been.  Outside the matrices: zeros.
-template <bool STEP>
-__device__ __forceinline__ void gram_load8(const GramParams& g, int blk, int ch, int line, int seg, float (&u)[8])
+// Eight values of u as they come from memory: the conversion waits for them, the
+// load does not.  (Not aligned: u itself, as fp32.)
+struct GramRaw {
+    uint4 g[2], m[2];
+};
+
+// Address of element k of `line`, `seg` .. of chunk `ch` of block `blk` (a line is a
+// row of the block when the matrices are wide and a position of the long side when
+// they are tall; seg runs along memory), or -1 outside the matrices.
+__device__ __forceinline__ long long gram_at(const GramParams& g, int blk, int ch, int line, int seg, int k)
 {
     const MuonParams& p = g.p;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) u[k] = 0.f;
-    long long e[8];
-    bool ok[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const int i = g.wide ? line : seg + k, n = ch * 64 + (g.wide ? seg + k : line);
-        const int f = i / p.m, b = blk * g.F + f, idx = i - f * p.m;
-        ok[k] = f < g.F && b < p.batch && n < g.N;
-        e[k] = (long long)b * p.bs + (g.wide ? idx * p.ld + n : n * p.ld + idx);
-        if (g.vec && k == 0) break;
-    }
+    const int i = g.wide ? line : seg + k, n = ch * 64 + (g.wide ? seg + k : line);
+    const int f = i / p.m, b = blk * g.F + f, idx = i - f * p.m;
+    if (f >= g.F || b >= p.batch || n >= g.N) return -1;
+    return (long long)b * p.bs + (g.wide ? idx * p.ld + n : n * p.ld + idx);
+}
+
+// STEP: the momentum's step is taken and written; otherwise it has been.
+template <bool STEP>
+__device__ __forceinline__ void gram_read(const GramParams& g, int blk, int ch, int line, int seg, GramRaw& r)
+{
+    const MuonParams& p = g.p;
+    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+    r.g[0] = r.g[1] = r.m[0] = r.m[1] = z;
     if (g.vec) {
-        if (!ok[0]) return;
-        muon_u<8, STEP>(p, e[0], u);
+        const long long e = gram_at(g, blk, ch, line, seg, 0);
+        if (e < 0) return;
+        if (p.grad_dtype == 2) {
+            const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p.grad) + e);
+            r.g[0] = q[0], r.g[1] = q[1];
+        } else {
+            r.g[0] = *reinterpret_cast<const uint4*>(static_cast<const __half*>(p.grad) + e);
+        }
+        if (p.mom) {
+            const uint4* q = reinterpret_cast<const uint4*>(p.mom + e);
+            r.m[0] = q[0], r.m[1] = q[1];
+        }
         return;
     }
+    uint32_t w[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        if (!ok[k]) continue;
-        float x[1];
-        muon_u<1, STEP>(p, e[k], x);
-        u[k] = x[0];
+        const long long e = gram_at(g, blk, ch, line, seg, k);
+        float x[1] = {0.f};
+        if (e >= 0) muon_u<1, STEP>(p, e, x);
+        w[k] = __float_as_uint(x[0]);
+    }
+    r.g[0] = make_uint4(w[0], w[1], w[2], w[3]), r.g[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+template <bool STEP>
+__device__ __forceinline__ void gram_make(const GramParams& g, int blk, int ch, int line, int seg, const GramRaw& r,
+                                          float (&u)[8])
+{
+    const MuonParams& p = g.p;
+    const uint32_t w[8] = {r.g[0].x, r.g[0].y, r.g[0].z, r.g[0].w, r.g[1].x, r.g[1].y, r.g[1].z, r.g[1].w};
+    if (!g.vec || p.grad_dtype == 2) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) u[k] = __uint_as_float(w[k]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 f = p.grad_dtype == 0 ? unpack_bf162(w[k]) : unpack_half2(w[k]);
+            u[2 * k] = f.x, u[2 * k + 1] = f.y;
+        }
+    }
+    if (!g.vec || !p.mom) return;
+    const uint32_t v[8] = {r.m[0].x, r.m[0].y, r.m[0].z, r.m[0].w, r.m[1].x, r.m[1].y, r.m[1].z, r.m[1].w};
+    float m[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m[k] = __uint_as_float(v[k]);
+    muon_make<8, STEP>(p, u, m);
+    if (STEP) {
+        const long long e = gram_at(g, blk, ch, line, seg, 0);
+        if (e >= 0) store_f32<float, 8>(p.mom + e, m);
     }
 }
 
@@ -268,13 +313,13 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
     // Two staged images (pairs), in A's place.  Wide: rows of the block, 64
     // positions along; tall: 64 positions, the block's rows along, in 64-wide atoms.
     const int line = tid >> 3, seg = (tid & 7) * 8;
-    auto stage = [&](uint8_t* img, const float (&u)[P / 64][8]) {
+    auto stage = [&](uint8_t* img, int ch, auto step, const GramRaw (&u)[P / 64]) {
 #pragma unroll
         for (int j = 0; j < P / 64; ++j) {
             float v[8];
+            gram_make<decltype(step)::value>(g, blk, ch, g.wide ? line + 64 * j : line, g.wide ? seg : seg + 64 * j, u[j], v);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                v[k] = u[j][k];
                 if (!(fabsf(v[k]) < INFINITY)) {
                     v[k] = 0.f;
                     bad[(g.wide ? line + 64 * j : seg + 64 * j + k)] = 1;
@@ -287,19 +332,19 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
             *reinterpret_cast<uint4*>(o + IMG) = l;
         }
     };
-    auto load = [&](int ch, auto step, float (&u)[P / 64][8]) {
+    auto load = [&](int ch, auto step, GramRaw (&u)[P / 64]) {
         if (ch >= g.chunks) return;
 #pragma unroll
         for (int j = 0; j < P / 64; ++j)
-            gram_load8<decltype(step)::value>(g, blk, ch, g.wide ? line + 64 * j : line, g.wide ? seg : seg + 64 * j, u[j]);
+            gram_read<decltype(step)::value>(g, blk, ch, g.wide ? line + 64 * j : line, g.wide ? seg : seg + 64 * j, u[j]);
     };
     const int nch = (g.chunks - rank + g.C - 1) / g.C;  // this CTA's chunks: rank, rank + C, ...
     if (!issuer) {
-        float u[P / 64][8];
+        GramRaw u[P / 64];
         load(rank, std::true_type{}, u);
         for (int it = 0; it < nch; ++it) {
             if (it >= 2) wait(it & 1);
-            stage(ba + (it & 1) * 2 * IMG, u);
+            stage(ba + (it & 1) * 2 * IMG, rank + it * g.C, std::true_type{}, u);
             ready();
             load(rank + (it + 1) * g.C, std::true_type{}, u);
         }
@@ -493,7 +538,7 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
         __threadfence();
     }
     // The first chunk of U comes back while Q is on its way.
-    float u[P / 64][8];
+    GramRaw u[P / 64];
     if (!issuer) load(rank, std::false_type{}, u);
     cluster_sync_all();
 
@@ -505,7 +550,7 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
         for (int it = 0; it < nch; ++it) {
             const int ch = rank + it * g.C;
             // (The MMAs that read this image two chunks ago are done: their sums have been read.)
-            stage((it & 1 ? bp : ba), u);
+            stage((it & 1 ? bp : ba), ch, std::false_type{}, u);
             ready();
             load(ch + g.C, std::false_type{}, u);
             wait(it & 1);
