@@ -128,17 +128,54 @@ __device__ __forceinline__ void muon_load8(const void* in, int dtype, long long 
         load_f32<__half, 8>(static_cast<const __half*>(in) + e, v);
 }
 
-// The results of eight elements along a row (every address 16-byte aligned).
-__device__ __forceinline__ void muon_finish8(const MuonParams& p, long long e, const float (&o)[8])
+// Eight elements as they come from memory: the conversion waits for them, the load does not.
+struct MuonRaw8 {
+    uint4 a, b;
+};
+__device__ __forceinline__ MuonRaw8 muon_raw8(const void* in, int dtype, long long e)
+{
+    MuonRaw8 r;
+    r.b = make_uint4(0u, 0u, 0u, 0u);
+    if (dtype == 2) {
+        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(in) + e);
+        r.a = q[0], r.b = q[1];
+    } else {
+        r.a = *reinterpret_cast<const uint4*>(static_cast<const __half*>(in) + e);
+    }
+    return r;
+}
+__device__ __forceinline__ void muon_unraw8(int dtype, const MuonRaw8& r, float (&f)[8])
+{
+    const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+    if (dtype == 2) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(w[k]);
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 x = dtype == 0 ? unpack_bf162(w[k]) : unpack_half2(w[k]);
+        f[2 * k] = x.x, f[2 * k + 1] = x.y;
+    }
+}
+
+// The results of eight elements along a row (every address 16-byte aligned), w the old weights.
+__device__ __forceinline__ void muon_finish8(const MuonParams& p, long long e, const float (&o)[8], const MuonRaw8& old)
 {
     if (p.out) muon_store8(p.out, p.out_dtype, e, o);
     if (p.weight) {
         float w[8];
-        muon_load8(p.weight, p.weight_dtype, e, w);
+        muon_unraw8(p.weight_dtype, old, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[i] = fmaf(p.keep, w[i], -p.lr * o[i]);
         muon_store8(p.weight, p.weight_dtype, e, w);
     }
+}
+__device__ __forceinline__ void muon_finish8(const MuonParams& p, long long e, const float (&o)[8])
+{
+    MuonRaw8 old = {};
+    if (p.weight) old = muon_raw8(p.weight, p.weight_dtype, e);
+    muon_finish8(p, e, o, old);
 }
 
 // Block sum in a fixed order; every thread gets it.

@@ -164,17 +164,20 @@ __device__ __forceinline__ void gram_sums(uint32_t taddr, float (&v)[NC])
     }
 }
 
-__device__ __forceinline__ void st_dsmem_v4(uint32_t addr, float4 v)
+__device__ __forceinline__ float2 ld_dsmem_v2(uint32_t addr)
 {
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z),
-                 "f"(v.w)
-                 : "memory");
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ void st_dsmem_v2(uint32_t addr, float2 v)
+{
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(v.x), "f"(v.y) : "memory");
 }
 
-// Eight values of u as they come from memory: the conversion waits for them, the
-// load does not.  (Not aligned: u itself, as fp32.)
+// What eight values of u are made of.  (Not aligned: u itself, as fp32.)
 struct GramRaw {
-    uint4 g[2], m[2];
+    MuonRaw8 g, m;
 };
 
 // Address of element k of `line`, `seg` .. of chunk `ch` of block `blk` (a line is a
@@ -195,20 +198,12 @@ __device__ __forceinline__ void gram_read(const GramParams& g, int blk, int ch, 
 {
     const MuonParams& p = g.p;
     const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-    r.g[0] = r.g[1] = r.m[0] = r.m[1] = z;
+    r.g.a = r.g.b = r.m.a = r.m.b = z;
     if (g.vec) {
         const long long e = gram_at(g, blk, ch, line, seg, 0);
         if (e < 0) return;
-        if (p.grad_dtype == 2) {
-            const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p.grad) + e);
-            r.g[0] = q[0], r.g[1] = q[1];
-        } else {
-            r.g[0] = *reinterpret_cast<const uint4*>(static_cast<const __half*>(p.grad) + e);
-        }
-        if (p.mom) {
-            const uint4* q = reinterpret_cast<const uint4*>(p.mom + e);
-            r.m[0] = q[0], r.m[1] = q[1];
-        }
+        r.g = muon_raw8(p.grad, p.grad_dtype, e);
+        if (p.mom) r.m = muon_raw8(p.mom, 2, e);
         return;
     }
     uint32_t w[8];
@@ -219,7 +214,7 @@ __device__ __forceinline__ void gram_read(const GramParams& g, int blk, int ch, 
         if (e >= 0) muon_u<1, STEP>(p, e, x);
         w[k] = __float_as_uint(x[0]);
     }
-    r.g[0] = make_uint4(w[0], w[1], w[2], w[3]), r.g[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    r.g.a = make_uint4(w[0], w[1], w[2], w[3]), r.g.b = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
 template <bool STEP>
@@ -227,22 +222,10 @@ __device__ __forceinline__ void gram_make(const GramParams& g, int blk, int ch, 
                                           float (&u)[8])
 {
     const MuonParams& p = g.p;
-    const uint32_t w[8] = {r.g[0].x, r.g[0].y, r.g[0].z, r.g[0].w, r.g[1].x, r.g[1].y, r.g[1].z, r.g[1].w};
-    if (!g.vec || p.grad_dtype == 2) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) u[k] = __uint_as_float(w[k]);
-    } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float2 f = p.grad_dtype == 0 ? unpack_bf162(w[k]) : unpack_half2(w[k]);
-            u[2 * k] = f.x, u[2 * k + 1] = f.y;
-        }
-    }
+    muon_unraw8(g.vec ? p.grad_dtype : 2, r.g, u);
     if (!g.vec || !p.mom) return;
-    const uint32_t v[8] = {r.m[0].x, r.m[0].y, r.m[0].z, r.m[0].w, r.m[1].x, r.m[1].y, r.m[1].z, r.m[1].w};
     float m[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) m[k] = __uint_as_float(v[k]);
+    muon_unraw8(2, r.m, m);
     muon_make<8, STEP>(p, u, m);
     if (STEP) {
         const long long e = gram_at(g, blk, ch, line, seg, 0);
@@ -340,13 +323,19 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
     };
     const int nch = (g.chunks - rank + g.C - 1) / g.C;  // this CTA's chunks: rank, rank + C, ...
     if (!issuer) {
-        GramRaw u[P / 64];
-        load(rank, std::true_type{}, u);
-        for (int it = 0; it < nch; ++it) {
+        // Two chunks ahead of the one that is staged.
+        GramRaw u0[P / 64], u1[P / 64];
+        load(rank, std::true_type{}, u0);
+        load(rank + g.C, std::true_type{}, u1);
+        auto chunk = [&](int it, GramRaw (&u)[P / 64]) {
             if (it >= 2) wait(it & 1);
             stage(ba + (it & 1) * 2 * IMG, rank + it * g.C, std::true_type{}, u);
+            load(rank + (it + 2) * g.C, std::true_type{}, u);
             ready();
-            load(rank + (it + 1) * g.C, std::true_type{}, u);
+        };
+        for (int it = 0; it < nch; it += 2) {
+            chunk(it, u0);
+            if (it + 1 < nch) chunk(it + 1, u1);
         }
         if (nch >= 2) wait(nch & 1);
         if (nch >= 1) wait((nch - 1) & 1);
@@ -394,17 +383,22 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
     cluster_sync_all();
     if (!issuer) {
         // Rows rank * P / C .. of the sum over the cluster, into rank 0's Q.
-        const int chunks16 = P * P / 4 / g.C;  // 16-byte chunks of a slice
+        const int pieces = P * P / 2 / g.C;  // 8-byte pieces of a slice
         const uint32_t src = smem_u32(bp), dst = mapa_shared(smem_u32(bq), 0u);
-        for (int i = tid; i < chunks16; i += kGramThreads) {
-            const uint32_t o = (uint32_t)(rank * chunks16 + i) << 4;
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-            for (int c = 0; c < g.C; ++c) {
-                const float4 x = ld_dsmem_v4(mapa_shared(src + o, (uint32_t)c));
-                s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+        for (int i = tid; i < pieces; i += kGramThreads) {
+            const uint32_t o = (uint32_t)(rank * pieces + i) << 3;
+            float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int c0 = 0; c0 < 16; c0 += 8) {
+                if (c0 >= g.C) break;
+                float2 x[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) x[c] = ld_dsmem_v2(mapa_shared(src + o, (uint32_t)min(c0 + c, g.C - 1)));
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    if (c0 + c < g.C) s.x += x[c].x, s.y += x[c].y;
             }
-            st_dsmem_v4(dst + o, s);
+            st_dsmem_v2(dst + o, s);
         }
     }
     cluster_sync_all();
@@ -414,6 +408,7 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
     if (rank == 0 && issuer) {
         const uint32_t sba = smem_u32(ba), sbp = smem_u32(bp), sbq = smem_u32(bq);
         __syncthreads();  // the diagonal
+        __syncthreads();  // and its sums
         for (int k = 0; k < g.steps; ++k) {
             const bool last = k == g.steps - 1;
             __syncthreads();
@@ -459,10 +454,17 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
                 if (c0 + i == row) diag[row] = v[i];
         }
         __syncthreads();
-        if (act) {
-            // |u|_F^2 is the trace; A_0 = U U^T / (|u|_F + eps)^2, zero between matrices.
+        for (int f = warp; f < g.F; f += kGramThreads / 32) {  // |u|_F^2 is the trace: a warp per matrix
             float s = 0.f;
-            for (int i = lo; i < hi; ++i) s += diag[i];
+            for (int i = lane; i < p.m; i += 32) s += diag[f * p.m + i];
+#pragma unroll
+            for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            if (lane == 0) fac[f] = s;
+        }
+        __syncthreads();
+        if (act) {
+            // A_0 = U U^T / (|u|_F + eps)^2, zero between matrices.
+            const float s = mine < g.F ? fac[mine] : 0.f;
             const float d = sqrtf(s) + p.eps;
             const bool fin = s < INFINITY;
             const float inv = fin && d > 0.f ? 1.f / d : 0.f;
@@ -525,17 +527,27 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
             }
         }
         if (act) {
-            // Q (v) as a pair of bf16 operand images, for every CTA of the cluster.
+            // Q (v) as a pair of bf16 operand images, for every CTA of the cluster: through
+            // shared memory, so that it goes out in whole lines (row by row from the lanes it
+            // took 3 us).
 #pragma unroll
             for (int i = 0; i < NC; i += 8) {
                 uint4 h, l;
                 split8<true>(v + i, &h, &l);
-                uint8_t* o = qimg + gram_off<P>(row, (c0 + i) >> 3);
+                uint8_t* o = bq + gram_off<P>(row, (c0 + i) >> 3);
                 *reinterpret_cast<uint4*>(o) = h;
                 *reinterpret_cast<uint4*>(o + MAT) = l;
             }
         }
-        __threadfence();
+        if (g.C > 1) {
+            named_bar_sync(1, kGramThreads);
+#pragma unroll
+            for (int i = 0; i < PAIR / 16 / kGramThreads; ++i) {
+                const int e = i * kGramThreads + tid;
+                __stcg(reinterpret_cast<uint4*>(qimg) + e, reinterpret_cast<const uint4*>(bq)[e]);
+            }
+            __threadfence();
+        }
     }
     // The first chunk of U comes back while Q is on its way.
     GramRaw u[P / 64];
@@ -544,23 +556,43 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
 
     // ---------------------------------------------------- results: X = Q U over this CTA's chunks
     if (!issuer) {
-        for (int i = tid; i < PAIR / 16; i += kGramThreads)
-            reinterpret_cast<uint4*>(bq)[i] = __ldcg(reinterpret_cast<const uint4*>(qimg) + i);
+        if (rank != 0) {
+            uint4 x[PAIR / 16 / kGramThreads];
+#pragma unroll
+            for (int i = 0; i < PAIR / 16 / kGramThreads; ++i)
+                x[i] = __ldcg(reinterpret_cast<const uint4*>(qimg) + i * kGramThreads + tid);
+#pragma unroll
+            for (int i = 0; i < PAIR / 16 / kGramThreads; ++i) reinterpret_cast<uint4*>(bq)[i * kGramThreads + tid] = x[i];
+        }
         if (tid < P) fac[tid] = __ldcg(g.factor + blk * 128 + tid);
-        for (int it = 0; it < nch; ++it) {
+        const int q0 = (warp >> 2) * 16;
+        // A chunk is staged and its MMAs begin before the results of the one before it are written.
+        auto begin = [&](int it) {
+            if (it >= nch) return;
             const int ch = rank + it * g.C;
             // (The MMAs that read this image two chunks ago are done: their sums have been read.)
             stage((it & 1 ? bp : ba), ch, std::false_type{}, u);
-            ready();
             load(ch + g.C, std::false_type{}, u);
+            ready();
+        };
+        begin(0);
+        for (int it = 0; it < nch; ++it) {
+            const int ch = rank + it * g.C;
+            const int b0 = blk * g.F + mine;
+            const bool mat = act && mine < g.F && b0 < p.batch;
+            MuonRaw8 old[2] = {};
+            if (g.wide && g.ovec && p.weight && mat) {
+                const long long e = (long long)b0 * p.bs + (row - lo) * p.ld + ch * 64 + q0;
+                if (ch * 64 + q0 < g.N) old[0] = muon_raw8(p.weight, p.weight_dtype, e);
+                if (ch * 64 + q0 + 8 < g.N) old[1] = muon_raw8(p.weight, p.weight_dtype, e + 8);
+            }
+            begin(it + 1);
             wait(it & 1);
             float x[16];
-            const int q0 = (warp >> 2) * 16;
             if (act) gram_ld<16>(tb + ((uint32_t)((warp & 3) * 32) << 16) + (it & 1 ? T2 : TA) + (uint32_t)q0, x);
-            const int b = blk * g.F + mine;
-            if (act && mine < g.F && b < p.batch) {
+            if (mat) {
                 const float f = fac[row];
-                const long long base = (long long)b * p.bs;
+                const long long base = (long long)b0 * p.bs;
                 const int n0 = ch * 64 + q0;
                 if (g.wide && g.ovec) {
 #pragma unroll
@@ -568,14 +600,23 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
                         float o[8];
 #pragma unroll
                         for (int k = 0; k < 8; ++k) o[k] = f * x[i + k];
-                        if (n0 + i < g.N) muon_finish8(p, base + (row - lo) * p.ld + n0 + i, o);
+                        if (n0 + i < g.N) muon_finish8(p, base + (row - lo) * p.ld + n0 + i, o, old[i / 8]);
                     }
                 } else {
+                    const long long e0 = base + (g.wide ? (row - lo) * p.ld + n0 : n0 * p.ld + (row - lo));
+                    const long long step = g.wide ? 1 : p.ld;
+                    const int n = min(16, g.N - n0);
+                    float w[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        w[i] = p.weight && i < n ? muon_load(p.weight, p.weight_dtype, e0 + i * step) : 0.f;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const int n = n0 + i;
-                        if (n < g.N)
-                            muon_finish(p, base + (g.wide ? (row - lo) * p.ld + n : n * p.ld + (row - lo)), f * x[i]);
+                        if (i >= n) break;
+                        const float o = f * x[i];
+                        if (p.out) muon_store(p.out, p.out_dtype, e0 + i * step, o);
+                        if (p.weight)
+                            muon_store(p.weight, p.weight_dtype, e0 + i * step, fmaf(p.keep, w[i], -p.lr * o));
                     }
                 }
             }
