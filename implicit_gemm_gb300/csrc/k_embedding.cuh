@@ -3,7 +3,7 @@
 //   lookup:    out[t, :]    = scale * table[token[t], :]
 //   gradient:  dtable[v, :] = scale * sum over the t with token[t] = v of dy[t, :]
 //
-// The gradient runs in three kernels, without atomics on data:
+// The gradient runs in two kernels, without atomics on data:
 //
 //  emb_sort_kernel    a stable counting sort of the positions by token.  Every CTA
 //                     owns a range of table rows and reads all tokens (a broadcast
@@ -13,14 +13,14 @@
 //                     below its range are its place in the list, so CTAs need
 //                     nothing from each other.  It also writes the zeros of the
 //                     rows that no token names.
-//  emb_reduce_kernel  a segmented sum over the sorted list: a warp takes 32 entries
-//                     (a window) by 256 columns.  A run of at most 64 entries is
+//  emb_reduce_kernel  a segmented sum over the sorted list: a warp takes W entries
+//                     (a window) by 256 columns.  A run of at most 2 W entries is
 //                     summed by the warp of the window it starts in, to its end;
-//                     a longer one leaves an fp32 partial row per window.  So no
-//                     warp has more than 95 entries, however often a token occurs.
-//  emb_join_kernel    adds the partial rows of the long runs, in the windows' order.
-//
-// Windows are fixed places of the sorted list, so every sum has one order.
+//                     a longer one leaves an fp32 partial row per window, and the
+//                     partial rows of 16 windows, then of 16 such groups and so on,
+//                     are added in order by whichever warp brings the last of them.
+//                     So no warp has more than 3 W entries, however often a token
+//                     occurs, and the order of every sum is fixed.
 #pragma once
 
 #include "ptx.cuh"
@@ -39,14 +39,19 @@ struct EmbParams {
     const void* in;  // table (lookup) or dy (gradient)
     void* out;       // out (lookup) or dtable (gradient)
     int accumulate;
-    int R;        // table rows of a CTA of emb_sort_kernel
-    int* meta;    // [0] entries of the list, [1] long runs that cross windows
-    int* count;   // [V] occurrences of a row's token
-    int* list;    // [T] positions, by (row, position)
-    int* row;     // [T] their rows
-    int4* cross;  // (row, first entry, entries, 0) of the long runs that cross windows
-    float* part;  // [windows][2][D] partial rows: of a run from before the window, of a run that goes on after it
-    int token16;  // token is 16-byte aligned
+    int R;          // table rows of a CTA of emb_sort_kernel
+    int keep;       // matches that a warp of it keeps from the count
+    int W;          // entries of a window: 8, 16 or 32
+    int tiles;      // 256-column tiles of a row
+    int level[8];   // first partial row of a level: windows, groups of 16 of them, ...
+    int narrived;   // counters
+    int* meta;      // [0] entries of the list
+    int* count;     // [V] occurrences of a row's token
+    int* start;     // [V] first entry of its run
+    int* list;      // [T] positions, by (row, position)
+    int* row;       // [T] their rows
+    float* part;    // [level rows][2][D] partial rows: of a run from before the child, of a run that starts in it
+    int* arrived;   // [level rows][2][tiles] partial rows of a run that are there, counted at its first child of a group
 };
 
 // The token at position t as a table row, or -1 when it is out of range.
@@ -82,24 +87,10 @@ __global__ void __launch_bounds__(256) emb_lookup_kernel(const __grid_constant__
 }
 
 constexpr int kEmbSortThreads = 1024, kEmbSortWarps = kEmbSortThreads / 32;
-constexpr int kEmbSortKept = 64;       // positions of its rows that a warp keeps from the count
-constexpr int kEmbSortMaxRows = 1536;  // 32 counters of 4 bytes a row: 192 KB of shared memory
-constexpr int kEmbWindow = 32, kEmbTile = 256, kEmbShort = 64;
-
-// The tokens at positions t .. t + 3 as table rows; -1: out of range, -2: past the last position.
-__device__ __forceinline__ void emb_tokens4(const EmbParams& p, long long t, int (&v)[4])
-{
-    if (!p.token64 && p.token16 && t + 4 <= p.T) {
-        const int4 x = *reinterpret_cast<const int4*>(static_cast<const int*>(p.token) + t);
-        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if ((unsigned)v[j] >= (unsigned)p.V) v[j] = -1;
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = t + j < p.T ? emb_token(p, t + j) : -2;
-}
+constexpr int kEmbSortMaxRows = 1472;     // 32 counters of 4 bytes a row: 184 KB of shared memory
+constexpr int kEmbSortRowBits = 11;       // a row of the range in a kept match
+constexpr int kEmbSortMaxSmem = 220 << 10;  // counters and kept matches
+constexpr int kEmbTile = 256, kEmbFan = 16;
 
 // n elements of zero from any element-aligned address, by one warp.
 template <typename T>
@@ -140,9 +131,10 @@ __device__ __forceinline__ int block_exclusive_1024(int v, int* total)
 template <typename TG>
 __global__ void __launch_bounds__(kEmbSortThreads, 1) emb_sort_kernel(const __grid_constant__ EmbParams p)
 {
-    extern __shared__ int hist[];  // [warps][R]: counts, then each warp's next entry of a row
+    // [warps][R]: counts, then each warp's next entry of a row; [warps][keep]: matches
+    // (position in the warp's range, row of the CTA's range).
+    extern __shared__ int hist[];
     __shared__ int first[kEmbSortMaxRows];
-    __shared__ int kept_t[kEmbSortWarps][kEmbSortKept], kept_r[kEmbSortWarps][kEmbSortKept];
     const int R = p.R, lo = blockIdx.x * R, nr = min(R, p.V - lo);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_launch_dependents();
@@ -150,55 +142,52 @@ __global__ void __launch_bounds__(kEmbSortThreads, 1) emb_sort_kernel(const __gr
     __syncthreads();
     pdl_wait();
     int* mine = hist + warp * R;
-    // Each warp's positions: a multiple of 128, four consecutive ones per lane and
-    // load.  Sixteen positions per lane are in flight at a time (one at a time the
-    // loads' latency alone took 30 us for 65,536 tokens).
-    constexpr int kAhead = 4;
-    const long long per = ((p.T + kEmbSortThreads * 4 - 1) / (kEmbSortThreads * 4)) * 128;
-    const long long t0 = warp * per, t1 = min(p.T, t0 + per);
+    for (int i = blockIdx.x * kEmbSortThreads + threadIdx.x; i < p.narrived; i += gridDim.x * kEmbSortThreads)
+        p.arrived[i] = 0;
+    // Each warp's positions: a multiple of 32.  Eight loads per lane are in flight at
+    // a time (one at a time their latency alone took 30 us for 65,536 tokens).
+    constexpr int kAhead = 8;
+    const long long per = (p.T + 32 * kEmbSortWarps - 1) / (32 * kEmbSortWarps) * 32;
+    const long long t0 = min(p.T, warp * per), t1 = min(p.T, t0 + per);
+    unsigned* keep = reinterpret_cast<unsigned*>(hist + kEmbSortWarps * R) + warp * p.keep;
+    const int cap = per < (1LL << (32 - kEmbSortRowBits)) ? p.keep : 0;
     int below = 0, kept = 0;
     bool bad = false;
-    for (long long t = t0; t < t1; t += 128 * kAhead) {
-        int v[kAhead][4];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const long long u = t + 128 * k + 4 * lane;
-            if (u < t1)
-                emb_tokens4(p, u, v[k]);
-            else
-                v[k][0] = v[k][1] = v[k][2] = v[k][3] = -2;
+    auto take = [&](int at, unsigned r, bool in) {  // 32 positions from t0 + at
+        const unsigned who = __ballot_sync(0xffffffffu, in);
+        if (!who) return;
+        if (in) {
+            const int k = kept + __popc(who & ((1u << lane) - 1u));
+            atomicAdd(&mine[r], 1);
+            if (k < cap) keep[k] = (unsigned)(at + lane) << kEmbSortRowBits | r;
         }
+        kept += __popc(who);
+    };
+    long long t = t0;
+    if (!p.token64 && p.padding < 0) {
+        const int* tok = static_cast<const int*>(p.token) + lane;
+        for (; t + 32 * kAhead <= t1; t += 32 * kAhead) {
+            int v[kAhead];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            unsigned in = 0;
+            for (int k = 0; k < kAhead; ++k) v[k] = tok[t + 32 * k];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                bad |= v[k][j] == -1;
-                const bool ok = v[k][j] >= 0 && v[k][j] != p.padding;
-                below += ok && v[k][j] < lo;
-                if (ok && (unsigned)(v[k][j] - lo) < (unsigned)nr) in |= 1u << j;
+            for (int k = 0; k < kAhead; ++k) {
+                // (A token out of range is a large unsigned number: neither below nor in the range.)
+                const unsigned r = (unsigned)v[k] - (unsigned)lo;
+                if ((unsigned)v[k] < (unsigned)lo) ++below;
+                take((int)(t - t0) + 32 * k, r, r < (unsigned)nr);
             }
-            if (!__any_sync(0xffffffffu, in)) continue;
-            // Keep the matches in the order of their positions: lane by lane, four in each.
-            const int n = __popc(in);
-            int at = n;
+            if (blockIdx.x == 0)
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, at, o);
-                if (lane >= o) at += y;
-            }
-            const int all = __shfl_sync(0xffffffffu, at, 31);
-            at += kept - n;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (in >> j & 1u) {
-                    const int r = v[k][j] - lo;
-                    atomicAdd(&mine[r], 1);
-                    if (at < kEmbSortKept) kept_t[warp][at] = (int)(t + 128 * k + 4 * lane + j), kept_r[warp][at] = r;
-                    ++at;
-                }
-            kept += all;
+                for (int k = 0; k < kAhead; ++k) bad |= (unsigned)v[k] >= (unsigned)p.V;
         }
+    }
+    for (; t < t1; t += 32) {
+        const int v = t + lane < t1 ? emb_token(p, t + lane) : -2;
+        const unsigned r = (unsigned)v - (unsigned)lo;
+        bad |= v == -1;
+        if ((unsigned)v < (unsigned)lo && v != p.padding) ++below;
+        take((int)(t - t0), r, r < (unsigned)nr && v != p.padding);
     }
     if (blockIdx.x == 0 && bad) atomicOr(&g_status, kStatusBadToken);
     int base, total;
@@ -222,6 +211,7 @@ __global__ void __launch_bounds__(kEmbSortThreads, 1) emb_sort_kernel(const __gr
         const int r = threadIdx.x + k * kEmbSortThreads;
         if (r < nr) {
             p.count[lo + r] = n[k];
+            p.start[lo + r] = at[k];
             first[r] = n[k];
             int o = at[k];
             if (n[k])
@@ -233,7 +223,7 @@ __global__ void __launch_bounds__(kEmbSortThreads, 1) emb_sort_kernel(const __gr
                 }
         }
     }
-    if (threadIdx.x == 0 && blockIdx.x == gridDim.x - 1) p.meta[0] = base + total, p.meta[1] = 0;
+    if (threadIdx.x == 0 && blockIdx.x == gridDim.x - 1) p.meta[0] = base + total;
     __syncthreads();
     // The matches in order; equal rows of 32 of them take consecutive entries.
     auto place = [&](bool in, long long t, int r) {
@@ -249,12 +239,13 @@ __global__ void __launch_bounds__(kEmbSortThreads, 1) emb_sort_kernel(const __gr
         }
         __syncwarp();
     };
-    if (kept <= kEmbSortKept) {
+    if (kept <= cap) {
         for (int i = 0; i < kept; i += 32) {
             const bool in = i + lane < kept;
-            place(in, in ? kept_t[warp][i + lane] : 0, in ? kept_r[warp][i + lane] : 0);
+            const unsigned m = in ? keep[i + lane] : 0u;
+            place(in, t0 + (m >> kEmbSortRowBits), (int)(m & ((1u << kEmbSortRowBits) - 1u)));
         }
-    } else {  // more than were kept (a frequent token, or a small table): the positions again
+    } else {  // more than were kept (many tokens for a small table): the positions again
         for (long long t = t0; t < t1; t += 128) {
             int v[4];
 #pragma unroll
@@ -295,122 +286,129 @@ __device__ __forceinline__ void emb_write(const EmbParams& p, int v, int c0, con
     }
 }
 
+// The partial row (one tile of it, in s) of a run that begins at entry `start` and
+// has n entries, from window w: kept, and added to its neighbours' by the warp that
+// finds all of a group there.
+template <typename TG, int VEC>
+__device__ __forceinline__ void emb_join(const EmbParams& p, int v, int w, int tile, float (&s)[8])
+{
+    constexpr int NV = 8 / VEC;
+    const int lane = threadIdx.x & 31, c0 = tile * kEmbTile + lane * VEC;
+    const int start = p.start[v];
+    int a = start / p.W, b = (start + p.count[v] - 1) / p.W, child = w;
+    for (int l = 0;; ++l) {
+        const long long base = p.level[l];
+        float* q = p.part + ((base + child) * 2 + (child == a ? 1 : 0)) * p.D;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = c0 + j * 32 * VEC;
+            float g[VEC];
+#pragma unroll
+            for (int x = 0; x < VEC; ++x) g[x] = s[j * VEC + x];
+            if (c < p.D) store_f32<float, VEC>(q + c, g);
+        }
+        __threadfence();
+        __syncwarp();
+        const int group = child / kEmbFan;
+        const int first = max(a, group * kEmbFan), last = min(b, group * kEmbFan + kEmbFan - 1);
+        int seen = 0;
+        if (lane == 0) seen = atomicAdd(&p.arrived[((base + first) * 2 + (first == a ? 1 : 0)) * p.tiles + tile], 1);
+        if (__shfl_sync(0xffffffffu, seen, 0) != last - first) return;
+        __threadfence();
+#pragma unroll
+        for (int x = 0; x < 8; ++x) s[x] = 0.f;
+        for (int h = first; h <= last; h += 8) {
+            float f[8][8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int c = min(h + k, last);
+                const float* in = p.part + ((base + c) * 2 + (c == a ? 1 : 0)) * p.D;
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+#pragma unroll
+                    for (int x = 0; x < VEC; ++x) f[k][j * VEC + x] = __ldcg(in + min(c0 + j * 32 * VEC + x, p.D - 1));
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (h + k <= last)
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) s[x] += f[k][x];
+        }
+        if (a / kEmbFan == b / kEmbFan) {
+            emb_write<TG, VEC>(p, v, c0, s);
+            return;
+        }
+        a /= kEmbFan, b /= kEmbFan, child = group;
+    }
+}
+
 template <typename TG, typename TY, int VEC>
-__global__ void __launch_bounds__(256) emb_reduce_kernel(const __grid_constant__ EmbParams p, int tiles)
+__global__ void __launch_bounds__(256, 2) emb_reduce_kernel(const __grid_constant__ EmbParams p)
 {
     constexpr int NV = 8 / VEC, AHEAD = 8;
     pdl_launch_dependents();
-    const int lane = threadIdx.x & 31;
-    const long long item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int w = (int)(item / tiles), tile = (int)(item - (long long)w * tiles);
+    const int lane = threadIdx.x & 31, W = p.W;
+    const long long item = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const int w = (int)(item / p.tiles), tile = (int)(item - (long long)w * p.tiles);
     pdl_wait();
-    const int n = p.meta[0], e0 = w * kEmbWindow;
+    const int n = p.meta[0], e0 = w * W;
     if (e0 >= n) return;
-    const int m = min(kEmbWindow, n - e0);
-    // The window's rows, where runs end in it, and the runs that cross its borders.
+    const int m = min(W, n - e0);
+    // The window's rows, and the runs that cross its borders.
     const int wrow = p.row[min(e0 + lane, e0 + m - 1)];
     const int prev = e0 > 0 ? p.row[e0 - 1] : -1, next = e0 + m < n ? p.row[e0 + m] : -1;
     const int head = __shfl_sync(0xffffffffu, wrow, 0), tail = __shfl_sync(0xffffffffu, wrow, m - 1);
-    const int ncut = head == prev ? p.count[head] : 0, ntail = tail == next ? p.count[tail] : 0;
-    const bool entered = ncut > kEmbShort, leaves = ntail > kEmbShort;  // long runs that cross
+    const int nhead = head == prev ? p.count[head] : 0, ntail = tail == next ? p.count[tail] : 0;
+    const bool entered = nhead > 2 * W, leaves = ntail > 2 * W;  // long runs that cross
     int b = e0, e = e0 + m;
-    if (ncut && !entered) b += __popc(__ballot_sync(0xffffffffu, lane < m && wrow == head));  // an earlier window's run
-    int tail0 = 0;  // first entry in the window of the run that goes on after it
-    if (ntail) tail0 = e0 + m - __popc(__ballot_sync(0xffffffffu, lane < m && wrow == tail));
-    if (ntail && !leaves && b < e) e = tail0 + ntail;  // this window's run, to its end
+    if (nhead && !entered) b += __popc(__ballot_sync(0xffffffffu, lane < m && wrow == head));  // an earlier window's run
+    if (ntail && !leaves && b < e)  // this window's run, to its end
+        e = e0 + m - __popc(__ballot_sync(0xffffffffu, lane < m && wrow == tail)) + ntail;
     const int c0 = tile * kEmbTile + lane * VEC;
     int col[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) col[j] = min(c0 + j * 32 * VEC, p.D - VEC);  // columns past the row read its last ones
     const TY* dy = static_cast<const TY*>(p.in);
-    float s[8] = {};
-    bool from_before = entered;
-    for (int base = b; base < e; base += 32) {
-        const int k = min(32, e - base);
-        const int pos = p.list[min(base + lane, e - 1)], row = p.row[min(base + lane, e - 1)];
-        const int after = base + lane + 1 < e ? p.row[base + lane + 1] : -1;
-        const unsigned ends = __ballot_sync(0xffffffffu, after != row);
-        for (int i0 = 0; i0 < k; i0 += AHEAD) {
-            // Eight rows in flight; entries past the last read its row again.
-            Vec<TY, VEC> f[AHEAD][NV];
+    // Three stretches of the list: the end of a long run (a partial row), whole runs,
+    // the beginning of a long run (a partial row).
+    const int nin = entered ? __popc(__ballot_sync(0xffffffffu, lane < m && wrow == head)) : 0;
+    const int nout = leaves && !(entered && nin == m) ? __popc(__ballot_sync(0xffffffffu, lane < m && wrow == tail)) : 0;
+#pragma unroll 1
+    for (int part = 0; part < 3; ++part) {
+        const int sb = part == 0 ? b : part == 1 ? b + nin : e - nout;
+        const int se = part == 0 ? b + nin : part == 1 ? e - nout : e;
+        float s[8] = {};
+        for (int base = sb; base < se; base += 32) {
+            const int k = min(32, se - base);
+            const int pos = p.list[min(base + lane, se - 1)], row = p.row[min(base + lane, se - 1)];
+            const int after = base + lane + 1 < se ? p.row[base + lane + 1] : -1;
+            const unsigned ends = part == 1 ? __ballot_sync(0xffffffffu, after != row) : 0u;
+            for (int i0 = 0; i0 < k; i0 += AHEAD) {
+                // Eight rows in flight; entries past the last read its row again.
+                Vec<TY, VEC> f[AHEAD][NV];
 #pragma unroll
-            for (int a = 0; a < AHEAD; ++a) {
-                const long long t = __shfl_sync(0xffffffffu, pos, i0 + a);
+                for (int a = 0; a < AHEAD; ++a) {
+                    const long long t = __shfl_sync(0xffffffffu, pos, i0 + a);
 #pragma unroll
-                for (int j = 0; j < NV; ++j)
-                    f[a][j] = *reinterpret_cast<const Vec<TY, VEC>*>(dy + t * p.ld_out + col[j]);
-            }
-#pragma unroll
-            for (int a = 0; a < AHEAD; ++a) {
-                const int i = i0 + a;
-                if (i >= k) break;
-#pragma unroll
-                for (int j = 0; j < NV; ++j)
-#pragma unroll
-                    for (int q = 0; q < VEC; ++q) s[j * VEC + q] += to_f32<TY>(f[a][j].v[q]);
-                if (!(ends >> i & 1u)) continue;
-                const int v = __shfl_sync(0xffffffffu, row, i);
-                const bool on = leaves && base + i == e - 1;
-                if (!from_before && !on) {
-                    emb_write<TG, VEC>(p, v, c0, s);
-                } else {
-                    float* q = p.part + ((long long)w * 2 + (from_before ? 0 : 1)) * p.D;
-#pragma unroll
-                    for (int j = 0; j < NV; ++j) {
-                        const int c = c0 + j * 32 * VEC;
-                        float g[VEC];
-#pragma unroll
-                        for (int x = 0; x < VEC; ++x) g[x] = s[j * VEC + x];
-                        if (c < p.D) store_f32<float, VEC>(q + c, g);
-                    }
-                    if (!from_before && tile == 0 && lane == 0)
-                        p.cross[atomicAdd(&p.meta[1], 1)] = make_int4(v, tail0, ntail, 0);
+                    for (int j = 0; j < NV; ++j)
+                        f[a][j] = *reinterpret_cast<const Vec<TY, VEC>*>(dy + t * p.ld_out + col[j]);
                 }
 #pragma unroll
-                for (int x = 0; x < 8; ++x) s[x] = 0.f;
-                from_before = false;
+                for (int a = 0; a < AHEAD; ++a) {
+                    const int i = i0 + a;
+                    if (i >= k) break;
+#pragma unroll
+                    for (int j = 0; j < NV; ++j)
+#pragma unroll
+                        for (int q = 0; q < VEC; ++q) s[j * VEC + q] += to_f32<TY>(f[a][j].v[q]);
+                    if (!(ends >> i & 1u)) continue;
+                    emb_write<TG, VEC>(p, __shfl_sync(0xffffffffu, row, i), c0, s);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) s[x] = 0.f;
+                }
             }
         }
-    }
-}
-
-// The partial rows of a long run, in the windows' order: eight warps a contiguous
-// range each, then the eight sums.
-template <typename TG, int VEC>
-__global__ void __launch_bounds__(256) emb_join_kernel(const __grid_constant__ EmbParams p, int tiles)
-{
-    __shared__ float sums[8][kEmbTile];
-    pdl_launch_dependents();
-    pdl_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int runs = p.meta[1];
-    for (long long item = blockIdx.x; item < (long long)runs * tiles; item += gridDim.x) {
-        const int4 run = p.cross[item / tiles];
-        const int tile = (int)(item % tiles), c0 = tile * kEmbTile + lane;
-        const int a = run.y / kEmbWindow, b = (run.y + run.z - 1) / kEmbWindow;
-        const int per = (b - a + 1 + 7) / 8;
-        const int w0 = a + warp * per, w1 = min(b + 1, w0 + per);
-        float s[8] = {};
-#pragma unroll 4
-        for (int w = w0; w < w1; ++w) {
-            const float* q = p.part + ((long long)w * 2 + (w == a ? 1 : 0)) * p.D;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) s[k] += q[min(c0 + 32 * k, p.D - 1)];
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) sums[warp][lane + 32 * k] = s[k];
-        __syncthreads();
-        if (warp == 0) {
-            const int l = lane * VEC;
-            float t[8] = {};
-            for (int w = 0; w < 8; ++w)
-#pragma unroll
-                for (int j = 0; j < 8 / VEC; ++j)
-#pragma unroll
-                    for (int k = 0; k < VEC; ++k) t[j * VEC + k] += sums[w][l + j * 32 * VEC + k];
-            emb_write<TG, VEC>(p, run.x, tile * kEmbTile + l, t);
-        }
-        __syncthreads();
+        if (part != 1 && sb < se) emb_join<TG, VEC>(p, part == 0 ? head : tail, w, tile, s);
     }
 }
 

@@ -451,8 +451,11 @@ int muon_run(const MuonPlan& pl, const void* grad, void* momentum, void* weight,
 struct EmbPlan {
     wg_embedding_problem p;
     int R;              // table rows of a CTA of the sort
+    int W, tiles;       // entries of a window, column tiles
     long long windows;  // windows of the sorted list
-    size_t off_meta, off_count, off_list, off_row, off_cross, off_part, bytes;
+    int level[8];       // first partial row of each level of the tree of long runs
+    long long nodes;    // partial rows of all levels
+    size_t off_meta, off_count, off_start, off_list, off_row, off_part, off_arrived, bytes;
 };
 
 int emb_plan(const wg_embedding_problem* p, EmbPlan* pl)
@@ -475,16 +478,31 @@ int emb_plan(const wg_embedding_problem* p, EmbPlan* pl)
         return set_err(WG_ERR_INVALID_ARGUMENT, "ld_table and ld_out must be 0 or at least dim");
     // One CTA of the sort per SM, unless its counters would not fit.
     pl->R = std::min((q.vocab + num_sms() - 1) / num_sms(), wg::kEmbSortMaxRows);
-    pl->windows = (q.tokens + wg::kEmbWindow - 1) / wg::kEmbWindow;
-    if (pl->windows * ((q.dim + wg::kEmbTile - 1) / wg::kEmbTile) > 8LL * 0x7fffffff)
+    // Windows of 32 entries, or of 16 or 8 while those make fewer than 16 warps per SM.
+    pl->tiles = (q.dim + wg::kEmbTile - 1) / wg::kEmbTile;
+    for (pl->W = 32; pl->W > 8 && q.tokens / pl->W * pl->tiles < 16LL * num_sms();) pl->W /= 2;
+    pl->windows = (q.tokens + pl->W - 1) / pl->W;
+    if (pl->windows * pl->tiles > 0x7fffffffLL)
+        return set_err(WG_ERR_NOT_SUPPORTED, "more tokens by columns than one launch covers");
+    pl->nodes = 0;
+    memset(pl->level, 0, sizeof pl->level);
+    long long n = pl->windows;
+    for (int l = 0; l < 8; ++l) {
+        pl->level[l] = (int)pl->nodes;
+        pl->nodes += n;
+        if (n <= 1) break;
+        n = (n + wg::kEmbFan - 1) / wg::kEmbFan;
+    }
+    if (pl->nodes * 2 * pl->tiles > 0x7fffffffLL)
         return set_err(WG_ERR_NOT_SUPPORTED, "more tokens by columns than one launch covers");
     size_t o = 0;
     pl->off_meta = o, o += 256;
     pl->off_count = o, o += up256((size_t)q.vocab * 4);
+    pl->off_start = o, o += up256((size_t)q.vocab * 4);
     pl->off_list = o, o += up256((size_t)q.tokens * 4);
     pl->off_row = o, o += up256((size_t)q.tokens * 4);
-    pl->off_cross = o, o += up256((size_t)pl->windows * 16);
-    pl->off_part = o, o += up256((size_t)pl->windows * 2 * q.dim * 4);
+    pl->off_part = o, o += up256((size_t)pl->nodes * 2 * q.dim * 4);
+    pl->off_arrived = o, o += up256((size_t)pl->nodes * 2 * pl->tiles * 4);
     pl->bytes = o;
     return WG_OK;
 }
@@ -494,7 +512,7 @@ wg::EmbParams emb_params(const EmbPlan& pl, const void* token, const void* in, v
     const wg_embedding_problem& q = pl.p;
     wg::EmbParams p = {};
     p.T = q.tokens, p.V = q.vocab, p.D = q.dim, p.ld_table = q.ld_table, p.ld_out = q.ld_out;
-    p.token = token, p.token64 = q.token_bits == 64, p.token16 = aligned16(token), p.padding = q.padding_token, p.scale = q.scale;
+    p.token = token, p.token64 = q.token_bits == 64, p.padding = q.padding_token, p.scale = q.scale;
     p.in = in, p.out = out;
     return p;
 }
@@ -525,20 +543,17 @@ int emb_lookup_t(const EmbPlan& pl, const wg::EmbParams& p, cudaStream_t s)
 template <typename TG, typename TY, int V>
 int emb_bwd_v(const EmbPlan& pl, const wg::EmbParams& p, cudaStream_t s)
 {
-    const int smem = wg::kEmbSortWarps * pl.R * 4;
+    const int smem = wg::kEmbSortWarps * (pl.R + p.keep) * 4;
     int st = wg::ensure_smem(wg::emb_sort_kernel<TG>, smem);
     if (!st)
         st = launch("emb_sort_kernel launch", wg::emb_sort_kernel<TG>, dim3((p.V + pl.R - 1) / pl.R),
                     dim3(wg::kEmbSortThreads), smem, s, p);
     if (st || p.T == 0) return st;
-    const int tiles = (p.D + wg::kEmbTile - 1) / wg::kEmbTile;
-    const long long items = pl.windows * tiles;
-    st = launch("emb_reduce_kernel launch", wg::emb_reduce_kernel<TG, TY, V>, dim3((unsigned)((items + 7) / 8)), dim3(256),
-                0, s, p, tiles);
-    if (!st)
-        st = launch("emb_join_kernel launch", wg::emb_join_kernel<TG, V>,
-                    dim3((unsigned)std::min<long long>(items, 4LL * num_sms())), dim3(256), 0, s, p, tiles);
-    return st;
+    // A warp per item; CTAs of two warps while there are fewer items than that fill the SMs.
+    const long long items = pl.windows * p.tiles;
+    const int warps = items < 16LL * num_sms() ? 2 : 8;
+    return launch("emb_reduce_kernel launch", wg::emb_reduce_kernel<TG, TY, V>, dim3((unsigned)((items + warps - 1) / warps)),
+                  dim3(32 * warps), 0, s, p);
 }
 
 template <typename TG, typename TY>
@@ -665,10 +680,16 @@ int wg_embedding_bwd_weight(const wg_embedding_problem* p, const void* token, co
     wg::EmbParams e = emb_params(pl, token, dy, dtable);
     char* ws = static_cast<char*>(workspace);
     e.accumulate = accumulate != 0;
-    e.R = pl.R;
+    // What shared memory is left keeps matches, of a quarter of a warp's positions at most.
+    const long long per = (pl.p.tokens + 1023) / 1024 * 32;
+    e.keep = (int)std::max(32LL, std::min<long long>((wg::kEmbSortMaxSmem / 4 / wg::kEmbSortWarps) - pl.R, per / 4 + 64));
+    e.R = pl.R, e.W = pl.W, e.tiles = pl.tiles;
+    memcpy(e.level, pl.level, sizeof e.level);
+    e.narrived = (int)(pl.nodes * 2 * pl.tiles);
     e.meta = reinterpret_cast<int*>(ws + pl.off_meta), e.count = reinterpret_cast<int*>(ws + pl.off_count);
+    e.start = reinterpret_cast<int*>(ws + pl.off_start);
     e.list = reinterpret_cast<int*>(ws + pl.off_list), e.row = reinterpret_cast<int*>(ws + pl.off_row);
-    e.cross = reinterpret_cast<int4*>(ws + pl.off_cross), e.part = reinterpret_cast<float*>(ws + pl.off_part);
+    e.part = reinterpret_cast<float*>(ws + pl.off_part), e.arrived = reinterpret_cast<int*>(ws + pl.off_arrived);
     return with_types(pl.p.table_dtype, pl.p.out_dtype, BwdCall{pl, e, static_cast<cudaStream_t>(stream)});
 }
 

@@ -383,8 +383,8 @@ WG_API int wg_muon_update(const wg_muon_problem* p, const void* grad, void* mome
  *   gradient:  dtable[v, :] = scale * sum over the t with token[t] = v of dy[t, :]
  *
  * Products and sums are fp32, rounded once (to nearest even).  The gradient's
- * sums run over ascending t, those of tokens that occur more than 64 times in
- * pieces of at most 32 that are then added in order: bitwise reproducible.
+ * sums run over ascending t, those of frequent tokens in pieces that are then
+ * added in order: bitwise reproducible.
  * A token outside [0, vocab) looks up zeros and adds to no row; wg_check_status
  * then returns WG_ERR_INVALID_TOKEN.
  *
