@@ -317,10 +317,10 @@ __device__ __forceinline__ void emb_join(const EmbParams& p, int v, int w, int t
         __threadfence();
 #pragma unroll
         for (int x = 0; x < 8; ++x) s[x] = 0.f;
-        for (int h = first; h <= last; h += 8) {
-            float f[8][8];
+        for (int h = first; h <= last; h += 4) {
+            float f[4][8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < 4; ++k) {
                 const int c = min(h + k, last);
                 const float* in = p.part + ((base + c) * 2 + (c == a ? 1 : 0)) * p.D;
 #pragma unroll
@@ -329,7 +329,7 @@ __device__ __forceinline__ void emb_join(const EmbParams& p, int v, int w, int t
                     for (int x = 0; x < VEC; ++x) f[k][j * VEC + x] = __ldcg(in + min(c0 + j * 32 * VEC + x, p.D - 1));
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
+            for (int k = 0; k < 4; ++k)
                 if (h + k <= last)
 #pragma unroll
                     for (int x = 0; x < 8; ++x) s[x] += f[k][x];
@@ -342,13 +342,45 @@ __device__ __forceinline__ void emb_join(const EmbParams& p, int v, int w, int t
     }
 }
 
-template <typename TG, typename TY, int VEC>
-__global__ void __launch_bounds__(256, 2) emb_reduce_kernel(const __grid_constant__ EmbParams p)
+// Rows of dy come into a ring of shared memory per warp, two batches of 4 KB, by
+// bulk copies: 24 warps on an SM have 192 KB on their way with few registers.
+// (Loads into registers, eight rows per warp ahead, left the kernel waiting for
+// memory two thirds of the time: 94 us for 65,536 rows of 2,048.)  A row piece that
+// does not start or end at 16 bytes is copied with what surrounds it, unless that
+// lies outside dy: then the warp loads it itself.
+template <typename TY, int VEC>
+struct EmbRing {
+    static constexpr int kPiece = kEmbTile * (int)sizeof(TY) + (VEC == 1 ? 16 : 0);
+    static constexpr int kBatch = 4096 / (kEmbTile * (int)sizeof(TY));
+    static constexpr int kBytes = 2 * kBatch * kPiece;
+};
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar)
 {
-    constexpr int NV = 8 / VEC, AHEAD = 8;
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+template <typename TG, typename TY, int VEC>
+__global__ void __launch_bounds__(256, 3) emb_reduce_kernel(const __grid_constant__ EmbParams p)
+{
+    typedef EmbRing<TY, VEC> Ring;
+    constexpr int B = Ring::kBatch, SZ = (int)sizeof(TY);
+    extern __shared__ __align__(16) uint8_t rings[];
+    __shared__ uint64_t bars[8][2];
     pdl_launch_dependents();
-    const int lane = threadIdx.x & 31, W = p.W;
-    const long long item = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = p.W;
+    uint8_t* ring = rings + warp * Ring::kBytes;
+    uint64_t* bar = bars[warp];
+    if (lane == 0) {
+        mbar_init(&bar[0], 1);
+        mbar_init(&bar[1], 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+    const long long item = (long long)blockIdx.x * (blockDim.x >> 5) + warp;
     const int w = (int)(item / p.tiles), tile = (int)(item - (long long)w * p.tiles);
     pdl_wait();
     const int n = p.meta[0], e0 = w * W;
@@ -364,51 +396,103 @@ __global__ void __launch_bounds__(256, 2) emb_reduce_kernel(const __grid_constan
     if (nhead && !entered) b += __popc(__ballot_sync(0xffffffffu, lane < m && wrow == head));  // an earlier window's run
     if (ntail && !leaves && b < e)  // this window's run, to its end
         e = e0 + m - __popc(__ballot_sync(0xffffffffu, lane < m && wrow == tail)) + ntail;
-    const int c0 = tile * kEmbTile + lane * VEC;
-    int col[NV];
+    if (b >= e) return;
+    // Up to three times 32 entries: positions, rows, and where runs end.
+    int pos[3], row[3];
+    unsigned ends[3];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) col[j] = min(c0 + j * 32 * VEC, p.D - VEC);  // columns past the row read its last ones
-    const TY* dy = static_cast<const TY*>(p.in);
-    // Three stretches of the list: the end of a long run (a partial row), whole runs,
-    // the beginning of a long run (a partial row).
-    const int nin = entered ? __popc(__ballot_sync(0xffffffffu, lane < m && wrow == head)) : 0;
-    const int nout = leaves && !(entered && nin == m) ? __popc(__ballot_sync(0xffffffffu, lane < m && wrow == tail)) : 0;
-#pragma unroll 1
-    for (int part = 0; part < 3; ++part) {
-        const int sb = part == 0 ? b : part == 1 ? b + nin : e - nout;
-        const int se = part == 0 ? b + nin : part == 1 ? e - nout : e;
-        float s[8] = {};
-        for (int base = sb; base < se; base += 32) {
-            const int k = min(32, se - base);
-            const int pos = p.list[min(base + lane, se - 1)], row = p.row[min(base + lane, se - 1)];
-            const int after = base + lane + 1 < se ? p.row[base + lane + 1] : -1;
-            const unsigned ends = part == 1 ? __ballot_sync(0xffffffffu, after != row) : 0u;
-            for (int i0 = 0; i0 < k; i0 += AHEAD) {
-                // Eight rows in flight; entries past the last read its row again.
-                Vec<TY, VEC> f[AHEAD][NV];
-#pragma unroll
-                for (int a = 0; a < AHEAD; ++a) {
-                    const long long t = __shfl_sync(0xffffffffu, pos, i0 + a);
-#pragma unroll
-                    for (int j = 0; j < NV; ++j)
-                        f[a][j] = *reinterpret_cast<const Vec<TY, VEC>*>(dy + t * p.ld_out + col[j]);
-                }
-#pragma unroll
-                for (int a = 0; a < AHEAD; ++a) {
-                    const int i = i0 + a;
-                    if (i >= k) break;
-#pragma unroll
-                    for (int j = 0; j < NV; ++j)
-#pragma unroll
-                        for (int q = 0; q < VEC; ++q) s[j * VEC + q] += to_f32<TY>(f[a][j].v[q]);
-                    if (!(ends >> i & 1u)) continue;
-                    emb_write<TG, VEC>(p, __shfl_sync(0xffffffffu, row, i), c0, s);
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) s[x] = 0.f;
-                }
-            }
+    for (int c = 0; c < 3; ++c) {
+        const int i = min(b + 32 * c + lane, e - 1);
+        pos[c] = p.list[i], row[c] = p.row[i];
+        const int after = b + 32 * c + lane + 1 < e ? p.row[b + 32 * c + lane + 1] : -1;
+        ends[c] = __ballot_sync(0xffffffffu, after != row[c]);
+    }
+    const int col0 = tile * kEmbTile, ncol = min(kEmbTile, p.D - col0);
+    const TY* dy = static_cast<const TY*>(p.in) + col0;
+    const uintptr_t dy0 = reinterpret_cast<uintptr_t>(p.in);
+    const uintptr_t dy1 = dy0 + (uintptr_t)((p.T - 1) * p.ld_out + p.D) * SZ;
+    const int batches = (e - b + B - 1) / B;
+    auto pick = [&](const int (&x)[3], int i) {  // entry b + i's
+        const int y = i < 32 ? x[0] : i < 64 ? x[1] : x[2];
+        return __shfl_sync(0xffffffffu, y, i & 31);
+    };
+    auto outside = [&](uintptr_t a) {  // the piece at a cannot be copied
+        return VEC == 1 && ((a & ~(uintptr_t)15) < dy0 || ((a + ncol * SZ + 15) & ~(uintptr_t)15) > dy1);
+    };
+    auto issue = [&](int q) {
+        if (q >= batches) return;
+        const int i = q * B + lane, k = min(B, e - b - q * B);
+        const int y = q * B < 32 ? pos[0] : q * B < 64 ? pos[1] : pos[2];
+        const long long t = __shfl_sync(0xffffffffu, y, i & 31);
+        const uintptr_t a = reinterpret_cast<uintptr_t>(dy + t * p.ld_out), lo = a & ~(uintptr_t)15;
+        uint32_t bytes = (uint32_t)(((a + ncol * SZ + 15) & ~(uintptr_t)15) - lo);
+        if (lane >= k || outside(a)) bytes = 0;
+        const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
+        if (lane == 0) mbar_arrive_expect_tx(&bar[q & 1], total);
+        __syncwarp();
+        if (bytes) bulk_load(ring + ((q & 1) * B + lane) * Ring::kPiece, reinterpret_cast<const void*>(lo), bytes, &bar[q & 1]);
+    };
+    issue(0);
+    issue(1);
+    const int c0 = col0 + lane * VEC;
+    float s[8] = {}, first[8] = {};
+    bool partial = entered;  // the run being summed came from before the window
+    for (int q = 0; q < batches; ++q) {
+        if (!mbar_wait(&bar[q & 1], (uint32_t)(q >> 1) & 1u)) {
+            if (q + 1 < batches) mbar_wait(&bar[(q + 1) & 1], (uint32_t)((q + 1) >> 1) & 1u);  // copies in flight
+            return;
         }
-        if (part != 1 && sb < se) emb_join<TG, VEC>(p, part == 0 ? head : tail, w, tile, s);
+        __syncwarp();
+        const int k = min(B, e - b - q * B);
+        const unsigned end = (q * B < 32 ? ends[0] : q * B < 64 ? ends[1] : ends[2]) >> (q * B & 31);
+#pragma unroll
+        for (int a = 0; a < B; ++a) {
+            if (a >= k) break;
+            const uint8_t* piece = ring + ((q & 1) * B + a) * Ring::kPiece;
+            if constexpr (VEC == 8) {
+                float f[8];
+                load_f32<TY, 8>(reinterpret_cast<const TY*>(piece) + lane * 8, f);
+#pragma unroll
+                for (int x = 0; x < 8; ++x) s[x] += f[x];
+            } else {
+                const long long t = pick(pos, q * B + a);
+                const TY* src = dy + t * p.ld_out;
+                const uintptr_t at = reinterpret_cast<uintptr_t>(src);
+                if (!outside(at)) src = reinterpret_cast<const TY*>(piece + (at & 15u));
+#pragma unroll
+                for (int x = 0; x < 8; ++x) s[x] += to_f32<TY>(src[min(lane + 32 * x, ncol - 1)]);
+            }
+            if (!(end >> a & 1u)) continue;
+            const int i = q * B + a;
+            if (partial) {  // (joined below)
+#pragma unroll
+                for (int x = 0; x < 8; ++x) first[x] = s[x];
+            } else if (leaves && b + i == e - 1) {
+                break;
+            } else {
+                emb_write<TG, VEC>(p, pick(row, i), c0, s);
+            }
+#pragma unroll
+            for (int x = 0; x < 8; ++x) s[x] = 0.f;
+            partial = false;
+        }
+        __syncwarp();
+        issue(q + 2);
+    }
+    // The partial rows: of the long run that entered, of the one that leaves (unless it is the same).
+    const bool through = entered && leaves && head == tail;
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+        if (i == 0 ? !entered : !leaves || through) continue;
+        if (i == 0) {
+            float x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = s[k], s[k] = first[k], first[k] = x[k];
+        } else if (entered) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s[k] = first[k];
+        }
+        emb_join<TG, VEC>(p, i == 0 ? head : tail, w, tile, s);
     }
 }
 

@@ -552,17 +552,17 @@ int emb_bwd_v(const EmbPlan& pl, const wg::EmbParams& p, cudaStream_t s)
     // A warp per item; CTAs of two warps while there are fewer items than that fill the SMs.
     const long long items = pl.windows * p.tiles;
     const int warps = items < 16LL * num_sms() ? 2 : 8;
+    const int ring = warps * wg::EmbRing<TY, V>::kBytes;
+    if ((st = wg::ensure_smem(wg::emb_reduce_kernel<TG, TY, V>, ring))) return st;
     return launch("emb_reduce_kernel launch", wg::emb_reduce_kernel<TG, TY, V>, dim3((unsigned)((items + warps - 1) / warps)),
-                  dim3(32 * warps), 0, s, p);
+                  dim3(32 * warps), ring, s, p);
 }
 
 template <typename TG, typename TY>
 int emb_bwd_t(const EmbPlan& pl, const wg::EmbParams& p, cudaStream_t s)
 {
-    constexpr int V = sizeof(TG) == 4 || sizeof(TY) == 4 ? 4 : 8;
-    const bool vec = p.D % V == 0 && p.ld_table % V == 0 && p.ld_out % V == 0 && aligned_to(p.in, V * sizeof(TY)) &&
-                     aligned_to(p.out, V * sizeof(TG));
-    return vec ? emb_bwd_v<TG, TY, V>(pl, p, s) : emb_bwd_v<TG, TY, 1>(pl, p, s);
+    const bool vec = p.D % 8 == 0 && p.ld_table % 8 == 0 && p.ld_out % 8 == 0 && aligned16(p.in) && aligned16(p.out);
+    return vec ? emb_bwd_v<TG, TY, 8>(pl, p, s) : emb_bwd_v<TG, TY, 1>(pl, p, s);
 }
 
 // Call f with the types of two dtypes.
