@@ -383,36 +383,46 @@ __global__ void __launch_bounds__(256, 3) emb_reduce_kernel(const __grid_constan
     const long long item = (long long)blockIdx.x * (blockDim.x >> 5) + warp;
     const int w = (int)(item / p.tiles), tile = (int)(item - (long long)w * p.tiles);
     pdl_wait();
-    const int n = p.meta[0], e0 = w * W;
-    if (e0 >= n) return;
-    const int m = min(W, n - e0);
-    // The window's rows, and the runs that cross its borders.
-    const int wrow = p.row[min(e0 + lane, e0 + m - 1)];
-    const int prev = e0 > 0 ? p.row[e0 - 1] : -1, next = e0 + m < n ? p.row[e0 + m] : -1;
-    const int head = __shfl_sync(0xffffffffu, wrow, 0), tail = __shfl_sync(0xffffffffu, wrow, m - 1);
-    const int nhead = head == prev ? p.count[head] : 0, ntail = tail == next ? p.count[tail] : 0;
-    const bool entered = nhead > 2 * W, leaves = ntail > 2 * W;  // long runs that cross
-    int b = e0, e = e0 + m;
-    if (nhead && !entered) b += __popc(__ballot_sync(0xffffffffu, lane < m && wrow == head));  // an earlier window's run
-    if (ntail && !leaves && b < e)  // this window's run, to its end
-        e = e0 + m - __popc(__ballot_sync(0xffffffffu, lane < m && wrow == tail)) + ntail;
-    if (b >= e) return;
-    // Up to three times 32 entries: positions, rows, and where runs end.
+    // Three times 32 entries from the window's first on, their rows and positions, asked
+    // for before it is known how many of them there are (what lies past the list's end is
+    // within its memory, and not used).
+    const int e0 = w * W, last_t = (int)p.T - 1;
     int pos[3], row[3];
-    unsigned ends[3];
 #pragma unroll
     for (int c = 0; c < 3; ++c) {
-        const int i = min(b + 32 * c + lane, e - 1);
+        const int i = min(e0 + 32 * c + lane, last_t);
         pos[c] = p.list[i], row[c] = p.row[i];
-        const int after = b + 32 * c + lane + 1 < e ? p.row[b + 32 * c + lane + 1] : -1;
-        ends[c] = __ballot_sync(0xffffffffu, after != row[c]);
+    }
+    const int before = e0 > 0 ? p.row[e0 - 1] : -1;
+    const int n = p.meta[0];
+    if (e0 >= n) return;
+    const int m = min(W, n - e0);
+    // The runs that cross the window's borders.
+    const int head = __shfl_sync(0xffffffffu, row[0], 0), tail = __shfl_sync(0xffffffffu, row[0], m - 1);
+    const int row32 = __shfl_sync(0xffffffffu, row[1], 0);
+    const int next = e0 + m < n ? (m < 32 ? __shfl_sync(0xffffffffu, row[0], m & 31) : row32) : -1;
+    const int nhead = head == before ? p.count[head] : 0, ntail = tail == next ? p.count[tail] : 0;
+    const bool entered = nhead > 2 * W, leaves = ntail > 2 * W;  // long runs that cross
+    int b = 0, e = m;  // this warp's entries, from e0 on
+    if (nhead && !entered) b = __popc(__ballot_sync(0xffffffffu, lane < m && row[0] == head));  // an earlier window's run
+    if (ntail && !leaves && b < e)  // this window's run, to its end
+        e = m - __popc(__ballot_sync(0xffffffffu, lane < m && row[0] == tail)) + ntail;
+    if (b >= e) return;
+    unsigned ends[3];  // where runs end
+#pragma unroll
+    for (int c = 0; c < 3; ++c) {
+        int after = __shfl_down_sync(0xffffffffu, row[c], 1);
+        const int over = c < 2 ? __shfl_sync(0xffffffffu, row[c < 2 ? c + 1 : 2], 0) : -1;
+        if (lane == 31) after = over;
+        ends[c] = __ballot_sync(0xffffffffu, after != row[c] || 32 * c + lane == e - 1);
     }
     const int col0 = tile * kEmbTile, ncol = min(kEmbTile, p.D - col0);
     const TY* dy = static_cast<const TY*>(p.in) + col0;
     const uintptr_t dy0 = reinterpret_cast<uintptr_t>(p.in);
     const uintptr_t dy1 = dy0 + (uintptr_t)((p.T - 1) * p.ld_out + p.D) * SZ;
-    const int batches = (e - b + B - 1) / B;
-    auto pick = [&](const int (&x)[3], int i) {  // entry b + i's
+    // Batches are aligned to the window: the first may begin at b.
+    const int q0 = b / B, q1 = (e + B - 1) / B;
+    auto pick = [&](const int (&x)[3], int i) {  // entry i's
         const int y = i < 32 ? x[0] : i < 64 ? x[1] : x[2];
         return __shfl_sync(0xffffffffu, y, i & 31);
     };
@@ -420,34 +430,35 @@ __global__ void __launch_bounds__(256, 3) emb_reduce_kernel(const __grid_constan
         return VEC == 1 && ((a & ~(uintptr_t)15) < dy0 || ((a + ncol * SZ + 15) & ~(uintptr_t)15) > dy1);
     };
     auto issue = [&](int q) {
-        if (q >= batches) return;
-        const int i = q * B + lane, k = min(B, e - b - q * B);
+        if (q >= q1) return;
+        const int i = q * B + lane;
         const int y = q * B < 32 ? pos[0] : q * B < 64 ? pos[1] : pos[2];
         const long long t = __shfl_sync(0xffffffffu, y, i & 31);
         const uintptr_t a = reinterpret_cast<uintptr_t>(dy + t * p.ld_out), lo = a & ~(uintptr_t)15;
         uint32_t bytes = (uint32_t)(((a + ncol * SZ + 15) & ~(uintptr_t)15) - lo);
-        if (lane >= k || outside(a)) bytes = 0;
+        if (lane >= B || i < b || i >= e || outside(a)) bytes = 0;
         const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
         if (lane == 0) mbar_arrive_expect_tx(&bar[q & 1], total);
         __syncwarp();
         if (bytes) bulk_load(ring + ((q & 1) * B + lane) * Ring::kPiece, reinterpret_cast<const void*>(lo), bytes, &bar[q & 1]);
     };
-    issue(0);
-    issue(1);
+    issue(q0);
+    issue(q0 + 1);
     const int c0 = col0 + lane * VEC;
     float s[8] = {}, first[8] = {};
     bool partial = entered;  // the run being summed came from before the window
-    for (int q = 0; q < batches; ++q) {
-        if (!mbar_wait(&bar[q & 1], (uint32_t)(q >> 1) & 1u)) {
-            if (q + 1 < batches) mbar_wait(&bar[(q + 1) & 1], (uint32_t)((q + 1) >> 1) & 1u);  // copies in flight
+    for (int q = q0; q < q1; ++q) {
+        if (!mbar_wait(&bar[q & 1], (uint32_t)((q - q0) >> 1) & 1u)) {
+            if (q + 1 < q1) mbar_wait(&bar[(q + 1) & 1], (uint32_t)((q + 1 - q0) >> 1) & 1u);  // copies in flight
             return;
         }
         __syncwarp();
-        const int k = min(B, e - b - q * B);
         const unsigned end = (q * B < 32 ? ends[0] : q * B < 64 ? ends[1] : ends[2]) >> (q * B & 31);
 #pragma unroll
         for (int a = 0; a < B; ++a) {
-            if (a >= k) break;
+            const int i = q * B + a;
+            if (i >= e) break;
+            if (i < b) continue;
             const uint8_t* piece = ring + ((q & 1) * B + a) * Ring::kPiece;
             if constexpr (VEC == 8) {
                 float f[8];
@@ -455,7 +466,7 @@ __global__ void __launch_bounds__(256, 3) emb_reduce_kernel(const __grid_constan
 #pragma unroll
                 for (int x = 0; x < 8; ++x) s[x] += f[x];
             } else {
-                const long long t = pick(pos, q * B + a);
+                const long long t = pick(pos, i);
                 const TY* src = dy + t * p.ld_out;
                 const uintptr_t at = reinterpret_cast<uintptr_t>(src);
                 if (!outside(at)) src = reinterpret_cast<const TY*>(piece + (at & 15u));
@@ -463,11 +474,10 @@ __global__ void __launch_bounds__(256, 3) emb_reduce_kernel(const __grid_constan
                 for (int x = 0; x < 8; ++x) s[x] += to_f32<TY>(src[min(lane + 32 * x, ncol - 1)]);
             }
             if (!(end >> a & 1u)) continue;
-            const int i = q * B + a;
             if (partial) {  // (joined below)
 #pragma unroll
                 for (int x = 0; x < 8; ++x) first[x] = s[x];
-            } else if (leaves && b + i == e - 1) {
+            } else if (leaves && i == e - 1) {
                 break;
             } else {
                 emb_write<TG, VEC>(p, pick(row, i), c0, s);
