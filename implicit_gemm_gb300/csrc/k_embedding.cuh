@@ -3,7 +3,7 @@
 //   lookup:    out[t, :]    = scale * table[token[t], :]
 //   gradient:  dtable[v, :] = scale * sum over the t with token[t] = v of dy[t, :]
 //
-// The gradient runs in two kernels, without atomics on data:
+// The gradient runs in three kernels, without atomics on data:
 //
 //  emb_sort_kernel    a stable counting sort of the positions by token.  Every CTA
 //                     owns a range of table rows and reads all tokens (a broadcast
@@ -14,13 +14,13 @@
 //                     nothing from each other.  It also writes the zeros of the
 //                     rows that no token names.
 //  emb_reduce_kernel  a segmented sum over the sorted list: a warp takes W entries
-//                     (a window) by 256 columns.  A run of at most 2 W entries is
+//                     (a window) by 512 columns.  A run of at most 2 W entries is
 //                     summed by the warp of the window it starts in, to its end;
-//                     a longer one leaves an fp32 partial row per window, and the
-//                     partial rows of 16 windows, then of 16 such groups and so on,
-//                     are added in order by whichever warp brings the last of them.
-//                     So no warp has more than 3 W entries, however often a token
-//                     occurs, and the order of every sum is fixed.
+//                     a longer one leaves an fp32 partial row per window.  So no
+//                     warp has more than 3 W entries, however often a token occurs.
+//  emb_join_kernel    adds the partial rows of the long runs, in the windows' order.
+//                     (Joined by whichever warp brought the last partial row instead,
+//                     the fences took longer than this kernel does.)
 #pragma once
 
 #include "ptx.cuh"
@@ -42,16 +42,13 @@ struct EmbParams {
     int R;          // table rows of a CTA of emb_sort_kernel
     int keep;       // matches that a warp of it keeps from the count
     int W;          // entries of a window: 8, 16 or 32
-    int tiles;      // 256-column tiles of a row
-    int level[8];   // first partial row of a level: windows, groups of 16 of them, ...
-    int narrived;   // counters
-    int* meta;      // [0] entries of the list
+    int tiles;      // 512-column tiles of a row
+    int* meta;      // [0] entries of the list, [1] long runs that cross windows
     int* count;     // [V] occurrences of a row's token
-    int* start;     // [V] first entry of its run
     int* list;      // [T] positions, by (row, position)
     int* row;       // [T] their rows
-    float* part;    // [level rows][2][D] partial rows: of a run from before the child, of a run that starts in it
-    int* arrived;   // [level rows][2][tiles] partial rows of a run that are there, counted at its first child of a group
+    int4* cross;    // (row, first entry, entries, 0) of the long runs that cross windows
+    float* part;    // [windows][2][D] partial rows: of a run from before the window, of a run that goes on after it
 };
 
 // The token at position t as a table row, or -1 when it is out of range.
@@ -90,7 +87,7 @@ constexpr int kEmbSortThreads = 1024, kEmbSortWarps = kEmbSortThreads / 32;
 constexpr int kEmbSortMaxRows = 1472;     // 32 counters of 4 bytes a row: 184 KB of shared memory
 constexpr int kEmbSortRowBits = 11;       // a row of the range in a kept match
 constexpr int kEmbSortMaxSmem = 220 << 10;  // counters and kept matches
-constexpr int kEmbTile = 256, kEmbFan = 16;
+constexpr int kEmbCols = 16, kEmbTile = 32 * kEmbCols;  // columns per lane and per warp
 
 // n elements of zero from any element-aligned address, by one warp.
 template <typename T>
@@ -142,8 +139,6 @@ __global__ void __launch_bounds__(kEmbSortThreads, 1) emb_sort_kernel(const __gr
     __syncthreads();
     pdl_wait();
     int* mine = hist + warp * R;
-    for (int i = blockIdx.x * kEmbSortThreads + threadIdx.x; i < p.narrived; i += gridDim.x * kEmbSortThreads)
-        p.arrived[i] = 0;
     // Each warp's positions: a multiple of 32.  Eight loads per lane are in flight at
     // a time (one at a time their latency alone took 30 us for 65,536 tokens).
     constexpr int kAhead = 8;
@@ -211,7 +206,6 @@ __global__ void __launch_bounds__(kEmbSortThreads, 1) emb_sort_kernel(const __gr
         const int r = threadIdx.x + k * kEmbSortThreads;
         if (r < nr) {
             p.count[lo + r] = n[k];
-            p.start[lo + r] = at[k];
             first[r] = n[k];
             int o = at[k];
             if (n[k])
@@ -223,7 +217,7 @@ __global__ void __launch_bounds__(kEmbSortThreads, 1) emb_sort_kernel(const __gr
                 }
         }
     }
-    if (threadIdx.x == 0 && blockIdx.x == gridDim.x - 1) p.meta[0] = base + total;
+    if (threadIdx.x == 0 && blockIdx.x == gridDim.x - 1) p.meta[0] = base + total, p.meta[1] = 0;
     __syncthreads();
     // The matches in order; equal rows of 32 of them take consecutive entries.
     auto place = [&](bool in, long long t, int r) {
@@ -264,13 +258,13 @@ __global__ void __launch_bounds__(kEmbSortThreads, 1) emb_sort_kernel(const __gr
             if (!first[r]) emb_zero_row(static_cast<TG*>(p.out) + (long long)(lo + r) * p.ld_table, p.D, lane);
 }
 
-// A finished row's 256 columns: scaled, added to what is there when accumulating, rounded.
+// A finished row's 512 columns: scaled, added to what is there when accumulating, rounded.
 template <typename TG, int VEC>
-__device__ __forceinline__ void emb_write(const EmbParams& p, int v, int c0, const float (&s)[8])
+__device__ __forceinline__ void emb_write(const EmbParams& p, int v, int c0, const float (&s)[kEmbCols])
 {
     TG* out = static_cast<TG*>(p.out) + v * p.ld_table;
 #pragma unroll
-    for (int j = 0; j < 8 / VEC; ++j) {
+    for (int j = 0; j < kEmbCols / VEC; ++j) {
         const int c = c0 + j * 32 * VEC;
         if (c >= p.D) continue;
         float f[VEC];
@@ -286,82 +280,34 @@ __device__ __forceinline__ void emb_write(const EmbParams& p, int v, int c0, con
     }
 }
 
-// The partial row (one tile of it, in s) of a run that begins at entry `start` and
-// has n entries, from window w: kept, and added to its neighbours' by the warp that
-// finds all of a group there.
-template <typename TG, int VEC>
-__device__ __forceinline__ void emb_join(const EmbParams& p, int v, int w, int tile, float (&s)[8])
-{
-    constexpr int NV = 8 / VEC;
-    const int lane = threadIdx.x & 31, c0 = tile * kEmbTile + lane * VEC;
-    const int start = p.start[v];
-    int a = start / p.W, b = (start + p.count[v] - 1) / p.W, child = w;
-    for (int l = 0;; ++l) {
-        const long long base = p.level[l];
-        float* q = p.part + ((base + child) * 2 + (child == a ? 1 : 0)) * p.D;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = c0 + j * 32 * VEC;
-            float g[VEC];
-#pragma unroll
-            for (int x = 0; x < VEC; ++x) g[x] = s[j * VEC + x];
-            if (c < p.D) store_f32<float, VEC>(q + c, g);
-        }
-        __threadfence();
-        __syncwarp();
-        const int group = child / kEmbFan;
-        const int first = max(a, group * kEmbFan), last = min(b, group * kEmbFan + kEmbFan - 1);
-        int seen = 0;
-        if (lane == 0) seen = atomicAdd(&p.arrived[((base + first) * 2 + (first == a ? 1 : 0)) * p.tiles + tile], 1);
-        if (__shfl_sync(0xffffffffu, seen, 0) != last - first) return;
-        __threadfence();
-#pragma unroll
-        for (int x = 0; x < 8; ++x) s[x] = 0.f;
-        for (int h = first; h <= last; h += 4) {
-            float f[4][8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int c = min(h + k, last);
-                const float* in = p.part + ((base + c) * 2 + (c == a ? 1 : 0)) * p.D;
-#pragma unroll
-                for (int j = 0; j < NV; ++j)
-#pragma unroll
-                    for (int x = 0; x < VEC; ++x) f[k][j * VEC + x] = __ldcg(in + min(c0 + j * 32 * VEC + x, p.D - 1));
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (h + k <= last)
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) s[x] += f[k][x];
-        }
-        if (a / kEmbFan == b / kEmbFan) {
-            emb_write<TG, VEC>(p, v, c0, s);
-            return;
-        }
-        a /= kEmbFan, b /= kEmbFan, child = group;
-    }
-}
-
 // Rows of dy come into a ring of shared memory per warp, two batches of 4 KB, by
-// bulk copies: 24 warps on an SM have 192 KB on their way with few registers.
-// (Loads into registers, eight rows per warp ahead, left the kernel waiting for
-// memory two thirds of the time: 94 us for 65,536 rows of 2,048.)  A row piece that
-// does not start or end at 16 bytes is copied with what surrounds it, unless that
-// lies outside dy: then the warp loads it itself.
+// asynchronous copies: 24 warps on an SM have 192 KB on their way with few
+// registers (loads into registers, eight rows per warp ahead, left the kernel
+// waiting for memory two thirds of the time: 94 us for 65,536 rows of 2,048), and
+// with aligned rows every lane reads back what it copied itself, so nothing waits
+// for another lane.  (Bulk copies, one per row and lane, took the kernel three times
+// the instructions.)  16-bit rows that start at odd elements are copied in the 4-byte
+// words that hold them, unless such a word lies outside dy: then the warp loads the
+// row when it needs it.
 template <typename TY, int VEC>
 struct EmbRing {
     static constexpr int kPiece = kEmbTile * (int)sizeof(TY) + (VEC == 1 ? 16 : 0);
     static constexpr int kBatch = 4096 / (kEmbTile * (int)sizeof(TY));
-    static constexpr int kBytes = 2 * kBatch * kPiece;
+    static constexpr int kEntries = 2 * kBatch * kPiece;  // then 96 positions, and 96 rows
+    static constexpr int kBytes = kEntries + 96 * 8;
 };
 
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar)
+template <int BYTES>
+__device__ __forceinline__ void async_copy(uint32_t dst, const void* src)
 {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                     smem_u32(dst)),
-                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the last group of this thread's copies are there.
+__device__ __forceinline__ void async_wait_1() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
 
 template <typename TG, typename TY, int VEC>
 __global__ void __launch_bounds__(256, 3) emb_reduce_kernel(const __grid_constant__ EmbParams p)
@@ -369,140 +315,176 @@ __global__ void __launch_bounds__(256, 3) emb_reduce_kernel(const __grid_constan
     typedef EmbRing<TY, VEC> Ring;
     constexpr int B = Ring::kBatch, SZ = (int)sizeof(TY);
     extern __shared__ __align__(16) uint8_t rings[];
-    __shared__ uint64_t bars[8][2];
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = p.W;
     uint8_t* ring = rings + warp * Ring::kBytes;
-    uint64_t* bar = bars[warp];
-    if (lane == 0) {
-        mbar_init(&bar[0], 1);
-        mbar_init(&bar[1], 1);
-        fence_mbar_init();
-    }
-    __syncwarp();
-    const long long item = (long long)blockIdx.x * (blockDim.x >> 5) + warp;
-    const int w = (int)(item / p.tiles), tile = (int)(item - (long long)w * p.tiles);
+    int* const pos = reinterpret_cast<int*>(ring + Ring::kEntries);
+    int* const row = pos + 96;
+    const unsigned item = blockIdx.x * (blockDim.x >> 5) + warp;
+    const int w = (int)(item / (unsigned)p.tiles), tile = (int)(item - (unsigned)w * p.tiles);
     pdl_wait();
     // Three times 32 entries from the window's first on, their rows and positions, asked
     // for before it is known how many of them there are (what lies past the list's end is
     // within its memory, and not used).
     const int e0 = w * W, last_t = (int)p.T - 1;
-    int pos[3], row[3];
+    int r[3], head, next;
 #pragma unroll
     for (int c = 0; c < 3; ++c) {
         const int i = min(e0 + 32 * c + lane, last_t);
-        pos[c] = p.list[i], row[c] = p.row[i];
+        pos[32 * c + lane] = p.list[i];
+        r[c] = p.row[i];
     }
     const int before = e0 > 0 ? p.row[e0 - 1] : -1;
     const int n = p.meta[0];
     if (e0 >= n) return;
+#pragma unroll
+    for (int c = 0; c < 3; ++c) row[32 * c + lane] = r[c];
+    __syncwarp();
     const int m = min(W, n - e0);
     // The runs that cross the window's borders.
-    const int head = __shfl_sync(0xffffffffu, row[0], 0), tail = __shfl_sync(0xffffffffu, row[0], m - 1);
-    const int row32 = __shfl_sync(0xffffffffu, row[1], 0);
-    const int next = e0 + m < n ? (m < 32 ? __shfl_sync(0xffffffffu, row[0], m & 31) : row32) : -1;
+    head = row[0], next = e0 + m < n ? row[m] : -1;
+    const int tail = row[m - 1];
     const int nhead = head == before ? p.count[head] : 0, ntail = tail == next ? p.count[tail] : 0;
-    const bool entered = nhead > 2 * W, leaves = ntail > 2 * W;  // long runs that cross
-    int b = 0, e = m;  // this warp's entries, from e0 on
-    if (nhead && !entered) b = __popc(__ballot_sync(0xffffffffu, lane < m && row[0] == head));  // an earlier window's run
+    const bool leaves = ntail > 2 * W;  // a long run that goes on
+    bool partial = nhead > 2 * W;       // the run being summed is a long one from before the window
+    int b = 0, e = m;                   // this warp's entries, from e0 on
+    if (nhead && !partial) b = __popc(__ballot_sync(0xffffffffu, lane < m && r[0] == head));  // an earlier window's run
     if (ntail && !leaves && b < e)  // this window's run, to its end
-        e = m - __popc(__ballot_sync(0xffffffffu, lane < m && row[0] == tail)) + ntail;
+        e = m - __popc(__ballot_sync(0xffffffffu, lane < m && r[0] == tail)) + ntail;
     if (b >= e) return;
-    unsigned ends[3];  // where runs end
-#pragma unroll
-    for (int c = 0; c < 3; ++c) {
-        int after = __shfl_down_sync(0xffffffffu, row[c], 1);
-        const int over = c < 2 ? __shfl_sync(0xffffffffu, row[c < 2 ? c + 1 : 2], 0) : -1;
-        if (lane == 31) after = over;
-        ends[c] = __ballot_sync(0xffffffffu, after != row[c] || 32 * c + lane == e - 1);
-    }
-    const int col0 = tile * kEmbTile, ncol = min(kEmbTile, p.D - col0);
+    const int col0 = tile * kEmbTile, ncol = min(kEmbTile, p.D - col0), c0 = col0 + lane * VEC;
     const TY* dy = static_cast<const TY*>(p.in) + col0;
     const uintptr_t dy0 = reinterpret_cast<uintptr_t>(p.in);
     const uintptr_t dy1 = dy0 + (uintptr_t)((p.T - 1) * p.ld_out + p.D) * SZ;
-    // Batches are aligned to the window: the first may begin at b.
-    const int q0 = b / B, q1 = (e + B - 1) / B;
-    auto pick = [&](const int (&x)[3], int i) {  // entry i's
-        const int y = i < 32 ? x[0] : i < 64 ? x[1] : x[2];
-        return __shfl_sync(0xffffffffu, y, i & 31);
+    auto outside = [&](uintptr_t a) {  // the words that hold the piece at a are not all in dy
+        return VEC == 1 && SZ == 2 && ((a & ~(uintptr_t)3) < dy0 || ((a + ncol * SZ + 3) & ~(uintptr_t)3) > dy1);
     };
-    auto outside = [&](uintptr_t a) {  // the piece at a cannot be copied
-        return VEC == 1 && ((a & ~(uintptr_t)15) < dy0 || ((a + ncol * SZ + 15) & ~(uintptr_t)15) > dy1);
-    };
-    auto issue = [&](int q) {
-        if (q >= q1) return;
-        const int i = q * B + lane;
-        const int y = q * B < 32 ? pos[0] : q * B < 64 ? pos[1] : pos[2];
-        const long long t = __shfl_sync(0xffffffffu, y, i & 31);
-        const uintptr_t a = reinterpret_cast<uintptr_t>(dy + t * p.ld_out), lo = a & ~(uintptr_t)15;
-        uint32_t bytes = (uint32_t)(((a + ncol * SZ + 15) & ~(uintptr_t)15) - lo);
-        if (lane >= B || i < b || i >= e || outside(a)) bytes = 0;
-        const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
-        if (lane == 0) mbar_arrive_expect_tx(&bar[q & 1], total);
-        __syncwarp();
-        if (bytes) bulk_load(ring + ((q & 1) * B + lane) * Ring::kPiece, reinterpret_cast<const void*>(lo), bytes, &bar[q & 1]);
-    };
-    issue(q0);
-    issue(q0 + 1);
-    const int c0 = col0 + lane * VEC;
-    float s[8] = {}, first[8] = {};
-    bool partial = entered;  // the run being summed came from before the window
-    for (int q = q0; q < q1; ++q) {
-        if (!mbar_wait(&bar[q & 1], (uint32_t)((q - q0) >> 1) & 1u)) {
-            if (q + 1 < q1) mbar_wait(&bar[(q + 1) & 1], (uint32_t)((q + 1 - q0) >> 1) & 1u);  // copies in flight
-            return;
-        }
-        __syncwarp();
-        const unsigned end = (q * B < 32 ? ends[0] : q * B < 64 ? ends[1] : ends[2]) >> (q * B & 31);
-#pragma unroll
-        for (int a = 0; a < B; ++a) {
-            const int i = q * B + a;
-            if (i >= e) break;
-            if (i < b) continue;
-            const uint8_t* piece = ring + ((q & 1) * B + a) * Ring::kPiece;
+    const uint32_t ring0 = smem_u32(ring);
+    // Entries i0 .. i0 + B - 1 (batches are aligned to the window).
+    auto issue = [&](int i0) {
+        const int lo = max(i0, b), hi = min(i0 + B, e);
+#pragma unroll 2
+        for (int i = lo; i < hi; ++i) {
+            const TY* src = dy + pos[i] * p.ld_out;
+            const uint32_t dst = ring0 + (uint32_t)((i & (2 * B - 1)) * Ring::kPiece);
             if constexpr (VEC == 8) {
-                float f[8];
-                load_f32<TY, 8>(reinterpret_cast<const TY*>(piece) + lane * 8, f);
 #pragma unroll
-                for (int x = 0; x < 8; ++x) s[x] += f[x];
+                for (int j = 0; j < kEmbCols / 8; ++j)
+                    if (c0 + 256 * j < p.D)
+#pragma unroll
+                        for (int x = 0; x < SZ / 2; ++x)
+                            async_copy<16>(dst + (uint32_t)((256 * j + lane * 8) * SZ + 16 * x),
+                                           src + 256 * j + lane * 8 + x * (16 / SZ));
+            } else if constexpr (SZ == 4) {
+#pragma unroll
+                for (int x = 0; x < kEmbCols; ++x)
+                    if (lane + 32 * x < ncol) async_copy<4>(dst + (uint32_t)((lane + 32 * x) * 4), src + lane + 32 * x);
             } else {
-                const long long t = pick(pos, i);
-                const TY* src = dy + t * p.ld_out;
                 const uintptr_t at = reinterpret_cast<uintptr_t>(src);
-                if (!outside(at)) src = reinterpret_cast<const TY*>(piece + (at & 15u));
+                const int words = outside(at) ? 0 : (int)((at & 3u) + ncol * SZ + 3) / 4;
+                const uint32_t* word = reinterpret_cast<const uint32_t*>(at & ~(uintptr_t)3);
 #pragma unroll
-                for (int x = 0; x < 8; ++x) s[x] += to_f32<TY>(src[min(lane + 32 * x, ncol - 1)]);
+                for (int x = 0; x < kEmbCols / 2 + 1; ++x)
+                    if (lane + 32 * x < words) async_copy<4>(dst + (uint32_t)((lane + 32 * x) * 4), word + lane + 32 * x);
             }
-            if (!(end >> a & 1u)) continue;
-            if (partial) {  // (joined below)
-#pragma unroll
-                for (int x = 0; x < 8; ++x) first[x] = s[x];
-            } else if (leaves && i == e - 1) {
-                break;
-            } else {
-                emb_write<TG, VEC>(p, pick(row, i), c0, s);
-            }
-#pragma unroll
-            for (int x = 0; x < 8; ++x) s[x] = 0.f;
-            partial = false;
         }
-        __syncwarp();
-        issue(q + 2);
-    }
-    // The partial rows: of the long run that entered, of the one that leaves (unless it is the same).
-    const bool through = entered && leaves && head == tail;
+        async_commit();  // (an empty group counts too)
+    };
+    const int q0 = b & ~(B - 1);
+    issue(q0);
+    issue(q0 + B);
+    float s[kEmbCols] = {};
+    for (int q = q0; q < e; q += B) {
+        async_wait_1();
+        if (VEC == 1) __syncwarp();  // other lanes' copies are read
+        const int lo = max(q, b), hi = min(q + B, e);
 #pragma unroll 1
-    for (int i = 0; i < 2; ++i) {
-        if (i == 0 ? !entered : !leaves || through) continue;
-        if (i == 0) {
-            float x[8];
+        for (int i = lo; i < hi; ++i) {
+            const uint8_t* piece = ring + (i & (2 * B - 1)) * Ring::kPiece;
+            if constexpr (VEC == 8) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = s[k], s[k] = first[k], first[k] = x[k];
-        } else if (entered) {
+                for (int j = 0; j < kEmbCols / 8; ++j) {
+                    float f[8];
+                    load_f32<TY, 8>(reinterpret_cast<const TY*>(piece) + 256 * j + lane * 8, f);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) s[k] = first[k];
+                    for (int x = 0; x < 8; ++x) s[8 * j + x] += f[x];
+                }
+            } else {
+                const TY* src = dy + pos[i] * p.ld_out;
+                const uintptr_t at = reinterpret_cast<uintptr_t>(src);
+                if (!outside(at)) src = reinterpret_cast<const TY*>(piece + (SZ == 2 ? at & 3u : 0u));
+#pragma unroll
+                for (int x = 0; x < kEmbCols; ++x) s[x] += to_f32<TY>(src[min(lane + 32 * x, ncol - 1)]);
+            }
+            const int v = row[i];
+            if (i + 1 < e && row[i + 1] == v) continue;
+            if (partial || (leaves && i == e - 1)) {
+                float* q = p.part + ((long long)w * 2 + (partial ? 0 : 1)) * p.D;
+#pragma unroll
+                for (int j = 0; j < kEmbCols / VEC; ++j) {
+                    const int c = c0 + j * 32 * VEC;
+                    float g[VEC];
+#pragma unroll
+                    for (int x = 0; x < VEC; ++x) g[x] = s[j * VEC + x];
+                    if (c < p.D) store_f32<float, VEC>(q + c, g);
+                }
+                // (The run's first entry: those of its row in this window are its first ones.)
+                if (!partial && tile == 0 && lane == 0) {
+                    int first = i;
+                    while (first > 0 && row[first - 1] == v) --first;
+                    p.cross[atomicAdd(&p.meta[1], 1)] = make_int4(v, e0 + first, ntail, 0);
+                }
+            } else {
+                emb_write<TG, VEC>(p, v, c0, s);
+            }
+            partial = false;
+#pragma unroll
+            for (int x = 0; x < kEmbCols; ++x) s[x] = 0.f;
         }
-        emb_join<TG, VEC>(p, i == 0 ? head : tail, w, tile, s);
+        if (VEC == 1) __syncwarp();
+        issue(q + 2 * B);
+    }
+}
+
+// The partial rows of a long run, in the windows' order: sixteen warps a
+// contiguous range each, then the sixteen sums.
+constexpr int kEmbJoinWarps = 16;
+
+template <typename TG>
+__global__ void __launch_bounds__(32 * kEmbJoinWarps) emb_join_kernel(const __grid_constant__ EmbParams p)
+{
+    __shared__ float sums[kEmbJoinWarps][256];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int runs = p.meta[1], tiles = (p.D + 255) / 256;
+    for (long long item = blockIdx.x; item < (long long)runs * tiles; item += gridDim.x) {
+        const int4 run = p.cross[item / tiles];
+        const int tile = (int)(item % tiles), c0 = tile * 256 + lane;
+        const int a = run.y / p.W, b = (run.y + run.z - 1) / p.W;
+        const int per = (b - a + kEmbJoinWarps) / kEmbJoinWarps;
+        const int w0 = a + warp * per, w1 = min(b + 1, w0 + per);
+        float s[8] = {};
+#pragma unroll 4
+        for (int w = w0; w < w1; ++w) {
+            const float* q = p.part + ((long long)w * 2 + (w == a ? 1 : 0)) * p.D;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s[k] += q[min(c0 + 32 * k, p.D - 1)];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sums[warp][lane + 32 * k] = s[k];
+        __syncthreads();
+        const int c = tile * 256 + (int)threadIdx.x;
+        if (threadIdx.x < 256 && c < p.D) {
+            float t = 0.f;
+#pragma unroll
+            for (int w = 0; w < kEmbJoinWarps; ++w) t += sums[w][threadIdx.x];
+            TG* out = static_cast<TG*>(p.out) + run.x * p.ld_table + c;
+            t *= p.scale;
+            if (p.accumulate) t += to_f32<TG>(*out);
+            *out = from_f32<TG>(t);
+        }
+        __syncthreads();
     }
 }
 

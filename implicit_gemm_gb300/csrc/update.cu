@@ -453,9 +453,7 @@ struct EmbPlan {
     int R;              // table rows of a CTA of the sort
     int W, tiles;       // entries of a window, column tiles
     long long windows;  // windows of the sorted list
-    int level[8];       // first partial row of each level of the tree of long runs
-    long long nodes;    // partial rows of all levels
-    size_t off_meta, off_count, off_start, off_list, off_row, off_part, off_arrived, bytes;
+    size_t off_meta, off_count, off_list, off_row, off_cross, off_part, bytes;
 };
 
 int emb_plan(const wg_embedding_problem* p, EmbPlan* pl)
@@ -484,25 +482,13 @@ int emb_plan(const wg_embedding_problem* p, EmbPlan* pl)
     pl->windows = (q.tokens + pl->W - 1) / pl->W;
     if (pl->windows * pl->tiles > 0x7fffffffLL)
         return set_err(WG_ERR_NOT_SUPPORTED, "more tokens by columns than one launch covers");
-    pl->nodes = 0;
-    memset(pl->level, 0, sizeof pl->level);
-    long long n = pl->windows;
-    for (int l = 0; l < 8; ++l) {
-        pl->level[l] = (int)pl->nodes;
-        pl->nodes += n;
-        if (n <= 1) break;
-        n = (n + wg::kEmbFan - 1) / wg::kEmbFan;
-    }
-    if (pl->nodes * 2 * pl->tiles > 0x7fffffffLL)
-        return set_err(WG_ERR_NOT_SUPPORTED, "more tokens by columns than one launch covers");
     size_t o = 0;
     pl->off_meta = o, o += 256;
     pl->off_count = o, o += up256((size_t)q.vocab * 4);
-    pl->off_start = o, o += up256((size_t)q.vocab * 4);
     pl->off_list = o, o += up256((size_t)q.tokens * 4);
     pl->off_row = o, o += up256((size_t)q.tokens * 4);
-    pl->off_part = o, o += up256((size_t)pl->nodes * 2 * q.dim * 4);
-    pl->off_arrived = o, o += up256((size_t)pl->nodes * 2 * pl->tiles * 4);
+    pl->off_cross = o, o += up256((size_t)pl->windows * 16);
+    pl->off_part = o, o += up256((size_t)pl->windows * 2 * q.dim * 4);
     pl->bytes = o;
     return WG_OK;
 }
@@ -554,8 +540,13 @@ int emb_bwd_v(const EmbPlan& pl, const wg::EmbParams& p, cudaStream_t s)
     const int warps = items < 16LL * num_sms() ? 2 : 8;
     const int ring = warps * wg::EmbRing<TY, V>::kBytes;
     if ((st = wg::ensure_smem(wg::emb_reduce_kernel<TG, TY, V>, ring))) return st;
-    return launch("emb_reduce_kernel launch", wg::emb_reduce_kernel<TG, TY, V>, dim3((unsigned)((items + warps - 1) / warps)),
-                  dim3(32 * warps), ring, s, p);
+    st = launch("emb_reduce_kernel launch", wg::emb_reduce_kernel<TG, TY, V>, dim3((unsigned)((items + warps - 1) / warps)),
+                dim3(32 * warps), ring, s, p);
+    // (A run of over 2 W entries needs as many tokens.)
+    if (!st && p.T > 2 * p.W)
+        st = launch("emb_join_kernel launch", wg::emb_join_kernel<TG>,
+                    dim3((unsigned)std::min<long long>(2 * items, 4LL * num_sms())), dim3(32 * wg::kEmbJoinWarps), 0, s, p);
+    return st;
 }
 
 template <typename TG, typename TY>
@@ -684,12 +675,9 @@ int wg_embedding_bwd_weight(const wg_embedding_problem* p, const void* token, co
     const long long per = (pl.p.tokens + 1023) / 1024 * 32;
     e.keep = (int)std::max(32LL, std::min<long long>((wg::kEmbSortMaxSmem / 4 / wg::kEmbSortWarps) - pl.R, per / 4 + 64));
     e.R = pl.R, e.W = pl.W, e.tiles = pl.tiles;
-    memcpy(e.level, pl.level, sizeof e.level);
-    e.narrived = (int)(pl.nodes * 2 * pl.tiles);
     e.meta = reinterpret_cast<int*>(ws + pl.off_meta), e.count = reinterpret_cast<int*>(ws + pl.off_count);
-    e.start = reinterpret_cast<int*>(ws + pl.off_start);
     e.list = reinterpret_cast<int*>(ws + pl.off_list), e.row = reinterpret_cast<int*>(ws + pl.off_row);
-    e.part = reinterpret_cast<float*>(ws + pl.off_part), e.arrived = reinterpret_cast<int*>(ws + pl.off_arrived);
+    e.cross = reinterpret_cast<int4*>(ws + pl.off_cross), e.part = reinterpret_cast<float*>(ws + pl.off_part);
     return with_types(pl.p.table_dtype, pl.p.out_dtype, BwdCall{pl, e, static_cast<cudaStream_t>(stream)});
 }
 

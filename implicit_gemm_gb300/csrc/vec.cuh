@@ -8,6 +8,11 @@
 namespace wg {
 
 template <typename T>
+constexpr bool is_half = false;
+template <>
+constexpr bool is_half<__half> = true;
+
+template <typename T>
 __device__ __forceinline__ float to_f32(T v);
 template <>
 __device__ __forceinline__ float to_f32<float>(float v) { return v; }
@@ -35,6 +40,22 @@ struct alignas((V * sizeof(T)) > 16 ? 16 : V * sizeof(T)) Vec {
 template <typename T, int V>
 __device__ __forceinline__ void load_f32(const T* p, float (&f)[V])
 {
+    if constexpr (V == 8 && sizeof(T) == 2) {
+        // Two elements per word: the halves of a bf16 word are fp32 values but for a shift or a mask.
+        const uint4 x = *reinterpret_cast<const uint4*>(p);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (!is_half<T>) {
+                f[2 * i] = __uint_as_float(w[i] << 16);
+                f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            } else {
+                const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                f[2 * i] = h.x, f[2 * i + 1] = h.y;
+            }
+        }
+        return;
+    }
     const Vec<T, V> x = *reinterpret_cast<const Vec<T, V>*>(p);
 #pragma unroll
     for (int i = 0; i < V; ++i) f[i] = to_f32<T>(x.v[i]);
