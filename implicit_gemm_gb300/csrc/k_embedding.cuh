@@ -446,9 +446,9 @@ __global__ void __launch_bounds__(256, 3) emb_reduce_kernel(const __grid_constan
     }
 }
 
-// The partial rows of a long run, in the windows' order: sixteen warps a
-// contiguous range each, then the sixteen sums.
-constexpr int kEmbJoinWarps = 16;
+// The partial rows of a long run, in the windows' order: eight warps a
+// contiguous range each, then the eight sums.
+constexpr int kEmbJoinWarps = 8;
 
 template <typename TG>
 __global__ void __launch_bounds__(32 * kEmbJoinWarps) emb_join_kernel(const __grid_constant__ EmbParams p)
