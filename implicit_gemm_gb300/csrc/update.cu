@@ -349,10 +349,13 @@ int muon_product(const MuonPlan& pl, const wg::MuonParams& p, wg::MuonProduct& g
     g.pairs = pl.pairs;
     // The tiles' width, whether a symmetric product takes only the tiles on and
     // below the diagonal, and the parts that the leftover tiles are cut into, by
-    // the time of the longest pair in us: a 64-long block of sums takes 0.33 for
-    // 256 columns (the rate of cuBLAS) and 0.18 for 128 (0.27 when all pairs are
-    // busy: their operands are twice the bytes per MMA); a tile's mirror image 1;
-    // parts that meet in memory 6 and 2.5 each.
+    // the time of the longest pair in us, as measured: a 64-long block of sums takes
+    // 0.33 for 256 columns (the rate of cuBLAS) and 0.22 for 128 (0.27 when all pairs
+    // are busy: their operands are twice the bytes per MMA); a tile's mirror image 1;
+    // parts that meet in memory 2, and 3 (256 columns) or 1.3 each (the Gram matrix of
+    // 512 x 32000: 142 us whole, 52 in eight parts).  Beside whole waves of tiles the others are not cut: their parts'
+    // way through memory is slow beside the tiles' operands (8 of 1024 x 1024: 349 us
+    // whole, 583 in four parts).
     const int tm = (g.M + 255) / 256, sym = g.sym;
     double best = 1e30;
     int bn = 256, parts = 1;
@@ -361,10 +364,10 @@ int muon_product(const MuonPlan& pl, const wg::MuonParams& p, wg::MuonProduct& g
             const int tn = (g.N * w + 255) / 256;
             const long long per = half ? (long long)w * (tm * (tm + 1) / 2) - (w * tm - tn) : (long long)tm * tn;
             const long long tiles = p.batch * per, full = tiles / g.pairs, rest = tiles % g.pairs;
-            const double unit = w == 1 ? 0.33 : full ? 0.27 : 0.18;
-            for (int n = 1; n <= 8; ++n) {
+            const double unit = w == 1 ? 0.33 : full ? 0.27 : 0.22;
+            for (int n = 1; n <= 16; ++n) {
                 if (n > 1 && (rest == 0 || rest * n > g.pairs || g.kb < 4 * n || full)) continue;
-                const double t = (full + (rest ? 1.0 / n : 0.0)) * g.kb * unit + half + (n > 1 ? 6 + 2.5 * n : 0);
+                const double t = (full + (rest ? 1.0 / n : 0.0)) * g.kb * unit + half + (n > 1 ? 2 + (w == 1 ? 3.0 : 1.3) * n : 0);
                 if (t < best) best = t, bn = 256 / w, parts = n, g.sym = half, g.per = (int)per, g.tn = tn;
             }
         }
