@@ -97,7 +97,10 @@ __device__ __forceinline__ void emb_zero_row(T* row, int n, int lane)
     const int body = (n - head) * (int)sizeof(T) / 16, tail = head + body * (16 / (int)sizeof(T));
     if (lane < head) row[lane] = from_f32<T>(0.f);
     uint4* q = reinterpret_cast<uint4*>(row + head);
-    for (int i = lane; i < body; i += 32) q[i] = make_uint4(0u, 0u, 0u, 0u);
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    int i = lane;
+    for (; i + 96 < body; i += 128) __stcs(q + i, zero), __stcs(q + i + 32, zero), __stcs(q + i + 64, zero), __stcs(q + i + 96, zero);
+    for (; i < body; i += 32) __stcs(q + i, zero);
     if (tail + lane < n) row[tail + lane] = from_f32<T>(0.f);
 }
 
@@ -485,6 +488,167 @@ __global__ void __launch_bounds__(32 * kEmbJoinWarps) emb_join_kernel(const __gr
             *out = from_f32<TG>(t);
         }
         __syncthreads();
+    }
+}
+
+// The whole gradient in one kernel, for few tokens: every CTA finds the positions of
+// its table rows (every G-th one: the grid then writes the table from its beginning
+// to its end) and sums them itself.  A warp takes a row
+// by 256 columns (zeros, or a run of at most 32), a run that is longer all warps of
+// the CTA, a contiguous range each.  One launch instead of three that wait for one
+// another (512 tokens of an 8192 x 512 table: 14 us before), at the price of one SM
+// reading all rows of a frequent token.
+constexpr int kEmbSmallThreads = 512, kEmbSmallWarps = kEmbSmallThreads / 32;
+constexpr int kEmbSmallMaxRows = 2048, kEmbSmallTokens = 1024;
+
+template <typename TG, typename TY, int VEC>
+__global__ void __launch_bounds__(kEmbSmallThreads, 2) emb_small_kernel(const __grid_constant__ EmbParams p)
+{
+    constexpr int NV = 8 / VEC, AHEAD = 4;
+    extern __shared__ int small_smem[];
+    __shared__ float part[kEmbSmallWarps][256];
+    __shared__ int wsum[kEmbSmallWarps];
+    const int T = (int)p.T, R = p.R, G = gridDim.x, nr = (p.V - (int)blockIdx.x + G - 1) / G;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int *count = small_smem, *next = count + R, *match_t = next + R, *match_r = match_t + T, *sorted = match_r + T;
+    pdl_launch_dependents();
+    for (int i = threadIdx.x; i < R; i += kEmbSmallThreads) count[i] = 0;
+    __syncthreads();
+    pdl_wait();
+    // The positions of this range's tokens, in order: counted per warp, then written.
+    const int per = (T + 32 * kEmbSmallWarps - 1) / (32 * kEmbSmallWarps) * 32;
+    const int t0 = min(T, warp * per), t1 = min(T, t0 + per);
+    int mine = 0;
+    for (int t = t0; t < t1; t += 32) {
+        const int v = t + lane < t1 ? emb_token(p, t + lane) : -2;
+        const bool in = v >= 0 && v != p.padding && v % G == (int)blockIdx.x;
+        if (in) atomicAdd(&count[v / G], 1);
+        mine += __popc(__ballot_sync(0xffffffffu, in));
+        if (blockIdx.x == 0 && v == -1) atomicOr(&g_status, kStatusBadToken);
+    }
+    if (lane == 0) wsum[warp] = mine;
+    __syncthreads();
+    int at = 0, total = 0;
+    for (int w = 0; w < kEmbSmallWarps; ++w) {
+        at += w < warp ? wsum[w] : 0;
+        total += wsum[w];
+    }
+    for (int t = t0; t < t1 && mine; t += 32) {
+        const int v = t + lane < t1 ? emb_token(p, t + lane) : -2;
+        const bool in = v >= 0 && v != p.padding && v % G == (int)blockIdx.x;
+        const unsigned who = __ballot_sync(0xffffffffu, in);
+        if (in) {
+            const int k = at + __popc(who & ((1u << lane) - 1u));
+            match_t[k] = t + lane, match_r[k] = v / G;
+        }
+        at += __popc(who);
+    }
+    __syncthreads();
+    if (warp == 0 && total > 0) {
+        // Where each row's positions begin, then the positions: equal rows of 32 take consecutive places.
+        int base = 0;
+        for (int r = 0; r < nr; r += 32) {
+            const int n = r + lane < nr ? count[r + lane] : 0;
+            int x = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            if (r + lane < nr) next[r + lane] = base + x - n;
+            base += __shfl_sync(0xffffffffu, x, 31);
+        }
+        __syncwarp();
+        for (int i = 0; i < total; i += 32) {
+            const bool in = i + lane < total;
+            const unsigned who = __ballot_sync(0xffffffffu, in);
+            if (in) {
+                const int r = match_r[i + lane];
+                const unsigned same = __match_any_sync(who, r);
+                const int rank = __popc(same & ((1u << lane) - 1u));
+                sorted[next[r] + rank] = match_t[i + lane];
+                __syncwarp(who);
+                if (rank == 0) next[r] += __popc(same);
+            }
+            __syncwarp();
+        }
+    }
+    const int tiles = (p.D + 255) / 256;
+    const TY* dy = static_cast<const TY*>(p.in);
+    // Entries a .. b - 1 of `sorted`, this lane's columns of a tile.
+    auto sum = [&](int a, int b, int c0, float (&s)[8]) {
+        int col[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) col[j] = min(c0 + j * 32 * VEC, p.D - VEC);  // columns past the row read its last ones
+        for (int i = a; i < b; i += AHEAD) {
+            Vec<TY, VEC> f[AHEAD][NV];
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                const long long t = sorted[min(i + k, b - 1)];
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+                    f[k][j] = *reinterpret_cast<const Vec<TY, VEC>*>(dy + t * p.ld_out + col[j]);
+            }
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k)
+                if (i + k < b)
+#pragma unroll
+                    for (int j = 0; j < NV; ++j)
+#pragma unroll
+                        for (int q = 0; q < VEC; ++q) s[j * VEC + q] += to_f32<TY>(f[k][j].v[q]);
+        }
+    };
+    auto write = [&](int r, int c0, const float (&s)[8]) {
+        TG* out = static_cast<TG*>(p.out) + ((long long)r * G + blockIdx.x) * p.ld_table;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = c0 + j * 32 * VEC;
+            if (c >= p.D) continue;
+            float f[VEC];
+            if (p.accumulate) load_f32<TG, VEC>(out + c, f);
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) f[k] = p.accumulate ? f[k] + p.scale * s[j * VEC + k] : p.scale * s[j * VEC + k];
+            store_f32<TG, VEC>(out + c, f);
+        }
+    };
+    __syncthreads();
+    // Zeros of the rows without a token: a warp per row.
+    if (!p.accumulate)
+        for (int r = warp; r < nr; r += kEmbSmallWarps)
+            if (!count[r]) emb_zero_row(static_cast<TG*>(p.out) + ((long long)r * G + blockIdx.x) * p.ld_table, p.D, lane);
+    if (total == 0) return;
+    // (next[r] is now the end of row r's positions.)
+    for (int i = warp; i < nr * tiles; i += kEmbSmallWarps) {
+        const int r = i / tiles, n = count[r], c0 = i % tiles * 256 + lane * VEC;
+        if (n == 0 || n > 32) continue;
+        float s[8] = {};
+        sum(next[r] - n, next[r], c0, s);
+        write(r, c0, s);
+    }
+    for (int r = 0; r < nr; ++r) {
+        const int n = count[r];
+        if (n <= 32) continue;
+        const int each = (n + kEmbSmallWarps - 1) / kEmbSmallWarps, a = next[r] - n;
+        for (int tile = 0; tile < tiles; ++tile) {
+            const int c0 = tile * 256 + lane * VEC;
+            float s[8] = {};
+            sum(a + min(n, warp * each), a + min(n, (warp + 1) * each), c0, s);
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int q = 0; q < VEC; ++q) part[warp][lane * VEC + j * 32 * VEC + q] = s[j * VEC + q];
+            __syncthreads();
+            if (warp == 0) {
+                float u[8] = {};
+                for (int w = 0; w < kEmbSmallWarps; ++w)
+#pragma unroll
+                    for (int j = 0; j < NV; ++j)
+#pragma unroll
+                        for (int q = 0; q < VEC; ++q) u[j * VEC + q] += part[w][lane * VEC + j * 32 * VEC + q];
+                write(r, c0, u);
+            }
+            __syncthreads();
+        }
     }
 }
 

@@ -453,7 +453,8 @@ int muon_run(const MuonPlan& pl, const void* grad, void* momentum, void* weight,
 // ---------------------------------------------------------------- embedding
 struct EmbPlan {
     wg_embedding_problem p;
-    int R;              // table rows of a CTA of the sort
+    bool small;         // the one-kernel form
+    int R;              // table rows of a CTA (of the sort)
     int W, tiles;       // entries of a window, column tiles
     long long windows;  // windows of the sorted list
     size_t off_meta, off_count, off_list, off_row, off_cross, off_part, bytes;
@@ -477,8 +478,16 @@ int emb_plan(const wg_embedding_problem* p, EmbPlan* pl)
     if (q.ld_out == 0) q.ld_out = q.dim;
     if (q.ld_table < q.dim || q.ld_out < q.dim)
         return set_err(WG_ERR_INVALID_ARGUMENT, "ld_table and ld_out must be 0 or at least dim");
-    // One CTA of the sort per SM, unless its counters would not fit.
-    pl->R = std::min((q.vocab + num_sms() - 1) / num_sms(), wg::kEmbSortMaxRows);
+    // Few tokens of a small table take one kernel: 512 tokens of 8192 x 512 in fp32 9 us
+    // against 14 in three, 1000 of 8192 x 1024 in bf16 14 against 15; 100 of 16384 x 1024
+    // 14 both ways, 64 of 32768 x 1024 24 against 17 (the SMs that have matches to place
+    // fall behind those that write zeros).
+    pl->small = q.tokens <= wg::kEmbSmallTokens && q.tokens * q.dim * esize(q.out_dtype) <= (2 << 20) &&
+                (long long)q.vocab * q.dim * esize(q.table_dtype) <= (16 << 20);
+    // One CTA of the sort per SM, unless its counters would not fit (two of the one-kernel form's).
+    const int per_sm = pl->small ? 2 : 1;
+    pl->R = std::min((q.vocab + per_sm * num_sms() - 1) / (per_sm * num_sms()),
+                     pl->small ? wg::kEmbSmallMaxRows : wg::kEmbSortMaxRows);
     // Windows of 32 entries, or of 16 or 8 while those make fewer than 16 warps per SM.
     pl->tiles = (q.dim + wg::kEmbTile - 1) / wg::kEmbTile;
     for (pl->W = 32; pl->W > 8 && q.tokens / pl->W * pl->tiles < 16LL * num_sms();) pl->W /= 2;
@@ -532,6 +541,13 @@ int emb_lookup_t(const EmbPlan& pl, const wg::EmbParams& p, cudaStream_t s)
 template <typename TG, typename TY, int V>
 int emb_bwd_v(const EmbPlan& pl, const wg::EmbParams& p, cudaStream_t s)
 {
+    if (pl.small) {
+        const int smem = (2 * pl.R + 3 * (int)p.T) * 4;
+        const int st = wg::ensure_smem(wg::emb_small_kernel<TG, TY, V>, smem);
+        return st ? st
+                  : launch("emb_small_kernel launch", wg::emb_small_kernel<TG, TY, V>, dim3((p.V + pl.R - 1) / pl.R),
+                           dim3(wg::kEmbSmallThreads), smem, s, p);
+    }
     const int smem = wg::kEmbSortWarps * (pl.R + p.keep) * 4;
     int st = wg::ensure_smem(wg::emb_sort_kernel<TG>, smem);
     if (!st)
