@@ -21,10 +21,11 @@
 // cannot reach the others of its block.
 //
 // A cluster of C CTAs takes a block.  Each adds up U U^T over its 64-column
-// chunks of the long side (the momentum's step on the way); the C partial sums
-// are added slice by slice through distributed shared memory into rank 0, which
-// alone runs the steps; Q goes through the workspace, and every CTA multiplies
-// its chunks of U, which it reads again (L2), and writes its part of the results.
+// chunks of the long side (the momentum's step on the way); each adds a slice of
+// the C partial sums through distributed shared memory and gives it to all; all
+// run the same steps (one that ran them for the others would have to hand Q out,
+// 2 us later); and each multiplies its chunks of U, which it reads again (L2), and
+// writes its part of the results.
 // Bound by latency: three dependent products a step, each MMA -> tensor memory ->
 // registers -> shared memory.  One warp does nothing but issue MMAs, so that A P
 // is on its way through the other sixteen while P Q runs.
@@ -57,8 +58,6 @@ struct GramParams {
     struct Step {
         float pa, pb, pc, rs, rq, ra, sa, sp, ss, sq;
     } step[kGramMaxSteps];
-    uint8_t* q;      // [blocks][P == 64 ? 16 : 64 KB] operand image of Q, bf16 pairs
-    float* factor;   // [blocks][128] scale / (|u|_F + eps) per row of a block
 };
 
 __host__ __device__ constexpr int gram_mat_bytes(int P) { return P * P * 2; }  // one fp16 image
@@ -244,7 +243,7 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bar[3];
     __shared__ uint32_t tslot;
-    __shared__ float diag[128], fac[128];
+    __shared__ float diag[128], norm2[64], fac[128];  // of A_0; |u|_F^2 per matrix; scale / (|u|_F + eps) per row
     __shared__ int bad[128];
     uint8_t* smem = align_shared<uint8_t>(smem_raw, 1024);
     uint8_t *ba = smem, *bp = smem + PAIR, *bq = smem + 2 * PAIR;  // A (and A P), P, Q
@@ -382,9 +381,9 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
     }
     cluster_sync_all();
     if (!issuer) {
-        // Rows rank * P / C .. of the sum over the cluster, into rank 0's Q.
+        // Rows rank * P / C .. of the sum over the cluster, into every CTA's Q.
         const int pieces = P * P / 2 / g.C;  // 8-byte pieces of a slice
-        const uint32_t src = smem_u32(bp), dst = mapa_shared(smem_u32(bq), 0u);
+        const uint32_t src = smem_u32(bp), dst = smem_u32(bq);
         for (int i = tid; i < pieces; i += kGramThreads) {
             const uint32_t o = (uint32_t)(rank * pieces + i) << 3;
             float2 s = make_float2(0.f, 0.f);
@@ -398,14 +397,14 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
                 for (int c = 0; c < 8; ++c)
                     if (c0 + c < g.C) s.x += x[c].x, s.y += x[c].y;
             }
-            st_dsmem_v2(dst + o, s);
+            for (int c = 0; c < g.C; ++c) st_dsmem_v2(mapa_shared(dst + o, (uint32_t)c), s);
         }
     }
     cluster_sync_all();
 
-    // ---------------------------------------------------- the steps, on rank 0
-    uint8_t* qimg = g.q + (size_t)blk * PAIR;
-    if (rank == 0 && issuer) {
+    // ---------------------------------------------------- the steps
+    GramRaw u[P / 64];
+    if (issuer) {
         const uint32_t sba = smem_u32(ba), sbp = smem_u32(bp), sbq = smem_u32(bq);
         __syncthreads();  // the diagonal
         __syncthreads();  // and its sums
@@ -441,17 +440,16 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
             }
             __syncwarp();
         }
-    } else if (rank == 0) {
+    } else {
         float v[NC];
+        if (tid < P)
+            diag[tid] = *reinterpret_cast<const float*>(bq + tid * (P * 4) + ((((tid >> 2) ^ (tid & 7)) << 4) | (tid & 3) << 2));
         if (act) {
 #pragma unroll
             for (int i = 0; i < NC; i += 4) {
                 const float4 x = *reinterpret_cast<const float4*>(bq + row * (P * 4) + (((((c0 + i) >> 2)) ^ (row & 7)) << 4));
                 v[i] = x.x, v[i + 1] = x.y, v[i + 2] = x.z, v[i + 3] = x.w;
             }
-#pragma unroll
-            for (int i = 0; i < NC; ++i)
-                if (c0 + i == row) diag[row] = v[i];
         }
         __syncthreads();
         for (int f = warp; f < g.F; f += kGramThreads / 32) {  // |u|_F^2 is the trace: a warp per matrix
@@ -459,16 +457,16 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
             for (int i = lane; i < p.m; i += 32) s += diag[f * p.m + i];
 #pragma unroll
             for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            if (lane == 0) fac[f] = s;
+            if (lane == 0) norm2[f] = s;
         }
         __syncthreads();
         if (act) {
             // A_0 = U U^T / (|u|_F + eps)^2, zero between matrices.
-            const float s = mine < g.F ? fac[mine] : 0.f;
+            const float s = mine < g.F ? norm2[mine] : 0.f;
             const float d = sqrtf(s) + p.eps;
             const bool fin = s < INFINITY;
             const float inv = fin && d > 0.f ? 1.f / d : 0.f;
-            if (c0 == 0) g.factor[blk * 128 + row] = fin ? p.scale * inv : NAN;
+            if (c0 == 0) fac[row] = fin ? p.scale * inv : NAN;
 #pragma unroll
             for (int i = 0; i < NC; ++i) v[i] = fin && (own >> i & 1u) ? v[i] * inv * inv : 0.f;
 #pragma unroll
@@ -526,10 +524,9 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
                 if (act) convert(TA, w.ra, ba, g.step[k + 1].sa);
             }
         }
+        // The first chunk of U comes back; Q (v) becomes a pair of bf16 operand images.
+        load(rank, std::false_type{}, u);
         if (act) {
-            // Q (v) as a pair of bf16 operand images, for every CTA of the cluster: through
-            // shared memory, so that it goes out in whole lines (row by row from the lanes it
-            // took 3 us).
 #pragma unroll
             for (int i = 0; i < NC; i += 8) {
                 uint4 h, l;
@@ -539,32 +536,10 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
                 *reinterpret_cast<uint4*>(o + MAT) = l;
             }
         }
-        if (g.C > 1) {
-            named_bar_sync(1, kGramThreads);
-#pragma unroll
-            for (int i = 0; i < PAIR / 16 / kGramThreads; ++i) {
-                const int e = i * kGramThreads + tid;
-                __stcg(reinterpret_cast<uint4*>(qimg) + e, reinterpret_cast<const uint4*>(bq)[e]);
-            }
-            __threadfence();
-        }
     }
-    // The first chunk of U comes back while Q is on its way.
-    GramRaw u[P / 64];
-    if (!issuer) load(rank, std::false_type{}, u);
-    cluster_sync_all();
 
     // ---------------------------------------------------- results: X = Q U over this CTA's chunks
     if (!issuer) {
-        if (rank != 0) {
-            uint4 x[PAIR / 16 / kGramThreads];
-#pragma unroll
-            for (int i = 0; i < PAIR / 16 / kGramThreads; ++i)
-                x[i] = __ldcg(reinterpret_cast<const uint4*>(qimg) + i * kGramThreads + tid);
-#pragma unroll
-            for (int i = 0; i < PAIR / 16 / kGramThreads; ++i) reinterpret_cast<uint4*>(bq)[i * kGramThreads + tid] = x[i];
-        }
-        if (tid < P) fac[tid] = __ldcg(g.factor + blk * 128 + tid);
         const int q0 = (warp >> 2) * 16;
         // A chunk is staged and its MMAs begin before the results of the one before it are written.
         auto begin = [&](int it) {

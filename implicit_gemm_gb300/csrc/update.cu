@@ -79,7 +79,6 @@ struct MuonPlan {
     wg::GramParams g;     // its problem (pointers are set by the call)
     int P, blocks;        // rows of a block of the Gram matrix, blocks
     int ldx, m, ldm, nparts;
-    size_t off_q, off_factor;
     int pairs;
     size_t off_x[2], off_xlo, off_a, off_b, off_part, off_sums, off_arrived, bytes;
 };
@@ -219,9 +218,7 @@ int make_muon_plan(const wg_muon_problem* p, MuonPlan* pl)
     pl->gram = q.steps > 0 && pl->m <= 128;
     if (pl->gram) {
         muon_gram_plan(pl);
-        pl->off_q = o, o += up256((size_t)pl->blocks * 2 * wg::gram_mat_bytes(pl->P));
-        pl->off_factor = o, o += up256((size_t)pl->blocks * 128 * 4);
-        pl->bytes = o;
+        pl->bytes = o = 256;  // (no kernel of this form needs any; callers need no case for that)
         return WG_OK;
     }
     const size_t x = up256((size_t)q.batch * q.rows * pl->ldx * 2), a = up256((size_t)q.batch * pl->m * pl->ldm * 2);
@@ -396,7 +393,6 @@ int muon_run(const MuonPlan& pl, const void* grad, void* momentum, void* weight,
         g.vec = al && aligned16(grad) && aligned16(momentum);
         g.ovec = al && aligned16(weight) && aligned16(out);
         g.split = momentum || q.grad_dtype != WG_BF16;
-        g.q = reinterpret_cast<uint8_t*>(ws + pl.off_q), g.factor = reinterpret_cast<float*>(ws + pl.off_factor);
         return pl.P == 64 ? muon_gram_launch<64>(pl, g, s) : muon_gram_launch<128>(pl, g, s);
     }
     p.part = reinterpret_cast<float*>(ws + pl.off_part), p.nparts = pl.nparts;
