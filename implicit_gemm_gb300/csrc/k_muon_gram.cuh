@@ -191,15 +191,15 @@ __device__ __forceinline__ long long gram_at(const GramParams& g, int blk, int c
     return (long long)b * p.bs + (g.wide ? idx * p.ld + n : n * p.ld + idx);
 }
 
-// STEP: the momentum's step is taken and written; otherwise it has been.
+// STEP: the momentum's step is taken and written; otherwise it has been.  e: the
+// address when eight elements are read at once (-1: outside).
 template <bool STEP>
-__device__ __forceinline__ void gram_read(const GramParams& g, int blk, int ch, int line, int seg, GramRaw& r)
+__device__ __forceinline__ void gram_read(const GramParams& g, int blk, int ch, int line, int seg, long long e, GramRaw& r)
 {
     const MuonParams& p = g.p;
     const uint4 z = make_uint4(0u, 0u, 0u, 0u);
     r.g.a = r.g.b = r.m.a = r.m.b = z;
     if (g.vec) {
-        const long long e = gram_at(g, blk, ch, line, seg, 0);
         if (e < 0) return;
         r.g = muon_raw8(p.grad, p.grad_dtype, e);
         if (p.mom) r.m = muon_raw8(p.mom, 2, e);
@@ -217,8 +217,7 @@ __device__ __forceinline__ void gram_read(const GramParams& g, int blk, int ch, 
 }
 
 template <bool STEP>
-__device__ __forceinline__ void gram_make(const GramParams& g, int blk, int ch, int line, int seg, const GramRaw& r,
-                                          float (&u)[8])
+__device__ __forceinline__ void gram_make(const GramParams& g, long long e, const GramRaw& r, float (&u)[8])
 {
     const MuonParams& p = g.p;
     muon_unraw8(g.vec ? p.grad_dtype : 2, r.g, u);
@@ -226,10 +225,7 @@ __device__ __forceinline__ void gram_make(const GramParams& g, int blk, int ch, 
     float m[8];
     muon_unraw8(2, r.m, m);
     muon_make<8, STEP>(p, u, m);
-    if (STEP) {
-        const long long e = gram_at(g, blk, ch, line, seg, 0);
-        if (e >= 0) store_f32<float, 8>(p.mom + e, m);
-    }
+    if (STEP && e >= 0) store_f32<float, 8>(p.mom + e, m);
 }
 
 template <int P>
@@ -295,18 +291,38 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
     // Two staged images (pairs), in A's place.  Wide: rows of the block, 64
     // positions along; tall: 64 positions, the block's rows along, in 64-wide atoms.
     const int line = tid >> 3, seg = (tid & 7) * 8;
+    // Where this thread's eight elements of chunk 0 lie (-1: no matrix there), and of chunk ch.
+    long long at0[P / 64];
+#pragma unroll
+    for (int j = 0; j < P / 64; ++j) {
+        const int i = (g.wide ? line : seg) + 64 * j, f = i / p.m, b = blk * g.F + f, idx = i - f * p.m;
+        at0[j] = f >= g.F || b >= p.batch ? -1 : (long long)b * p.bs + (g.wide ? idx * p.ld + seg : line * p.ld + idx);
+    }
+    auto addr = [&](int ch, int j) -> long long {
+        if (at0[j] < 0 || ch * 64 + (g.wide ? seg : line) >= g.N) return -1;
+        return at0[j] + ch * (g.wide ? 64 : 64 * p.ld);
+    };
     auto stage = [&](uint8_t* img, int ch, auto step, const GramRaw (&u)[P / 64]) {
 #pragma unroll
         for (int j = 0; j < P / 64; ++j) {
             float v[8];
-            gram_make<decltype(step)::value>(g, blk, ch, g.wide ? line + 64 * j : line, g.wide ? seg : seg + 64 * j, u[j], v);
+            gram_make<decltype(step)::value>(g, addr(ch, j), u[j], v);
+            float odd = 0.f;  // NaN when one of them is a NaN or an infinity
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                if (!(fabsf(v[k]) < INFINITY)) {
-                    v[k] = 0.f;
-                    bad[(g.wide ? line + 64 * j : seg + 64 * j + k)] = 1;
+            for (int k = 0; k < 8; ++k) odd = fmaf(v[k], 0.f, odd);
+            if (odd != 0.f)
+#pragma unroll 1
+                for (int k = 0; k < 8; ++k) {
+                    float x = 0.f;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        if (q == k) x = v[q];
+                    if (fabsf(x) < INFINITY) continue;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        if (q == k) v[q] = 0.f;
+                    bad[g.wide ? line + 64 * j : seg + 64 * j + k] = 1;
                 }
-            }
             uint4 h, l;
             split8<true>(v, &h, &l);
             uint8_t* o = img + j * 8192 + line * 128 + ((((tid & 7) ^ (line & 7))) << 4);
@@ -318,7 +334,7 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
         if (ch >= g.chunks) return;
 #pragma unroll
         for (int j = 0; j < P / 64; ++j)
-            gram_read<decltype(step)::value>(g, blk, ch, g.wide ? line + 64 * j : line, g.wide ? seg : seg + 64 * j, u[j]);
+            gram_read<decltype(step)::value>(g, blk, ch, g.wide ? line + 64 * j : line, g.wide ? seg : seg + 64 * j, addr(ch, j), u[j]);
     };
     const int nch = (g.chunks - rank + g.C - 1) / g.C;  // this CTA's chunks: rank, rank + C, ...
     if (!issuer) {
