@@ -218,7 +218,7 @@ int make_muon_plan(const wg_muon_problem* p, MuonPlan* pl)
     pl->gram = q.steps > 0 && pl->m <= 128;
     if (pl->gram) {
         muon_gram_plan(pl);
-        pl->bytes = o = 256;  // (no kernel of this form needs any; callers need no case for that)
+        pl->bytes = 256;  // nothing is kept there; callers need no case for a form without a workspace
         return WG_OK;
     }
     const size_t x = up256((size_t)q.batch * q.rows * pl->ldx * 2), a = up256((size_t)q.batch * pl->m * pl->ldm * 2);
@@ -272,7 +272,7 @@ int muon_gram_launch(const MuonPlan& pl, const wg::GramParams& g, cudaStream_t s
     const int smem = wg::gram_smem_bytes(P);
     const int st = wg::ensure_smem(wg::muon_gram_kernel<P>, smem);
     if (st) return st;
-    if (g.C > 8) {
+    if (g.C > 8) {  // beyond the portable cluster size
         const cudaError_t e = cudaFuncSetAttribute(wg::muon_gram_kernel<P>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute", e);
     }
@@ -459,8 +459,8 @@ struct EmbPlan {
 int emb_plan(const wg_embedding_problem* p, EmbPlan* pl)
 {
     if (!p) return set_err(WG_ERR_INVALID_ARGUMENT, "problem is NULL");
-    if (p->tokens < 0 || p->tokens > 0x7fffffffLL || p->vocab < 1 || p->dim < 1)
-        return set_err(WG_ERR_INVALID_ARGUMENT, "tokens must be in 0..2^31-1, vocab and dim at least 1");
+    if (p->tokens < 0 || p->tokens > 0x7fffff00LL || p->vocab < 1 || p->dim < 1)
+        return set_err(WG_ERR_INVALID_ARGUMENT, "tokens must be in 0..2^31-256, vocab and dim at least 1");
     if (!dtype_ok(p->table_dtype) || !dtype_ok(p->out_dtype))
         return set_err(WG_ERR_INVALID_ARGUMENT, "table_dtype and out_dtype must be WG_FP32, WG_BF16 or WG_FP16");
     if (p->token_bits != 32 && p->token_bits != 64)

@@ -388,7 +388,7 @@ WG_API int wg_muon_update(const wg_muon_problem* p, const void* grad, void* mome
  * A token outside [0, vocab) looks up zeros and adds to no row; wg_check_status
  * then returns WG_ERR_INVALID_TOKEN.
  *
- *  tokens in 0..2^31-1 (0: a lookup does nothing, a gradient is zero), vocab and
+ *  tokens in 0..2^31-256 (0: a lookup does nothing, a gradient is zero), vocab and
  *  dim >= 1.
  *  ld_table, ld_out: elements between rows of table / dtable and of out / dy;
  *    0 = dim.  Elements between rows are neither read nor written.
