@@ -451,34 +451,35 @@ __global__ void __launch_bounds__(256, 3) emb_reduce_kernel(const __grid_constan
 
 // The partial rows of a long run, in the windows' order: eight warps a
 // contiguous range each, then the eight sums.
-constexpr int kEmbJoinWarps = 8;
+constexpr int kEmbJoinWarps = 8, kEmbJoinCols = 128;
 
 template <typename TG>
 __global__ void __launch_bounds__(32 * kEmbJoinWarps) emb_join_kernel(const __grid_constant__ EmbParams p)
 {
-    __shared__ float sums[kEmbJoinWarps][256];
+    constexpr int NK = kEmbJoinCols / 32;
+    __shared__ float sums[kEmbJoinWarps][kEmbJoinCols];
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int runs = p.meta[1], tiles = (p.D + 255) / 256;
+    const int runs = p.meta[1], tiles = (p.D + kEmbJoinCols - 1) / kEmbJoinCols;
     for (long long item = blockIdx.x; item < (long long)runs * tiles; item += gridDim.x) {
         const int4 run = p.cross[item / tiles];
-        const int tile = (int)(item % tiles), c0 = tile * 256 + lane;
+        const int tile = (int)(item % tiles), c0 = tile * kEmbJoinCols + lane;
         const int a = run.y / p.W, b = (run.y + run.z - 1) / p.W;
         const int per = (b - a + kEmbJoinWarps) / kEmbJoinWarps;
         const int w0 = a + warp * per, w1 = min(b + 1, w0 + per);
-        float s[8] = {};
-#pragma unroll 4
+        float s[NK] = {};
+#pragma unroll 8
         for (int w = w0; w < w1; ++w) {
             const float* q = p.part + ((long long)w * 2 + (w == a ? 1 : 0)) * p.D;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) s[k] += q[min(c0 + 32 * k, p.D - 1)];
+            for (int k = 0; k < NK; ++k) s[k] += q[min(c0 + 32 * k, p.D - 1)];
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) sums[warp][lane + 32 * k] = s[k];
+        for (int k = 0; k < NK; ++k) sums[warp][lane + 32 * k] = s[k];
         __syncthreads();
-        const int c = tile * 256 + (int)threadIdx.x;
-        if (threadIdx.x < 256 && c < p.D) {
+        const int c = tile * kEmbJoinCols + (int)threadIdx.x;
+        if (threadIdx.x < kEmbJoinCols && c < p.D) {
             float t = 0.f;
 #pragma unroll
             for (int w = 0; w < kEmbJoinWarps; ++w) t += sums[w][threadIdx.x];

@@ -560,7 +560,7 @@ int emb_bwd_v(const EmbPlan& pl, const wg::EmbParams& p, cudaStream_t s)
     // (A run of over 2 W entries needs as many tokens.)
     if (!st && p.T > 2 * p.W)
         st = launch("emb_join_kernel launch", wg::emb_join_kernel<TG>,
-                    dim3((unsigned)std::min<long long>(2 * items, 4LL * num_sms())), dim3(32 * wg::kEmbJoinWarps), 0, s, p);
+                    dim3((unsigned)std::min<long long>(4 * items, 8LL * num_sms())), dim3(32 * wg::kEmbJoinWarps), 0, s, p);
     return st;
 }
 
