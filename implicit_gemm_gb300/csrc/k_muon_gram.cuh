@@ -191,6 +191,20 @@ __device__ __forceinline__ long long gram_at(const GramParams& g, int blk, int c
     return (long long)b * p.bs + (g.wide ? idx * p.ld + n : n * p.ld + idx);
 }
 
+// Eight elements one by one.  (A call of its own: inlined at every load, the code of
+// this path and the like came to 600 KB, and the kernel waited for instructions.)
+template <bool STEP>
+__device__ __noinline__ void gram_read_each(const GramParams& g, int blk, int ch, int line, int seg, uint32_t* w)
+{
+#pragma unroll 1
+    for (int k = 0; k < 8; ++k) {
+        const long long e = gram_at(g, blk, ch, line, seg, k);
+        float x[1] = {0.f};
+        if (e >= 0) muon_u<1, STEP>(g.p, e, x);
+        w[k] = __float_as_uint(x[0]);
+    }
+}
+
 // STEP: the momentum's step is taken and written; otherwise it has been.  e: the
 // address when eight elements are read at once (-1: outside).
 template <bool STEP>
@@ -206,13 +220,7 @@ __device__ __forceinline__ void gram_read(const GramParams& g, int blk, int ch, 
         return;
     }
     uint32_t w[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const long long e = gram_at(g, blk, ch, line, seg, k);
-        float x[1] = {0.f};
-        if (e >= 0) muon_u<1, STEP>(p, e, x);
-        w[k] = __float_as_uint(x[0]);
-    }
+    gram_read_each<STEP>(g, blk, ch, line, seg, w);
     r.g.a = make_uint4(w[0], w[1], w[2], w[3]), r.g.b = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
@@ -226,6 +234,25 @@ __device__ __forceinline__ void gram_make(const GramParams& g, long long e, cons
     muon_unraw8(2, r.m, m);
     muon_make<8, STEP>(p, u, m);
     if (STEP && e >= 0) store_f32<float, 8>(p.mom + e, m);
+}
+
+// n <= 16 results, `step` elements apart: all loads, then all stores.
+template <typename T>
+__device__ __forceinline__ void gram_put_each(T* out, long long step, int n, const float (&o)[16])
+{
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (i < n) out[i * step] = from_f32<T>(o[i]);
+}
+template <typename T>
+__device__ __forceinline__ void gram_weight_each(const MuonParams& p, T* w, long long step, int n, const float (&o)[16])
+{
+    T x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = i < n ? w[i * step] : T();
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (i < n) w[i * step] = from_f32<T>(fmaf(p.keep, to_f32<T>(x[i]), -p.lr * o[i]));
 }
 
 template <int P>
@@ -250,7 +277,8 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
     // This thread's part of a Gram-sized matrix: row, first column, and which of
     // its columns are of the row's own matrix.
     const int row = (warp & 3) * 32 + lane, c0 = (warp >> 2) * NC;
-    const bool act = row < P && !issuer;
+    // Rows and columns past the matrices are left as they are: nothing reads their products.
+    const bool rows = !issuer && (warp & 3) * 32 < 16 * g.kn, act = rows && c0 < 16 * g.kn;
     const int mine = row / p.m, lo = mine * p.m, hi = mine < g.F ? lo + p.m : lo;
     uint32_t own = 0;
 #pragma unroll
@@ -340,17 +368,14 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
     if (!issuer) {
         // Two chunks ahead of the one that is staged.
         GramRaw u0[P / 64], u1[P / 64];
-        load(rank, std::true_type{}, u0);
-        load(rank + g.C, std::true_type{}, u1);
-        auto chunk = [&](int it, GramRaw (&u)[P / 64]) {
+#pragma unroll 1
+        for (int it = -2; it < nch; ++it) {
             if (it >= 2) wait(it & 1);
-            stage(ba + (it & 1) * 2 * IMG, rank + it * g.C, std::true_type{}, u);
-            load(rank + (it + 2) * g.C, std::true_type{}, u);
-            ready();
-        };
-        for (int it = 0; it < nch; it += 2) {
-            chunk(it, u0);
-            if (it + 1 < nch) chunk(it + 1, u1);
+            if (it >= 0) stage(ba + (it & 1) * 2 * IMG, rank + it * g.C, std::true_type{}, u0);
+#pragma unroll
+            for (int j = 0; j < P / 64; ++j) u0[j] = u1[j];
+            load(rank + (it + 2) * g.C, std::true_type{}, u1);
+            if (it >= 0) ready();
         }
         if (nch >= 2) wait(nch & 1);
         if (nch >= 1) wait((nch - 1) & 1);
@@ -397,8 +422,8 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
     }
     cluster_sync_all();
     if (!issuer) {
-        // Rows rank * P / C .. of the sum over the cluster, into every CTA's Q.
-        const int pieces = P * P / 2 / g.C;  // 8-byte pieces of a slice
+        // A slice of the sum over the cluster, into every CTA's Q.
+        const int pieces = 16 * g.kn * P / 2 / g.C;  // 8-byte pieces of a slice
         const uint32_t src = smem_u32(bp), dst = smem_u32(bq);
         for (int i = tid; i < pieces; i += kGramThreads) {
             const uint32_t o = (uint32_t)(rank * pieces + i) << 3;
@@ -558,29 +583,27 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
     if (!issuer) {
         const int q0 = (warp >> 2) * 16;
         // A chunk is staged and its MMAs begin before the results of the one before it are written.
-        auto begin = [&](int it) {
-            if (it >= nch) return;
-            const int ch = rank + it * g.C;
-            // (The MMAs that read this image two chunks ago are done: their sums have been read.)
-            stage((it & 1 ? bp : ba), ch, std::false_type{}, u);
-            load(ch + g.C, std::false_type{}, u);
-            ready();
-        };
-        begin(0);
-        for (int it = 0; it < nch; ++it) {
+#pragma unroll 1
+        for (int it = -1; it < nch; ++it) {
             const int ch = rank + it * g.C;
             const int b0 = blk * g.F + mine;
-            const bool mat = act && mine < g.F && b0 < p.batch;
+            const bool mat = rows && mine < g.F && b0 < p.batch;
             MuonRaw8 old[2] = {};
-            if (g.wide && g.ovec && p.weight && mat) {
+            if (it >= 0 && g.wide && g.ovec && p.weight && mat) {
                 const long long e = (long long)b0 * p.bs + (row - lo) * p.ld + ch * 64 + q0;
                 if (ch * 64 + q0 < g.N) old[0] = muon_raw8(p.weight, p.weight_dtype, e);
                 if (ch * 64 + q0 + 8 < g.N) old[1] = muon_raw8(p.weight, p.weight_dtype, e + 8);
             }
-            begin(it + 1);
+            if (it + 1 < nch) {
+                // (The MMAs that read this image two chunks ago are done: their sums have been read.)
+                stage((it & 1 ? ba : bp), ch + g.C, std::false_type{}, u);
+                load(ch + 2 * g.C, std::false_type{}, u);
+                ready();
+            }
+            if (it < 0) continue;
             wait(it & 1);
             float x[16];
-            if (act) gram_ld<16>(tb + ((uint32_t)((warp & 3) * 32) << 16) + (it & 1 ? T2 : TA) + (uint32_t)q0, x);
+            if (rows) gram_ld<16>(tb + ((uint32_t)((warp & 3) * 32) << 16) + (it & 1 ? T2 : TA) + (uint32_t)q0, x);
             if (mat) {
                 const float f = fac[row];
                 const long long base = (long long)b0 * p.bs;
@@ -597,17 +620,23 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
                     const long long e0 = base + (g.wide ? (row - lo) * p.ld + n0 : n0 * p.ld + (row - lo));
                     const long long step = g.wide ? 1 : p.ld;
                     const int n = min(16, g.N - n0);
-                    float w[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        w[i] = p.weight && i < n ? muon_load(p.weight, p.weight_dtype, e0 + i * step) : 0.f;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        if (i >= n) break;
-                        const float o = f * x[i];
-                        if (p.out) muon_store(p.out, p.out_dtype, e0 + i * step, o);
-                        if (p.weight)
-                            muon_store(p.weight, p.weight_dtype, e0 + i * step, fmaf(p.keep, w[i], -p.lr * o));
+                    for (int i = 0; i < 16; ++i) x[i] *= f;
+                    if (p.out) {
+                        if (p.out_dtype == 2)
+                            gram_put_each(static_cast<float*>(p.out) + e0, step, n, x);
+                        else if (p.out_dtype == 0)
+                            gram_put_each(static_cast<__nv_bfloat16*>(p.out) + e0, step, n, x);
+                        else
+                            gram_put_each(static_cast<__half*>(p.out) + e0, step, n, x);
+                    }
+                    if (p.weight) {
+                        if (p.weight_dtype == 2)
+                            gram_weight_each(p, static_cast<float*>(p.weight) + e0, step, n, x);
+                        else if (p.weight_dtype == 0)
+                            gram_weight_each(p, static_cast<__nv_bfloat16*>(p.weight) + e0, step, n, x);
+                        else
+                            gram_weight_each(p, static_cast<__half*>(p.weight) + e0, step, n, x);
                     }
                 }
             }
