@@ -366,15 +366,16 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
     };
     const int nch = (g.chunks - rank + g.C - 1) / g.C;  // this CTA's chunks: rank, rank + C, ...
     if (!issuer) {
-        // Two chunks ahead of the one that is staged.
-        GramRaw u0[P / 64], u1[P / 64];
+        // Chunks on their way ahead of the one that is staged: two, or one where two are too many registers.
+        constexpr int AHEAD = P == 64 ? 2 : 1;
+        GramRaw u[AHEAD][P / 64];
 #pragma unroll 1
-        for (int it = -2; it < nch; ++it) {
+        for (int it = -AHEAD; it < nch; ++it) {
             if (it >= 2) wait(it & 1);
-            if (it >= 0) stage(ba + (it & 1) * 2 * IMG, rank + it * g.C, std::true_type{}, u0);
+            if (it >= 0) stage(ba + (it & 1) * 2 * IMG, rank + it * g.C, std::true_type{}, u[0]);
 #pragma unroll
-            for (int j = 0; j < P / 64; ++j) u0[j] = u1[j];
-            load(rank + (it + 2) * g.C, std::true_type{}, u1);
+            for (int j = 0; j < P / 64; ++j) u[0][j] = u[AHEAD - 1][j];
+            load(rank + (it + AHEAD) * g.C, std::true_type{}, u[AHEAD - 1]);
             if (it >= 0) ready();
         }
         if (nch >= 2) wait(nch & 1);
