@@ -409,17 +409,17 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
     // the row); NaN on the diagonal of a row that held a NaN or an infinity.
     __syncthreads();
     if (act) {
-        float v[NC];
-        gram_ld<NC>(trow + TA, v);
+#pragma unroll 1
+        for (int h = 0; h < NC; h += 16) {
+            float v[16];
+            gram_ld<16>(trow + TA + h, v);
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            if (nch <= 0) v[i] = 0.f;
-            if (c0 + i == row && bad[row]) v[i] = NAN;
+            for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<float4*>(bp + row * (P * 4) + (((((c0 + h + i) >> 2)) ^ (row & 7)) << 4)) =
+                    nch > 0 ? make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-#pragma unroll
-        for (int i = 0; i < NC; i += 4)
-            *reinterpret_cast<float4*>(bp + row * (P * 4) + (((((c0 + i) >> 2)) ^ (row & 7)) << 4)) =
-                make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        if (row >= c0 && row < c0 + NC && bad[row])
+            *reinterpret_cast<float*>(bp + row * (P * 4) + ((((row >> 2) ^ (row & 7)) << 4) | (row & 3) << 2)) = NAN;
     }
     cluster_sync_all();
     if (!issuer) {
@@ -483,16 +483,8 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
             __syncwarp();
         }
     } else {
-        float v[NC];
         if (tid < P)
             diag[tid] = *reinterpret_cast<const float*>(bq + tid * (P * 4) + ((((tid >> 2) ^ (tid & 7)) << 4) | (tid & 3) << 2));
-        if (act) {
-#pragma unroll
-            for (int i = 0; i < NC; i += 4) {
-                const float4 x = *reinterpret_cast<const float4*>(bq + row * (P * 4) + (((((c0 + i) >> 2)) ^ (row & 7)) << 4));
-                v[i] = x.x, v[i + 1] = x.y, v[i + 2] = x.z, v[i + 3] = x.w;
-            }
-        }
         __syncthreads();
         for (int f = warp; f < g.F; f += kGramThreads / 32) {  // |u|_F^2 is the trace: a warp per matrix
             float s = 0.f;
@@ -509,26 +501,45 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
             const bool fin = s < INFINITY;
             const float inv = fin && d > 0.f ? 1.f / d : 0.f;
             if (c0 == 0) fac[row] = fin ? p.scale * inv : NAN;
+#pragma unroll 1
+            for (int h = 0; h < NC; h += 16) {
+                float v[16];
 #pragma unroll
-            for (int i = 0; i < NC; ++i) v[i] = fin && (own >> i & 1u) ? v[i] * inv * inv : 0.f;
+                for (int i = 0; i < 16; i += 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(bq + row * (P * 4) +
+                                                                      (((((c0 + h + i) >> 2)) ^ (row & 7)) << 4));
+                    v[i] = x.x, v[i + 1] = x.y, v[i + 2] = x.z, v[i + 3] = x.w;
+                }
 #pragma unroll
-            for (int i = 0; i < NC; i += 16) tmem_st16(trow + TA + i, v + i);
-            gram_put<P, NC>(ba, row, c0, v, g.step[0].sa);
+                for (int i = 0; i < 16; ++i) v[i] = fin && (own >> (h + i) & 1u) ? v[i] * inv * inv : 0.f;
+                tmem_st16(trow + TA + h, v);
+                gram_put<P, 16>(ba, row, c0 + h, v, g.step[0].sa);
+            }
             if (P == 64) {
-                float z[NC] = {};
-#pragma unroll
-                for (int i = 0; i < NC; i += 16) tmem_st16(trow + TA + 64 + i, z + i);
+                const float z[16] = {};
+                tmem_st16(trow + TA + 64, z);
             }
         }
-        // v = f (sums at t), times s into the pair at img.  (What A_0 has zero between
-        // matrices stays zero: every product adds zeros there.)
-        auto convert = [&](uint32_t t, float f, uint8_t* img, float s) {
-            gram_sums<P, NC>(trow + t, v);
-            if (img) {
-                gram_put<P, NC>(img, row, c0, v, f * s);
-            } else {
+        // f times the sums at t into the pair at img, sixteen columns at a time (all 32 of a
+        // block of 128 at once are more than the registers hold).  What A_0 has zero between
+        // matrices stays zero: every product adds zeros there.
+        auto convert = [&](uint32_t t, float f, uint8_t* img) {
+#pragma unroll 1
+            for (int h = 0; h < NC; h += 16) {
+                float v[16];
+                gram_sums<P, 16>(trow + t + h, v);
+                gram_put<P, 16>(img, row, c0 + h, v, f);
+            }
+        };
+        // Q as a pair of bf16 images, in Q's place.
+        auto put_q = [&](int h, const float (&v)[16]) {
 #pragma unroll
-                for (int i = 0; i < NC; ++i) v[i] *= f;
+            for (int i = 0; i < 16; i += 8) {
+                uint4 hi8, lo8;
+                split8<true>(v + i, &hi8, &lo8);
+                uint8_t* o = bq + gram_off<P>(row, (c0 + h + i) >> 3);
+                *reinterpret_cast<uint4*>(o) = hi8;
+                *reinterpret_cast<uint4*>(o + MAT) = lo8;
             }
         };
         const uint32_t diagonal = row >= c0 && row < c0 + NC ? 1u << (row - c0) : 0u;
@@ -539,43 +550,50 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
             wait(0);
             if (act) {
                 // P = a I + b A + c A A
-                float x[NC];
-                gram_sums<P, NC>(trow + T2, v);
-                gram_sums<P, NC>(trow + TA, x);
+#pragma unroll 1
+                for (int h = 0; h < NC; h += 16) {
+                    float v[16], x[16];
+                    gram_sums<P, 16>(trow + T2 + h, v);
+                    gram_sums<P, 16>(trow + TA + h, x);
 #pragma unroll
-                for (int i = 0; i < NC; ++i) {
-                    v[i] = fmaf(w.pc, v[i], w.pb * x[i]);
-                    if (diagonal >> i & 1u) v[i] += w.pa;
+                    for (int i = 0; i < 16; ++i) {
+                        v[i] = fmaf(w.pc, v[i], w.pb * x[i]);
+                        if (diagonal >> (h + i) & 1u) v[i] += w.pa;
+                    }
+                    if (last && k == 0) {
+                        put_q(h, v);
+                        continue;
+                    }
+                    gram_put<P, 16>(bp, row, c0 + h, v, w.sp);
+                    if (k == 0) gram_put<P, 16>(bq, row, c0 + h, v, w.sq);
                 }
-                gram_put<P, NC>(bp, row, c0, v, w.sp);
-                if (k == 0 && !last) gram_put<P, NC>(bq, row, c0, v, w.sq);
             }
             if (last && k == 0) break;
             ready();
             if (!last) {
                 wait(0);
-                if (act) convert(T2, w.rs, ba, w.ss);  // S = A P, in A's place
+                if (act) convert(T2, w.rs * w.ss, ba);  // S = A P, in A's place
                 ready();
             }
             if (k > 0) {
                 wait(1);
-                if (act) convert(TQ, w.rq, last ? nullptr : bq, w.sq);
+                if (act && !last) convert(TQ, w.rq * w.sq, bq);
             }
             if (!last) {
                 wait(2);
-                if (act) convert(TA, w.ra, ba, g.step[k + 1].sa);
+                if (act) convert(TA, w.ra * g.step[k + 1].sa, ba);
             }
         }
-        // The first chunk of U comes back; Q (v) becomes a pair of bf16 operand images.
-        load(rank, std::false_type{}, u);
-        if (act) {
+        load(rank, std::false_type{}, u);  // the first chunk of U comes back
+        if (act && g.steps > 1) {
+            const float f = g.step[g.steps - 1].rq;
+#pragma unroll 1
+            for (int h = 0; h < NC; h += 16) {
+                float v[16];
+                gram_sums<P, 16>(trow + TQ + h, v);
 #pragma unroll
-            for (int i = 0; i < NC; i += 8) {
-                uint4 h, l;
-                split8<true>(v + i, &h, &l);
-                uint8_t* o = bq + gram_off<P>(row, (c0 + i) >> 3);
-                *reinterpret_cast<uint4*>(o) = h;
-                *reinterpret_cast<uint4*>(o + MAT) = l;
+                for (int i = 0; i < 16; ++i) v[i] *= f;
+                put_q(h, v);
             }
         }
     }
