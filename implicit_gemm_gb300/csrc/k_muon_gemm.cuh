@@ -321,14 +321,16 @@ __global__ void __launch_bounds__(kMgThreads, 1)
         fence_mbar_init();
     }
     if (warp == 1) {
-        pdl_wait();  // tensor memory may still be held by the kernel before this one
+        // (Waits while another kernel's CTA on this SM holds tensor memory; that one does
+        // not wait for this grid.)
         tmem_alloc_pair(tslot, Mg<BN>::kTmem);
         tc_fence_before();
     }
     cluster_sync_all();  // both CTAs' barriers are initialised and both hold tensor memory
     tc_fence_after();
     const uint32_t tbase = *tslot;
-    pdl_wait();
+    // (All of the above runs beside the end of the kernel before this one, which the
+    // loads of this one wait for.)
 
     if (warp == 0) {
         if (lane == 0) {
@@ -337,7 +339,10 @@ __global__ void __launch_bounds__(kMgThreads, 1)
             uint32_t ph = 0;
             bool ok = true;
             MgPiece w;
-            for (MgWalk walk(g, pair); ok && walk.next(g, w);) {
+            MgWalk walk(g, pair);
+            bool more = walk.next(g, w);
+            pdl_wait();
+            for (; ok && more; more = walk.next(g, w)) {
                 const MgTile t = mg_tile<BN>(g, w.t);
                 const int m0 = t.m + rank * 128, n0 = t.n + rank * (BN / 2);
                 for (int k = w.k0; k < w.k1; ++k) {
@@ -413,6 +418,7 @@ __global__ void __launch_bounds__(kMgThreads, 1)
         const size_t mine = (size_t)rank * BN * 128 + (size_t)col * 128 + row;
         MgPiece w;
         MgWalk walk(g, pair);
+        pdl_wait();
         for (int i = 0; walk.next(g, w); ++i) {
             const int buf = i & 1;
             const MgTile t = mg_tile<BN>(g, w.t);
