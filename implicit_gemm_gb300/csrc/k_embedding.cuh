@@ -289,9 +289,9 @@ __device__ __forceinline__ void emb_write(const EmbParams& p, int v, int c0, con
 // waiting for memory two thirds of the time: 94 us for 65,536 rows of 2,048), and
 // with aligned rows every lane reads back what it copied itself, so nothing waits
 // for another lane.  (Bulk copies, one per row and lane, took the kernel three times
-// the instructions.)  16-bit rows that start at odd elements are copied in the 4-byte
-// words that hold them, unless such a word lies outside dy: then the warp loads the
-// row when it needs it.
+// the instructions.)  Rows that start anywhere are copied in the aligned 16-byte
+// chunks that hold them (16,001 rows of 999: 19 us, 30 in 4-byte words), unless such a
+// chunk lies partly outside dy: then the warp loads the row when it needs it.
 template <typename TY, int VEC>
 struct EmbRing {
     static constexpr int kPiece = kEmbTile * (int)sizeof(TY) + (VEC == 1 ? 16 : 0);
@@ -300,13 +300,9 @@ struct EmbRing {
     static constexpr int kBytes = kEntries + 96 * 8;
 };
 
-template <int BYTES>
 __device__ __forceinline__ void async_copy(uint32_t dst, const void* src)
 {
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // All but the last group of this thread's copies are there.
@@ -359,8 +355,8 @@ __global__ void __launch_bounds__(256, 3) emb_reduce_kernel(const __grid_constan
     const TY* dy = static_cast<const TY*>(p.in) + col0;
     const uintptr_t dy0 = reinterpret_cast<uintptr_t>(p.in);
     const uintptr_t dy1 = dy0 + (uintptr_t)((p.T - 1) * p.ld_out + p.D) * SZ;
-    auto outside = [&](uintptr_t a) {  // the words that hold the piece at a are not all in dy
-        return VEC == 1 && SZ == 2 && ((a & ~(uintptr_t)3) < dy0 || ((a + ncol * SZ + 3) & ~(uintptr_t)3) > dy1);
+    auto outside = [&](uintptr_t a) {  // the chunks that hold the piece at a are not all in dy
+        return VEC == 1 && ((a & ~(uintptr_t)15) < dy0 || ((a + ncol * SZ + 15) & ~(uintptr_t)15) > dy1);
     };
     const uint32_t ring0 = smem_u32(ring);
     // Entries i0 .. i0 + B - 1 (batches are aligned to the window).
@@ -376,19 +372,15 @@ __global__ void __launch_bounds__(256, 3) emb_reduce_kernel(const __grid_constan
                     if (c0 + 256 * j < p.D)
 #pragma unroll
                         for (int x = 0; x < SZ / 2; ++x)
-                            async_copy<16>(dst + (uint32_t)((256 * j + lane * 8) * SZ + 16 * x),
-                                           src + 256 * j + lane * 8 + x * (16 / SZ));
-            } else if constexpr (SZ == 4) {
-#pragma unroll
-                for (int x = 0; x < kEmbCols; ++x)
-                    if (lane + 32 * x < ncol) async_copy<4>(dst + (uint32_t)((lane + 32 * x) * 4), src + lane + 32 * x);
+                            async_copy(dst + (uint32_t)((256 * j + lane * 8) * SZ + 16 * x),
+                                       src + 256 * j + lane * 8 + x * (16 / SZ));
             } else {
                 const uintptr_t at = reinterpret_cast<uintptr_t>(src);
-                const int words = outside(at) ? 0 : (int)((at & 3u) + ncol * SZ + 3) / 4;
-                const uint32_t* word = reinterpret_cast<const uint32_t*>(at & ~(uintptr_t)3);
+                const int chunks = outside(at) ? 0 : (int)((at & 15u) + ncol * SZ + 15) / 16;
+                const uint4* chunk = reinterpret_cast<const uint4*>(at & ~(uintptr_t)15);
 #pragma unroll
-                for (int x = 0; x < kEmbCols / 2 + 1; ++x)
-                    if (lane + 32 * x < words) async_copy<4>(dst + (uint32_t)((lane + 32 * x) * 4), word + lane + 32 * x);
+                for (int x = 0; x < Ring::kPiece / 512 + 1; ++x)
+                    if (lane + 32 * x < chunks) async_copy(dst + (uint32_t)((lane + 32 * x) * 16), chunk + lane + 32 * x);
             }
         }
         async_commit();  // (an empty group counts too)
@@ -415,7 +407,7 @@ __global__ void __launch_bounds__(256, 3) emb_reduce_kernel(const __grid_constan
             } else {
                 const TY* src = dy + pos[i] * p.ld_out;
                 const uintptr_t at = reinterpret_cast<uintptr_t>(src);
-                if (!outside(at)) src = reinterpret_cast<const TY*>(piece + (SZ == 2 ? at & 3u : 0u));
+                if (!outside(at)) src = reinterpret_cast<const TY*>(piece + (at & 15u));
 #pragma unroll
                 for (int x = 0; x < kEmbCols; ++x) s[x] += to_f32<TY>(src[min(lane + 32 * x, ncol - 1)]);
             }
