@@ -438,24 +438,54 @@ def _on(stream, *tensors):
         t.record_stream(s)
 
 
-def _packed(**tensors):
+def _expect(name, t, dtype: str, shape=None, elements: int = 0) -> None:
+    """Refuse a tensor that is not what the call will take it for: of `dtype`, contiguous and of `shape`, or (no shape)
+    with `elements` elements from its first one on."""
+    if t is None:
+        return
+    names = {"torch.float32": "fp32", "torch.bfloat16": "bf16", "torch.float16": "fp16"}
+    if names.get(str(t.dtype)) != dtype:
+        raise ValueError(f"{name} is {t.dtype}, not {dtype}")
+    if shape is None:
+        if t.untyped_storage().nbytes() // t.element_size() - t.storage_offset() < elements:
+            raise ValueError(f"{name} holds fewer than {elements} elements")
+    elif tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    elif not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _on_gpu(**tensors) -> None:
     for name, t in tensors.items():
-        if t is not None and not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+        if t is not None and not t.is_cuda:
+            raise ValueError(f"{name} is not a CUDA tensor")
 
 
 def muon_update(spec: dict, grad, momentum=None, weight=None, out=None, stream=None):
-    """Convenience wrapper over wg_muon_update for torch CUDA tensors: allocates the workspace, and `out`
-    (grad's shape) when no weight is given, then calls the library.  Returns out, or the weight."""
+    """Convenience wrapper over wg_muon_update for torch CUDA tensors: allocates the workspace, and `out` (grad's
+    shape; with ld or batch_stride a (batch, rows, cols) view of that layout) when no weight is given, then calls the
+    library.  Returns out, or the weight.  Tensors of another type or size than the spec's are refused."""
     import torch
-    if out is None and weight is None:
-        tdt = {"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16}[spec.get("out_dtype", "bf16")]
-        out = torch.empty_like(grad, dtype=tdt)
-    if not (spec.get("ld", 0) or spec.get("batch_stride", 0)):
-        _packed(grad=grad, momentum=momentum, weight=weight, out=out)
-    nbytes = wg_muon_workspace_size(spec)
+    nbytes = wg_muon_workspace_size(spec)  # (checks the spec)
+    b, rows, cols, ld, bs = (spec.get(k, 0) for k in ("batch", "rows", "cols", "ld", "batch_stride"))
+    b, ld = b or 1, ld or cols
+    span = (b - 1) * (bs or rows * ld) + (rows - 1) * ld + cols
+    made = out is None and weight is None
+    types = {"grad": spec.get("grad_dtype", "fp32"), "momentum": "fp32", "weight": spec.get("weight_dtype", "bf16"),
+             "out": spec.get("out_dtype", "bf16")}
+    for name, t in (("grad", grad), ("momentum", momentum), ("weight", weight), ("out", out)):
+        _expect(name, t, types[name], elements=span)
+        if t is not None and not (spec.get("ld", 0) or bs) and not (t.is_contiguous() and t.numel() == span):
+            raise ValueError(f"{name} must be contiguous, of batch * rows * cols elements")
+    _on_gpu(grad=grad, momentum=momentum, weight=weight, out=out)
+    if made:
+        tdt = {"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16}[types["out"]]
+        if spec.get("ld", 0) or bs:
+            out = torch.empty(span, dtype=tdt, device=grad.device).as_strided((b, rows, cols), (bs or rows * ld, ld, 1))
+        else:
+            out = torch.empty_like(grad, dtype=tdt)
     ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=grad.device)
-    _on(stream, ws)
+    _on(stream, ws, *([out] if made else []))
     wg_muon_update(spec, grad, momentum, weight, out, ws, nbytes, stream)
     return out if out is not None else weight
 
@@ -529,19 +559,30 @@ class PreparedEmbeddingBwd:
 
 def _embedding_spec(token, vocab, dim, table_dtype, out_dtype, scale, padding_token):
     names = {"torch.float32": "fp32", "torch.bfloat16": "bf16", "torch.float16": "fp16"}
+    tokens = {"torch.int32": "i32", "torch.int64": "i64"}
+    if str(token.dtype) not in tokens or not token.is_contiguous():
+        raise ValueError("token must be a contiguous int32 or int64 tensor")
+    for t in (table_dtype, out_dtype):
+        if str(t) not in names:
+            raise ValueError(f"{t} is not supported")
     return {"tokens": token.numel(), "vocab": vocab, "dim": dim, "table_dtype": names[str(table_dtype)],
-            "out_dtype": names[str(out_dtype)], "token_dtype": {"torch.int32": "i32", "torch.int64": "i64"}[
-                str(token.dtype)], "scale": scale, "padding_token": padding_token}
+            "out_dtype": names[str(out_dtype)], "token_dtype": tokens[str(token.dtype)], "scale": scale,
+            "padding_token": padding_token}
 
 
 def embedding_lookup(token, table, scale: float = 1.0, out=None, stream=None):
     """Convenience wrapper over wg_embedding_lookup for torch CUDA tensors: contiguous int32 or int64 tokens of any
     shape, a contiguous (vocab, dim) table.  Returns (*token.shape, dim) in table's dtype (or `out`)."""
     import torch
-    if out is None:
-        out = torch.empty((*token.shape, table.shape[1]), dtype=table.dtype, device=table.device)
-    _packed(token=token, table=table, out=out)
-    spec = _embedding_spec(token, table.shape[0], table.shape[1], table.dtype, out.dtype, scale, -1)
+    vocab, dim = table.shape
+    made = out is None
+    spec = _embedding_spec(token, vocab, dim, table.dtype, table.dtype if made else out.dtype, scale, -1)
+    _expect("table", table, spec["table_dtype"], (vocab, dim))
+    _expect("out", out, spec["out_dtype"], (*token.shape, dim))
+    _on_gpu(token=token, table=table, out=out)
+    if made:
+        out = torch.empty((*token.shape, dim), dtype=table.dtype, device=table.device)
+        _on(stream, out)
     wg_embedding_lookup(spec, token, table, out, stream)
     return out
 
@@ -551,13 +592,17 @@ def embedding_bwd_weight(token, dy, vocab: int, scale: float = 1.0, padding_toke
     """Convenience wrapper over wg_embedding_bwd_weight for torch CUDA tensors: contiguous dy of shape
     (*token.shape, dim).  Returns the (vocab, dim) gradient in dy's dtype (or `out`, added to when accumulate)."""
     import torch
-    if out is None:
-        if accumulate:
-            raise ValueError("accumulate needs out")
-        out = torch.empty((vocab, dy.shape[-1]), dtype=dy.dtype, device=dy.device)
-    _packed(token=token, dy=dy, out=out)
-    spec = _embedding_spec(token, vocab, dy.shape[-1], out.dtype, dy.dtype, scale, padding_token)
-    nbytes = wg_embedding_workspace_size(spec)
+    made, dim = out is None, dy.shape[-1]
+    if made and accumulate:
+        raise ValueError("accumulate needs out")
+    spec = _embedding_spec(token, vocab, dim, dy.dtype if made else out.dtype, dy.dtype, scale, padding_token)
+    nbytes = wg_embedding_workspace_size(spec)  # (checks the spec)
+    _expect("dy", dy, spec["out_dtype"], (*token.shape, dim))
+    _expect("out", out, spec["table_dtype"], (vocab, dim))
+    _on_gpu(token=token, dy=dy, out=out)
+    if made:
+        out = torch.empty((vocab, dim), dtype=dy.dtype, device=dy.device)
+        _on(stream, out)
     ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dy.device)
     _on(stream, ws)
     wg_embedding_bwd_weight(spec, token, dy, out, accumulate, ws, nbytes, stream)

@@ -131,7 +131,7 @@ void muon_gram_plan(MuonPlan* pl)
     g.steps = q.steps;
     pl->blocks = (q.batch + g.F - 1) / g.F;
     // A CTA per chunk up to the largest cluster, while every block has its cluster at
-    // once (96 x 3456: 52 us with 16 CTAs, 61 with 8, 82 with 4).
+    // once (96 x 3456: 45 us with 16 CTAs, 57 with 8, 90 with 4).
     g.C = 1;
     const int cmax = muon_gram_max_cluster();
     while (g.C < cmax && 2 * g.C <= g.chunks && 2LL * g.C * pl->blocks <= num_sms()) g.C *= 2;
@@ -238,13 +238,15 @@ int make_muon_plan(const wg_muon_problem* p, MuonPlan* pl)
 }
 
 // Plans are a pure function of the problem, its coefficients and the SM count;
-// successful ones are cached, so that repeated calls skip the range checks.
+// successful ones are cached, so that repeated calls skip the range checks.  (Where
+// the cache cannot have memory, the plan is made anew.)
 int muon_plan(const wg_muon_problem* p, MuonPlan* pl)
 {
+    if (!p || p->steps < 0 || p->steps > kMuonMaxSteps) return make_muon_plan(p, pl);
     static std::mutex mu;
     static std::map<std::string, MuonPlan> cache;
     std::string key;
-    if (p && p->steps >= 0 && p->steps <= kMuonMaxSteps) {
+    try {
         // (The record without its pointer and its tail padding.)
         const int sms = num_sms();
         key.assign(reinterpret_cast<const char*>(p), offsetof(wg_muon_problem, coef));
@@ -252,17 +254,22 @@ int muon_plan(const wg_muon_problem* p, MuonPlan* pl)
         key.append(reinterpret_cast<const char*>(&sms), sizeof sms);
         if (p->coef) key.append(reinterpret_cast<const char*>(p->coef), (size_t)p->steps * 3 * sizeof(float));
         std::lock_guard<std::mutex> lk(mu);
-        auto it = cache.find(key);
+        const auto it = cache.find(key);
         if (it != cache.end()) {
             *pl = it->second;
             return WG_OK;
         }
+    } catch (...) {
+        return make_muon_plan(p, pl);
     }
     const int st = make_muon_plan(p, pl);
     if (st) return st;
-    std::lock_guard<std::mutex> lk(mu);
-    if (cache.size() > 1024) cache.clear();
-    cache.emplace(key, *pl);
+    try {
+        std::lock_guard<std::mutex> lk(mu);
+        if (cache.size() > 1024) cache.clear();
+        cache.emplace(std::move(key), *pl);
+    } catch (...) {
+    }
     return WG_OK;
 }
 
@@ -446,6 +453,13 @@ int muon_run(const MuonPlan& pl, const void* grad, void* momentum, void* weight,
     return WG_OK;
 }
 
+// Whether [a, a + na) and [b, b + nb) share bytes (NULL: nothing there).
+bool overlap(const void* a, long long na, const void* b, long long nb)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x && y && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
 // ---------------------------------------------------------------- embedding
 struct EmbPlan {
     wg_embedding_problem p;
@@ -511,7 +525,8 @@ wg::EmbParams emb_params(const EmbPlan& pl, const void* token, const void* in, v
     return p;
 }
 
-int emb_check(const EmbPlan& pl, const void* token, const void* table, const void* out)
+// `written`: the one of table and out that the call writes.
+int emb_check(const EmbPlan& pl, const void* token, const void* table, const void* out, const void* written)
 {
     const wg_embedding_problem& q = pl.p;
     if ((q.tokens > 0 && (!token || !out)) || !table)
@@ -519,6 +534,11 @@ int emb_check(const EmbPlan& pl, const void* token, const void* table, const voi
     if (!aligned_to(token, q.token_bits / 8) || !aligned_to(table, esize(q.table_dtype)) ||
         !aligned_to(out, esize(q.out_dtype)))
         return set_err(WG_ERR_MISALIGNED, "a pointer is not aligned to its elements");
+    if (q.tokens == 0) return WG_OK;
+    const long long nt = ((q.vocab - 1) * q.ld_table + q.dim) * esize(q.table_dtype);
+    const long long no = ((q.tokens - 1) * q.ld_out + q.dim) * esize(q.out_dtype);
+    if (overlap(table, nt, out, no) || overlap(written, written == out ? no : nt, token, q.tokens * (q.token_bits / 8)))
+        return set_err(WG_ERR_INVALID_ARGUMENT, "token, table and out (or dy and dtable) must not overlap");
     return WG_OK;
 }
 
@@ -646,11 +666,9 @@ int wg_muon_update(const wg_muon_problem* p, const void* grad, void* momentum, v
     const int es[4] = {esize(p->grad_dtype), 4, esize(p->weight_dtype), esize(p->out_dtype)};
     const long long span = (long long)(pl.p.batch - 1) * pl.p.batch_stride + (long long)(pl.p.rows - 1) * pl.p.ld + pl.p.cols;
     for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < i; ++j) {
-            const uintptr_t a = reinterpret_cast<uintptr_t>(buf[i]), b = reinterpret_cast<uintptr_t>(buf[j]);
-            if (a && b && a < b + (uintptr_t)(span * es[j]) && b < a + (uintptr_t)(span * es[i]))
+        for (int j = 0; j < i; ++j)
+            if (overlap(buf[i], span * es[i], buf[j], span * es[j]))
                 return set_err(WG_ERR_INVALID_ARGUMENT, "grad, momentum, weight and out must not overlap");
-        }
     if ((st = check_workspace(pl.bytes, workspace, ws_bytes))) return st;
     return muon_run(pl, grad, momentum, weight, out, static_cast<char*>(workspace), static_cast<cudaStream_t>(stream));
 }
@@ -660,7 +678,7 @@ int wg_embedding_lookup(const wg_embedding_problem* p, const void* token, const 
     EmbPlan pl;
     int st = emb_plan(p, &pl);
     if (st) return st;
-    if ((st = emb_check(pl, token, table, out))) return st;
+    if ((st = emb_check(pl, token, table, out, out))) return st;
     if (pl.p.tokens == 0) return WG_OK;
     const wg::EmbParams e = emb_params(pl, token, table, out);
     return with_types(pl.p.table_dtype, pl.p.out_dtype, LookupCall{pl, e, static_cast<cudaStream_t>(stream)});
@@ -681,7 +699,7 @@ int wg_embedding_bwd_weight(const wg_embedding_problem* p, const void* token, co
     EmbPlan pl;
     int st = emb_plan(p, &pl);
     if (st) return st;
-    if ((st = emb_check(pl, token, dtable, dy))) return st;
+    if ((st = emb_check(pl, token, dtable, dy, dtable))) return st;
     if ((st = check_workspace(pl.bytes, workspace, ws_bytes))) return st;
     wg::EmbParams e = emb_params(pl, token, dy, dtable);
     char* ws = static_cast<char*>(workspace);

@@ -407,7 +407,8 @@ typedef struct {
     float scale;
 } wg_embedding_problem;
 
-/* Look up `tokens` rows of `table` into `out` on `stream`.
+/* Look up `tokens` rows of `table` into `out` on `stream`.  No two of token, table
+ * and out may overlap (nor token, dy and dtable below).
  * Returns WG_OK or an error status; nothing is launched on an error. */
 WG_API int wg_embedding_lookup(const wg_embedding_problem* p, const void* token, const void* table, void* out,
                                void* stream);

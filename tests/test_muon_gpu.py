@@ -200,6 +200,15 @@ def test_steps_and_coefficients(r, c, steps):
         assert float((x @ x.mT - eye).abs().max()) < 0.02
 
 
+def test_wrapper_lays_its_result_out_like_the_gradient():
+    b, r, c, ld = 2, 24, 40, 51
+    room = torch.zeros((b, r, ld), device="cuda")
+    room[..., :c] = gradient(14, b, r, c)
+    out = binding.muon_update({"batch": b, "rows": r, "cols": c, "ld": ld}, room[..., :c])
+    assert out.shape == (b, r, c) and out.stride() == (r * ld, ld, 1)
+    close(out.contiguous(), exact_x(room[..., :c].contiguous()), "bf16")
+
+
 def test_batches_past_32_bits():
     r, c, bs = 24, 40, (1 << 31) + 24
     grad = torch.zeros(bs + r * c, dtype=torch.bfloat16, device="cuda")

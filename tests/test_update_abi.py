@@ -91,3 +91,50 @@ def test_embedding_buffer_refusals():
 
 def test_status_of_a_bad_token_has_a_name():
     assert binding.wg_status_string(7) == "WG_ERR_INVALID_TOKEN"
+
+
+def test_embedding_overlap_refusals():
+    sp, big = emb(), 1 << 30  # 56 bytes of tokens, a table of 352 bytes, out of 224
+    for args in ((8 * A, A, A + 336), (8 * A, A + 208, A), (A + 208, 8 * A, A)):
+        refused(1, binding.wg_embedding_lookup, sp, *args, stream=0)
+    for args in ((8 * A, A + 336, A), (8 * A, A, A + 208), (A + 336, 8 * A, A)):
+        refused(1, binding.wg_embedding_bwd_weight, sp, *args, workspace=4 * A, ws_bytes=big, stream=0)
+
+
+def test_wrappers_refuse_tensors_that_do_not_fit():
+    """Shapes, types and layouts are refused before anything is allocated; so are tensors in host memory."""
+    import torch
+    b16 = torch.bfloat16
+    tok, table = torch.zeros((2, 3), dtype=torch.int64), torch.zeros((11, 16), dtype=b16)
+
+    def bad(why, f, **kw):
+        with pytest.raises(ValueError, match=why):
+            f(**kw)
+
+    look, lk = binding.embedding_lookup, {"token": tok, "table": table}
+    bad("token", look, **{**lk, "token": tok.short()})
+    bad("token", look, **{**lk, "token": tok.mT})
+    bad("table must be contiguous", look, **{**lk, "table": torch.zeros((16, 11), dtype=b16).mT})
+    bad("float64", look, **{**lk, "table": table.double()})
+    bad("out has shape", look, **lk, out=torch.zeros((2, 3, 15), dtype=b16))
+    bad("out has shape", look, **lk, out=torch.zeros((3, 2, 16), dtype=b16))
+    bad("token is not a CUDA tensor", look, **lk)
+    dy = torch.zeros((2, 3, 16), dtype=b16)
+    grad, gk = binding.embedding_bwd_weight, {"token": tok, "dy": dy, "vocab": 11}
+    bad("dy has shape", grad, **{**gk, "dy": dy[:1]})
+    bad("dy must be contiguous", grad, **{**gk, "dy": torch.zeros((2, 3, 32), dtype=b16)[..., ::2]})
+    bad("accumulate needs out", grad, **gk, accumulate=True)
+    bad("out has shape", grad, **gk, out=torch.zeros((10, 16)))
+    bad("int32", grad, **gk, out=torch.zeros((11, 16), dtype=torch.int32))
+    bad("token is not a CUDA tensor", grad, **gk)
+    g, up = torch.zeros((24, 40)), binding.muon_update
+    bad("grad holds fewer", up, spec=muon(), grad=torch.zeros((23, 40)))
+    bad("grad must be contiguous", up, spec=muon(), grad=g.mT)
+    bad("grad is", up, spec=muon(), grad=g.to(b16))
+    bad("grad is", up, spec=muon(grad_dtype="bf16"), grad=g)
+    bad("momentum is", up, spec=muon(), grad=g, momentum=g.to(b16))
+    bad("weight is", up, spec=muon(), grad=g, weight=g)
+    bad("out holds fewer", up, spec=muon(), grad=g, out=torch.zeros(24 * 40 - 1, dtype=b16))
+    bad("out holds fewer", up, spec=muon(ld=48), grad=torch.zeros((24, 48))[:, :40], out=torch.zeros((24, 40), dtype=b16))
+    bad("grad holds fewer", up, spec=muon(batch=2, batch_stride=1000), grad=torch.zeros(1959))
+    bad("grad is not a CUDA tensor", up, spec=muon(), grad=g)
