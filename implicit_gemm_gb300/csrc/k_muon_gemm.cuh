@@ -39,7 +39,11 @@ template <int BN>
 struct Mg {
     static constexpr int kStageBytes = 16384 + BN * 64;
     static constexpr int kStages = BN == 256 ? 5 : 6;
-    static constexpr int kSmem = kStages * kStageBytes + kMgEpiWarps * kMgWarpStaging + 1024 + 256;
+    // All the shared memory that a CTA may have: no other kernel's CTA is beside this
+    // one, so that tensor memory can be taken before the kernel before this one has ended
+    // (a CTA of that one which has yet to take its own cannot be on this SM).
+    static constexpr int kSmem = 227 * 1024;
+    static_assert(kStages * kStageBytes + kMgEpiWarps * kMgWarpStaging + 1024 + 256 <= kSmem, "shared memory of a CTA");
     static constexpr int kTmem = 2 * BN;  // columns: the sums, twice
 };
 
@@ -324,8 +328,6 @@ __global__ void __launch_bounds__(kMgThreads, 1)
         fence_mbar_init();
     }
     if (warp == 1) {
-        // (Waits while another kernel's CTA on this SM holds tensor memory; that one does
-        // not wait for this grid.)
         tmem_alloc_pair(tslot, Mg<BN>::kTmem);
         tc_fence_before();
     }

@@ -305,16 +305,16 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
         fence_mbar_init();
     }
     if (tid < 128) bad[tid] = 0;
+    pdl_wait();
     if (warp == 0) {
-        // (Waits while another kernel's CTA on this SM holds tensor memory; that one does
-        // not wait for this grid.)
+        // After the wait: a CTA of the kernel before, which may be on this SM, may have yet
+        // to take its own.
         tmem_alloc(&tslot, TCOLS);
         tmem_relinquish();
         tc_fence_before();
     }
     __syncthreads();
     tc_fence_after();
-    pdl_wait();
     const uint32_t tb = tslot, trow = tb + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)c0;
 
     // ---------------------------------------------------- A_0 = U U^T over this CTA's chunks
