@@ -473,8 +473,10 @@ struct EmbPlan {
 int emb_plan(const wg_embedding_problem* p, EmbPlan* pl)
 {
     if (!p) return set_err(WG_ERR_INVALID_ARGUMENT, "problem is NULL");
-    if (p->tokens < 0 || p->tokens > 0x7fffff00LL || p->vocab < 1 || p->dim < 1)
-        return set_err(WG_ERR_INVALID_ARGUMENT, "tokens must be in 0..2^31-256, vocab and dim at least 1");
+    // (Numbers of rows and columns are 32-bit, those past the end of a CTA's share too.)
+    if (p->tokens < 0 || p->tokens > 0x7fffff00LL || p->vocab < 1 || p->vocab > 0x7fff0000 || p->dim < 1 ||
+        p->dim > 0x7fff0000)
+        return set_err(WG_ERR_INVALID_ARGUMENT, "tokens must be in 0..2^31-256, vocab and dim in 1..2^31-65536");
     if (!dtype_ok(p->table_dtype) || !dtype_ok(p->out_dtype))
         return set_err(WG_ERR_INVALID_ARGUMENT, "table_dtype and out_dtype must be WG_FP32, WG_BF16 or WG_FP16");
     if (p->token_bits != 32 && p->token_bits != 64)

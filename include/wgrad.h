@@ -389,7 +389,7 @@ WG_API int wg_muon_update(const wg_muon_problem* p, const void* grad, void* mome
  * then returns WG_ERR_INVALID_TOKEN.
  *
  *  tokens in 0..2^31-256 (0: a lookup does nothing, a gradient is zero), vocab and
- *  dim >= 1.
+ *  dim in 1..2^31-65536.
  *  ld_table, ld_out: elements between rows of table / dtable and of out / dy;
  *    0 = dim.  Elements between rows are neither read nor written.
  *  table_dtype: table and dtable; out_dtype: out and dy (WG_FP32, WG_BF16, WG_FP16).

@@ -68,6 +68,7 @@ def test_muon_buffer_refusals():
 @pytest.mark.parametrize("bad,status", [
     (dict(tokens=-1), 1), (dict(tokens=1 << 31), 1), (dict(vocab=0), 1), (dict(dim=0), 1), (dict(ld_table=15), 1),
     (dict(ld_out=15), 1), (dict(padding_token=11), 1), (dict(padding_token=-2), 1), (dict(scale=math.nan), 1),
+    (dict(vocab=(1 << 31) - 1), 1), (dict(dim=(1 << 31) - 1), 1),
 ])
 def test_embedding_problem_refusals(bad, status):
     refused(status, binding.wg_embedding_workspace_size, emb(**bad))
