@@ -23,6 +23,8 @@
 //                     the fences took longer than this kernel does.)
 #pragma once
 
+#include <type_traits>
+
 #include "ptx.cuh"
 #include "vec.cuh"
 
@@ -162,24 +164,33 @@ __global__ void __launch_bounds__(kEmbSortThreads, 1) emb_sort_kernel(const __gr
         kept += __popc(who);
     };
     long long t = t0;
-    if (!p.token64 && p.padding < 0) {
-        const int* tok = static_cast<const int*>(p.token) + lane;
+    auto scan = [&](auto* token) {
+        typedef std::remove_const_t<std::remove_pointer_t<decltype(token)>> I;
+        typedef std::make_unsigned_t<I> U;
+        token += lane;
         for (; t + 32 * kAhead <= t1; t += 32 * kAhead) {
-            int v[kAhead];
+            I v[kAhead];
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) v[k] = tok[t + 32 * k];
+            for (int k = 0; k < kAhead; ++k) v[k] = token[t + 32 * k];
+            if (blockIdx.x == 0)
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) bad |= (U)v[k] >= (U)p.V;
+            if (p.padding >= 0)
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) v[k] = v[k] == (I)p.padding ? (I)-1 : v[k];
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 // (A token out of range is a large unsigned number: neither below nor in the range.)
-                const unsigned r = (unsigned)v[k] - (unsigned)lo;
-                if ((unsigned)v[k] < (unsigned)lo) ++below;
-                take((int)(t - t0) + 32 * k, r, r < (unsigned)nr);
+                const U r = (U)v[k] - (U)lo;
+                if ((U)v[k] < (U)lo) ++below;
+                take((int)(t - t0) + 32 * k, (unsigned)r, r < (U)nr);
             }
-            if (blockIdx.x == 0)
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k) bad |= (unsigned)v[k] >= (unsigned)p.V;
         }
-    }
+    };
+    if (p.token64)
+        scan(static_cast<const long long*>(p.token));
+    else
+        scan(static_cast<const int*>(p.token));
     for (; t < t1; t += 32) {
         const int v = t + lane < t1 ? emb_token(p, t + lane) : -2;
         const unsigned r = (unsigned)v - (unsigned)lo;
