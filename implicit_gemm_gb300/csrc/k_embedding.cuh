@@ -85,6 +85,42 @@ __global__ void __launch_bounds__(256) emb_lookup_kernel(const __grid_constant__
     }
 }
 
+// The same for rows that start anywhere: a warp per row and 256 columns, VEC (1 or 2)
+// neighbouring elements per lane and access.  (Element by element over all rows, as
+// above, the divisions and one load in flight took 32,768 rows of 2,047 154 us.)
+constexpr int kEmbLookCols = 256;
+template <typename TT, typename TO, int VEC>
+__global__ void __launch_bounds__(256) emb_lookup_any_kernel(const __grid_constant__ EmbParams p)
+{
+    constexpr int U = kEmbLookCols / (32 * VEC);
+    pdl_launch_dependents();
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const unsigned tiles = (unsigned)((p.D + kEmbLookCols - 1) / kEmbLookCols);
+    const long long n = p.T * tiles;
+    for (long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); i < n; i += (long long)gridDim.x * 8) {
+        const long long t = n <= 0xffffffffLL ? (unsigned)i / tiles : i / tiles;
+        const int tile = (int)(i - t * tiles), c0 = tile * kEmbLookCols + lane * VEC, v = emb_token(p, t);
+        if (v < 0 && tile == 0 && lane == 0) atomicOr(&g_status, kStatusBadToken);
+        const TT* in = static_cast<const TT*>(p.in) + v * p.ld_table + c0;
+        TO* out = static_cast<TO*>(p.out) + t * p.ld_out + c0;
+        float f[U][VEC];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) f[u][k] = 0.f;
+            if (v >= 0 && c0 + 32 * VEC * u < p.D) load_f32<TT, VEC>(in + 32 * VEC * u, f[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (c0 + 32 * VEC * u >= p.D) break;
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) f[u][k] *= p.scale;
+            store_f32<TO, VEC>(out + 32 * VEC * u, f[u]);
+        }
+    }
+}
+
 constexpr int kEmbSortThreads = 1024, kEmbSortWarps = kEmbSortThreads / 32;
 constexpr int kEmbSortMaxRows = 1472;     // 32 counters of 4 bytes a row: 184 KB of shared memory
 constexpr int kEmbSortRowBits = 11;       // a row of the range in a kept match

@@ -548,12 +548,19 @@ template <typename TT, typename TO>
 int emb_lookup_t(const EmbPlan& pl, const wg::EmbParams& p, cudaStream_t s)
 {
     constexpr int V = sizeof(TT) == 4 || sizeof(TO) == 4 ? 4 : 8;
-    const bool vec = p.D % V == 0 && p.ld_table % V == 0 && p.ld_out % V == 0 && aligned_to(p.in, V * sizeof(TT)) &&
-                     aligned_to(p.out, V * sizeof(TO));
-    const long long n = p.T * (p.D / (vec ? V : 1));
-    const unsigned blocks = (unsigned)std::max(1LL, std::min<long long>((n + 255) / 256, 16LL * num_sms()));
-    return launch("emb_lookup_kernel launch", vec ? wg::emb_lookup_kernel<TT, TO, V> : wg::emb_lookup_kernel<TT, TO, 1>,
-                  dim3(blocks), dim3(256), 0, s, p);
+    const auto fits = [&](int v) {
+        return p.D % v == 0 && p.ld_table % v == 0 && p.ld_out % v == 0 && aligned_to(p.in, v * (int)sizeof(TT)) &&
+               aligned_to(p.out, v * (int)sizeof(TO));
+    };
+    const auto blocks = [&](long long n) {
+        return dim3((unsigned)std::max(1LL, std::min<long long>((n + 255) / 256, 16LL * num_sms())));
+    };
+    if (fits(V))
+        return launch("emb_lookup_kernel launch", wg::emb_lookup_kernel<TT, TO, V>, blocks(p.T * (p.D / V)), dim3(256), 0, s, p);
+    const long long n = 32 * p.T * ((p.D + wg::kEmbLookCols - 1) / wg::kEmbLookCols);
+    return launch("emb_lookup_any_kernel launch",
+                  fits(2) ? wg::emb_lookup_any_kernel<TT, TO, 2> : wg::emb_lookup_any_kernel<TT, TO, 1>, blocks(n), dim3(256),
+                  0, s, p);
 }
 
 template <typename TG, typename TY, int V>

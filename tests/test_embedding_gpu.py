@@ -70,6 +70,27 @@ def test_lookup(tdt, odt, T, V, D):
     binding.wg_check_status()
 
 
+@pytest.mark.parametrize("tdt,odt", [("bf16", "bf16"), ("fp16", "fp32"), ("fp32", "bf16"), ("fp32", "fp32")])
+@pytest.mark.parametrize("off", [0, 1, 2])
+@pytest.mark.parametrize("D", [2, 254, 258, 510, 1001])
+def test_lookup_of_rows_that_start_anywhere(tdt, odt, D, off):
+    g = rng(D + off)
+    T, V = 77, 50
+    table = randn(g, (off + V * D,), tdt)
+    tok = torch.randint(V, (T,), generator=g, device="cuda").int()
+    tok[5], tok[6] = -1, V
+    out = torch.full((off + T * D + 3,), float("nan"), dtype=DT[odt], device="cuda")
+    sp = {"tokens": T, "vocab": V, "dim": D, "table_dtype": tdt, "out_dtype": odt, "token_dtype": "i32", "scale": 3.7}
+    binding.wg_embedding_lookup(sp, tok, table[off:], out[off:])
+    ref = table[off:].view(V, D)[tok.long().clamp(0, V - 1)].double() * float(np.float32(3.7))
+    ref[5:7] = 0
+    close(out[off:off + T * D].view(T, D), ref, 2.0 ** -23 * ref.abs(), odt)
+    assert torch.isnan(out[:off]).all() and torch.isnan(out[off + T * D:]).all()
+    with pytest.raises(binding.WgradError) as e:
+        binding.wg_check_status()
+    assert e.value.status == 7
+
+
 def test_lookup_strides_and_offsets():
     """Rows apart, buffers that start at any element; what lies between rows stays as it was."""
     g = rng(1)
