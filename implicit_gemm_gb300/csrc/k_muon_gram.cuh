@@ -48,8 +48,6 @@ struct GramParams {
     int wide;        // rows <= cols
     int chunks;      // 64-column chunks of the long side
     int C;           // CTAs of a cluster
-    int vec;         // eight elements along memory of grad and momentum are aligned and of one matrix
-    int ovec;        // and of weight and out
     int split;       // U needs its second bf16 value
     int kn;          // 16-wide parts of a block's rows that are used
     int steps;
@@ -174,66 +172,129 @@ __device__ __forceinline__ void st_dsmem_v2(uint32_t addr, float2 v)
     asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(v.x), "f"(v.y) : "memory");
 }
 
-// What eight values of u are made of.  (Not aligned: u itself, as fp32.)
+// What eight values of u are made of, as it comes from memory: a conversion would wait
+// for it.  (Rows that start anywhere: an element in each word.)
 struct GramRaw {
     MuonRaw8 g, m;
 };
 
-// Address of element k of `line`, `seg` .. of chunk `ch` of block `blk` (a line is a
-// row of the block when the matrices are wide and a position of the long side when
-// they are tall; seg runs along memory), or -1 outside the matrices.
-__device__ __forceinline__ long long gram_at(const GramParams& g, int blk, int ch, int line, int seg, int k)
+// The eight elements from address e0 (-1: outside) one by one, f(k, address, whether
+// it is inside): `pos` is the first one's position along the long side (wide) or its
+// row of the block (tall; the rows go on in the next matrix).
+template <typename F>
+__device__ __forceinline__ void gram_each(const GramParams& g, int blk, long long e0, int pos, F f)
 {
     const MuonParams& p = g.p;
-    const int i = g.wide ? line : seg + k, n = ch * 64 + (g.wide ? seg + k : line);
-    const int f = i / p.m, b = blk * g.F + f, idx = i - f * p.m;
-    if (f >= g.F || b >= p.batch || n >= g.N) return -1;
-    return (long long)b * p.bs + (g.wide ? idx * p.ld + n : n * p.ld + idx);
-}
-
-// Eight elements one by one.  (A call of its own: inlined at every load, the code of
-// this path and the like came to 600 KB, and the kernel waited for instructions.)
-template <bool STEP>
-__device__ __noinline__ void gram_read_each(const GramParams& g, int blk, int ch, int line, int seg, uint32_t* w)
-{
-#pragma unroll 1
+    const int nf = min(g.F, p.batch - blk * g.F);
+    int at = g.wide ? 0 : pos / p.m, idx = g.wide ? pos : pos - at * p.m;
+    long long e = e0;
+#pragma unroll
     for (int k = 0; k < 8; ++k) {
-        const long long e = gram_at(g, blk, ch, line, seg, k);
-        float x[1] = {0.f};
-        if (e >= 0) muon_u<1, STEP>(g.p, e, x);
-        w[k] = __float_as_uint(x[0]);
+        f(k, e, e0 >= 0 && (g.wide ? idx < g.N : at < nf));
+        ++e, ++idx;
+        if (!g.wide && idx == p.m) idx = 0, ++at, e += p.bs - p.m;
     }
 }
 
-// STEP: the momentum's step is taken and written; otherwise it has been.  e: the
-// address when eight elements are read at once (-1: outside).
-template <bool STEP>
-__device__ __forceinline__ void gram_read(const GramParams& g, int blk, int ch, int line, int seg, long long e, GramRaw& r)
+// STEP: the momentum's step is taken and written; otherwise it has been.
+template <bool VEC>
+__device__ __forceinline__ void gram_read(const GramParams& g, int blk, long long e, int pos, GramRaw& r)
 {
     const MuonParams& p = g.p;
     const uint4 z = make_uint4(0u, 0u, 0u, 0u);
     r.g.a = r.g.b = r.m.a = r.m.b = z;
-    if (g.vec) {
+    if (VEC) {
         if (e < 0) return;
         r.g = muon_raw8(p.grad, p.grad_dtype, e);
         if (p.mom) r.m = muon_raw8(p.mom, 2, e);
         return;
     }
-    uint32_t w[8];
-    gram_read_each<STEP>(g, blk, ch, line, seg, w);
+    uint32_t w[8] = {}, m[8] = {};
+    gram_each(g, blk, e, pos, [&](int k, long long at, bool in) {
+        if (!in) return;
+        if (p.grad_dtype == 2)
+            w[k] = static_cast<const uint32_t*>(p.grad)[at];
+        else
+            w[k] = static_cast<const uint16_t*>(p.grad)[at];
+        if (p.mom) m[k] = __float_as_uint(p.mom[at]);
+    });
     r.g.a = make_uint4(w[0], w[1], w[2], w[3]), r.g.b = make_uint4(w[4], w[5], w[6], w[7]);
+    r.m.a = make_uint4(m[0], m[1], m[2], m[3]), r.m.b = make_uint4(m[4], m[5], m[6], m[7]);
 }
 
-template <bool STEP>
-__device__ __forceinline__ void gram_make(const GramParams& g, long long e, const GramRaw& r, float (&u)[8])
+template <bool VEC, bool STEP>
+__device__ __forceinline__ void gram_make(const GramParams& g, int blk, long long e, int pos, const GramRaw& r, float (&u)[8])
 {
     const MuonParams& p = g.p;
-    muon_unraw8(g.vec ? p.grad_dtype : 2, r.g, u);
-    if (!g.vec || !p.mom) return;
+    if (VEC || p.grad_dtype == 2) {
+        muon_unraw8(VEC ? p.grad_dtype : 2, r.g, u);
+    } else {
+        const uint32_t w[8] = {r.g.a.x, r.g.a.y, r.g.a.z, r.g.a.w, r.g.b.x, r.g.b.y, r.g.b.z, r.g.b.w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            u[k] = p.grad_dtype == 0 ? __uint_as_float(w[k] << 16) : __half2float(__ushort_as_half((unsigned short)w[k]));
+    }
+    if (!p.mom) return;
     float m[8];
     muon_unraw8(2, r.m, m);
     muon_make<8, STEP>(p, u, m);
-    if (STEP && e >= 0) store_f32<float, 8>(p.mom + e, m);
+    if (!STEP) return;
+    if (VEC) {
+        if (e >= 0) store_f32<float, 8>(p.mom + e, m);
+    } else {
+        gram_each(g, blk, e, pos, [&](int k, long long at, bool in) {
+            if (in) p.mom[at] = m[k];
+        });
+    }
+}
+
+// x[k] of lane l <-> x[l % 16] of lane k, within each half of the warp.
+__device__ __forceinline__ void transpose16(float (&x)[16])
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int s = 8; s; s >>= 1)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (!(i & s)) {
+                const bool up = lane & s;
+                const float y = __shfl_xor_sync(0xffffffffu, up ? x[i] : x[i + s], s);
+                x[i] = up ? y : x[i];
+                x[i + s] = up ? x[i + s] : y;
+            }
+}
+
+// Results of 16 rows of the block from row r0 on, one column: o[k] belongs to row
+// r0 + k, n is the column.  Weights are all loaded before the first is written.
+template <typename F>
+__device__ __forceinline__ void gram_rows(const GramParams& g, int blk, int r0, int n, F f)
+{
+    const MuonParams& p = g.p;
+    const int nf = min(g.F, p.batch - blk * g.F);
+    int at = r0 / p.m, idx = r0 - at * p.m;
+    long long e = (long long)(blk * g.F + at) * p.bs + idx * p.ld + n;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        f(k, e, at < nf && n < g.N);
+        e += p.ld;
+        if (++idx == p.m) idx = 0, ++at, e += p.bs - p.m * p.ld;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void gram_put_rows(const GramParams& g, T* out, int blk, int r0, int n, const float (&o)[16])
+{
+    gram_rows(g, blk, r0, n, [&](int k, long long e, bool in) {
+        if (in) out[e] = from_f32<T>(o[k]);
+    });
+}
+template <typename T>
+__device__ __forceinline__ void gram_weight_rows(const GramParams& g, T* w, int blk, int r0, int n, const float (&o)[16])
+{
+    T x[16];
+    gram_rows(g, blk, r0, n, [&](int k, long long e, bool in) { x[k] = in ? w[e] : from_f32<T>(0.f); });
+    gram_rows(g, blk, r0, n, [&](int k, long long e, bool in) {
+        if (in) w[e] = from_f32<T>(fmaf(g.p.keep, to_f32<T>(x[k]), -g.p.lr * o[k]));
+    });
 }
 
 // n <= 16 results, `step` elements apart: all loads, then all stores.
@@ -255,7 +316,13 @@ __device__ __forceinline__ void gram_weight_each(const MuonParams& p, T* w, long
         if (i < n) w[i * step] = from_f32<T>(fmaf(p.keep, to_f32<T>(x[i]), -p.lr * o[i]));
 }
 
-template <int P>
+// VEC: every eight elements of a row of grad, momentum, weight and out lie in an
+// aligned 16 (or 32) bytes.  Otherwise each is a load of its own, as far ahead as the
+// wide ones, and results are turned so that neighbouring lanes write neighbouring
+// elements: 64 x 577 28 us and 127 x 4001 71 (one element after another and a row per
+// lane: 48 and 177); 64 x 576 and 128 x 4000 take 23 and 54.  A kernel of its own,
+// since the code of both, inlined, kept the kernel waiting for instructions.
+template <int P, bool VEC>
 __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_constant__ GramParams g)
 {
     constexpr int NC = P / 4;                     // columns per thread: four warps share a row
@@ -332,11 +399,12 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
         if (at0[j] < 0 || ch * 64 + (g.wide ? seg : line) >= g.N) return -1;
         return at0[j] + ch * (g.wide ? 64 : 64 * p.ld);
     };
+    auto pos = [&](int ch, int j) { return g.wide ? ch * 64 + seg : seg + 64 * j; };
     auto stage = [&](uint8_t* img, int ch, auto step, const GramRaw (&u)[P / 64]) {
 #pragma unroll
         for (int j = 0; j < P / 64; ++j) {
             float v[8];
-            gram_make<decltype(step)::value>(g, addr(ch, j), u[j], v);
+            gram_make<VEC, decltype(step)::value>(g, blk, addr(ch, j), pos(ch, j), u[j], v);
             float odd = 0.f;  // NaN when one of them is a NaN or an infinity
 #pragma unroll
             for (int k = 0; k < 8; ++k) odd = fmaf(v[k], 0.f, odd);
@@ -360,11 +428,11 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
             *reinterpret_cast<uint4*>(o + IMG) = l;
         }
     };
-    auto load = [&](int ch, auto step, GramRaw (&u)[P / 64]) {
+    auto load = [&](int ch, GramRaw (&u)[P / 64]) {
         if (ch >= g.chunks) return;
 #pragma unroll
         for (int j = 0; j < P / 64; ++j)
-            gram_read<decltype(step)::value>(g, blk, ch, g.wide ? line + 64 * j : line, g.wide ? seg : seg + 64 * j, addr(ch, j), u[j]);
+            gram_read<VEC>(g, blk, addr(ch, j), pos(ch, j), u[j]);
     };
     const int nch = (g.chunks - rank + g.C - 1) / g.C;  // this CTA's chunks: rank, rank + C, ...
     if (!issuer) {
@@ -377,7 +445,7 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
             if (it >= 0) stage(ba + (it & 1) * 2 * IMG, rank + it * g.C, std::true_type{}, u[0]);
 #pragma unroll
             for (int j = 0; j < P / 64; ++j) u[0][j] = u[AHEAD - 1][j];
-            load(rank + (it + AHEAD) * g.C, std::true_type{}, u[AHEAD - 1]);
+            load(rank + (it + AHEAD) * g.C, u[AHEAD - 1]);
             if (it >= 0) ready();
         }
         if (nch >= 2) wait(nch & 1);
@@ -586,7 +654,7 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
                 if (act) convert(TA, w.ra * g.step[k + 1].sa, ba);
             }
         }
-        load(rank, std::false_type{}, u);  // the first chunk of U comes back
+        load(rank, u);  // the first chunk of U comes back
         if (act && g.steps > 1) {
             const float f = g.step[g.steps - 1].rq;
 #pragma unroll 1
@@ -610,7 +678,7 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
             const int b0 = blk * g.F + mine;
             const bool mat = rows && mine < g.F && b0 < p.batch;
             MuonRaw8 old[2] = {};
-            if (it >= 0 && g.wide && g.ovec && p.weight && mat) {
+            if (VEC && it >= 0 && g.wide && p.weight && mat) {
                 const long long e = (long long)b0 * p.bs + (row - lo) * p.ld + ch * 64 + q0;
                 if (ch * 64 + q0 < g.N) old[0] = muon_raw8(p.weight, p.weight_dtype, e);
                 if (ch * 64 + q0 + 8 < g.N) old[1] = muon_raw8(p.weight, p.weight_dtype, e + 8);
@@ -618,18 +686,42 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
             if (it + 1 < nch) {
                 // (The MMAs that read this image two chunks ago are done: their sums have been read.)
                 stage((it & 1 ? ba : bp), ch + g.C, std::false_type{}, u);
-                load(ch + 2 * g.C, std::false_type{}, u);
+                load(ch + 2 * g.C, u);
                 ready();
             }
             if (it < 0) continue;
             wait(it & 1);
             float x[16];
             if (rows) gram_ld<16>(tb + ((uint32_t)((warp & 3) * 32) << 16) + (it & 1 ? T2 : TA) + (uint32_t)q0, x);
-            if (mat) {
+            if (!VEC && g.wide) {
+                // A column per lane (a row per lane touches 32 rows an access).
+                if (!rows) continue;
+                const float f = fac[row];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] *= f;
+                transpose16(x);
+                const int r0 = (warp & 3) * 32 + (lane & 16), n = ch * 64 + q0 + (lane & 15);
+                if (p.out) {
+                    if (p.out_dtype == 2)
+                        gram_put_rows(g, static_cast<float*>(p.out), blk, r0, n, x);
+                    else if (p.out_dtype == 0)
+                        gram_put_rows(g, static_cast<__nv_bfloat16*>(p.out), blk, r0, n, x);
+                    else
+                        gram_put_rows(g, static_cast<__half*>(p.out), blk, r0, n, x);
+                }
+                if (p.weight) {
+                    if (p.weight_dtype == 2)
+                        gram_weight_rows(g, static_cast<float*>(p.weight), blk, r0, n, x);
+                    else if (p.weight_dtype == 0)
+                        gram_weight_rows(g, static_cast<__nv_bfloat16*>(p.weight), blk, r0, n, x);
+                    else
+                        gram_weight_rows(g, static_cast<__half*>(p.weight), blk, r0, n, x);
+                }
+            } else if (mat) {
                 const float f = fac[row];
                 const long long base = (long long)b0 * p.bs;
                 const int n0 = ch * 64 + q0;
-                if (g.wide && g.ovec) {
+                if (VEC && g.wide) {
 #pragma unroll
                     for (int i = 0; i < 16; i += 8) {
                         float o[8];
@@ -638,8 +730,8 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
                         if (n0 + i < g.N) muon_finish8(p, base + (row - lo) * p.ld + n0 + i, o, old[i / 8]);
                     }
                 } else {
-                    const long long e0 = base + (g.wide ? (row - lo) * p.ld + n0 : n0 * p.ld + (row - lo));
-                    const long long step = g.wide ? 1 : p.ld;
+                    // (Tall: neighbouring lanes write neighbouring elements.)
+                    const long long e0 = base + n0 * p.ld + (row - lo), step = p.ld;
                     const int n = min(16, g.N - n0);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) x[i] *= f;

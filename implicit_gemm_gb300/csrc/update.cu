@@ -99,8 +99,8 @@ int muon_gram_max_cluster()
     if (it != cache.end()) return it->second;
     int n = 0;
     const int smem = wg::gram_smem_bytes(128);
-    if (wg::ensure_smem(wg::muon_gram_kernel<128>, smem) == WG_OK &&
-        cudaFuncSetAttribute(wg::muon_gram_kernel<128>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
+    if (wg::ensure_smem(wg::muon_gram_kernel<128, true>, smem) == WG_OK &&
+        cudaFuncSetAttribute(wg::muon_gram_kernel<128, true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -109,7 +109,7 @@ int muon_gram_max_cluster()
         cfg.attrs = attr, cfg.numAttrs = 1;
         cfg.gridDim = dim3(16), cfg.blockDim = dim3(wg::kGramBlock);
         cfg.dynamicSmemBytes = (size_t)smem;
-        if (cudaOccupancyMaxActiveClusters(&n, wg::muon_gram_kernel<128>, &cfg) != cudaSuccess) n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, wg::muon_gram_kernel<128, true>, &cfg) != cudaSuccess) n = 0;
     }
     cudaGetLastError();
     return cache[dev] = n > 0 ? 16 : 8;
@@ -131,7 +131,7 @@ void muon_gram_plan(MuonPlan* pl)
     g.steps = q.steps;
     pl->blocks = (q.batch + g.F - 1) / g.F;
     // A CTA per chunk up to the largest cluster, while every block has its cluster at
-    // once (96 x 3456: 45 us with 16 CTAs, 57 with 8, 90 with 4).
+    // once (96 x 3456: 44 us with 16 CTAs, 57 with 8, 90 with 4).
     g.C = 1;
     const int cmax = muon_gram_max_cluster();
     while (g.C < cmax && 2 * g.C <= g.chunks && 2LL * g.C * pl->blocks <= num_sms()) g.C *= 2;
@@ -273,14 +273,14 @@ int muon_plan(const wg_muon_problem* p, MuonPlan* pl)
     return WG_OK;
 }
 
-template <int P>
+template <int P, bool VEC>
 int muon_gram_launch(const MuonPlan& pl, const wg::GramParams& g, cudaStream_t s)
 {
     const int smem = wg::gram_smem_bytes(P);
-    const int st = wg::ensure_smem(wg::muon_gram_kernel<P>, smem);
+    const int st = wg::ensure_smem(wg::muon_gram_kernel<P, VEC>, smem);
     if (st) return st;
     if (g.C > 8) {  // beyond the portable cluster size
-        const cudaError_t e = cudaFuncSetAttribute(wg::muon_gram_kernel<P>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        const cudaError_t e = cudaFuncSetAttribute(wg::muon_gram_kernel<P, VEC>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute", e);
     }
     cudaLaunchConfig_t cfg = {};
@@ -294,7 +294,7 @@ int muon_gram_launch(const MuonPlan& pl, const wg::GramParams& g, cudaStream_t s
     cfg.gridDim = dim3((unsigned)(pl.blocks * g.C));
     cfg.blockDim = dim3(wg::kGramBlock);
     cfg.dynamicSmemBytes = (size_t)smem;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, wg::muon_gram_kernel<P>, g);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, wg::muon_gram_kernel<P, VEC>, g);
     return e == cudaSuccess ? WG_OK : cuda_fail("muon_gram_kernel launch", e);
 }
 
@@ -397,10 +397,10 @@ int muon_run(const MuonPlan& pl, const void* grad, void* momentum, void* weight,
         wg::GramParams g = pl.g;
         g.p = p;
         const bool al = q.cols % 8 == 0 && q.ld % 8 == 0 && q.batch_stride % 8 == 0;
-        g.vec = al && aligned16(grad) && aligned16(momentum);
-        g.ovec = al && aligned16(weight) && aligned16(out);
+        const bool vec = al && aligned16(grad) && aligned16(momentum) && aligned16(weight) && aligned16(out);
         g.split = momentum || q.grad_dtype != WG_BF16;
-        return pl.P == 64 ? muon_gram_launch<64>(pl, g, s) : muon_gram_launch<128>(pl, g, s);
+        if (vec) return pl.P == 64 ? muon_gram_launch<64, true>(pl, g, s) : muon_gram_launch<128, true>(pl, g, s);
+        return pl.P == 64 ? muon_gram_launch<64, false>(pl, g, s) : muon_gram_launch<128, false>(pl, g, s);
     }
     p.part = reinterpret_cast<float*>(ws + pl.off_part), p.nparts = pl.nparts;
     if (q.steps > 0) {
