@@ -164,6 +164,33 @@ __device__ __forceinline__ void mg_read(const MuonParams& p, const MuonProduct& 
     }
 }
 
+// The first n of 32 staged rows, a column per lane.
+__device__ __forceinline__ float mg_staged(const uint8_t* stg, int r)
+{
+    const int lane = threadIdx.x & 31;
+    return *reinterpret_cast<const float*>(stg + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+}
+template <typename T>
+__device__ __forceinline__ void mg_put_rows(T* out, long long ld, int n, const uint8_t* stg)
+{
+#pragma unroll 8
+    for (int r = 0; r < 32; ++r, out += ld)
+        if (r < n) *out = from_f32<T>(mg_staged(stg, r));
+}
+template <typename T>
+__device__ __forceinline__ void mg_weight_rows(const MuonParams& p, T* w, int n, const uint8_t* stg)
+{
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32; r0 += 8, w += 8 * p.ld) {
+        T x[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) x[q] = r0 + q < n ? w[q * p.ld] : from_f32<T>(0.f);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (r0 + q < n) w[q * p.ld] = from_f32<T>(fmaf(p.keep, to_f32<T>(x[q]), -p.lr * mg_staged(stg, r0 + q)));
+    }
+}
+
 // 32 finished sums of row i0 + lane, columns j .. j + 31 of matrix b, by one warp.
 // Global memory is read and written in rows of 64 bytes through the warp's 4 KB of
 // shared memory, whose 16-byte chunks are swizzled by the row: row by row from the
@@ -235,35 +262,6 @@ __device__ __forceinline__ void mg_epilogue(const MuonParams& p, const MuonProdu
         *reinterpret_cast<float4*>(stg + lane * 128 + ((k ^ (lane & 7)) << 4)) =
             make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
     __syncwarp();
-    if (g.last && !g.ovec) {
-        // Results whose rows start anywhere: a row at a time, a column per lane (eight
-        // elements per lane, one by one, took the last product of 1000 x 2731 35 us instead of 20).
-        const int c = j + lane;
-        for (int r0 = 0; r0 < 32; r0 += 8) {
-            float x[8], w[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const int i = i0 + r0 + q;
-                x[q] = w[q] = 0.f;
-                if (i >= g.M || c >= g.N) continue;
-                const long long e = b * p.xs + (long long)i * p.ldx + c;
-                x[q] = __half2float(p.x[g.xin][e]) + __half2float(p.xlo[e]);
-                if (p.weight) w[q] = muon_load(p.weight, p.weight_dtype, (long long)b * p.bs + i * p.ld + c);
-            }
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const int r = r0 + q, i = i0 + r;
-                if (i >= g.M || c >= g.N) continue;
-                const float d = *reinterpret_cast<const float*>(stg + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
-                const float o = p.scale * (1.f / kMuonXScale) * fmaf(g.a, x[q], d * 0x1p-10f);
-                const long long e = (long long)b * p.bs + i * p.ld + c;
-                if (p.out) muon_store(p.out, p.out_dtype, e, o);
-                if (p.weight) muon_store(p.weight, p.weight_dtype, e, fmaf(p.keep, w[q], -p.lr * o));
-            }
-        }
-        __syncwarp();
-        return;
-    }
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
         const int r = 8 * it + sub, i = i0 + r;
@@ -288,12 +286,40 @@ __device__ __forceinline__ void mg_epilogue(const MuonParams& p, const MuonProdu
             *reinterpret_cast<uint4*>(p.xlo + e) = l;
             continue;
         }
-        const long long o = (long long)b * p.bs + i * p.ld + jc;
 #pragma unroll
         for (int q = 0; q < 8; ++q) y[q] *= p.scale * (1.f / kMuonXScale);
-        muon_finish8(p, o, y);
+        if (g.ovec) {
+            muon_finish8(p, (long long)b * p.bs + i * p.ld + jc, y);
+        } else {
+            *reinterpret_cast<float4*>(stg + r * 128 + (((2 * c4) ^ (r & 7)) << 4)) = make_float4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<float4*>(stg + r * 128 + (((2 * c4 + 1) ^ (r & 7)) << 4)) = make_float4(y[4], y[5], y[6], y[7]);
+        }
     }
     __syncwarp();
+    if (g.last && !g.ovec) {
+        // Results whose rows start anywhere: a row at a time, a column per lane (eight
+        // elements per lane, one by one, took the last product of 1000 x 2731 35 us
+        // instead of 20, and with X read by the column that of 8 of 1023 x 1023 @@).
+        const long long e = (long long)b * p.bs + i0 * p.ld + j + lane;
+        const int n = j + lane < g.N ? g.M - i0 : 0;
+        if (p.out) {
+            if (p.out_dtype == 2)
+                mg_put_rows(static_cast<float*>(p.out) + e, p.ld, n, stg);
+            else if (p.out_dtype == 0)
+                mg_put_rows(static_cast<__nv_bfloat16*>(p.out) + e, p.ld, n, stg);
+            else
+                mg_put_rows(static_cast<__half*>(p.out) + e, p.ld, n, stg);
+        }
+        if (p.weight) {
+            if (p.weight_dtype == 2)
+                mg_weight_rows(p, static_cast<float*>(p.weight) + e, n, stg);
+            else if (p.weight_dtype == 0)
+                mg_weight_rows(p, static_cast<__nv_bfloat16*>(p.weight) + e, n, stg);
+            else
+                mg_weight_rows(p, static_cast<__half*>(p.weight) + e, n, stg);
+        }
+        __syncwarp();
+    }
 }
 
 template <int BN>
