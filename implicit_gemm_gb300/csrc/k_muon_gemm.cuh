@@ -20,8 +20,7 @@
 //
 // Main loop: 0.33 us per 64 of a 256 x 256 tile's sum on all pairs, 1.9 PFLOP/s,
 // the rate of a large library product.  Around it a launch costs some 7 us: 1 from
-// the kernel before (2, and 248 us instead of 233 for 1000 x 2731, with the set-up
-// after the wait for it), 1.7 to the first operands, 3 to 6 for the last tile's
+// the kernel before (2 with the set-up after the wait for it, some 15 us of 1000 x 2731), 1.7 to the first operands, 3 to 6 for the last tile's
 // epilogue; 15 of them bound updates of up to some 1024 rows.  Each of the roles that
 // touch global memory waits for the kernel before by itself, after it has found its
 // first tile.
@@ -47,8 +46,19 @@ struct Mg {
     static constexpr int kTmem = 2 * BN;  // columns: the sums, twice
 };
 
+// What a product's epilogue writes.  A kernel each: in one, the registers of the
+// results cost the others spills (8 of 1024 x 1024 321 us against 311, 512 x 8192 207
+// against 190; 300 x 1000, whose kernels are short, 118 against 120).
+enum MuonKind {
+    kMuonA,        // stage 0
+    kMuonB,        // stage 1
+    kMuonX,        // stage 2
+    kMuonLast,     // the results, every eight elements of a row in an aligned 16 (or 32) bytes
+    kMuonLastAny,  // the results, rows that start anywhere
+};
+
 struct MuonProduct {
-    int stage, xin, last;
+    int kind, xin;
     float a, b, c;
     int a_mn, b_mn;           // operand is read across its rows
     int M, N, kb;             // extents of D, 64-wide blocks of the sum
@@ -58,7 +68,6 @@ struct MuonProduct {
     int whole;                // tiles of whole waves
     int pairs;
     int cut;                  // pairs that share the blocks of sums of the other tiles (at most as many as blocks)
-    int ovec;                 // eight elements along a row of weight and out are aligned
     float* part;              // [pairs][2][2][BN][128] sums of parts of tiles
     int* arrived;             // [pairs][2][16] parts of a tile that are there (zero between launches)
 };
@@ -145,16 +154,17 @@ __device__ __forceinline__ MgTile mg_tile(const MuonProduct& g, int t)
 struct MgRead {
     uint4 x[4], y[4];
 };
+template <int KIND>
 __device__ __forceinline__ void mg_read(const MuonParams& p, const MuonProduct& g, int b, int i0, int j, MgRead& r)
 {
     const int lane = threadIdx.x & 31, sub = lane >> 2, jc = j + 8 * (lane & 3);
-    if (g.stage == 0) return;
+    if (KIND == kMuonA) return;
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
         const int i = i0 + 8 * it + sub;
         r.x[it] = r.y[it] = make_uint4(0u, 0u, 0u, 0u);
         if (i >= g.M || jc >= g.N) continue;
-        if (g.stage == 1) {
+        if (KIND == kMuonB) {
             r.x[it] = *reinterpret_cast<const uint4*>(p.a + b * p.ms + (long long)i * p.ldm + jc);
         } else {
             const long long e = b * p.xs + (long long)i * p.ldx + jc;
@@ -196,18 +206,19 @@ __device__ __forceinline__ void mg_weight_rows(const MuonParams& p, T* w, int n,
 // shared memory, whose 16-byte chunks are swizzled by the row: row by row from the
 // lanes, a request touched 32 lines and the epilogue took longer than the MMAs of a
 // 4096-long sum.  `mirror`: the tile's mirror image is written too.
+template <int KIND>
 __device__ __forceinline__ void mg_epilogue(const MuonParams& p, const MuonProduct& g, uint8_t* stg, int b, int i0, int j,
                                             bool mirror, float (&v)[32], const MgRead& rd)
 {
     const int lane = threadIdx.x & 31, sub = lane >> 2, c4 = lane & 3;
     const int jc = j + 8 * c4;
-    if (g.stage < 2) {
+    if (KIND < kMuonX) {
         // fp16 rows of 64 bytes: chunk k of row r at k ^ (r / 2) % 4.
-        __half* base = (g.stage == 0 ? p.a : p.b) + b * p.ms;
+        __half* base = (KIND == kMuonA ? p.a : p.b) + b * p.ms;
         uint8_t* own = stg + lane * 64;
         const int osw = (lane >> 1) & 3;
         uint32_t h[16];
-        if (g.stage == 0) {
+        if (KIND == kMuonA) {
 #pragma unroll
             for (int k = 0; k < 16; ++k) h[k] = pack_half2(v[2 * k] * 0x1p-6f, v[2 * k + 1] * 0x1p-6f);
         } else {
@@ -278,7 +289,7 @@ __device__ __forceinline__ void mg_epilogue(const MuonParams& p, const MuonProdu
             y[2 * q + 1] = fmaf(g.a, h.y + l.y, d[2 * q + 1] * 0x1p-10f);
         }
         if (i >= g.M || jc >= g.N) continue;
-        if (!g.last) {
+        if (KIND == kMuonX) {
             const long long e = b * p.xs + (long long)i * p.ldx + jc;
             uint4 h, l;
             split8<false>(y, &h, &l);
@@ -288,7 +299,7 @@ __device__ __forceinline__ void mg_epilogue(const MuonParams& p, const MuonProdu
         }
 #pragma unroll
         for (int q = 0; q < 8; ++q) y[q] *= p.scale * (1.f / kMuonXScale);
-        if (g.ovec) {
+        if (KIND == kMuonLast) {
             muon_finish8(p, (long long)b * p.bs + i * p.ld + jc, y);
         } else {
             *reinterpret_cast<float4*>(stg + r * 128 + (((2 * c4) ^ (r & 7)) << 4)) = make_float4(y[0], y[1], y[2], y[3]);
@@ -296,10 +307,11 @@ __device__ __forceinline__ void mg_epilogue(const MuonParams& p, const MuonProdu
         }
     }
     __syncwarp();
-    if (g.last && !g.ovec) {
+    if (KIND == kMuonLastAny) {
         // Results whose rows start anywhere: a row at a time, a column per lane (eight
         // elements per lane, one by one, took the last product of 1000 x 2731 35 us
-        // instead of 20, and with X read by the column that of 8 of 1023 x 1023 @@).
+        // instead of 20, and with X read by the column that of 8 of 1023 x 1023 51
+        // instead of 33).
         const long long e = (long long)b * p.bs + i0 * p.ld + j + lane;
         const int n = j + lane < g.N ? g.M - i0 : 0;
         if (p.out) {
@@ -322,7 +334,7 @@ __device__ __forceinline__ void mg_epilogue(const MuonParams& p, const MuonProdu
     }
 }
 
-template <int BN>
+template <int BN, int KIND>
 __global__ void __launch_bounds__(kMgThreads, 1)
     muon_product_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                         const __grid_constant__ MuonParams p, const __grid_constant__ MuonProduct g)
@@ -457,7 +469,7 @@ __global__ void __launch_bounds__(kMgThreads, 1)
             const uint32_t tacc = trow + (uint32_t)(buf * BN);
             const bool whole = w.k0 == 0 && w.k1 == g.kb;
             MgRead rd;
-            if (whole) mg_read(p, g, t.b, i0, j0, rd);  // on its way while the sums are made
+            if (whole) mg_read<KIND>(p, g, t.b, i0, j0, rd);  // on its way while the sums are made
             if (!mbar_wait_sleep(&accf[buf], (uint32_t)(i >> 1) & 1u)) break;
             __syncwarp();
             tc_fence_after();
@@ -493,7 +505,7 @@ __global__ void __launch_bounds__(kMgThreads, 1)
                 for (int ch = 0; ch < BN / 128; ++ch) {
                     float v[32];
                     if (whole) {
-                        if (ch) mg_read(p, g, t.b, i0, j0 + ch * 32, rd);
+                        if (ch) mg_read<KIND>(p, g, t.b, i0, j0 + ch * 32, rd);
                         gram_ld<32>(tacc + (uint32_t)(ch * 32), v);
                     } else {
                         // 32 loads in flight at a time (left to the compiler, one after another).
@@ -509,9 +521,9 @@ __global__ void __launch_bounds__(kMgThreads, 1)
 #pragma unroll
                             for (int k = 0; k < 32; ++k) v[k] += x[k];
                         }
-                        mg_read(p, g, t.b, i0, j0 + ch * 32, rd);
+                        mg_read<KIND>(p, g, t.b, i0, j0 + ch * 32, rd);
                     }
-                    mg_epilogue(p, g, staging + e * kMgWarpStaging, t.b, i0, j0 + ch * 32, t.mirror, v, rd);
+                    mg_epilogue<KIND>(p, g, staging + e * kMgWarpStaging, t.b, i0, j0 + ch * 32, t.mirror, v, rd);
                 }
             }
             tc_fence_before();

@@ -320,15 +320,15 @@ struct MuonOperand {
     long long bs;
 };
 
-template <int BN>
-int muon_product_bn(const MuonPlan& pl, const wg::MuonParams& p, wg::MuonProduct& g, const MuonOperand& oa,
+template <int BN, int KIND>
+int muon_product_launch(const MuonPlan& pl, const wg::MuonParams& p, wg::MuonProduct& g, const MuonOperand& oa,
                     const MuonOperand& ob, cudaStream_t s)
 {
     const int used = g.whole ? g.pairs : std::max(g.cut, 1);
     CUtensorMap ta, tb;
     int st = muon_map(&ta, oa.base, oa.cols, oa.rows, p.batch, oa.ld, oa.bs, g.a_mn ? 64 : 128);
     if (!st) st = muon_map(&tb, ob.base, ob.cols, ob.rows, p.batch, ob.ld, ob.bs, g.b_mn ? 64 : BN / 2);
-    if (!st) st = wg::ensure_smem(wg::muon_product_kernel<BN>, wg::Mg<BN>::kSmem);
+    if (!st) st = wg::ensure_smem(wg::muon_product_kernel<BN, KIND>, wg::Mg<BN>::kSmem);
     if (st) return st;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
@@ -341,8 +341,21 @@ int muon_product_bn(const MuonPlan& pl, const wg::MuonParams& p, wg::MuonProduct
     cfg.gridDim = dim3((unsigned)(2 * used));
     cfg.blockDim = dim3(wg::kMgThreads);
     cfg.dynamicSmemBytes = wg::Mg<BN>::kSmem;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, wg::muon_product_kernel<BN>, ta, tb, p, g);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, wg::muon_product_kernel<BN, KIND>, ta, tb, p, g);
     return e == cudaSuccess ? WG_OK : cuda_fail("muon_product_kernel launch", e);
+}
+
+template <int BN>
+int muon_product_bn(const MuonPlan& pl, const wg::MuonParams& p, wg::MuonProduct& g, const MuonOperand& oa,
+                    const MuonOperand& ob, cudaStream_t s)
+{
+    switch (g.kind) {
+        case wg::kMuonA: return muon_product_launch<BN, wg::kMuonA>(pl, p, g, oa, ob, s);
+        case wg::kMuonB: return muon_product_launch<BN, wg::kMuonB>(pl, p, g, oa, ob, s);
+        case wg::kMuonX: return muon_product_launch<BN, wg::kMuonX>(pl, p, g, oa, ob, s);
+        case wg::kMuonLast: return muon_product_launch<BN, wg::kMuonLast>(pl, p, g, oa, ob, s);
+        default: return muon_product_launch<BN, wg::kMuonLastAny>(pl, p, g, oa, ob, s);
+    }
 }
 
 // One product over a sum of length K.
@@ -438,14 +451,14 @@ int muon_run(const MuonPlan& pl, const void* grad, void* momentum, void* weight,
         const int in = i & 1;
         wg::MuonProduct g = {};
         g.a = pl.coef[i][0], g.b = pl.coef[i][1], g.c = pl.coef[i][2];
-        g.xin = in, g.last = i == q.steps - 1, g.ovec = ovec;
+        g.xin = in;
         g.part = reinterpret_cast<float*>(ws + pl.off_sums), g.arrived = p.arrived;
-        g.stage = 0, g.M = g.N = pl.m, g.sym = 1;
+        g.kind = wg::kMuonA, g.M = g.N = pl.m, g.sym = 1;
         g.a_mn = g.b_mn = !wide;
         if ((st = muon_product(pl, p, g, x[in], x[in], std::max(q.rows, q.cols), s))) return st;
-        g.stage = 1, g.a_mn = g.b_mn = 0;
+        g.kind = wg::kMuonB, g.a_mn = g.b_mn = 0;
         if ((st = muon_product(pl, p, g, ma, ma, pl.m, s))) return st;
-        g.stage = 2, g.M = q.rows, g.N = q.cols, g.sym = 0;
+        g.kind = i < q.steps - 1 ? wg::kMuonX : ovec ? wg::kMuonLast : wg::kMuonLastAny, g.M = q.rows, g.N = q.cols, g.sym = 0;
         g.b_mn = wide;
         st = wide ? muon_product(pl, p, g, mb, x[in], pl.m, s) : muon_product(pl, p, g, x[in], mb, pl.m, s);
         if (st) return st;
