@@ -20,8 +20,8 @@
 //
 // Main loop: 0.33 us per 64 of a 256 x 256 tile's sum on all pairs, 1.9 PFLOP/s,
 // the rate of a large library product.  Around it a launch costs some 7 us: 1 from
-// the kernel before (2 with the set-up after the wait for it, some 15 us of 1000 x 2731), 1.7 to the first operands, 3 to 6 for the last tile's
-// epilogue; 15 of them bound updates of up to some 1024 rows.  Each of the roles that
+// the kernel before (2 with the set-up after the wait for it, some 15 us of 1000 x
+// 2731), 1.7 to the first operands, 3 to 6 for the last tile's epilogue; 15 of them bound updates of up to some 1024 rows.  Each of the roles that
 // touch global memory waits for the kernel before by itself, after it has found its
 // first tile.
 #pragma once

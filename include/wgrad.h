@@ -339,7 +339,9 @@ WG_API int wg_bwd_data_plan_string(const wg_problem* p, char* buf, size_t n);
  * 16-bit operands and fp32 sums (X carried to 22 bits beside its 16-bit operand).
  * X's relative error (2-norm of all elements) is below 4e-3 in either form on
  * gradients of rank 1 to full rank; out and w are then rounded to nearest even.
- * A zero matrix gives zeros; a NaN or an infinity in u makes its matrix's X NaN.
+ * A zero matrix gives zeros; a NaN or an infinity in u makes its matrix's X NaN, and
+ * so does |u|_F above 1.8e19, whose square is beyond fp32 (elements below 1e-22 count
+ * as zero beside it).
  * Results are bitwise reproducible from run to run.
  *
  *  batch >= 1, rows >= 1, cols >= 1; rows, cols <= 32768; batch <= 65535.
@@ -391,7 +393,8 @@ WG_API int wg_muon_update(const wg_muon_problem* p, const void* grad, void* mome
  *  tokens in 0..2^31-256 (0: a lookup does nothing, a gradient is zero), vocab and
  *  dim in 1..2^31-65536.
  *  ld_table, ld_out: elements between rows of table / dtable and of out / dy;
- *    0 = dim.  Elements between rows are neither read nor written.
+ *    0 = dim.  Elements between rows are not used and not written (rows of dy that
+ *    start anywhere are fetched in the aligned 16 bytes around them, within dy).
  *  table_dtype: table and dtable; out_dtype: out and dy (WG_FP32, WG_BF16, WG_FP16).
  *  token_bits: 32 or 64 (signed integers).
  *  padding_token: a token whose row takes no gradient; -1 = none.
