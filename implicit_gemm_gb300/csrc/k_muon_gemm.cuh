@@ -59,7 +59,10 @@ enum MuonKind {
 
 struct MuonProduct {
     int kind, xin;
-    float a, b, c;
+    // The last two steps take B + t I and a - t: where B's eigenvalues are near -t, the
+    // product is small, and so are its roundings beside a X, which has 22 bits.
+    float a, b, c;            // (a: less t)
+    float tc;                 // t in units of the sums of A A
     int a_mn, b_mn;           // operand is read across its rows
     int M, N, kb;             // extents of D, 64-wide blocks of the sum
     int tm, tn, sym;          // tiles along M and N of a matrix
@@ -229,6 +232,9 @@ __device__ __forceinline__ void mg_epilogue(const MuonParams& p, const MuonProdu
             }
             __syncwarp();
             const float c = g.c * 0x1p-10f;
+            if (i0 == j)  // t I (see MuonProduct)
+#pragma unroll
+                for (int k = 0; k < 32; ++k) v[k] += lane == k ? g.tc : 0.f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const uint4 y = *reinterpret_cast<const uint4*>(own + ((k ^ osw) << 4));
