@@ -60,7 +60,15 @@ struct GramParams {
 
 __host__ __device__ constexpr int gram_mat_bytes(int P) { return P * P * 2; }  // one fp16 image
 // Three pairs of images, and slack for A operands of 128 rows read from images of 64.
-__host__ __device__ constexpr int gram_smem_bytes(int P) { return 6 * gram_mat_bytes(P) + 8192 + 2048; }
+__host__ __device__ constexpr int gram_used_bytes(int P) { return 6 * gram_mat_bytes(P) + 8192 + 1024; }
+// What is asked for: all that a CTA may have beside the static variables, so that no
+// other CTA that takes tensor memory, of this kernel or another, is on the SM.  A CTA
+// takes all of tensor memory and then waits for its cluster; two clusters of two
+// streams that share a pair of SMs would each hold what the other waits for, and
+// tcgen05.alloc has no limit.
+constexpr int kGramSmem = 224 * 1024;
+static_assert(gram_used_bytes(128) <= kGramSmem, "shared memory of a CTA");
+static_assert(2 * kGramSmem > 228 * 1024, "one CTA on an SM");
 
 // Byte offset of the 16-byte chunk that holds elements 8 c8 .. 8 c8 + 7 of row r of a K-major image of P rows:
 // 64-element (128-byte) columns of P rows, 128-byte swizzle.

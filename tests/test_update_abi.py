@@ -139,3 +139,11 @@ def test_wrappers_refuse_tensors_that_do_not_fit():
     bad("out holds fewer", up, spec=muon(ld=48), grad=torch.zeros((24, 48))[:, :40], out=torch.zeros((24, 40), dtype=b16))
     bad("grad holds fewer", up, spec=muon(batch=2, batch_stride=1000), grad=torch.zeros(1959))
     bad("grad is not a CUDA tensor", up, spec=muon(), grad=g)
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 1), (8, 72), (64, 576), (128, 128), (300, 400)])
+def test_muon_kernels_take_an_sm_whole(rows, cols):
+    """A CTA of these kernels takes tensor memory and then waits for its cluster: two that shared an SM could wait for
+    each other for ever.  They ask for (nearly) all of an SM's 228 KB of shared memory."""
+    plan = dict(kv.split("=") for kv in binding.wg_muon_plan_string(muon(rows=rows, cols=cols)).split())
+    assert int(plan["smem"]) >= 224 * 1024
