@@ -295,9 +295,9 @@ def conv_bwd_data(spec: dict, dy, w, out=None, stream=None):
     import torch
     tdt = {"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16}[spec.get("out_dtype", "fp32")]
     if out is None:
-        out = torch.empty((spec["N"], *spec["in"], spec["G"], spec["C"]), dtype=tdt, device=dy.device)
+        out = _empty(stream, (spec["N"], *spec["in"], spec["G"], spec["C"]), tdt, dy.device, returned=True)
     nbytes = wg_bwd_data_workspace_size(spec)
-    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dy.device) if nbytes else None
+    ws = _empty(stream, nbytes, torch.uint8, dy.device) if nbytes else None
     wg_conv_bwd_data(spec, dy, w, out, ws, nbytes, stream)
     return out
 
@@ -341,6 +341,22 @@ def _stream_handle(stream):
     return int(stream.cuda_stream)
 
 
+def _empty(stream, shape, dtype, device, returned: bool = False):
+    """torch.empty for a call on `stream` (None: the current one).  The memory comes from that stream's own blocks: one
+    of the current stream's may still be in use by work that is pending there, which `stream` does not wait for.
+    `returned`: the caller gets the tensor, so work on the current stream may use it too."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
+    on = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream_handle(stream), device)
+    with torch.cuda.stream(on):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(here)
+    return t
+
+
 def conv_bwd_weight(spec: dict, x, dy, split_k: int = 0, mode: str = "auto", group_merge: int = 0, out=None,
                     stream=None, *, cluster: int = 0, kernel: str = "auto"):
     """Convenience wrapper over wg_conv_bwd_weight for torch CUDA tensors: allocates dW
@@ -349,9 +365,9 @@ def conv_bwd_weight(spec: dict, x, dy, split_k: int = 0, mode: str = "auto", gro
     import torch
     tdt = {"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16}[spec.get("out_dtype", "fp32")]
     if out is None:
-        out = torch.empty((spec["G"], spec["K"], *spec["filt"], spec["C"]), dtype=tdt, device=x.device)
+        out = _empty(stream, (spec["G"], spec["K"], *spec["filt"], spec["C"]), tdt, x.device, returned=True)
     nbytes = wg_workspace_size(spec, split_k, mode, group_merge, cluster=cluster, kernel=kernel)
-    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=x.device) if nbytes else None
+    ws = _empty(stream, nbytes, torch.uint8, x.device) if nbytes else None
     wg_conv_bwd_weight(spec, x, dy, out, split_k, mode, group_merge, ws, nbytes, stream, cluster=cluster,
                        kernel=kernel)
     return out
@@ -427,17 +443,6 @@ class PreparedMuonUpdate:
             _check(st)
 
 
-def _on(stream, *tensors):
-    """Tell torch's allocator that `tensors` (made on the current stream) are used on `stream`, so that their
-    memory is not handed out again while that stream still works on them."""
-    if stream is None:
-        return
-    import torch
-    s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
-    for t in tensors:
-        t.record_stream(s)
-
-
 def _expect(name, t, dtype: str, shape=None, elements: int = 0) -> None:
     """Refuse a tensor that is not what the call will take it for: of `dtype`, contiguous and of `shape`, or (no shape)
     with `elements` elements from its first one on."""
@@ -481,11 +486,10 @@ def muon_update(spec: dict, grad, momentum=None, weight=None, out=None, stream=N
     if made:
         tdt = {"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16}[types["out"]]
         if spec.get("ld", 0) or bs:
-            out = torch.empty(span, dtype=tdt, device=grad.device).as_strided((b, rows, cols), (bs or rows * ld, ld, 1))
+            out = _empty(stream, span, tdt, grad.device, returned=True).as_strided((b, rows, cols), (bs or rows * ld, ld, 1))
         else:
-            out = torch.empty_like(grad, dtype=tdt)
-    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=grad.device)
-    _on(stream, ws, *([out] if made else []))
+            out = _empty(stream, grad.shape, tdt, grad.device, returned=True)
+    ws = _empty(stream, max(nbytes, 1), torch.uint8, grad.device)
     wg_muon_update(spec, grad, momentum, weight, out, ws, nbytes, stream)
     return out if out is not None else weight
 
@@ -573,7 +577,6 @@ def _embedding_spec(token, vocab, dim, table_dtype, out_dtype, scale, padding_to
 def embedding_lookup(token, table, scale: float = 1.0, out=None, stream=None):
     """Convenience wrapper over wg_embedding_lookup for torch CUDA tensors: contiguous int32 or int64 tokens of any
     shape, a contiguous (vocab, dim) table.  Returns (*token.shape, dim) in table's dtype (or `out`)."""
-    import torch
     vocab, dim = table.shape
     made = out is None
     spec = _embedding_spec(token, vocab, dim, table.dtype, table.dtype if made else out.dtype, scale, -1)
@@ -581,8 +584,7 @@ def embedding_lookup(token, table, scale: float = 1.0, out=None, stream=None):
     _expect("out", out, spec["out_dtype"], (*token.shape, dim))
     _on_gpu(token=token, table=table, out=out)
     if made:
-        out = torch.empty((*token.shape, dim), dtype=table.dtype, device=table.device)
-        _on(stream, out)
+        out = _empty(stream, (*token.shape, dim), table.dtype, table.device, returned=True)
     wg_embedding_lookup(spec, token, table, out, stream)
     return out
 
@@ -601,9 +603,7 @@ def embedding_bwd_weight(token, dy, vocab: int, scale: float = 1.0, padding_toke
     _expect("out", out, spec["table_dtype"], (vocab, dim))
     _on_gpu(token=token, dy=dy, out=out)
     if made:
-        out = torch.empty((vocab, dim), dtype=dy.dtype, device=dy.device)
-        _on(stream, out)
-    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dy.device)
-    _on(stream, ws)
+        out = _empty(stream, (vocab, dim), dy.dtype, dy.device, returned=True)
+    ws = _empty(stream, max(nbytes, 1), torch.uint8, dy.device)
     wg_embedding_bwd_weight(spec, token, dy, out, accumulate, ws, nbytes, stream)
     return out
