@@ -16,8 +16,9 @@
 //
 // A block of P = 64 or 128 rows of the Gram matrix holds as many whole matrices
 // as fit (the block-diagonal fold of the convolution kernels): entries of A_0
-// between different matrices are set to zero, and products keep them so.  A matrix
-// that holds a NaN or an infinity enters as zeros and leaves as NaN, so that it
+// between different matrices are set to zero, and products keep them so.  Elements that
+// are NaN, infinite or at least 2^64 (whose square is beyond fp32, and which bf16 may
+// round to infinity) enter as zeros, and their matrix leaves as NaN, so that they
 // cannot reach the others of its block.
 //
 // A cluster of C CTAs takes a block.  Each adds up U U^T over its 64-column
@@ -413,17 +414,17 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
         for (int j = 0; j < P / 64; ++j) {
             float v[8];
             gram_make<VEC, decltype(step)::value>(g, blk, addr(ch, j), pos(ch, j), u[j], v);
-            float odd = 0.f;  // NaN when one of them is a NaN or an infinity
+            float odd = 0.f;  // not finite when one of them is a NaN or of 2^64 or more
 #pragma unroll
-            for (int k = 0; k < 8; ++k) odd = fmaf(v[k], 0.f, odd);
-            if (odd != 0.f)
+            for (int k = 0; k < 8; ++k) odd = fmaf(v[k], 0x1p64f, odd);
+            if (!(fabsf(odd) < INFINITY))
 #pragma unroll 1
                 for (int k = 0; k < 8; ++k) {
                     float x = 0.f;
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
                         if (q == k) x = v[q];
-                    if (fabsf(x) < INFINITY) continue;
+                    if (fabsf(x) < 0x1p64f) continue;
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
                         if (q == k) v[q] = 0.f;
