@@ -84,6 +84,21 @@ __device__ __forceinline__ void split8(const float* v, uint4* hi, uint4* lo)
     *lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
+// Eight values as three bf16 chunks, each of what those before it round away: 24 bits, fp32's.
+__device__ __forceinline__ void split8_bf16x3(const float* v, uint4* hi, uint4* mid, uint4* lo)
+{
+    float r[8];
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        h[i] = pack_bf162(v[2 * i], v[2 * i + 1]);
+        const float2 f = unpack_bf162(h[i]);
+        r[2 * i] = v[2 * i] - f.x, r[2 * i + 1] = v[2 * i + 1] - f.y;
+    }
+    *hi = make_uint4(h[0], h[1], h[2], h[3]);
+    split8<true>(r, mid, lo);
+}
+
 __device__ __forceinline__ void muon_store(void* out, int dtype, long long e, float v)
 {
     if (dtype == 2)

@@ -11,8 +11,12 @@
 // step, so A, P and Q keep 22 bits: every operand is a pair of fp16 values (what
 // the first rounds away is the second), a product three MMAs, sums fp32 in
 // tensor memory.  (With single fp16 operands gradients of low rank lose every
-// digit.)  U is a pair of bf16 values (16 bits; exact for 16-bit gradients), its
-// range is fp32's.
+// digit.)  U U^T takes u as up to three bf16 values, whose range is fp32's: one for
+// bf16 gradients, two for fp16, three for fp32 and with momentum (with two of fp32's
+// three, noise beside a strong direction came out up to 8% off).  X = Q U takes it as a
+// pair of fp16 values under its matrix's power of two, which the norm gives by then,
+// and so has all of Q's 22 bits (with Q as a pair of bf16 values gradients of rank one
+// were 3e-3 off, instead of 1e-4).
 //
 // A block of P = 64 or 128 rows of the Gram matrix holds as many whole matrices
 // as fit (the block-diagonal fold of the convolution kernels): entries of A_0
@@ -49,7 +53,7 @@ struct GramParams {
     int wide;        // rows <= cols
     int chunks;      // 64-column chunks of the long side
     int C;           // CTAs of a cluster
-    int split;       // U needs its second bf16 value
+    int parts;       // bf16 values that an element of u takes in U U^T
     int kn;          // 16-wide parts of a block's rows that are used
     int steps;
     // Per step: P = pa I + pb (TA) + pc (T2); S = rs (T2); Q = rq (TQ); A = ra (TA), the
@@ -342,7 +346,9 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bar[3];
     __shared__ uint32_t tslot;
-    __shared__ float diag[128], norm2[64], fac[128];  // of A_0; |u|_F^2 per matrix; scale / (|u|_F + eps) per row
+    __shared__ float diag[128], norm2[64];  // of A_0; |u|_F^2 per matrix
+    // Per row: the power of two under which u is staged for Q U, and what is left to multiply its results by.
+    __shared__ float up[128], fac[128];
     __shared__ int bad[128];
     uint8_t* smem = align_shared<uint8_t>(smem_raw, 1024);
     uint8_t *ba = smem, *bp = smem + PAIR, *bq = smem + 2 * PAIR;  // A (and A P), P, Q
@@ -380,7 +386,7 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
         for (int i = 0; i < 3; ++i) mbar_init(&bar[i], 1);
         fence_mbar_init();
     }
-    if (tid < 128) bad[tid] = 0;
+    if (tid < 128) bad[tid] = 0, up[tid] = 0.f;
     pdl_wait();
     if (warp == 0) {
         // After the wait: a CTA of the kernel before, which may be on this SM, may have yet
@@ -394,8 +400,8 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
     const uint32_t tb = tslot, trow = tb + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)c0;
 
     // ---------------------------------------------------- A_0 = U U^T over this CTA's chunks
-    // Two staged images (pairs), in A's place.  Wide: rows of the block, 64
-    // positions along; tall: 64 positions, the block's rows along, in 64-wide atoms.
+    // Two chunks' images (three each), where A, P and Q will be.  Wide: rows of the block,
+    // 64 positions along; tall: 64 positions, the block's rows along, in 64-wide atoms.
     const int line = tid >> 3, seg = (tid & 7) * 8;
     // Where this thread's eight elements of chunk 0 lie (-1: no matrix there), and of chunk ch.
     long long at0[P / 64];
@@ -430,11 +436,25 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
                         if (q == k) v[q] = 0.f;
                     bad[g.wide ? line + 64 * j : seg + 64 * j + k] = 1;
                 }
-            uint4 h, l;
-            split8<true>(v, &h, &l);
             uint8_t* o = img + j * 8192 + line * 128 + ((((tid & 7) ^ (line & 7))) << 4);
+            uint4 h, m, l;
+            if constexpr (decltype(step)::value) {
+                split8_bf16x3(v, &h, &m, &l);
+                if (g.parts > 2) *reinterpret_cast<uint4*>(o + 2 * IMG) = l;
+            } else {
+                // (|u| is below 2^14 then, and 0 where |u|_F is not finite.)
+                if (g.wide) {
+                    const float f = up[line + 64 * j];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] *= f;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] *= up[seg + 64 * j + k];
+                }
+                split8<false>(v, &h, &m);
+            }
             *reinterpret_cast<uint4*>(o) = h;
-            *reinterpret_cast<uint4*>(o + IMG) = l;
+            if (g.parts > 1) *reinterpret_cast<uint4*>(o + IMG) = m;
         }
     };
     auto load = [&](int ch, GramRaw (&u)[P / 64]) {
@@ -451,7 +471,7 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
 #pragma unroll 1
         for (int it = -AHEAD; it < nch; ++it) {
             if (it >= 2) wait(it & 1);
-            if (it >= 0) stage(ba + (it & 1) * 2 * IMG, rank + it * g.C, std::true_type{}, u[0]);
+            if (it >= 0) stage(ba + (it & 1) * 3 * IMG, rank + it * g.C, std::true_type{}, u[0]);
 #pragma unroll
             for (int j = 0; j < P / 64; ++j) u[0][j] = u[AHEAD - 1][j];
             load(rank + (it + AHEAD) * g.C, u[AHEAD - 1]);
@@ -466,17 +486,22 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
             __syncthreads();
             tc_fence_after();
             if (elect_one()) {
-                const uint32_t a = smem_u32(ba + (it & 1) * 2 * IMG);
+                const uint32_t a = smem_u32(ba + (it & 1) * 3 * IMG);
                 // Tall blocks of 64 rows: the second 64 rows of the MMA read the first again.
                 const uint64_t d = g.wide ? make_sdesc(a, 16u, 1024u, 2u, 0u)
                                           : make_sdesc(a, P == 128 ? 8192u : 0u, 1024u, 2u, 0u);
 #pragma unroll 1
                 for (int ks = 0; ks < 4; ++ks) {
-                    const uint64_t o = (uint64_t)(ks * (g.wide ? 2 : 128)), l = IMG >> 4;
-                    umma_f16(tb + TA, d + o, d + o, idesc, (it | ks) ? 1u : 0u);
-                    if (g.split) {
-                        umma_f16(tb + TA, d + o, d + o + l, idesc, 1u);
-                        umma_f16(tb + TA, d + o + l, d + o, idesc, 1u);
+                    const uint64_t h = d + (uint64_t)(ks * (g.wide ? 2 : 128)), m = h + (IMG >> 4), l = m + (IMG >> 4);
+                    umma_f16(tb + TA, h, h, idesc, (it | ks) ? 1u : 0u);
+                    if (g.parts > 1) {
+                        umma_f16(tb + TA, h, m, idesc, 1u);
+                        umma_f16(tb + TA, m, h, idesc, 1u);
+                        umma_f16(tb + TA, m, m, idesc, 1u);
+                    }
+                    if (g.parts > 2) {  // (What the others make is below 2^-26 of the first.)
+                        umma_f16(tb + TA, h, l, idesc, 1u);
+                        umma_f16(tb + TA, l, h, idesc, 1u);
                     }
                 }
                 umma_commit(&bar[it & 1]);
@@ -576,10 +601,16 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
         if (act) {
             // A_0 = U U^T / (|u|_F + eps)^2, zero between matrices.
             const float s = mine < g.F ? norm2[mine] : 0.f;
-            const float d = sqrtf(s) + p.eps;
+            const float norm = sqrtf(s), d = norm + p.eps;
             const bool fin = s < INFINITY;
             const float inv = fin && d > 0.f ? 1.f / d : 0.f;
-            if (c0 == 0) fac[row] = fin ? p.scale * inv : NAN;
+            if (c0 == 0) {
+                // |u| < 2^(e + 1); below 2^-60 s may have lost squares, and u keeps its bits all the same.
+                const int e = max((int)(__float_as_uint(norm) >> 23) - 127, -60);
+                up[row] = fin ? __uint_as_float((uint32_t)(127 + 13 - e) << 23) : 0.f;
+                const float down = __uint_as_float((uint32_t)(127 - 13 + e) << 23);
+                fac[row] = fin ? p.scale * (inv * down) / g.step[g.steps - 1].sq : NAN;
+            }
 #pragma unroll 1
             for (int h = 0; h < NC; h += 16) {
                 float v[16];
@@ -610,17 +641,6 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
                 gram_put<P, 16>(img, row, c0 + h, v, f);
             }
         };
-        // Q as a pair of bf16 images, in Q's place.
-        auto put_q = [&](int h, const float (&v)[16]) {
-#pragma unroll
-            for (int i = 0; i < 16; i += 8) {
-                uint4 hi8, lo8;
-                split8<true>(v + i, &hi8, &lo8);
-                uint8_t* o = bq + gram_off<P>(row, (c0 + h + i) >> 3);
-                *reinterpret_cast<uint4*>(o) = hi8;
-                *reinterpret_cast<uint4*>(o + MAT) = lo8;
-            }
-        };
         const uint32_t diagonal = row >= c0 && row < c0 + NC ? 1u << (row - c0) : 0u;
         for (int k = 0; k < g.steps; ++k) {
             const bool last = k == g.steps - 1;
@@ -639,41 +659,27 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
                         v[i] = fmaf(w.pc, v[i], w.pb * x[i]);
                         if (diagonal >> (h + i) & 1u) v[i] += w.pa;
                     }
-                    if (last && k == 0) {
-                        put_q(h, v);
-                        continue;
-                    }
-                    gram_put<P, 16>(bp, row, c0 + h, v, w.sp);
+                    if (k > 0 || !last) gram_put<P, 16>(bp, row, c0 + h, v, w.sp);
                     if (k == 0) gram_put<P, 16>(bq, row, c0 + h, v, w.sq);
                 }
             }
             if (last && k == 0) break;
             ready();
-            if (!last) {
-                wait(0);
-                if (act) convert(T2, w.rs * w.ss, ba);  // S = A P, in A's place
-                ready();
-            }
+            if (last) break;
+            wait(0);
+            if (act) convert(T2, w.rs * w.ss, ba);  // S = A P, in A's place
+            ready();
             if (k > 0) {
                 wait(1);
-                if (act && !last) convert(TQ, w.rq * w.sq, bq);
+                if (act) convert(TQ, w.rq * w.sq, bq);
             }
-            if (!last) {
-                wait(2);
-                if (act) convert(TA, w.ra * g.step[k + 1].sa, ba);
-            }
+            wait(2);
+            if (act) convert(TA, w.ra * g.step[k + 1].sa, ba);
         }
         load(rank, u);  // the first chunk of U comes back
-        if (act && g.steps > 1) {
-            const float f = g.step[g.steps - 1].rq;
-#pragma unroll 1
-            for (int h = 0; h < NC; h += 16) {
-                float v[16];
-                gram_sums<P, 16>(trow + TQ + h, v);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] *= f;
-                put_q(h, v);
-            }
+        if (g.steps > 1) {
+            wait(1);
+            if (act) convert(TQ, g.step[g.steps - 1].rq * g.step[g.steps - 1].sq, bq);
         }
     }
 
@@ -764,7 +770,7 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
             }
         }
     } else {
-        const uint32_t idesc = make_idesc_f16(true, false, g.wide != 0, 128, 64);
+        const uint32_t idesc = make_idesc_f16(false, false, g.wide != 0, 128, 64);
         const uint64_t qd = make_sdesc(smem_u32(bq), 16u, 1024u, 2u, 0u);
         for (int it = 0; it < nch; ++it) {
             __syncthreads();
@@ -779,7 +785,7 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
                     const uint64_t uo = g.wide ? (uint64_t)(128 * ks) : (uint64_t)((ks >> 2) * 512 + 2 * (ks & 3));
                     umma_f16(d, qd + qo, ud + uo, idesc, ks ? 1u : 0u);
                     umma_f16(d, qd + qo + ql, ud + uo, idesc, 1u);
-                    if (g.split) umma_f16(d, qd + qo, ud + uo + ul, idesc, 1u);
+                    if (g.parts > 1) umma_f16(d, qd + qo, ud + uo + ul, idesc, 1u);
                 }
                 umma_commit(&bar[it & 1]);
             }

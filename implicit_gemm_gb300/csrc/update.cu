@@ -425,7 +425,7 @@ int muon_run(const MuonPlan& pl, const void* grad, void* momentum, void* weight,
         g.p = p;
         const bool al = q.cols % 8 == 0 && q.ld % 8 == 0 && q.batch_stride % 8 == 0;
         const bool vec = al && aligned16(grad) && aligned16(momentum) && aligned16(weight) && aligned16(out);
-        g.split = momentum || q.grad_dtype != WG_BF16;
+        g.parts = momentum || q.grad_dtype == WG_FP32 ? 3 : q.grad_dtype == WG_FP16 ? 2 : 1;
         if (vec) return pl.P == 64 ? muon_gram_launch<64, true>(pl, g, s) : muon_gram_launch<128, true>(pl, g, s);
         return pl.P == 64 ? muon_gram_launch<64, false>(pl, g, s) : muon_gram_launch<128, false>(pl, g, s);
     }
