@@ -21,6 +21,7 @@ namespace wg {
 struct MuonParams {
     int batch, rows, cols;
     long long ld, bs;
+    long long gld, gbs;  // the same of grad and mom where the Gram kernel reads them
     const void* grad;
     float* mom;
     void* weight;

@@ -25,6 +25,10 @@
 // round to infinity) enter as zeros, and their matrix leaves as NaN, so that they
 // cannot reach the others of its block.
 //
+// Errors of A grow by a^2 a step, so a launch takes no more steps than its bits carry
+// (see muon_gram_plan): X is multiplied out then, and the next launch starts from X and
+// its own Gram matrix.
+//
 // A cluster of C CTAs takes a block.  Each adds up U U^T over its 64-column
 // chunks of the long side (the momentum's step on the way); each adds a slice of
 // the C partial sums through distributed shared memory and gives it to all; all
@@ -56,6 +60,7 @@ struct GramParams {
     int parts;       // bf16 values that an element of u takes in U U^T
     int kn;          // 16-wide parts of a block's rows that are used
     int steps;
+    int raw;         // what is read is X of the launch before: no norm
     // Per step: P = pa I + pb (TA) + pc (T2); S = rs (T2); Q = rq (TQ); A = ra (TA), the
     // tensor-memory sums holding products of operands scaled by sa, sp, ss and sq (powers of two).
     struct Step {
@@ -133,8 +138,13 @@ __device__ __forceinline__ void gram_put(uint8_t* img, int r, int c0, const floa
 // (symmetric up to roundings) transposes the roundings of Q between a direction
 // the matrix has and one it lacks, which are 482 times larger on one side than on
 // the other: gradients of rank one were 10% off.
+// The small products come first, or apart: every MMA cuts its sums off at fp32's last
+// bit, towards zero, and so each one that adds to the large sums makes them smaller.
+// (24 in turn took up to 4e-7 of A A.  With factors that fall from 8.3, whose map has a
+// slope of 3e4 at 1, 128 x 128 of rank one was 1.0e-2 off; 3.3e-3 with this and with
+// what muon_gram_plan puts back.)
 // P = 64: the two images of Y lie one after the other, and one MMA of 128 columns
-// multiplies both: hi hi + lo hi in columns 0 .. 63, hi lo in columns 64 .. 127 (an
+// multiplies both: hi hi in columns 0 .. 63, hi lo (and lo hi) in columns 64 .. 127 (an
 // MMA takes some 66 cycles whatever its columns up to 128: 2 instead of 3).
 template <int P>
 __device__ __forceinline__ void gram_product(uint32_t d, uint32_t x, uint32_t y, int kn)
@@ -148,12 +158,16 @@ __device__ __forceinline__ void gram_product(uint32_t d, uint32_t x, uint32_t y,
         const uint64_t xo = (uint64_t)((ks >> 2) * (P * 8) + 2 * (ks & 3)), yo = (uint64_t)(128 * ks);
         if (P == 64) {
             umma_f16(d, xd + xo, yd + yo, idesc2, ks ? 1u : 0u);
+            umma_f16(d + 64, xd + xo + lo, yd + yo, idesc, 1u);
         } else {
-            umma_f16(d, xd + xo, yd + yo, idesc, ks ? 1u : 0u);
-            umma_f16(d, xd + xo, yd + yo + lo, idesc, 1u);
+            umma_f16(d, xd + xo, yd + yo + lo, idesc, ks ? 1u : 0u);
+            umma_f16(d, xd + xo + lo, yd + yo, idesc, 1u);
         }
-        umma_f16(d, xd + xo + lo, yd + yo, idesc, 1u);
     }
+    if (P == 64) return;
+#pragma unroll 1
+    for (int ks = 0; ks < kn; ++ks)
+        umma_f16(d, xd + (uint64_t)((ks >> 2) * (P * 8) + 2 * (ks & 3)), yd + (uint64_t)(128 * ks), idesc, 1u);
 }
 
 // NC columns of a product, from column c0 (and of its second half).
@@ -205,7 +219,7 @@ __device__ __forceinline__ void gram_each(const GramParams& g, int blk, long lon
     for (int k = 0; k < 8; ++k) {
         f(k, e, e0 >= 0 && (g.wide ? idx < g.N : at < nf));
         ++e, ++idx;
-        if (!g.wide && idx == p.m) idx = 0, ++at, e += p.bs - p.m;
+        if (!g.wide && idx == p.m) idx = 0, ++at, e += p.gbs - p.m;
     }
 }
 
@@ -408,11 +422,11 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
 #pragma unroll
     for (int j = 0; j < P / 64; ++j) {
         const int i = (g.wide ? line : seg) + 64 * j, f = i / p.m, b = blk * g.F + f, idx = i - f * p.m;
-        at0[j] = f >= g.F || b >= p.batch ? -1 : (long long)b * p.bs + (g.wide ? idx * p.ld + seg : line * p.ld + idx);
+        at0[j] = f >= g.F || b >= p.batch ? -1 : (long long)b * p.gbs + (g.wide ? idx * p.gld + seg : line * p.gld + idx);
     }
     auto addr = [&](int ch, int j) -> long long {
         if (at0[j] < 0 || ch * 64 + (g.wide ? seg : line) >= g.N) return -1;
-        return at0[j] + ch * (g.wide ? 64 : 64 * p.ld);
+        return at0[j] + ch * (g.wide ? 64 : 64 * p.gld);
     };
     auto pos = [&](int ch, int j) { return g.wide ? ch * 64 + seg : seg + 64 * j; };
     auto stage = [&](uint8_t* img, int ch, auto step, const GramRaw (&u)[P / 64]) {
@@ -493,15 +507,16 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
 #pragma unroll 1
                 for (int ks = 0; ks < 4; ++ks) {
                     const uint64_t h = d + (uint64_t)(ks * (g.wide ? 2 : 128)), m = h + (IMG >> 4), l = m + (IMG >> 4);
+                    // The small products have sums of their own (see gram_product).
                     umma_f16(tb + TA, h, h, idesc, (it | ks) ? 1u : 0u);
                     if (g.parts > 1) {
-                        umma_f16(tb + TA, h, m, idesc, 1u);
-                        umma_f16(tb + TA, m, h, idesc, 1u);
-                        umma_f16(tb + TA, m, m, idesc, 1u);
+                        umma_f16(tb + T2, h, m, idesc, (it | ks) ? 1u : 0u);
+                        umma_f16(tb + T2, m, h, idesc, 1u);
+                        umma_f16(tb + T2, m, m, idesc, 1u);
                     }
                     if (g.parts > 2) {  // (What the others make is below 2^-26 of the first.)
-                        umma_f16(tb + TA, h, l, idesc, 1u);
-                        umma_f16(tb + TA, l, h, idesc, 1u);
+                        umma_f16(tb + T2, h, l, idesc, 1u);
+                        umma_f16(tb + T2, l, h, idesc, 1u);
                     }
                 }
                 umma_commit(&bar[it & 1]);
@@ -517,6 +532,12 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
         for (int h = 0; h < NC; h += 16) {
             float v[16];
             gram_ld<16>(trow + TA + h, v);
+            if (g.parts > 1) {
+                float x[16];
+                gram_ld<16>(trow + T2 + h, x);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] += x[i];
+            }
 #pragma unroll
             for (int i = 0; i < 16; i += 4)
                 *reinterpret_cast<float4*>(bp + row * (P * 4) + (((((c0 + h + i) >> 2)) ^ (row & 7)) << 4)) =
@@ -603,7 +624,7 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
             const float s = mine < g.F ? norm2[mine] : 0.f;
             const float norm = sqrtf(s), d = norm + p.eps;
             const bool fin = s < INFINITY;
-            const float inv = fin && d > 0.f ? 1.f / d : 0.f;
+            const float inv = g.raw ? 1.f : fin && d > 0.f ? 1.f / d : 0.f;
             if (c0 == 0) {
                 // |u| < 2^(e + 1); below 2^-60 s may have lost squares, and u keeps its bits all the same.
                 const int e = max((int)(__float_as_uint(norm) >> 23) - 127, -60);
@@ -780,12 +801,13 @@ __global__ void __launch_bounds__(kGramBlock, 1) muon_gram_kernel(const __grid_c
                 const uint64_t ud = g.wide ? make_sdesc(img, 8192u, 1024u, 2u, 0u) : make_sdesc(img, 16u, 1024u, 2u, 0u);
                 const uint64_t ql = MAT >> 4, ul = IMG >> 4;
 #pragma unroll 1
-                for (int ks = 0; ks < g.kn; ++ks) {
+                for (int i = 0; i < 2 * g.kn; ++i) {  // the small products first (see gram_product)
+                    const bool large = i >= g.kn;
+                    const int ks = large ? i - g.kn : i;
                     const uint64_t qo = (uint64_t)((ks >> 2) * (P * 8) + 2 * (ks & 3));
                     const uint64_t uo = g.wide ? (uint64_t)(128 * ks) : (uint64_t)((ks >> 2) * 512 + 2 * (ks & 3));
-                    umma_f16(d, qd + qo, ud + uo, idesc, ks ? 1u : 0u);
-                    umma_f16(d, qd + qo + ql, ud + uo, idesc, 1u);
-                    if (g.parts > 1) umma_f16(d, qd + qo, ud + uo + ul, idesc, 1u);
+                    umma_f16(d, qd + qo + (large ? 0 : ql), ud + uo, idesc, i ? 1u : 0u);
+                    if (!large && g.parts > 1) umma_f16(d, qd + qo, ud + uo + ul, idesc, 1u);
                 }
                 umma_commit(&bar[it & 1]);
             }

@@ -76,7 +76,8 @@ struct MuonPlan {
     wg_muon_problem p;
     float coef[kMuonMaxSteps][3];
     bool gram;            // the Gram-matrix kernel
-    wg::GramParams g;     // its problem (pointers are set by the call)
+    wg::GramParams g;     // its problem (pointers are set by the call), with every launch's steps
+    int launches, first[kMuonMaxSteps + 1];  // its launches, and the first step of each (and the end)
     int P, blocks;        // rows of a block of the Gram matrix, blocks
     int ldx, m, ldm, nparts;
     int pairs;
@@ -115,6 +116,18 @@ int muon_gram_max_cluster()
     return cache[dev] = n > 0 ? 16 : 8;
 }
 
+// Largest value over s in [0, smax] of what a step (a, b, c) makes of a singular value s,
+// and of the factor that it multiplies s by.
+void factor_range(const float* k, double smax, double* grown, double* factor)
+{
+    *grown = *factor = 0.0;
+    for (int i = 0; i <= 512; ++i) {
+        const double s = smax * i / 512, l = s * s, v = fabs(k[0] + k[1] * l + k[2] * l * l);
+        *grown = std::max(*grown, s * v);
+        *factor = std::max(*factor, v);
+    }
+}
+
 // The Gram-matrix kernel's problem: blocks of whole matrices, CTAs of a cluster,
 // and the powers of two that bring each operand's largest singular value to at
 // most 2^13 in fp16 (a factor of eight is left to roundings).
@@ -136,27 +149,59 @@ void muon_gram_plan(MuonPlan* pl)
     const int cmax = muon_gram_max_cluster();
     while (g.C < cmax && 2 * g.C <= g.chunks && 2LL * g.C * pl->blocks <= num_sms()) g.C *= 2;
     g.kn = (g.F * pl->m + 15) / 16;
-    double grid[513], prod[513], smax = 1.0;
-    for (int i = 0; i <= 512; ++i) grid[i] = i / 512.0, prod[i] = 1.0;
-    auto power = [](double bound) { return ldexpf(1.f, (int)floor(log2(8192.0 / std::max(bound, 1e-6)))); };
-    float ra = 1.f;  // A = ra * (its sums in tensor memory)
+    // Steps of a launch.  An error of A or Q in directions that u (nearly) lacks grows with
+    // the product of the steps' factors |a + b l + c l^2|, A's with its square.  The largest
+    // error of X in a simulation of every rounding, over spectra of one direction and noise
+    // of many sizes, for 3 x 7 (the worst) and 64 x 576: products of up to 600 in a launch
+    // (five default steps) 1.7e-3 and 3e-4, up to 170 (four) 1e-4 and 2e-5, 1,700 (six)
+    // 2e-2 and 3e-3, 5,800 (seven) 0.2 and 4e-2; beyond, A leaves [0, 1] and X is NaN.  So
+    // one launch up to 600, and where that is not enough launches of up to 170, with which
+    // six and seven steps are 1.2e-3 off at most (5e-4 for 64 x 576).
+    double factor[kMuonMaxSteps], all = 1.0, smax = 1.0;
     for (int k = 0; k < q.steps; ++k) {
-        const float* c = pl->coef[k];
-        wg::GramParams::Step& w = g.step[k];
-        double pmax = 0.0, spmax = 0.0, grown = 0.0, qmax = 0.0;
-        for (int i = 0; i <= 512; ++i) {
-            const double s = smax * i / 512, l = s * s, v = c[0] + c[1] * l + c[2] * l * l;
-            pmax = std::max(pmax, fabs(v)), spmax = std::max(spmax, l * fabs(v)), grown = std::max(grown, s * fabs(v));
-            const double t = grid[i] * grid[i], u = c[0] + c[1] * t + c[2] * t * t;
-            prod[i] *= u, grid[i] *= u;
-            qmax = std::max(qmax, fabs(prod[i]));
-        }
-        w.sa = power(smax * smax), w.sp = power(pmax), w.ss = power(spmax), w.sq = power(qmax);
-        w.pa = c[0], w.pb = c[1] * ra, w.pc = c[2] / (w.sa * w.sa);
-        w.rs = 1.f / (w.sa * w.sp);
-        w.rq = k ? 1.f / (w.sp * g.step[k - 1].sq) : 1.f;
-        w.ra = ra = 1.f / (w.ss * w.sp);
+        double grown;
+        factor_range(pl->coef[k], smax, &grown, &factor[k]);
+        all *= std::max(factor[k], 1.0);
         smax = std::max(grown, 1e-3);
+    }
+    pl->launches = 1, pl->first[0] = 0;
+    double part = 1.0;
+    for (int k = 0; k < q.steps; ++k) {
+        const double f = std::max(factor[k], 1.0);
+        if (all > 600.0 && k > 0 && part * f > 170.0) pl->first[pl->launches++] = k, part = 1.0;
+        part *= f;
+    }
+    pl->first[pl->launches] = q.steps;
+    auto power = [](double bound) { return ldexpf(1.f, (int)floor(log2(8192.0 / std::max(bound, 1e-6)))); };
+    // Every MMA cuts its sums off towards zero, by half a last bit in the mean (0.72 2^-24
+    // of a value whose digits are spread evenly in their logarithm), and n of them add to
+    // sums that grow evenly: what they leave out in the mean is put back.  (128 x 128 of
+    // rank one with factors that fall from 8.3, whose map has a slope of 3e4 at 1: see
+    // gram_product.)
+    const double put_back = 1.0 + 0.72 * 0x1p-24 * ((pl->m + 15) / 16 + 1) / 2;
+    smax = 1.0;
+    for (int n = 0; n < pl->launches; ++n) {
+        double grid[513], prod[513];
+        for (int i = 0; i <= 512; ++i) grid[i] = smax * i / 512, prod[i] = 1.0;
+        float ra = 1.f;  // A = ra * (its sums in tensor memory)
+        for (int k = pl->first[n]; k < pl->first[n + 1]; ++k) {
+            const float* c = pl->coef[k];
+            wg::GramParams::Step& w = g.step[k];
+            double pmax = 0.0, spmax = 0.0, grown = 0.0, qmax = 0.0;
+            for (int i = 0; i <= 512; ++i) {
+                const double s = smax * i / 512, l = s * s, v = c[0] + c[1] * l + c[2] * l * l;
+                pmax = std::max(pmax, fabs(v)), spmax = std::max(spmax, l * fabs(v)), grown = std::max(grown, s * fabs(v));
+                const double t = grid[i] * grid[i], u = c[0] + c[1] * t + c[2] * t * t;
+                prod[i] *= u, grid[i] *= u;
+                qmax = std::max(qmax, fabs(prod[i]));
+            }
+            w.sa = power(smax * smax), w.sp = power(pmax), w.ss = power(spmax), w.sq = power(qmax);
+            w.pa = c[0], w.pb = c[1] * ra, w.pc = (float)(c[2] / (w.sa * w.sa) * put_back);
+            w.rs = (float)(put_back / (w.sa * w.sp));
+            w.rq = k > pl->first[n] ? (float)(put_back / (w.sp * g.step[k - 1].sq)) : 1.f;
+            w.ra = ra = (float)(put_back / (w.ss * w.sp));
+            smax = std::max(grown, 1e-3);
+        }
     }
 }
 
@@ -218,7 +263,8 @@ int make_muon_plan(const wg_muon_problem* p, MuonPlan* pl)
     pl->gram = q.steps > 0 && pl->m <= 128;
     if (pl->gram) {
         muon_gram_plan(pl);
-        pl->bytes = 256;  // nothing is kept there; callers need no case for a form without a workspace
+        // X between launches; of one, nothing (callers need no case for a form without a workspace).
+        pl->bytes = pl->launches > 1 ? up256((size_t)q.batch * q.rows * q.cols * 4) : 256;
         return WG_OK;
     }
     const size_t x = up256((size_t)q.batch * q.rows * pl->ldx * 2), a = up256((size_t)q.batch * pl->m * pl->ldm * 2);
@@ -413,21 +459,38 @@ int muon_run(const MuonPlan& pl, const void* grad, void* momentum, void* weight,
 {
     const wg_muon_problem& q = pl.p;
     wg::MuonParams p = {};
-    p.batch = q.batch, p.rows = q.rows, p.cols = q.cols, p.ld = q.ld, p.bs = q.batch_stride;
+    p.batch = q.batch, p.rows = q.rows, p.cols = q.cols, p.ld = p.gld = q.ld, p.bs = p.gbs = q.batch_stride;
     p.grad = grad, p.mom = static_cast<float*>(momentum), p.weight = weight, p.out = out;
     p.grad_dtype = q.grad_dtype, p.out_dtype = q.out_dtype, p.weight_dtype = q.weight_dtype;
     p.nesterov = q.nesterov, p.mu = q.mu, p.gain = 1.f - q.dampening, p.eps = q.eps;
     p.scale = q.scale, p.keep = 1.f - q.lr * q.weight_decay, p.lr = q.lr;
     p.ldx = pl.ldx, p.m = pl.m, p.ldm = pl.ldm;
     p.xs = (long long)q.rows * pl.ldx, p.ms = (long long)pl.m * pl.ldm;
+    const bool al = q.cols % 8 == 0 && q.ld % 8 == 0 && q.batch_stride % 8 == 0;
     if (pl.gram) {
-        wg::GramParams g = pl.g;
-        g.p = p;
-        const bool al = q.cols % 8 == 0 && q.ld % 8 == 0 && q.batch_stride % 8 == 0;
-        const bool vec = al && aligned16(grad) && aligned16(momentum) && aligned16(weight) && aligned16(out);
-        g.parts = momentum || q.grad_dtype == WG_FP32 ? 3 : q.grad_dtype == WG_FP16 ? 2 : 1;
-        if (vec) return pl.P == 64 ? muon_gram_launch<64, true>(pl, g, s) : muon_gram_launch<128, true>(pl, g, s);
-        return pl.P == 64 ? muon_gram_launch<64, false>(pl, g, s) : muon_gram_launch<128, false>(pl, g, s);
+        for (int n = 0; n < pl.launches; ++n) {
+            const bool start = n == 0, end = n == pl.launches - 1;
+            wg::GramParams g = pl.g;
+            g.p = p;
+            g.steps = pl.first[n + 1] - pl.first[n];
+            std::copy(pl.g.step + pl.first[n], pl.g.step + pl.first[n + 1], g.step);
+            g.parts = momentum || q.grad_dtype == WG_FP32 ? 3 : q.grad_dtype == WG_FP16 ? 2 : 1;
+            if (!start) {  // X, packed
+                g.raw = 1, g.parts = 3;
+                g.p.grad = ws, g.p.grad_dtype = WG_FP32, g.p.mom = nullptr;
+                g.p.gld = q.cols, g.p.gbs = (long long)q.rows * q.cols;
+            }
+            if (!end) {  // (A CTA has read an element of X before it writes it, and no other CTA reads it.)
+                g.p.out = ws, g.p.out_dtype = WG_FP32, g.p.weight = nullptr, g.p.scale = 1.f;
+                g.p.ld = q.cols, g.p.bs = (long long)q.rows * q.cols;
+            }
+            const bool vec = (start ? al && aligned16(grad) && aligned16(momentum) : q.cols % 8 == 0) &&
+                             (end ? al && aligned16(weight) && aligned16(out) : q.cols % 8 == 0);
+            const int st = pl.P == 64 ? vec ? muon_gram_launch<64, true>(pl, g, s) : muon_gram_launch<64, false>(pl, g, s)
+                                      : vec ? muon_gram_launch<128, true>(pl, g, s) : muon_gram_launch<128, false>(pl, g, s);
+            if (st) return st;
+        }
+        return WG_OK;
     }
     p.part = reinterpret_cast<float*>(ws + pl.off_part), p.nparts = pl.nparts;
     if (q.steps > 0) {
@@ -437,7 +500,6 @@ int muon_run(const MuonPlan& pl, const void* grad, void* momentum, void* weight,
     }
     if (q.steps > 0)
         p.arrived = reinterpret_cast<int*>(ws + pl.off_arrived), p.narrived = pl.pairs * 2 * wg::kMgEpiWarps;
-    const bool al = q.cols % 8 == 0 && q.ld % 8 == 0 && q.batch_stride % 8 == 0;
     const bool ivec = al && aligned16(grad) && aligned16(momentum), ovec = al && aligned16(weight) && aligned16(out);
     const dim3 egrid(pl.nparts, q.batch);
     // Division of vector indexes (below 2^31) by the vectors of a row.
@@ -680,10 +742,10 @@ int wg_muon_plan_string(const wg_muon_problem* p, char* buf, size_t n)
     const int st = muon_plan(p, &pl);
     if (st) return st;
     if (pl.gram)
-        snprintf(buf, n, "kernel=muon_gram side=%s m=%d block=%d fold=%d blocks=%d cluster=%d chunks=%d steps=%d smem=%d "
-                 "ws=%zu",
+        snprintf(buf, n, "kernel=muon_gram side=%s m=%d block=%d fold=%d blocks=%d cluster=%d chunks=%d steps=%d launches=%d "
+                 "smem=%d ws=%zu",
                  p->rows <= p->cols ? "left" : "right", pl.m, pl.P, pl.g.F, pl.blocks, pl.g.C, pl.g.chunks, p->steps,
-                 wg::kGramSmem, pl.bytes);
+                 pl.launches, wg::kGramSmem, pl.bytes);
     else
         snprintf(buf, n, "kernel=muon_product side=%s m=%d steps=%d smem=%d ws=%zu", p->rows <= p->cols ? "left" : "right",
                  pl.m, p->steps, wg::Mg<256>::kSmem, pl.bytes);

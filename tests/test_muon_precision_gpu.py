@@ -100,3 +100,20 @@ def test_few_directions_and_steep_spectra(b, r, c, kind, momentum):
     binding.muon_update(sp, grad, momentum=mom, out=out)
     check(out, exact_x(u, [QUINTIC] * 5), [QUINTIC] * 5)
     binding.wg_check_status()
+
+
+SCHEDULES = {"6": [QUINTIC] * 6, "7": [QUINTIC] * 7, "8": [QUINTIC] * 8, "10": [QUINTIC] * 10, "16": [QUINTIC] * 16,
+             "cubic 16": [CUBIC] * 16, "8 + 2": [QUINTIC] * 8 + [CUBIC] * 2, "falling": FALLING,
+             "falling 8": FALLING + [CUBIC] * 3}
+
+
+@pytest.mark.parametrize("b,r,c", [(64, 3, 7), (32, 8, 72), (5, 100, 31), (2, 64, 576), (2, 128, 128), (1, 61, 1001)])
+@pytest.mark.parametrize("name", SCHEDULES)
+@pytest.mark.parametrize("kind", [("rank", 1, 0.0), ("rank", 8, 0.0), ("rank", 8, 1e-3), ("power", 2), ("rank", 1, 1.0)],
+                         ids=str)
+def test_many_steps_and_large_factors_of_small_matrices(b, r, c, name, kind):
+    coef = SCHEDULES[name]
+    grad = gradient(b + r + c, b, r, c, kind)
+    sp = {"batch": b, "rows": r, "cols": c, "out_dtype": "fp32", "steps": len(coef), "coef": coef}
+    check(binding.muon_update(sp, grad), exact_x(grad, coef), coef)
+    binding.wg_check_status()

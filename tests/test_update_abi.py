@@ -147,3 +147,20 @@ def test_muon_kernels_take_an_sm_whole(rows, cols):
     each other for ever.  They ask for (nearly) all of an SM's 228 KB of shared memory."""
     plan = dict(kv.split("=") for kv in binding.wg_muon_plan_string(muon(rows=rows, cols=cols)).split())
     assert int(plan["smem"]) >= 224 * 1024
+
+
+def test_muon_steps_of_a_launch():
+    """Small matrices: five default steps in one launch, without a workspace to speak of; more steps, or larger factors,
+    in several, with X kept in between."""
+    def plan(**kw):
+        sp = muon(**kw)
+        text = dict(kv.split("=") for kv in binding.wg_muon_plan_string(sp).split())
+        assert int(text["ws"]) == binding.wg_muon_workspace_size(sp)
+        return int(text["launches"]), int(text["ws"])
+
+    assert plan() == (1, 256) and plan(steps=1) == (1, 256)
+    assert plan(steps=16, coef=[(1.2, -0.2, 0.0)] * 16)[0] == 1
+    for kw in (dict(steps=6), dict(steps=16), dict(steps=2, coef=[(8.2872, -23.5959, 17.3004), (3.4, -2.0, 0.3)])):
+        n, ws = plan(**kw)
+        assert n == 1 and kw["steps"] == 2 or n > 1 and ws >= 24 * 40 * 4
+    assert plan(steps=4, coef=[(8.2872, -23.5959, 17.3004)] + [(3.9487, -2.9089, 0.5518)] * 3)[0] > 1
