@@ -10,7 +10,9 @@
 // (X by 2^8, A and B = b A + c A A by 2^10); X is carried as a second fp16
 // array of what the first one rounds away, used in the a X term: without it the
 // rounding of X costs up to 6e-3 of the result on gradients of low rank, with it
-// the result is within 2e-3.
+// the result is within 3e-3 after five default steps.  Where the steps make more of
+// A's and B's roundings (see muon_single_error) these have second arrays too, and a
+// product is three: two of a first and a second value, one of the first ones.
 #pragma once
 
 #include "ptx.cuh"
@@ -33,7 +35,8 @@ struct MuonParams {
     // workspace
     int ldx, m, ldm;      // row lengths of X and of A and B; m = min(rows, cols)
     long long xs, ms;     // elements between matrices
-    __half *x[2], *xlo, *a, *b;
+    __half *x[2], *xlo[2], *a, *b;  // (xlo: one array twice where products do not read it)
+    __half *alo, *blo;              // second values of A and B, or null
     float* part;          // [batch][nparts] partial sums of squares
     int nparts;
     int nv;  // vectors of a row (the elementwise kernels), and i / nv = i * nv_mul >> nv_shift
@@ -329,14 +332,14 @@ __global__ void __launch_bounds__(256) muon_normalize_kernel(const __grid_consta
                     uint4 h, l;
                     split8<false>(u[q], &h, &l);
                     *reinterpret_cast<uint4*>(p.x[0] + k) = h;
-                    *reinterpret_cast<uint4*>(p.xlo + k) = l;
+                    *reinterpret_cast<uint4*>(p.xlo[0] + k) = l;
                 }
             } else if (last) {
                 muon_finish(p, base + r * p.ld + c, u[q][0]);
             } else {
                 const __half h = __float2half_rn(u[q][0]);
                 p.x[0][k] = h;
-                p.xlo[k] = __float2half_rn(u[q][0] - __half2float(h));
+                p.xlo[0][k] = __float2half_rn(u[q][0] - __half2float(h));
             }
         }
     }

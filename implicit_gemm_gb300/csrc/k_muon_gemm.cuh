@@ -18,6 +18,10 @@
 // in the order of the sum, so the result does not depend on who that is.  Nothing
 // waits for another CTA except within the pair.
 //
+// Operands of two values: the sum is three times as long, its blocks those of second
+// by first values, first by second, and first by first (the small ones first: MMAs add
+// with truncation, see gram_product and muon_put_back).
+//
 // Main loop: 0.33 us per 64 of a 256 x 256 tile's sum on all pairs, 1.9 PFLOP/s,
 // the rate of a large library product.  Around it a launch costs some 7 us: 1 from
 // the kernel before (2 with the set-up after the wait for it, some 15 us of 1000 x
@@ -57,6 +61,14 @@ enum MuonKind {
     kMuonLastAny,  // the results, rows that start anywhere
 };
 
+// The operands' tensor maps: A, B, and with TWO those of their second values.  (Kernels of
+// their own: 8192 x 4096 with one value each 1,974 us against 1,944 where the maps are
+// chosen as the kernel runs.)
+template <bool TWO>
+struct MgMaps {
+    CUtensorMap m[TWO ? 4 : 2];
+};
+
 struct MuonProduct {
     int kind, xin;
     // The last two steps take B + t I and a - t: where B's eigenvalues are near -t, the
@@ -64,7 +76,8 @@ struct MuonProduct {
     float a, b, c;            // (a: less t)
     float tc;                 // t in units of the sums of A A
     int a_mn, b_mn;           // operand is read across its rows
-    int M, N, kb;             // extents of D, 64-wide blocks of the sum
+    float sums;               // A A and B X in units of X (2^-10 and what truncation left out)
+    int M, N, kb, kb1;        // extents of D, 64-wide blocks of the sum, and of one of its terms
     int tm, tn, sym;          // tiles along M and N of a matrix
     int per;                  // tiles of a matrix
     int tiles;                // of all matrices
@@ -157,24 +170,61 @@ __device__ __forceinline__ MgTile mg_tile(const MuonProduct& g, int t)
 struct MgRead {
     uint4 x[4], y[4];
 };
-template <int KIND>
+template <int KIND, bool TWO>
 __device__ __forceinline__ void mg_read(const MuonParams& p, const MuonProduct& g, int b, int i0, int j, MgRead& r)
 {
-    const int lane = threadIdx.x & 31, sub = lane >> 2, jc = j + 8 * (lane & 3);
-    if (KIND == kMuonA) return;
+    if constexpr (KIND != kMuonA) {
+        const int lane = threadIdx.x & 31, sub = lane >> 2, jc = j + 8 * (lane & 3);
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-        const int i = i0 + 8 * it + sub;
-        r.x[it] = r.y[it] = make_uint4(0u, 0u, 0u, 0u);
-        if (i >= g.M || jc >= g.N) continue;
-        if (KIND == kMuonB) {
-            r.x[it] = *reinterpret_cast<const uint4*>(p.a + b * p.ms + (long long)i * p.ldm + jc);
-        } else {
-            const long long e = b * p.xs + (long long)i * p.ldx + jc;
-            r.x[it] = *reinterpret_cast<const uint4*>(p.x[g.xin] + e);
-            r.y[it] = *reinterpret_cast<const uint4*>(p.xlo + e);
+        for (int it = 0; it < 4; ++it) {
+            const int i = i0 + 8 * it + sub;
+            r.x[it] = r.y[it] = make_uint4(0u, 0u, 0u, 0u);
+            if (i >= g.M || jc >= g.N) continue;
+            if (KIND == kMuonB) {
+                const long long e = b * p.ms + (long long)i * p.ldm + jc;
+                r.x[it] = *reinterpret_cast<const uint4*>(p.a + e);
+                if (TWO) r.y[it] = *reinterpret_cast<const uint4*>(p.alo + e);
+            } else {
+                const long long e = b * p.xs + (long long)i * p.ldx + jc;
+                r.x[it] = *reinterpret_cast<const uint4*>(p.x[g.xin] + e);
+                r.y[it] = *reinterpret_cast<const uint4*>(p.xlo[g.xin] + e);
+            }
         }
     }
+}
+
+// Rows i0 + lane, columns j .. j + 31 of a square matrix of fp16 at `base`, from packed
+// pairs h, and their mirror image.  Chunk k of row r of the staging at k ^ (r / 2) % 4.
+__device__ __forceinline__ void mg_put_square(const MuonParams& p, const MuonProduct& g, uint8_t* stg, __half* base, int i0,
+                                              int j, bool mirror, const uint32_t (&h)[16])
+{
+    const int lane = threadIdx.x & 31, sub = lane >> 2, c4 = lane & 3, jc = j + 8 * c4;
+    uint8_t* own = stg + lane * 64;
+    const int osw = (lane >> 1) & 3;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<uint4*>(own + ((k ^ osw) << 4)) = make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
+    __syncwarp();
+    // Rows are padded to eight elements; the padding may be written.
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+        const int r = 8 * it + sub;
+        const uint4 y = *reinterpret_cast<const uint4*>(stg + r * 64 + ((c4 ^ ((r >> 1) & 3)) << 4));
+        if (i0 + r < g.M && jc < g.N) *reinterpret_cast<uint4*>(base + (long long)(i0 + r) * p.ldm + jc) = y;
+    }
+    if (mirror) {
+        // Neighbouring lanes exchange so that each has two rows' values of one column.
+        const bool odd = lane & 1;
+        const int i2 = i0 + (lane & ~1);
+        __half* col = base + (long long)(j + (odd ? 1 : 0)) * p.ldm + i2;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, h[k], 1);
+            const uint32_t w = odd ? __byte_perm(other, h[k], 0x7632) : __byte_perm(h[k], other, 0x5410);
+            if (j + 2 * k + (odd ? 1 : 0) < g.N && i2 < g.M) *reinterpret_cast<uint32_t*>(col + 2 * k * p.ldm) = w;
+        }
+    }
+    __syncwarp();
 }
 
 // The first n of 32 staged rows, a column per lane.
@@ -204,75 +254,72 @@ __device__ __forceinline__ void mg_weight_rows(const MuonParams& p, T* w, int n,
     }
 }
 
-// 32 finished sums of row i0 + lane, columns j .. j + 31 of matrix b, by one warp.
-// Global memory is read and written in rows of 64 bytes through the warp's 4 KB of
+// 32 finished sums of row i0 + lane, columns j .. j + 31 of matrix b, by one warp: of a
+// square matrix, A or B.  Global memory is read and written in rows of 64 bytes through the warp's 4 KB of
 // shared memory, whose 16-byte chunks are swizzled by the row: row by row from the
 // lanes, a request touched 32 lines and the epilogue took longer than the MMAs of a
 // 4096-long sum.  `mirror`: the tile's mirror image is written too.
-template <int KIND>
-__device__ __forceinline__ void mg_epilogue(const MuonParams& p, const MuonProduct& g, uint8_t* stg, int b, int i0, int j,
-                                            bool mirror, float (&v)[32], const MgRead& rd)
+template <int KIND, bool TWO>
+__device__ __forceinline__ void mg_square(const MuonParams& p, const MuonProduct& g, uint8_t* stg, int b, int i0, int j,
+                                          bool mirror, float (&v)[32], const MgRead& rd)
 {
     const int lane = threadIdx.x & 31, sub = lane >> 2, c4 = lane & 3;
-    const int jc = j + 8 * c4;
-    if (KIND < kMuonX) {
-        // fp16 rows of 64 bytes: chunk k of row r at k ^ (r / 2) % 4.
-        __half* base = (KIND == kMuonA ? p.a : p.b) + b * p.ms;
-        uint8_t* own = stg + lane * 64;
-        const int osw = (lane >> 1) & 3;
-        uint32_t h[16];
-        if (KIND == kMuonA) {
+    uint32_t h[16];
+    if constexpr (KIND == kMuonA) {
+        const float f = TWO ? 16.f * g.sums : 0x1p-6f;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) h[k] = pack_half2(v[2 * k] * 0x1p-6f, v[2 * k + 1] * 0x1p-6f);
-        } else {
+        for (int k = 0; k < 32; ++k) v[k] *= f;
+    } else {
+        const float c = g.c * (TWO ? g.sums : 0x1p-10f);
+        if (i0 == j)  // t I (see MuonProduct)
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] += lane == k ? g.tc : 0.f;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] *= c;
+#pragma unroll
+        for (int two = 0; two < (TWO ? 2 : 1); ++two) {
+            // A's values come by the row: rows of 64 bytes, chunk k of row r at k ^ (r / 2) % 4.
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
                 const int r = 8 * it + sub;
-                *reinterpret_cast<uint4*>(stg + r * 64 + ((c4 ^ ((r >> 1) & 3)) << 4)) = rd.x[it];
+                *reinterpret_cast<uint4*>(stg + r * 64 + ((c4 ^ ((r >> 1) & 3)) << 4)) = two ? rd.y[it] : rd.x[it];
             }
             __syncwarp();
-            const float c = g.c * 0x1p-10f;
-            if (i0 == j)  // t I (see MuonProduct)
-#pragma unroll
-                for (int k = 0; k < 32; ++k) v[k] += lane == k ? g.tc : 0.f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const uint4 y = *reinterpret_cast<const uint4*>(own + ((k ^ osw) << 4));
+                const uint4 y = *reinterpret_cast<const uint4*>(stg + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4));
                 const uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float2 f = unpack_half2(w[e]);
-                    h[4 * k + e] = pack_half2(fmaf(g.b, f.x, c * v[8 * k + 2 * e]), fmaf(g.b, f.y, c * v[8 * k + 2 * e + 1]));
+                    v[8 * k + 2 * e] = fmaf(g.b, f.x, v[8 * k + 2 * e]);
+                    v[8 * k + 2 * e + 1] = fmaf(g.b, f.y, v[8 * k + 2 * e + 1]);
                 }
             }
             __syncwarp();
         }
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            *reinterpret_cast<uint4*>(own + ((k ^ osw) << 4)) = make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
-        __syncwarp();
-        // Rows are padded to eight elements; the padding may be written.
-#pragma unroll
-        for (int it = 0; it < 4; ++it) {
-            const int r = 8 * it + sub;
-            const uint4 y = *reinterpret_cast<const uint4*>(stg + r * 64 + ((c4 ^ ((r >> 1) & 3)) << 4));
-            if (i0 + r < g.M && jc < g.N) *reinterpret_cast<uint4*>(base + (long long)(i0 + r) * p.ldm + jc) = y;
-        }
-        if (mirror) {
-            // Neighbouring lanes exchange so that each has two rows' values of one column.
-            const bool odd = lane & 1;
-            const int i2 = i0 + (lane & ~1);
-            __half* col = base + (long long)(j + (odd ? 1 : 0)) * p.ldm + i2;
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const uint32_t other = __shfl_xor_sync(0xffffffffu, h[k], 1);
-                const uint32_t w = odd ? __byte_perm(other, h[k], 0x7632) : __byte_perm(h[k], other, 0x5410);
-                if (j + 2 * k + (odd ? 1 : 0) < g.N && i2 < g.M) *reinterpret_cast<uint32_t*>(col + 2 * k * p.ldm) = w;
-            }
-        }
-        __syncwarp();
-        return;
     }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) h[k] = pack_half2(v[2 * k], v[2 * k + 1]);
+    mg_put_square(p, g, stg, (KIND == kMuonA ? p.a : p.b) + b * p.ms, i0, j, mirror, h);
+    if constexpr (TWO) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const float2 f = unpack_half2(h[k]);
+            h[k] = pack_half2(v[2 * k] - f.x, v[2 * k + 1] - f.y);
+        }
+        mg_put_square(p, g, stg, (KIND == kMuonA ? p.alo : p.blo) + b * p.ms, i0, j, mirror, h);
+    }
+}
+
+// The same of the next X, or of the results.
+template <int KIND, bool TWO>
+__device__ __forceinline__ void mg_result(const MuonParams& p, const MuonProduct& g, uint8_t* stg, int b, int i0, int j,
+                                          float (&v)[32], const MgRead& rd)
+{
+    const int lane = threadIdx.x & 31, sub = lane >> 2, c4 = lane & 3;
+    const int jc = j + 8 * c4;
+    const float sums = TWO ? g.sums : 0x1p-10f;
     // fp32 rows of 128 bytes: chunk k of row r at k ^ r % 8.
 #pragma unroll
     for (int k = 0; k < 8; ++k)
@@ -291,25 +338,25 @@ __device__ __forceinline__ void mg_epilogue(const MuonParams& p, const MuonProdu
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const float2 h = unpack_half2(wh[q]), l = unpack_half2(wl[q]);
-            y[2 * q] = fmaf(g.a, h.x + l.x, d[2 * q] * 0x1p-10f);
-            y[2 * q + 1] = fmaf(g.a, h.y + l.y, d[2 * q + 1] * 0x1p-10f);
+            y[2 * q] = fmaf(g.a, h.x + l.x, d[2 * q] * sums);
+            y[2 * q + 1] = fmaf(g.a, h.y + l.y, d[2 * q + 1] * sums);
         }
         if (i >= g.M || jc >= g.N) continue;
-        if (KIND == kMuonX) {
+        if constexpr (KIND == kMuonX) {
             const long long e = b * p.xs + (long long)i * p.ldx + jc;
             uint4 h, l;
             split8<false>(y, &h, &l);
             *reinterpret_cast<uint4*>(p.x[g.xin ^ 1] + e) = h;
-            *reinterpret_cast<uint4*>(p.xlo + e) = l;
-            continue;
-        }
-#pragma unroll
-        for (int q = 0; q < 8; ++q) y[q] *= p.scale * (1.f / kMuonXScale);
-        if (KIND == kMuonLast) {
-            muon_finish8(p, (long long)b * p.bs + i * p.ld + jc, y);
+            *reinterpret_cast<uint4*>(p.xlo[g.xin ^ 1] + e) = l;
         } else {
-            *reinterpret_cast<float4*>(stg + r * 128 + (((2 * c4) ^ (r & 7)) << 4)) = make_float4(y[0], y[1], y[2], y[3]);
-            *reinterpret_cast<float4*>(stg + r * 128 + (((2 * c4 + 1) ^ (r & 7)) << 4)) = make_float4(y[4], y[5], y[6], y[7]);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) y[q] *= p.scale * (1.f / kMuonXScale);
+            if (KIND == kMuonLast) {
+                muon_finish8(p, (long long)b * p.bs + i * p.ld + jc, y);
+            } else {
+                *reinterpret_cast<float4*>(stg + r * 128 + (((2 * c4) ^ (r & 7)) << 4)) = make_float4(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<float4*>(stg + r * 128 + (((2 * c4 + 1) ^ (r & 7)) << 4)) = make_float4(y[4], y[5], y[6], y[7]);
+            }
         }
     }
     __syncwarp();
@@ -340,10 +387,10 @@ __device__ __forceinline__ void mg_epilogue(const MuonParams& p, const MuonProdu
     }
 }
 
-template <int BN, int KIND>
+template <int BN, int KIND, bool TWO>
 __global__ void __launch_bounds__(kMgThreads, 1)
-    muon_product_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
-                        const __grid_constant__ MuonParams p, const __grid_constant__ MuonProduct g)
+    muon_product_kernel(const __grid_constant__ MgMaps<TWO> maps, const __grid_constant__ MuonParams p,
+                        const __grid_constant__ MuonProduct g)
 {
     constexpr int kMgStages = Mg<BN>::kStages, kMgStageBytes = Mg<BN>::kStageBytes;
     extern __shared__ uint8_t smem_raw[];
@@ -359,8 +406,7 @@ __global__ void __launch_bounds__(kMgThreads, 1)
 
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
-        tma_prefetch_desc(&ta);
-        tma_prefetch_desc(&tb);
+        for (int i = 0; i < (TWO ? 4 : 2); ++i) tma_prefetch_desc(&maps.m[i]);
         for (int i = 0; i < kMgStages; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
@@ -399,20 +445,28 @@ __global__ void __launch_bounds__(kMgThreads, 1)
                         ok = false;
                         break;
                     }
+                    const CUtensorMap *ma = &maps.m[0], *mb = &maps.m[1];
+                    int kc = 64 * k;
+                    if constexpr (TWO) {  // the block's term of the sum
+                        const int term = k >= 2 * g.kb1 ? 2 : k >= g.kb1 ? 1 : 0;
+                        if (term == 0) ma = &maps.m[2];
+                        if (term == 1) mb = &maps.m[3];
+                        kc -= 64 * g.kb1 * term;
+                    }
                     uint8_t* s = smem + st * kMgStageBytes;
                     const uint32_t bar = full0 + (uint32_t)(st * 8);
                     if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * kMgStageBytes);
                     if (g.a_mn) {
-                        tma_load_3d_pair(s, &ta, bar, m0, k * 64, t.b);
-                        tma_load_3d_pair(s + 8192, &ta, bar, m0 + 64, k * 64, t.b);
+                        tma_load_3d_pair(s, ma, bar, m0, kc, t.b);
+                        tma_load_3d_pair(s + 8192, ma, bar, m0 + 64, kc, t.b);
                     } else {
-                        tma_load_3d_pair(s, &ta, bar, k * 64, m0, t.b);
+                        tma_load_3d_pair(s, ma, bar, kc, m0, t.b);
                     }
                     if (g.b_mn) {
-                        tma_load_3d_pair(s + 16384, &tb, bar, n0, k * 64, t.b);
-                        if (BN == 256) tma_load_3d_pair(s + 16384 + 8192, &tb, bar, n0 + 64, k * 64, t.b);
+                        tma_load_3d_pair(s + 16384, mb, bar, n0, kc, t.b);
+                        if (BN == 256) tma_load_3d_pair(s + 16384 + 8192, mb, bar, n0 + 64, kc, t.b);
                     } else {
-                        tma_load_3d_pair(s + 16384, &tb, bar, k * 64, n0, t.b);
+                        tma_load_3d_pair(s + 16384, mb, bar, kc, n0, t.b);
                     }
                     if (++st == kMgStages) st = 0, ph ^= 1u;
                 }
@@ -475,7 +529,7 @@ __global__ void __launch_bounds__(kMgThreads, 1)
             const uint32_t tacc = trow + (uint32_t)(buf * BN);
             const bool whole = w.k0 == 0 && w.k1 == g.kb;
             MgRead rd;
-            if (whole) mg_read<KIND>(p, g, t.b, i0, j0, rd);  // on its way while the sums are made
+            if (whole) mg_read<KIND, TWO>(p, g, t.b, i0, j0, rd);  // on its way while the sums are made
             if (!mbar_wait_sleep(&accf[buf], (uint32_t)(i >> 1) & 1u)) break;
             __syncwarp();
             tc_fence_after();
@@ -511,7 +565,7 @@ __global__ void __launch_bounds__(kMgThreads, 1)
                 for (int ch = 0; ch < BN / 128; ++ch) {
                     float v[32];
                     if (whole) {
-                        if (ch) mg_read<KIND>(p, g, t.b, i0, j0 + ch * 32, rd);
+                        if (ch) mg_read<KIND, TWO>(p, g, t.b, i0, j0 + ch * 32, rd);
                         gram_ld<32>(tacc + (uint32_t)(ch * 32), v);
                     } else {
                         // 32 loads in flight at a time (left to the compiler, one after another).
@@ -527,9 +581,13 @@ __global__ void __launch_bounds__(kMgThreads, 1)
 #pragma unroll
                             for (int k = 0; k < 32; ++k) v[k] += x[k];
                         }
-                        mg_read<KIND>(p, g, t.b, i0, j0 + ch * 32, rd);
+                        mg_read<KIND, TWO>(p, g, t.b, i0, j0 + ch * 32, rd);
                     }
-                    mg_epilogue<KIND>(p, g, staging + e * kMgWarpStaging, t.b, i0, j0 + ch * 32, t.mirror, v, rd);
+                    uint8_t* stg = staging + e * kMgWarpStaging;
+                    if constexpr (KIND < kMuonX)
+                        mg_square<KIND, TWO>(p, g, stg, t.b, i0, j0 + ch * 32, t.mirror, v, rd);
+                    else
+                        mg_result<KIND, TWO>(p, g, stg, t.b, i0, j0 + ch * 32, v, rd);
                 }
             }
             tc_fence_before();

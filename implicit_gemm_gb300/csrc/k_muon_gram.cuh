@@ -138,11 +138,9 @@ __device__ __forceinline__ void gram_put(uint8_t* img, int r, int c0, const floa
 // (symmetric up to roundings) transposes the roundings of Q between a direction
 // the matrix has and one it lacks, which are 482 times larger on one side than on
 // the other: gradients of rank one were 10% off.
-// The small products come first, or apart: every MMA cuts its sums off at fp32's last
-// bit, towards zero, and so each one that adds to the large sums makes them smaller.
-// (24 in turn took up to 4e-7 of A A.  With factors that fall from 8.3, whose map has a
-// slope of 3e4 at 1, 128 x 128 of rank one was 1.0e-2 off; 3.3e-3 with this and with
-// what muon_gram_plan puts back.)
+// The small products come first, or apart: MMAs add with truncation, and so each one
+// that adds to the large sums makes them smaller.
+// (What is left is put back, see muon_put_back.)
 // P = 64: the two images of Y lie one after the other, and one MMA of 128 columns
 // multiplies both: hi hi in columns 0 .. 63, hi lo (and lo hi) in columns 64 .. 127 (an
 // MMA takes some 66 cycles whatever its columns up to 128: 2 instead of 3).
@@ -164,10 +162,11 @@ __device__ __forceinline__ void gram_product(uint32_t d, uint32_t x, uint32_t y,
             umma_f16(d, xd + xo + lo, yd + yo, idesc, 1u);
         }
     }
-    if (P == 64) return;
+    if constexpr (P != 64) {
 #pragma unroll 1
-    for (int ks = 0; ks < kn; ++ks)
-        umma_f16(d, xd + (uint64_t)((ks >> 2) * (P * 8) + 2 * (ks & 3)), yd + (uint64_t)(128 * ks), idesc, 1u);
+        for (int ks = 0; ks < kn; ++ks)
+            umma_f16(d, xd + (uint64_t)((ks >> 2) * (P * 8) + 2 * (ks & 3)), yd + (uint64_t)(128 * ks), idesc, 1u);
+    }
 }
 
 // NC columns of a product, from column c0 (and of its second half).

@@ -81,7 +81,8 @@ struct MuonPlan {
     int P, blocks;        // rows of a block of the Gram matrix, blocks
     int ldx, m, ldm, nparts;
     int pairs;
-    size_t off_x[2], off_xlo, off_a, off_b, off_part, off_sums, off_arrived, bytes;
+    bool two;             // general form: A, B and X of the products have two fp16 values
+    size_t off_x[2], off_xlo[2], off_a, off_b, off_alo, off_blo, off_part, off_sums, off_arrived, bytes;
 };
 
 // CTAs of the Gram-matrix kernel's largest cluster: 16 where the device takes it
@@ -115,6 +116,15 @@ int muon_gram_max_cluster()
     cudaGetLastError();
     return cache[dev] = n > 0 ? 16 : 8;
 }
+
+// MMAs add to their sums with truncation: a sum of equal signs over 16 n elements comes
+// out short by 0.95e-7 n^2 / (n + 5) of itself, measured on products of matrices of rank
+// one: 1.8e-7 for n = 4, 4.5e-7 for 8, 12e-7 for 16, 59e-7 for 64 and 509e-7 for 512.
+// Maps with slopes of 1e4 and more make that visible (the factors that fall from 8.3
+// have 3e4 at 1: 256 x 512 of rank one 4.8e-2 off without, 3e-3 with), so it is put
+// back; sums of mixed signs lose less, and no map makes much of theirs.
+double muon_put_back(double n) { return 1.0 + 0.95e-7 * n * n / (n + 5.0); }
+
 
 // Largest value over s in [0, smax] of what a step (a, b, c) makes of a singular value s,
 // and of the factor that it multiplies s by.
@@ -173,12 +183,7 @@ void muon_gram_plan(MuonPlan* pl)
     }
     pl->first[pl->launches] = q.steps;
     auto power = [](double bound) { return ldexpf(1.f, (int)floor(log2(8192.0 / std::max(bound, 1e-6)))); };
-    // Every MMA cuts its sums off towards zero, by half a last bit in the mean (0.72 2^-24
-    // of a value whose digits are spread evenly in their logarithm), and n of them add to
-    // sums that grow evenly: what they leave out in the mean is put back.  (128 x 128 of
-    // rank one with factors that fall from 8.3, whose map has a slope of 3e4 at 1: see
-    // gram_product.)
-    const double put_back = 1.0 + 0.72 * 0x1p-24 * ((pl->m + 15) / 16 + 1) / 2;
+    const double put_back = muon_put_back(pl->m / 16.0);
     smax = 1.0;
     for (int n = 0; n < pl->launches; ++n) {
         double grid[513], prod[513];
@@ -215,6 +220,27 @@ void step_range(const float* k, double smax, double* grown, double* poly)
         *grown = std::max(*grown, fabs(s * (k[0] + q)));
         *poly = std::max(*poly, fabs(q));
     }
+}
+
+// What rounding A, B and X to 11 bits costs the general form, in units of 2^-15 or so:
+// the largest |b| s^3 + |c| s^5 of a step, grown by the slopes of the later steps' maps,
+// over s in [0, 1] and all steps.  Five default steps have 88, six 144, seven 231; an
+// error of X of 3.0e-3, 4.4e-3 and 4.8e-3 (the largest over spectra, 130 x 160 to 256 x
+// 512, simulated).  Factors that fall from 8.3 have 1e5: rank one was 18 to 45% off, and
+// with three cubic steps behind them 170 times too large.
+double muon_single_error(const float (*coef)[3], int steps)
+{
+    double worst = 0.0;
+    for (int i = 0; i <= 4096; ++i) {
+        double s = i / 4096.0, e = 0.0;
+        for (int k = 0; k < steps; ++k) {
+            const double a = coef[k][0], b = coef[k][1], c = coef[k][2], l = s * s;
+            e = e * fabs(a + 3.0 * b * l + 5.0 * c * l * l) + (fabs(b) * l + fabs(c) * l * l) * s;
+            worst = std::max(worst, e);
+            s *= a + b * l + c * l * l;
+        }
+    }
+    return worst;
 }
 
 int make_muon_plan(const wg_muon_problem* p, MuonPlan* pl)
@@ -267,14 +293,20 @@ int make_muon_plan(const wg_muon_problem* p, MuonPlan* pl)
         pl->bytes = pl->launches > 1 ? up256((size_t)q.batch * q.rows * q.cols * 4) : 256;
         return WG_OK;
     }
+    pl->two = muon_single_error(pl->coef, q.steps) > 100.0;
     const size_t x = up256((size_t)q.batch * q.rows * pl->ldx * 2), a = up256((size_t)q.batch * pl->m * pl->ldm * 2);
     pl->off_part = o, o += up256((size_t)q.batch * pl->nparts * 4);
     if (q.steps > 0) {
         pl->off_x[0] = o, o += x;
         pl->off_x[1] = o, o += x;
-        pl->off_xlo = o, o += x;
+        pl->off_xlo[0] = pl->off_xlo[1] = o, o += x;
         pl->off_a = o, o += a;
         pl->off_b = o, o += a;
+        if (pl->two) {
+            pl->off_xlo[1] = o, o += x;
+            pl->off_alo = o, o += a;
+            pl->off_blo = o, o += a;
+        }
         pl->pairs = std::max(1, num_sms() / 2);
         pl->off_sums = o, o += (size_t)pl->pairs * 2 * 256 * 256 * 4;
         pl->off_arrived = o, o += up256((size_t)pl->pairs * 2 * wg::kMgEpiWarps * 4);
@@ -359,22 +391,26 @@ int muon_map(CUtensorMap* tm, void* base, int cols, int rows, int batch, int ld,
     return WG_OK;
 }
 
-// A matrix of the workspace as an operand.
+// A matrix of the workspace as an operand (lo: its second values).
 struct MuonOperand {
-    void* base;
+    void *base, *lo;
     int cols, rows, ld;
     long long bs;
 };
 
-template <int BN, int KIND>
+template <int BN, int KIND, bool TWO>
 int muon_product_launch(const MuonPlan& pl, const wg::MuonParams& p, wg::MuonProduct& g, const MuonOperand& oa,
-                    const MuonOperand& ob, cudaStream_t s)
+                        const MuonOperand& ob, cudaStream_t s)
 {
     const int used = g.whole ? g.pairs : std::max(g.cut, 1);
-    CUtensorMap ta, tb;
-    int st = muon_map(&ta, oa.base, oa.cols, oa.rows, p.batch, oa.ld, oa.bs, g.a_mn ? 64 : 128);
-    if (!st) st = muon_map(&tb, ob.base, ob.cols, ob.rows, p.batch, ob.ld, ob.bs, g.b_mn ? 64 : BN / 2);
-    if (!st) st = wg::ensure_smem(wg::muon_product_kernel<BN, KIND>, wg::Mg<BN>::kSmem);
+    wg::MgMaps<TWO> maps;
+    int st = WG_OK;
+    for (int i = 0; !st && i < (TWO ? 4 : 2); ++i) {
+        const MuonOperand& o = i & 1 ? ob : oa;
+        const int box = (i & 1 ? g.b_mn : g.a_mn) ? 64 : i & 1 ? BN / 2 : 128;
+        st = muon_map(&maps.m[i], i < 2 ? o.base : o.lo, o.cols, o.rows, p.batch, o.ld, o.bs, box);
+    }
+    if (!st) st = wg::ensure_smem(wg::muon_product_kernel<BN, KIND, TWO>, wg::Mg<BN>::kSmem);
     if (st) return st;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
@@ -387,7 +423,7 @@ int muon_product_launch(const MuonPlan& pl, const wg::MuonParams& p, wg::MuonPro
     cfg.gridDim = dim3((unsigned)(2 * used));
     cfg.blockDim = dim3(wg::kMgThreads);
     cfg.dynamicSmemBytes = wg::Mg<BN>::kSmem;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, wg::muon_product_kernel<BN, KIND>, ta, tb, p, g);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, wg::muon_product_kernel<BN, KIND, TWO>, maps, p, g);
     return e == cudaSuccess ? WG_OK : cuda_fail("muon_product_kernel launch", e);
 }
 
@@ -396,11 +432,24 @@ int muon_product_bn(const MuonPlan& pl, const wg::MuonParams& p, wg::MuonProduct
                     const MuonOperand& ob, cudaStream_t s)
 {
     switch (g.kind) {
-        case wg::kMuonA: return muon_product_launch<BN, wg::kMuonA>(pl, p, g, oa, ob, s);
-        case wg::kMuonB: return muon_product_launch<BN, wg::kMuonB>(pl, p, g, oa, ob, s);
-        case wg::kMuonX: return muon_product_launch<BN, wg::kMuonX>(pl, p, g, oa, ob, s);
-        case wg::kMuonLast: return muon_product_launch<BN, wg::kMuonLast>(pl, p, g, oa, ob, s);
-        default: return muon_product_launch<BN, wg::kMuonLastAny>(pl, p, g, oa, ob, s);
+        case wg::kMuonA: return muon_product_launch<BN, wg::kMuonA, false>(pl, p, g, oa, ob, s);
+        case wg::kMuonB: return muon_product_launch<BN, wg::kMuonB, false>(pl, p, g, oa, ob, s);
+        case wg::kMuonX: return muon_product_launch<BN, wg::kMuonX, false>(pl, p, g, oa, ob, s);
+        case wg::kMuonLast: return muon_product_launch<BN, wg::kMuonLast, false>(pl, p, g, oa, ob, s);
+        default: return muon_product_launch<BN, wg::kMuonLastAny, false>(pl, p, g, oa, ob, s);
+    }
+}
+
+// Products of two values each have one form of results.
+template <int BN>
+int muon_product_two(const MuonPlan& pl, const wg::MuonParams& p, wg::MuonProduct& g, const MuonOperand& oa,
+                     const MuonOperand& ob, cudaStream_t s)
+{
+    switch (g.kind) {
+        case wg::kMuonA: return muon_product_launch<BN, wg::kMuonA, true>(pl, p, g, oa, ob, s);
+        case wg::kMuonB: return muon_product_launch<BN, wg::kMuonB, true>(pl, p, g, oa, ob, s);
+        case wg::kMuonX: return muon_product_launch<BN, wg::kMuonX, true>(pl, p, g, oa, ob, s);
+        default: return muon_product_launch<BN, wg::kMuonLastAny, true>(pl, p, g, oa, ob, s);
     }
 }
 
@@ -408,7 +457,7 @@ int muon_product_bn(const MuonPlan& pl, const wg::MuonParams& p, wg::MuonProduct
 int muon_product(const MuonPlan& pl, const wg::MuonParams& p, wg::MuonProduct& g, const MuonOperand& oa,
                  const MuonOperand& ob, int K, cudaStream_t s)
 {
-    g.kb = (K + 63) / 64;
+    g.kb1 = (K + 63) / 64, g.kb = pl.two ? 3 * g.kb1 : g.kb1;
     g.pairs = pl.pairs;
     // The tiles' width, whether a symmetric product takes only the tiles on and
     // below the diagonal, and the parts that the leftover tiles are cut into, by
@@ -438,6 +487,14 @@ int muon_product(const MuonPlan& pl, const wg::MuonParams& p, wg::MuonProduct& g
     g.tiles = p.batch * g.per;
     g.whole = g.tiles / g.pairs * g.pairs;
     g.cut = std::max(1, (g.tiles - g.whole) * parts);
+    // What truncation takes of the products of first values, by the parts that they are in.
+    double back = 0.0;
+    for (int i = 0; pl.two && i < parts; ++i) {
+        const int k0 = std::max(2 * g.kb1, g.kb * i / parts), k1 = g.kb * (i + 1) / parts;
+        if (k1 > k0) back += (muon_put_back(K / 16.0 * (k1 - k0) / g.kb1) - 1.0) * (k1 - k0) / g.kb1;
+    }
+    g.sums = (float)(0x1p-10 * (1.0 + back));
+    if (pl.two) return bn == 256 ? muon_product_two<256>(pl, p, g, oa, ob, s) : muon_product_two<128>(pl, p, g, oa, ob, s);
     return bn == 256 ? muon_product_bn<256>(pl, p, g, oa, ob, s) : muon_product_bn<128>(pl, p, g, oa, ob, s);
 }
 
@@ -481,7 +538,8 @@ int muon_run(const MuonPlan& pl, const void* grad, void* momentum, void* weight,
                 g.p.gld = q.cols, g.p.gbs = (long long)q.rows * q.cols;
             }
             if (!end) {  // (A CTA has read an element of X before it writes it, and no other CTA reads it.)
-                g.p.out = ws, g.p.out_dtype = WG_FP32, g.p.weight = nullptr, g.p.scale = 1.f;
+                g.p.out = ws, g.p.out_dtype = WG_FP32, g.p.weight = nullptr;
+                g.p.scale = (float)muon_put_back(pl.m / 16.0);
                 g.p.ld = q.cols, g.p.bs = (long long)q.rows * q.cols;
             }
             const bool vec = (start ? al && aligned16(grad) && aligned16(momentum) : q.cols % 8 == 0) &&
@@ -495,8 +553,9 @@ int muon_run(const MuonPlan& pl, const void* grad, void* momentum, void* weight,
     p.part = reinterpret_cast<float*>(ws + pl.off_part), p.nparts = pl.nparts;
     if (q.steps > 0) {
         for (int i = 0; i < 2; ++i) p.x[i] = reinterpret_cast<__half*>(ws + pl.off_x[i]);
-        p.xlo = reinterpret_cast<__half*>(ws + pl.off_xlo);
+        for (int i = 0; i < 2; ++i) p.xlo[i] = reinterpret_cast<__half*>(ws + pl.off_xlo[i]);
         p.a = reinterpret_cast<__half*>(ws + pl.off_a), p.b = reinterpret_cast<__half*>(ws + pl.off_b);
+        if (pl.two) p.alo = reinterpret_cast<__half*>(ws + pl.off_alo), p.blo = reinterpret_cast<__half*>(ws + pl.off_blo);
     }
     if (q.steps > 0)
         p.arrived = reinterpret_cast<int*>(ws + pl.off_arrived), p.narrived = pl.pairs * 2 * wg::kMgEpiWarps;
@@ -521,13 +580,13 @@ int muon_run(const MuonPlan& pl, const void* grad, void* momentum, void* weight,
                     dim3(256), 0, s, p, (int)(q.steps == 0));
     if (st || q.steps == 0) return st;
     const bool wide = q.rows <= q.cols;
-    const MuonOperand x[2] = {{p.x[0], q.cols, q.rows, pl.ldx, p.xs}, {p.x[1], q.cols, q.rows, pl.ldx, p.xs}};
-    const MuonOperand ma = {p.a, pl.m, pl.m, pl.ldm, p.ms}, mb = {p.b, pl.m, pl.m, pl.ldm, p.ms};
+    const MuonOperand x[2] = {{p.x[0], p.xlo[0], q.cols, q.rows, pl.ldx, p.xs}, {p.x[1], p.xlo[1], q.cols, q.rows, pl.ldx, p.xs}};
+    const MuonOperand ma = {p.a, p.alo, pl.m, pl.m, pl.ldm, p.ms}, mb = {p.b, p.blo, pl.m, pl.m, pl.ldm, p.ms};
     for (int i = 0; i < q.steps; ++i) {
         const int in = i & 1;
         wg::MuonProduct g = {};
         g.a = pl.coef[i][0], g.b = pl.coef[i][1], g.c = pl.coef[i][2];
-        const float t = muon_shift(pl.coef[i], q.steps - 1 - i);
+        const float t = pl.two ? 0.f : muon_shift(pl.coef[i], q.steps - 1 - i);
         if (t > 0.f) g.a -= t, g.tc = t * 0x1p20f / g.c;
         g.xin = in;
         g.part = reinterpret_cast<float*>(ws + pl.off_sums), g.arrived = p.arrived;
@@ -747,8 +806,8 @@ int wg_muon_plan_string(const wg_muon_problem* p, char* buf, size_t n)
                  p->rows <= p->cols ? "left" : "right", pl.m, pl.P, pl.g.F, pl.blocks, pl.g.C, pl.g.chunks, p->steps,
                  pl.launches, wg::kGramSmem, pl.bytes);
     else
-        snprintf(buf, n, "kernel=muon_product side=%s m=%d steps=%d smem=%d ws=%zu", p->rows <= p->cols ? "left" : "right",
-                 pl.m, p->steps, wg::Mg<256>::kSmem, pl.bytes);
+        snprintf(buf, n, "kernel=muon_product side=%s m=%d steps=%d values=%d smem=%d ws=%zu",
+                 p->rows <= p->cols ? "left" : "right", pl.m, p->steps, pl.two ? 2 : 1, wg::Mg<256>::kSmem, pl.bytes);
     return WG_OK;
 }
 

@@ -331,14 +331,22 @@ WG_API int wg_bwd_data_plan_string(const wg_problem* p, char* buf, size_t n);
  *
  * The products are the same on the left and on the right of X; the kernels take
  * the shorter side.  With the default coefficients (3.4445, -4.7750, 2.0315) five
- * steps bring every singular value that was above about 1e-3 of |u|_F into
- * [0.7, 1.2].
+ * steps bring every singular value that was above 1.6e-3 of |u|_F into [0.68, 1.21].
  *
  * Arithmetic: u, the norm and m in fp32.  A matrix whose shorter side is at most
  * 128 is iterated on its Gram matrix in fp32-like precision; a larger one with
- * 16-bit operands and fp32 sums (X carried to 22 bits beside its 16-bit operand).
- * X's relative error (2-norm of all elements) is below 4e-3 in either form on
- * gradients of rank 1 to full rank; out and w are then rounded to nearest even.
+ * 16-bit operands and fp32 sums (X carried to 22 bits beside its 16-bit operand),
+ * or, where steps make more of their roundings than five default ones do (more of
+ * them, larger factors), with operands of two 16-bit values.
+ * X's relative error (2-norm of all elements) is below 4e-3 (5e-3 for a shorter side
+ * of 2 or 3) on gradients of rank 1 to full rank, or below 2^-22 S where that is more.
+ * S is the largest slope on [0, 1] of what the steps together make of a singular value:
+ * by that much a rounding of u or of an early X grows.  At 0 it is the product of the
+ * a's: 485 for five default steps, 2e4 for eight (5e-3), 2.4e5 for ten (6e-2).  (Sums
+ * of n > 512 elements lose bits as they grow: S n / 512, in operands of two values.)
+ * Where S nears 2^22, as of sixteen default steps, directions that u lacks hold
+ * roundings brought up to singular values near 1; X stays finite all the same.
+ * out and w are then rounded to nearest even.
  * A zero matrix gives zeros; a NaN or an infinity in u makes its matrix's X NaN, and
  * so does |u|_F above 1.8e19, whose square is beyond fp32 (elements below 1e-22 count
  * as zero beside it).

@@ -166,3 +166,17 @@ def test_muon_steps_of_a_launch():
     for kw in (dict(steps=6), dict(steps=16), dict(steps=5, coef=falling)):
         n, ws = plan(**kw)
         assert n > 1 and ws >= 24 * 40 * 4
+
+
+def test_muon_operands_of_larger_matrices():
+    """Five default steps multiply matrices of one 16-bit value an element; more, or steeper ones, of two."""
+    values = lambda **kw: dict(kv.split("=") for kv in binding.wg_muon_plan_string(  # noqa: E731
+        {"rows": 300, "cols": 400, **kw}).split())["values"]
+    assert values() == "1" and values(steps=3) == "1" and values(steps=16, coef=[(1.875, -1.25, 0.375)] * 16) == "1"
+    falling = [(8.2872, -23.5959, 17.3004), (4.1071, -2.9478, 0.5448), (3.9487, -2.9089, 0.5518),
+               (3.3184, -2.4885, 0.5100), (2.3007, -1.6690, 0.4188)]
+    assert values(steps=6) == "2" and values(steps=16) == "2" and values(steps=5, coef=falling) == "2"
+    # What follows does not mend what a steep step has spoilt.
+    assert values(steps=8, coef=falling + [(1.875, -1.25, 0.375)] * 3) == "2"
+    one, two = (binding.wg_muon_workspace_size({"rows": 300, "cols": 400, "steps": n}) for n in (5, 6))
+    assert two >= one + 300 * 400 * 2 + 2 * 300 * 304 * 2
