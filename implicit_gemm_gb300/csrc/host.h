@@ -1,5 +1,5 @@
 // Host helpers shared by the library's translation units (defined in wgrad.cu,
-// take_update_status in update.cu).  Internal: nothing here is exported.
+// the update status in update.cu).  Internal: nothing here is exported.
 #pragma once
 
 #include <cuda.h>
@@ -36,7 +36,8 @@ bool aligned16(const void* ptr);
 // Programmatic stream serialization for a launch.
 void pdl_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, unsigned* na, cudaStream_t stream);
 
-// Read and clear the device status word of update.cu.
-cudaError_t take_update_status(unsigned int* v);
+// The device status word of update.cu.
+cudaError_t read_update_status(unsigned int* v);
+cudaError_t write_update_status(unsigned int v);
 
 }  // namespace wg

@@ -20,13 +20,8 @@
 
 namespace wg {
 
-cudaError_t take_update_status(unsigned int* v)
-{
-    cudaError_t e = cudaMemcpyFromSymbol(v, g_status, sizeof *v);
-    const unsigned int zero = 0;
-    if (e == cudaSuccess && *v) e = cudaMemcpyToSymbol(g_status, &zero, sizeof zero);
-    return e;
-}
+cudaError_t read_update_status(unsigned int* v) { return cudaMemcpyFromSymbol(v, g_status, sizeof *v); }
+cudaError_t write_update_status(unsigned int v) { return cudaMemcpyToSymbol(g_status, &v, sizeof v); }
 
 }  // namespace wg
 

@@ -686,15 +686,6 @@ int check_buffers(const wg::Plan& pl, const void* x, const void* dy, const void*
     return WG_OK;
 }
 
-// Read and clear this translation unit's device status word.
-cudaError_t take_status(unsigned int* v)
-{
-    cudaError_t e = cudaMemcpyFromSymbol(v, wg::g_status, sizeof *v);
-    const unsigned int zero = 0;
-    if (e == cudaSuccess && *v) e = cudaMemcpyToSymbol(wg::g_status, &zero, sizeof zero);
-    return e;
-}
-
 }  // namespace
 
 extern "C" {
@@ -805,12 +796,20 @@ int wg_check_status(void* stream)
     cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail("cudaStreamSynchronize", e);
     // Each translation unit with kernels has a status word of its own.
-    unsigned int v = 0, u = 0;
-    e = take_status(&v);
-    if (e == cudaSuccess) e = wg::take_update_status(&u);
+    unsigned int w = 0, u = 0;
+    e = cudaMemcpyFromSymbol(&w, wg::g_status, sizeof w);
+    if (e == cudaSuccess) e = wg::read_update_status(&u);
     if (e != cudaSuccess) return cuda_fail("reading the device status", e);
-    v |= u;
-    if (v & (wg::kStatusBadPlan | wg::kStatusTimeout))
+    // What is reported is cleared: a token's bit beside a timeout's is left for the next call.
+    const unsigned int v = w | u, waits = wg::kStatusBadPlan | wg::kStatusTimeout;
+    const unsigned int told = v & waits ? waits : wg::kStatusBadToken;
+    if (w & told) {
+        w &= ~told;
+        e = cudaMemcpyToSymbol(wg::g_status, &w, sizeof w);
+    }
+    if (e == cudaSuccess && (u & told)) e = wg::write_update_status(u & ~told);
+    if (e != cudaSuccess) return cuda_fail("clearing the device status", e);
+    if (v & waits)
         return set_err(WG_ERR_DEVICE_TIMEOUT, (v & wg::kStatusBadPlan)
                                                   ? "internal error: a kernel instance got a plan it is not built for"
                                                   : "a kernel's bounded wait ran out");

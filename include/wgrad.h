@@ -192,8 +192,9 @@ WG_API int wg_workspace_size(const wg_problem* p, const wg_options* opt, size_t*
 WG_API int wg_conv_bwd_weight(const wg_problem* p, const void* x, const void* dy, void* dw, const wg_options* opt,
                        void* workspace, size_t ws_bytes, void* stream);
 
-/* Synchronise `stream`, then read and clear the device status word that the
- * kernels set when a bounded wait runs out or a token is out of range.
+/* Synchronise `stream`, then read the device status word that the kernels set
+ * when a bounded wait runs out or a token is out of range, and clear what is
+ * reported (where both have happened, the token is left for the next call).
  * Returns WG_OK, WG_ERR_DEVICE_TIMEOUT, WG_ERR_INVALID_TOKEN or WG_ERR_CUDA. */
 WG_API int wg_check_status(void* stream);
 
