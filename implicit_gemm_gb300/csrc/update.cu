@@ -65,6 +65,9 @@ int check_workspace(size_t need, const void* workspace, size_t ws_bytes)
 }
 
 // ---------------------------------------------------------------- orthogonalised update
+// Elements that a layout may span: their bytes and the sums of their addresses stay in 64 bits.
+constexpr long long kMaxSpan = 1LL << 48;
+
 constexpr int kMuonMaxDim = 32768, kMuonMaxSteps = 16, kMuonMaxParts = 1216;
 
 struct MuonPlan {
@@ -254,11 +257,15 @@ int make_muon_plan(const wg_muon_problem* p, MuonPlan* pl)
     pl->p = *p;
     wg_muon_problem& q = pl->p;
     if (q.ld == 0) q.ld = q.cols;
-    if (q.batch_stride == 0) q.batch_stride = (long long)q.rows * q.ld;
+    if (q.ld < q.cols) return set_err(WG_ERR_INVALID_ARGUMENT, "ld must be 0 or at least cols");
+    const bool far = q.ld > kMaxSpan / q.rows;
+    if (!far && (q.batch_stride == 0 || q.batch == 1)) q.batch_stride = (long long)q.rows * q.ld;
+    if (far || q.batch_stride > kMaxSpan / q.batch)
+        return set_err(WG_ERR_INVALID_ARGUMENT, "ld or batch_stride is larger than any memory");
     // Matrices after one another, or side by side (a matrix per head of a fused weight).
     const bool apart = q.batch_stride >= (long long)(q.rows - 1) * q.ld + q.cols;
     const bool beside = q.batch_stride >= q.cols && q.ld >= (long long)(q.batch - 1) * q.batch_stride + q.cols;
-    if (q.ld < q.cols || (q.batch > 1 && !apart && !beside))
+    if (q.batch > 1 && !apart && !beside)
         return set_err(WG_ERR_INVALID_ARGUMENT, "ld or batch_stride makes rows overlap");
     static const float kDefault[3] = {3.4445f, -4.7750f, 2.0315f};
     double smax = 1.0;
@@ -635,6 +642,8 @@ int emb_plan(const wg_embedding_problem* p, EmbPlan* pl)
     if (q.ld_out == 0) q.ld_out = q.dim;
     if (q.ld_table < q.dim || q.ld_out < q.dim)
         return set_err(WG_ERR_INVALID_ARGUMENT, "ld_table and ld_out must be 0 or at least dim");
+    if (q.ld_table > kMaxSpan / q.vocab || q.ld_out > kMaxSpan / std::max(q.tokens, 1LL))
+        return set_err(WG_ERR_INVALID_ARGUMENT, "ld_table or ld_out is larger than any memory");
     // Few tokens of a small table take one kernel: 512 tokens of 8192 x 512 in fp32 9 us
     // against 14 in three, 1000 of 8192 x 1024 in bf16 14 against 15; 100 of 16384 x 1024
     // 14 both ways, 64 of 32768 x 1024 24 against 17 (the SMs that have matches to place

@@ -180,3 +180,20 @@ def test_muon_operands_of_larger_matrices():
     assert values(steps=8, coef=falling + [(1.875, -1.25, 0.375)] * 3) == "2"
     one, two = (binding.wg_muon_workspace_size({"rows": 300, "cols": 400, "steps": n}) for n in (5, 6))
     assert two >= one + 300 * 400 * 2 + 2 * 300 * 304 * 2
+
+
+@pytest.mark.parametrize("big", [(1 << 63) - 1, 1 << 62, 1 << 50])
+def test_strides_whose_addresses_would_overflow_are_refused(big):
+    for bad in (dict(ld=big), dict(batch=2, batch_stride=big), dict(rows=30000, ld=big)):
+        refused(1, binding.wg_muon_workspace_size, muon(**bad))
+        refused(1, binding.wg_muon_update, muon(**bad), A, out=2 * A, workspace=3 * A, ws_bytes=1 << 40, stream=0)
+    for bad in (dict(ld_table=big, vocab=1 << 30), dict(ld_out=big, tokens=1 << 30)):
+        refused(1, binding.wg_embedding_workspace_size, emb(**bad))
+        refused(1, binding.wg_embedding_lookup, emb(**bad), A, 2 * A, 3 * A, stream=0)
+        refused(1, binding.wg_embedding_bwd_weight, emb(**bad), A, 2 * A, 3 * A, workspace=4 * A, ws_bytes=1 << 60,
+                stream=0)
+    refused(1, binding.wg_muon_workspace_size, muon(batch=60000, rows=30000, ld=1 << 33))
+    refused(1, binding.wg_muon_workspace_size, muon(ld=-big))
+    refused(1, binding.wg_muon_workspace_size, muon(batch=2, batch_stride=-big))
+    # What no address is made of does not count: the distance to a second matrix that is not there.
+    assert binding.wg_muon_workspace_size(muon(batch_stride=big)) > 0
