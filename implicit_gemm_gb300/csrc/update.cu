@@ -241,6 +241,12 @@ double muon_single_error(const float (*coef)[3], int steps)
     return worst;
 }
 
+bool muon_factors_ok(const wg_muon_problem& p)
+{
+    return p.mu >= 0.f && p.mu < 1.f && p.dampening >= 0.f && p.dampening <= 1.f && p.eps >= 0.f && isfinite(p.eps) &&
+           isfinite(p.scale) && isfinite(p.lr) && isfinite(p.weight_decay);
+}
+
 int make_muon_plan(const wg_muon_problem* p, MuonPlan* pl)
 {
     if (!p) return set_err(WG_ERR_INVALID_ARGUMENT, "problem is NULL");
@@ -251,8 +257,7 @@ int make_muon_plan(const wg_muon_problem* p, MuonPlan* pl)
     if (!dtype_ok(p->grad_dtype) || !dtype_ok(p->out_dtype) || !dtype_ok(p->weight_dtype))
         return set_err(WG_ERR_INVALID_ARGUMENT, "grad_dtype, out_dtype and weight_dtype must be WG_FP32, WG_BF16 or WG_FP16");
     if (p->steps < 0 || p->steps > kMuonMaxSteps) return set_err(WG_ERR_INVALID_ARGUMENT, "steps must be 0..16");
-    if (!(p->mu >= 0.f && p->mu < 1.f) || !(p->dampening >= 0.f && p->dampening <= 1.f) || !(p->eps >= 0.f) ||
-        !isfinite(p->eps) || !isfinite(p->scale) || !isfinite(p->lr) || !isfinite(p->weight_decay))
+    if (!muon_factors_ok(*p))
         return set_err(WG_ERR_INVALID_ARGUMENT, "mu must be in [0, 1), dampening in [0, 1], eps >= 0, and every factor finite");
     pl->p = *p;
     wg_muon_problem& q = pl->p;
@@ -317,26 +322,31 @@ int make_muon_plan(const wg_muon_problem* p, MuonPlan* pl)
     return WG_OK;
 }
 
-// Plans are a pure function of the problem, its coefficients and the SM count;
-// successful ones are cached, so that repeated calls skip the range checks.  (Where
-// the cache cannot have memory, the plan is made anew.)
+// Plans are a pure function of the sizes, types and strides, the coefficients and the SM
+// count; successful ones are cached, so that repeated calls skip the range checks.  (Where
+// the cache cannot have memory, the plan is made anew.)  The factors, of which a learning
+// rate changes from step to step, are the call's own.
 int muon_plan(const wg_muon_problem* p, MuonPlan* pl)
 {
-    if (!p || p->steps < 0 || p->steps > kMuonMaxSteps) return make_muon_plan(p, pl);
+    if (!p || p->steps < 0 || p->steps > kMuonMaxSteps || !muon_factors_ok(*p)) return make_muon_plan(p, pl);
     static std::mutex mu;
     static std::map<std::string, MuonPlan> cache;
     std::string key;
     try {
-        // (The record without its pointer and its tail padding.)
-        const int sms = num_sms();
-        key.assign(reinterpret_cast<const char*>(p), offsetof(wg_muon_problem, coef));
-        key.append(reinterpret_cast<const char*>(&p->mu), 6 * sizeof(float));
-        key.append(reinterpret_cast<const char*>(&sms), sizeof sms);
+        // (The record's members one by one: what lies between them may be anything.)
+        const auto add = [&key](const auto& v) { key.append(reinterpret_cast<const char*>(&v), sizeof v); };
+        key.reserve(384);
+        add(p->batch), add(p->rows), add(p->cols), add(p->ld), add(p->batch_stride);
+        add(p->grad_dtype), add(p->out_dtype), add(p->weight_dtype), add(p->steps), add(p->nesterov);
+        add(num_sms());
         if (p->coef) key.append(reinterpret_cast<const char*>(p->coef), (size_t)p->steps * 3 * sizeof(float));
         std::lock_guard<std::mutex> lk(mu);
         const auto it = cache.find(key);
         if (it != cache.end()) {
             *pl = it->second;
+            wg_muon_problem& q = pl->p;
+            q.mu = p->mu, q.dampening = p->dampening, q.eps = p->eps;
+            q.scale = p->scale, q.lr = p->lr, q.weight_decay = p->weight_decay;
             return WG_OK;
         }
     } catch (...) {

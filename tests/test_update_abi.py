@@ -197,3 +197,35 @@ def test_strides_whose_addresses_would_overflow_are_refused(big):
     refused(1, binding.wg_muon_workspace_size, muon(batch=2, batch_stride=-big))
     # What no address is made of does not count: the distance to a second matrix that is not there.
     assert binding.wg_muon_workspace_size(muon(batch_stride=big)) > 0
+
+
+def test_plans_are_found_whatever_the_record_s_padding_and_factors_hold():
+    """A caller in C leaves the bytes between the record's members as they were, and a learning rate changes with every
+    step: such a call finds the plan all the same, instead of making it anew (some 30 times as long)."""
+    import ctypes
+    import time
+    lib, p, n = binding.load(), binding.make_muon_problem({"rows": 1000, "cols": 2731}), ctypes.c_size_t(0)
+    raw = (ctypes.c_ubyte * ctypes.sizeof(p)).from_buffer(p)
+    used = set()
+    for name, kind in p._fields_:
+        at = getattr(type(p), name).offset
+        used |= set(range(at, at + ctypes.sizeof(kind)))
+    holes = [i for i in range(ctypes.sizeof(p)) if i not in used]
+    assert holes
+
+    def best(change):
+        times = []
+        for k in range(400):
+            if change:
+                for i in holes:
+                    raw[i] = (37 * best.calls + i) & 255
+                p.lr, p.scale = 1e-3 / (1 + best.calls), 1 + best.calls
+                best.calls += 1
+            t = time.perf_counter()
+            assert lib.wg_muon_workspace_size(ctypes.byref(p), ctypes.byref(n)) == 0
+            times.append(time.perf_counter() - t)
+        return sorted(times)[200]
+
+    best.calls = 0
+    same = best(False)
+    assert best(True) < 5 * same
