@@ -349,8 +349,9 @@ WG_API int wg_bwd_data_plan_string(const wg_problem* p, char* buf, size_t n);
  * roundings brought up to singular values near 1; X stays finite all the same.
  * out and w are then rounded to nearest even.
  * A zero matrix gives zeros; a NaN or an infinity in u makes its matrix's X NaN, and
- * so does |u|_F above 1.8e19, whose square is beyond fp32 (elements below 1e-22 count
- * as zero beside it).
+ * so does |u|_F above 1.8e19, whose square is beyond fp32.  Squares of elements below
+ * some 1e-19 are lost from |u|_F (which shows only where eps is smaller still), and X of
+ * a larger matrix, held in fp16, loses bits where |u|_F is below 1e-7 sqrt(rows cols) eps.
  * Results are bitwise reproducible from run to run.
  *
  *  batch >= 1, rows >= 1, cols >= 1; rows, cols <= 32768; batch <= 65535.
