@@ -212,8 +212,7 @@ __device__ __forceinline__ float block_sum_256(float s)
     return s;
 }
 
-// What u at VEC elements along a row is made of, and u.  STEP: the momentum's step
-// is taken (m is then the new momentum); otherwise it has been.
+// What u at VEC elements along a row is made of.
 template <int VEC>
 __device__ __forceinline__ void muon_read(const MuonParams& p, long long e, float (&g)[VEC], float (&m)[VEC])
 {
@@ -223,6 +222,7 @@ __device__ __forceinline__ void muon_read(const MuonParams& p, long long e, floa
         g[0] = muon_elem(p, e);
     if (p.mom) load_f32<float, VEC>(p.mom + e, m);
 }
+// u.  STEP: the momentum's step is taken (m is then the new momentum); otherwise it has been.
 template <int VEC, bool STEP>
 __device__ __forceinline__ void muon_make(const MuonParams& p, float (&u)[VEC], float (&m)[VEC])
 {
@@ -234,15 +234,6 @@ __device__ __forceinline__ void muon_make(const MuonParams& p, float (&u)[VEC], 
         u[k] = p.nesterov ? fmaf(p.mu, m[k], y) : m[k];
     }
 }
-template <int VEC, bool STEP>
-__device__ __forceinline__ void muon_u(const MuonParams& p, long long e, float (&u)[VEC])
-{
-    float m[VEC];
-    muon_read<VEC>(p, e, u, m);
-    muon_make<VEC, STEP>(p, u, m);
-    if (STEP && p.mom) store_f32<float, VEC>(p.mom + e, m);
-}
-
 // The row of vector i of a matrix of p.nv vectors a row (i < 2^31).
 __device__ __forceinline__ int muon_row(const MuonParams& p, int i)
 {

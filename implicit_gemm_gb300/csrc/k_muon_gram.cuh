@@ -1,5 +1,6 @@
-// Orthogonalised update of matrices whose shorter side is at most 128, in one
-// launch: the whole iteration runs on the Gram matrix.
+// Orthogonalised update of matrices whose shorter side is at most 128: the iteration
+// runs on the Gram matrix, in one launch as long as errors stay small (five default
+// steps do).
 //
 // With A = X X^T and P = a I + b A + c A A a step is X <- P X, so A <- P A P and
 // X_k = Q_k X_0 with Q <- P Q.  All of these are polynomials of one symmetric
@@ -13,10 +14,10 @@
 // tensor memory.  (With single fp16 operands gradients of low rank lose every
 // digit.)  U U^T takes u as up to three bf16 values, whose range is fp32's: one for
 // bf16 gradients, two for fp16, three for fp32 and with momentum (with two of fp32's
-// three, noise beside a strong direction came out up to 8% off).  X = Q U takes it as a
-// pair of fp16 values under its matrix's power of two, which the norm gives by then,
-// and so has all of Q's 22 bits (with Q as a pair of bf16 values gradients of rank one
-// were 3e-3 off, instead of 1e-4).
+// three, noise beside one strong direction came out up to 2% off for 8 x 72 and 8% for
+// 3 x 7; now 1.5e-3 and 2.9e-3).  X = Q U takes it as a pair of fp16 values under its
+// matrix's power of two, which the norm gives by then, and so has all of Q's 22 bits
+// (64 x 576 of rank one 1.0e-3 off, with Q as a pair of bf16 values 2.8e-3).
 //
 // A block of P = 64 or 128 rows of the Gram matrix holds as many whole matrices
 // as fit (the block-diagonal fold of the convolution kernels): entries of A_0
@@ -222,7 +223,6 @@ __device__ __forceinline__ void gram_each(const GramParams& g, int blk, long lon
     }
 }
 
-// STEP: the momentum's step is taken and written; otherwise it has been.
 template <bool VEC>
 __device__ __forceinline__ void gram_read(const GramParams& g, int blk, long long e, int pos, GramRaw& r)
 {
@@ -248,6 +248,7 @@ __device__ __forceinline__ void gram_read(const GramParams& g, int blk, long lon
     r.m.a = make_uint4(m[0], m[1], m[2], m[3]), r.m.b = make_uint4(m[4], m[5], m[6], m[7]);
 }
 
+// STEP: the momentum's step is taken and written; otherwise it has been.
 template <bool VEC, bool STEP>
 __device__ __forceinline__ void gram_make(const GramParams& g, int blk, long long e, int pos, const GramRaw& r, float (&u)[8])
 {
