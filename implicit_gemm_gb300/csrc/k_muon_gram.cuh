@@ -72,14 +72,17 @@ struct GramParams {
 __host__ __device__ constexpr int gram_mat_bytes(int P) { return P * P * 2; }  // one fp16 image
 // Three pairs of images, and slack for A operands of 128 rows read from images of 64.
 __host__ __device__ constexpr int gram_used_bytes(int P) { return 6 * gram_mat_bytes(P) + 8192 + 1024; }
-// What is asked for: all that a CTA may have beside the static variables, so that no
-// other CTA that takes tensor memory, of this kernel or another, is on the SM.  A CTA
-// takes all of tensor memory and then waits for its cluster; two clusters of two
-// streams that share a pair of SMs would each hold what the other waits for, and
-// tcgen05.alloc has no limit.
-constexpr int kGramSmem = 224 * 1024;
-static_assert(gram_used_bytes(128) <= kGramSmem, "shared memory of a CTA");
-static_assert(2 * kGramSmem > 228 * 1024, "one CTA on an SM");
+// What is asked for: so much that no other CTA that takes tensor memory and waits for
+// its cluster is on the SM, of this kernel or another.  A CTA takes all of tensor memory
+// and then waits for its cluster; two clusters of two streams that share a pair of SMs
+// would each hold what the other waits for, and tcgen05.alloc has no limit.  The least
+// that such a kernel asks for is 35 KB (eight stages of 4 KB, and 3, of a convolution
+// reduced over a cluster), and 1 KB per CTA is the system's.  No more than that for P =
+// 64, since the rest is L1, from which rows that start anywhere are read (64 x 577 with
+// momentum: 34 us, 40 with 224 KB).
+__host__ __device__ constexpr int gram_smem_bytes(int P) { return (P == 64 ? 192 : 224) * 1024; }
+static_assert(gram_used_bytes(64) <= gram_smem_bytes(64) && gram_used_bytes(128) <= gram_smem_bytes(128), "shared memory");
+static_assert(gram_smem_bytes(64) + 1024 + 35 * 1024 + 1024 > 228 * 1024, "one CTA on an SM");
 
 // Byte offset of the 16-byte chunk that holds elements 8 c8 .. 8 c8 + 7 of row r of a K-major image of P rows:
 // 64-element (128-byte) columns of P rows, 128-byte swizzle.

@@ -98,7 +98,7 @@ int muon_gram_max_cluster()
     auto it = cache.find(dev);
     if (it != cache.end()) return it->second;
     int n = 0;
-    const int smem = wg::kGramSmem;
+    const int smem = wg::gram_smem_bytes(128);
     if (wg::ensure_smem(wg::muon_gram_kernel<128, true>, smem) == WG_OK &&
         cudaFuncSetAttribute(wg::muon_gram_kernel<128, true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
@@ -366,7 +366,7 @@ int muon_plan(const wg_muon_problem* p, MuonPlan* pl)
 template <int P, bool VEC>
 int muon_gram_launch(const MuonPlan& pl, const wg::GramParams& g, cudaStream_t s)
 {
-    const int smem = wg::kGramSmem;
+    const int smem = wg::gram_smem_bytes(P);
     const int st = wg::ensure_smem(wg::muon_gram_kernel<P, VEC>, smem);
     if (st) return st;
     if (g.C > 8) {  // beyond the portable cluster size
@@ -818,7 +818,7 @@ int wg_muon_plan_string(const wg_muon_problem* p, char* buf, size_t n)
         snprintf(buf, n, "kernel=muon_gram side=%s m=%d block=%d fold=%d blocks=%d cluster=%d chunks=%d steps=%d launches=%d "
                  "smem=%d ws=%zu",
                  p->rows <= p->cols ? "left" : "right", pl.m, pl.P, pl.g.F, pl.blocks, pl.g.C, pl.g.chunks, p->steps,
-                 pl.launches, wg::kGramSmem, pl.bytes);
+                 pl.launches, wg::gram_smem_bytes(pl.P), pl.bytes);
     else
         snprintf(buf, n, "kernel=muon_product side=%s m=%d steps=%d values=%d smem=%d ws=%zu",
                  p->rows <= p->cols ? "left" : "right", pl.m, p->steps, pl.two ? 2 : 1, wg::Mg<256>::kSmem, pl.bytes);

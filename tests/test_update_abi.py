@@ -144,9 +144,26 @@ def test_wrappers_refuse_tensors_that_do_not_fit():
 @pytest.mark.parametrize("rows,cols", [(1, 1), (8, 72), (64, 576), (128, 128), (300, 400)])
 def test_muon_kernels_take_an_sm_whole(rows, cols):
     """A CTA of these kernels takes tensor memory and then waits for its cluster: two that shared an SM could wait for
-    each other for ever.  They ask for (nearly) all of an SM's 228 KB of shared memory."""
+    each other for ever.  They ask for so much of an SM's 228 KB of shared memory (1 KB of it per CTA is the system's)
+    that none fits beside another, nor beside a convolution's that is reduced over a cluster or runs on a pair."""
     plan = dict(kv.split("=") for kv in binding.wg_muon_plan_string(muon(rows=rows, cols=cols)).split())
-    assert int(plan["smem"]) >= 224 * 1024
+    least = 228 * 1024 - 1024 - int(plan["smem"])  # what another CTA could have, the system's part of it included
+    assert least < 1024 + int(plan["smem"])
+    conv = {"ndim": 1, "G": 1, "N": 2, "C": 8, "K": 8, "in": [8], "filt": [1], "stride": [1], "dil": [1], "pad_l": [0],
+            "pad_r": [0], "in_dtype": "bf16", "out_dtype": "fp32"}
+    seen = 0
+    for n in (2, 8, 32):
+        for c, k, cluster in ((8, 8, 2), (8, 8, 4), (16, 8, 8), (8, 64, 2), (64, 64, 2)):
+            for x in (1, 3):
+                sp = {**conv, "N": n, "C": c, "K": k, "in": [16], "filt": [x], "pad_l": [x // 2], "pad_r": [x // 2]}
+                try:
+                    text = binding.wg_plan_string(sp, 2 * cluster, "deterministic", cluster=cluster)
+                except binding.WgradError:
+                    continue
+                other = dict(kv.split("=", 1) for kv in text.split() if "=" in kv)
+                seen += other.get("cluster", "1") != "1"
+                assert least < 1024 + int(other["smem"]), text
+    assert seen
 
 
 def test_muon_steps_of_a_launch():
