@@ -20,7 +20,8 @@ from . import build as _build
 DTYPES = {"bf16": 0, "fp16": 1, "fp32": 2}
 MODES = {"auto": 0, "direct": 1, "atomic": 2, "deterministic": 3}
 STATUS = {0: "WG_OK", 1: "WG_ERR_INVALID_ARGUMENT", 2: "WG_ERR_NOT_SUPPORTED", 3: "WG_ERR_MISALIGNED",
-          4: "WG_ERR_WORKSPACE", 5: "WG_ERR_CUDA", 6: "WG_ERR_DEVICE_TIMEOUT", 7: "WG_ERR_INVALID_TOKEN"}
+          4: "WG_ERR_WORKSPACE", 5: "WG_ERR_CUDA", 6: "WG_ERR_DEVICE_TIMEOUT", 7: "WG_ERR_INVALID_TOKEN",
+          8: "WG_ERR_INVALID_OFFSET"}
 
 
 class WgProblem(ctypes.Structure):
@@ -52,6 +53,23 @@ class WgEmbeddingProblem(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+class WgLinearProblem(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_longlong), ("in_", ctypes.c_int), ("out", ctypes.c_int), ("experts", ctypes.c_int),
+                ("ld_in", ctypes.c_longlong), ("ld_out", ctypes.c_longlong), ("ld_weight", ctypes.c_longlong),
+                ("weight_stride", ctypes.c_longlong), ("ld_z", ctypes.c_longlong), ("ld_residual", ctypes.c_longlong),
+                ("in_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int), ("bias_dtype", ctypes.c_int),
+                ("offset_bits", ctypes.c_int), ("activation", ctypes.c_int), ("dropout", ctypes.c_float),
+                ("seed", ctypes.c_ulonglong), ("offset", ctypes.c_ulonglong), ("counter", ctypes.c_void_p)]
+
+
+class WgActivationProblem(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_longlong), ("dim", ctypes.c_int), ("ld_x", ctypes.c_longlong),
+                ("ld_y", ctypes.c_longlong), ("ld_residual", ctypes.c_longlong), ("ld_dx", ctypes.c_longlong),
+                ("in_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int), ("bias_dtype", ctypes.c_int),
+                ("activation", ctypes.c_int), ("dropout", ctypes.c_float), ("seed", ctypes.c_ulonglong),
+                ("offset", ctypes.c_ulonglong), ("counter", ctypes.c_void_p)]
+
+
 class WgradError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{STATUS.get(status, status)}: {message}")
@@ -62,7 +80,9 @@ EXPORTS = ("wg_problem_normalize", "wg_workspace_size", "wg_conv_bwd_weight", "w
            "wg_plan_string", "wg_status_string", "wg_last_error", "wg_conv_bwd_weight_noalloc",
            "wg_set_mark_event", "wg_conv_bwd_data", "wg_bwd_data_plan_string", "wg_bwd_data_workspace_size",
            "wg_conv_bwd_weight_host", "wg_selftest_timeout", "wg_muon_workspace_size", "wg_muon_plan_string",
-           "wg_muon_update", "wg_embedding_lookup", "wg_embedding_workspace_size", "wg_embedding_bwd_weight")
+           "wg_muon_update", "wg_embedding_lookup", "wg_embedding_workspace_size", "wg_embedding_bwd_weight",
+           "wg_linear_workspace_size", "wg_linear_plan_string", "wg_linear", "wg_linear_bwd_data", "wg_linear_bwd_weight",
+           "wg_activation_workspace_size", "wg_activation", "wg_activation_bwd")
 
 _lib = None
 _lock = threading.Lock()
@@ -106,6 +126,15 @@ def load():
             lib.wg_embedding_workspace_size.argtypes = [EP, ctypes.POINTER(ctypes.c_size_t)]
             lib.wg_embedding_bwd_weight.argtypes = [EP] + [ctypes.c_void_p] * 3 + [ctypes.c_int, ctypes.c_void_p,
                                                                                    ctypes.c_size_t, ctypes.c_void_p]
+            LP, AP, V = ctypes.POINTER(WgLinearProblem), ctypes.POINTER(WgActivationProblem), ctypes.c_void_p
+            lib.wg_linear_workspace_size.argtypes = [LP, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]
+            lib.wg_linear_plan_string.argtypes = [LP, ctypes.c_int, ctypes.c_char_p, ctypes.c_size_t]
+            lib.wg_linear.argtypes = [LP] + [V] * 8 + [ctypes.c_size_t, V]
+            lib.wg_linear_bwd_data.argtypes = [LP] + [V] * 7 + [ctypes.c_size_t, V]
+            lib.wg_linear_bwd_weight.argtypes = [LP] + [V] * 5 + [ctypes.c_int, V, ctypes.c_size_t, V]
+            lib.wg_activation_workspace_size.argtypes = [AP, ctypes.POINTER(ctypes.c_size_t)]
+            lib.wg_activation.argtypes = [AP] + [V] * 5
+            lib.wg_activation_bwd.argtypes = [AP] + [V] * 6 + [ctypes.c_size_t, V]
             lib.wg_status_string.argtypes = [ctypes.c_int]
             lib.wg_status_string.restype = ctypes.c_char_p
             lib.wg_last_error.restype = ctypes.c_char_p
@@ -354,6 +383,16 @@ def _empty(stream, shape, dtype, device, returned: bool = False):
         t = torch.empty(shape, dtype=dtype, device=device)
     if returned:
         t.record_stream(here)
+    return t
+
+
+def _zeros(stream, shape, dtype, device, returned: bool = False):
+    """The same, filled with zeros on the call's stream."""
+    import torch
+    t = _empty(stream, shape, dtype, device, returned)
+    with torch.cuda.stream(torch.cuda.current_stream(device) if stream is None else stream if isinstance(stream, torch.cuda.Stream)
+                           else torch.cuda.ExternalStream(_stream_handle(stream), device)):
+        t.zero_()
     return t
 
 
@@ -606,4 +645,319 @@ def embedding_bwd_weight(token, dy, vocab: int, scale: float = 1.0, padding_toke
         out = _empty(stream, (vocab, dim), dy.dtype, dy.device, returned=True)
     ws = _empty(stream, max(nbytes, 1), torch.uint8, dy.device)
     wg_embedding_bwd_weight(spec, token, dy, out, accumulate, ws, nbytes, stream)
+    return out
+
+
+# ---------------------------------------------------------------- layers
+
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+LINEAR_CALLS = {"forward": 0, "bwd_data": 1, "bwd_weight": 2}
+
+
+def _set_tail(p, spec: dict) -> None:
+    p.in_dtype, p.out_dtype = DTYPES[spec.get("in_dtype", "bf16")], DTYPES[spec.get("out_dtype", "bf16")]
+    p.bias_dtype = DTYPES[spec.get("bias_dtype", "fp32")]
+    p.activation, p.dropout = ACTIVATIONS[spec.get("activation", "none")], spec.get("dropout", 0.0)
+    p.seed, p.offset = int(spec.get("seed", 0)) % (1 << 64), int(spec.get("offset", 0)) % (1 << 64)
+    p.counter = _addr(spec.get("counter")) or None
+
+
+def make_linear_problem(spec: dict) -> WgLinearProblem:
+    """A spec is a dict: tokens, in, out, and optionally experts (0), ld_in, ld_out, ld_weight, weight_stride, ld_z,
+    ld_residual (elements; 0 = packed), in_dtype, out_dtype ('bf16'), bias_dtype ('fp32'), offset_dtype ('i32' | 'i64',
+    default i32), activation ('none' | 'relu' | 'gelu' | 'gelu_tanh' | 'silu'), dropout (0), seed, offset (0), counter (a
+    device tensor of one 64-bit integer, or None; the caller keeps it).  See include/wgrad.h for the formulas."""
+    p = WgLinearProblem()
+    p.tokens, p.in_, p.out, p.experts = spec["tokens"], spec["in"], spec["out"], spec.get("experts", 0)
+    for key in ("ld_in", "ld_out", "ld_weight", "weight_stride", "ld_z", "ld_residual"):
+        setattr(p, key, spec.get(key, 0))
+    p.offset_bits = {"i32": 32, "i64": 64}[spec.get("offset_dtype", "i32")]
+    _set_tail(p, spec)
+    return p
+
+
+def make_activation_problem(spec: dict) -> WgActivationProblem:
+    """A spec is a dict: tokens, dim, and optionally ld_x, ld_y, ld_residual, ld_dx (elements; 0 = dim), in_dtype,
+    out_dtype ('bf16'), bias_dtype ('fp32'), activation, dropout, seed, offset, counter (as in make_linear_problem)."""
+    p = WgActivationProblem()
+    p.tokens, p.dim = spec["tokens"], spec["dim"]
+    for key in ("ld_x", "ld_y", "ld_residual", "ld_dx"):
+        setattr(p, key, spec.get(key, 0))
+    _set_tail(p, spec)
+    return p
+
+
+def wg_linear_workspace_size(spec: dict, call: str = "forward") -> int:
+    """Bytes of workspace of a call: 'forward', 'bwd_data' or 'bwd_weight'."""
+    p, n = make_linear_problem(spec), ctypes.c_size_t(0)
+    _check(load().wg_linear_workspace_size(ctypes.byref(p), LINEAR_CALLS[call], ctypes.byref(n)))
+    return int(n.value)
+
+
+def wg_linear_plan_string(spec: dict, call: str = "forward") -> str:
+    p, buf = make_linear_problem(spec), ctypes.create_string_buffer(1024)
+    _check(load().wg_linear_plan_string(ctypes.byref(p), LINEAR_CALLS[call], buf, len(buf)))
+    return buf.value.decode()
+
+
+def wg_activation_workspace_size(spec: dict) -> int:
+    p, n = make_activation_problem(spec), ctypes.c_size_t(0)
+    _check(load().wg_activation_workspace_size(ctypes.byref(p), ctypes.byref(n)))
+    return int(n.value)
+
+
+class _Prepared:
+    """A call with its arguments marshalled once: calling it makes one ctypes call.  Keeps references to the tensors it
+    was built from.  `p` is the problem record: a change to it (p.offset of a dropout, say) counts for later calls."""
+
+    def _set(self, fn, p, tensors, extra, keep, workspace, ws_bytes, has_workspace=True):
+        self._keep = (*tensors, workspace, keep)
+        self.p, self.fn = p, fn
+        self.args = (ctypes.byref(p), *(ctypes.c_void_p(_addr(t)) for t in tensors), *extra)
+        if has_workspace:
+            self.args += (ctypes.c_void_p(_addr(workspace)), ctypes.c_size_t(_bytes_of(workspace, ws_bytes)))
+
+    def __call__(self, stream_handle: int | None = None) -> None:
+        st = self.fn(*self.args, stream_handle)
+        if st:
+            _check(st)
+
+
+class PreparedLinear(_Prepared):
+    """wg_linear with its arguments marshalled once."""
+
+    def __init__(self, spec: dict, x, w, y, bias=None, residual=None, z=None, offsets=None, workspace=None,
+                 ws_bytes: int | None = None):
+        self._set(load().wg_linear, make_linear_problem(spec), (offsets, x, w, bias, residual, y, z), (), spec.get("counter"),
+                  workspace, ws_bytes)
+
+
+class PreparedLinearBwdData(_Prepared):
+    """wg_linear_bwd_data with its arguments marshalled once."""
+
+    def __init__(self, spec: dict, dy, w, dx, z=None, residual=None, offsets=None, workspace=None, ws_bytes: int | None = None):
+        self._set(load().wg_linear_bwd_data, make_linear_problem(spec), (offsets, dy, w, z, residual, dx), (),
+                  spec.get("counter"), workspace, ws_bytes)
+
+
+class PreparedLinearBwdWeight(_Prepared):
+    """wg_linear_bwd_weight with its arguments marshalled once."""
+
+    def __init__(self, spec: dict, x, dy, dw, dbias=None, accumulate: bool = False, offsets=None, workspace=None,
+                 ws_bytes: int | None = None):
+        self._set(load().wg_linear_bwd_weight, make_linear_problem(spec), (offsets, x, dy, dw, dbias),
+                  (ctypes.c_int(int(accumulate)),), spec.get("counter"), workspace, ws_bytes)
+
+
+class PreparedActivation(_Prepared):
+    """wg_activation with its arguments marshalled once."""
+
+    def __init__(self, spec: dict, x, y, bias=None, residual=None):
+        self._set(load().wg_activation, make_activation_problem(spec), (x, bias, residual, y), (), spec.get("counter"), None, 0,
+                  False)
+
+
+class PreparedActivationBwd(_Prepared):
+    """wg_activation_bwd with its arguments marshalled once."""
+
+    def __init__(self, spec: dict, dy, x, dx, bias=None, dbias=None, workspace=None, ws_bytes: int | None = None):
+        self._set(load().wg_activation_bwd, make_activation_problem(spec), (dy, x, bias, dx, dbias), (), spec.get("counter"),
+                  workspace, ws_bytes)
+
+
+def wg_linear(spec: dict, x, w, y, bias=None, residual=None, z=None, offsets=None, workspace=None, ws_bytes: int | None = None,
+              stream=None) -> None:
+    """y = residual + D(act(x w' + bias)), z the pre-activations where given; by expert where the spec has experts."""
+    PreparedLinear(spec, x, w, y, bias, residual, z, offsets, workspace, ws_bytes)(_stream_handle(stream))
+
+
+def wg_linear_bwd_data(spec: dict, dy, w, dx, z=None, residual=None, offsets=None, workspace=None, ws_bytes: int | None = None,
+                       stream=None) -> None:
+    """dx = residual + D(act'(z) (dy w))."""
+    PreparedLinearBwdData(spec, dy, w, dx, z, residual, offsets, workspace, ws_bytes)(_stream_handle(stream))
+
+
+def wg_linear_bwd_weight(spec: dict, x, dy, dw, dbias=None, accumulate: bool = False, offsets=None, workspace=None,
+                         ws_bytes: int | None = None, stream=None) -> None:
+    """dw = dy' x and dbias = column sums of dy, per expert; added to what is there when accumulate."""
+    PreparedLinearBwdWeight(spec, x, dy, dw, dbias, accumulate, offsets, workspace, ws_bytes)(_stream_handle(stream))
+
+
+def wg_activation(spec: dict, x, y, bias=None, residual=None, stream=None) -> None:
+    """y = residual + D(act(x + bias))."""
+    PreparedActivation(spec, x, y, bias, residual)(_stream_handle(stream))
+
+
+def wg_activation_bwd(spec: dict, dy, x, dx, bias=None, dbias=None, workspace=None, ws_bytes: int | None = None,
+                      stream=None) -> None:
+    """dx = D(act'(x + bias) dy), dbias = column sums of dx."""
+    PreparedActivationBwd(spec, dy, x, dx, bias, dbias, workspace, ws_bytes)(_stream_handle(stream))
+
+
+_NAMES = {"torch.float32": "fp32", "torch.bfloat16": "bf16", "torch.float16": "fp16"}
+
+
+def _name(t, what: str) -> str:
+    if str(t) not in _NAMES:
+        raise ValueError(f"{what} of type {t} is not supported")
+    return _NAMES[str(t)]
+
+
+def _tail_spec(activation, dropout, seed, offset, counter) -> dict:
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation {activation!r} is not one of {', '.join(ACTIVATIONS)}")
+    if counter is not None and (str(counter.dtype) != "torch.int64" or counter.numel() != 1):
+        raise ValueError("counter must be an int64 tensor of one element")
+    _on_gpu(counter=counter)
+    return {"activation": activation, "dropout": dropout, "seed": seed, "offset": offset, "counter": counter}
+
+
+def _same_device(**tensors) -> None:
+    _on_gpu(**tensors)
+    devices = {t.device for t in tensors.values() if t is not None}
+    if len(devices) > 1:
+        raise ValueError("tensors on different devices: " + ", ".join(sorted(map(str, devices))))
+
+
+def _linear_spec(rows, w, offsets, in_dtype, out_dtype, bias, tail) -> dict:
+    """Of x or dy's rows and w (or the weight gradient's shape): (out, in), or (experts, out, in) with offsets."""
+    shape = tuple(w)
+    if len(shape) != (2 if offsets is None else 3):
+        raise ValueError("w must have shape (out, in), or (experts, out, in) with offsets")
+    experts = 0 if offsets is None else shape[0]
+    spec = {"tokens": rows, "in": shape[-1], "out": shape[-2], "experts": experts, "in_dtype": in_dtype, "out_dtype": out_dtype,
+            "bias_dtype": "fp32" if bias is None else _name(bias.dtype, "a bias"), **tail}
+    if offsets is not None:
+        kinds = {"torch.int32": "i32", "torch.int64": "i64"}
+        if str(offsets.dtype) not in kinds or not offsets.is_contiguous() or offsets.numel() != experts + 1:
+            raise ValueError("offsets must be contiguous int32 or int64, one more than experts")
+        spec["offset_dtype"] = kinds[str(offsets.dtype)]
+    return spec
+
+
+def linear(x, w, bias=None, residual=None, activation: str = "none", dropout: float = 0.0, seed: int = 0, offset: int = 0,
+           counter=None, offsets=None, keep_z: bool = False, out=None, stream=None):
+    """Convenience wrapper over wg_linear for contiguous torch CUDA tensors: x of shape (..., in), w (out, in) and bias
+    (out,), or with offsets (experts + 1 row numbers) x (rows, in), w (experts, out, in) and bias (experts, out).  Returns
+    y of shape (..., out) in x's type (or residual's, or `out`), or (y, z) when keep_z.  Without `out`, rows of no expert
+    are zeros."""
+    import torch
+    dt = _name(x.dtype, "x")
+    ydt = out.dtype if out is not None else residual.dtype if residual is not None else x.dtype
+    rows = x.numel() // x.shape[-1] if x.shape[-1] else 0
+    spec = _linear_spec(rows, w.shape, offsets, dt, _name(ydt, "y"), bias, _tail_spec(activation, dropout, seed, offset, counter))
+    nbytes = wg_linear_workspace_size(spec, "forward")  # (checks the spec)
+    shape = (*x.shape[:-1], spec["out"])
+    _expect("x", x, dt, (*x.shape[:-1], spec["in"]))
+    _expect("w", w, dt, w.shape)
+    _expect("bias", bias, spec["bias_dtype"], w.shape[:-1])
+    _expect("residual", residual, spec["out_dtype"], shape)
+    _expect("out", out, spec["out_dtype"], shape)
+    _same_device(x=x, w=w, bias=bias, residual=residual, out=out, offsets=offsets, counter=counter)
+    with torch.cuda.device(x.device):
+        make = _zeros if offsets is not None else _empty
+        z = make(stream, shape, x.dtype, x.device, returned=True) if keep_z else None
+        if out is None:
+            out = make(stream, shape, ydt, x.device, returned=True)
+        ws = _empty(stream, nbytes, torch.uint8, x.device)
+        wg_linear(spec, x, w, out, bias, residual, z, offsets, ws, nbytes, stream)
+    return (out, z) if keep_z else out
+
+
+def linear_bwd_data(dy, w, z=None, residual=None, activation: str = "none", dropout: float = 0.0, seed: int = 0, offset: int = 0,
+                    counter=None, offsets=None, out=None, stream=None):
+    """Convenience wrapper over wg_linear_bwd_data: dy (..., out), w as in linear; z (..., in) and the factors of the layer
+    below where its activation and dropout made x.  Returns dx (..., in) in dy's type (or residual's, or `out`)."""
+    import torch
+    dt = _name(dy.dtype, "dy")
+    xdt = out.dtype if out is not None else residual.dtype if residual is not None else dy.dtype
+    rows = dy.numel() // dy.shape[-1] if dy.shape[-1] else 0
+    spec = _linear_spec(rows, w.shape, offsets, dt, _name(xdt, "dx"), None, _tail_spec(activation, dropout, seed, offset, counter))
+    nbytes = wg_linear_workspace_size(spec, "bwd_data")
+    shape = (*dy.shape[:-1], spec["in"])
+    _expect("dy", dy, dt, (*dy.shape[:-1], spec["out"]))
+    _expect("w", w, dt, w.shape)
+    _expect("z", z, dt, shape)
+    _expect("residual", residual, spec["out_dtype"], shape)
+    _expect("out", out, spec["out_dtype"], shape)
+    _same_device(dy=dy, w=w, z=z, residual=residual, out=out, offsets=offsets, counter=counter)
+    with torch.cuda.device(dy.device):
+        if out is None:
+            out = (_zeros if offsets is not None else _empty)(stream, shape, xdt, dy.device, returned=True)
+        ws = _empty(stream, nbytes, torch.uint8, dy.device)
+        wg_linear_bwd_data(spec, dy, w, out, z, residual, offsets, ws, nbytes, stream)
+    return out
+
+
+def linear_bwd_weight(x, dy, offsets=None, out=None, dbias=None, accumulate: bool = False, stream=None):
+    """Convenience wrapper over wg_linear_bwd_weight: x (..., in), dy (..., out).  Returns dw (out, in), or (experts, out,
+    in) with offsets, fp32 (or `out`, added to when accumulate).  dbias ((out,) or (experts, out)) is written where given."""
+    import torch
+    dt = _name(x.dtype, "x")
+    if out is None and accumulate:
+        raise ValueError("accumulate needs out")
+    shape = (dy.shape[-1], x.shape[-1]) if offsets is None else (offsets.numel() - 1, dy.shape[-1], x.shape[-1])
+    rows = x.numel() // x.shape[-1] if x.shape[-1] else 0
+    wdt = torch.float32 if out is None else out.dtype
+    spec = _linear_spec(rows, shape, offsets, dt, _name(wdt, "dw"), dbias, {})
+    nbytes = wg_linear_workspace_size(spec, "bwd_weight")
+    _expect("x", x, dt, (*x.shape[:-1], spec["in"]))
+    _expect("dy", dy, dt, (*x.shape[:-1], spec["out"]))
+    _expect("out", out, spec["out_dtype"], shape)
+    _expect("dbias", dbias, spec["bias_dtype"], shape[:-1])
+    _same_device(x=x, dy=dy, out=out, dbias=dbias, offsets=offsets)
+    with torch.cuda.device(x.device):
+        if out is None:
+            out = _empty(stream, shape, wdt, x.device, returned=True)
+        ws = _empty(stream, nbytes, torch.uint8, x.device)
+        wg_linear_bwd_weight(spec, x, dy, out, dbias, accumulate, offsets, ws, nbytes, stream)
+    return out
+
+
+def activation(x, bias=None, residual=None, activation: str = "none", dropout: float = 0.0, seed: int = 0, offset: int = 0,
+               counter=None, out=None, stream=None):
+    """Convenience wrapper over wg_activation for contiguous torch CUDA tensors: residual + D(act(x + bias)), x of shape
+    (..., dim).  Returns y in x's type (or residual's, or `out`, which may be x or residual)."""
+    import torch
+    ydt = out.dtype if out is not None else residual.dtype if residual is not None else x.dtype
+    dim = x.shape[-1]
+    spec = {"tokens": x.numel() // dim if dim else 0, "dim": dim, "in_dtype": _name(x.dtype, "x"), "out_dtype": _name(ydt, "y"),
+            "bias_dtype": "fp32" if bias is None else _name(bias.dtype, "bias"),
+            **_tail_spec(activation, dropout, seed, offset, counter)}
+    wg_activation_workspace_size(spec)  # (checks the spec)
+    _expect("x", x, spec["in_dtype"], x.shape)
+    _expect("bias", bias, spec["bias_dtype"], (dim,))
+    _expect("residual", residual, spec["out_dtype"], x.shape)
+    _expect("out", out, spec["out_dtype"], x.shape)
+    _same_device(x=x, bias=bias, residual=residual, out=out, counter=counter)
+    with torch.cuda.device(x.device):
+        if out is None:
+            out = _empty(stream, x.shape, ydt, x.device, returned=True)
+        wg_activation(spec, x, out, bias, residual, stream)
+    return out
+
+
+def activation_bwd(dy, x=None, bias=None, activation: str = "none", dropout: float = 0.0, seed: int = 0, offset: int = 0,
+                   counter=None, dbias=None, out=None, stream=None):
+    """Convenience wrapper over wg_activation_bwd: dx = D(act'(x + bias) dy) in x's type (dy's without x, or `out`, which
+    may be x or dy).  dbias (dim,) is written where given, in bias's type."""
+    import torch
+    xdt = out.dtype if out is not None else x.dtype if x is not None else dy.dtype
+    dim = dy.shape[-1]
+    b = bias if bias is not None else dbias
+    spec = {"tokens": dy.numel() // dim if dim else 0, "dim": dim, "in_dtype": _name(xdt, "dx"), "out_dtype": _name(dy.dtype, "dy"),
+            "bias_dtype": "fp32" if b is None else _name(b.dtype, "a bias"),
+            **_tail_spec(activation, dropout, seed, offset, counter)}
+    nbytes = wg_activation_workspace_size(spec)  # (checks the spec)
+    _expect("dy", dy, spec["out_dtype"], dy.shape)
+    _expect("x", x, spec["in_dtype"], dy.shape)
+    _expect("bias", bias, spec["bias_dtype"], (dim,))
+    _expect("dbias", dbias, spec["bias_dtype"], (dim,))
+    _expect("out", out, spec["in_dtype"], dy.shape)
+    _same_device(dy=dy, x=x, bias=bias, dbias=dbias, out=out, counter=counter)
+    with torch.cuda.device(dy.device):
+        if out is None:
+            out = _empty(stream, dy.shape, xdt, dy.device, returned=True)
+        ws = _empty(stream, nbytes, torch.uint8, dy.device) if dbias is not None else None
+        wg_activation_bwd(spec, dy, x, out, bias, dbias, ws, None, stream)
     return out

@@ -1,5 +1,5 @@
 // Host helpers shared by the library's translation units (defined in wgrad.cu,
-// the update status in update.cu).  Internal: nothing here is exported.
+// the status words of other units in those).  Internal: nothing here is exported.
 #pragma once
 
 #include <cuda.h>
@@ -36,8 +36,10 @@ bool aligned16(const void* ptr);
 // Programmatic stream serialization for a launch.
 void pdl_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, unsigned* na, cudaStream_t stream);
 
-// The device status word of update.cu.
+// The device status words of update.cu and layer.cu.
 cudaError_t read_update_status(unsigned int* v);
 cudaError_t write_update_status(unsigned int v);
+cudaError_t read_layer_status(unsigned int* v);
+cudaError_t write_layer_status(unsigned int v);
 
 }  // namespace wg

@@ -1,0 +1,613 @@
+// Products of a layer, for one weight or one per expert and its rows:
+//
+//   kForward:  y[t, n]  = sum over k of x[t, k] w[e, n, k]          rows t of expert e
+//   kData:     dx[t, k] = sum over n of dy[t, n] w[e, n, k]
+//   kWeight:   dw[e, n, k] = sum over the rows t of e of dy[t, n] x[t, k]
+//
+// with layer_tail's bias, activation, dropout and residual on the finished sums.
+//
+// On CTA pairs (tcgen05 .cta_group::2).  The MMA's 256 rows are columns of the result
+// (features), its columns are rows of the result (tokens; of dw the n): the number of MMA
+// columns is free in steps of 32, so an expert with 40 rows pays for 64 and not for 256.
+// Operands are read as they lie, along the sum (K-major) or across it (MN-major):
+//
+//   MMA rows     w (K-major) / w (MN-major) / x (MN-major)
+//   MMA columns  x (K-major) / dy (K-major) / dy (MN-major)
+//
+// 64 of the sum per stage of the ring; each CTA stages 128 MMA rows and half of the MMA
+// columns by TMA and holds 128 x 256 fp32 sums in tensor memory, twice, so that a tile's
+// epilogue runs beside the next tile's MMAs.
+//
+// MMAs add to their sums with truncation (a sum of equal signs over 16 n elements comes
+// out short by some 1e-7 n of itself), so a sum is taken kLinChunk blocks at a time and
+// the chunks are added in registers, rounded to nearest.
+//
+// A sum over an expert's rows ends inside a block: its last block's rows that belong to
+// the next expert are zeroed in shared memory, in both operands (0 times an infinity is
+// NaN), by a warp of their own in each CTA, which then hands the block to the MMA warp.
+//
+// Where there are fewer tiles than pairs the sum is cut into `split` parts, whose fp32
+// sums go through the workspace to linear_join_kernel, in the order of the parts.
+// Nothing waits for another CTA except within the pair, and no atomics touch data.
+#pragma once
+
+#include "k_layer.cuh"
+
+namespace wg {
+
+constexpr int kLinEpiWarps = 16;
+constexpr int kLinThreads = 32 * (3 + kLinEpiWarps);  // TMA, MMA, fixing, then the epilogue
+constexpr int kLinWarpStaging = 2048;                 // 16 result rows by 32 columns of fp32
+constexpr int kLinMaxStages = 12;
+constexpr int kLinMaxExperts = 1024;
+constexpr int kLinChunk = 8;                          // blocks of 64 per sum in tensor memory
+constexpr int kLinABytes = 16384;
+// All the shared memory that a CTA may have (see muon_product_kernel: tensor memory is
+// taken before the kernel before this one has ended).
+constexpr int kLinSmem = 227 * 1024;
+constexpr int kLinFixed = kLinEpiWarps * kLinWarpStaging + 2 * 4 * (kLinMaxExperts + 4) + 512 + 1024;
+constexpr int kLinRing = kLinSmem - kLinFixed;
+
+struct LinParams {
+    LayerTail t;
+    int experts;            // 0: one weight, every row
+    const void* offsets;    // [experts + 1] rows before each expert's
+    int offsets64;
+    long long tokens;
+    int M, N;               // columns of the result (MMA rows), and rows of it (kWeight) or 0
+    int kb;                 // 64-wide blocks of the sum (not kWeight)
+    int bf16;
+    int bt;                 // most MMA columns of a tile
+    int stages, stage_bytes;
+    int split, pairs;
+    float* part;            // [split][rows][ldp] sums of parts (split > 1)
+    long long ldp, part_rows;
+};
+
+// ---------------------------------------------------------------- experts' rows
+// off[0 .. experts]: the offsets brought into order and into [0, tokens] (a status bit
+// tells of any that were not).  Whole block; ends with a barrier.
+__device__ __forceinline__ void load_offsets(int experts, const void* offsets, int is64, long long tokens, int* off)
+{
+    if (experts == 0) {
+        if (threadIdx.x == 0) off[0] = 0, off[1] = (int)tokens;
+    } else {
+        bool bad = false;
+        for (int i = threadIdx.x; i <= experts; i += blockDim.x) {
+            const long long v = is64 ? static_cast<const long long*>(offsets)[i] : static_cast<const int*>(offsets)[i];
+            bad |= v < 0 || v > tokens;
+            off[i] = (int)max(0LL, min(tokens, v));
+        }
+        __syncthreads();
+        if (threadIdx.x < 32) {
+            int run = 0;
+            for (int i0 = 0; i0 <= experts; i0 += 32) {
+                const int i = i0 + (int)threadIdx.x;
+                const int v = i <= experts ? off[i] : 0;
+                int m = v;
+#pragma unroll
+                for (int d = 1; d < 32; d *= 2) {
+                    const int o = __shfl_up_sync(0xffffffffu, m, d);
+                    if ((int)threadIdx.x >= d) m = max(m, o);
+                }
+                m = max(m, run);
+                if (i <= experts) {
+                    bad |= m > v;
+                    off[i] = m;
+                }
+                run = __shfl_sync(0xffffffffu, m, 31);
+            }
+        }
+        if (bad) atomicOr(&g_status, kStatusBadOffset);
+    }
+    __syncthreads();
+}
+
+// The last i with first[i] <= v, i < n (first ascending, first[0] <= v): empty experts have the
+// same first as the one after them, and the one that holds v is the last of those.
+__device__ __forceinline__ int find_last(const int* first, int n, int v)
+{
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first[mid] <= v)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// ---------------------------------------------------------------- tiles
+struct LinTile {
+    int e;           // expert
+    int m;           // first column of the result
+    int n, rows;     // first row of the result (of e's matrix for kWeight), rows
+    int wide;        // MMA columns
+    int k0, k1;      // blocks of the sum
+    int row0, valid; // kWeight: first row of the sum, and rows of its last block (64: nothing to zero)
+    int part;
+};
+
+// n rows in tiles of at most bt: as even as steps of 32 allow.
+__device__ __forceinline__ void lin_width(int n, int bt, int& tiles, int& width)
+{
+    tiles = (n + bt - 1) / bt;
+    width = tiles ? ((n + tiles - 1) / tiles + 31) / 32 * 32 : 32;
+}
+
+template <int KIND>
+struct LinWalk {
+    const LinParams& p;
+    const int *off, *first;
+    int im, total, item;
+    __device__ __forceinline__ LinWalk(const LinParams& p_, const int* off_, const int* first_, int pair)
+        : p(p_), off(off_), first(first_), im((p_.M + 255) / 256), item(pair)
+    {
+        int tiles, width;
+        if (KIND == kWeight) {
+            lin_width(p.N, p.bt, tiles, width);
+            total = max(p.experts, 1) * im * tiles * p.split;
+        } else {
+            total = first[max(p.experts, 1)] * im * p.split;
+        }
+    }
+    __device__ __forceinline__ bool next(LinTile& t)
+    {
+        if (item >= total) return false;
+        int i = item / p.split;
+        t.part = item - i * p.split;
+        item += p.pairs;
+        int tiles, width, n, kb = p.kb;
+        if (KIND == kWeight) {
+            n = p.N;
+            lin_width(n, p.bt, tiles, width);
+            t.e = i / (im * tiles);
+            i -= t.e * im * tiles;
+            t.row0 = off[t.e];
+            const int rows = off[t.e + 1] - t.row0;
+            kb = (rows + 63) >> 6;
+            t.valid = rows & 63 ? rows & 63 : 64;
+        } else {
+            t.e = find_last(first, max(p.experts, 1), i / im);
+            i -= first[t.e] * im;
+            n = off[t.e + 1] - off[t.e];
+            lin_width(n, p.bt, tiles, width);
+        }
+        // Eight tiles along the rows, then the columns: what the pairs work on at one time
+        // is about as many rows' operands as columns'.
+        const int g = i / (8 * im), gs = min(8, tiles - 8 * g), in = i - 8 * g * im;
+        const int c = in / gs, j = 8 * g + in - c * gs;
+        t.m = 256 * c;
+        t.n = j * width;
+        t.rows = min(width, n - t.n);
+        t.wide = (t.rows + 31) / 32 * 32;
+        if (KIND != kWeight) t.n += off[t.e];
+        t.k0 = (int)((long long)kb * t.part / p.split);
+        t.k1 = (int)((long long)kb * (t.part + 1) / p.split);
+        return true;
+    }
+};
+
+// Arrive on an mbarrier of the cluster and add to the bytes that its phase expects.
+__device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_at(void* dst, const CUtensorMap* tm, uint32_t bar_cluster, int c0, int c1, int c2)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(c2), "r"(bar_cluster)
+        : "memory");
+}
+
+template <int KIND>
+__global__ void __launch_bounds__(kLinThreads, 1)
+    linear_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                          const __grid_constant__ LinParams p)
+{
+    constexpr bool kAmn = KIND != kForward, kBmn = KIND == kWeight;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = align_shared<uint8_t>(smem_raw, 1024);
+    uint8_t* staging = smem + kLinRing;
+    int* off = reinterpret_cast<int*>(staging + kLinEpiWarps * kLinWarpStaging);   // [experts + 1]
+    int* first = off + kLinMaxExperts + 4;                                         // [experts + 1] tiles along the rows
+    uint64_t* full = reinterpret_cast<uint64_t*>(first + kLinMaxExperts + 4);      // [stages], rank 0's count
+    uint64_t* empty = full + kLinMaxStages;                                        // [stages]
+    uint64_t* tail = empty + kLinMaxStages;                                        // [stages] a block to be fixed is there
+    uint64_t* accf = tail + kLinMaxStages;                                         // [2] sums complete
+    uint64_t* acce = accf + 2;                                                     // [2] sums read (rank 0's count)
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(acce + 2);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_ctarank(), pair = blockIdx.x >> 1;
+
+    pdl_launch_dependents();
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&map_a);
+        tma_prefetch_desc(&map_b);
+        for (int i = 0; i < p.stages; ++i) {
+            mbar_init(&full[i], 2);
+            mbar_init(&empty[i], 1);
+            mbar_init(&tail[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&accf[i], 1);
+            mbar_init(&acce[i], 2 * kLinEpiWarps);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tslot, 512);
+        tc_fence_before();
+    }
+    if (p.experts) pdl_wait();  // the offsets may be the result of the kernel before
+    load_offsets(p.experts, p.offsets, p.offsets64, p.tokens, off);
+    if (KIND != kWeight) {
+        if (warp == 0) {
+            const int n = max(p.experts, 1);
+            int run = 0;
+            for (int i0 = 0; i0 < n; i0 += 32) {
+                int tiles = 0, width;
+                if (i0 + lane < n) lin_width(off[i0 + lane + 1] - off[i0 + lane], p.bt, tiles, width);
+                int s = tiles;
+#pragma unroll
+                for (int d = 1; d < 32; d *= 2) {
+                    const int o = __shfl_up_sync(0xffffffffu, s, d);
+                    if (lane >= d) s += o;
+                }
+                if (i0 + lane < n) first[i0 + lane] = run + s - tiles;
+                run += __shfl_sync(0xffffffffu, s, 31);
+            }
+            if (lane == 0) first[n] = run;
+        }
+    }
+    cluster_sync_all();  // both CTAs' barriers, offsets and tensor memory are there
+    tc_fence_after();
+    const uint32_t tbase = *tslot;
+    LinTile t;
+    LinWalk<KIND> walk(p, off, first, pair);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0u), mine = mapa_shared(smem_u32(&tail[0]), (uint32_t)rank);
+            int st = 0;
+            uint32_t ph = 0;
+            bool ok = true, more = walk.next(t);
+            if (!p.experts) pdl_wait();
+            for (; ok && more; more = walk.next(t)) {
+                const int m0 = t.m + rank * 128, n0 = t.n + rank * (t.wide >> 1);
+                for (int k = t.k0; k < t.k1; ++k) {
+                    if (!mbar_wait(&empty[st], ph ^ 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* s = smem + st * p.stage_bytes;
+                    uint32_t bar = full0 + (uint32_t)(st * 8);
+                    int kc = 64 * k;
+                    if (KIND == kWeight) {
+                        if (t.valid < 64 && kc + 64 > off[t.e + 1] - t.row0) bar = mine + (uint32_t)(st * 8);
+                        kc += t.row0;
+                    }
+                    mbar_arrive_expect_tx_cluster(bar, (uint32_t)p.stage_bytes);
+                    if (KIND == kForward) {
+                        tma_load_3d_at(s, &map_a, bar, kc, m0, t.e);
+                    } else {
+                        const int b = KIND == kData ? t.e : 0;
+                        tma_load_3d_at(s, &map_a, bar, m0, kc, b);
+                        tma_load_3d_at(s + 8192, &map_a, bar, m0 + 64, kc, b);
+                    }
+                    if (kBmn) {
+                        tma_load_3d_at(s + kLinABytes, &map_b, bar, n0, kc, 0);
+                        if (p.bt > 128) tma_load_3d_at(s + kLinABytes + 8192, &map_b, bar, n0 + 64, kc, 0);
+                    } else {
+                        tma_load_3d_at(s + kLinABytes, &map_b, bar, kc, n0, 0);
+                    }
+                    if (++st == p.stages) st = 0, ph ^= 1u;
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (rank == 0) {
+            const uint32_t sbase = smem_u32(smem);
+            const uint64_t ad = make_sdesc(sbase, kAmn ? 8192u : 16u, 1024u, 2u, 0u);
+            const uint64_t bd = make_sdesc(sbase + (uint32_t)kLinABytes, kBmn ? 8192u : 16u, 1024u, 2u, 0u);
+            constexpr uint64_t ak = kAmn ? 128 : 2, bk = kBmn ? 128 : 2;
+            int st = 0, use = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            while (ok && walk.next(t)) {
+                const uint32_t idesc = make_idesc_f16(p.bf16, kAmn, kBmn, 256, t.wide);
+                for (int c0 = t.k0; ok && c0 < t.k1; c0 += kLinChunk, ++use) {
+                    const int buf = use & 1, c1 = min(t.k1, c0 + kLinChunk);
+                    if (!mbar_wait(&acce[buf], ((uint32_t)(use >> 1) & 1u) ^ 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t d = tbase + (uint32_t)(buf * 256);
+                    for (int k = c0; k < c1; ++k) {
+                        if (!mbar_wait(&full[st], ph)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        int ks1 = 4;
+                        if (KIND == kWeight && 64 * k + 64 > off[t.e + 1] - t.row0) ks1 = (t.valid + 15) >> 4;
+                        const uint64_t so = (uint64_t)(st * (p.stage_bytes >> 4));
+                        if (elect_one()) {
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                if (ks < ks1) umma_f16_pair(d, ad + so + ak * ks, bd + so + bk * ks, idesc, (k > c0 || ks) ? 1u : 0u);
+                            umma_commit_pair(&empty[st]);
+                        }
+                        __syncwarp();
+                        if (++st == p.stages) st = 0, ph ^= 1u;
+                    }
+                    if (!ok) break;
+                    if (elect_one()) umma_commit_pair(&accf[buf]);
+                    __syncwarp();
+                }
+            }
+        }
+    } else if (warp == 2) {
+        if (KIND == kWeight) {
+            // Rows of an expert's last block that are the next one's become zeros.  (A row is
+            // one line of 128 bytes per 64 columns, whatever the swizzle does within it.)
+            const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0u);
+            int st = 0;
+            uint32_t seen = 0;
+            bool ok = true;
+            while (ok && walk.next(t)) {
+                const int rows = off[t.e + 1] - t.row0, n = t.k1 - t.k0;
+                if (n <= 0) continue;
+                const int last = (st + n - 1) % p.stages;
+                st = (st + n) % p.stages;
+                if (t.valid == 64 || 64 * t.k1 <= rows) continue;
+                ok = mbar_wait_sleep(&tail[last], (seen >> last) & 1u);
+                seen ^= 1u << last;
+                __syncwarp();
+                if (!ok) break;
+                uint8_t* s = smem + last * p.stage_bytes;
+                const int zeros = ((t.valid + 15) >> 4 << 4) - t.valid;  // rows, of 8 chunks of 16 bytes each
+                for (int c = 0; c < p.stage_bytes >> 13; ++c)
+                    for (int i = lane; i < 8 * zeros; i += 32)
+                        *reinterpret_cast<uint4*>(s + 8192 * c + 128 * t.valid + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_at(full0 + (uint32_t)(last * 8));
+                __syncwarp();
+            }
+        }
+    } else {
+        // Warp e of the epilogue: 32 columns of the result (its tensor-memory quadrant) by
+        // every fourth 16 of the tile's rows.
+        const int e = warp - 3, q = warp & 3, cg = e >> 2;
+        const uint32_t acce0 = mapa_shared(smem_u32(&acce[0]), 0u);
+        const uint32_t trow = tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)(16 * cg);
+        uint8_t* stg = staging + e * kLinWarpStaging;
+        const int sub = lane >> 2, c4 = lane & 3;
+        int use = 0;
+        bool ok = true, more = walk.next(t);
+        if (!p.experts) pdl_wait();
+        const unsigned long long offset = layer_offset(p.t);
+        for (; ok && more; more = walk.next(t)) {
+            const int groups = t.wide >> 4;
+            float acc[4][16];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int k = 0; k < 16; ++k) acc[i][k] = 0.f;
+            for (int c0 = t.k0; c0 < t.k1; c0 += kLinChunk, ++use) {
+                const int buf = use & 1;
+                if (!mbar_wait_sleep(&accf[buf], (uint32_t)(use >> 1) & 1u)) {
+                    ok = false;
+                    break;
+                }
+                __syncwarp();
+                tc_fence_after();
+                const uint32_t tacc = trow + (uint32_t)(buf * 256);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (cg + 4 * i < groups) {
+                        uint32_t r[16];
+                        tmem_ld16_issue(tacc + 64 * i, r);
+                        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                        reg_fence16(r);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) acc[i][k] += __uint_as_float(r[k]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_at(acce0 + (uint32_t)(buf * 8));
+            }
+            if (!ok) break;
+            const int j = t.m + rank * 128 + q * 32 + 8 * c4, n = min(8, p.M - j);
+            // One copy of the code that follows the sums: the next 16 rows' sums move down.
+#pragma unroll 1
+            for (int r0 = 16 * cg; r0 < t.rows; r0 += 64) {
+                TailRead<KIND> rd0, rd1;
+                const bool in0 = n > 0 && r0 + sub < t.rows, in1 = n > 0 && r0 + 8 + sub < t.rows;
+                if (p.split == 1) {
+                    if (in0) tail_read<KIND>(p.t, t.e, t.n + r0 + sub, j, n, rd0);
+                    if (in1) tail_read<KIND>(p.t, t.e, t.n + r0 + 8 + sub, j, n, rd1);
+                }
+                // A column of the result per lane becomes eight columns of a row per lane: rows
+                // of 128 bytes, chunk k of row r at k ^ r % 8.
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    *reinterpret_cast<float*>(stg + k * 128 + (((lane >> 2) ^ (k & 7)) << 4) + (lane & 3) * 4) = acc[0][k];
+                    acc[0][k] = acc[1][k], acc[1][k] = acc[2][k], acc[2][k] = acc[3][k];
+                }
+                __syncwarp();
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    if (h ? in1 : in0) {
+                        const uint8_t* s = stg + (8 * h + sub) * 128;
+                        const float4 a = *reinterpret_cast<const float4*>(s + (((2 * c4) ^ sub) << 4));
+                        const float4 b = *reinterpret_cast<const float4*>(s + (((2 * c4 + 1) ^ sub) << 4));
+                        const long long row = t.n + r0 + 8 * h + sub;
+                        if (p.split == 1) {
+                            float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                            tail_write<KIND>(p.t, offset, t.e, row, j, n, h ? rd1 : rd0, v);
+                        } else {
+                            float* o = p.part + ((long long)t.part * p.part_rows + (KIND == kWeight ? (long long)t.e * p.N : 0) + row) * p.ldp + j;
+                            *reinterpret_cast<float4*>(o) = a;
+                            *reinterpret_cast<float4*>(o + 4) = b;
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+        }
+    }
+    // Neither CTA releases tensor memory or leaves while the other may still use it.
+    tc_fence_before();
+    cluster_sync_all();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tbase, 512);
+    }
+}
+
+// ---------------------------------------------------------------- parts of sums
+// The parts of each result in order, and what follows: eight columns a thread.
+template <int KIND>
+__global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ LinParams p)
+{
+    __shared__ int off[kLinMaxExperts + 1];
+    pdl_launch_dependents();
+    pdl_wait();
+    if (KIND != kWeight) load_offsets(p.experts, p.offsets, p.offsets64, p.tokens, off);
+    const unsigned long long offset = layer_offset(p.t);
+    const int groups = (p.M + 7) / 8, experts = max(p.experts, 1);
+    const long long total = p.part_rows * groups, step = (long long)gridDim.x * blockDim.x;
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += step) {
+        const long long r = i / groups;
+        const int j = 8 * (int)(i - r * groups), n = min(8, p.M - j);
+        int e;
+        long long row = r;
+        if (KIND == kWeight) {
+            e = (int)(r / p.N);
+            row = r - (long long)e * p.N;
+        } else {
+            if (r < off[0] || r >= off[experts]) continue;
+            e = find_last(off, experts, (int)r);
+        }
+        TailRead<KIND> rd;
+        tail_read<KIND>(p.t, e, row, j, n, rd);
+        float v[8] = {};
+        const float* q = p.part + r * p.ldp + j;
+#pragma unroll 4
+        for (int s = 0; s < p.split; ++s, q += p.part_rows * p.ldp) {
+            const float4 a = __ldcg(reinterpret_cast<const float4*>(q)), b = __ldcg(reinterpret_cast<const float4*>(q) + 1);
+            v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+            v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+        }
+        tail_write<KIND>(p.t, offset, e, row, j, n, rd, v);
+    }
+}
+
+// ---------------------------------------------------------------- operands that TMA cannot read
+// Rows of 16-bit elements that start anywhere, copied to rows of whole 16-byte chunks.
+__global__ void __launch_bounds__(256) linear_pack_kernel(const unsigned short* in, unsigned short* out, long long rows, int batch,
+                                                          int cols, long long ld, long long bs, int ldp)
+{
+    pdl_launch_dependents();
+    pdl_wait();
+    const int groups = ldp / 8;
+    const long long total = rows * batch * groups, step = (long long)gridDim.x * blockDim.x;
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += step) {
+        const long long r = i / groups, b = r / rows;
+        const int j = 8 * (int)(i - r * groups);
+        const unsigned short* s = in + b * bs + (r - b * rows) * ld + j;
+        uint32_t h[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) h[k] = j + k < cols ? s[k] : 0;
+        *reinterpret_cast<uint4*>(out + r * ldp + j) =
+            make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+    }
+}
+
+// ---------------------------------------------------------------- bias gradients
+// Sums of dy's columns over an expert's rows, `chunk` rows at a time: part[chunk][N], and how
+// many chunks come before each expert's (first, written by one block).
+struct ColumnParams {
+    const void* dy;
+    long long tokens, ld;
+    int N, dtype, vec;
+    int experts, offsets64;
+    const void* offsets;
+    int cx_log, chunk;
+    float* part;
+    int* first;
+};
+__global__ void __launch_bounds__(256) column_sum_kernel(const __grid_constant__ ColumnParams p)
+{
+    __shared__ int off[kLinMaxExperts + 1], first[kLinMaxExperts + 1];
+    __shared__ float s[8][256];
+    pdl_launch_dependents();
+    pdl_wait();
+    load_offsets(p.experts, p.offsets, p.offsets64, p.tokens, off);
+    const int n = max(p.experts, 1);
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int run = 0;
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            const int c = i0 + lane < n ? (off[i0 + lane + 1] - off[i0 + lane] + p.chunk - 1) / p.chunk : 0;
+            int a = c;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const int o = __shfl_up_sync(0xffffffffu, a, d);
+                if (lane >= d) a += o;
+            }
+            if (i0 + lane < n) first[i0 + lane] = run + a - c;
+            run += __shfl_sync(0xffffffffu, a, 31);
+        }
+        if (lane == 0) first[n] = run;
+    }
+    __syncthreads();
+    if (blockIdx.x == 0 && blockIdx.y == 0)
+        for (int i = threadIdx.x; i <= n; i += 256) p.first[i] = first[i];
+    const int cx = 1 << p.cx_log, tx = threadIdx.x & (cx - 1), ty = threadIdx.x >> p.cx_log, ny = 256 >> p.cx_log;
+    const int col = 8 * (blockIdx.x * cx + tx), m = min(8, p.N - col);
+    for (int c = blockIdx.y; c < first[n]; c += gridDim.y) {
+        const int e = find_last(first, n, c);
+        const int r0 = off[e] + (c - first[e]) * p.chunk, r1 = min(off[e + 1], r0 + p.chunk);
+        float sum[8] = {};
+        if (m > 0)
+            for (int r = r0 + ty; r < r1; r += 4 * ny) {
+                Raw8 x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (r + i * ny < r1) x[i] = load_raw8(p.dy, (r + i * ny) * p.ld + col, p.dtype, p.vec, m);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (r + i * ny >= r1) continue;
+                    float v[8];
+                    unpack8(x[i], p.dtype, v);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) sum[k] += v[k];
+                }
+            }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s[k][threadIdx.x] = sum[k];
+        __syncthreads();
+        for (int i = threadIdx.x; i < 8 * cx; i += 256) {
+            const int k = i & 7, x = i >> 3, j = 8 * (blockIdx.x * cx + x) + k;
+            float a = 0.f;
+            for (int y = 0; y < ny; ++y) a += s[k][(y << p.cx_log) + x];
+            if (j < p.N) p.part[(long long)c * p.N + j] = a;
+        }
+    }
+}
+
+}  // namespace wg

@@ -10,12 +10,13 @@ namespace wg {
 
 // Device status word: bit 0 = a bounded wait ran out; bit 1 = a kernel
 // instance was launched for a plan it is not compiled for (an internal
-// error); bit 2 = a token outside the embedding table.  Read and cleared by
-// wg_check_status on the host.  One word per translation unit.
+// error); bit 2 = a token outside the embedding table; bit 3 = experts' offsets
+// that descend or lie outside the rows.  Read and cleared by wg_check_status on the host.  One word per translation unit.
 static __device__ unsigned int g_status;
 constexpr unsigned int kStatusTimeout = 1u;
 constexpr unsigned int kStatusBadPlan = 2u;
 constexpr unsigned int kStatusBadToken = 4u;
+constexpr unsigned int kStatusBadOffset = 8u;
 
 // Upper bound of any single wait, in nanoseconds of %globaltimer.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;

@@ -701,6 +701,7 @@ const char* wg_status_string(int s)
         case WG_ERR_CUDA: return "WG_ERR_CUDA";
         case WG_ERR_DEVICE_TIMEOUT: return "WG_ERR_DEVICE_TIMEOUT";
         case WG_ERR_INVALID_TOKEN: return "WG_ERR_INVALID_TOKEN";
+        case WG_ERR_INVALID_OFFSET: return "WG_ERR_INVALID_OFFSET";
         default: return "WG_ERR_UNKNOWN";
     }
 }
@@ -796,24 +797,28 @@ int wg_check_status(void* stream)
     cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail("cudaStreamSynchronize", e);
     // Each translation unit with kernels has a status word of its own.
-    unsigned int w = 0, u = 0;
-    e = cudaMemcpyFromSymbol(&w, wg::g_status, sizeof w);
-    if (e == cudaSuccess) e = wg::read_update_status(&u);
+    unsigned int w[3] = {};
+    e = cudaMemcpyFromSymbol(&w[0], wg::g_status, sizeof w[0]);
+    if (e == cudaSuccess) e = wg::read_update_status(&w[1]);
+    if (e == cudaSuccess) e = wg::read_layer_status(&w[2]);
     if (e != cudaSuccess) return cuda_fail("reading the device status", e);
-    // What is reported is cleared: a token's bit beside a timeout's is left for the next call.
-    const unsigned int v = w | u, waits = wg::kStatusBadPlan | wg::kStatusTimeout;
-    const unsigned int told = v & waits ? waits : wg::kStatusBadToken;
-    if (w & told) {
-        w &= ~told;
-        e = cudaMemcpyToSymbol(wg::g_status, &w, sizeof w);
+    // What is reported is cleared; what has also happened is left for the next call.
+    const unsigned int v = w[0] | w[1] | w[2], waits = wg::kStatusBadPlan | wg::kStatusTimeout;
+    const unsigned int told = v & waits ? waits : v & wg::kStatusBadToken ? wg::kStatusBadToken : wg::kStatusBadOffset;
+    for (int i = 0; i < 3 && e == cudaSuccess; ++i) {
+        if (!(w[i] & told)) continue;
+        w[i] &= ~told;
+        e = i == 0 ? cudaMemcpyToSymbol(wg::g_status, &w[0], sizeof w[0])
+                   : i == 1 ? wg::write_update_status(w[1]) : wg::write_layer_status(w[2]);
     }
-    if (e == cudaSuccess && (u & told)) e = wg::write_update_status(u & ~told);
     if (e != cudaSuccess) return cuda_fail("clearing the device status", e);
     if (v & waits)
         return set_err(WG_ERR_DEVICE_TIMEOUT, (v & wg::kStatusBadPlan)
                                                   ? "internal error: a kernel instance got a plan it is not built for"
                                                   : "a kernel's bounded wait ran out");
     if (v & wg::kStatusBadToken) return set_err(WG_ERR_INVALID_TOKEN, "an embedding call read a token outside [0, vocab)");
+    if (v & wg::kStatusBadOffset)
+        return set_err(WG_ERR_INVALID_OFFSET, "a layer call read experts' offsets that descend or lie outside [0, tokens]");
     return WG_OK;
 }
 

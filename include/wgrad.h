@@ -86,7 +86,9 @@ typedef enum {
     WG_ERR_CUDA = 5,             /* a CUDA runtime/driver call failed */
     WG_ERR_DEVICE_TIMEOUT = 6,   /* a kernel's bounded wait ran out, or (an internal error) a kernel
                                     found its launch inconsistent; reported by wg_check_status */
-    WG_ERR_INVALID_TOKEN = 7     /* an embedding call read a token outside [0, vocab); reported by wg_check_status */
+    WG_ERR_INVALID_TOKEN = 7,    /* an embedding call read a token outside [0, vocab); reported by wg_check_status */
+    WG_ERR_INVALID_OFFSET = 8    /* a layer call read experts' offsets that descend or lie outside [0, tokens];
+                                    reported by wg_check_status */
 } wg_status;
 
 /* Problem record (the host arguments of the CK page: G_, N_, C_, K_, spatial
@@ -193,9 +195,11 @@ WG_API int wg_conv_bwd_weight(const wg_problem* p, const void* x, const void* dy
                        void* workspace, size_t ws_bytes, void* stream);
 
 /* Synchronise `stream`, then read the device status word that the kernels set
- * when a bounded wait runs out or a token is out of range, and clear what is
- * reported (where both have happened, the token is left for the next call).
- * Returns WG_OK, WG_ERR_DEVICE_TIMEOUT, WG_ERR_INVALID_TOKEN or WG_ERR_CUDA. */
+ * when a bounded wait runs out or a token or an expert's offset is out of range,
+ * and clear what is reported (where several have happened, the timeout is told
+ * first, then the token; the others are left for the next call).
+ * Returns WG_OK, WG_ERR_DEVICE_TIMEOUT, WG_ERR_INVALID_TOKEN, WG_ERR_INVALID_OFFSET
+ * or WG_ERR_CUDA. */
 WG_API int wg_check_status(void* stream);
 
 /* Human-readable plan for (p, opt): kernel, tiles, split degree, mode, grid,
@@ -436,6 +440,145 @@ WG_API int wg_embedding_workspace_size(const wg_embedding_problem* p, size_t* by
  * Returns WG_OK or an error status; nothing is launched on an error. */
 WG_API int wg_embedding_bwd_weight(const wg_embedding_problem* p, const void* token, const void* dy, void* dtable,
                                    int accumulate, void* workspace, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Layers: the matrix product with what follows it in one call, its gradients,
+ * the same for rows grouped by expert, and what follows a product or a
+ * convolution alone (no counterparts in the CK page).  The conventions at the top
+ * of this file hold here too, but for alignment, which is stated per call. */
+
+typedef enum {
+    WG_ACT_NONE = 0,
+    WG_ACT_RELU = 1,
+    WG_ACT_GELU = 2,      /* v (1 + erf(v / sqrt 2)) / 2 */
+    WG_ACT_GELU_TANH = 3, /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
+    WG_ACT_SILU = 4       /* v / (1 + exp(-v)) */
+} wg_activation_kind;
+
+/* Dropout D(a): an element is kept with probability 1 - p and then multiplied by
+ * 1 / (1 - p); else it is 0, whatever a was.  p is rounded to a multiple of 2^-16
+ * (thr = round(65536 p), at most 65535; the factor is 65536 / (65536 - thr)).  The
+ * mask is never stored: element (row, column) is kept where its 16 bits are at
+ * least thr, those being half column % 8 (low half first) of the four words of
+ * Philox 4x32 with ten rounds (Salmon et al., 2011), key (seed low, seed high),
+ * counter (column / 8, row, o low, o high), o = offset + *counter.  So the gradient
+ * calls make a forward call's mask again from the same seed, offset and number in
+ * counter, and two calls of one program need different offsets (or seeds) to draw
+ * masks of their own.  counter (a DEVICE pointer to a 64-bit number, 8-byte aligned,
+ * or NULL: 0) is read when the kernels run: with it a captured call draws a new
+ * mask at each replay. */
+
+/* A layer of `out` features on `in`, for `tokens` rows.
+ *
+ *   forward:          v[t, n]     = sum over k of x[t, k] w[e, n, k] + bias[e, n]
+ *                     z[t, n]     = v[t, n]                                (when z is given)
+ *                     y[t, n]     = residual[t, n] + D(act(v[t, n]))
+ *   input gradient:   dx[t, k]    = residual[t, k] + D(act'(z[t, k]) sum over n of dy[t, n] w[e, n, k])
+ *   weight gradient:  dw[e, n, k] = sum over the rows t of e of dy[t, n] x[t, k]
+ *                     dbias[e, n] = sum over the rows t of e of dy[t, n]
+ *
+ * bias, residual (none: 0) and dbias are optional.  In the input gradient,
+ * activation and dropout are those that made this layer's x from the layer below
+ * (x = D(act(z))), so dx is the gradient of z; without an activation z is not read.
+ * dy is the gradient of v: of a layer whose y is D(act(v)), what wg_activation_bwd or
+ * the layer above's input gradient gives.
+ *
+ *  experts = 0: one weight; offsets is NULL.  experts >= 1: rows offsets[e] ..
+ *    offsets[e + 1] - 1 are expert e's, offsets being experts + 1 ascending integers of
+ *    offset_bits in device memory, read when the kernels run.  Rows before offsets[0] and
+ *    from offsets[experts] on are neither read nor written (y, z, dx there stay as they
+ *    are).  An expert without rows has a zero weight gradient.  Offsets that descend or
+ *    lie outside [0, tokens] are brought into order (the largest so far) and into range,
+ *    and wg_check_status then returns WG_ERR_INVALID_OFFSET.
+ *
+ * Products and sums are fp32 (512 terms at a time on the tensor cores, those added
+ * rounded to nearest), as is all that follows, rounded once to nearest even; z is rounded
+ * by itself, y is made from the unrounded v.  Results are bitwise reproducible.  Zeros
+ * are added for no one: rows and experts do not touch one another's results, infinities
+ * and NaN included.
+ *
+ *  tokens 0..2^31-65536, in and out 1..2^20, experts 0..1024; at most 2^31 - 1 tiles of
+ *    256 features by 32 rows.
+ *  ld_in, ld_out, ld_z, ld_residual: elements between rows of x and dx, of y and dy,
+ *    of z, of residual; 0 = packed (in, out, the columns of y or dx).  ld_weight,
+ *    weight_stride: elements between rows and between experts' matrices of w and dw
+ *    (0 = in, out * ld_weight).  bias and dbias are packed.
+ *  in_dtype: x, w, dy and z, WG_BF16 or WG_FP16.  out_dtype: y and residual, dx, dw
+ *    (WG_FP32, WG_BF16, WG_FP16).  bias_dtype: bias and dbias.
+ *  dropout: p in [0, 1). */
+typedef struct {
+    long long tokens;
+    int in, out, experts;
+    long long ld_in, ld_out, ld_weight, weight_stride, ld_z, ld_residual;
+    wg_dtype in_dtype, out_dtype, bias_dtype;
+    int offset_bits; /* 32 or 64 */
+    wg_activation_kind activation;
+    float dropout;
+    unsigned long long seed, offset;
+    const unsigned long long* counter;
+} wg_linear_problem;
+
+typedef enum { WG_LINEAR_FORWARD = 0, WG_LINEAR_BWD_DATA = 1, WG_LINEAR_BWD_WEIGHT = 2 } wg_linear_call;
+
+/* Bytes of device workspace a call needs for p: fp32 sums of parts where the sum is cut
+ * among the SMs, copies of operands whose rows are not all 16-byte aligned, partial
+ * sums of dbias.  Host only. */
+WG_API int wg_linear_workspace_size(const wg_linear_problem* p, wg_linear_call call, size_t* bytes);
+
+/* Human-readable plan of a call for p.  Host only. */
+WG_API int wg_linear_plan_string(const wg_linear_problem* p, wg_linear_call call, char* buf, size_t n);
+
+/* The three calls on `stream`.  x, w and dy need 16-byte aligned bases where their
+ * ld (and, with several experts, weight_stride) is a multiple of 8 elements, else
+ * only their elements' alignment; every other tensor only its elements' (16-byte
+ * aligned rows are faster); workspace 16 bytes.  residual may be y (or dx) itself, with
+ * the same strides; else no output may overlap another tensor of the call.
+ * accumulate: dw and dbias are added to what is there (in fp32, then rounded).
+ * With tokens = 0 nothing is written but the weight gradient's zeros.
+ * Returns WG_OK or an error status; nothing is launched on an error. */
+WG_API int wg_linear(const wg_linear_problem* p, const void* offsets, const void* x, const void* w, const void* bias,
+                     const void* residual, void* y, void* z, void* workspace, size_t ws_bytes, void* stream);
+WG_API int wg_linear_bwd_data(const wg_linear_problem* p, const void* offsets, const void* dy, const void* w,
+                              const void* z, const void* residual, void* dx, void* workspace, size_t ws_bytes,
+                              void* stream);
+WG_API int wg_linear_bwd_weight(const wg_linear_problem* p, const void* offsets, const void* x, const void* dy, void* dw,
+                                void* dbias, int accumulate, void* workspace, size_t ws_bytes, void* stream);
+
+/* What follows a product or a convolution, alone, on `tokens` rows of `dim` columns:
+ *
+ *   forward:   y[t, n]  = residual[t, n] + D(act(x[t, n] + bias[n]))
+ *   gradient:  dx[t, n] = D(act'(x[t, n] + bias[n]) dy[t, n])
+ *              dbias[n] = sum over t of dx[t, n]  (before its rounding)
+ *
+ * bias, residual, dbias, and one of dx and dbias, are optional; the gradient needs no x
+ * without an activation.  fp32 arithmetic, rounded once to nearest even; bitwise reproducible.
+ *
+ *  tokens 0..2^31-65536, dim 1..2^20.
+ *  ld_x, ld_y, ld_residual, ld_dx: elements between rows of x, of y and dy, of
+ *    residual, of dx; 0 = dim.
+ *  in_dtype: x and dx; out_dtype: y, dy and residual; bias_dtype: bias and dbias. */
+typedef struct {
+    long long tokens;
+    int dim;
+    long long ld_x, ld_y, ld_residual, ld_dx;
+    wg_dtype in_dtype, out_dtype, bias_dtype;
+    wg_activation_kind activation;
+    float dropout;
+    unsigned long long seed, offset;
+    const unsigned long long* counter;
+} wg_activation_problem;
+
+/* Bytes of device workspace wg_activation_bwd needs for p (dbias's partial sums).  Host only. */
+WG_API int wg_activation_workspace_size(const wg_activation_problem* p, size_t* bytes);
+
+/* The two calls on `stream`.  Tensors need only their elements' alignment; workspace (needed
+ * with dbias only) 16 bytes.  y may be x or residual, and dx may be x or dy, where
+ * their types and strides are the same; else no output may overlap another tensor.
+ * Returns WG_OK or an error status; nothing is launched on an error. */
+WG_API int wg_activation(const wg_activation_problem* p, const void* x, const void* bias, const void* residual, void* y,
+                         void* stream);
+WG_API int wg_activation_bwd(const wg_activation_problem* p, const void* dy, const void* x, const void* bias, void* dx,
+                             void* dbias, void* workspace, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }
