@@ -278,6 +278,149 @@ __device__ __forceinline__ void tail_write(const LayerTail& t, unsigned long lon
     store8(t.y, (KIND == kWeight ? expert * t.y_stride : 0) + row * t.ldy + col, t.y_dtype, t.vec & kVecY, n, v);
 }
 
+// ---------------------------------------------------------------- a column per lane
+// What sixteen rows of 32 neighbouring columns, a column per lane, become.
+__device__ __forceinline__ float bias_at(const LayerTail& t, int expert, int col)
+{
+    const char* q = at(t.bias, expert * t.bias_stride + col, t.bias_dtype);
+    if (t.bias_dtype == 2) return *reinterpret_cast<const float*>(q);
+    if (t.bias_dtype == 0) return __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(q));
+    return __half2float(*reinterpret_cast<const __half*>(q));
+}
+
+// The first n of sixteen elements, ld apart, as they lie in memory.
+template <typename T>
+__device__ __forceinline__ void load_rows(const void* p, long long e, long long ld, int n, uint32_t (&w)[16])
+{
+    const T* q = static_cast<const T*>(p) + e;
+#pragma unroll
+    for (int k = 0; k < 16; ++k, q += ld) w[k] = k < n ? *q : 0;
+}
+__device__ __forceinline__ float as_float(uint32_t w, int dtype)
+{
+    if (dtype == 0) return __uint_as_float(w << 16);
+    if (dtype == 1) return __half2float(__ushort_as_half((unsigned short)w));
+    return __uint_as_float(w);
+}
+template <typename T>
+__device__ __forceinline__ void store_rows(void* p, long long e, long long ld, int n, const uint32_t (&v)[16])
+{
+    T* q = static_cast<T*>(p) + e;
+#pragma unroll
+    for (int k = 0; k < 16; ++k, q += ld)
+        if (k < n) *q = from_f32<T>(__uint_as_float(v[k]));
+}
+__device__ __forceinline__ void store_rows(void* p, long long e, long long ld, int dtype, int n, const uint32_t (&v)[16])
+{
+    if (dtype == 0)
+        store_rows<__nv_bfloat16>(p, e, ld, n, v);
+    else if (dtype == 1)
+        store_rows<__half>(p, e, ld, n, v);
+    else
+        store_rows<float>(p, e, ld, n, v);
+}
+
+// Dropout of rows row .. row + 7 of the warp's 32 columns (the first a multiple of 8): bit k is
+// row k's.  Lane l draws for row l % 8 of the columns of lanes l / 8 * 8 .. + 7; its eight
+// answers reach the lanes of those columns by a ballot each.
+__device__ __forceinline__ uint32_t keep_columns(const LayerTail& t, unsigned long long offset, long long row, int col)
+{
+    const int lane = threadIdx.x & 31;
+    const uint4 r = philox(make_uint4((uint32_t)(col >> 3), (uint32_t)(row + (lane & 7)), (uint32_t)offset, (uint32_t)(offset >> 32)),
+                           make_uint2((uint32_t)t.seed, (uint32_t)(t.seed >> 32)));
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    uint32_t mine = 0;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        const uint32_t h = c & 1 ? w[c >> 1] >> 16 : w[c >> 1] & 0xffffu;
+        const uint32_t b = __ballot_sync(0xffffffffu, h >= t.thr);
+        if ((lane & 7) == c) mine = b;
+    }
+    return mine >> (lane & 24);
+}
+
+// What column_tail will read of `rows` rows from `row` on, 16 of every `step`, is brought to L2.
+template <int KIND>
+__device__ __forceinline__ void tail_prefetch(const LayerTail& t, int expert, long long row, int rows, int step, int col)
+{
+    const bool z = KIND == kData && t.z;
+    if (!t.res && !z) return;
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += step) {
+        const int lane = threadIdx.x & 31, r = lane & 15;  // a row per lane; the warp's columns are a line or two
+        if (r0 + r >= rows) continue;
+        const long long c = col - lane;
+        if (t.res && lane < 16)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(at(t.res, (KIND == kWeight ? expert * t.y_stride : 0) + (row + r0 + r) * t.ldr + c, t.y_dtype)));
+        if (z && lane >= 16) asm volatile("prefetch.global.L2 [%0];" ::"l"(at(t.z, (row + r0 + r) * t.ldz + c, t.z_dtype)));
+    }
+}
+
+// The sums v of rows row .. row + 15, of which the first n are there (none: the column is not).
+// The whole warp, converged.
+template <int KIND>
+__device__ __forceinline__ void column_tail(const LayerTail& t, unsigned long long offset, int expert, long long row, int n, int col,
+                                            uint32_t (&v)[16])
+{
+    const long long base = KIND == kWeight ? expert * t.y_stride : 0;
+    uint32_t x[16];
+    if (KIND == kForward) {
+        if (t.bias && n > 0) {
+            const float b = bias_at(t, expert, col);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) + b);
+        }
+        if (t.z) {
+            if (t.z_dtype == 0)
+                store_rows<__nv_bfloat16>(t.z, row * t.ldz + col, t.ldz, n, v);
+            else
+                store_rows<__half>(t.z, row * t.ldz + col, t.ldz, n, v);
+        }
+        if (t.act != kActNone) {
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {  // one copy of the activations: eight rows, then the other eight
+                float f[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(v[k]);
+                act8(t.act, f);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = v[8 + k], v[8 + k] = __float_as_uint(f[k]);
+            }
+        }
+    }
+    if (KIND == kData && t.z) {
+        load_rows<unsigned short>(t.z, row * t.ldz + col, t.ldz, n, x);
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+            float f[8], z[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(v[k]), z[k] = as_float(x[k], t.z_dtype);
+            slope8(t.act, z, f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = v[8 + k], v[8 + k] = __float_as_uint(f[k]), x[k] = x[8 + k];
+        }
+    }
+    if (t.res) {  // (on its way while the mask is made)
+        if (t.y_dtype == 2)
+            load_rows<uint32_t>(t.res, base + row * t.ldr + col, t.ldr, n, x);
+        else
+            load_rows<unsigned short>(t.res, base + row * t.ldr + col, t.ldr, n, x);
+    }
+    if (KIND != kWeight && t.thr) {
+#pragma unroll
+        for (int h = 0; h < 16; h += 8) {
+            const uint32_t keep = keep_columns(t, offset, row + h, col);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[h + k] = keep >> k & 1 ? __float_as_uint(__uint_as_float(v[h + k]) * t.gain) : 0u;
+        }
+    }
+    if (t.res) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) + as_float(x[k], t.y_dtype));
+    }
+    store_rows(t.y, base + row * t.ldy + col, t.ldy, t.y_dtype, n, v);
+}
+
 // ---------------------------------------------------------------- activation alone
 // y = residual + D(act(x + bias)), or dx = D(act'(x + bias) dy) and dbias's partial sums.
 // A thread has eight columns and walks down rows, kActRows in flight; 2^cx_log threads side by side.

@@ -19,7 +19,7 @@
 // epilogue runs beside the next tile's MMAs.
 //
 // MMAs add to their sums with truncation (a sum of equal signs over 16 n elements comes
-// out short by some 1e-7 n of itself), so a sum is taken kLinChunk blocks at a time and
+// out short by some 1e-7 n of itself), so a sum is taken `chunk` blocks at a time and
 // the chunks are added in registers, rounded to nearest.
 //
 // A sum over an expert's rows ends inside a block: its last block's rows that belong to
@@ -35,18 +35,18 @@
 
 namespace wg {
 
-constexpr int kLinEpiWarps = 16;
-constexpr int kLinThreads = 32 * (3 + kLinEpiWarps);  // TMA, MMA, fixing, then the epilogue
-constexpr int kLinWarpStaging = 2048;                 // 16 result rows by 32 columns of fp32
+// Warps: TMA, MMA, fixing, then the epilogue: sixteen warps, or eight where sums of several
+// chunks are added up, which takes 128 registers of each (sixteen would have 96 in all, and
+// what does not fit goes to L2: no L1 is left beside the ring).
+constexpr int lin_epi_warps(bool chunked) { return chunked ? 8 : 16; }
+constexpr int lin_threads(bool chunked) { return 32 * (3 + lin_epi_warps(chunked)); }
 constexpr int kLinMaxStages = 12;
 constexpr int kLinMaxExperts = 1024;
-constexpr int kLinChunk = 8;                          // blocks of 64 per sum in tensor memory
 constexpr int kLinABytes = 16384;
 // All the shared memory that a CTA may have (see muon_product_kernel: tensor memory is
 // taken before the kernel before this one has ended).
 constexpr int kLinSmem = 227 * 1024;
-constexpr int kLinFixed = kLinEpiWarps * kLinWarpStaging + 2 * 4 * (kLinMaxExperts + 4) + 512 + 1024;
-constexpr int kLinRing = kLinSmem - kLinFixed;
+constexpr int kLinRing = (kLinSmem - 2 * 4 * (kLinMaxExperts + 4) - 512 - 1024) / 1024 * 1024;
 
 struct LinParams {
     LayerTail t;
@@ -59,6 +59,7 @@ struct LinParams {
     int bf16;
     int bt;                 // most MMA columns of a tile
     int stages, stage_bytes;
+    int chunk;              // blocks per sum in tensor memory
     int split, pairs;
     float* part;            // [split][rows][ldp] sums of parts (split > 1)
     long long ldp, part_rows;
@@ -189,10 +190,12 @@ struct LinWalk {
     }
 };
 
-// Arrive on an mbarrier of the cluster and add to the bytes that its phase expects.
+// Arrive on an mbarrier of the cluster and add to the bytes that its phase expects.  The thread
+// has written nothing that another one reads, so the arrival orders nothing (as a release it
+// waited for the thread's own traffic, and a block took 0.9 us instead of 0.33).
 __device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t bar, uint32_t bytes)
 {
-    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_at(uint32_t bar)
 {
@@ -207,16 +210,30 @@ __device__ __forceinline__ void tma_load_3d_at(void* dst, const CUtensorMap* tm,
         : "memory");
 }
 
-template <int KIND>
-__global__ void __launch_bounds__(kLinThreads, 1)
+// 16 consecutive 32-bit columns of this warp's 32 tensor-memory lanes.  Whole warp, converged.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16])
+{
+    uint32_t r[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i]);
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 "
+        "[%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+template <int KIND, bool CHUNKED>
+__global__ void __launch_bounds__(lin_threads(CHUNKED), 1)
     linear_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                           const __grid_constant__ LinParams p)
 {
     constexpr bool kAmn = KIND != kForward, kBmn = KIND == kWeight;
+    constexpr int kEpiWarps = lin_epi_warps(CHUNKED);
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align_shared<uint8_t>(smem_raw, 1024);
-    uint8_t* staging = smem + kLinRing;
-    int* off = reinterpret_cast<int*>(staging + kLinEpiWarps * kLinWarpStaging);   // [experts + 1]
+    int* off = reinterpret_cast<int*>(smem + kLinRing);                            // [experts + 1]
     int* first = off + kLinMaxExperts + 4;                                         // [experts + 1] tiles along the rows
     uint64_t* full = reinterpret_cast<uint64_t*>(first + kLinMaxExperts + 4);      // [stages], rank 0's count
     uint64_t* empty = full + kLinMaxStages;                                        // [stages]
@@ -238,7 +255,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&accf[i], 1);
-            mbar_init(&acce[i], 2 * kLinEpiWarps);
+            mbar_init(&acce[i], 2 * kEpiWarps);
         }
         fence_mbar_init();
     }
@@ -324,8 +341,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             bool ok = true;
             while (ok && walk.next(t)) {
                 const uint32_t idesc = make_idesc_f16(p.bf16, kAmn, kBmn, 256, t.wide);
-                for (int c0 = t.k0; ok && c0 < t.k1; c0 += kLinChunk, ++use) {
-                    const int buf = use & 1, c1 = min(t.k1, c0 + kLinChunk);
+                for (int c0 = t.k0; ok && c0 < t.k1; c0 += p.chunk, ++use) {
+                    const int buf = use & 1, c1 = min(t.k1, c0 + p.chunk);
                     if (!mbar_wait(&acce[buf], ((uint32_t)(use >> 1) & 1u) ^ 1u)) {
                         ok = false;
                         break;
@@ -386,85 +403,99 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             }
         }
     } else {
-        // Warp e of the epilogue: 32 columns of the result (its tensor-memory quadrant) by
-        // every fourth 16 of the tile's rows.
-        const int e = warp - 3, q = warp & 3, cg = e >> 2;
+        // Warp e of the epilogue: 32 columns of the result (its tensor-memory quadrant), one
+        // per lane, by every kStep / 16th 16 of the tile's rows.  Results go to memory as they
+        // come from tensor memory, a row of 32 columns per instruction, whatever their
+        // alignment: shared memory has no bandwidth to spare beside the operands (staged
+        // through it, a tile's epilogue took 15 us).
+        constexpr int kStep = 4 * kEpiWarps, kOwn = 256 / kStep;
+        const int e = warp - 3, q = warp & 3, first_row = 16 * (e >> 2);
         const uint32_t acce0 = mapa_shared(smem_u32(&acce[0]), 0u);
-        const uint32_t trow = tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)(16 * cg);
-        uint8_t* stg = staging + e * kLinWarpStaging;
-        const int sub = lane >> 2, c4 = lane & 3;
+        const uint32_t trow = tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)first_row;
         int use = 0;
         bool ok = true, more = walk.next(t);
         if (!p.experts) pdl_wait();
         const unsigned long long offset = layer_offset(p.t);
         for (; ok && more; more = walk.next(t)) {
-            const int groups = t.wide >> 4;
-            float acc[4][16];
+            const int j = t.m + rank * 128 + q * 32 + lane;
+            const int rows = j < p.M ? t.rows : 0;  // of this column
+            if (p.split == 1) tail_prefetch<KIND>(p.t, t.e, t.n + first_row, rows - first_row, kStep, j);
+            if (CHUNKED && t.k1 - t.k0 > p.chunk) {
+                // Sums of several chunks are added up in registers, and the total goes back to
+                // where the last one was: no register of it is held while what follows is computed.
+                float acc[kOwn][16];
+                for (int k = t.k0;;) {
+                    if (!mbar_wait_sleep(&accf[use & 1], (uint32_t)(use >> 1) & 1u)) ok = false;
+                    __syncwarp();
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t tacc = trow + (uint32_t)((use & 1) * 256);
+                    if (k == t.k0) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int k = 0; k < 16; ++k) acc[i][k] = 0.f;
-            for (int c0 = t.k0; c0 < t.k1; c0 += kLinChunk, ++use) {
-                const int buf = use & 1;
-                if (!mbar_wait_sleep(&accf[buf], (uint32_t)(use >> 1) & 1u)) {
-                    ok = false;
-                    break;
-                }
-                __syncwarp();
-                tc_fence_after();
-                const uint32_t tacc = trow + (uint32_t)(buf * 256);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (cg + 4 * i < groups) {
-                        uint32_t r[16];
-                        tmem_ld16_issue(tacc + 64 * i, r);
+                        for (int i = 0; i < kOwn; ++i)
+                            if (first_row + kStep * i < t.wide) tmem_ld16_issue(tacc + kStep * i, reinterpret_cast<uint32_t*>(acc[i]));
                         asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-                        reg_fence16(r);
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) acc[i][k] += __uint_as_float(r[k]);
-                    }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_at(acce0 + (uint32_t)(buf * 8));
-            }
-            if (!ok) break;
-            const int j = t.m + rank * 128 + q * 32 + 8 * c4, n = min(8, p.M - j);
-            // One copy of the code that follows the sums: the next 16 rows' sums move down.
-#pragma unroll 1
-            for (int r0 = 16 * cg; r0 < t.rows; r0 += 64) {
-                TailRead<KIND> rd0, rd1;
-                const bool in0 = n > 0 && r0 + sub < t.rows, in1 = n > 0 && r0 + 8 + sub < t.rows;
-                if (p.split == 1) {
-                    if (in0) tail_read<KIND>(p.t, t.e, t.n + r0 + sub, j, n, rd0);
-                    if (in1) tail_read<KIND>(p.t, t.e, t.n + r0 + 8 + sub, j, n, rd1);
-                }
-                // A column of the result per lane becomes eight columns of a row per lane: rows
-                // of 128 bytes, chunk k of row r at k ^ r % 8.
+                        for (int i = 0; i < kOwn; ++i) reg_fence16(reinterpret_cast<uint32_t*>(acc[i]));
+                    } else {
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    *reinterpret_cast<float*>(stg + k * 128 + (((lane >> 2) ^ (k & 7)) << 4) + (lane & 3) * 4) = acc[0][k];
-                    acc[0][k] = acc[1][k], acc[1][k] = acc[2][k], acc[2][k] = acc[3][k];
-                }
-                __syncwarp();
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    if (h ? in1 : in0) {
-                        const uint8_t* s = stg + (8 * h + sub) * 128;
-                        const float4 a = *reinterpret_cast<const float4*>(s + (((2 * c4) ^ sub) << 4));
-                        const float4 b = *reinterpret_cast<const float4*>(s + (((2 * c4 + 1) ^ sub) << 4));
-                        const long long row = t.n + r0 + 8 * h + sub;
-                        if (p.split == 1) {
-                            float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-                            tail_write<KIND>(p.t, offset, t.e, row, j, n, h ? rd1 : rd0, v);
-                        } else {
-                            float* o = p.part + ((long long)t.part * p.part_rows + (KIND == kWeight ? (long long)t.e * p.N : 0) + row) * p.ldp + j;
-                            *reinterpret_cast<float4*>(o) = a;
-                            *reinterpret_cast<float4*>(o + 4) = b;
+                        for (int i = 0; i < kOwn; ++i) {
+                            if (first_row + kStep * i < t.wide) {
+                                uint32_t r[16];
+                                tmem_ld16_issue(tacc + kStep * i, r);
+                                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                                reg_fence16(r);
+#pragma unroll
+                                for (int n = 0; n < 16; ++n) acc[i][n] += __uint_as_float(r[n]);
+                            }
                         }
                     }
+                    k += p.chunk;
+                    if (k >= t.k1) {
+#pragma unroll
+                        for (int i = 0; i < kOwn; ++i)
+                            if (first_row + kStep * i < t.wide) tmem_st16(tacc + kStep * i, acc[i]);
+                        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                        break;
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_at(acce0 + (uint32_t)((use & 1) * 8));
+                    ++use;
                 }
+            } else if (t.k0 < t.k1) {
+                if (!mbar_wait_sleep(&accf[use & 1], (uint32_t)(use >> 1) & 1u)) ok = false;
                 __syncwarp();
+                tc_fence_after();
+            }
+            if (!ok) break;
+            uint32_t tacc = trow + (uint32_t)((use & 1) * 256);
+#pragma unroll 1
+            for (int r0 = first_row; r0 < t.rows; r0 += kStep, tacc += kStep) {
+                uint32_t r[16];
+                if (t.k0 < t.k1) {
+                    tmem_ld16_issue(tacc, r);
+                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                    reg_fence16(r);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) r[k] = 0u;
+                }
+                const long long row = t.n + r0;
+                if (p.split == 1) {
+                    column_tail<KIND>(p.t, offset, t.e, row, rows - r0, j, r);
+                } else {
+                    float* o = p.part + ((long long)t.part * p.part_rows + (KIND == kWeight ? (long long)t.e * p.N : 0) + row) * p.ldp + j;
+#pragma unroll
+                    for (int k = 0; k < 16; ++k, o += p.ldp)
+                        if (k < rows - r0) *o = __uint_as_float(r[k]);
+                }
+            }
+            if (t.k0 < t.k1) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_at(acce0 + (uint32_t)((use & 1) * 8));
+                ++use;
             }
         }
     }

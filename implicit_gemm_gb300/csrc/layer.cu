@@ -141,6 +141,11 @@ struct LinPlan {
     size_t off_a, off_b, off_part, off_sum, off_first, bytes;
 };
 
+// Blocks of 64 per sum in tensor memory.  Truncation takes up to 0.95e-7 n of a sum of n
+// MMAs (16 terms each) of equal signs, a few times less of mixed ones: 6e-6 of an fp32
+// result's (n = 64), 1e-4 of a 16-bit one's (n = 1024), a fifth of fp16's rounding.
+constexpr int kChunkFp32 = 16, kChunk16 = 256;
+
 // us of a block of 64 of a tile's sum on every pair at once, by the tile's MMA columns
 // (measured on the update's products: 0.33 for 256, 0.27 for 128, L2 to shared memory being
 // what bounds the narrower ones).
@@ -268,13 +273,13 @@ int lin_pack(LinOperand* o, char* to, cudaStream_t s)
     return st;
 }
 
-template <int KIND>
+template <int KIND, bool CHUNKED>
 int lin_launch(const LinPlan& pl, const wg::LinParams& g, const LinOperand& a, const LinOperand& b, cudaStream_t s)
 {
     CUtensorMap ma, mb;
     int st = lin_map(&ma, a.p, g.bf16, a.cols, a.rows, a.batch, a.ld, a.bs, KIND == wg::kForward ? 128 : 64);
     if (!st) st = lin_map(&mb, b.p, g.bf16, b.cols, b.rows, 1, b.ld, 0, KIND == wg::kWeight ? 64 : pl.bt / 2);
-    if (!st) st = wg::ensure_smem(wg::linear_product_kernel<KIND>, wg::kLinSmem);
+    if (!st) st = wg::ensure_smem(wg::linear_product_kernel<KIND, CHUNKED>, wg::kLinSmem);
     if (st) return st;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
@@ -285,9 +290,9 @@ int lin_launch(const LinPlan& pl, const wg::LinParams& g, const LinOperand& a, c
     ++na;
     wg::pdl_config(&cfg, attr, &na, s);
     cfg.gridDim = dim3((unsigned)(2 * g.pairs));
-    cfg.blockDim = dim3(wg::kLinThreads);
+    cfg.blockDim = dim3(wg::lin_threads(CHUNKED));
     cfg.dynamicSmemBytes = wg::kLinSmem;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, wg::linear_product_kernel<KIND>, ma, mb, g);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, wg::linear_product_kernel<KIND, CHUNKED>, ma, mb, g);
     if (e != cudaSuccess) return cuda_fail("linear_product_kernel launch", e);
     if (pl.split == 1) return WG_OK;
     const long long items = g.part_rows * (g.ldp / 8);
@@ -313,12 +318,16 @@ int lin_run(const LinPlan& pl, const void* offsets, LinOperand a, LinOperand b, 
     g.t = tail;
     g.experts = q.experts, g.offsets = offsets, g.offsets64 = q.offset_bits == 64, g.tokens = q.tokens;
     g.M = pl.M, g.N = pl.N, g.kb = pl.kb, g.bf16 = q.in_dtype == WG_BF16;
+    g.chunk = q.out_dtype == WG_FP32 ? kChunkFp32 : kChunk16;
     g.bt = pl.bt, g.stages = pl.stages, g.stage_bytes = pl.stage_bytes, g.split = pl.split, g.pairs = pl.pairs;
     g.part = reinterpret_cast<float*>(ws + pl.off_part), g.ldp = pl.ldp, g.part_rows = pl.part_rows;
+    // Blocks of the longest sum (a part's, or an expert's that has every row).
+    const long long blocks = pl.call == WG_LINEAR_BWD_WEIGHT ? (q.tokens + 63) / 64 : pl.kb;
+    const bool chunked = (blocks + pl.split - 1) / pl.split > g.chunk;
     switch (pl.call) {
-        case WG_LINEAR_FORWARD: return lin_launch<wg::kForward>(pl, g, a, b, s);
-        case WG_LINEAR_BWD_DATA: return lin_launch<wg::kData>(pl, g, a, b, s);
-        default: return lin_launch<wg::kWeight>(pl, g, a, b, s);
+        case WG_LINEAR_FORWARD: return chunked ? lin_launch<wg::kForward, true>(pl, g, a, b, s) : lin_launch<wg::kForward, false>(pl, g, a, b, s);
+        case WG_LINEAR_BWD_DATA: return chunked ? lin_launch<wg::kData, true>(pl, g, a, b, s) : lin_launch<wg::kData, false>(pl, g, a, b, s);
+        default: return chunked ? lin_launch<wg::kWeight, true>(pl, g, a, b, s) : lin_launch<wg::kWeight, false>(pl, g, a, b, s);
     }
 }
 
