@@ -20,7 +20,8 @@ namespace wg {
 
 enum LayerAct { kActNone, kActRelu, kActGelu, kActGeluTanh, kActSilu };
 enum LayerKind { kForward, kData, kWeight };
-enum { kVecBias = 1, kVecRes = 2, kVecY = 4, kVecZ = 8 };  // 16-byte accesses
+// 16-byte accesses of eight columns; 4-byte accesses of two.
+enum { kVecBias = 1, kVecRes = 2, kVecY = 4, kVecZ = 8, kPairRes = 16, kPairY = 32, kPairZ = 64 };
 
 struct LayerTail {
     const void* bias;
@@ -290,34 +291,78 @@ __device__ __forceinline__ float bias_at(const LayerTail& t, int expert, int col
 
 // The first n of sixteen elements, ld apart, as they lie in memory.
 template <typename T>
-__device__ __forceinline__ void load_rows(const void* p, long long e, long long ld, int n, uint32_t (&w)[16])
+__device__ __forceinline__ void load_each(const void* p, long long e, long long ld, int n, uint32_t (&w)[16])
 {
     const T* q = static_cast<const T*>(p) + e;
 #pragma unroll
     for (int k = 0; k < 16; ++k, q += ld) w[k] = k < n ? *q : 0;
 }
-__device__ __forceinline__ float as_float(uint32_t w, int dtype)
-{
-    if (dtype == 0) return __uint_as_float(w << 16);
-    if (dtype == 1) return __half2float(__ushort_as_half((unsigned short)w));
-    return __uint_as_float(w);
-}
 template <typename T>
-__device__ __forceinline__ void store_rows(void* p, long long e, long long ld, int n, const uint32_t (&v)[16])
+__device__ __forceinline__ void store_each(void* p, long long e, long long ld, int n, const uint32_t (&v)[16])
 {
     T* q = static_cast<T*>(p) + e;
 #pragma unroll
     for (int k = 0; k < 16; ++k, q += ld)
         if (k < n) *q = from_f32<T>(__uint_as_float(v[k]));
 }
-__device__ __forceinline__ void store_rows(void* p, long long e, long long ld, int dtype, int n, const uint32_t (&v)[16])
+// The same of 16-bit elements whose columns lie on 4 bytes by twos: a lane of a pair has two
+// columns of the even rows in memory, the other those of the odd rows.  Half the accesses,
+// and half the instructions (the addresses are most of them).
+__device__ __forceinline__ void load_pairs(const void* p, long long e, long long ld, int n, uint32_t (&w)[16])
 {
-    if (dtype == 0)
-        store_rows<__nv_bfloat16>(p, e, ld, n, v);
-    else if (dtype == 1)
-        store_rows<__half>(p, e, ld, n, v);
+    const int odd = threadIdx.x & 1;
+    const unsigned short* q = static_cast<const unsigned short*>(p) + e + (odd ? ld - 1 : 0);
+    const uint32_t sel = odd ? 0x3276u : 0x5410u;
+    uint32_t x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k, q += 2 * ld) x[k] = 2 * k + odd < n ? *reinterpret_cast<const uint32_t*>(q) : 0u;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        // Even lanes: own low half (row 2 k), the other's low half (row 2 k + 1); odd lanes the high ones.
+        const uint32_t o = __shfl_xor_sync(0xffffffffu, x[k], 1), b = __byte_perm(x[k], o, sel);
+        w[2 * k] = b & 0xffffu, w[2 * k + 1] = b >> 16;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store_pairs(void* p, long long e, long long ld, int n, const uint32_t (&v)[16])
+{
+    const int odd = threadIdx.x & 1;
+    unsigned short* q = static_cast<unsigned short*>(p) + e + (odd ? ld - 1 : 0);
+    const uint32_t sel = odd ? 0x3276u : 0x5410u;
+#pragma unroll
+    for (int k = 0; k < 8; ++k, q += 2 * ld) {
+        const uint32_t w = pack2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]), is_half<T> ? 1 : 0);
+        const uint32_t o = __shfl_xor_sync(0xffffffffu, w, 1);
+        if (2 * k + odd < n) *reinterpret_cast<uint32_t*>(q) = __byte_perm(w, o, sel);
+    }
+}
+__device__ __forceinline__ void load_rows(const void* p, long long e, long long ld, int dtype, bool pair, int n, uint32_t (&w)[16])
+{
+    if (dtype == 2)
+        load_each<uint32_t>(p, e, ld, n, w);
+    else if (pair)
+        load_pairs(p, e, ld, n, w);
     else
-        store_rows<float>(p, e, ld, n, v);
+        load_each<unsigned short>(p, e, ld, n, w);
+}
+__device__ __forceinline__ void store_rows(void* p, long long e, long long ld, int dtype, bool pair, int n, const uint32_t (&v)[16])
+{
+    if (dtype == 2)
+        store_each<float>(p, e, ld, n, v);
+    else if (dtype == 0 && pair)
+        store_pairs<__nv_bfloat16>(p, e, ld, n, v);
+    else if (dtype == 0)
+        store_each<__nv_bfloat16>(p, e, ld, n, v);
+    else if (pair)
+        store_pairs<__half>(p, e, ld, n, v);
+    else
+        store_each<__half>(p, e, ld, n, v);
+}
+__device__ __forceinline__ float as_float(uint32_t w, int dtype)
+{
+    if (dtype == 0) return __uint_as_float(w << 16);
+    if (dtype == 1) return __half2float(__ushort_as_half((unsigned short)w));
+    return __uint_as_float(w);
 }
 
 // Dropout of rows row .. row + 7 of the warp's 32 columns (the first a multiple of 8): bit k is
@@ -370,12 +415,7 @@ __device__ __forceinline__ void column_tail(const LayerTail& t, unsigned long lo
 #pragma unroll
             for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) + b);
         }
-        if (t.z) {
-            if (t.z_dtype == 0)
-                store_rows<__nv_bfloat16>(t.z, row * t.ldz + col, t.ldz, n, v);
-            else
-                store_rows<__half>(t.z, row * t.ldz + col, t.ldz, n, v);
-        }
+        if (t.z) store_rows(t.z, row * t.ldz + col, t.ldz, t.z_dtype, t.vec & kPairZ, n, v);
         if (t.act != kActNone) {
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {  // one copy of the activations: eight rows, then the other eight
@@ -389,7 +429,7 @@ __device__ __forceinline__ void column_tail(const LayerTail& t, unsigned long lo
         }
     }
     if (KIND == kData && t.z) {
-        load_rows<unsigned short>(t.z, row * t.ldz + col, t.ldz, n, x);
+        load_rows(t.z, row * t.ldz + col, t.ldz, t.z_dtype, t.vec & kPairZ, n, x);
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
             float f[8], z[8];
@@ -400,12 +440,8 @@ __device__ __forceinline__ void column_tail(const LayerTail& t, unsigned long lo
             for (int k = 0; k < 8; ++k) v[k] = v[8 + k], v[8 + k] = __float_as_uint(f[k]), x[k] = x[8 + k];
         }
     }
-    if (t.res) {  // (on its way while the mask is made)
-        if (t.y_dtype == 2)
-            load_rows<uint32_t>(t.res, base + row * t.ldr + col, t.ldr, n, x);
-        else
-            load_rows<unsigned short>(t.res, base + row * t.ldr + col, t.ldr, n, x);
-    }
+    if (t.res)  // (on its way while the mask is made)
+        load_rows(t.res, base + row * t.ldr + col, t.ldr, t.y_dtype, t.vec & kPairRes, n, x);
     if (KIND != kWeight && t.thr) {
 #pragma unroll
         for (int h = 0; h < 16; h += 8) {
@@ -418,7 +454,7 @@ __device__ __forceinline__ void column_tail(const LayerTail& t, unsigned long lo
 #pragma unroll
         for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) + as_float(x[k], t.y_dtype));
     }
-    store_rows(t.y, base + row * t.ldy + col, t.ldy, t.y_dtype, n, v);
+    store_rows(t.y, base + row * t.ldy + col, t.ldy, t.y_dtype, t.vec & kPairY, n, v);
 }
 
 // ---------------------------------------------------------------- activation alone
@@ -507,45 +543,43 @@ __global__ void __launch_bounds__(kActThreads) activation_kernel(const __grid_co
     }
 }
 
-// dbias from its partial sums: part[first .. first + count - 1][dim], 32 of them side by
-// side per column, then those in order.
+// dbias from its partial sums: those of part[first .. first + count - 1][dim] that are ny apart
+// by each of ny threads of a column, then the threads' in order.
+constexpr int kJoinThreads = 256;
 struct SumParams {
     const float* part;
     void* out;
-    long long out_stride;
     int dim, dtype, accumulate;
+    int ny_log;
     int chunks;            // of a problem without experts
     const int* first;      // [experts + 1] chunks before each expert's, or null
 };
-__global__ void __launch_bounds__(1024) column_join_kernel(const __grid_constant__ SumParams p)
+__global__ void __launch_bounds__(kJoinThreads) column_join_kernel(const __grid_constant__ SumParams p)
 {
     pdl_launch_dependents();
-    __shared__ float s[32][33];
-    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, j = blockIdx.x * 32 + tx, e = blockIdx.y;
+    __shared__ float s[kJoinThreads];
+    const int nx = kJoinThreads >> p.ny_log, ny = 1 << p.ny_log, tx = threadIdx.x & (nx - 1), ty = threadIdx.x / nx;
+    const int j = blockIdx.x * nx + tx, e = blockIdx.y;
     pdl_wait();
     const int c0 = p.first ? p.first[e] : 0, c1 = p.first ? p.first[e + 1] : p.chunks;
     float a = 0.f;
     if (j < p.dim)
-#pragma unroll 4
-        for (int c = c0 + ty; c < c1; c += 32) a += p.part[(long long)c * p.dim + j];
-    s[ty][tx] = a;
+#pragma unroll 8
+        for (int c = c0 + ty; c < c1; c += ny) a += p.part[(long long)c * p.dim + j];
+    s[threadIdx.x] = a;
     __syncthreads();
-    if (ty == 0 && j < p.dim) {
-        a = 0.f;
-#pragma unroll
-        for (int y = 0; y < 32; ++y) a += s[y][tx];
-        const long long i = e * p.out_stride + j;
-        if (p.accumulate && c0 == c1) return;
-        if (p.dtype == 2) {
-            float* o = static_cast<float*>(p.out) + i;
-            *o = p.accumulate ? *o + a : a;
-        } else if (p.dtype == 0) {
-            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + i;
-            *o = __float2bfloat16_rn(p.accumulate ? __bfloat162float(*o) + a : a);
-        } else {
-            __half* o = static_cast<__half*>(p.out) + i;
-            *o = __float2half_rn(p.accumulate ? __half2float(*o) + a : a);
-        }
+    if (ty || j >= p.dim || (p.accumulate && c0 == c1)) return;
+    for (int y = 1; y < ny; ++y) a += s[y * nx + tx];
+    const long long i = (long long)e * p.dim + j;
+    if (p.dtype == 2) {
+        float* o = static_cast<float*>(p.out) + i;
+        *o = p.accumulate ? *o + a : a;
+    } else if (p.dtype == 0) {
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + i;
+        *o = __float2bfloat16_rn(p.accumulate ? __bfloat162float(*o) + a : a);
+    } else {
+        __half* o = static_cast<__half*>(p.out) + i;
+        *o = __float2half_rn(p.accumulate ? __half2float(*o) + a : a);
     }
 }
 

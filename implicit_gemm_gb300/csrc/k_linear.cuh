@@ -35,11 +35,15 @@
 
 namespace wg {
 
-// Warps: TMA, MMA, fixing, then the epilogue: sixteen warps, or eight where sums of several
-// chunks are added up, which takes 128 registers of each (sixteen would have 96 in all, and
-// what does not fit goes to L2: no L1 is left beside the ring).
+// Four warps that direct (TMA, MMA, fixing, and one that makes up the warpgroup), then the
+// epilogue: sixteen warps of 96 registers, or, where sums of several chunks are added up
+// in 128 registers of each, eight of 224, which the first four give up of their 168:
+// 384 x 168 = 128 x 56 + 256 x 224.  (Nothing may spill: no L1 is left beside the ring, and what
+// spills comes back from L2.  Eight warps of 168: 8.5 us a tile where 4 is what its stores take.)
+constexpr int kLinDirect = 4, kLinDirectRegs = 56, kLinChunkedRegs = 224;
 constexpr int lin_epi_warps(bool chunked) { return chunked ? 8 : 16; }
-constexpr int lin_threads(bool chunked) { return 32 * (3 + lin_epi_warps(chunked)); }
+constexpr int lin_threads(bool chunked) { return 32 * (kLinDirect + lin_epi_warps(chunked)); }
+static_assert(384 * 168 >= 128 * kLinDirectRegs + 256 * kLinChunkedRegs && 384 * 168 <= 65536, "registers of a CTA");
 constexpr int kLinMaxStages = 12;
 constexpr int kLinMaxExperts = 1024;
 constexpr int kLinABytes = 16384;
@@ -142,10 +146,10 @@ struct LinWalk {
     const LinParams& p;
     const int *off, *first;
     int im, total, item;
+    int tiles, width;  // along the rows (of every expert's matrix for kWeight)
     __device__ __forceinline__ LinWalk(const LinParams& p_, const int* off_, const int* first_, int pair)
         : p(p_), off(off_), first(first_), im((p_.M + 255) / 256), item(pair)
     {
-        int tiles, width;
         if (KIND == kWeight) {
             lin_width(p.N, p.bt, tiles, width);
             total = max(p.experts, 1) * im * tiles * p.split;
@@ -156,36 +160,43 @@ struct LinWalk {
     __device__ __forceinline__ bool next(LinTile& t)
     {
         if (item >= total) return false;
-        int i = item / p.split;
-        t.part = item - i * p.split;
+        int i = item, n, kb = p.kb;
+        t.part = 0;
+        if (p.split > 1) i = item / p.split, t.part = item - i * p.split;
         item += p.pairs;
-        int tiles, width, n, kb = p.kb;
+        t.e = 0;
         if (KIND == kWeight) {
             n = p.N;
-            lin_width(n, p.bt, tiles, width);
-            t.e = i / (im * tiles);
-            i -= t.e * im * tiles;
+            if (p.experts > 1) {
+                t.e = i / (im * tiles);
+                i -= t.e * im * tiles;
+            }
             t.row0 = off[t.e];
             const int rows = off[t.e + 1] - t.row0;
             kb = (rows + 63) >> 6;
             t.valid = rows & 63 ? rows & 63 : 64;
         } else {
-            t.e = find_last(first, max(p.experts, 1), i / im);
-            i -= first[t.e] * im;
+            if (p.experts > 1) {
+                t.e = find_last(first, p.experts, i / im);
+                i -= first[t.e] * im;
+            }
             n = off[t.e + 1] - off[t.e];
             lin_width(n, p.bt, tiles, width);
         }
         // Eight tiles along the rows, then the columns: what the pairs work on at one time
         // is about as many rows' operands as columns'.
         const int g = i / (8 * im), gs = min(8, tiles - 8 * g), in = i - 8 * g * im;
-        const int c = in / gs, j = 8 * g + in - c * gs;
+        const int c = gs == 8 ? in >> 3 : in / gs, j = 8 * g + in - c * gs;
         t.m = 256 * c;
         t.n = j * width;
         t.rows = min(width, n - t.n);
         t.wide = (t.rows + 31) / 32 * 32;
         if (KIND != kWeight) t.n += off[t.e];
-        t.k0 = (int)((long long)kb * t.part / p.split);
-        t.k1 = (int)((long long)kb * (t.part + 1) / p.split);
+        t.k0 = 0, t.k1 = kb;
+        if (p.split > 1) {  // (parts below 17, blocks below 2^25)
+            t.k0 = (int)((unsigned)kb * (unsigned)t.part / (unsigned)p.split);
+            t.k1 = (int)((unsigned)kb * (unsigned)(t.part + 1) / (unsigned)p.split);
+        }
         return true;
     }
 };
@@ -197,6 +208,14 @@ __device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t bar, uint
 {
     asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
+// Arrive on an mbarrier of the cluster.  The thread's own CTA sees what it has written: enough where
+// the next owner is told of tensor memory that has been read.  (A release to the cluster waits
+// for the thread's stores to memory, 1 us of a tile of few blocks.)
+__device__ __forceinline__ void mbar_arrive_read(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The same, for what the cluster sees.
 __device__ __forceinline__ void mbar_arrive_at(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -289,127 +308,130 @@ __global__ void __launch_bounds__(lin_threads(CHUNKED), 1)
     const uint32_t tbase = *tslot;
     LinTile t;
     LinWalk<KIND> walk(p, off, first, pair);
-
-    if (warp == 0) {
-        if (lane == 0) {
-            const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0u), mine = mapa_shared(smem_u32(&tail[0]), (uint32_t)rank);
-            int st = 0;
-            uint32_t ph = 0;
-            bool ok = true, more = walk.next(t);
-            if (!p.experts) pdl_wait();
-            for (; ok && more; more = walk.next(t)) {
-                const int m0 = t.m + rank * 128, n0 = t.n + rank * (t.wide >> 1);
-                for (int k = t.k0; k < t.k1; ++k) {
-                    if (!mbar_wait(&empty[st], ph ^ 1u)) {
-                        ok = false;
-                        break;
+    if (warp < kLinDirect) {
+        if (CHUNKED) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLinDirectRegs));
+        if (warp == 0) {
+            if (lane == 0) {
+                const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0u), mine = mapa_shared(smem_u32(&tail[0]), (uint32_t)rank);
+                int st = 0;
+                uint32_t ph = 0;
+                bool ok = true, more = walk.next(t);
+                if (!p.experts) pdl_wait();
+                for (; ok && more; more = walk.next(t)) {
+                    const int m0 = t.m + rank * 128, n0 = t.n + rank * (t.wide >> 1);
+                    for (int k = t.k0; k < t.k1; ++k) {
+                        if (!mbar_wait(&empty[st], ph ^ 1u)) {
+                            ok = false;
+                            break;
+                        }
+                        uint8_t* s = smem + st * p.stage_bytes;
+                        uint32_t bar = full0 + (uint32_t)(st * 8);
+                        int kc = 64 * k;
+                        if (KIND == kWeight) {
+                            if (t.valid < 64 && kc + 64 > off[t.e + 1] - t.row0) bar = mine + (uint32_t)(st * 8);
+                            kc += t.row0;
+                        }
+                        mbar_arrive_expect_tx_cluster(bar, (uint32_t)p.stage_bytes);
+                        if (KIND == kForward) {
+                            tma_load_3d_at(s, &map_a, bar, kc, m0, t.e);
+                        } else {
+                            const int b = KIND == kData ? t.e : 0;
+                            tma_load_3d_at(s, &map_a, bar, m0, kc, b);
+                            tma_load_3d_at(s + 8192, &map_a, bar, m0 + 64, kc, b);
+                        }
+                        if (kBmn) {
+                            tma_load_3d_at(s + kLinABytes, &map_b, bar, n0, kc, 0);
+                            if (p.bt > 128) tma_load_3d_at(s + kLinABytes + 8192, &map_b, bar, n0 + 64, kc, 0);
+                        } else {
+                            tma_load_3d_at(s + kLinABytes, &map_b, bar, kc, n0, 0);
+                        }
+                        if (++st == p.stages) st = 0, ph ^= 1u;
                     }
-                    uint8_t* s = smem + st * p.stage_bytes;
-                    uint32_t bar = full0 + (uint32_t)(st * 8);
-                    int kc = 64 * k;
-                    if (KIND == kWeight) {
-                        if (t.valid < 64 && kc + 64 > off[t.e + 1] - t.row0) bar = mine + (uint32_t)(st * 8);
-                        kc += t.row0;
-                    }
-                    mbar_arrive_expect_tx_cluster(bar, (uint32_t)p.stage_bytes);
-                    if (KIND == kForward) {
-                        tma_load_3d_at(s, &map_a, bar, kc, m0, t.e);
-                    } else {
-                        const int b = KIND == kData ? t.e : 0;
-                        tma_load_3d_at(s, &map_a, bar, m0, kc, b);
-                        tma_load_3d_at(s + 8192, &map_a, bar, m0 + 64, kc, b);
-                    }
-                    if (kBmn) {
-                        tma_load_3d_at(s + kLinABytes, &map_b, bar, n0, kc, 0);
-                        if (p.bt > 128) tma_load_3d_at(s + kLinABytes + 8192, &map_b, bar, n0 + 64, kc, 0);
-                    } else {
-                        tma_load_3d_at(s + kLinABytes, &map_b, bar, kc, n0, 0);
-                    }
-                    if (++st == p.stages) st = 0, ph ^= 1u;
                 }
             }
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        if (rank == 0) {
-            const uint32_t sbase = smem_u32(smem);
-            const uint64_t ad = make_sdesc(sbase, kAmn ? 8192u : 16u, 1024u, 2u, 0u);
-            const uint64_t bd = make_sdesc(sbase + (uint32_t)kLinABytes, kBmn ? 8192u : 16u, 1024u, 2u, 0u);
-            constexpr uint64_t ak = kAmn ? 128 : 2, bk = kBmn ? 128 : 2;
-            int st = 0, use = 0;
-            uint32_t ph = 0;
-            bool ok = true;
-            while (ok && walk.next(t)) {
-                const uint32_t idesc = make_idesc_f16(p.bf16, kAmn, kBmn, 256, t.wide);
-                for (int c0 = t.k0; ok && c0 < t.k1; c0 += p.chunk, ++use) {
-                    const int buf = use & 1, c1 = min(t.k1, c0 + p.chunk);
-                    if (!mbar_wait(&acce[buf], ((uint32_t)(use >> 1) & 1u) ^ 1u)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t d = tbase + (uint32_t)(buf * 256);
-                    for (int k = c0; k < c1; ++k) {
-                        if (!mbar_wait(&full[st], ph)) {
+            __syncwarp();
+        } else if (warp == 1) {
+            if (rank == 0) {
+                const uint32_t sbase = smem_u32(smem);
+                const uint64_t ad = make_sdesc(sbase, kAmn ? 8192u : 16u, 1024u, 2u, 0u);
+                const uint64_t bd = make_sdesc(sbase + (uint32_t)kLinABytes, kBmn ? 8192u : 16u, 1024u, 2u, 0u);
+                constexpr uint64_t ak = kAmn ? 128 : 2, bk = kBmn ? 128 : 2;
+                int st = 0, use = 0;
+                uint32_t ph = 0;
+                bool ok = true;
+                while (ok && walk.next(t)) {
+                    const uint32_t idesc = make_idesc_f16(p.bf16, kAmn, kBmn, 256, t.wide);
+                    for (int c0 = t.k0; ok && c0 < t.k1; c0 += p.chunk, ++use) {
+                        const int buf = use & 1, c1 = min(t.k1, c0 + p.chunk);
+                        if (!mbar_wait(&acce[buf], ((uint32_t)(use >> 1) & 1u) ^ 1u)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        int ks1 = 4;
-                        if (KIND == kWeight && 64 * k + 64 > off[t.e + 1] - t.row0) ks1 = (t.valid + 15) >> 4;
-                        const uint64_t so = (uint64_t)(st * (p.stage_bytes >> 4));
-                        if (elect_one()) {
+                        const uint32_t d = tbase + (uint32_t)(buf * 256);
+                        for (int k = c0; k < c1; ++k) {
+                            if (!mbar_wait(&full[st], ph)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            int ks1 = 4;
+                            if (KIND == kWeight && 64 * k + 64 > off[t.e + 1] - t.row0) ks1 = (t.valid + 15) >> 4;
+                            const uint64_t so = (uint64_t)(st * (p.stage_bytes >> 4));
+                            if (elect_one()) {
 #pragma unroll
-                            for (int ks = 0; ks < 4; ++ks)
-                                if (ks < ks1) umma_f16_pair(d, ad + so + ak * ks, bd + so + bk * ks, idesc, (k > c0 || ks) ? 1u : 0u);
-                            umma_commit_pair(&empty[st]);
+                                for (int ks = 0; ks < 4; ++ks)
+                                    if (ks < ks1) umma_f16_pair(d, ad + so + ak * ks, bd + so + bk * ks, idesc, (k > c0 || ks) ? 1u : 0u);
+                                umma_commit_pair(&empty[st]);
+                            }
+                            __syncwarp();
+                            if (++st == p.stages) st = 0, ph ^= 1u;
                         }
+                        if (!ok) break;
+                        if (elect_one()) umma_commit_pair(&accf[buf]);
                         __syncwarp();
-                        if (++st == p.stages) st = 0, ph ^= 1u;
                     }
+                }
+            }
+        } else if (warp == 2) {
+            if (KIND == kWeight) {
+                // Rows of an expert's last block that are the next one's become zeros.  (A row is
+                // one line of 128 bytes per 64 columns, whatever the swizzle does within it.)
+                const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0u);
+                int st = 0;
+                uint32_t seen = 0;
+                bool ok = true;
+                while (ok && walk.next(t)) {
+                    const int rows = off[t.e + 1] - t.row0, n = t.k1 - t.k0;
+                    if (n <= 0) continue;
+                    const int last = (st + n - 1) % p.stages;
+                    st = (st + n) % p.stages;
+                    if (t.valid == 64 || 64 * t.k1 <= rows) continue;
+                    ok = mbar_wait_sleep(&tail[last], (seen >> last) & 1u);
+                    seen ^= 1u << last;
+                    __syncwarp();
                     if (!ok) break;
-                    if (elect_one()) umma_commit_pair(&accf[buf]);
+                    uint8_t* s = smem + last * p.stage_bytes;
+                    const int zeros = ((t.valid + 15) >> 4 << 4) - t.valid;  // rows, of 8 chunks of 16 bytes each
+                    for (int c = 0; c < p.stage_bytes >> 13; ++c)
+                        for (int i = lane; i < 8 * zeros; i += 32)
+                            *reinterpret_cast<uint4*>(s + 8192 * c + 128 * t.valid + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_at(full0 + (uint32_t)(last * 8));
                     __syncwarp();
                 }
             }
         }
-    } else if (warp == 2) {
-        if (KIND == kWeight) {
-            // Rows of an expert's last block that are the next one's become zeros.  (A row is
-            // one line of 128 bytes per 64 columns, whatever the swizzle does within it.)
-            const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0u);
-            int st = 0;
-            uint32_t seen = 0;
-            bool ok = true;
-            while (ok && walk.next(t)) {
-                const int rows = off[t.e + 1] - t.row0, n = t.k1 - t.k0;
-                if (n <= 0) continue;
-                const int last = (st + n - 1) % p.stages;
-                st = (st + n) % p.stages;
-                if (t.valid == 64 || 64 * t.k1 <= rows) continue;
-                ok = mbar_wait_sleep(&tail[last], (seen >> last) & 1u);
-                seen ^= 1u << last;
-                __syncwarp();
-                if (!ok) break;
-                uint8_t* s = smem + last * p.stage_bytes;
-                const int zeros = ((t.valid + 15) >> 4 << 4) - t.valid;  // rows, of 8 chunks of 16 bytes each
-                for (int c = 0; c < p.stage_bytes >> 13; ++c)
-                    for (int i = lane; i < 8 * zeros; i += 32)
-                        *reinterpret_cast<uint4*>(s + 8192 * c + 128 * t.valid + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_at(full0 + (uint32_t)(last * 8));
-                __syncwarp();
-            }
-        }
     } else {
+        if (CHUNKED) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kLinChunkedRegs));
         // Warp e of the epilogue: 32 columns of the result (its tensor-memory quadrant), one
         // per lane, by every kStep / 16th 16 of the tile's rows.  Results go to memory as they
         // come from tensor memory, a row of 32 columns per instruction, whatever their
         // alignment: shared memory has no bandwidth to spare beside the operands (staged
         // through it, a tile's epilogue took 15 us).
         constexpr int kStep = 4 * kEpiWarps, kOwn = 256 / kStep;
-        const int e = warp - 3, q = warp & 3, first_row = 16 * (e >> 2);
+        const int e = warp - kLinDirect, q = warp & 3, first_row = 16 * (e >> 2);
         const uint32_t acce0 = mapa_shared(smem_u32(&acce[0]), 0u);
         const uint32_t trow = tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)first_row;
         int use = 0;
@@ -460,7 +482,7 @@ __global__ void __launch_bounds__(lin_threads(CHUNKED), 1)
                     }
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_at(acce0 + (uint32_t)((use & 1) * 8));
+                    if (lane == 0) mbar_arrive_read(acce0 + (uint32_t)((use & 1) * 8));
                     ++use;
                 }
             } else if (t.k0 < t.k1) {
@@ -470,6 +492,11 @@ __global__ void __launch_bounds__(lin_threads(CHUNKED), 1)
             }
             if (!ok) break;
             uint32_t tacc = trow + (uint32_t)((use & 1) * 256);
+            const auto read_all = [&]() {  // this warp has read its share of the buffer
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_read(acce0 + (uint32_t)((use & 1) * 8));
+            };
 #pragma unroll 1
             for (int r0 = first_row; r0 < t.rows; r0 += kStep, tacc += kStep) {
                 uint32_t r[16];
@@ -477,6 +504,7 @@ __global__ void __launch_bounds__(lin_threads(CHUNKED), 1)
                     tmem_ld16_issue(tacc, r);
                     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
                     reg_fence16(r);
+                    if (r0 + kStep >= t.rows) read_all();
                 } else {
 #pragma unroll
                     for (int k = 0; k < 16; ++k) r[k] = 0u;
@@ -492,9 +520,7 @@ __global__ void __launch_bounds__(lin_threads(CHUNKED), 1)
                 }
             }
             if (t.k0 < t.k1) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_at(acce0 + (uint32_t)((use & 1) * 8));
+                if (first_row >= t.rows) read_all();
                 ++use;
             }
         }

@@ -121,11 +121,26 @@ bool vec_rows(const void* p, long long ld, int cols, int es, long long stride = 
     return cols % 8 == 0 && (ld * es) % 16 == 0 && (stride * es) % 16 == 0 && aligned16(p);
 }
 
+// 4-byte accesses of two 16-bit elements.
+bool pair_rows(const void* p, long long ld, int cols, int es, long long stride = 0)
+{
+    return es == 2 && cols % 2 == 0 && ld % 2 == 0 && stride % 2 == 0 && aligned_to(p, 4);
+}
+
 int log2_floor(long long n)
 {
     int b = 0;
     while ((2LL << b) <= n) ++b;
     return b;
+}
+
+// dbias of `experts` from `chunks` partial sums in all; as many threads a column as leave each some four.
+int join_columns(wg::SumParams m, int experts, long long chunks, cudaStream_t s)
+{
+    m.ny_log = std::min(5, log2_floor(std::max(1LL, chunks / experts / 4)));
+    const int nx = wg::kJoinThreads >> m.ny_log;
+    return launch("column_join_kernel launch", wg::column_join_kernel, dim3((unsigned)((m.dim + nx - 1) / nx), (unsigned)experts),
+                  dim3(wg::kJoinThreads), s, m);
 }
 
 // ---------------------------------------------------------------- products
@@ -451,8 +466,11 @@ int wg_linear(const wg_linear_problem* p, const void* offsets, const void* x, co
     g.z = z, g.z_dtype = q.in_dtype, g.ldz = q.ld_z, g.act = q.activation;
     g.bias = bias, g.bias_dtype = q.bias_dtype, g.bias_stride = q.out;
     if (vec_rows(y, q.ld_out, q.out, oe)) g.vec |= wg::kVecY;
+    if (pair_rows(y, q.ld_out, q.out, oe)) g.vec |= wg::kPairY;
     if (vec_rows(z, q.ld_z, q.out, ie)) g.vec |= wg::kVecZ;
+    if (pair_rows(z, q.ld_z, q.out, ie)) g.vec |= wg::kPairZ;
     if (vec_rows(residual, q.ld_residual, q.out, oe)) g.vec |= wg::kVecRes;
+    if (pair_rows(residual, q.ld_residual, q.out, oe)) g.vec |= wg::kPairRes;
     if (vec_rows(bias, q.out, q.out, be)) g.vec |= wg::kVecBias;
     set_dropout(&g, q.dropout, q.seed, q.offset, q.counter);
     return lin_run(pl, offsets, {w, q.out, q.in, q.ld_weight, ne, q.weight_stride}, {x, q.tokens, q.in, q.ld_in, 1, 0}, g,
@@ -484,8 +502,11 @@ int wg_linear_bwd_data(const wg_linear_problem* p, const void* offsets, const vo
     g.y = dx, g.y_dtype = q.out_dtype, g.ldy = q.ld_in, g.res = residual, g.ldr = q.ld_residual;
     g.z = const_cast<void*>(z), g.z_dtype = q.in_dtype, g.ldz = q.ld_z, g.act = q.activation;
     if (vec_rows(dx, q.ld_in, q.in, oe)) g.vec |= wg::kVecY;
+    if (pair_rows(dx, q.ld_in, q.in, oe)) g.vec |= wg::kPairY;
     if (vec_rows(z, q.ld_z, q.in, ie)) g.vec |= wg::kVecZ;
+    if (pair_rows(z, q.ld_z, q.in, ie)) g.vec |= wg::kPairZ;
     if (vec_rows(residual, q.ld_residual, q.in, oe)) g.vec |= wg::kVecRes;
+    if (pair_rows(residual, q.ld_residual, q.in, oe)) g.vec |= wg::kPairRes;
     set_dropout(&g, q.dropout, q.seed, q.offset, q.counter);
     return lin_run(pl, offsets, {w, q.out, q.in, q.ld_weight, ne, q.weight_stride}, {dy, q.tokens, q.out, q.ld_out, 1, 0}, g,
                    static_cast<char*>(workspace), static_cast<cudaStream_t>(stream));
@@ -513,6 +534,7 @@ int wg_linear_bwd_weight(const wg_linear_problem* p, const void* offsets, const 
     g.y = dw, g.y_dtype = q.out_dtype, g.ldy = q.ld_weight, g.y_stride = q.weight_stride;
     if (accumulate) g.res = dw, g.ldr = q.ld_weight;
     if (vec_rows(dw, q.ld_weight, q.in, oe, ne > 1 ? q.weight_stride : 0)) g.vec |= wg::kVecY | wg::kVecRes;
+    if (pair_rows(dw, q.ld_weight, q.in, oe, ne > 1 ? q.weight_stride : 0)) g.vec |= wg::kPairY | wg::kPairRes;
     st = lin_run(pl, offsets, {x, q.tokens, q.in, q.ld_in, 1, 0}, {dy, q.tokens, q.out, q.ld_out, 1, 0}, g, ws, s);
     if (st || !dbias) return st;
     wg::ColumnParams c = {};
@@ -526,9 +548,9 @@ int wg_linear_bwd_weight(const wg_linear_problem* p, const void* offsets, const 
                 dim3(256), s, c);
     if (st) return st;
     wg::SumParams m = {};
-    m.part = c.part, m.out = dbias, m.out_stride = q.out, m.dim = q.out, m.dtype = q.bias_dtype, m.accumulate = accumulate != 0;
+    m.part = c.part, m.out = dbias, m.dim = q.out, m.dtype = q.bias_dtype, m.accumulate = accumulate != 0;
     m.first = c.first;
-    return launch("column_join_kernel launch", wg::column_join_kernel, dim3((unsigned)((q.out + 31) / 32), (unsigned)ne), dim3(1024), s, m);
+    return join_columns(m, ne, pl.sum_chunks, s);
 }
 
 int wg_activation_workspace_size(const wg_activation_problem* p, size_t* bytes)
@@ -592,7 +614,7 @@ int wg_activation_bwd(const wg_activation_problem* p, const void* dy, const void
     if ((st = act_launch<true>(pl, g, s)) || !dbias) return st;
     wg::SumParams m = {};
     m.part = g.part, m.out = dbias, m.dim = q.dim, m.dtype = q.bias_dtype, m.chunks = (int)pl.chunks;
-    return launch("column_join_kernel launch", wg::column_join_kernel, dim3((unsigned)((q.dim + 31) / 32)), dim3(1024), s, m);
+    return join_columns(m, 1, pl.chunks, s);
 }
 
 }  // extern "C"
