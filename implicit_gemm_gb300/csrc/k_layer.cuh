@@ -33,36 +33,34 @@ struct LayerTail {
     long long y_stride;               // elements between experts' results (and res's), of the weight gradient
     int bias_dtype, y_dtype, z_dtype;
     int act, vec;
-    unsigned thr;                     // 0: no dropout
+    unsigned thr;                     // of an element's 16 bits, times 2^16; 0: no dropout
     float gain;
-    unsigned long long seed, offset;
+    uint2 key[10];                    // the generator's keys, a round each
+    unsigned long long offset;
     const unsigned long long* counter;  // added to the offset, or null
 };
 
 // ---------------------------------------------------------------- dropout
-__device__ __forceinline__ uint4 philox(uint4 c, uint2 k)
+__device__ __forceinline__ uint4 philox(uint4 c, const uint2 (&key)[10])
 {
 #pragma unroll
     for (int i = 0; i < 10; ++i) {
-        const uint32_t h0 = __umulhi(c.x, 0xD2511F53u), l0 = c.x * 0xD2511F53u;
-        const uint32_t h1 = __umulhi(c.z, 0xCD9E8D57u), l1 = c.z * 0xCD9E8D57u;
-        c = make_uint4(h1 ^ c.y ^ k.x, l1, h0 ^ c.w ^ k.y, l0);
-        k.x += 0x9E3779B9u, k.y += 0xBB67AE85u;
+        const uint64_t a = (uint64_t)c.x * 0xD2511F53u, b = (uint64_t)c.z * 0xCD9E8D57u;
+        c = make_uint4((uint32_t)(b >> 32) ^ c.y ^ key[i].x, (uint32_t)b, (uint32_t)(a >> 32) ^ c.w ^ key[i].y, (uint32_t)a);
     }
     return c;
 }
 
-// Elements 8 * group .. + 7 of a row times what dropout makes of them.
+// Elements 8 * group .. + 7 of a row, zeros where they are dropped (the gain is still to come).
 __device__ __forceinline__ void drop8(const LayerTail& t, unsigned long long offset, long long row, int group,
                                       float (&v)[8])
 {
-    const uint4 r = philox(make_uint4((uint32_t)group, (uint32_t)row, (uint32_t)offset, (uint32_t)(offset >> 32)),
-                           make_uint2((uint32_t)t.seed, (uint32_t)(t.seed >> 32)));
+    const uint4 r = philox(make_uint4((uint32_t)group, (uint32_t)row, (uint32_t)offset, (uint32_t)(offset >> 32)), t.key);
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        v[2 * i] = (w[i] & 0xffffu) >= t.thr ? v[2 * i] * t.gain : 0.f;
-        v[2 * i + 1] = (w[i] >> 16) >= t.thr ? v[2 * i + 1] * t.gain : 0.f;
+        v[2 * i] = w[i] << 16 >= t.thr ? v[2 * i] : 0.f;
+        v[2 * i + 1] = w[i] >= t.thr ? v[2 * i + 1] : 0.f;
     }
 }
 
@@ -83,11 +81,73 @@ __device__ __forceinline__ float sigmoid_f(float a) { return __fdividef(1.f, 1.f
 __device__ __forceinline__ float square_f(float v) { return fminf(v * v, 1e10f); }
 __device__ __forceinline__ float gelu_2u(float v) { return v * fmaf(0.0713548162726f, square_f(v), 1.59576912161f); }
 
+// The normal distribution's tails by Abramowitz and Stegun's 7.1.26 (Hastings, 1955):
+// erfc(x) = t (a1 + ... + a5 t^4) exp(-x^2), t = 1 / (1 + p x), off by 1.5e-7 at most, in a third
+// of erff's instructions (instructions are what bounds the activation alone).
+// Two values at a time: fp32 operations on pairs issue once.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b)
+{
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void split(F2 x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v)); }
+__device__ __forceinline__ F2 mul(F2 a, F2 b)
+{
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c)
+{
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ float rcp_f(float a) { return __fdividef(1.f, a); }
+
+// q = erfc(|v| / sqrt 2) / 2 and e = exp(-v^2 / 2) of a pair.
+__device__ __forceinline__ F2 tails(float a, float b, F2& e)
+{
+    const F2 v = f2(a, b), x = f2(fabsf(a), fabsf(b));
+    const F2 d = fma(x, f2(0.23164190f, 0.23164190f), f2(1.f, 1.f)), g = mul(mul(v, v), f2(-0.72134752f, -0.72134752f));
+    float d0, d1, g0, g1;
+    split(d, d0, d1), split(g, g0, g1);
+    const F2 t = f2(rcp_f(d0), rcp_f(d1));
+    e = f2(exp2f(g0), exp2f(g1));
+    F2 q = fma(t, f2(0.5f * 1.061405429f, 0.5f * 1.061405429f), f2(0.5f * -1.453152027f, 0.5f * -1.453152027f));
+    q = fma(t, q, f2(0.5f * 1.421413741f, 0.5f * 1.421413741f));
+    q = fma(t, q, f2(0.5f * -0.284496736f, 0.5f * -0.284496736f));
+    q = fma(t, q, f2(0.5f * 0.254829592f, 0.5f * 0.254829592f));
+    return mul(mul(q, t), e);
+}
+__device__ __forceinline__ void gelu2(float& a, float& b)
+{
+    F2 e;
+    float q0, q1;
+    split(tails(a, b, e), q0, q1);
+    // v - v q above 0, v q below: the size of v q taken off what is above 0 (an infinity times
+    // a tail of 0 is 0).
+    a = fmaxf(a, 0.f) - fminf(fabsf(a), 1e30f) * q0;
+    b = fmaxf(b, 0.f) - fminf(fabsf(b), 1e30f) * q1;
+}
+__device__ __forceinline__ void gelu_slope2(float& a, float& b)
+{
+    F2 e;
+    float q0, q1, p0, p1;
+    split(tails(a, b, e), q0, q1);
+    split(mul(mul(e, f2(0.39894228f, 0.39894228f)), f2(a, b)), p0, p1);
+    a = (a < 0.f ? q0 : 1.f - q0) + p0;
+    b = (b < 0.f ? q1 : 1.f - q1) + p1;
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_f(float v)
 {
     if (ACT == kActRelu) return v < 0.f ? 0.f : v;
-    if (ACT == kActGelu) return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
     if (ACT == kActGeluTanh) return v * sigmoid_f(gelu_2u(v));
     if (ACT == kActSilu) return v * sigmoid_f(v);
     return v;
@@ -96,8 +156,6 @@ __device__ __forceinline__ float act_f(float v)
 template <int ACT>
 __device__ __forceinline__ float slope_f(float v)
 {
-    if (ACT == kActGelu)
-        return fmaf(v * 0.39894228040143268f, __expf(-0.5f * v * v), 0.5f * (1.f + erff(v * 0.70710678118654752f)));
     if (ACT == kActGeluTanh) {
         const float s = sigmoid_f(gelu_2u(v));  // d(2u)/dv = 1.5957... + 3 * 0.0713... v^2
         return fmaf(v * s * (1.f - s), fmaf(0.2140644488178f, square_f(v), 1.59576912161f), s);
@@ -116,7 +174,8 @@ __device__ __forceinline__ void act8(int act, float (&v)[8])
     if (act == kActRelu) {
         WG_EACH(kActRelu)
     } else if (act == kActGelu) {
-        WG_EACH(kActGelu)
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) gelu2(v[i], v[i + 1]);
     } else if (act == kActGeluTanh) {
         WG_EACH(kActGeluTanh)
     } else if (act == kActSilu) {
@@ -133,7 +192,12 @@ __device__ __forceinline__ void slope8(int act, const float (&z)[8], float (&v)[
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = z[i] <= 0.f ? 0.f : v[i];
     } else if (act == kActGelu) {
-        WG_EACH(kActGelu)
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            float a = z[i], b = z[i + 1];
+            gelu_slope2(a, b);
+            v[i] *= a, v[i + 1] *= b;
+        }
     } else if (act == kActGeluTanh) {
         WG_EACH(kActGeluTanh)
     } else if (act == kActSilu) {
@@ -274,7 +338,10 @@ __device__ __forceinline__ void tail_write(const LayerTail& t, unsigned long lon
     if (t.res) {
         unpack8(r.res, t.y_dtype, x);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += x[i];
+        for (int i = 0; i < 8; ++i) v[i] = fmaf(v[i], t.gain, x[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= t.gain;
     }
     store8(t.y, (KIND == kWeight ? expert * t.y_stride : 0) + row * t.ldy + col, t.y_dtype, t.vec & kVecY, n, v);
 }
@@ -371,14 +438,12 @@ __device__ __forceinline__ float as_float(uint32_t w, int dtype)
 __device__ __forceinline__ uint32_t keep_columns(const LayerTail& t, unsigned long long offset, long long row, int col)
 {
     const int lane = threadIdx.x & 31;
-    const uint4 r = philox(make_uint4((uint32_t)(col >> 3), (uint32_t)(row + (lane & 7)), (uint32_t)offset, (uint32_t)(offset >> 32)),
-                           make_uint2((uint32_t)t.seed, (uint32_t)(t.seed >> 32)));
+    const uint4 r = philox(make_uint4((uint32_t)(col >> 3), (uint32_t)(row + (lane & 7)), (uint32_t)offset, (uint32_t)(offset >> 32)), t.key);
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
     uint32_t mine = 0;
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-        const uint32_t h = c & 1 ? w[c >> 1] >> 16 : w[c >> 1] & 0xffffu;
-        const uint32_t b = __ballot_sync(0xffffffffu, h >= t.thr);
+        const uint32_t b = __ballot_sync(0xffffffffu, (c & 1 ? w[c >> 1] : w[c >> 1] << 16) >= t.thr);
         if ((lane & 7) == c) mine = b;
     }
     return mine >> (lane & 24);
@@ -447,24 +512,108 @@ __device__ __forceinline__ void column_tail(const LayerTail& t, unsigned long lo
         for (int h = 0; h < 16; h += 8) {
             const uint32_t keep = keep_columns(t, offset, row + h, col);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[h + k] = keep >> k & 1 ? __float_as_uint(__uint_as_float(v[h + k]) * t.gain) : 0u;
+            for (int k = 0; k < 8; ++k) v[h + k] = keep >> k & 1 ? v[h + k] : 0u;
         }
     }
     if (t.res) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) + as_float(x[k], t.y_dtype));
+        for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(fmaf(__uint_as_float(v[k]), t.gain, as_float(x[k], t.y_dtype)));
+    } else if (KIND != kWeight && t.thr) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * t.gain);
     }
     store_rows(t.y, base + row * t.ldy + col, t.ldy, t.y_dtype, t.vec & kPairY, n, v);
 }
 
+// ---------------------------------------------------------------- rows that start anywhere
+// Eight 16-bit elements per lane of a row whose lanes' elements follow one another, in aligned
+// 16-byte accesses: a lane's elements are parts of two of them, of which the second is the
+// next lane's first.  (An element at a time: eight times the requests, 5001 x 2047 in fp16
+// 80 us.)  `a` is the address of the lane's first element, `end` that of the row's end; chunks
+// that hold no element of the row are not touched.  The whole warp, converged.
+__device__ __forceinline__ uint4 load_shifted(uintptr_t a, uintptr_t end)
+{
+    const uintptr_t c = a & ~(uintptr_t)15;
+    const uint32_t s = (uint32_t)(a & 15);  // the same for every lane
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (c < end) x = *reinterpret_cast<const uint4*>(c);
+    if (s == 0) return x;
+    uint4 y = make_uint4(__shfl_down_sync(0xffffffffu, x.x, 1), __shfl_down_sync(0xffffffffu, x.y, 1),
+                         __shfl_down_sync(0xffffffffu, x.z, 1), __shfl_down_sync(0xffffffffu, x.w, 1));
+    if ((threadIdx.x & 31) == 31) {
+        y = make_uint4(0u, 0u, 0u, 0u);
+        if (c + 16 < end) y = *reinterpret_cast<const uint4*>(c + 16);
+    }
+    const uint32_t h = (s & 2u) * 8u;
+    if (s < 4) return make_uint4(__funnelshift_r(x.x, x.y, h), __funnelshift_r(x.y, x.z, h), __funnelshift_r(x.z, x.w, h), __funnelshift_r(x.w, y.x, h));
+    if (s < 8) return make_uint4(__funnelshift_r(x.y, x.z, h), __funnelshift_r(x.z, x.w, h), __funnelshift_r(x.w, y.x, h), __funnelshift_r(y.x, y.y, h));
+    if (s < 12) return make_uint4(__funnelshift_r(x.z, x.w, h), __funnelshift_r(x.w, y.x, h), __funnelshift_r(y.x, y.y, h), __funnelshift_r(y.y, y.z, h));
+    return make_uint4(__funnelshift_r(x.w, y.x, h), __funnelshift_r(y.x, y.y, h), __funnelshift_r(y.y, y.z, h), __funnelshift_r(y.z, y.w, h));
+}
+
+__device__ __forceinline__ void store_halves(uintptr_t c, const uint4& v, uintptr_t begin, uintptr_t end)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (c + 2 * i >= begin && c + 2 * i < end)
+            *reinterpret_cast<unsigned short*>(c + 2 * i) = (unsigned short)(i & 1 ? w[i >> 1] >> 16 : w[i >> 1]);
+}
+__device__ __forceinline__ void store_shifted(uintptr_t a, uintptr_t end, const uint4& x)
+{
+    const uint32_t s = (uint32_t)(a & 15);
+    const int lane = threadIdx.x & 31;
+    const uintptr_t begin = a - 16 * lane;
+    end = min(end, begin + 512);
+    if (s == 0) {
+        if (a + 16 <= end)
+            *reinterpret_cast<uint4*>(a) = x;
+        else
+            store_halves(a, x, begin, end);
+        return;
+    }
+    const uintptr_t c = a - s;
+    const uint4 p = make_uint4(__shfl_up_sync(0xffffffffu, x.x, 1), __shfl_up_sync(0xffffffffu, x.y, 1),
+                               __shfl_up_sync(0xffffffffu, x.z, 1), __shfl_up_sync(0xffffffffu, x.w, 1));
+    // The aligned chunk at c: the last s bytes of the lane before, then the first of this one;
+    // and (of the last lane) the chunk after it, which begins with this lane's last s bytes.
+    const uint32_t o = 16 - s, h = (o & 2u) * 8u;
+    uint4 v, z;
+    if (o < 4) {
+        v = make_uint4(__funnelshift_r(p.x, p.y, h), __funnelshift_r(p.y, p.z, h), __funnelshift_r(p.z, p.w, h), __funnelshift_r(p.w, x.x, h));
+        z = make_uint4(__funnelshift_r(x.x, x.y, h), __funnelshift_r(x.y, x.z, h), __funnelshift_r(x.z, x.w, h), __funnelshift_r(x.w, 0u, h));
+    } else if (o < 8) {
+        v = make_uint4(__funnelshift_r(p.y, p.z, h), __funnelshift_r(p.z, p.w, h), __funnelshift_r(p.w, x.x, h), __funnelshift_r(x.x, x.y, h));
+        z = make_uint4(__funnelshift_r(x.y, x.z, h), __funnelshift_r(x.z, x.w, h), __funnelshift_r(x.w, 0u, h), 0u);
+    } else if (o < 12) {
+        v = make_uint4(__funnelshift_r(p.z, p.w, h), __funnelshift_r(p.w, x.x, h), __funnelshift_r(x.x, x.y, h), __funnelshift_r(x.y, x.z, h));
+        z = make_uint4(__funnelshift_r(x.z, x.w, h), __funnelshift_r(x.w, 0u, h), 0u, 0u);
+    } else {
+        v = make_uint4(__funnelshift_r(p.w, x.x, h), __funnelshift_r(x.x, x.y, h), __funnelshift_r(x.y, x.z, h), __funnelshift_r(x.z, x.w, h));
+        z = make_uint4(__funnelshift_r(x.w, 0u, h), 0u, 0u, 0u);
+    }
+    if (c >= begin && c + 16 <= end)
+        *reinterpret_cast<uint4*>(c) = v;
+    else
+        store_halves(c, v, begin, end);
+    if (lane == 31) store_halves(c + 16, z, begin, end);
+}
+
 // ---------------------------------------------------------------- activation alone
 // y = residual + D(act(x + bias)), or dx = D(act'(x + bias) dy) and dbias's partial sums.
-// A thread has eight columns and walks down rows, kActRows in flight; 2^cx_log threads side by side.
-constexpr int kActThreads = 256, kActRows = 4;
+// A thread has eight columns and walks down rows, several in flight; 2^cx_log threads side by
+// side.  HBM bound where arithmetic is cheap (16384 x 4096 in bf16 with a residual: 60 us of
+// bytes); gelu and dropout together are as many instructions as that leaves time for.
+constexpr int kActThreads = 256;
+enum ActMode {
+    kActWide,     // 16-bit tensors, every chunk of eight columns on 16 bytes
+    kActShifted,  // 16-bit tensors, rows of more than 248 columns that start anywhere
+    kActAny,      // any types and alignment
+};
 
 struct ActParams {
     LayerTail t;          // forward: y, res; gradient: y = dx, res = null
-    const void* x;        // 16- or 32-bit, may be null in a gradient without an activation
+    const void* x;        // may be null in a gradient without an activation
     const void* dy;
     long long rows, ldx, lddy;
     int dim, x_dtype, dy_dtype, vec_x, vec_dy;
@@ -472,9 +621,32 @@ struct ActParams {
     float* part;          // [chunks][dim] sums of dx, or null
 };
 
-template <bool BWD>
-__global__ void __launch_bounds__(kActThreads) activation_kernel(const __grid_constant__ ActParams p)
+template <int MODE>
+__device__ __forceinline__ Raw8 act_load(const void* p, long long row, long long ld, int col, int n, int dim, int dtype, bool vec)
 {
+    Raw8 r;
+    if (MODE == kActShifted) {
+        const uintptr_t b = reinterpret_cast<uintptr_t>(p) + 2 * row * ld;
+        r.a = load_shifted(b + 2 * (uintptr_t)col, b + 2 * (uintptr_t)dim);
+        return r;
+    }
+    if (MODE == kActWide) {
+        r.a = *reinterpret_cast<const uint4*>(at(p, row * ld + col, 0));
+        return r;
+    }
+    return load_raw8(p, row * ld + col, dtype, vec, n);
+}
+template <int MODE>
+__device__ __forceinline__ void act_unpack(const Raw8& r, int dtype, float (&f)[8])
+{
+    if (MODE != kActAny && dtype == 2) __builtin_unreachable();
+    unpack8(r, dtype, f);
+}
+
+template <bool BWD, int MODE>
+__global__ void __launch_bounds__(kActThreads, MODE == kActAny ? 2 : 3) activation_kernel(const __grid_constant__ ActParams p)
+{
+    constexpr int kRows = MODE == kActWide && !BWD ? 4 : 2;
     pdl_launch_dependents();
     const int cx = 1 << p.cx_log, tx = threadIdx.x & (cx - 1), ty = threadIdx.x >> p.cx_log, ny = kActThreads >> p.cx_log;
     const int col = 8 * (blockIdx.x * cx + tx), n = min(8, p.dim - col);
@@ -482,33 +654,33 @@ __global__ void __launch_bounds__(kActThreads) activation_kernel(const __grid_co
     float sum[8] = {}, bias[8] = {};
     pdl_wait();
     const unsigned long long offset = layer_offset(t);
-    if (n > 0) {
-        if (t.bias) unpack8(load_raw8(t.bias, col, t.bias_dtype, t.vec & kVecBias, n), t.bias_dtype, bias);
+    if (t.bias && n > 0) unpack8(load_raw8(t.bias, col, t.bias_dtype, t.vec & kVecBias, n), t.bias_dtype, bias);
+    if (n > 0 || MODE == kActShifted) {  // (there, lanes behind the row's end hold what the last ones shift in)
         const long long r1 = min(p.rows, (long long)(blockIdx.y + 1) * p.chunk);
-        for (long long r0 = (long long)blockIdx.y * p.chunk + ty; r0 < r1; r0 += kActRows * ny) {
-            Raw8 x[kActRows], o[kActRows];
+        for (long long r0 = (long long)blockIdx.y * p.chunk + ty; r0 < r1; r0 += kRows * ny) {
+            Raw8 x[kRows], o[kRows];
 #pragma unroll
-            for (int i = 0; i < kActRows; ++i) {
+            for (int i = 0; i < kRows; ++i) {
                 const long long r = r0 + i * ny;
                 if (r >= r1) continue;
-                if (p.x) x[i] = load_raw8(p.x, r * p.ldx + col, p.x_dtype, p.vec_x, n);
+                if (p.x) x[i] = act_load<MODE>(p.x, r, p.ldx, col, n, p.dim, p.x_dtype, p.vec_x);
                 if (BWD)
-                    o[i] = load_raw8(p.dy, r * p.lddy + col, p.dy_dtype, p.vec_dy, n);
+                    o[i] = act_load<MODE>(p.dy, r, p.lddy, col, n, p.dim, p.dy_dtype, p.vec_dy);
                 else if (t.res)
-                    o[i] = load_raw8(t.res, r * t.ldr + col, t.y_dtype, t.vec & kVecRes, n);
+                    o[i] = act_load<MODE>(t.res, r, t.ldr, col, n, p.dim, t.y_dtype, t.vec & kVecRes);
             }
 #pragma unroll
-            for (int i = 0; i < kActRows; ++i) {
+            for (int i = 0; i < kRows; ++i) {
                 const long long r = r0 + i * ny;
                 if (r >= r1) continue;
                 float v[8], z[8];
                 if (p.x) {
-                    unpack8(x[i], p.x_dtype, z);
+                    act_unpack<MODE>(x[i], p.x_dtype, z);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) z[k] += bias[k];
                 }
                 if (BWD) {
-                    unpack8(o[i], p.dy_dtype, v);
+                    act_unpack<MODE>(o[i], p.dy_dtype, v);
                     slope8(t.act, z, v);
                 } else {
 #pragma unroll
@@ -517,11 +689,26 @@ __global__ void __launch_bounds__(kActThreads) activation_kernel(const __grid_co
                 }
                 if (t.thr) drop8(t, offset, r, col >> 3, v);
                 if (!BWD && t.res) {
-                    unpack8(o[i], t.y_dtype, z);
+                    act_unpack<MODE>(o[i], t.y_dtype, z);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) v[k] += z[k];
+                    for (int k = 0; k < 8; ++k) v[k] = fmaf(v[k], t.gain, z[k]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] *= t.gain;
                 }
-                if (t.y) store8(t.y, r * t.ldy + col, t.y_dtype, t.vec & kVecY, n, v);
+                if (t.y) {
+                    if (MODE == kActAny) {
+                        store8(t.y, r * t.ldy + col, t.y_dtype, t.vec & kVecY, n, v);
+                    } else {
+                        const int d = t.y_dtype == 1;
+                        const uint4 w = make_uint4(pack2(v[0], v[1], d), pack2(v[2], v[3], d), pack2(v[4], v[5], d), pack2(v[6], v[7], d));
+                        const uintptr_t b = reinterpret_cast<uintptr_t>(t.y) + 2 * r * t.ldy;
+                        if (MODE == kActWide)
+                            *reinterpret_cast<uint4*>(b + 2 * (uintptr_t)col) = w;
+                        else
+                            store_shifted(b + 2 * (uintptr_t)col, b + 2 * (uintptr_t)p.dim, w);
+                    }
+                }
                 if (BWD)
 #pragma unroll
                     for (int k = 0; k < 8; ++k) sum[k] += v[k];

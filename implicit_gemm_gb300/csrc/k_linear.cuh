@@ -572,6 +572,169 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
     }
 }
 
+// ---------------------------------------------------------------- few rows
+// The forward product of at most 8 XR rows per expert and pass: every byte of the weights is
+// read once, and that is what bounds it.  A CTA has 8 FG columns of the result (rows of w) of one
+// expert; its eight warps take 32 of the sum each in turn, so that a row of w is read in 512
+// bytes at a time, straight to registers: MMAs of 16 rows of x by 8 of w by 16, of which a
+// lane's operands are 16 consecutive bytes (the sum's terms may come in any order, as long as it is
+// one for both operands).  One batch of loads is in flight while the one before is multiplied;
+// x's come with them (loaded where they were needed, each waited for L2: 4096 x 4096 for one
+// row 14 us).  The warps' sums meet in shared memory, in the order of the warps.
+constexpr int kRowsThreads = 256;
+struct RowsParams {
+    LayerTail t;
+    int experts, offsets64;
+    const void* offsets;
+    long long tokens;
+    const void *x, *w;
+    long long ldx, ldw, wstride;
+    int K, M;                // terms of the sum, columns of the result
+};
+
+template <bool BF16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if (BF16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Eight elements k .. k + 7 of a row of `end` elements (zeros behind it; none of a row that is not there).
+template <bool WIDE>
+__device__ __forceinline__ uint4 rows_load(const unsigned short* row, int k, int end, bool stream)
+{
+    uint4 r = make_uint4(0u, 0u, 0u, 0u);
+    if (!row || k >= end) return r;
+    if (WIDE) {
+        if (stream)
+            asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(row + k));
+        else
+            r = __ldg(reinterpret_cast<const uint4*>(row + k));
+        return r;
+    }
+    uint32_t h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = k + i < end ? __ldg(row + k + i) : 0;
+    return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+}
+
+template <int XR, int FG, bool BF16, bool WIDE>
+__global__ void __launch_bounds__(kRowsThreads, 2) linear_rows_kernel(const __grid_constant__ RowsParams p)
+{
+    constexpr int kAhead = XR == 1 && FG == 2 ? 3 : 2;  // steps of a batch: two of them fill 128 registers
+    struct Batch {
+        uint4 w[kAhead][FG], x[kAhead][XR];
+    };
+    __shared__ int off[kLinMaxExperts + 1];
+    __shared__ short used[kLinMaxExperts];  // experts that have rows
+    __shared__ int count;
+    __shared__ float sums[8][8 * XR][8 * FG + 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
+    pdl_launch_dependents();
+    pdl_wait();
+    load_offsets(p.experts, p.offsets, p.offsets64, p.tokens, off);
+    const int n = max(p.experts, 1);
+    if (warp == 0) {
+        int c = 0;
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            const int i = i0 + lane;
+            const bool has = i < n && off[i + 1] > off[i];
+            const uint32_t b = __ballot_sync(0xffffffffu, has);
+            if (has) used[c + __popc(b & ((1u << lane) - 1u))] = (short)i;
+            c += __popc(b);
+        }
+        if (lane == 0) count = c;
+    }
+    __syncthreads();
+    const unsigned long long offset = layer_offset(p.t);
+    const int per = (p.M + 8 * FG - 1) / (8 * FG);
+    const int total = count * per;
+    for (int item = blockIdx.x; item < total; item += gridDim.x) {
+        const int ei = item / per, e = used[ei], j0 = 8 * FG * (item - ei * per);
+        const unsigned short* w = static_cast<const unsigned short*>(p.w) + e * p.wstride;
+        const unsigned short* wrow[FG];
+#pragma unroll
+        for (int f = 0; f < FG; ++f) wrow[f] = j0 + 8 * f + g < p.M ? w + (j0 + 8 * f + g) * p.ldw : nullptr;
+        for (int r0 = off[e]; r0 < off[e + 1]; r0 += 8 * XR) {
+            const int rows = min(8 * XR, off[e + 1] - r0);
+            const unsigned short* xrow[XR];
+#pragma unroll
+            for (int m = 0; m < XR; ++m)
+                xrow[m] = 8 * m + g < rows ? static_cast<const unsigned short*>(p.x) + (r0 + 8 * m + g) * p.ldx : nullptr;
+            float d[FG][4] = {};
+            const auto load = [&](Batch& c, int k) {
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+#pragma unroll
+                    for (int f = 0; f < FG; ++f) c.w[u][f] = rows_load<WIDE>(wrow[f], k + 256 * u + 8 * tig, p.K, true);
+#pragma unroll
+                    for (int m = 0; m < XR; ++m) c.x[u][m] = rows_load<WIDE>(xrow[m], k + 256 * u + 8 * tig, p.K, false);
+                }
+            };
+            const auto multiply = [&](const Batch& c) {
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const uint4 x0 = c.x[u][0], x1 = XR > 1 ? c.x[u][XR - 1] : make_uint4(0u, 0u, 0u, 0u);
+                    const uint32_t lo[4] = {x0.x, x1.x, x0.y, x1.y}, hi[4] = {x0.z, x1.z, x0.w, x1.w};
+#pragma unroll
+                    for (int f = 0; f < FG; ++f) {
+                        mma16816<BF16>(d[f], lo, c.w[u][f].x, c.w[u][f].y);
+                        mma16816<BF16>(d[f], hi, c.w[u][f].z, c.w[u][f].w);
+                    }
+                }
+            };
+            // The warp's sums so far, to its own place in shared memory: every 64 MMAs (they add with
+            // truncation, see above).
+            bool begun = false;
+            const auto put = [&]() {
+#pragma unroll
+                for (int f = 0; f < FG; ++f)
+#pragma unroll
+                    for (int i = 0; i < 2 * XR; ++i) {
+                        float& s = sums[warp][g + 8 * (i >> 1)][8 * f + 2 * tig + (i & 1)];
+                        s = begun ? s + d[f][i] : d[f][i];
+                        d[f][i] = 0.f;
+                    }
+                begun = true;
+            };
+            constexpr int kStep = 256 * kAhead, kPut = 64 / (2 * kAhead) / 2 * 2 * kStep;
+            Batch b0, b1;
+            int k = 32 * warp, next = k + kPut;
+            if (k < p.K) load(b0, k);
+            while (k < p.K) {
+                if (k >= next) put(), next += kPut;
+                if (k + kStep < p.K) load(b1, k + kStep);
+                multiply(b0);
+                if ((k += kStep) >= p.K) break;
+                if (k + kStep < p.K) load(b0, k + kStep);
+                multiply(b1);
+                k += kStep;
+            }
+            put();
+            __syncthreads();
+            for (int i = threadIdx.x; i < rows * FG; i += kRowsThreads) {
+                const int r = i / FG, f = i - r * FG, j = j0 + 8 * f, nc = min(8, p.M - j);
+                if (nc <= 0) continue;
+                TailRead<kForward> rd;
+                tail_read<kForward>(p.t, e, r0 + r, j, nc, rd);
+                float v[8] = {};
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) v[c] += sums[q][r][8 * f + c];
+                tail_write<kForward>(p.t, offset, e, r0 + r, j, nc, rd, v);
+            }
+            __syncthreads();
+        }
+    }
+}
+
 // ---------------------------------------------------------------- operands that TMA cannot read
 // Rows of 16-bit elements that start anywhere, copied to rows of whole 16-byte chunks.
 __global__ void __launch_bounds__(256) linear_pack_kernel(const unsigned short* in, unsigned short* out, long long rows, int batch,
@@ -640,13 +803,13 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const __grid_constant__
         const int r0 = off[e] + (c - first[e]) * p.chunk, r1 = min(off[e + 1], r0 + p.chunk);
         float sum[8] = {};
         if (m > 0)
-            for (int r = r0 + ty; r < r1; r += 4 * ny) {
-                Raw8 x[4];
+            for (int r = r0 + ty; r < r1; r += 8 * ny) {
+                Raw8 x[8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 8; ++i)
                     if (r + i * ny < r1) x[i] = load_raw8(p.dy, (r + i * ny) * p.ld + col, p.dtype, p.vec, m);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 8; ++i) {
                     if (r + i * ny >= r1) continue;
                     float v[8];
                     unpack8(x[i], p.dtype, v);

@@ -102,9 +102,12 @@ int launch(const char* what, void (*k)(P...), dim3 grid, dim3 block, cudaStream_
 // Dropout of probability p in [0, 1) on the grid of 2^-16.
 void set_dropout(wg::LayerTail* t, float p, unsigned long long seed, unsigned long long offset, const unsigned long long* counter)
 {
-    t->thr = (unsigned)std::min(65535.0, floor(65536.0 * (double)p + 0.5));
-    t->gain = (float)(65536.0 / (65536.0 - t->thr));
-    t->seed = seed, t->offset = offset, t->counter = counter;
+    const unsigned thr = (unsigned)std::min(65535.0, floor(65536.0 * (double)p + 0.5));
+    t->thr = thr << 16;
+    t->gain = (float)(65536.0 / (65536.0 - thr));
+    for (unsigned i = 0; i < 10; ++i)
+        t->key[i] = make_uint2((unsigned)seed + i * 0x9E3779B9u, (unsigned)(seed >> 32) + i * 0xBB67AE85u);
+    t->offset = offset, t->counter = counter;
 }
 
 int check_factors(int act, float dropout, const unsigned long long* counter)
@@ -149,6 +152,7 @@ struct LinPlan {
     wg_linear_call call;
     int M, N, kb;             // columns of the result, rows (weight gradient), 64-wide blocks of the sum
     int bt, split, stages, stage_bytes, pairs;
+    bool few;                 // linear_rows_kernel
     bool pack_a, pack_b;      // operands that TMA cannot read
     long long part_rows, ldp;
     int sum_rows;             // rows of a partial sum of dbias
@@ -158,8 +162,17 @@ struct LinPlan {
 
 // Blocks of 64 per sum in tensor memory.  Truncation takes up to 0.95e-7 n of a sum of n
 // MMAs (16 terms each) of equal signs, a few times less of mixed ones: 6e-6 of an fp32
-// result's (n = 64), 1e-4 of a 16-bit one's (n = 1024), a fifth of fp16's rounding.
-constexpr int kChunkFp32 = 16, kChunk16 = 256;
+// result's (n = 64), 2e-4 of a 16-bit one's (n = 2048), 0.4 of fp16's rounding.
+constexpr int kChunkFp32 = 16, kChunk16 = 512;
+
+// Rows up to which the forward product is linear_rows_kernel's: eight at a time; 16 of one
+// weight matrix below 64 MB (4096 x 4096 for 9 rows 9.7 us against 14.1 on the tensor-core tiles,
+// 4096 x 16384 for 16 rows 31 against 25; 32 experts' 2048 x 1024 for 32 rows 24 against 26).
+constexpr int kFewRows = 16;
+bool few_rows(const wg_linear_problem& q)
+{
+    return q.tokens <= 8 || (q.tokens <= kFewRows && (q.experts > 1 || (long long)q.in * q.out < (32LL << 20)));
+}
 
 // us of a block of 64 of a tile's sum on every pair at once, by the tile's MMA columns
 // (measured on the update's products: 0.33 for 256, 0.27 for 128, L2 to shared memory being
@@ -201,6 +214,12 @@ int lin_plan(const wg_linear_problem* p, int call, LinPlan* pl)
         return set_err(WG_ERR_INVALID_ARGUMENT, "weight_stride makes experts' matrices overlap");
     if (q.weight_stride > kMaxSpan / ne) return set_err(WG_ERR_INVALID_ARGUMENT, "weight_stride is larger than any memory");
 
+    // Few rows: the forward product that reads the weights once, in one launch.
+    if (call == WG_LINEAR_FORWARD && few_rows(q)) {
+        pl->few = true;
+        pl->bytes = 256;
+        return WG_OK;
+    }
     pl->M = call == WG_LINEAR_FORWARD ? q.out : q.in;
     pl->N = weight ? q.out : 0;
     pl->kb = ((weight ? (int)std::min<long long>((q.tokens + ne - 1) / ne, 1 << 30) : data ? q.out : q.in) + 63) / 64;
@@ -242,9 +261,10 @@ int lin_plan(const wg_linear_problem* p, int call, LinPlan* pl)
     if (pl->pack_b) pl->off_b = o, o += packed(n, weight || data ? q.out : q.in);
     if (pl->split > 1) pl->off_part = o, o += up256((size_t)pl->split * pl->part_rows * pl->ldp * 4);
     if (weight) {
-        // Rows of a partial sum: some 1,000 blocks of them, of 64 to 1024 rows each.
+        // Rows of a partial sum: 64 for each of a block's eight rows of threads to have eight in
+        // flight, more where that is still two blocks for every place on the GPU.
         const long long cols = (q.out + 255) / 256;
-        pl->sum_rows = (int)std::max(64LL, std::min(1024LL, (q.tokens * cols / (6 * num_sms()) + 63) / 64 * 64));
+        pl->sum_rows = (int)std::max(64LL, std::min(512LL, q.tokens * cols / (12 * num_sms()) / 64 * 64));
         pl->sum_chunks = q.tokens / pl->sum_rows + ne + 1;
         pl->off_sum = o, o += up256((size_t)pl->sum_chunks * q.out * 4);
         pl->off_first = o, o += up256((size_t)(ne + 1) * 4);
@@ -346,6 +366,32 @@ int lin_run(const LinPlan& pl, const void* offsets, LinOperand a, LinOperand b, 
     }
 }
 
+template <int XR, int FG, bool WIDE>
+int rows_launch(const wg::RowsParams& g, bool bf16, cudaStream_t s)
+{
+    const long long items = (long long)std::max(1, std::min<int>(std::max(g.experts, 1), (int)g.tokens)) * ((g.M + 8 * FG - 1) / (8 * FG));
+    const dim3 grid((unsigned)std::min<long long>(items, 8LL * num_sms()));
+    return launch("linear_rows_kernel launch", bf16 ? wg::linear_rows_kernel<XR, FG, true, WIDE> : wg::linear_rows_kernel<XR, FG, false, WIDE>,
+                  grid, dim3(wg::kRowsThreads), s, g);
+}
+int rows_run(const LinPlan& pl, const void* offsets, const void* x, const void* w, const wg::LayerTail& tail, cudaStream_t s)
+{
+    const wg_linear_problem& q = pl.p;
+    wg::RowsParams g = {};
+    g.t = tail, g.experts = q.experts, g.offsets64 = q.offset_bits == 64, g.offsets = offsets, g.tokens = q.tokens;
+    g.x = x, g.w = w, g.ldx = q.ld_in, g.ldw = q.ld_weight, g.wstride = q.weight_stride, g.K = q.in, g.M = q.out;
+    const bool wide = q.in % 8 == 0 && q.ld_in % 8 == 0 && q.ld_weight % 8 == 0 && (q.experts <= 1 || q.weight_stride % 8 == 0) &&
+                      aligned16(x) && aligned16(w);
+    const bool bf16 = q.in_dtype == WG_BF16;
+    const bool one = q.tokens <= 8 || q.experts > 1;
+    if (!wide) return one ? rows_launch<1, 1, false>(g, bf16, s) : rows_launch<2, 1, false>(g, bf16, s);
+    if (!one) return rows_launch<2, 2, true>(g, bf16, s);
+    // 32 columns of the result per CTA where those are enough CTAs (8192 x 8192 23.5 us against 24.7
+    // with 16, 4096 x 16384 25.1 against 27.4), else 16 (4096 x 4096 9.2 against 11.7).
+    const long long wide_items = (q.out + 31) / 32 * std::min<long long>(std::max(q.experts, 1), q.tokens);
+    return 2 * wide_items >= 3 * num_sms() ? rows_launch<1, 4, true>(g, bf16, s) : rows_launch<1, 2, true>(g, bf16, s);
+}
+
 int lin_offsets(const LinPlan& pl, const void* offsets)
 {
     if ((pl.p.experts > 0) != (offsets != nullptr))
@@ -387,7 +433,7 @@ int act_plan(const wg_activation_problem* p, ActPlan* pl)
     const long long want = std::max(1LL, 12LL * num_sms() / cols);
     long long rows = std::max(ny, (q.tokens + want - 1) / want);
     rows = (rows + ny - 1) / ny * ny;
-    if (rows > ny) rows = (rows + wg::kActRows * ny - 1) / (wg::kActRows * ny) * (wg::kActRows * ny);
+    if (rows > ny) rows = (rows + 4 * ny - 1) / (4 * ny) * (4 * ny);  // (four rows in flight)
     rows = std::max(rows, ((q.tokens + 65534) / 65535 + ny - 1) / ny * ny);
     pl->chunk = (int)rows;
     pl->chunks = std::max(1LL, (q.tokens + rows - 1) / rows);
@@ -395,12 +441,20 @@ int act_plan(const wg_activation_problem* p, ActPlan* pl)
     return WG_OK;
 }
 
+template <bool BWD, int MODE>
+int act_launch_mode(const ActPlan& pl, const wg::ActParams& g, cudaStream_t s)
+{
+    const int groups = (pl.p.dim + 7) / 8;
+    return launch("activation_kernel launch", wg::activation_kernel<BWD, MODE>,
+                  dim3((unsigned)((groups + (1 << pl.cx_log) - 1) >> pl.cx_log), (unsigned)pl.chunks), dim3(wg::kActThreads), s, g);
+}
 template <bool BWD>
 int act_launch(const ActPlan& pl, const wg::ActParams& g, cudaStream_t s)
 {
-    const int groups = (pl.p.dim + 7) / 8;
-    return launch("activation_kernel launch", wg::activation_kernel<BWD>,
-                  dim3((unsigned)((groups + (1 << pl.cx_log) - 1) >> pl.cx_log), (unsigned)pl.chunks), dim3(wg::kActThreads), s, g);
+    const bool half = g.t.y_dtype != 2 && (!g.x || g.x_dtype != 2) && (!BWD || g.dy_dtype != 2);
+    const bool wide = (!g.x || g.vec_x) && (!BWD || g.vec_dy) && (!g.t.y || (g.t.vec & wg::kVecY)) && (!g.t.res || (g.t.vec & wg::kVecRes));
+    if (half && wide) return act_launch_mode<BWD, wg::kActWide>(pl, g, s);
+    return half && pl.cx_log == 5 ? act_launch_mode<BWD, wg::kActShifted>(pl, g, s) : act_launch_mode<BWD, wg::kActAny>(pl, g, s);
 }
 
 wg::ActParams act_params(const ActPlan& pl, const void* x, const void* bias)
@@ -435,6 +489,10 @@ int wg_linear_plan_string(const wg_linear_problem* p, wg_linear_call call, char*
     LinPlan pl;
     const int st = lin_plan(p, call, &pl);
     if (st) return st;
+    if (pl.few) {
+        snprintf(buf, n, "kernel=linear_rows call=forward ws=%zu", pl.bytes);
+        return WG_OK;
+    }
     static const char* const kNames[3] = {"forward", "bwd_data", "bwd_weight"};
     snprintf(buf, n, "kernel=linear_product call=%s columns=%d rows=%d split=%d stages=%d pairs=%d pack=%d%d smem=%d ws=%zu",
              kNames[pl.call], 256, pl.bt, pl.split, pl.stages, pl.pairs, pl.pack_a, pl.pack_b, wg::kLinSmem, pl.bytes);
@@ -473,6 +531,7 @@ int wg_linear(const wg_linear_problem* p, const void* offsets, const void* x, co
     if (pair_rows(residual, q.ld_residual, q.out, oe)) g.vec |= wg::kPairRes;
     if (vec_rows(bias, q.out, q.out, be)) g.vec |= wg::kVecBias;
     set_dropout(&g, q.dropout, q.seed, q.offset, q.counter);
+    if (pl.few) return rows_run(pl, offsets, x, w, g, static_cast<cudaStream_t>(stream));
     return lin_run(pl, offsets, {w, q.out, q.in, q.ld_weight, ne, q.weight_stride}, {x, q.tokens, q.in, q.ld_in, 1, 0}, g,
                    static_cast<char*>(workspace), static_cast<cudaStream_t>(stream));
 }
@@ -532,6 +591,7 @@ int wg_linear_bwd_weight(const wg_linear_problem* p, const void* offsets, const 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     wg::LayerTail g = {};
     g.y = dw, g.y_dtype = q.out_dtype, g.ldy = q.ld_weight, g.y_stride = q.weight_stride;
+    g.gain = 1.f;
     if (accumulate) g.res = dw, g.ldr = q.ld_weight;
     if (vec_rows(dw, q.ld_weight, q.in, oe, ne > 1 ? q.weight_stride : 0)) g.vec |= wg::kVecY | wg::kVecRes;
     if (pair_rows(dw, q.ld_weight, q.in, oe, ne > 1 ? q.weight_stride : 0)) g.vec |= wg::kPairY | wg::kPairRes;
@@ -543,8 +603,9 @@ int wg_linear_bwd_weight(const wg_linear_problem* p, const void* offsets, const 
     c.part = reinterpret_cast<float*>(ws + pl.off_sum), c.first = reinterpret_cast<int*>(ws + pl.off_first);
     const int groups = (q.out + 7) / 8;
     c.cx_log = std::min(5, log2_floor(groups) + ((groups & (groups - 1)) ? 1 : 0));
+    const long long cols = (groups + (1 << c.cx_log) - 1) >> c.cx_log;
     st = launch("column_sum_kernel launch", wg::column_sum_kernel,
-                dim3((unsigned)((groups + (1 << c.cx_log) - 1) >> c.cx_log), (unsigned)std::max(1LL, std::min(pl.sum_chunks, 65535LL))),
+                dim3((unsigned)cols, (unsigned)std::max(1LL, std::min(pl.sum_chunks, (6LL * num_sms() + cols - 1) / cols))),
                 dim3(256), s, c);
     if (st) return st;
     wg::SumParams m = {};

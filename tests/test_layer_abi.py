@@ -155,6 +155,9 @@ def test_plans_of_random_problems():
         sp = lin(tokens=log(1 << 20), in_=log(1 << 15), out=log(1 << 15), experts=rng.choice([0, 0, log(1024)]))
         for call in CALLS:
             plan = dict(v.split("=") for v in binding.wg_linear_plan_string(sp, call).split())
+            if plan["kernel"] == "linear_rows":
+                assert call == "forward" and sp["tokens"] <= 16
+                continue
             rows, split, stages = int(plan["rows"]), int(plan["split"]), int(plan["stages"])
             assert rows % 32 == 0 and 32 <= rows <= 256 and 1 <= split <= 16 and 2 <= stages <= 12
             cols = sp["out"] if call == "forward" else sp["in"]
