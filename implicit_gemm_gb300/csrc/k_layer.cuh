@@ -70,20 +70,20 @@ __device__ __forceinline__ unsigned long long layer_offset(const LayerTail& t)
 }
 
 // ---------------------------------------------------------------- activations
-__device__ __forceinline__ float sigmoid_f(float a) { return __fdividef(1.f, 1.f + __expf(-a)); }
-
-// gelu's tanh form is v sigmoid(2 u): (1 + tanh u) / 2 is sigmoid(2 u).  (__expf is off by
-// some 2^-24 |a| of itself beyond its last places, and 1 + exp(-a) is that near 1 wherever
-// the result is not small beside v.  __fdividef gives 0 for divisors above 2^126, where
-// the quotient is below 2^-126.)
-// Squares are held below 1e10, where every sigmoid has long been 0 or 1, so that no 0 meets
-// an infinity.
-__device__ __forceinline__ float square_f(float v) { return fminf(v * v, 1e10f); }
-__device__ __forceinline__ float gelu_2u(float v) { return v * fmaf(0.0713548162726f, square_f(v), 1.59576912161f); }
-
-// The normal distribution's tails by Abramowitz and Stegun's 7.1.26 (Hastings, 1955):
-// erfc(x) = t (a1 + ... + a5 t^4) exp(-x^2), t = 1 / (1 + p x), off by 1.5e-7 at most, in a third
-// of erff's instructions (instructions are what bounds the activation alone).
+// The hardware's reciprocal and power of two, each one instruction (2^-23 or so of the result;
+// numbers below 2^-126 count as zeros, an infinity's reciprocal is 0).
+__device__ __forceinline__ float rcp_f(float a)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
+    return r;
+}
+__device__ __forceinline__ float exp2_f(float a)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
+    return r;
+}
 // Two values at a time: fp32 operations on pairs issue once.
 struct F2 {
     uint64_t v;
@@ -107,8 +107,37 @@ __device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c)
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
     return r;
 }
-__device__ __forceinline__ float rcp_f(float a) { return __fdividef(1.f, a); }
+__device__ __forceinline__ F2 both(float a) { return f2(a, a); }
+__device__ __forceinline__ F2 add(F2 a, F2 b)
+{
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
 
+// 1 / (1 + exp(-a)).
+__device__ __forceinline__ F2 sigmoid2(F2 a)
+{
+    float x, y;
+    split(mul(a, both(-1.4426950408889634f)), x, y);
+    split(add(f2(exp2_f(x), exp2_f(y)), both(1.f)), x, y);
+    return f2(rcp_f(x), rcp_f(y));
+}
+
+// gelu's tanh form is v sigmoid(2 u): (1 + tanh u) / 2 is sigmoid(2 u).  (The exponential is off by
+// some 2^-24 |a| of itself beyond its last places, and 1 + exp(-a) is that near 1 wherever
+// the result is not small beside v.)  Squares are held below 1e10, where every sigmoid has
+// long been 0 or 1, so that no 0 meets an infinity.
+__device__ __forceinline__ F2 square2(F2 v)
+{
+    float x, y;
+    split(mul(v, v), x, y);
+    return f2(fminf(x, 1e10f), fminf(y, 1e10f));
+}
+
+// The normal distribution's tails by Abramowitz and Stegun's 7.1.26 (Hastings, 1955):
+// erfc(x) = t (a1 + ... + a5 t^4) exp(-x^2), t = 1 / (1 + p x), off by 1.5e-7 at most, in a third
+// of erff's instructions (instructions are what bounds the activation alone).
 // q = erfc(|v| / sqrt 2) / 2 and e = exp(-v^2 / 2) of a pair.
 __device__ __forceinline__ F2 tails(float a, float b, F2& e)
 {
@@ -117,7 +146,7 @@ __device__ __forceinline__ F2 tails(float a, float b, F2& e)
     float d0, d1, g0, g1;
     split(d, d0, d1), split(g, g0, g1);
     const F2 t = f2(rcp_f(d0), rcp_f(d1));
-    e = f2(exp2f(g0), exp2f(g1));
+    e = f2(exp2_f(g0), exp2_f(g1));
     F2 q = fma(t, f2(0.5f * 1.061405429f, 0.5f * 1.061405429f), f2(0.5f * -1.453152027f, 0.5f * -1.453152027f));
     q = fma(t, q, f2(0.5f * 1.421413741f, 0.5f * 1.421413741f));
     q = fma(t, q, f2(0.5f * -0.284496736f, 0.5f * -0.284496736f));
@@ -144,66 +173,91 @@ __device__ __forceinline__ void gelu_slope2(float& a, float& b)
     b = (b < 0.f ? q1 : 1.f - q1) + p1;
 }
 
-template <int ACT>
-__device__ __forceinline__ float act_f(float v)
+// The activation of each of a pair.
+__device__ __forceinline__ F2 gelu2(F2 v)
 {
-    if (ACT == kActRelu) return v < 0.f ? 0.f : v;
-    if (ACT == kActGeluTanh) return v * sigmoid_f(gelu_2u(v));
-    if (ACT == kActSilu) return v * sigmoid_f(v);
-    return v;
+    float a, b;
+    split(v, a, b);
+    gelu2(a, b);
+    return f2(a, b);
 }
-
-template <int ACT>
-__device__ __forceinline__ float slope_f(float v)
+__device__ __forceinline__ F2 gelu_tanh2(F2 v) { return mul(v, sigmoid2(mul(v, fma(both(0.0713548162726f), square2(v), both(1.59576912161f))))); }
+__device__ __forceinline__ F2 silu2(F2 v) { return mul(v, sigmoid2(v)); }
+// Its slope: of v sigmoid(w), s (1 + v w' (1 - s)).
+__device__ __forceinline__ F2 gelu_slope2(F2 v)
 {
-    if (ACT == kActGeluTanh) {
-        const float s = sigmoid_f(gelu_2u(v));  // d(2u)/dv = 1.5957... + 3 * 0.0713... v^2
-        return fmaf(v * s * (1.f - s), fmaf(0.2140644488178f, square_f(v), 1.59576912161f), s);
-    }
-    if (ACT == kActSilu) {
-        const float s = sigmoid_f(v);
-        return s * fmaf(v, 1.f - s, 1.f);
-    }
-    return 1.f;
+    float a, b;
+    split(v, a, b);
+    gelu_slope2(a, b);
+    return f2(a, b);
+}
+__device__ __forceinline__ F2 gelu_tanh_slope2(F2 v)
+{
+    const F2 q = square2(v), s = sigmoid2(mul(v, fma(both(0.0713548162726f), q, both(1.59576912161f))));
+    const F2 r = mul(mul(v, s), fma(s, both(-1.f), both(1.f)));
+    return fma(r, fma(both(0.2140644488178f), q, both(1.59576912161f)), s);
+}
+__device__ __forceinline__ F2 silu_slope2(F2 v)
+{
+    const F2 s = sigmoid2(v);
+    return mul(s, fma(v, fma(s, both(-1.f), both(1.f)), both(1.f)));
 }
 
 __device__ __forceinline__ void act8(int act, float (&v)[8])
 {
-#define WG_EACH(A)                                     \
-    _Pragma("unroll") for (int i = 0; i < 8; ++i) v[i] = act_f<A>(v[i]);
+#define WG_EACH(F)                                  \
+    _Pragma("unroll") for (int i = 0; i < 8; i += 2) \
+    {                                               \
+        split(F(f2(v[i], v[i + 1])), v[i], v[i + 1]); \
+    }
     if (act == kActRelu) {
-        WG_EACH(kActRelu)
-    } else if (act == kActGelu) {
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) gelu2(v[i], v[i + 1]);
+        for (int i = 0; i < 8; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];
+    } else if (act == kActGelu) {
+        WG_EACH(gelu2)
     } else if (act == kActGeluTanh) {
-        WG_EACH(kActGeluTanh)
+        WG_EACH(gelu_tanh2)
     } else if (act == kActSilu) {
-        WG_EACH(kActSilu)
+        WG_EACH(silu2)
     }
 #undef WG_EACH
 }
 // v times the activation's slope at z.
 __device__ __forceinline__ void slope8(int act, const float (&z)[8], float (&v)[8])
 {
-#define WG_EACH(A)                                     \
-    _Pragma("unroll") for (int i = 0; i < 8; ++i) v[i] *= slope_f<A>(z[i]);
+#define WG_EACH(F)                                                                      \
+    _Pragma("unroll") for (int i = 0; i < 8; i += 2)                                     \
+    {                                                                                   \
+        split(mul(f2(v[i], v[i + 1]), F(f2(z[i], z[i + 1]))), v[i], v[i + 1]);            \
+    }
     if (act == kActRelu) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = z[i] <= 0.f ? 0.f : v[i];
     } else if (act == kActGelu) {
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            float a = z[i], b = z[i + 1];
-            gelu_slope2(a, b);
-            v[i] *= a, v[i + 1] *= b;
-        }
+        WG_EACH(gelu_slope2)
     } else if (act == kActGeluTanh) {
-        WG_EACH(kActGeluTanh)
+        WG_EACH(gelu_tanh_slope2)
     } else if (act == kActSilu) {
-        WG_EACH(kActSilu)
+        WG_EACH(silu_slope2)
     }
 #undef WG_EACH
+}
+
+// v * gain + x of eight.
+__device__ __forceinline__ void gain8(float gain, const float (&x)[8], float (&v)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) split(fma(f2(v[i], v[i + 1]), both(gain), f2(x[i], x[i + 1])), v[i], v[i + 1]);
+}
+__device__ __forceinline__ void gain8(float gain, float (&v)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) split(mul(f2(v[i], v[i + 1]), both(gain)), v[i], v[i + 1]);
+}
+__device__ __forceinline__ void add8(const float (&x)[8], float (&v)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) split(add(f2(v[i], v[i + 1]), f2(x[i], x[i + 1])), v[i], v[i + 1]);
 }
 
 // ---------------------------------------------------------------- eight elements of a row
@@ -337,11 +391,9 @@ __device__ __forceinline__ void tail_write(const LayerTail& t, unsigned long lon
     if (KIND != kWeight && t.thr) drop8(t, offset, row, col >> 3, v);
     if (t.res) {
         unpack8(r.res, t.y_dtype, x);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = fmaf(v[i], t.gain, x[i]);
+        gain8(t.gain, x, v);
     } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= t.gain;
+        gain8(t.gain, v);
     }
     store8(t.y, (KIND == kWeight ? expert * t.y_stride : 0) + row * t.ldy + col, t.y_dtype, t.vec & kVecY, n, v);
 }
@@ -676,8 +728,7 @@ __global__ void __launch_bounds__(kActThreads, MODE == kActAny ? 2 : 3) activati
                 float v[8], z[8];
                 if (p.x) {
                     act_unpack<MODE>(x[i], p.x_dtype, z);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) z[k] += bias[k];
+                    add8(bias, z);
                 }
                 if (BWD) {
                     act_unpack<MODE>(o[i], p.dy_dtype, v);
@@ -690,11 +741,9 @@ __global__ void __launch_bounds__(kActThreads, MODE == kActAny ? 2 : 3) activati
                 if (t.thr) drop8(t, offset, r, col >> 3, v);
                 if (!BWD && t.res) {
                     act_unpack<MODE>(o[i], t.y_dtype, z);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) v[k] = fmaf(v[k], t.gain, z[k]);
+                    gain8(t.gain, z, v);
                 } else {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) v[k] *= t.gain;
+                    gain8(t.gain, v);
                 }
                 if (t.y) {
                     if (MODE == kActAny) {
@@ -709,9 +758,7 @@ __global__ void __launch_bounds__(kActThreads, MODE == kActAny ? 2 : 3) activati
                             store_shifted(b + 2 * (uintptr_t)col, b + 2 * (uintptr_t)p.dim, w);
                     }
                 }
-                if (BWD)
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) sum[k] += v[k];
+                if (BWD) add8(v, sum);
             }
         }
     }
