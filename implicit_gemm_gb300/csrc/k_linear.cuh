@@ -736,23 +736,22 @@ __global__ void __launch_bounds__(kRowsThreads, 2) linear_rows_kernel(const __gr
 }
 
 // ---------------------------------------------------------------- operands that TMA cannot read
-// Rows of 16-bit elements that start anywhere, copied to rows of whole 16-byte chunks.
+// Rows of 16-bit elements that start anywhere, copied to rows of whole 16-byte chunks: a warp
+// per row and 256 columns.  (What comes after a row's last column may be anything: TMA gives
+// zeros there.)
 __global__ void __launch_bounds__(256) linear_pack_kernel(const unsigned short* in, unsigned short* out, long long rows, int batch,
                                                           int cols, long long ld, long long bs, int ldp)
 {
     pdl_launch_dependents();
     pdl_wait();
-    const int groups = ldp / 8;
-    const long long total = rows * batch * groups, step = (long long)gridDim.x * blockDim.x;
-    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += step) {
-        const long long r = i / groups, b = r / rows;
-        const int j = 8 * (int)(i - r * groups);
-        const unsigned short* s = in + b * bs + (r - b * rows) * ld + j;
-        uint32_t h[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) h[k] = j + k < cols ? s[k] : 0;
-        *reinterpret_cast<uint4*>(out + r * ldp + j) =
-            make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+    const int lane = threadIdx.x & 31, segments = (cols + 255) / 256;
+    const long long total = rows * batch * segments, step = (long long)gridDim.x * (blockDim.x / 32);
+    for (long long i = (long long)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; i < total; i += step) {
+        const long long r = i / segments, b = batch > 1 ? r / rows : 0;
+        const int j = 256 * (int)(i - r * segments) + 8 * lane;
+        const uintptr_t row = reinterpret_cast<uintptr_t>(in + b * bs + (r - b * rows) * ld);
+        const uint4 v = load_shifted(row + 2 * (uintptr_t)j, row + 2 * (uintptr_t)cols);
+        if (j < cols) *reinterpret_cast<uint4*>(out + r * ldp + j) = v;
     }
 }
 

@@ -299,9 +299,9 @@ struct LinOperand {
 int lin_pack(LinOperand* o, char* to, cudaStream_t s)
 {
     const int ldp = (o->cols + 7) / 8 * 8;
-    const long long items = o->rows * o->batch * (ldp / 8);
+    const long long warps = o->rows * o->batch * ((o->cols + 255) / 256);
     const int st = launch("linear_pack_kernel launch", wg::linear_pack_kernel,
-                          dim3((unsigned)std::max(1LL, std::min<long long>((items + 255) / 256, 16LL * num_sms()))), dim3(256), s,
+                          dim3((unsigned)std::max(1LL, std::min<long long>((warps + 7) / 8, 8LL * num_sms()))), dim3(256), s,
                           static_cast<const unsigned short*>(o->p), reinterpret_cast<unsigned short*>(to), o->rows, (int)o->batch,
                           o->cols, o->ld, o->bs, ldp);
     o->p = to, o->ld = ldp, o->bs = o->rows * ldp;
