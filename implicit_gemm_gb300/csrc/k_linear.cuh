@@ -52,6 +52,22 @@ constexpr int kLinABytes = 16384;
 constexpr int kLinSmem = 227 * 1024;
 constexpr int kLinRing = (kLinSmem - 2 * 4 * (kLinMaxExperts + 4) - 512 - 1024) / 1024 * 1024;
 
+// Division of numbers below 2^31 by a number that the host knows.  (A division as the kernel runs
+// is some twenty instructions one after another; five of them were 1 us before the first load.)
+struct FastDiv {
+    unsigned mul, shift;
+};
+inline FastDiv fast_div(unsigned d)
+{
+    FastDiv f;
+    unsigned bits = 0;
+    while ((1ull << bits) < d) ++bits;
+    f.shift = 31 + bits;
+    f.mul = (unsigned)(((1ull << f.shift) + d - 1) / d);
+    return f;
+}
+__device__ __forceinline__ int div_by(int n, const FastDiv& f) { return (int)(((uint64_t)(unsigned)n * f.mul) >> f.shift); }
+
 struct LinParams {
     LayerTail t;
     int experts;            // 0: one weight, every row
@@ -62,9 +78,11 @@ struct LinParams {
     int kb;                 // 64-wide blocks of the sum (not kWeight)
     int bf16;
     int bt;                 // most MMA columns of a tile
+    FastDiv by_bt, by_im, by_8im, by_per;  // im: tiles along the columns; per: tiles of an expert (kWeight)
     int stages, stage_bytes;
     int chunk;              // blocks per sum in tensor memory
     int split, pairs;
+    int early;              // the kernel before has waited for those before it, and nothing here is its result
     float* part;            // [split][rows][ldp] sums of parts (split > 1)
     long long ldp, part_rows;
 };
@@ -135,10 +153,10 @@ struct LinTile {
 };
 
 // n rows in tiles of at most bt: as even as steps of 32 allow.
-__device__ __forceinline__ void lin_width(int n, int bt, int& tiles, int& width)
+__device__ __forceinline__ void lin_width(int n, const LinParams& p, int& tiles, int& width)
 {
-    tiles = (n + bt - 1) / bt;
-    width = tiles ? ((n + tiles - 1) / tiles + 31) / 32 * 32 : 32;
+    tiles = div_by(n + p.bt - 1, p.by_bt);
+    width = tiles > 1 ? ((n + tiles - 1) / tiles + 31) / 32 * 32 : max(32, (n + 31) / 32 * 32);
 }
 
 template <int KIND>
@@ -151,7 +169,7 @@ struct LinWalk {
         : p(p_), off(off_), first(first_), im((p_.M + 255) / 256), item(pair)
     {
         if (KIND == kWeight) {
-            lin_width(p.N, p.bt, tiles, width);
+            lin_width(p.N, p, tiles, width);
             total = max(p.experts, 1) * im * tiles * p.split;
         } else {
             total = first[max(p.experts, 1)] * im * p.split;
@@ -168,7 +186,7 @@ struct LinWalk {
         if (KIND == kWeight) {
             n = p.N;
             if (p.experts > 1) {
-                t.e = i / (im * tiles);
+                t.e = div_by(i, p.by_per);
                 i -= t.e * im * tiles;
             }
             t.row0 = off[t.e];
@@ -177,16 +195,16 @@ struct LinWalk {
             t.valid = rows & 63 ? rows & 63 : 64;
         } else {
             if (p.experts > 1) {
-                t.e = find_last(first, p.experts, i / im);
+                t.e = find_last(first, p.experts, div_by(i, p.by_im));
                 i -= first[t.e] * im;
             }
             n = off[t.e + 1] - off[t.e];
-            lin_width(n, p.bt, tiles, width);
+            lin_width(n, p, tiles, width);
         }
         // Eight tiles along the rows, then the columns: what the pairs work on at one time
         // is about as many rows' operands as columns'.
-        const int g = i / (8 * im), gs = min(8, tiles - 8 * g), in = i - 8 * g * im;
-        const int c = gs == 8 ? in >> 3 : in / gs, j = 8 * g + in - c * gs;
+        const int g = div_by(i, p.by_8im), gs = min(8, tiles - 8 * g), in = i - 8 * g * im;
+        const int c = gs == 8 ? in >> 3 : gs == 1 ? in : in / gs, j = 8 * g + in - c * gs;
         t.m = 256 * c;
         t.n = j * width;
         t.rows = min(width, n - t.n);
@@ -282,7 +300,7 @@ __global__ void __launch_bounds__(lin_threads(CHUNKED), 1)
         tmem_alloc_pair(tslot, 512);
         tc_fence_before();
     }
-    if (p.experts) pdl_wait();  // the offsets may be the result of the kernel before
+    if (p.experts && !p.early) pdl_wait();  // the offsets may be the result of the kernel before
     load_offsets(p.experts, p.offsets, p.offsets64, p.tokens, off);
     if (KIND != kWeight) {
         if (warp == 0) {
@@ -290,7 +308,7 @@ __global__ void __launch_bounds__(lin_threads(CHUNKED), 1)
             int run = 0;
             for (int i0 = 0; i0 < n; i0 += 32) {
                 int tiles = 0, width;
-                if (i0 + lane < n) lin_width(off[i0 + lane + 1] - off[i0 + lane], p.bt, tiles, width);
+                if (i0 + lane < n) lin_width(off[i0 + lane + 1] - off[i0 + lane], p, tiles, width);
                 int s = tiles;
 #pragma unroll
                 for (int d = 1; d < 32; d *= 2) {
@@ -316,7 +334,7 @@ __global__ void __launch_bounds__(lin_threads(CHUNKED), 1)
                 int st = 0;
                 uint32_t ph = 0;
                 bool ok = true, more = walk.next(t);
-                if (!p.experts) pdl_wait();
+                if (!p.experts && !p.early) pdl_wait();
                 for (; ok && more; more = walk.next(t)) {
                     const int m0 = t.m + rank * 128, n0 = t.n + rank * (t.wide >> 1);
                     for (int k = t.k0; k < t.k1; ++k) {
@@ -436,7 +454,7 @@ __global__ void __launch_bounds__(lin_threads(CHUNKED), 1)
         const uint32_t trow = tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)first_row;
         int use = 0;
         bool ok = true, more = walk.next(t);
-        if (!p.experts) pdl_wait();
+        if (!p.experts && !p.early) pdl_wait();
         const unsigned long long offset = layer_offset(p.t);
         for (; ok && more; more = walk.next(t)) {
             const int j = t.m + rank * 128 + q * 32 + lane;
@@ -525,6 +543,9 @@ __global__ void __launch_bounds__(lin_threads(CHUNKED), 1)
             }
         }
     }
+    // (This one is complete only after the one before it: the next waits for this one alone.)
+    if (p.early && threadIdx.x == 0) pdl_wait();
+    __syncwarp();
     // Neither CTA releases tensor memory or leaves while the other may still use it.
     tc_fence_before();
     cluster_sync_all();
@@ -739,19 +760,29 @@ __global__ void __launch_bounds__(kRowsThreads, 2) linear_rows_kernel(const __gr
 // Rows of 16-bit elements that start anywhere, copied to rows of whole 16-byte chunks: a warp
 // per row and 256 columns.  (What comes after a row's last column may be anything: TMA gives
 // zeros there.)
-__global__ void __launch_bounds__(256) linear_pack_kernel(const unsigned short* in, unsigned short* out, long long rows, int batch,
-                                                          int cols, long long ld, long long bs, int ldp)
+struct PackParams {
+    const unsigned short* in;
+    unsigned short* out;
+    long long rows, ld, bs;
+    int batch, cols, ldp;
+    long long segments;  // rows by 256 columns, of all
+};
+__global__ void __launch_bounds__(256) linear_pack_kernel(const __grid_constant__ PackParams a, const __grid_constant__ PackParams b)
 {
     pdl_launch_dependents();
     pdl_wait();
-    const int lane = threadIdx.x & 31, segments = (cols + 255) / 256;
-    const long long total = rows * batch * segments, step = (long long)gridDim.x * (blockDim.x / 32);
-    for (long long i = (long long)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; i < total; i += step) {
-        const long long r = i / segments, b = batch > 1 ? r / rows : 0;
-        const int j = 256 * (int)(i - r * segments) + 8 * lane;
-        const uintptr_t row = reinterpret_cast<uintptr_t>(in + b * bs + (r - b * rows) * ld);
-        const uint4 v = load_shifted(row + 2 * (uintptr_t)j, row + 2 * (uintptr_t)cols);
-        if (j < cols) *reinterpret_cast<uint4*>(out + r * ldp + j) = v;
+    const int lane = threadIdx.x & 31;
+    const long long step = (long long)gridDim.x * (blockDim.x / 32);
+    for (long long i = (long long)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; i < a.segments + b.segments; i += step) {
+        const bool first = i < a.segments;
+        const PackParams& p = first ? a : b;
+        const long long n = first ? i : i - a.segments;
+        const int per = (p.cols + 255) / 256;
+        const long long r = n / per, m = p.batch > 1 ? r / p.rows : 0;
+        const int j = 256 * (int)(n - r * per) + 8 * lane;
+        const uintptr_t row = reinterpret_cast<uintptr_t>(p.in + m * p.bs + (r - m * p.rows) * p.ld);
+        const uint4 v = load_shifted(row + 2 * (uintptr_t)j, row + 2 * (uintptr_t)p.cols);
+        if (j < p.cols) *reinterpret_cast<uint4*>(p.out + r * p.ldp + j) = v;
     }
 }
 
@@ -772,8 +803,8 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const __grid_constant__
 {
     __shared__ int off[kLinMaxExperts + 1], first[kLinMaxExperts + 1];
     __shared__ float s[8][256];
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();  // (after the wait: see LinParams::early)
     load_offsets(p.experts, p.offsets, p.offsets64, p.tokens, off);
     const int n = max(p.experts, 1);
     if (threadIdx.x < 32) {

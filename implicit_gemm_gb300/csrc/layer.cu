@@ -296,16 +296,12 @@ struct LinOperand {
     int cols;
     long long ld, batch, bs;
 };
-int lin_pack(LinOperand* o, char* to, cudaStream_t s)
+wg::PackParams lin_pack(LinOperand* o, char* to)
 {
-    const int ldp = (o->cols + 7) / 8 * 8;
-    const long long warps = o->rows * o->batch * ((o->cols + 255) / 256);
-    const int st = launch("linear_pack_kernel launch", wg::linear_pack_kernel,
-                          dim3((unsigned)std::max(1LL, std::min<long long>((warps + 7) / 8, 8LL * num_sms()))), dim3(256), s,
-                          static_cast<const unsigned short*>(o->p), reinterpret_cast<unsigned short*>(to), o->rows, (int)o->batch,
-                          o->cols, o->ld, o->bs, ldp);
-    o->p = to, o->ld = ldp, o->bs = o->rows * ldp;
-    return st;
+    wg::PackParams k = {static_cast<const unsigned short*>(o->p), reinterpret_cast<unsigned short*>(to), o->rows, o->ld, o->bs,
+                        (int)o->batch, o->cols, (o->cols + 7) / 8 * 8, o->rows * o->batch * ((o->cols + 255) / 256)};
+    o->p = to, o->ld = k.ldp, o->bs = o->rows * k.ldp;
+    return k;
 }
 
 template <int KIND, bool CHUNKED>
@@ -335,26 +331,46 @@ int lin_launch(const LinPlan& pl, const wg::LinParams& g, const LinOperand& a, c
                   dim3((unsigned)std::min<long long>((items + 255) / 256, 8LL * num_sms())), dim3(256), s, g);
 }
 
-// w, or x of the weight gradient, is operand a (MMA rows); the other operand b.
-int lin_run(const LinPlan& pl, const void* offsets, LinOperand a, LinOperand b, const wg::LayerTail& tail, char* ws, cudaStream_t s)
+int columns_launch(const wg::ColumnParams& c, const LinPlan& pl, cudaStream_t s)
+{
+    const int groups = (c.N + 7) / 8;
+    const long long cols = (groups + (1 << c.cx_log) - 1) >> c.cx_log;
+    return launch("column_sum_kernel launch", wg::column_sum_kernel,
+                  dim3((unsigned)cols, (unsigned)std::max(1LL, std::min(pl.sum_chunks, (6LL * num_sms() + cols - 1) / cols))), dim3(256), s, c);
+}
+
+// w, or x of the weight gradient, is operand a (MMA rows); the other operand b.  sums: dbias's partial sums,
+// made before the product, which need not wait for them.
+int lin_run(const LinPlan& pl, const void* offsets, LinOperand a, LinOperand b, const wg::LayerTail& tail, char* ws, cudaStream_t s,
+            const wg::ColumnParams* sums = nullptr)
 {
     const wg_linear_problem& q = pl.p;
     if (!pl.pack_a && !aligned16(a.p)) return set_err(WG_ERR_MISALIGNED, "x, w or dy with 16-byte strides must be 16-byte aligned");
     if (!pl.pack_b && !aligned16(b.p)) return set_err(WG_ERR_MISALIGNED, "x, w or dy with 16-byte strides must be 16-byte aligned");
     int st = WG_OK;
     if (q.tokens > 0) {
-        if (pl.pack_a) st = lin_pack(&a, ws + pl.off_a, s);
-        if (!st && pl.pack_b) st = lin_pack(&b, ws + pl.off_b, s);
-        if (st) return st;
+        wg::PackParams ka = {}, kb = {};
+        if (pl.pack_a) ka = lin_pack(&a, ws + pl.off_a);
+        if (pl.pack_b) kb = lin_pack(&b, ws + pl.off_b);
+        const long long segments = ka.segments + kb.segments;
+        if (segments > 0)
+            st = launch("linear_pack_kernel launch", wg::linear_pack_kernel,
+                        dim3((unsigned)std::min<long long>((segments + 7) / 8, 8LL * num_sms())), dim3(256), s, ka, kb);
     } else {
         a.p = b.p = ws, a.ld = b.ld = 8LL * (kMaxFeatures / 8), a.rows = b.rows = 1, a.batch = 1, a.bs = a.ld;  // (never read)
     }
+    if (!st && sums) st = columns_launch(*sums, pl, s);
+    if (st) return st;
     wg::LinParams g = {};
     g.t = tail;
+    g.early = sums != nullptr;
     g.experts = q.experts, g.offsets = offsets, g.offsets64 = q.offset_bits == 64, g.tokens = q.tokens;
     g.M = pl.M, g.N = pl.N, g.kb = pl.kb, g.bf16 = q.in_dtype == WG_BF16;
     g.chunk = q.out_dtype == WG_FP32 ? kChunkFp32 : kChunk16;
     g.bt = pl.bt, g.stages = pl.stages, g.stage_bytes = pl.stage_bytes, g.split = pl.split, g.pairs = pl.pairs;
+    const unsigned im = (unsigned)(pl.M + 255) / 256;
+    g.by_bt = wg::fast_div((unsigned)pl.bt), g.by_im = wg::fast_div(im), g.by_8im = wg::fast_div(8 * im);
+    g.by_per = wg::fast_div(im * (unsigned)((std::max(pl.N, 1) + pl.bt - 1) / pl.bt));
     g.part = reinterpret_cast<float*>(ws + pl.off_part), g.ldp = pl.ldp, g.part_rows = pl.part_rows;
     // Blocks of the longest sum (a part's, or an expert's that has every row).
     const long long blocks = pl.call == WG_LINEAR_BWD_WEIGHT ? (q.tokens + 63) / 64 : pl.kb;
@@ -595,19 +611,14 @@ int wg_linear_bwd_weight(const wg_linear_problem* p, const void* offsets, const 
     if (accumulate) g.res = dw, g.ldr = q.ld_weight;
     if (vec_rows(dw, q.ld_weight, q.in, oe, ne > 1 ? q.weight_stride : 0)) g.vec |= wg::kVecY | wg::kVecRes;
     if (pair_rows(dw, q.ld_weight, q.in, oe, ne > 1 ? q.weight_stride : 0)) g.vec |= wg::kPairY | wg::kPairRes;
-    st = lin_run(pl, offsets, {x, q.tokens, q.in, q.ld_in, 1, 0}, {dy, q.tokens, q.out, q.ld_out, 1, 0}, g, ws, s);
-    if (st || !dbias) return st;
     wg::ColumnParams c = {};
     c.dy = dy, c.tokens = q.tokens, c.ld = q.ld_out, c.N = q.out, c.dtype = q.in_dtype, c.vec = vec_rows(dy, q.ld_out, q.out, ie);
     c.experts = q.experts, c.offsets64 = q.offset_bits == 64, c.offsets = offsets, c.chunk = pl.sum_rows;
     c.part = reinterpret_cast<float*>(ws + pl.off_sum), c.first = reinterpret_cast<int*>(ws + pl.off_first);
     const int groups = (q.out + 7) / 8;
     c.cx_log = std::min(5, log2_floor(groups) + ((groups & (groups - 1)) ? 1 : 0));
-    const long long cols = (groups + (1 << c.cx_log) - 1) >> c.cx_log;
-    st = launch("column_sum_kernel launch", wg::column_sum_kernel,
-                dim3((unsigned)cols, (unsigned)std::max(1LL, std::min(pl.sum_chunks, (6LL * num_sms() + cols - 1) / cols))),
-                dim3(256), s, c);
-    if (st) return st;
+    st = lin_run(pl, offsets, {x, q.tokens, q.in, q.ld_in, 1, 0}, {dy, q.tokens, q.out, q.ld_out, 1, 0}, g, ws, s, dbias ? &c : nullptr);
+    if (st || !dbias) return st;
     wg::SumParams m = {};
     m.part = c.part, m.out = dbias, m.dim = q.out, m.dtype = q.bias_dtype, m.accumulate = accumulate != 0;
     m.first = c.first;
