@@ -3,11 +3,13 @@
     python examples/conv_lm_step.py [--steps 30]
 
 Tokens are looked up (wg_embedding_lookup), pass through residual blocks of a causal 1-D convolution, and are scored
-against the same table.  Per step the library computes each convolution's weight gradient (wg_conv_bwd_weight) and
-input gradient (wg_conv_bwd_data), the table's gradient (wg_embedding_bwd_weight, added to what the scores leave
-there), and the convolutions' orthogonalised update (wg_muon_update: momentum, Newton-Schulz products, weights).  torch
-computes what the library has no operator for: the convolutions' forward pass, the activations, the scores and the
-loss.  The data are sequences in which every token follows from the two before it.
+against the same table (wg_linear).  Per step the library computes the blocks' activations and residuals
+(wg_activation) and their gradients (wg_activation_bwd), each convolution's weight gradient (wg_conv_bwd_weight) and
+input gradient (wg_conv_bwd_data), the scores' gradients (wg_linear_bwd_data, wg_linear_bwd_weight), the table's gradient
+as it was looked up (wg_embedding_bwd_weight, added to what the scores leave there), and the convolutions'
+orthogonalised update (wg_muon_update: momentum, Newton-Schulz products, weights).  torch computes what the library has
+no operator for: the convolutions' forward pass and the loss.  The data are sequences in which every token follows from
+the two before it.
 """
 from __future__ import annotations
 
@@ -65,21 +67,20 @@ class ConvLM:
         kept = []
         for layer in self.layers:
             y = layer.forward(h.bfloat16())
-            act = F.gelu(y.float())
             kept.append(y)
-            h = h + act
-        flat = h.reshape(-1, self.channels)
-        scores = flat @ self.table.t()
+            h = binding.activation(y, residual=h, activation="gelu")  # y in bf16, h in fp32
+        flat, table = h.reshape(-1, self.channels).bfloat16(), self.table.bfloat16()
+        rows = len(flat)
+        scores = binding.linear(flat, table, out=torch.empty((rows, self.vocab), device="cuda"))
         loss = F.cross_entropy(scores, targets.reshape(-1))
         d = torch.softmax(scores, -1)
-        d[torch.arange(len(flat), device="cuda"), targets.reshape(-1)] -= 1.0
-        d /= len(flat)
-        self.dtable = d.t() @ flat
-        dh = (d @ self.table).view_as(h)
+        d[torch.arange(rows, device="cuda"), targets.reshape(-1)] -= 1.0
+        d = d.bfloat16()  # (of the loss's sum over the rows: the mean's would lose bits in 16)
+        self.dtable = binding.linear_bwd_weight(flat, d) / rows
+        dh = (binding.linear_bwd_data(d, table, out=torch.empty(flat.shape, device="cuda")) / rows).view_as(h)
         for layer, y in zip(reversed(self.layers), reversed(kept)):
-            v = y.float()
-            slope = 0.5 * (1 + torch.erf(v / math.sqrt(2))) + v * torch.exp(-0.5 * v * v) / math.sqrt(2 * math.pi)
-            dh = dh + layer.backward((dh * slope).bfloat16().contiguous()).view_as(dh)
+            dy = binding.activation_bwd(dh, y, activation="gelu")
+            dh = dh + layer.backward(dy).view_as(dh)
         binding.embedding_bwd_weight(tokens, dh.contiguous(), self.vocab, self.scale, out=self.dtable, accumulate=True)
         return loss
 

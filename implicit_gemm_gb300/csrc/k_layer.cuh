@@ -590,26 +590,31 @@ __device__ __forceinline__ uint4 load_shifted(uintptr_t a, uintptr_t end)
     uint4 x = make_uint4(0u, 0u, 0u, 0u);
     if (c < end) x = *reinterpret_cast<const uint4*>(c);
     if (s == 0) return x;
-    uint4 y = make_uint4(__shfl_down_sync(0xffffffffu, x.x, 1), __shfl_down_sync(0xffffffffu, x.y, 1),
-                         __shfl_down_sync(0xffffffffu, x.z, 1), __shfl_down_sync(0xffffffffu, x.w, 1));
-    if ((threadIdx.x & 31) == 31) {
-        y = make_uint4(0u, 0u, 0u, 0u);
-        if (c + 16 < end) y = *reinterpret_cast<const uint4*>(c + 16);
-    }
-    const uint32_t h = (s & 2u) * 8u;
-    if (s < 4) return make_uint4(__funnelshift_r(x.x, x.y, h), __funnelshift_r(x.y, x.z, h), __funnelshift_r(x.z, x.w, h), __funnelshift_r(x.w, y.x, h));
-    if (s < 8) return make_uint4(__funnelshift_r(x.y, x.z, h), __funnelshift_r(x.z, x.w, h), __funnelshift_r(x.w, y.x, h), __funnelshift_r(y.x, y.y, h));
-    if (s < 12) return make_uint4(__funnelshift_r(x.z, x.w, h), __funnelshift_r(x.w, y.x, h), __funnelshift_r(y.x, y.y, h), __funnelshift_r(y.y, y.z, h));
-    return make_uint4(__funnelshift_r(x.w, y.x, h), __funnelshift_r(y.x, y.y, h), __funnelshift_r(y.y, y.z, h), __funnelshift_r(y.z, y.w, h));
+    uint4 l = make_uint4(0u, 0u, 0u, 0u);  // what follows the last lane's
+    const bool last = (threadIdx.x & 31) == 31;
+    if (last && c + 16 < end) l = *reinterpret_cast<const uint4*>(c + 16);
+    const auto next = [&](uint32_t own, uint32_t behind) {
+        const uint32_t y = __shfl_down_sync(0xffffffffu, own, 1);
+        return last ? behind : y;
+    };
+    const uint32_t h = (s & 2u) * 8u, y0 = next(x.x, l.x);
+    if (s < 4) return make_uint4(__funnelshift_r(x.x, x.y, h), __funnelshift_r(x.y, x.z, h), __funnelshift_r(x.z, x.w, h), __funnelshift_r(x.w, y0, h));
+    const uint32_t y1 = next(x.y, l.y);
+    if (s < 8) return make_uint4(__funnelshift_r(x.y, x.z, h), __funnelshift_r(x.z, x.w, h), __funnelshift_r(x.w, y0, h), __funnelshift_r(y0, y1, h));
+    const uint32_t y2 = next(x.z, l.z);
+    if (s < 12) return make_uint4(__funnelshift_r(x.z, x.w, h), __funnelshift_r(x.w, y0, h), __funnelshift_r(y0, y1, h), __funnelshift_r(y1, y2, h));
+    const uint32_t y3 = next(x.w, l.w);
+    return make_uint4(__funnelshift_r(x.w, y0, h), __funnelshift_r(y0, y1, h), __funnelshift_r(y1, y2, h), __funnelshift_r(y2, y3, h));
 }
 
+// Those of the eight halves at c that lie in [begin, end).
 __device__ __forceinline__ void store_halves(uintptr_t c, const uint4& v, uintptr_t begin, uintptr_t end)
 {
+    const int lo = c < begin ? (int)(begin - c) : 0, hi = c >= end ? 0 : end - c >= 16 ? 16 : (int)(end - c);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        if (c + 2 * i >= begin && c + 2 * i < end)
-            *reinterpret_cast<unsigned short*>(c + 2 * i) = (unsigned short)(i & 1 ? w[i >> 1] >> 16 : w[i >> 1]);
+        if (2 * i >= lo && 2 * i < hi) *reinterpret_cast<unsigned short*>(c + 2 * i) = (unsigned short)(i & 1 ? w[i >> 1] >> 16 : w[i >> 1]);
 }
 __device__ __forceinline__ void store_shifted(uintptr_t a, uintptr_t end, const uint4& x)
 {
@@ -624,31 +629,34 @@ __device__ __forceinline__ void store_shifted(uintptr_t a, uintptr_t end, const 
             store_halves(a, x, begin, end);
         return;
     }
-    const uintptr_t c = a - s;
-    const uint4 p = make_uint4(__shfl_up_sync(0xffffffffu, x.x, 1), __shfl_up_sync(0xffffffffu, x.y, 1),
-                               __shfl_up_sync(0xffffffffu, x.z, 1), __shfl_up_sync(0xffffffffu, x.w, 1));
     // The aligned chunk at c: the last s bytes of the lane before, then the first of this one;
     // and (of the last lane) the chunk after it, which begins with this lane's last s bytes.
-    const uint32_t o = 16 - s, h = (o & 2u) * 8u;
+    const uintptr_t c = a - s;
+    const uint32_t h = ((16 - s) & 2u) * 8u;
+    const auto before = [](uint32_t own) { return __shfl_up_sync(0xffffffffu, own, 1); };
+    const uint32_t p3 = before(x.w);
     uint4 v, z;
-    if (o < 4) {
-        v = make_uint4(__funnelshift_r(p.x, p.y, h), __funnelshift_r(p.y, p.z, h), __funnelshift_r(p.z, p.w, h), __funnelshift_r(p.w, x.x, h));
-        z = make_uint4(__funnelshift_r(x.x, x.y, h), __funnelshift_r(x.y, x.z, h), __funnelshift_r(x.z, x.w, h), __funnelshift_r(x.w, 0u, h));
-    } else if (o < 8) {
-        v = make_uint4(__funnelshift_r(p.y, p.z, h), __funnelshift_r(p.z, p.w, h), __funnelshift_r(p.w, x.x, h), __funnelshift_r(x.x, x.y, h));
-        z = make_uint4(__funnelshift_r(x.y, x.z, h), __funnelshift_r(x.z, x.w, h), __funnelshift_r(x.w, 0u, h), 0u);
-    } else if (o < 12) {
-        v = make_uint4(__funnelshift_r(p.z, p.w, h), __funnelshift_r(p.w, x.x, h), __funnelshift_r(x.x, x.y, h), __funnelshift_r(x.y, x.z, h));
-        z = make_uint4(__funnelshift_r(x.z, x.w, h), __funnelshift_r(x.w, 0u, h), 0u, 0u);
-    } else {
-        v = make_uint4(__funnelshift_r(p.w, x.x, h), __funnelshift_r(x.x, x.y, h), __funnelshift_r(x.y, x.z, h), __funnelshift_r(x.z, x.w, h));
+    if (s <= 4) {
+        v = make_uint4(__funnelshift_r(p3, x.x, h), __funnelshift_r(x.x, x.y, h), __funnelshift_r(x.y, x.z, h), __funnelshift_r(x.z, x.w, h));
         z = make_uint4(__funnelshift_r(x.w, 0u, h), 0u, 0u, 0u);
+    } else if (s <= 8) {
+        const uint32_t p2 = before(x.z);
+        v = make_uint4(__funnelshift_r(p2, p3, h), __funnelshift_r(p3, x.x, h), __funnelshift_r(x.x, x.y, h), __funnelshift_r(x.y, x.z, h));
+        z = make_uint4(__funnelshift_r(x.z, x.w, h), __funnelshift_r(x.w, 0u, h), 0u, 0u);
+    } else if (s <= 12) {
+        const uint32_t p2 = before(x.z), p1 = before(x.y);
+        v = make_uint4(__funnelshift_r(p1, p2, h), __funnelshift_r(p2, p3, h), __funnelshift_r(p3, x.x, h), __funnelshift_r(x.x, x.y, h));
+        z = make_uint4(__funnelshift_r(x.y, x.z, h), __funnelshift_r(x.z, x.w, h), __funnelshift_r(x.w, 0u, h), 0u);
+    } else {
+        const uint32_t p2 = before(x.z), p1 = before(x.y), p0 = before(x.x);
+        v = make_uint4(__funnelshift_r(p0, p1, h), __funnelshift_r(p1, p2, h), __funnelshift_r(p2, p3, h), __funnelshift_r(p3, x.x, h));
+        z = make_uint4(__funnelshift_r(x.x, x.y, h), __funnelshift_r(x.y, x.z, h), __funnelshift_r(x.z, x.w, h), __funnelshift_r(x.w, 0u, h));
     }
     if (c >= begin && c + 16 <= end)
         *reinterpret_cast<uint4*>(c) = v;
     else
         store_halves(c, v, begin, end);
-    if (lane == 31) store_halves(c + 16, z, begin, end);
+    if (lane == 31 && c + 16 < end) store_halves(c + 16, z, begin, end);
 }
 
 // ---------------------------------------------------------------- activation alone
