@@ -304,12 +304,28 @@ wg::PackParams lin_pack(LinOperand* o, char* to)
     return k;
 }
 
+// The chunked kernels' warps pass registers on (setmaxnreg), out of those that a launch takes: with fewer than
+// they are written for, the epilogue's warps would wait for ever.  Asked of the built kernel, once.
+template <int KIND>
+int check_registers()
+{
+    static const int st = [] {
+        cudaFuncAttributes a;
+        const cudaError_t e = cudaFuncGetAttributes(&a, wg::linear_product_kernel<KIND, true>);
+        return e != cudaSuccess ? -1 : a.numRegs;
+    }();
+    const int need = 128 * wg::kLinDirectRegs + 32 * wg::lin_epi_warps(true) * wg::kLinChunkedRegs;
+    if (st * wg::lin_threads(true) >= need) return WG_OK;
+    return set_err(WG_ERR_CUDA, "linear_product_kernel was built with " + std::to_string(st) + " registers a thread, fewer than it hands out");
+}
+
 template <int KIND, bool CHUNKED>
 int lin_launch(const LinPlan& pl, const wg::LinParams& g, const LinOperand& a, const LinOperand& b, cudaStream_t s)
 {
     CUtensorMap ma, mb;
     int st = lin_map(&ma, a.p, g.bf16, a.cols, a.rows, a.batch, a.ld, a.bs, KIND == wg::kForward ? 128 : 64);
     if (!st) st = lin_map(&mb, b.p, g.bf16, b.cols, b.rows, 1, b.ld, 0, KIND == wg::kWeight ? 64 : pl.bt / 2);
+    if (!st && CHUNKED) st = check_registers<KIND>();
     if (!st) st = wg::ensure_smem(wg::linear_product_kernel<KIND, CHUNKED>, wg::kLinSmem);
     if (st) return st;
     cudaLaunchConfig_t cfg = {};

@@ -486,16 +486,17 @@ typedef enum {
  *  experts = 0: one weight; offsets is NULL.  experts >= 1: rows offsets[e] ..
  *    offsets[e + 1] - 1 are expert e's, offsets being experts + 1 ascending integers of
  *    offset_bits in device memory, read when the kernels run.  Rows before offsets[0] and
- *    from offsets[experts] on are neither read nor written (y, z, dx there stay as they
- *    are).  An expert without rows has a zero weight gradient.  Offsets that descend or
+ *    from offsets[experts] on may hold anything and are not written (y, z, dx there stay
+ *    as they are).  An expert without rows has a zero weight gradient.  Offsets that descend or
  *    lie outside [0, tokens] are brought into order (the largest so far) and into range,
  *    and wg_check_status then returns WG_ERR_INVALID_OFFSET.
  *
- * Products and sums are fp32 (512 terms at a time on the tensor cores, those added
- * rounded to nearest), as is all that follows, rounded once to nearest even; z is rounded
- * by itself, y is made from the unrounded v.  Results are bitwise reproducible.  Zeros
- * are added for no one: rows and experts do not touch one another's results, infinities
- * and NaN included.
+ * Products and sums are fp32, as is all that follows, rounded once to nearest even; z is
+ * rounded by itself, y is made from the unrounded v.  The tensor cores add with
+ * truncation: 1024 terms at a time for an fp32 result (which takes at most 6e-6 of a sum
+ * of equal signs), 32768 for a 16-bit one (2e-4, 0.4 of fp16's rounding); those sums are
+ * added rounded to nearest.  Results are bitwise reproducible.  Rows and experts do not
+ * touch one another's results, infinities and NaN included.
  *
  *  tokens 0..2^31-65536, in and out 1..2^20, experts 0..1024; at most 2^31 - 1 tiles of
  *    256 features by 32 rows.
@@ -530,8 +531,10 @@ WG_API int wg_linear_plan_string(const wg_linear_problem* p, wg_linear_call call
 
 /* The three calls on `stream`.  x, w and dy need 16-byte aligned bases where their
  * ld (and, with several experts, weight_stride) is a multiple of 8 elements, else
- * only their elements' alignment; every other tensor only its elements' (16-byte
- * aligned rows are faster); workspace 16 bytes.  residual may be y (or dx) itself, with
+ * only their elements' alignment (such rows are fetched in the aligned 16 bytes around
+ * them); every other tensor only its elements' (16-byte aligned rows are faster);
+ * workspace 16 bytes, its contents of no use before or after a call: calls whose work may
+ * overlap on the GPU, replayed graphs among them, need one each.  residual may be y (or dx) itself, with
  * the same strides; else no output may overlap another tensor of the call.
  * accumulate: dw and dbias are added to what is there (in fp32, then rounded).
  * With tokens = 0 nothing is written but the weight gradient's zeros.
@@ -571,8 +574,9 @@ typedef struct {
 /* Bytes of device workspace wg_activation_bwd needs for p (dbias's partial sums).  Host only. */
 WG_API int wg_activation_workspace_size(const wg_activation_problem* p, size_t* bytes);
 
-/* The two calls on `stream`.  Tensors need only their elements' alignment; workspace (needed
- * with dbias only) 16 bytes.  y may be x or residual, and dx may be x or dy, where
+/* The two calls on `stream`.  Tensors need only their elements' alignment (rows that start
+ * anywhere are fetched in the aligned 16 bytes around them); workspace (needed with dbias
+ * only) 16 bytes, one for each call whose work may overlap.  y may be x or residual, and dx may be x or dy, where
  * their types and strides are the same; else no output may overlap another tensor.
  * Returns WG_OK or an error status; nothing is launched on an error. */
 WG_API int wg_activation(const wg_activation_problem* p, const void* x, const void* bias, const void* residual, void* y,

@@ -1,9 +1,11 @@
 """The layer operators in 64 bits, from their definitions, and how far a call may be from them.
 
-Tolerances.  Products of two 16-bit values are exact in fp32.  The tensor cores add 16 of them at a time to a sum of at
-most 512 terms with truncation: 32 additions, each off by at most two units of fp32's last place of the sum of the terms'
-sizes A (one for the aligned terms, one for the sum): 64 * 2^-23 A; then a rounding 2^-24 A for each 512 terms (and each
-part of a cut sum, of which there are fewer).  What follows is fp32: the bias adds 2^-24 |v|, an activation's value is off
+Tolerances.  Products of two 16-bit values are exact in fp32.  The tensor cores add 16 of them at a time, with
+truncation, to a sum of at most 1024 terms (of an fp32 result): 64 additions, each off by at most a unit of fp32's last
+place of the sum of the terms' sizes A: 64 * 2^-23 A; then a rounding 2^-24 A for each such sum (and each part of a cut
+one).  A 16-bit result's sums have up to 32768 terms, so up to 2048 additions, but truncation takes what is proportional to
+the sum so far, which stays near the root of the terms' number for terms of both signs, as all inputs here have: less than
+the same bound.  What follows is fp32: the bias adds 2^-24 |v|, an activation's value is off
 by at most 2^-20 (|v| + 1) (exponential, quotient and erf to a few last places of their own and of their arguments; |v| up
 to 40 grows the exponential's argument error by as much where its value is below 2^-50) and carries v's error with a slope of at most
 1.13 (its slope's slope is at most 1.6, and a slope is off by 2^-19), dropout's factor and the residual 2^-23 of their

@@ -330,3 +330,133 @@ def test_two_calls_at_once_give_what_they_give_alone():
     for i in range(2):
         for y in got[i]:
             assert torch.equal(y, want[i])
+
+
+@pytest.mark.parametrize("tokens", [3, 20, 700])
+def test_many_experts(tokens):
+    """As many experts as there may be, most of them without rows; offsets of 64 bits."""
+    n, inf, out = 1024, 64, 40
+    g = torch.Generator().manual_seed(tokens)
+    count = torch.bincount(torch.randint(n, (tokens,), generator=g), minlength=n)
+    off = offsets_of(count.tolist(), 0, torch.int64)
+    x, w, dy = randn(1, tokens, inf, dt="bf16"), randn(2, n, out, inf, size=0.1, dt="bf16"), randn(3, tokens, out, dt="bf16")
+    bias, offs = randn(4, n, out), off.tolist()
+    y = binding.linear(x, w, bias, activation="relu", offsets=off)
+    _, (want, err) = forward(x, w, bias, activation="relu", offsets=offs)
+    close(y, want, err, "bf16")
+    dx = binding.linear_bwd_data(dy, w, offsets=off)
+    want, err = data(dy, w, offsets=offs)
+    close(dx, want, err, "bf16")
+    db = torch.empty(n, out, device="cuda")
+    dw = binding.linear_bwd_weight(x, dy, off, dbias=db)
+    (want, err), (wb, berr) = weight(x, dy, offs, n)
+    close(dw, want, err, "fp32")
+    close(db, wb, berr, "fp32")
+
+
+@pytest.mark.parametrize("counts,inf,out", [([30, 0, 11], 2048, 264), ([2, 90], 4096, 72), ([5000, 1, 3000], 64, 72),
+                                            ([0, 6000], 200, 136), ([17], 5000, 257)])
+def test_experts_with_cut_sums(counts, inf, out):
+    """Few tiles and long sums: the sum is cut among the SMs, of an expert's rows too."""
+    n = len(counts)
+    off = offsets_of(counts, 1)
+    rows = int(off[-1]) + 2
+    x, w, dy = randn(1, rows, inf, dt="fp16"), randn(2, n, out, inf, size=inf ** -0.5, dt="fp16"), randn(3, rows, out, dt="fp16")
+    x[0], dy[0], x[-2:], dy[-2:] = float("nan"), float("nan"), float("inf"), float("inf")
+    sp = {"tokens": rows, "in": inf, "out": out, "experts": n, "in_dtype": "fp16", "out_dtype": "fp16"}
+    assert any("split=1 " not in binding.wg_linear_plan_string(sp, c) for c in ("forward", "bwd_weight"))
+    offs, used = off.tolist(), slice(1, rows - 2)
+    res = randn(4, rows, out, dt="fp16")
+    y = binding.linear(x, w, None, res, "gelu_tanh", 0.2, SEED, OFFSET, offsets=off)
+    _, (want, err) = forward(x, w, None, res, "gelu_tanh", 0.2, SEED, OFFSET, offs)
+    close(y[used], want[used], err[used], "fp16")
+    assert not y[0].any() and not y[-2:].any()
+    acc = randn(5, n, out, inf)
+    start = acc.clone()
+    db = torch.empty(n, out, device="cuda")
+    binding.linear_bwd_weight(x, dy, off, out=acc, accumulate=True)
+    binding.linear_bwd_weight(x, dy, off, out=torch.empty_like(acc), dbias=db)
+    (want, err), (wb, berr) = weight(x, dy, offs, n)
+    close(acc, want + start.double(), err + 2.0 ** -23 * (want.abs() + start.double().abs()), "fp32")
+    close(db, wb, berr, "fp32")
+
+
+@pytest.mark.parametrize("tokens", [7, 20, 300])
+@pytest.mark.parametrize("ydt", ["bf16", "fp32"])
+def test_very_long_sums(tokens, ydt):
+    inf, out = 40008, 40
+    x, w = randn(1, tokens, inf, dt="bf16"), randn(2, out, inf, size=inf ** -0.5, dt="bf16")
+    y = torch.empty(tokens, out, dtype=DT[ydt], device="cuda")
+    binding.linear(x, w, out=y)
+    _, (want, err) = forward(x, w[None])
+    close(y, want, err, ydt)
+    dx = binding.linear_bwd_data(x, w.t().contiguous(), out=torch.empty(tokens, out, dtype=DT[ydt], device="cuda"))
+    close(dx, want, err, ydt)
+
+
+def test_results_are_the_same_again():
+    """Bit for bit, cut sums and bias sums too, and in whatever workspace."""
+    x, w, dy = randn(1, 500, 2048, dt="bf16"), randn(2, 264, 2048, size=0.1, dt="bf16"), randn(3, 500, 264, dt="bf16")
+    db = [torch.empty(264, device="cuda") for _ in range(2)]
+    first = [binding.linear(x, w), binding.linear_bwd_data(dy, w), binding.linear_bwd_weight(x, dy, dbias=db[0]), db[0]]
+    torch.empty(1 << 26, dtype=torch.uint8, device="cuda").fill_(0xff)  # what the next workspaces may hold
+    again = [binding.linear(x, w), binding.linear_bwd_data(dy, w), binding.linear_bwd_weight(x, dy, dbias=db[1]), db[1]]
+    for a, b in zip(first, again):
+        assert torch.equal(a, b)
+
+
+def test_calls_after_one_another_in_one_workspace():
+    """One workspace for calls of one stream, as in a captured training step: packed operands, parts of sums and bias sums
+    of each call give way to the next one's."""
+    t, a, b = 260, 1001, 135
+    x, w, dy = randn(1, t, a, dt="bf16"), randn(2, b, a, size=0.03, dt="bf16"), randn(3, t, b, dt="bf16")
+    sp = {"tokens": t, "in": a, "out": b, "out_dtype": "fp32"}
+    ws = torch.empty(max(binding.wg_linear_workspace_size(sp, c) for c in binding.LINEAR_CALLS), dtype=torch.uint8, device="cuda")
+    out = {k: torch.empty(s, device="cuda") for k, s in (("y", (t, b)), ("dx", (t, a)), ("dw", (b, a)), ("db", (b,)))}
+    calls = [binding.PreparedLinear(sp, x, w, out["y"], workspace=ws), binding.PreparedLinearBwdData(sp, dy, w, out["dx"], workspace=ws),
+             binding.PreparedLinearBwdWeight(sp, x, dy, out["dw"], dbias=out["db"], workspace=ws)]
+    g = torch.cuda.CUDAGraph()
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        for c in calls:
+            c(st.cuda_stream)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        for c in calls:
+            c(torch.cuda.current_stream().cuda_stream)
+    for v in out.values():
+        v.fill_(float("nan"))
+    for _ in range(4):
+        g.replay()
+    torch.cuda.synchronize()
+    _, (want, err) = forward(x, w[None])
+    close(out["y"], want, err, "fp32", "y")
+    want, err = data(dy, w[None])
+    close(out["dx"], want, err, "fp32", "dx")
+    (want, err), (wb, berr) = weight(x, dy)
+    close(out["dw"], want[0], err[0], "fp32", "dw")
+    close(out["db"], wb[0], berr[0], "fp32", "db")
+
+
+def test_memory_of_a_call_on_another_stream():
+    """The convenience calls' results and workspaces come from their stream's blocks (test_wrapper_streams_gpu.py)."""
+    x, w, dy = randn(1, 120, 1001, dt="bf16"), randn(2, 72, 1001, size=0.1, dt="bf16"), randn(3, 120, 72, dt="bf16")
+    off = offsets_of([50, 70])
+    we = randn(4, 2, 72, 1001, size=0.1, dt="bf16")
+    calls = [lambda **k: binding.linear(x, w, activation="gelu", **k), lambda **k: binding.linear(x, we, offsets=off, **k),
+             lambda **k: binding.linear_bwd_data(dy, w, **k), lambda **k: binding.linear_bwd_weight(x, dy, **k),
+             lambda **k: binding.activation(x, activation="silu", dropout=0.1, **k),
+             lambda **k: binding.activation_bwd(x, x, activation="silu", **k)]
+    for f in calls:
+        want = f().clone()
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        s = torch.cuda.Stream()
+        torch.cuda._sleep(50_000_000)
+        blocks = [torch.empty_like(want) for _ in range(2)] + [torch.empty(1 << 20, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        for block in blocks:
+            block.fill_(77)
+        del block, blocks
+        got = f(stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
