@@ -796,6 +796,21 @@ struct SumParams {
     int chunks;            // of a problem without experts
     const int* first;      // [experts + 1] chunks before each expert's, or null
 };
+// A finished sum into element i of dbias, or added to it.
+__device__ __forceinline__ void put_sum(void* out, long long i, int dtype, bool accumulate, float a)
+{
+    if (dtype == 2) {
+        float* o = static_cast<float*>(out) + i;
+        *o = accumulate ? *o + a : a;
+    } else if (dtype == 0) {
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out) + i;
+        *o = __float2bfloat16_rn(accumulate ? __bfloat162float(*o) + a : a);
+    } else {
+        __half* o = static_cast<__half*>(out) + i;
+        *o = __float2half_rn(accumulate ? __half2float(*o) + a : a);
+    }
+}
+
 __global__ void __launch_bounds__(kJoinThreads) column_join_kernel(const __grid_constant__ SumParams p)
 {
     pdl_launch_dependents();
@@ -812,17 +827,7 @@ __global__ void __launch_bounds__(kJoinThreads) column_join_kernel(const __grid_
     __syncthreads();
     if (ty || j >= p.dim || (p.accumulate && c0 == c1)) return;
     for (int y = 1; y < ny; ++y) a += s[y * nx + tx];
-    const long long i = (long long)e * p.dim + j;
-    if (p.dtype == 2) {
-        float* o = static_cast<float*>(p.out) + i;
-        *o = p.accumulate ? *o + a : a;
-    } else if (p.dtype == 0) {
-        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + i;
-        *o = __float2bfloat16_rn(p.accumulate ? __bfloat162float(*o) + a : a);
-    } else {
-        __half* o = static_cast<__half*>(p.out) + i;
-        *o = __float2half_rn(p.accumulate ? __half2float(*o) + a : a);
-    }
+    put_sum(p.out, (long long)e * p.dim + j, p.dtype, p.accumulate, a);
 }
 
 }  // namespace wg

@@ -787,8 +787,9 @@ __global__ void __launch_bounds__(256) linear_pack_kernel(const __grid_constant_
 }
 
 // ---------------------------------------------------------------- bias gradients
-// Sums of dy's columns over an expert's rows, `chunk` rows at a time: part[chunk][N], and how
-// many chunks come before each expert's (first, written by one block).
+// Sums of dy's columns over an expert's rows: all of them by one block, which writes dbias (no
+// launch to join parts: few rows, beside the product), or `chunk` rows at a time to
+// part[chunk][N], with how many chunks come before each expert's (first, written by one block).
 struct ColumnParams {
     const void* dy;
     long long tokens, ld;
@@ -796,8 +797,10 @@ struct ColumnParams {
     int experts, offsets64;
     const void* offsets;
     int cx_log, chunk;
-    float* part;
+    float* part;           // null: one block for all rows of an expert (blockIdx.y)
     int* first;
+    void* out;
+    int out_dtype, accumulate;
 };
 __global__ void __launch_bounds__(256) column_sum_kernel(const __grid_constant__ ColumnParams p)
 {
@@ -807,30 +810,32 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const __grid_constant__
     pdl_launch_dependents();  // (after the wait: see LinParams::early)
     load_offsets(p.experts, p.offsets, p.offsets64, p.tokens, off);
     const int n = max(p.experts, 1);
-    if (threadIdx.x < 32) {
-        const int lane = threadIdx.x;
-        int run = 0;
-        for (int i0 = 0; i0 < n; i0 += 32) {
-            const int c = i0 + lane < n ? (off[i0 + lane + 1] - off[i0 + lane] + p.chunk - 1) / p.chunk : 0;
-            int a = c;
+    if (p.part) {
+        if (threadIdx.x < 32) {
+            const int lane = threadIdx.x;
+            int run = 0;
+            for (int i0 = 0; i0 < n; i0 += 32) {
+                const int c = i0 + lane < n ? (off[i0 + lane + 1] - off[i0 + lane] + p.chunk - 1) / p.chunk : 0;
+                int a = c;
 #pragma unroll
-            for (int d = 1; d < 32; d *= 2) {
-                const int o = __shfl_up_sync(0xffffffffu, a, d);
-                if (lane >= d) a += o;
+                for (int d = 1; d < 32; d *= 2) {
+                    const int o = __shfl_up_sync(0xffffffffu, a, d);
+                    if (lane >= d) a += o;
+                }
+                if (i0 + lane < n) first[i0 + lane] = run + a - c;
+                run += __shfl_sync(0xffffffffu, a, 31);
             }
-            if (i0 + lane < n) first[i0 + lane] = run + a - c;
-            run += __shfl_sync(0xffffffffu, a, 31);
+            if (lane == 0) first[n] = run;
         }
-        if (lane == 0) first[n] = run;
+        __syncthreads();
+        if (blockIdx.x == 0 && blockIdx.y == 0)
+            for (int i = threadIdx.x; i <= n; i += 256) p.first[i] = first[i];
     }
-    __syncthreads();
-    if (blockIdx.x == 0 && blockIdx.y == 0)
-        for (int i = threadIdx.x; i <= n; i += 256) p.first[i] = first[i];
     const int cx = 1 << p.cx_log, tx = threadIdx.x & (cx - 1), ty = threadIdx.x >> p.cx_log, ny = 256 >> p.cx_log;
     const int col = 8 * (blockIdx.x * cx + tx), m = min(8, p.N - col);
-    for (int c = blockIdx.y; c < first[n]; c += gridDim.y) {
-        const int e = find_last(first, n, c);
-        const int r0 = off[e] + (c - first[e]) * p.chunk, r1 = min(off[e + 1], r0 + p.chunk);
+    for (int c = blockIdx.y; c < (p.part ? first[n] : n); c += gridDim.y) {
+        const int e = p.part ? find_last(first, n, c) : c;
+        const int r0 = off[e] + (p.part ? (c - first[e]) * p.chunk : 0), r1 = p.part ? min(off[e + 1], r0 + p.chunk) : off[e + 1];
         float sum[8] = {};
         if (m > 0)
             for (int r = r0 + ty; r < r1; r += 8 * ny) {
@@ -855,7 +860,11 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const __grid_constant__
             const int k = i & 7, x = i >> 3, j = 8 * (blockIdx.x * cx + x) + k;
             float a = 0.f;
             for (int y = 0; y < ny; ++y) a += s[k][(y << p.cx_log) + x];
-            if (j < p.N) p.part[(long long)c * p.N + j] = a;
+            if (j >= p.N) continue;
+            if (p.part)
+                p.part[(long long)c * p.N + j] = a;
+            else if (!p.accumulate || r0 < r1)
+                put_sum(p.out, (long long)e * p.N + j, p.out_dtype, p.accumulate, a);
         }
     }
 }
