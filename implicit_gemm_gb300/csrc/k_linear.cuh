@@ -793,7 +793,7 @@ __global__ void __launch_bounds__(256) linear_pack_kernel(const __grid_constant_
 struct ColumnParams {
     const void* dy;
     long long tokens, ld;
-    int N, dtype, vec;
+    int N, dtype;
     int experts, offsets64;
     const void* offsets;
     int cx_log, chunk;
@@ -802,7 +802,8 @@ struct ColumnParams {
     void* out;
     int out_dtype, accumulate;
 };
-__global__ void __launch_bounds__(256) column_sum_kernel(const __grid_constant__ ColumnParams p)
+template <int MODE>
+__global__ void __launch_bounds__(256, 4) column_sum_kernel(const __grid_constant__ ColumnParams p)
 {
     __shared__ int off[kLinMaxExperts + 1], first[kLinMaxExperts + 1];
     __shared__ float s[8][256];
@@ -837,19 +838,18 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const __grid_constant__
         const int e = p.part ? find_last(first, n, c) : c;
         const int r0 = off[e] + (p.part ? (c - first[e]) * p.chunk : 0), r1 = p.part ? min(off[e + 1], r0 + p.chunk) : off[e + 1];
         float sum[8] = {};
-        if (m > 0)
+        if (m > 0 || MODE == kActShifted)
             for (int r = r0 + ty; r < r1; r += 8 * ny) {
-                Raw8 x[8];
+                uint4 x[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    if (r + i * ny < r1) x[i] = load_raw8(p.dy, (r + i * ny) * p.ld + col, p.dtype, p.vec, m);
+                    if (r + i * ny < r1) x[i] = act_load<MODE>(p.dy, r + i * ny, p.ld, col, m, p.N, p.dtype, false).a;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     if (r + i * ny >= r1) continue;
                     float v[8];
-                    unpack8(x[i], p.dtype, v);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) sum[k] += v[k];
+                    act_unpack<kActWide>({x[i], x[i]}, p.dtype, v);
+                    add8(v, sum);
                 }
             }
         __syncthreads();

@@ -349,10 +349,13 @@ int lin_launch(const LinPlan& pl, const wg::LinParams& g, const LinOperand& a, c
 
 int columns_launch(const wg::ColumnParams& c, const LinPlan& pl, cudaStream_t s)
 {
+    const bool vec = vec_rows(c.dy, c.ld, c.N, 2);
     const int groups = (c.N + 7) / 8;
     const long long cols = (groups + (1 << c.cx_log) - 1) >> c.cx_log;
-    const long long rows = c.part ? std::min(pl.sum_chunks, (6LL * num_sms() + cols - 1) / cols) : std::max(c.experts, 1);
-    return launch("column_sum_kernel launch", wg::column_sum_kernel, dim3((unsigned)cols, (unsigned)std::max(1LL, rows)), dim3(256), s, c);
+    const long long rows = c.part ? std::min(pl.sum_chunks, (4LL * num_sms() + cols - 1) / cols) : std::max(c.experts, 1);
+    const auto kernel = vec ? wg::column_sum_kernel<wg::kActWide>
+                            : c.cx_log == 5 ? wg::column_sum_kernel<wg::kActShifted> : wg::column_sum_kernel<wg::kActAny>;
+    return launch("column_sum_kernel launch", kernel, dim3((unsigned)cols, (unsigned)std::max(1LL, rows)), dim3(256), s, c);
 }
 
 // w, or x of the weight gradient, is operand a (MMA rows); the other operand b.  sums: dbias's partial sums,
@@ -628,12 +631,13 @@ int wg_linear_bwd_weight(const wg_linear_problem* p, const void* offsets, const 
     if (vec_rows(dw, q.ld_weight, q.in, oe, ne > 1 ? q.weight_stride : 0)) g.vec |= wg::kVecY | wg::kVecRes;
     if (pair_rows(dw, q.ld_weight, q.in, oe, ne > 1 ? q.weight_stride : 0)) g.vec |= wg::kPairY | wg::kPairRes;
     wg::ColumnParams c = {};
-    c.dy = dy, c.tokens = q.tokens, c.ld = q.ld_out, c.N = q.out, c.dtype = q.in_dtype, c.vec = vec_rows(dy, q.ld_out, q.out, ie);
+    c.dy = dy, c.tokens = q.tokens, c.ld = q.ld_out, c.N = q.out, c.dtype = q.in_dtype;
     c.experts = q.experts, c.offsets64 = q.offset_bits == 64, c.offsets = offsets, c.chunk = pl.sum_rows;
     c.part = reinterpret_cast<float*>(ws + pl.off_sum), c.first = reinterpret_cast<int*>(ws + pl.off_first);
     c.out = dbias, c.out_dtype = q.bias_dtype, c.accumulate = accumulate != 0;
     // Few rows: 64 columns and every row of an expert per block (512 x 1000 with the product 10 us instead of 12).
-    const bool once = c.vec && q.tokens <= 1024 && ne * ((q.out + 63LL) / 64) <= 4LL * num_sms();
+    const bool vec = vec_rows(dy, q.ld_out, q.out, ie);
+    const bool once = vec && q.tokens <= 1024 && ne * ((q.out + 63LL) / 64) <= 4LL * num_sms();
     if (once) c.part = nullptr;
     const int groups = (q.out + 7) / 8;
     c.cx_log = std::min(once ? 3 : 5, log2_floor(groups) + ((groups & (groups - 1)) ? 1 : 0));
