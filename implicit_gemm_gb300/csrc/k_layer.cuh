@@ -704,9 +704,11 @@ __device__ __forceinline__ void act_unpack(const Raw8& r, int dtype, float (&f)[
 }
 
 template <bool BWD, int MODE>
-__global__ void __launch_bounds__(kActThreads, MODE == kActAny ? 2 : 3) activation_kernel(const __grid_constant__ ActParams p)
+__global__ void __launch_bounds__(kActThreads, MODE == kActAny ? 2 : 4) activation_kernel(const __grid_constant__ ActParams p)
 {
-    constexpr int kRows = MODE == kActWide && !BWD ? 4 : 2;
+    // Rows in flight, as many as leave four blocks of an SM their registers (16384 x 4096: forward 88 us
+    // with two, 92 with four and three blocks, 92 with one; gradient 103 with one, 111 with two).
+    constexpr int kRows = MODE == kActWide && !BWD ? 2 : MODE == kActAny ? 2 : 1;
     pdl_launch_dependents();
     const int cx = 1 << p.cx_log, tx = threadIdx.x & (cx - 1), ty = threadIdx.x >> p.cx_log, ny = kActThreads >> p.cx_log;
     const int col = 8 * (blockIdx.x * cx + tx), n = min(8, p.dim - col);
