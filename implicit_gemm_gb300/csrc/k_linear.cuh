@@ -557,8 +557,9 @@ __global__ void __launch_bounds__(lin_threads(CHUNKED), 1)
 
 // ---------------------------------------------------------------- parts of sums
 // The parts of each result in order, and what follows: eight columns a thread.
+constexpr int kJoinBlock = 64;  // (few results, so many blocks)
 template <int KIND>
-__global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ LinParams p)
+__global__ void __launch_bounds__(kJoinBlock) linear_join_kernel(const __grid_constant__ LinParams p)
 {
     __shared__ int off[kLinMaxExperts + 1];
     pdl_launch_dependents();
@@ -583,11 +584,21 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
         tail_read<KIND>(p.t, e, row, j, n, rd);
         float v[8] = {};
         const float* q = p.part + r * p.ldp + j;
-#pragma unroll 4
-        for (int s = 0; s < p.split; ++s, q += p.part_rows * p.ldp) {
-            const float4 a = __ldcg(reinterpret_cast<const float4*>(q)), b = __ldcg(reinterpret_cast<const float4*>(q) + 1);
-            v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
-            v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+        const long long between = p.part_rows * p.ldp;
+        for (int s = 0; s < p.split; s += 8, q += 8 * between) {  // eight parts in flight
+            float4 a[8], b[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (s + k < p.split) {
+                    a[k] = __ldcg(reinterpret_cast<const float4*>(q + k * between));
+                    b[k] = __ldcg(reinterpret_cast<const float4*>(q + k * between) + 1);
+                }
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (s + k < p.split) {
+                    v[0] += a[k].x, v[1] += a[k].y, v[2] += a[k].z, v[3] += a[k].w;
+                    v[4] += b[k].x, v[5] += b[k].y, v[6] += b[k].z, v[7] += b[k].w;
+                }
         }
         tail_write<KIND>(p.t, offset, e, row, j, n, rd, v);
     }

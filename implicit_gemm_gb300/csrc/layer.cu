@@ -344,7 +344,7 @@ int lin_launch(const LinPlan& pl, const wg::LinParams& g, const LinOperand& a, c
     if (pl.split == 1) return WG_OK;
     const long long items = g.part_rows * (g.ldp / 8);
     return launch("linear_join_kernel launch", wg::linear_join_kernel<KIND>,
-                  dim3((unsigned)std::min<long long>((items + 255) / 256, 8LL * num_sms())), dim3(256), s, g);
+                  dim3((unsigned)std::min<long long>((items + wg::kJoinBlock - 1) / wg::kJoinBlock, 16LL * num_sms())), dim3(wg::kJoinBlock), s, g);
 }
 
 int columns_launch(const wg::ColumnParams& c, const LinPlan& pl, cudaStream_t s)
