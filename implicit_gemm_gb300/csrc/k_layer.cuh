@@ -583,16 +583,25 @@ __device__ __forceinline__ void column_tail(const LayerTail& t, unsigned long lo
 // next lane's first.  (An element at a time: eight times the requests, 5001 x 2047 in fp16
 // 80 us.)  `a` is the address of the lane's first element, `end` that of the row's end; chunks
 // that hold no element of the row are not touched.  The whole warp, converged.
-__device__ __forceinline__ uint4 load_shifted(uintptr_t a, uintptr_t end)
+// In two steps, so that the loads of several rows are in flight before the first is waited for.
+struct Fetched {
+    uint4 x, l;  // the lane's aligned chunk, and (the last lane) the one behind it
+};
+__device__ __forceinline__ Fetched fetch_shifted(uintptr_t a, uintptr_t end)
 {
     const uintptr_t c = a & ~(uintptr_t)15;
+    Fetched f;
+    f.x = f.l = make_uint4(0u, 0u, 0u, 0u);
+    if (c < end) f.x = *reinterpret_cast<const uint4*>(c);
+    if ((threadIdx.x & 31) == 31 && (a & 15) && c + 16 < end) f.l = *reinterpret_cast<const uint4*>(c + 16);
+    return f;
+}
+__device__ __forceinline__ uint4 join_shifted(const Fetched& f, uintptr_t a)
+{
+    const uint4 &x = f.x, &l = f.l;
     const uint32_t s = (uint32_t)(a & 15);  // the same for every lane
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    if (c < end) x = *reinterpret_cast<const uint4*>(c);
     if (s == 0) return x;
-    uint4 l = make_uint4(0u, 0u, 0u, 0u);  // what follows the last lane's
     const bool last = (threadIdx.x & 31) == 31;
-    if (last && c + 16 < end) l = *reinterpret_cast<const uint4*>(c + 16);
     const auto next = [&](uint32_t own, uint32_t behind) {
         const uint32_t y = __shfl_down_sync(0xffffffffu, own, 1);
         return last ? behind : y;
@@ -681,20 +690,27 @@ struct ActParams {
     float* part;          // [chunks][dim] sums of dx, or null
 };
 
+// Eight columns of a row as they come from memory: a Raw8, or what join_shifted takes.
 template <int MODE>
 __device__ __forceinline__ Raw8 act_load(const void* p, long long row, long long ld, int col, int n, int dim, int dtype, bool vec)
 {
-    Raw8 r;
     if (MODE == kActShifted) {
         const uintptr_t b = reinterpret_cast<uintptr_t>(p) + 2 * row * ld;
-        r.a = load_shifted(b + 2 * (uintptr_t)col, b + 2 * (uintptr_t)dim);
-        return r;
+        const Fetched f = fetch_shifted(b + 2 * (uintptr_t)col, b + 2 * (uintptr_t)dim);
+        return {f.x, f.l};
     }
     if (MODE == kActWide) {
+        Raw8 r;
         r.a = *reinterpret_cast<const uint4*>(at(p, row * ld + col, 0));
         return r;
     }
     return load_raw8(p, row * ld + col, dtype, vec, n);
+}
+// The eight columns that act_load has loaded.  (Shifted: the whole warp, converged.)
+template <int MODE>
+__device__ __forceinline__ void act_ready(Raw8& r, const void* p, long long row, long long ld, int col)
+{
+    if (MODE == kActShifted) r.a = join_shifted({r.a, r.b}, reinterpret_cast<uintptr_t>(p) + 2 * (uintptr_t)(row * ld + col));
 }
 template <int MODE>
 __device__ __forceinline__ void act_unpack(const Raw8& r, int dtype, float (&f)[8])
@@ -704,7 +720,7 @@ __device__ __forceinline__ void act_unpack(const Raw8& r, int dtype, float (&f)[
 }
 
 template <bool BWD, int MODE>
-__global__ void __launch_bounds__(kActThreads, MODE == kActAny ? 2 : 4) activation_kernel(const __grid_constant__ ActParams p)
+__global__ void __launch_bounds__(kActThreads, MODE == kActAny ? 2 : BWD && MODE == kActShifted ? 3 : 4) activation_kernel(const __grid_constant__ ActParams p)
 {
     // Rows in flight, as many as leave four blocks of an SM their registers (16384 x 4096: forward 88 us
     // with two, 92 with four and three blocks, 92 with one; gradient 103 with one, 111 with two).
@@ -737,10 +753,12 @@ __global__ void __launch_bounds__(kActThreads, MODE == kActAny ? 2 : 4) activati
                 if (r >= r1) continue;
                 float v[8], z[8];
                 if (p.x) {
+                    act_ready<MODE>(x[i], p.x, r, p.ldx, col);
                     act_unpack<MODE>(x[i], p.x_dtype, z);
                     add8(bias, z);
                 }
                 if (BWD) {
+                    act_ready<MODE>(o[i], p.dy, r, p.lddy, col);
                     act_unpack<MODE>(o[i], p.dy_dtype, v);
                     slope8(t.act, z, v);
                 } else {
@@ -750,6 +768,7 @@ __global__ void __launch_bounds__(kActThreads, MODE == kActAny ? 2 : 4) activati
                 }
                 if (t.thr) drop8(t, offset, r, col >> 3, v);
                 if (!BWD && t.res) {
+                    act_ready<MODE>(o[i], t.res, r, t.ldr, col);
                     act_unpack<MODE>(o[i], t.y_dtype, z);
                     gain8(t.gain, z, v);
                 } else {

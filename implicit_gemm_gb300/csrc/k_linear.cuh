@@ -126,6 +126,21 @@ __device__ __forceinline__ void load_offsets(int experts, const void* offsets, i
     __syncthreads();
 }
 
+// used[0 .. count - 1]: the experts that have rows.  The first warp; the block synchronises after it.
+__device__ __forceinline__ int list_used(const int* off, int n, short* used)
+{
+    const int lane = threadIdx.x & 31;
+    int c = 0;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const int i = i0 + lane;
+        const bool has = i < n && off[i + 1] > off[i];
+        const uint32_t b = __ballot_sync(0xffffffffu, has);
+        if (has) used[c + __popc(b & ((1u << lane) - 1u))] = (short)i;
+        c += __popc(b);
+    }
+    return c;
+}
+
 // The last i with first[i] <= v, i < n (first ascending, first[0] <= v): empty experts have the
 // same first as the one after them, and the one that holds v is the last of those.
 __device__ __forceinline__ int find_last(const int* first, int n, int v)
@@ -673,14 +688,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) linear_rows_kernel(const __gr
     load_offsets(p.experts, p.offsets, p.offsets64, p.tokens, off);
     const int n = max(p.experts, 1);
     if (warp == 0) {
-        int c = 0;
-        for (int i0 = 0; i0 < n; i0 += 32) {
-            const int i = i0 + lane;
-            const bool has = i < n && off[i + 1] > off[i];
-            const uint32_t b = __ballot_sync(0xffffffffu, has);
-            if (has) used[c + __popc(b & ((1u << lane) - 1u))] = (short)i;
-            c += __popc(b);
-        }
+        const int c = list_used(off, n, used);
         if (lane == 0) count = c;
     }
     __syncthreads();
@@ -776,24 +784,45 @@ struct PackParams {
     unsigned short* out;
     long long rows, ld, bs;
     int batch, cols, ldp;
-    long long segments;  // rows by 256 columns, of all
+    int segments;        // rows by 256 columns, of a matrix (fewer than 2^31 fit any memory)
+    FastDiv by_per, by_segments;
 };
-__global__ void __launch_bounds__(256) linear_pack_kernel(const __grid_constant__ PackParams a, const __grid_constant__ PackParams b)
+// b has one matrix; of a's, experts' weights, those are copied whose expert has rows.
+__global__ void __launch_bounds__(256) linear_pack_kernel(const __grid_constant__ PackParams a, const __grid_constant__ PackParams b,
+                                                          const void* offsets, int is64, long long tokens)
 {
+    __shared__ int off[kLinMaxExperts + 1];
+    __shared__ short used[kLinMaxExperts];
+    __shared__ int count;
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31;
-    const long long step = (long long)gridDim.x * (blockDim.x / 32);
-    for (long long i = (long long)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; i < a.segments + b.segments; i += step) {
-        const bool first = i < a.segments;
+    long long matrices = a.batch;
+    if (a.batch > 1) {
+        load_offsets(a.batch, offsets, is64, tokens, off);
+        if (threadIdx.x < 32) {
+            const int c = list_used(off, a.batch, used);
+            if (lane == 0) count = c;
+        }
+        __syncthreads();
+        matrices = count;
+    }
+    const long long step = (long long)gridDim.x * (blockDim.x / 32), of_a = matrices * a.segments;
+    for (long long i = (long long)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; i < of_a + b.segments; i += step) {
+        const bool first = i < of_a;
         const PackParams& p = first ? a : b;
-        const long long n = first ? i : i - a.segments;
-        const int per = (p.cols + 255) / 256;
-        const long long r = n / per, m = p.batch > 1 ? r / p.rows : 0;
-        const int j = 256 * (int)(n - r * per) + 8 * lane;
-        const uintptr_t row = reinterpret_cast<uintptr_t>(p.in + m * p.bs + (r - m * p.rows) * p.ld);
-        const uint4 v = load_shifted(row + 2 * (uintptr_t)j, row + 2 * (uintptr_t)p.cols);
-        if (j < p.cols) *reinterpret_cast<uint4*>(p.out + r * p.ldp + j) = v;
+        int n = (int)(first ? i : i - of_a);
+        long long m = 0;
+        if (first && a.batch > 1) {
+            const int k = div_by(n, a.by_segments);
+            n -= k * a.segments;
+            m = used[k];
+        }
+        const long long r = div_by(n, p.by_per);
+        const int j = 256 * (n - (int)r * ((p.cols + 255) / 256)) + 8 * lane;
+        const uintptr_t row = reinterpret_cast<uintptr_t>(p.in + m * p.bs + r * p.ld), from = row + 2 * (uintptr_t)j;
+        const uint4 v = join_shifted(fetch_shifted(from, row + 2 * (uintptr_t)p.cols), from);
+        if (j < p.cols) *reinterpret_cast<uint4*>(p.out + (m * p.rows + r) * p.ldp + j) = v;
     }
 }
 
@@ -817,6 +846,7 @@ template <int MODE>
 __global__ void __launch_bounds__(256, 4) column_sum_kernel(const __grid_constant__ ColumnParams p)
 {
     __shared__ int off[kLinMaxExperts + 1], first[kLinMaxExperts + 1];
+    constexpr int kAhead = MODE == kActWide ? 8 : 4;  // rows in flight per thread
     __shared__ float s[8][256];
     pdl_wait();
     pdl_launch_dependents();  // (after the wait: see LinParams::early)
@@ -850,16 +880,17 @@ __global__ void __launch_bounds__(256, 4) column_sum_kernel(const __grid_constan
         const int r0 = off[e] + (p.part ? (c - first[e]) * p.chunk : 0), r1 = p.part ? min(off[e + 1], r0 + p.chunk) : off[e + 1];
         float sum[8] = {};
         if (m > 0 || MODE == kActShifted)
-            for (int r = r0 + ty; r < r1; r += 8 * ny) {
-                uint4 x[8];
+            for (int r = r0 + ty; r < r1; r += kAhead * ny) {
+                Raw8 x[kAhead];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (r + i * ny < r1) x[i] = act_load<MODE>(p.dy, r + i * ny, p.ld, col, m, p.N, p.dtype, false).a;
+                for (int i = 0; i < kAhead; ++i)
+                    if (r + i * ny < r1) x[i] = act_load<MODE>(p.dy, r + i * ny, p.ld, col, m, p.N, p.dtype, false);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < kAhead; ++i) {
                     if (r + i * ny >= r1) continue;
                     float v[8];
-                    act_unpack<kActWide>({x[i], x[i]}, p.dtype, v);
+                    act_ready<MODE>(x[i], p.dy, r + i * ny, p.ld, col);
+                    act_unpack<kActWide>(x[i], p.dtype, v);
                     add8(v, sum);
                 }
             }

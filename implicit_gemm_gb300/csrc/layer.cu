@@ -234,6 +234,11 @@ int lin_plan(const wg_linear_problem* p, int call, LinPlan* pl)
     const long long used = weight ? ne : std::min<long long>(ne, n);
     pl->ldp = (pl->M + 7) / 8 * 8;
     pl->part_rows = weight ? (long long)ne * q.out : q.tokens;
+    // us of what follows the products of a tile of 256 x 256, measured with short sums: its stores (2.0
+    // in 16 bits, 3 in 32), an activation 2, dropout 4; twice that in the kernel for long sums of fp32 results.
+    double tail256 = q.out_dtype == WG_FP32 ? 3.0 : 2.0;
+    if (!weight) tail256 += (q.activation != WG_ACT_NONE ? 2.0 : 0.0) + (q.dropout > 0.f ? 4.0 : 0.0);
+    if (q.out_dtype == WG_FP32 && pl->kb > kChunkFp32) tail256 *= 2.0;
     double best = 1e30;
     for (int bt = 256; bt >= 32; bt -= 32) {
         const int least = (int)std::min<long long>((rows + 31) / 32 * 32, 256);
@@ -242,9 +247,11 @@ int lin_plan(const wg_linear_problem* p, int call, LinPlan* pl)
         const long long tiles = std::max(1LL, im * along);
         for (int s = 1; s <= 16; ++s) {
             if (s > 1 && (tiles * s > 2 * pl->pairs || pl->kb < 4 * s)) break;
+            // A pair's tiles: the products of one beside what follows those of the tile before.
             const double rounds = (double)((tiles * s + pl->pairs - 1) / pl->pairs);
-            double t = rounds * ((pl->kb + s - 1) / s) * block_us(bt) + 3.0 + 0.5 * rounds;
-            if (s > 1) t += 3.0 + (double)s * pl->part_rows * pl->ldp * 8 / 5e6;
+            const double main = ((pl->kb + s - 1) / s) * block_us(bt), tail = s > 1 ? 1.5 : 1.0 + (tail256 - 1.0) * bt / 256;
+            double t = 3.0 + rounds * std::max(main, tail) + std::min(main, tail);
+            if (s > 1) t += 3.0 + (double)s * pl->part_rows * pl->ldp * 8 / 1e7;
             if (t < best - 1e-9) best = t, pl->bt = bt, pl->split = s;
         }
     }
@@ -298,8 +305,9 @@ struct LinOperand {
 };
 wg::PackParams lin_pack(LinOperand* o, char* to)
 {
+    const int per = (o->cols + 255) / 256, segments = (int)(o->rows * per);
     wg::PackParams k = {static_cast<const unsigned short*>(o->p), reinterpret_cast<unsigned short*>(to), o->rows, o->ld, o->bs,
-                        (int)o->batch, o->cols, (o->cols + 7) / 8 * 8, o->rows * o->batch * ((o->cols + 255) / 256)};
+                        (int)o->batch, o->cols, (o->cols + 7) / 8 * 8, segments, wg::fast_div((unsigned)per), wg::fast_div((unsigned)segments)};
     o->p = to, o->ld = k.ldp, o->bs = o->rows * k.ldp;
     return k;
 }
@@ -371,10 +379,10 @@ int lin_run(const LinPlan& pl, const void* offsets, LinOperand a, LinOperand b, 
         wg::PackParams ka = {}, kb = {};
         if (pl.pack_a) ka = lin_pack(&a, ws + pl.off_a);
         if (pl.pack_b) kb = lin_pack(&b, ws + pl.off_b);
-        const long long segments = ka.segments + kb.segments;
+        const long long segments = (long long)ka.segments * ka.batch + kb.segments;
         if (segments > 0)
-            st = launch("linear_pack_kernel launch", wg::linear_pack_kernel,
-                        dim3((unsigned)std::min<long long>((segments + 7) / 8, 8LL * num_sms())), dim3(256), s, ka, kb);
+            st = launch("linear_pack_kernel launch", wg::linear_pack_kernel, dim3((unsigned)std::min<long long>((segments + 7) / 8, 8LL * num_sms())),
+                        dim3(256), s, ka, kb, offsets, (int)(q.offset_bits == 64), q.tokens);
     } else {
         a.p = b.p = ws, a.ld = b.ld = 8LL * (kMaxFeatures / 8), a.rows = b.rows = 1, a.batch = 1, a.bs = a.ld;  // (never read)
     }
@@ -637,7 +645,7 @@ int wg_linear_bwd_weight(const wg_linear_problem* p, const void* offsets, const 
     c.out = dbias, c.out_dtype = q.bias_dtype, c.accumulate = accumulate != 0;
     // Few rows: 64 columns and every row of an expert per block (512 x 1000 with the product 10 us instead of 12).
     const bool vec = vec_rows(dy, q.ld_out, q.out, ie);
-    const bool once = vec && q.tokens <= 1024 && ne * ((q.out + 63LL) / 64) <= 4LL * num_sms();
+    const bool once = q.tokens <= (vec ? 1024 : 256) && ne * ((q.out + 63LL) / 64) <= 4LL * num_sms();
     if (once) c.part = nullptr;
     const int groups = (q.out + 7) / 8;
     c.cx_log = std::min(once ? 3 : 5, log2_floor(groups) + ((groups & (groups - 1)) ? 1 : 0));
