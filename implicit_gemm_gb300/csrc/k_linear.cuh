@@ -652,29 +652,44 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Eight elements k .. k + 7 of a row of `end` elements (zeros behind it; none of a row that is not there).
-template <bool WIDE>
+// Eight elements k .. k + 7 (k a multiple of 8) of a row of `end` elements, zeros behind it and of a
+// row that is not there.  VEC 8 and 2: rows whose starts and lengths are multiples of VEC, in
+// accesses of VEC elements; 1: rows that start anywhere, in the aligned pairs around the
+// elements (one by one, 3840 rows of 3917 took 37 us; those of 3918 in pairs 12).
+template <int VEC>
 __device__ __forceinline__ uint4 rows_load(const unsigned short* row, int k, int end, bool stream)
 {
     uint4 r = make_uint4(0u, 0u, 0u, 0u);
     if (!row || k >= end) return r;
-    if (WIDE) {
+    if (VEC == 8) {
         if (stream)
             asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(row + k));
         else
             r = __ldg(reinterpret_cast<const uint4*>(row + k));
         return r;
     }
-    uint32_t h[8];
+    const int odd = VEC == 1 ? (int)(reinterpret_cast<uintptr_t>(row) >> 1 & 1) : 0;
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(row + k - odd);
+    const int n = end - k;
+    uint32_t w[5] = {};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = k + i < end ? __ldg(row + k + i) : 0;
-    return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+    for (int i = 0; i < 4; ++i)
+        if (2 * i - odd < n) w[i] = __ldg(p + i);
+    if (VEC == 1) {
+        if (odd && n > 7) w[4] = __ldg(p + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = __funnelshift_r(w[i], w[i + 1], 16 * odd);
+            w[i] = 2 * i + 1 < n ? w[i] : 2 * i < n ? w[i] & 0xffffu : 0u;
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int XR, int FG, bool BF16, bool WIDE>
+template <int XR, int FG, bool BF16, int VEC>
 __global__ void __launch_bounds__(kRowsThreads, 2) linear_rows_kernel(const __grid_constant__ RowsParams p)
 {
-    constexpr int kAhead = XR == 1 && FG == 2 ? 3 : 2;  // steps of a batch: two of them fill 128 registers
+    constexpr int kAhead = VEC == 8 && XR == 1 && FG == 2 ? 3 : 2;  // steps of a batch: two of them fill 128 registers
     struct Batch {
         uint4 w[kAhead][FG], x[kAhead][XR];
     };
@@ -712,9 +727,9 @@ __global__ void __launch_bounds__(kRowsThreads, 2) linear_rows_kernel(const __gr
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) {
 #pragma unroll
-                    for (int f = 0; f < FG; ++f) c.w[u][f] = rows_load<WIDE>(wrow[f], k + 256 * u + 8 * tig, p.K, true);
+                    for (int f = 0; f < FG; ++f) c.w[u][f] = rows_load<VEC>(wrow[f], k + 256 * u + 8 * tig, p.K, true);
 #pragma unroll
-                    for (int m = 0; m < XR; ++m) c.x[u][m] = rows_load<WIDE>(xrow[m], k + 256 * u + 8 * tig, p.K, false);
+                    for (int m = 0; m < XR; ++m) c.x[u][m] = rows_load<VEC>(xrow[m], k + 256 * u + 8 * tig, p.K, false);
                 }
             };
             const auto multiply = [&](const Batch& c) {

@@ -409,12 +409,12 @@ int lin_run(const LinPlan& pl, const void* offsets, LinOperand a, LinOperand b, 
     }
 }
 
-template <int XR, int FG, bool WIDE>
+template <int XR, int FG, int VEC>
 int rows_launch(const wg::RowsParams& g, bool bf16, cudaStream_t s)
 {
     const long long items = (long long)std::max(1, std::min<int>(std::max(g.experts, 1), (int)g.tokens)) * ((g.M + 8 * FG - 1) / (8 * FG));
     const dim3 grid((unsigned)std::min<long long>(items, 8LL * num_sms()));
-    return launch("linear_rows_kernel launch", bf16 ? wg::linear_rows_kernel<XR, FG, true, WIDE> : wg::linear_rows_kernel<XR, FG, false, WIDE>,
+    return launch("linear_rows_kernel launch", bf16 ? wg::linear_rows_kernel<XR, FG, true, VEC> : wg::linear_rows_kernel<XR, FG, false, VEC>,
                   grid, dim3(wg::kRowsThreads), s, g);
 }
 int rows_run(const LinPlan& pl, const void* offsets, const void* x, const void* w, const wg::LayerTail& tail, cudaStream_t s)
@@ -423,16 +423,22 @@ int rows_run(const LinPlan& pl, const void* offsets, const void* x, const void* 
     wg::RowsParams g = {};
     g.t = tail, g.experts = q.experts, g.offsets64 = q.offset_bits == 64, g.offsets = offsets, g.tokens = q.tokens;
     g.x = x, g.w = w, g.ldx = q.ld_in, g.ldw = q.ld_weight, g.wstride = q.weight_stride, g.K = q.in, g.M = q.out;
-    const bool wide = q.in % 8 == 0 && q.ld_in % 8 == 0 && q.ld_weight % 8 == 0 && (q.experts <= 1 || q.weight_stride % 8 == 0) &&
-                      aligned16(x) && aligned16(w);
-    const bool bf16 = q.in_dtype == WG_BF16;
-    const bool one = q.tokens <= 8 || q.experts > 1;
-    if (!wide) return one ? rows_launch<1, 1, false>(g, bf16, s) : rows_launch<2, 1, false>(g, bf16, s);
-    if (!one) return rows_launch<2, 2, true>(g, bf16, s);
+    const auto rows_of = [&](int v) {
+        return q.in % v == 0 && q.ld_in % v == 0 && q.ld_weight % v == 0 && (q.experts <= 1 || q.weight_stride % v == 0) &&
+               aligned_to(x, 2 * v) && aligned_to(w, 2 * v);
+    };
+    const bool bf16 = q.in_dtype == WG_BF16, one = q.tokens <= 8 || q.experts > 1;
+    const long long used = std::min<long long>(std::max(q.experts, 1), q.tokens);
+    const auto many = [&](int columns) { return 2 * ((q.out + columns - 1) / columns) * used >= 3LL * num_sms(); };  // CTAs
+    if (!rows_of(8)) {
+        if (rows_of(2)) return one ? rows_launch<1, 2, 2>(g, bf16, s) : rows_launch<2, 2, 2>(g, bf16, s);
+        if (!one) return rows_launch<2, 2, 1>(g, bf16, s);
+        return many(16) ? rows_launch<1, 2, 1>(g, bf16, s) : rows_launch<1, 1, 1>(g, bf16, s);
+    }
+    if (!one) return rows_launch<2, 2, 8>(g, bf16, s);
     // 32 columns of the result per CTA where those are enough CTAs (8192 x 8192 23.5 us against 24.7
     // with 16, 4096 x 16384 25.1 against 27.4), else 16 (4096 x 4096 9.2 against 11.7).
-    const long long wide_items = (q.out + 31) / 32 * std::min<long long>(std::max(q.experts, 1), q.tokens);
-    return 2 * wide_items >= 3 * num_sms() ? rows_launch<1, 4, true>(g, bf16, s) : rows_launch<1, 2, true>(g, bf16, s);
+    return many(32) ? rows_launch<1, 4, 8>(g, bf16, s) : rows_launch<1, 2, 8>(g, bf16, s);
 }
 
 int lin_offsets(const LinPlan& pl, const void* offsets)
