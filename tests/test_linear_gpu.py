@@ -460,3 +460,51 @@ def test_memory_of_a_call_on_another_stream():
         got = f(stream=s)
         torch.cuda.synchronize()
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("xat,wat", [(0, 0), (2, 4), (1, 0), (0, 3), (5, 7)])
+@pytest.mark.parametrize("tokens,inf,out,pad,counts", [(1, 1000, 130, 0, None), (1, 1002, 130, 2, None), (1, 1001, 67, 0, None),
+                                                       (7, 70, 200, 1, None), (13, 515, 72, 1, None), (16, 1030, 72, 4, None),
+                                                       (2, 7, 9, 1, None), (3, 1, 5, 0, None), (9, 518, 40, 0, [3, 0, 5]),
+                                                       (15, 261, 33, 2, [0, 14]), (8, 264, 24, 0, [1, 1, 1, 4])])
+def test_few_rows_that_start_anywhere(tokens, inf, out, pad, counts, xat, wat):
+    """Rows of even and odd lengths, starts and strides, for one weight and for experts'; NaN all around them."""
+    n = len(counts) if counts else 1
+    ld, wstride = inf + pad, out * (inf + pad) + 3
+    aligned = ld % 8 == 0 and (n == 1 or wstride % 8 == 0)
+    if aligned and (xat or wat):
+        xat, wat = 8 * xat, 8 * wat
+    xb, wb = (torch.full((k,), float("nan"), dtype=DT["fp16"], device="cuda") for k in (64 + tokens * ld, 64 + n * wstride))
+    x = torch.as_strided(xb, (tokens, inf), (ld, 1), xat)
+    w = torch.as_strided(wb, (n, out, inf), (wstride, ld, 1), wat)
+    x.copy_(randn(1, tokens, inf, dt="fp16"))
+    w.copy_(randn(2, n, out, inf, size=inf ** -0.5, dt="fp16"))
+    off = offsets_of(counts) if counts else None
+    y = torch.full((tokens, out), 7.0, device="cuda")
+    sp = {"tokens": tokens, "in": inf, "out": out, "experts": n if counts else 0, "ld_in": ld, "ld_weight": ld,
+          "weight_stride": wstride, "in_dtype": "fp16", "out_dtype": "fp32"}
+    assert "linear_rows" in binding.wg_linear_plan_string(sp)
+    binding.wg_linear(sp, x, w, y, offsets=off, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    _, (want, err) = forward(x, w, offsets=off.tolist() if counts else None)
+    used = slice(0, sum(counts) if counts else tokens)
+    close(y[used], want[used], err[used], "fp32")
+    assert bool((y[used.stop:] == 7).all())
+
+
+@pytest.mark.parametrize("counts", [[0, 40, 0, 0, 61, 0], [0, 0, 0], [17, 0, 0, 0, 0, 0, 0, 90]])
+def test_weights_of_experts_without_rows_are_not_read(counts):
+    """Unaligned weights go through copies, of the experts that have rows only; the others' may hold anything."""
+    n, inf, out = len(counts), 333, 77
+    off = offsets_of(counts, 4)
+    rows = int(off[-1]) + 40
+    x, dy, w = randn(1, rows, inf, dt="bf16"), randn(2, rows, out, dt="bf16"), randn(3, n, out, inf, size=0.05, dt="bf16")
+    for e, c in enumerate(counts):
+        if c == 0:
+            w[e] = float("nan")
+    offs, used = off.tolist(), slice(4, rows - 40)
+    y = binding.linear(x, w, offsets=off)
+    _, (want, err) = forward(x, w, offsets=offs)
+    close(y[used], want[used], err[used], "bf16")
+    dx = binding.linear_bwd_data(dy, w, offsets=off)
+    want, err = data(dy, w, offsets=offs)
+    close(dx[used], want[used], err[used], "bf16")
