@@ -676,7 +676,7 @@ __device__ __forceinline__ void store_shifted(uintptr_t a, uintptr_t end, const 
 constexpr int kActThreads = 256;
 enum ActMode {
     kActWide,     // 16-bit tensors, every chunk of eight columns on 16 bytes
-    kActShifted,  // 16-bit tensors, rows of more than 248 columns that start anywhere
+    kActShifted,  // 16-bit tensors, rows of more than 128 columns (a warp is in one row) that start anywhere
     kActAny,      // any types and alignment
 };
 

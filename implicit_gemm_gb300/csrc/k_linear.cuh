@@ -4,7 +4,7 @@
 //   kData:     dx[t, k] = sum over n of dy[t, n] w[e, n, k]
 //   kWeight:   dw[e, n, k] = sum over the rows t of e of dy[t, n] x[t, k]
 //
-// with layer_tail's bias, activation, dropout and residual on the finished sums.
+// with the bias, activation, dropout and residual of a layer's tail on the finished sums.
 //
 // On CTA pairs (tcgen05 .cta_group::2).  The MMA's 256 rows are columns of the result
 // (features), its columns are rows of the result (tokens; of dw the n): the number of MMA
@@ -262,6 +262,10 @@ __device__ __forceinline__ void tma_load_3d_at(void* dst, const CUtensorMap* tm,
         : "memory");
 }
 
+// Whether every lane's wait has ended as it should: where one has run out of time the warp stops as one
+// (lanes that went on alone would be missed at the next barrier).
+__device__ __forceinline__ bool all_waited(bool mine) { return __all_sync(0xffffffffu, mine); }
+
 // 16 consecutive 32-bit columns of this warp's 32 tensor-memory lanes.  Whole warp, converged.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16])
 {
@@ -396,14 +400,14 @@ __global__ void __launch_bounds__(lin_threads(CHUNKED), 1)
                     const uint32_t idesc = make_idesc_f16(p.bf16, kAmn, kBmn, 256, t.wide);
                     for (int c0 = t.k0; ok && c0 < t.k1; c0 += p.chunk, ++use) {
                         const int buf = use & 1, c1 = min(t.k1, c0 + p.chunk);
-                        if (!mbar_wait(&acce[buf], ((uint32_t)(use >> 1) & 1u) ^ 1u)) {
+                        if (!all_waited(mbar_wait(&acce[buf], ((uint32_t)(use >> 1) & 1u) ^ 1u))) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
                         const uint32_t d = tbase + (uint32_t)(buf * 256);
                         for (int k = c0; k < c1; ++k) {
-                            if (!mbar_wait(&full[st], ph)) {
+                            if (!all_waited(mbar_wait(&full[st], ph))) {
                                 ok = false;
                                 break;
                             }
@@ -440,9 +444,8 @@ __global__ void __launch_bounds__(lin_threads(CHUNKED), 1)
                     const int last = (st + n - 1) % p.stages;
                     st = (st + n) % p.stages;
                     if (t.valid == 64 || 64 * t.k1 <= rows) continue;
-                    ok = mbar_wait_sleep(&tail[last], (seen >> last) & 1u);
+                    ok = all_waited(mbar_wait_sleep(&tail[last], (seen >> last) & 1u));
                     seen ^= 1u << last;
-                    __syncwarp();
                     if (!ok) break;
                     uint8_t* s = smem + last * p.stage_bytes;
                     const int zeros = ((t.valid + 15) >> 4 << 4) - t.valid;  // rows, of 8 chunks of 16 bytes each
@@ -480,8 +483,7 @@ __global__ void __launch_bounds__(lin_threads(CHUNKED), 1)
                 // where the last one was: no register of it is held while what follows is computed.
                 float acc[kOwn][16];
                 for (int k = t.k0;;) {
-                    if (!mbar_wait_sleep(&accf[use & 1], (uint32_t)(use >> 1) & 1u)) ok = false;
-                    __syncwarp();
+                    ok = all_waited(mbar_wait_sleep(&accf[use & 1], (uint32_t)(use >> 1) & 1u));
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t tacc = trow + (uint32_t)((use & 1) * 256);
@@ -519,8 +521,7 @@ __global__ void __launch_bounds__(lin_threads(CHUNKED), 1)
                     ++use;
                 }
             } else if (t.k0 < t.k1) {
-                if (!mbar_wait_sleep(&accf[use & 1], (uint32_t)(use >> 1) & 1u)) ok = false;
-                __syncwarp();
+                ok = all_waited(mbar_wait_sleep(&accf[use & 1], (uint32_t)(use >> 1) & 1u));
                 tc_fence_after();
             }
             if (!ok) break;

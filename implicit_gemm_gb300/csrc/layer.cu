@@ -482,7 +482,7 @@ int act_plan(const wg_activation_problem* p, ActPlan* pl)
     const long long want = std::max(1LL, 12LL * num_sms() / cols);
     long long rows = std::max(ny, (q.tokens + want - 1) / want);
     rows = (rows + ny - 1) / ny * ny;
-    if (rows > ny) rows = (rows + 4 * ny - 1) / (4 * ny) * (4 * ny);  // (four rows in flight)
+    if (rows > ny) rows = (rows + 4 * ny - 1) / (4 * ny) * (4 * ny);  // (whole rounds of the rows in flight)
     rows = std::max(rows, ((q.tokens + 65534) / 65535 + ny - 1) / ny * ny);
     pl->chunk = (int)rows;
     pl->chunks = std::max(1LL, (q.tokens + rows - 1) / rows);

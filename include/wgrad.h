@@ -495,8 +495,10 @@ typedef enum {
  * rounded by itself, y is made from the unrounded v.  The tensor cores add with
  * truncation: 1024 terms at a time for an fp32 result (which takes at most 6e-6 of a sum
  * of equal signs), 32768 for a 16-bit one (2e-4, 0.4 of fp16's rounding); those sums are
- * added rounded to nearest.  Results are bitwise reproducible.  Rows and experts do not
- * touch one another's results, infinities and NaN included.
+ * added rounded to nearest.  An activation is within 2^-20 (|v| + 1) of its formula, a slope
+ * within 2^-19; where v or z is infinite they are what the formula gives in fp32 or its limit.
+ * Results are bitwise reproducible.  Rows and experts do not touch one another's results,
+ * infinities and NaN included.
  *
  *  tokens 0..2^31-65536, in and out 1..2^20, experts 0..1024; at most 2^31 - 1 tiles of
  *    256 features by 32 rows.
