@@ -580,12 +580,13 @@ __device__ __forceinline__ void column_tail(const LayerTail& t, unsigned long lo
 // ---------------------------------------------------------------- rows that start anywhere
 // Eight 16-bit elements per lane of a row whose lanes' elements follow one another, in aligned
 // 16-byte accesses: a lane's elements are parts of two of them, of which the second is the
-// next lane's first.  (An element at a time: eight times the requests, 5001 x 2047 in fp16
-// 80 us.)  `a` is the address of the lane's first element, `end` that of the row's end; chunks
-// that hold no element of the row are not touched.  The whole warp, converged.
+// next lane's first.  Both are loaded (the second comes from L1; taken from the next lane by
+// shuffles, the gradient of 5001 x 2047 in fp16 took 35 us instead of 33; an element at a time, eight
+// times the requests, 80).  `a` is the address of the lane's first element, `end` that of the row's
+// end; chunks that hold no element of the row are not touched.
 // In two steps, so that the loads of several rows are in flight before the first is waited for.
 struct Fetched {
-    uint4 x, l;  // the lane's aligned chunk, and (the last lane) the one behind it
+    uint4 x, l;  // the lane's aligned chunk, and the one behind it
 };
 __device__ __forceinline__ Fetched fetch_shifted(uintptr_t a, uintptr_t end)
 {
@@ -593,27 +594,17 @@ __device__ __forceinline__ Fetched fetch_shifted(uintptr_t a, uintptr_t end)
     Fetched f;
     f.x = f.l = make_uint4(0u, 0u, 0u, 0u);
     if (c < end) f.x = *reinterpret_cast<const uint4*>(c);
-    if ((threadIdx.x & 31) == 31 && (a & 15) && c + 16 < end) f.l = *reinterpret_cast<const uint4*>(c + 16);
+    if ((a & 15) && c + 16 < end) f.l = *reinterpret_cast<const uint4*>(c + 16);
     return f;
 }
 __device__ __forceinline__ uint4 join_shifted(const Fetched& f, uintptr_t a)
 {
     const uint4 &x = f.x, &l = f.l;
-    const uint32_t s = (uint32_t)(a & 15);  // the same for every lane
-    if (s == 0) return x;
-    const bool last = (threadIdx.x & 31) == 31;
-    const auto next = [&](uint32_t own, uint32_t behind) {
-        const uint32_t y = __shfl_down_sync(0xffffffffu, own, 1);
-        return last ? behind : y;
-    };
-    const uint32_t h = (s & 2u) * 8u, y0 = next(x.x, l.x);
-    if (s < 4) return make_uint4(__funnelshift_r(x.x, x.y, h), __funnelshift_r(x.y, x.z, h), __funnelshift_r(x.z, x.w, h), __funnelshift_r(x.w, y0, h));
-    const uint32_t y1 = next(x.y, l.y);
-    if (s < 8) return make_uint4(__funnelshift_r(x.y, x.z, h), __funnelshift_r(x.z, x.w, h), __funnelshift_r(x.w, y0, h), __funnelshift_r(y0, y1, h));
-    const uint32_t y2 = next(x.z, l.z);
-    if (s < 12) return make_uint4(__funnelshift_r(x.z, x.w, h), __funnelshift_r(x.w, y0, h), __funnelshift_r(y0, y1, h), __funnelshift_r(y1, y2, h));
-    const uint32_t y3 = next(x.w, l.w);
-    return make_uint4(__funnelshift_r(x.w, y0, h), __funnelshift_r(y0, y1, h), __funnelshift_r(y1, y2, h), __funnelshift_r(y2, y3, h));
+    const uint32_t s = (uint32_t)(a & 15), h = (s & 2u) * 8u;  // (the same for every lane)
+    if (s < 4) return make_uint4(__funnelshift_r(x.x, x.y, h), __funnelshift_r(x.y, x.z, h), __funnelshift_r(x.z, x.w, h), __funnelshift_r(x.w, l.x, h));
+    if (s < 8) return make_uint4(__funnelshift_r(x.y, x.z, h), __funnelshift_r(x.z, x.w, h), __funnelshift_r(x.w, l.x, h), __funnelshift_r(l.x, l.y, h));
+    if (s < 12) return make_uint4(__funnelshift_r(x.z, x.w, h), __funnelshift_r(x.w, l.x, h), __funnelshift_r(l.x, l.y, h), __funnelshift_r(l.y, l.z, h));
+    return make_uint4(__funnelshift_r(x.w, l.x, h), __funnelshift_r(l.x, l.y, h), __funnelshift_r(l.y, l.z, h), __funnelshift_r(l.z, l.w, h));
 }
 
 // Those of the eight halves at c that lie in [begin, end).
@@ -625,6 +616,7 @@ __device__ __forceinline__ void store_halves(uintptr_t c, const uint4& v, uintpt
     for (int i = 0; i < 8; ++i)
         if (2 * i >= lo && 2 * i < hi) *reinterpret_cast<unsigned short*>(c + 2 * i) = (unsigned short)(i & 1 ? w[i >> 1] >> 16 : w[i >> 1]);
 }
+// (Stores take the lane before's last bytes by shuffles: the whole warp, converged.)
 __device__ __forceinline__ void store_shifted(uintptr_t a, uintptr_t end, const uint4& x)
 {
     const uint32_t s = (uint32_t)(a & 15);
@@ -706,7 +698,7 @@ __device__ __forceinline__ Raw8 act_load(const void* p, long long row, long long
     }
     return load_raw8(p, row * ld + col, dtype, vec, n);
 }
-// The eight columns that act_load has loaded.  (Shifted: the whole warp, converged.)
+// The eight columns that act_load has loaded.
 template <int MODE>
 __device__ __forceinline__ void act_ready(Raw8& r, const void* p, long long row, long long ld, int col)
 {
@@ -733,7 +725,7 @@ __global__ void __launch_bounds__(kActThreads, MODE == kActAny ? 2 : BWD && MODE
     pdl_wait();
     const unsigned long long offset = layer_offset(t);
     if (t.bias && n > 0) unpack8(load_raw8(t.bias, col, t.bias_dtype, t.vec & kVecBias, n), t.bias_dtype, bias);
-    if (n > 0 || MODE == kActShifted) {  // (there, lanes behind the row's end hold what the last ones shift in)
+    if (n > 0 || MODE == kActShifted) {  // (there, lanes behind the row's end store what is left of the last ones')
         const long long r1 = min(p.rows, (long long)(blockIdx.y + 1) * p.chunk);
         for (long long r0 = (long long)blockIdx.y * p.chunk + ty; r0 < r1; r0 += kRows * ny) {
             Raw8 x[kRows], o[kRows];
