@@ -136,3 +136,48 @@ def test_many_rows_of_one_column():
     close(dx, want, 2.0 ** -23 * want.abs(), "fp32")
     # At most 128 + 2 * 2048 roundings along any way through the sums.
     assert abs(float(db) - float(want.sum())) < 4500 * 2.0 ** -24 * float(want.abs().sum())
+
+
+@pytest.mark.parametrize("dim,pad,at", [(129, 0, (0, 0, 0)), (255, 1, (1, 2, 3)), (257, 2, (7, 0, 5)), (999, 0, (3, 3, 3)),
+                                        (1000, 4, (4, 1, 6)), (2047, 1, (0, 5, 2)), (264, 0, (1, 1, 1))])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_long_rows_that_start_anywhere(dim, pad, at, dt):
+    """16-bit rows at every distance from 16 bytes, in place and not; what lies around the rows stays as it is."""
+    rows, ld = 83, dim + pad
+
+    def place(t, k):
+        buf = randn(9, 16 + rows * ld, dt=dt)
+        view = torch.as_strided(buf, (rows, dim), (ld, 1), k)
+        view.copy_(t)
+        return buf, view
+
+    def check(buf, view, want, err):
+        rest = buf.clone()
+        torch.as_strided(rest, (rows, dim), (ld, 1), view.storage_offset()).zero_()
+        clean = randn(9, 16 + rows * ld, dt=dt)
+        torch.as_strided(clean, (rows, dim), (ld, 1), view.storage_offset()).zero_()
+        assert torch.equal(rest, clean)
+        close(view, want, err, dt)
+
+    x0, r0, bias = randn(1, rows, dim, size=2, dt=dt), randn(2, rows, dim, dt=dt), randn(3, dim)
+    sp = {"tokens": rows, "dim": dim, "ld_x": ld, "ld_y": ld, "ld_residual": ld, "ld_dx": ld, "in_dtype": dt, "out_dtype": dt,
+          "activation": "silu", "dropout": 0.2, "seed": SEED, "offset": OFFSET}
+    v = x0.double() + bias.double()
+    want, err = value("silu", v, 0.2, r0)
+    grad = slope("silu", v) * r0.double()
+    gerr = (2.0 ** -19 + 1.6 * 2.0 ** -24 * v.abs()) * r0.double().abs()
+    grad, gain = drop(grad, 0.2, SEED, OFFSET)
+    gerr = gerr * gain + 2.0 ** -23 * grad.abs()
+    ws = torch.empty(binding.wg_activation_workspace_size(sp), dtype=torch.uint8, device="cuda")
+    for over in ("", "x", "other"):
+        (xb, x), (rb, r), (yb, y) = place(x0, at[0]), place(r0, at[1]), place(torch.zeros_like(x0), at[2])
+        b, t = {"": (yb, y), "x": (xb, x), "other": (rb, r)}[over]
+        binding.wg_activation(sp, x, t, bias, r)
+        check(b, t, want, err)
+        (xb, x), (rb, r) = place(x0, at[0]), place(r0, at[1])
+        b, t = {"": (yb, y), "x": (xb, x), "other": (rb, r)}[over]
+        db = torch.full((dim,), float("nan"), device="cuda")
+        binding.wg_activation_bwd(sp, r, x, t, bias, db, ws)
+        check(b, t, grad, gerr)
+        # dbias: fewer than 256 roundings of sums that are at most the sum of the terms' sizes.
+        close(db, grad.sum(0), gerr.sum(0) + 256 * 2.0 ** -24 * grad.abs().sum(0), "fp32", "dbias")
