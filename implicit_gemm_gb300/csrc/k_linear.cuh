@@ -653,46 +653,71 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Eight elements k .. k + 7 (k a multiple of 8) of a row of `end` elements, zeros behind it and of a
-// row that is not there.  VEC 8 and 2: rows whose starts and lengths are multiples of VEC, in
-// accesses of VEC elements; 1: rows that start anywhere, in the aligned pairs around the
-// elements (one by one, 3840 rows of 3917 took 37 us; those of 3918 in pairs 12).
+// Eight elements k .. k + 7 (k a multiple of 8) of a row of `end` elements, in two steps: as they lie in
+// memory, to be in flight, and then in their places, zeros behind the row and of a row that is not
+// there.  VEC 8 and 2: rows whose starts and lengths are multiples of VEC, in accesses of VEC elements;
+// 1: rows that start anywhere, as the two aligned chunks that hold the eight (7168 rows of 8191
+// 50 us; in the pairs around them 100.  8192 rows of 8190 33 us in pairs, 44 in chunks).
 template <int VEC>
-__device__ __forceinline__ uint4 rows_load(const unsigned short* row, int k, int end, bool stream)
+struct RowsRaw {
+    uint4 a;
+};
+template <>
+struct RowsRaw<1> {
+    uint4 a, b;
+};
+template <int VEC>
+__device__ __forceinline__ RowsRaw<VEC> rows_load(const unsigned short* row, int k, int end, bool stream)
 {
-    uint4 r = make_uint4(0u, 0u, 0u, 0u);
+    RowsRaw<VEC> r = {};
     if (!row || k >= end) return r;
-    if (VEC == 8) {
+    if constexpr (VEC == 8) {
         if (stream)
-            asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(row + k));
+            asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.a.x), "=r"(r.a.y), "=r"(r.a.z), "=r"(r.a.w) : "l"(row + k));
         else
-            r = __ldg(reinterpret_cast<const uint4*>(row + k));
-        return r;
+            r.a = __ldg(reinterpret_cast<const uint4*>(row + k));
+    } else if constexpr (VEC == 2) {
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(row + k);
+        r.a.x = __ldg(p);
+        if (k + 2 < end) r.a.y = __ldg(p + 1);
+        if (k + 4 < end) r.a.z = __ldg(p + 2);
+        if (k + 6 < end) r.a.w = __ldg(p + 3);
+    } else {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(row + k), c = at & ~(uintptr_t)15;
+        r.a = __ldg(reinterpret_cast<const uint4*>(c));
+        if (c != at && c + 16 < reinterpret_cast<uintptr_t>(row + end)) r.b = __ldg(reinterpret_cast<const uint4*>(c + 16));
     }
-    const int odd = VEC == 1 ? (int)(reinterpret_cast<uintptr_t>(row) >> 1 & 1) : 0;
-    const uint32_t* p = reinterpret_cast<const uint32_t*>(row + k - odd);
-    const int n = end - k;
-    uint32_t w[5] = {};
+    return r;
+}
+template <int VEC>
+__device__ __forceinline__ uint4 rows_take(const RowsRaw<VEC>& r, const unsigned short* row, int k, int end)
+{
+    if constexpr (VEC > 1) {
+        return r.a;
+    } else {
+        const uint32_t s = (uint32_t)reinterpret_cast<uintptr_t>(row) & 15u;  // (each row its own)
+        const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+        uint32_t v[6], u[5], o[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (2 * i - odd < n) w[i] = __ldg(p + i);
-    if (VEC == 1) {
-        if (odd && n > 7) w[4] = __ldg(p + 4);
+        for (int i = 0; i < 6; ++i) v[i] = s & 8u ? w[i + 2] : w[i];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            w[i] = __funnelshift_r(w[i], w[i + 1], 16 * odd);
-            w[i] = 2 * i + 1 < n ? w[i] : 2 * i < n ? w[i] & 0xffffu : 0u;
+        for (int i = 0; i < 5; ++i) u[i] = s & 4u ? v[i + 1] : v[i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = __funnelshift_r(u[i], u[i + 1], (s & 2u) * 8u);
+        if (k + 8 > end) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = k + 2 * i + 1 < end ? o[i] : k + 2 * i < end ? o[i] & 0xffffu : 0u;
         }
+        return make_uint4(o[0], o[1], o[2], o[3]);
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <int XR, int FG, bool BF16, int VEC>
 __global__ void __launch_bounds__(kRowsThreads, 2) linear_rows_kernel(const __grid_constant__ RowsParams p)
 {
-    constexpr int kAhead = VEC == 8 && XR == 1 && FG == 2 ? 3 : 2;  // steps of a batch: two of them fill 128 registers
+    constexpr int kAhead = VEC == 1 ? 1 : VEC == 8 && XR == 1 && FG == 2 ? 3 : 2;  // steps of a batch: two of them fill 128 registers
     struct Batch {
-        uint4 w[kAhead][FG], x[kAhead][XR];
+        RowsRaw<VEC> w[kAhead][FG], x[kAhead][XR];
     };
     __shared__ int off[kLinMaxExperts + 1];
     __shared__ short used[kLinMaxExperts];  // experts that have rows
@@ -733,15 +758,18 @@ __global__ void __launch_bounds__(kRowsThreads, 2) linear_rows_kernel(const __gr
                     for (int m = 0; m < XR; ++m) c.x[u][m] = rows_load<VEC>(xrow[m], k + 256 * u + 8 * tig, p.K, false);
                 }
             };
-            const auto multiply = [&](const Batch& c) {
+            const auto multiply = [&](const Batch& c, int k) {
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) {
-                    const uint4 x0 = c.x[u][0], x1 = XR > 1 ? c.x[u][XR - 1] : make_uint4(0u, 0u, 0u, 0u);
+                    const int at = k + 256 * u + 8 * tig;
+                    const uint4 x0 = rows_take<VEC>(c.x[u][0], xrow[0], at, p.K);
+                    const uint4 x1 = XR > 1 ? rows_take<VEC>(c.x[u][XR - 1], xrow[XR - 1], at, p.K) : make_uint4(0u, 0u, 0u, 0u);
                     const uint32_t lo[4] = {x0.x, x1.x, x0.y, x1.y}, hi[4] = {x0.z, x1.z, x0.w, x1.w};
 #pragma unroll
                     for (int f = 0; f < FG; ++f) {
-                        mma16816<BF16>(d[f], lo, c.w[u][f].x, c.w[u][f].y);
-                        mma16816<BF16>(d[f], hi, c.w[u][f].z, c.w[u][f].w);
+                        const uint4 v = rows_take<VEC>(c.w[u][f], wrow[f], at, p.K);
+                        mma16816<BF16>(d[f], lo, v.x, v.y);
+                        mma16816<BF16>(d[f], hi, v.z, v.w);
                     }
                 }
             };
@@ -766,10 +794,10 @@ __global__ void __launch_bounds__(kRowsThreads, 2) linear_rows_kernel(const __gr
             while (k < p.K) {
                 if (k >= next) put(), next += kPut;
                 if (k + kStep < p.K) load(b1, k + kStep);
-                multiply(b0);
+                multiply(b0, k);
                 if ((k += kStep) >= p.K) break;
                 if (k + kStep < p.K) load(b0, k + kStep);
-                multiply(b1);
+                multiply(b1, k);
                 k += kStep;
             }
             put();

@@ -167,11 +167,13 @@ constexpr int kChunkFp32 = 16, kChunk16 = 512;
 
 // Rows up to which the forward product is linear_rows_kernel's: eight at a time; 16 of one
 // weight matrix below 64 MB (4096 x 4096 for 9 rows 9.7 us against 14.1 on the tensor-core tiles,
-// 4096 x 16384 for 16 rows 31 against 25; 32 experts' 2048 x 1024 for 32 rows 24 against 26).
+// 4096 x 16384 for 16 rows 31 against 25; 32 experts' 2048 x 1024 for 32 rows 24 against 26), or one that
+// the tiles would need a copy of (12 rows of 8191 x 7168 61 against 75, of 8190 x 8192 39 against 84).
 constexpr int kFewRows = 16;
 bool few_rows(const wg_linear_problem& q)
 {
-    return q.tokens <= 8 || (q.tokens <= kFewRows && (q.experts > 1 || (long long)q.in * q.out < (32LL << 20)));
+    return q.tokens <= 8 ||
+           (q.tokens <= kFewRows && (q.experts > 1 || (long long)q.in * q.out < (32LL << 20) || q.ld_in % 8 || q.ld_weight % 8));
 }
 
 // us of a block of 64 of a tile's sum on every pair at once, by the tile's MMA columns
@@ -430,15 +432,13 @@ int rows_run(const LinPlan& pl, const void* offsets, const void* x, const void* 
     const bool bf16 = q.in_dtype == WG_BF16, one = q.tokens <= 8 || q.experts > 1;
     const long long used = std::min<long long>(std::max(q.experts, 1), q.tokens);
     const auto many = [&](int columns) { return 2 * ((q.out + columns - 1) / columns) * used >= 3LL * num_sms(); };  // CTAs
-    if (!rows_of(8)) {
-        if (rows_of(2)) return one ? rows_launch<1, 2, 2>(g, bf16, s) : rows_launch<2, 2, 2>(g, bf16, s);
-        if (!one) return rows_launch<2, 2, 1>(g, bf16, s);
-        return many(16) ? rows_launch<1, 2, 1>(g, bf16, s) : rows_launch<1, 1, 1>(g, bf16, s);
-    }
-    if (!one) return rows_launch<2, 2, 8>(g, bf16, s);
     // 32 columns of the result per CTA where those are enough CTAs (8192 x 8192 23.5 us against 24.7
-    // with 16, 4096 x 16384 25.1 against 27.4), else 16 (4096 x 4096 9.2 against 11.7).
-    return many(32) ? rows_launch<1, 4, 8>(g, bf16, s) : rows_launch<1, 2, 8>(g, bf16, s);
+    // with 16, 4096 x 16384 25.1 against 27.4, 8000 rows of 999 9.4 against 11.3), else 16 (4096 x 4096 9.2
+    // against 11.7).
+    if (rows_of(8)) return !one ? rows_launch<2, 2, 8>(g, bf16, s) : many(32) ? rows_launch<1, 4, 8>(g, bf16, s) : rows_launch<1, 2, 8>(g, bf16, s);
+    if (rows_of(2)) return one ? rows_launch<1, 2, 2>(g, bf16, s) : rows_launch<2, 2, 2>(g, bf16, s);
+    if (!one) return rows_launch<2, 2, 1>(g, bf16, s);
+    return many(32) ? rows_launch<1, 4, 1>(g, bf16, s) : many(16) ? rows_launch<1, 2, 1>(g, bf16, s) : rows_launch<1, 1, 1>(g, bf16, s);
 }
 
 int lin_offsets(const LinPlan& pl, const void* offsets)
