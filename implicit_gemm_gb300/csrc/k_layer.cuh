@@ -808,6 +808,7 @@ struct SumParams {
     int ny_log;
     int chunks;            // of a problem without experts
     const int* first;      // [experts + 1] chunks before each expert's, or null
+    int across, units;     // blocks of threads along the columns, and of all experts (where another kernel does it)
 };
 // A finished sum into element i of dbias, or added to it.
 __device__ __forceinline__ void put_sum(void* out, long long i, int dtype, bool accumulate, float a)
@@ -824,23 +825,31 @@ __device__ __forceinline__ void put_sum(void* out, long long i, int dtype, bool 
     }
 }
 
-__global__ void __launch_bounds__(kJoinThreads) column_join_kernel(const __grid_constant__ SumParams p)
+// Block bx along the columns of expert e's, by THREADS threads that `sync` brings together; s: a float each.
+template <int THREADS, typename Sync>
+__device__ __forceinline__ void column_join(const SumParams& p, int tid, int bx, int e, float* s, Sync sync)
 {
-    pdl_launch_dependents();
-    __shared__ float s[kJoinThreads];
-    const int nx = kJoinThreads >> p.ny_log, ny = 1 << p.ny_log, tx = threadIdx.x & (nx - 1), ty = threadIdx.x / nx;
-    const int j = blockIdx.x * nx + tx, e = blockIdx.y;
-    pdl_wait();
+    const int nx = THREADS >> p.ny_log, ny = 1 << p.ny_log, tx = tid & (nx - 1), ty = tid / nx;
+    const int j = bx * nx + tx;
     const int c0 = p.first ? p.first[e] : 0, c1 = p.first ? p.first[e + 1] : p.chunks;
     float a = 0.f;
     if (j < p.dim)
 #pragma unroll 8
         for (int c = c0 + ty; c < c1; c += ny) a += p.part[(long long)c * p.dim + j];
-    s[threadIdx.x] = a;
-    __syncthreads();
-    if (ty || j >= p.dim || (p.accumulate && c0 == c1)) return;
-    for (int y = 1; y < ny; ++y) a += s[y * nx + tx];
-    put_sum(p.out, (long long)e * p.dim + j, p.dtype, p.accumulate, a);
+    s[tid] = a;
+    sync();
+    if (ty == 0 && j < p.dim && !(p.accumulate && c0 == c1)) {
+        for (int y = 1; y < ny; ++y) a += s[y * nx + tx];
+        put_sum(p.out, (long long)e * p.dim + j, p.dtype, p.accumulate, a);
+    }
+}
+
+__global__ void __launch_bounds__(kJoinThreads) column_join_kernel(const __grid_constant__ SumParams p)
+{
+    pdl_launch_dependents();
+    __shared__ float s[kJoinThreads];
+    pdl_wait();
+    column_join<kJoinThreads>(p, threadIdx.x, blockIdx.x, blockIdx.y, s, [] { __syncthreads(); });
 }
 
 }  // namespace wg

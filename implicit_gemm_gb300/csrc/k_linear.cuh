@@ -92,6 +92,8 @@ struct LinParams {
     int early;              // the kernel before has waited for those before it, and nothing here is its result
     float* part;            // [split][rows][ldp] sums of parts (split > 1)
     long long ldp, part_rows;
+    SumParams sums;         // kWeight: dbias's parts, joined at the end (of linear_join_kernel where there is one), or none
+    int join_blocks;        // of linear_join_kernel, that join parts of the product
 };
 
 // ---------------------------------------------------------------- experts' rows
@@ -565,6 +567,17 @@ __global__ void __launch_bounds__(lin_threads(CHUNKED), 1)
                 ++use;
             }
         }
+        if (KIND == kWeight && p.split == 1 && p.sums.part && e < 8) {
+            // dbias, by the first eight of these warps (the others have few registers): 2 us here, 4 in a launch of its own.
+            // The pair's MMAs and loads are over, so the ring is free.
+            pdl_wait();
+            const auto sync = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+            float* s = reinterpret_cast<float*>(smem);
+            for (int u = blockIdx.x; u < p.sums.units; u += gridDim.x) {
+                column_join<256>(p.sums, threadIdx.x - 32 * kLinDirect, u % p.sums.across, u / p.sums.across, s, sync);
+                sync();
+            }
+        }
     }
     // (This one is complete only after the one before it: the next waits for this one alone.)
     if (p.early && threadIdx.x == 0) pdl_wait();
@@ -588,10 +601,15 @@ __global__ void __launch_bounds__(kJoinBlock) linear_join_kernel(const __grid_co
     __shared__ int off[kLinMaxExperts + 1];
     pdl_launch_dependents();
     pdl_wait();
+    if (KIND == kWeight && (int)blockIdx.x >= p.join_blocks) {
+        const int u = (int)blockIdx.x - p.join_blocks;
+        column_join<kJoinBlock>(p.sums, threadIdx.x, u % p.sums.across, u / p.sums.across, reinterpret_cast<float*>(off), [] { __syncthreads(); });
+        return;
+    }
     if (KIND != kWeight) load_offsets(p.experts, p.offsets, p.offsets64, p.tokens, off);
     const unsigned long long offset = layer_offset(p.t);
     const int groups = (p.M + 7) / 8, experts = max(p.experts, 1);
-    const long long total = p.part_rows * groups, step = (long long)gridDim.x * blockDim.x;
+    const long long total = p.part_rows * groups, step = (long long)p.join_blocks * blockDim.x;
     for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += step) {
         const long long r = i / groups;
         const int j = 8 * (int)(i - r * groups), n = min(8, p.M - j);
@@ -934,7 +952,7 @@ __global__ void __launch_bounds__(256, 4) column_sum_kernel(const __grid_constan
         const int e = p.part ? find_last(first, n, c) : c;
         const int r0 = off[e] + (p.part ? (c - first[e]) * p.chunk : 0), r1 = p.part ? min(off[e + 1], r0 + p.chunk) : off[e + 1];
         float sum[8] = {};
-        if (m > 0 || MODE == kActShifted)
+        if (m > 0)
             for (int r = r0 + ty; r < r1; r += kAhead * ny) {
                 Raw8 x[kAhead];
 #pragma unroll

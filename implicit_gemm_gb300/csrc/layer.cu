@@ -138,12 +138,16 @@ int log2_floor(long long n)
 }
 
 // dbias of `experts` from `chunks` partial sums in all; as many threads a column as leave each some four.
+void plan_join(wg::SumParams* m, int experts, long long chunks, int threads)
+{
+    m->ny_log = std::min(5, log2_floor(std::max(1LL, chunks / experts / 4)));
+    const int nx = threads >> m->ny_log;
+    m->across = (m->dim + nx - 1) / nx, m->units = m->across * experts;
+}
 int join_columns(wg::SumParams m, int experts, long long chunks, cudaStream_t s)
 {
-    m.ny_log = std::min(5, log2_floor(std::max(1LL, chunks / experts / 4)));
-    const int nx = wg::kJoinThreads >> m.ny_log;
-    return launch("column_join_kernel launch", wg::column_join_kernel, dim3((unsigned)((m.dim + nx - 1) / nx), (unsigned)experts),
-                  dim3(wg::kJoinThreads), s, m);
+    plan_join(&m, experts, chunks, wg::kJoinThreads);
+    return launch("column_join_kernel launch", wg::column_join_kernel, dim3((unsigned)m.across, (unsigned)experts), dim3(wg::kJoinThreads), s, m);
 }
 
 // ---------------------------------------------------------------- products
@@ -352,9 +356,8 @@ int lin_launch(const LinPlan& pl, const wg::LinParams& g, const LinOperand& a, c
     const cudaError_t e = cudaLaunchKernelEx(&cfg, wg::linear_product_kernel<KIND, CHUNKED>, ma, mb, g);
     if (e != cudaSuccess) return cuda_fail("linear_product_kernel launch", e);
     if (pl.split == 1) return WG_OK;
-    const long long items = g.part_rows * (g.ldp / 8);
     return launch("linear_join_kernel launch", wg::linear_join_kernel<KIND>,
-                  dim3((unsigned)std::min<long long>((items + wg::kJoinBlock - 1) / wg::kJoinBlock, 16LL * num_sms())), dim3(wg::kJoinBlock), s, g);
+                  dim3((unsigned)(g.join_blocks + (g.sums.part ? g.sums.units : 0))), dim3(wg::kJoinBlock), s, g);
 }
 
 int columns_launch(const wg::ColumnParams& c, const LinPlan& pl, cudaStream_t s)
@@ -371,7 +374,7 @@ int columns_launch(const wg::ColumnParams& c, const LinPlan& pl, cudaStream_t s)
 // w, or x of the weight gradient, is operand a (MMA rows); the other operand b.  sums: dbias's partial sums,
 // made before the product, which need not wait for them.
 int lin_run(const LinPlan& pl, const void* offsets, LinOperand a, LinOperand b, const wg::LayerTail& tail, char* ws, cudaStream_t s,
-            const wg::ColumnParams* sums = nullptr)
+            const wg::ColumnParams* sums = nullptr, wg::SumParams* joined = nullptr)
 {
     const wg_linear_problem& q = pl.p;
     if (!pl.pack_a && !aligned16(a.p)) return set_err(WG_ERR_MISALIGNED, "x, w or dy with 16-byte strides must be 16-byte aligned");
@@ -401,6 +404,15 @@ int lin_run(const LinPlan& pl, const void* offsets, LinOperand a, LinOperand b, 
     g.by_bt = wg::fast_div((unsigned)pl.bt), g.by_im = wg::fast_div(im), g.by_8im = wg::fast_div(8 * im);
     g.by_per = wg::fast_div(im * (unsigned)((std::max(pl.N, 1) + pl.bt - 1) / pl.bt));
     g.part = reinterpret_cast<float*>(ws + pl.off_part), g.ldp = pl.ldp, g.part_rows = pl.part_rows;
+    const long long items = g.part_rows * (g.ldp / 8);
+    g.join_blocks = (int)std::min<long long>((items + wg::kJoinBlock - 1) / wg::kJoinBlock, 16LL * num_sms());
+    if (joined && joined->part) {
+        // In the last launch, where one round of its blocks does it (64 experts' 2048 columns are 512 units).
+        wg::SumParams m = *joined;
+        const int ne = std::max(q.experts, 1);
+        plan_join(&m, ne, pl.sum_chunks, pl.split > 1 ? wg::kJoinBlock : wg::kJoinThreads);
+        if (m.units <= (pl.split > 1 ? 4 * num_sms() : 2 * pl.pairs)) g.sums = m, joined->part = nullptr;
+    }
     // Blocks of the longest sum (a part's, or an expert's that has every row).
     const long long blocks = pl.call == WG_LINEAR_BWD_WEIGHT ? (q.tokens + 63) / 64 : pl.kb;
     const bool chunked = (blocks + pl.split - 1) / pl.split > g.chunk;
@@ -655,12 +667,12 @@ int wg_linear_bwd_weight(const wg_linear_problem* p, const void* offsets, const 
     if (once) c.part = nullptr;
     const int groups = (q.out + 7) / 8;
     c.cx_log = std::min(once ? 3 : 5, log2_floor(groups) + ((groups & (groups - 1)) ? 1 : 0));
-    st = lin_run(pl, offsets, {x, q.tokens, q.in, q.ld_in, 1, 0}, {dy, q.tokens, q.out, q.ld_out, 1, 0}, g, ws, s, dbias ? &c : nullptr);
-    if (st || !dbias || once) return st;
     wg::SumParams m = {};
-    m.part = c.part, m.out = dbias, m.dim = q.out, m.dtype = q.bias_dtype, m.accumulate = accumulate != 0;
-    m.first = c.first;
-    return join_columns(m, ne, pl.sum_chunks, s);
+    if (!once) m.part = c.part;
+    m.out = dbias, m.dim = q.out, m.dtype = q.bias_dtype, m.accumulate = accumulate != 0, m.first = c.first;
+    st = lin_run(pl, offsets, {x, q.tokens, q.in, q.ld_in, 1, 0}, {dy, q.tokens, q.out, q.ld_out, 1, 0}, g, ws, s, dbias ? &c : nullptr,
+                 dbias ? &m : nullptr);
+    return st || !dbias || !m.part ? st : join_columns(m, ne, pl.sum_chunks, s);
 }
 
 int wg_activation_workspace_size(const wg_activation_problem* p, size_t* bytes)
