@@ -366,8 +366,7 @@ int columns_launch(const wg::ColumnParams& c, const LinPlan& pl, cudaStream_t s)
     const int groups = (c.N + 7) / 8;
     const long long cols = (groups + (1 << c.cx_log) - 1) >> c.cx_log;
     const long long rows = c.part ? std::min(pl.sum_chunks, (4LL * num_sms() + cols - 1) / cols) : std::max(c.experts, 1);
-    const auto kernel = vec ? wg::column_sum_kernel<wg::kActWide>
-                            : c.cx_log == 5 ? wg::column_sum_kernel<wg::kActShifted> : wg::column_sum_kernel<wg::kActAny>;
+    const auto kernel = vec ? wg::column_sum_kernel<wg::kActWide> : wg::column_sum_kernel<wg::kActShifted>;
     return launch("column_sum_kernel launch", kernel, dim3((unsigned)cols, (unsigned)std::max(1LL, rows)), dim3(256), s, c);
 }
 
@@ -661,9 +660,9 @@ int wg_linear_bwd_weight(const wg_linear_problem* p, const void* offsets, const 
     c.experts = q.experts, c.offsets64 = q.offset_bits == 64, c.offsets = offsets, c.chunk = pl.sum_rows;
     c.part = reinterpret_cast<float*>(ws + pl.off_sum), c.first = reinterpret_cast<int*>(ws + pl.off_first);
     c.out = dbias, c.out_dtype = q.bias_dtype, c.accumulate = accumulate != 0;
-    // Few rows: 64 columns and every row of an expert per block (512 x 1000 with the product 10 us instead of 12).
-    const bool vec = vec_rows(dy, q.ld_out, q.out, ie);
-    const bool once = q.tokens <= (vec ? 1024 : 256) && ne * ((q.out + 63LL) / 64) <= 4LL * num_sms();
+    // Few rows: 64 columns and every row of an expert per block (1000 x 2048 with the product 12.2 us against 14.7 with
+    // parts; rows that start anywhere, 300 x 1515 11.1 against 13.4, but 700 x 2047 20.3 against 17.0).
+    const bool once = q.tokens <= (vec_rows(dy, q.ld_out, q.out, ie) ? 1024 : 512) && ne * ((q.out + 63LL) / 64) <= 4LL * num_sms();
     if (once) c.part = nullptr;
     const int groups = (q.out + 7) / 8;
     c.cx_log = std::min(once ? 3 : 5, log2_floor(groups) + ((groups & (groups - 1)) ? 1 : 0));
