@@ -508,3 +508,57 @@ def test_weights_of_experts_without_rows_are_not_read(counts):
     dx = binding.linear_bwd_data(dy, w, offsets=off)
     want, err = data(dy, w, offsets=offs)
     close(dx[used], want[used], err[used], "bf16")
+
+
+@pytest.mark.parametrize("tokens,inf,out,experts", [(5000, 64, 264, 0), (3000, 520, 640, 0), (5000, 96, 333, 7), (600, 136, 1000, 0),
+                                                    (2500, 72, 2000, 40), (4100, 1001, 77, 0)])
+def test_gradients_of_what_the_call_before_wrote(tokens, inf, out, experts):
+    """dy, dw and dbias are written and read by one call after another without a pause, as in a captured step: the results
+    are those of calls that wait for each other."""
+    off = offsets_of([tokens // experts] * experts, 1) if experts else None
+    n = max(experts, 1)
+    x, w = randn(1, tokens, inf, dt="bf16"), randn(2, n, out, inf, size=0.1, dt="bf16")
+    zs, gs = [randn(3 + i, tokens, out, dt="bf16") for i in range(2)], [randn(5 + i, tokens, out, dt="bf16") for i in range(2)]
+    dy, dw, db = torch.empty_like(zs[0]), torch.empty(n, out, inf, device="cuda"), torch.empty(n, out, device="cuda")
+    dx = torch.zeros(tokens, inf, dtype=DT["bf16"], device="cuda")
+    sa = {"tokens": tokens, "dim": out, "activation": "silu"}
+    sp = {"tokens": tokens, "in": inf, "out": out, "experts": experts, "out_dtype": "fp32"}
+    sd = dict(sp, out_dtype="bf16")
+    ws = torch.empty(max(binding.wg_linear_workspace_size(sp, "bwd_weight"), binding.wg_linear_workspace_size(sd, "bwd_data")),
+                     dtype=torch.uint8, device="cuda")
+    calls = []
+    for i in range(2):
+        calls += [binding.PreparedActivationBwd(sa, gs[i], zs[i], dy),
+                  binding.PreparedLinearBwdWeight(sp, x, dy, dw, dbias=db, accumulate=i == 1, offsets=off, workspace=ws),
+                  binding.PreparedLinearBwdData(sd, dy, w, dx, offsets=off, workspace=ws)]
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for c in calls:
+        c(st.cuda_stream)
+        torch.cuda.synchronize()
+    want = [t.clone() for t in (dw, db, dx)]
+    for t in (dw, db, dx, dy):
+        t.fill_(float("nan") if t is not dx else 0.0)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c in calls:
+            c(st.cuda_stream)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip((dw, db, dx), want))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for c in calls:
+            c(torch.cuda.current_stream().cuda_stream)
+    for t in (dw, db, dx, dy):
+        t.fill_(float("nan") if t is not dx else 0.0)
+    for _ in range(5):
+        g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip((dw, db, dx), want))
+    (wdw, werr), (wdb, berr) = [0, 0], [0, 0]
+    for i in range(2):
+        d = binding.activation_bwd(gs[i], zs[i], activation="silu")
+        (a, b), (c, e) = weight(x, d, off.tolist() if experts else None, n)
+        wdw, werr, wdb, berr = wdw + a, werr + b, wdb + c, berr + e
+    close(dw, wdw, werr + 2.0 ** -22 * wdw.abs() + 2.0 ** -23 * werr, "fp32", "dw")
+    close(db, wdb, berr + 2.0 ** -22 * wdb.abs(), "fp32", "dbias")
