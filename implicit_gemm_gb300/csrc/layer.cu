@@ -171,13 +171,16 @@ constexpr int kChunkFp32 = 16, kChunk16 = 512;
 
 // Rows up to which the forward product is linear_rows_kernel's: eight at a time; 16 of one
 // weight matrix below 64 MB (4096 x 4096 for 9 rows 9.7 us against 14.1 on the tensor-core tiles,
-// 4096 x 16384 for 16 rows 31 against 25; 32 experts' 2048 x 1024 for 32 rows 24 against 26), or one that
-// the tiles would need a copy of (12 rows of 8191 x 7168 61 against 75, of 8190 x 8192 39 against 84).
-constexpr int kFewRows = 16;
+// 4096 x 16384 for 16 rows 31 against 25; 32 experts' 2048 x 1024 for 32 rows 24 against 26).  Where the tiles
+// would need a copy of the weights, 16 of any matrix (12 rows of 8191 x 7168 61 against 75, of 8190 x 8192 39
+// against 84) and 64 of experts with eight each at most on average (20 rows of 4 experts' 3918 x 3840 42
+// against 80, 64 of 16 experts' 2047 x 2048 49 against 78, of 8 experts' 999 x 4000 42 against 46).
+constexpr int kFewRows = 16, kFewCopied = 64;
 bool few_rows(const wg_linear_problem& q)
 {
-    return q.tokens <= 8 ||
-           (q.tokens <= kFewRows && (q.experts > 1 || (long long)q.in * q.out < (32LL << 20) || q.ld_in % 8 || q.ld_weight % 8));
+    const bool copied = q.ld_in % 8 || q.ld_weight % 8 || (q.experts > 1 && q.weight_stride % 8);
+    return q.tokens <= 8 || (q.tokens <= kFewRows && (q.experts > 1 || (long long)q.in * q.out < (32LL << 20) || copied)) ||
+           (copied && q.tokens <= std::min(kFewCopied, 8 * q.experts));
 }
 
 // us of a block of 64 of a tile's sum on every pair at once, by the tile's MMA columns

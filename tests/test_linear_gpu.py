@@ -562,3 +562,18 @@ def test_gradients_of_what_the_call_before_wrote(tokens, inf, out, experts):
         wdw, werr, wdb, berr = wdw + a, werr + b, wdb + c, berr + e
     close(dw, wdw, werr + 2.0 ** -22 * wdw.abs() + 2.0 ** -23 * werr, "fp32", "dw")
     close(db, wdb, berr + 2.0 ** -22 * wdb.abs(), "fp32", "dbias")
+
+
+@pytest.mark.parametrize("counts", [[64, 0, 0, 0, 0, 0, 0, 0], [0, 7, 9, 0, 17, 8, 0, 22], [1] * 8, [20, 0, 21]])
+def test_few_rows_of_experts_with_unaligned_weights(counts):
+    """Up to 64 rows, of one expert or of many, in passes of eight."""
+    n, inf, out, rows = len(counts), 517, 90, sum(counts)
+    off = offsets_of(counts)
+    x, w, bias, res = randn(1, rows, inf, dt="bf16"), randn(2, n, out, inf, size=0.05, dt="bf16"), randn(3, n, out), randn(4, rows, out, dt="bf16")
+    for e, c in enumerate(counts):
+        if c == 0:
+            w[e] = float("nan")
+    y, z = binding.linear(x, w, bias, res, "gelu_tanh", 0.2, SEED, OFFSET, offsets=off, keep_z=True)
+    (v, verr), (want, err) = forward(x, w, bias, res, "gelu_tanh", 0.2, SEED, OFFSET, off.tolist())
+    close(z, v, verr, "bf16", "z")
+    close(y, want, err, "bf16", "y")
