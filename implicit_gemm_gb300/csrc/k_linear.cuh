@@ -899,9 +899,9 @@ __global__ void __launch_bounds__(256) linear_pack_kernel(const __grid_constant_
 }
 
 // ---------------------------------------------------------------- bias gradients
-// Sums of dy's columns over an expert's rows: all of them by one block, which writes dbias (no
-// launch to join parts: few rows, beside the product), or `chunk` rows at a time to
-// part[chunk][N], with how many chunks come before each expert's (first, written by one block).
+// Sums of dy's columns over an expert's rows, beside the product: all of them by one block, which
+// writes dbias (few rows), or `chunk` rows at a time to part[chunk][N], with how many chunks come
+// before each expert's (first, written by one block), which column_join adds up at the end.
 // HBM's reads bound it, eight rows a thread in flight (8192 x 16384 46 us, 5.8 TB/s).
 struct ColumnParams {
     const void* dy;
