@@ -429,7 +429,8 @@ template <int XR, int FG, int VEC>
 int rows_launch(const wg::RowsParams& g, bool bf16, cudaStream_t s)
 {
     const long long items = (long long)std::max(1, std::min<int>(std::max(g.experts, 1), (int)g.tokens)) * ((g.M + 8 * FG - 1) / (8 * FG));
-    const dim3 grid((unsigned)std::min<long long>(items, 8LL * num_sms()));
+    // (What an SM holds: 4 rows of 16 experts' 1024 x 4096 12.0 us against 12.6 with four times that.)
+    const dim3 grid((unsigned)std::min<long long>(items, 2LL * num_sms()));
     return launch("linear_rows_kernel launch", bf16 ? wg::linear_rows_kernel<XR, FG, true, VEC> : wg::linear_rows_kernel<XR, FG, false, VEC>,
                   grid, dim3(wg::kRowsThreads), s, g);
 }
