@@ -115,13 +115,19 @@ __device__ __forceinline__ F2 add(F2 a, F2 b)
     return r;
 }
 
-// 1 / (1 + exp(-a)).
-__device__ __forceinline__ F2 sigmoid2(F2 a)
+// 1 / (1 + exp(-a)), and e = exp(-a).
+__device__ __forceinline__ F2 sigmoid2(F2 a, F2& e)
 {
     float x, y;
     split(mul(a, both(-1.4426950408889634f)), x, y);
-    split(add(f2(exp2_f(x), exp2_f(y)), both(1.f)), x, y);
+    e = f2(exp2_f(x), exp2_f(y));
+    split(add(e, both(1.f)), x, y);
     return f2(rcp_f(x), rcp_f(y));
+}
+__device__ __forceinline__ F2 sigmoid2(F2 a)
+{
+    F2 e;
+    return sigmoid2(a, e);
 }
 
 // gelu's tanh form is v sigmoid(2 u): (1 + tanh u) / 2 is sigmoid(2 u).  (The exponential is off by
@@ -183,7 +189,9 @@ __device__ __forceinline__ F2 gelu2(F2 v)
 }
 __device__ __forceinline__ F2 gelu_tanh2(F2 v) { return mul(v, sigmoid2(mul(v, fma(both(0.0713548162726f), square2(v), both(1.59576912161f))))); }
 __device__ __forceinline__ F2 silu2(F2 v) { return mul(v, sigmoid2(v)); }
-// Its slope: of v sigmoid(w), s (1 + v w' (1 - s)).
+// Its slope: of v sigmoid(w), s (1 + v w' (1 - s)).  With gelu's w, v w' reaches 35 where s is still below 1: there
+// 1 - s is taken as exp(-w) s, whose error is of its own size (subtracted from 1 it left the slope 1.002 times
+// 2^-19 off at 4.962).  The power is held below 2^100, where s has long been 0, so that no 0 meets an infinity.
 __device__ __forceinline__ F2 gelu_slope2(F2 v)
 {
     float a, b;
@@ -193,8 +201,11 @@ __device__ __forceinline__ F2 gelu_slope2(F2 v)
 }
 __device__ __forceinline__ F2 gelu_tanh_slope2(F2 v)
 {
-    const F2 q = square2(v), s = sigmoid2(mul(v, fma(both(0.0713548162726f), q, both(1.59576912161f))));
-    const F2 r = mul(mul(v, s), fma(s, both(-1.f), both(1.f)));
+    F2 e;
+    const F2 q = square2(v), s = sigmoid2(mul(v, fma(both(0.0713548162726f), q, both(1.59576912161f))), e);
+    float x, y;
+    split(e, x, y);
+    const F2 r = mul(mul(v, s), mul(f2(fminf(x, 0x1p100f), fminf(y, 0x1p100f)), s));
     return fma(r, fma(both(0.2140644488178f), q, both(1.59576912161f)), s);
 }
 __device__ __forceinline__ F2 silu_slope2(F2 v)
