@@ -75,6 +75,18 @@ inline FastDiv fast_div(unsigned d)
 }
 __device__ __forceinline__ int div_by(int n, const FastDiv& f) { return (int)(((uint64_t)(unsigned)n * f.mul) >> f.shift); }
 
+// Sums of dy's columns over few rows, made by the weight gradient's own epilogue warps while the first tile's
+// products run: 64 columns of an expert at a time.  (A kernel of its own before the product costs 2 to 7 us more,
+// because the product has to wait for it: what the calls before have written is promised to be seen only by a
+// kernel that has waited for them itself.)
+struct FewSums {
+    const void* dy;
+    long long ld;
+    void* out;              // [experts][N]
+    int dtype, out_dtype, accumulate, vec;
+    int across, units;      // of 64 columns, and of all experts; units 0: none
+};
+
 struct LinParams {
     LayerTail t;
     int experts;            // 0: one weight, every row
@@ -89,9 +101,9 @@ struct LinParams {
     int stages, stage_bytes;
     int chunk;              // blocks per sum in tensor memory
     int split, pairs;
-    int early;              // the kernel before has waited for those before it, and nothing here is its result
     float* part;            // [split][rows][ldp] sums of parts (split > 1)
     long long ldp, part_rows;
+    FewSums few;            // kWeight: dbias of few rows, or none
     SumParams sums;         // kWeight: dbias's parts, joined at the end (of linear_join_kernel where there is one), or none
     int join_blocks;        // of linear_join_kernel, that join parts of the product
 };
@@ -289,6 +301,49 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16])
         : "memory");
 }
 
+// Eight columns a thread, 64 columns by 4 WARPS rows at a time, several rows in flight; lanes of one column are eight
+// apart, and the warps' sums meet in s (64 WARPS floats), in their order.  `tid` of 32 WARPS threads, converged.
+template <int WARPS, int MODE>
+__device__ __forceinline__ void few_sums_of(const FewSums& p, int N, const int* off, float* s, int tid)
+{
+    constexpr int kAhead = MODE == kActWide ? 8 : 4, kRows = 4 * WARPS;
+    const int lane = tid & 31;
+    for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
+        const int e = u / p.across, c = 64 * (u - e * p.across), col = c + 8 * (tid & 7), m = min(8, N - col);
+        const int r0 = off[e], r1 = off[e + 1];
+        float sum[8] = {};
+        if (m > 0)
+            for (int r = r0 + (tid >> 3); r < r1; r += kAhead * kRows) {
+                Raw8 x[kAhead];
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i)
+                    if (r + i * kRows < r1) x[i] = act_load<MODE>(p.dy, r + i * kRows, p.ld, col, m, N, p.dtype, false);
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    if (r + i * kRows >= r1) continue;
+                    float v[8];
+                    act_ready<MODE>(x[i], p.dy, r + i * kRows, p.ld, col);
+                    act_unpack<kActWide>(x[i], p.dtype, v);
+                    add8(v, sum);
+                }
+            }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 8);
+            sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 16);
+            if (lane < 8) s[64 * (tid >> 5) + 8 * lane + k] = sum[k];
+        }
+        asm volatile("bar.sync 2, %0;" ::"n"(32 * WARPS) : "memory");
+        if (tid < 64 && c + tid < N && !(p.accumulate && r0 == r1)) {
+            float a = s[tid];
+            for (int w = 1; w < WARPS; ++w) a += s[64 * w + tid];
+            put_sum(p.out, (long long)e * N + c + tid, p.out_dtype, p.accumulate, a);
+        }
+        asm volatile("bar.sync 2, %0;" ::"n"(32 * WARPS) : "memory");
+    }
+}
+
 template <int KIND, bool CHUNKED>
 __global__ void __launch_bounds__(lin_threads(CHUNKED), 1)
     linear_product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
@@ -328,7 +383,7 @@ __global__ void __launch_bounds__(lin_threads(CHUNKED), 1)
         tmem_alloc_pair(tslot, 512);
         tc_fence_before();
     }
-    if (p.experts && !p.early) pdl_wait();  // the offsets may be the result of the kernel before
+    if (p.experts) pdl_wait();  // the offsets may be the result of the kernel before
     load_offsets(p.experts, p.offsets, p.offsets64, p.tokens, off);
     if (KIND != kWeight) {
         if (warp == 0) {
@@ -362,7 +417,7 @@ __global__ void __launch_bounds__(lin_threads(CHUNKED), 1)
                 int st = 0;
                 uint32_t ph = 0;
                 bool ok = true, more = walk.next(t);
-                if (!p.experts && !p.early) pdl_wait();
+                if (!p.experts) pdl_wait();
                 for (; ok && more; more = walk.next(t)) {
                     const int m0 = t.m + rank * 128, n0 = t.n + rank * (t.wide >> 1);
                     for (int k = t.k0; k < t.k1; ++k) {
@@ -481,8 +536,16 @@ __global__ void __launch_bounds__(lin_threads(CHUNKED), 1)
         const uint32_t trow = tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)first_row;
         int use = 0;
         bool ok = true, more = walk.next(t);
-        if (!p.experts && !p.early) pdl_wait();
+        if (!p.experts) pdl_wait();
         const unsigned long long offset = layer_offset(p.t);
+        if (KIND == kWeight && p.few.units) {
+            float* s = reinterpret_cast<float*>(first);  // (of use to the other kinds only)
+            static_assert(64 * kEpiWarps <= kLinMaxExperts + 4, "the warps' sums");
+            if (p.few.vec)
+                few_sums_of<kEpiWarps, kActWide>(p.few, p.N, off, s, threadIdx.x - 32 * kLinDirect);
+            else
+                few_sums_of<kEpiWarps, kActShifted>(p.few, p.N, off, s, threadIdx.x - 32 * kLinDirect);
+        }
         for (; ok && more; more = walk.next(t)) {
             const int j = t.m + rank * 128 + q * 32 + lane;
             const int rows = j < p.M ? t.rows : 0;  // of this column
@@ -570,7 +633,6 @@ __global__ void __launch_bounds__(lin_threads(CHUNKED), 1)
         if (KIND == kWeight && p.split == 1 && p.sums.part && e < 8) {
             // dbias, by the first eight of these warps (the others have few registers): 2 us here, 4 in a launch of its own.
             // The pair's MMAs and loads are over, so the ring is free.
-            pdl_wait();
             const auto sync = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
             float* s = reinterpret_cast<float*>(smem);
             for (int u = blockIdx.x; u < p.sums.units; u += gridDim.x) {
@@ -579,8 +641,6 @@ __global__ void __launch_bounds__(lin_threads(CHUNKED), 1)
             }
         }
     }
-    // (This one is complete only after the one before it: the next waits for this one alone.)
-    if (p.early && threadIdx.x == 0) pdl_wait();
     __syncwarp();
     // Neither CTA releases tensor memory or leaves while the other may still use it.
     tc_fence_before();
@@ -899,9 +959,8 @@ __global__ void __launch_bounds__(256) linear_pack_kernel(const __grid_constant_
 }
 
 // ---------------------------------------------------------------- bias gradients
-// Sums of dy's columns over an expert's rows, beside the product: all of them by one block, which
-// writes dbias (few rows), or `chunk` rows at a time to part[chunk][N], with how many chunks come
-// before each expert's (first, written by one block), which column_join adds up at the end.
+// Sums of dy's columns over an expert's rows, `chunk` rows at a time, to part[chunk][N], with how many chunks come
+// before each expert's (first, written by one block): column_join adds them up at the end.  (Few rows: FewSums.)
 // HBM's reads bound it, eight rows a thread in flight (8192 x 16384 46 us, 5.8 TB/s).
 struct ColumnParams {
     const void* dy;
@@ -910,10 +969,8 @@ struct ColumnParams {
     int experts, offsets64;
     const void* offsets;
     int cx_log, chunk;
-    float* part;           // null: one block for all rows of an expert (blockIdx.y)
+    float* part;
     int* first;
-    void* out;
-    int out_dtype, accumulate;
 };
 template <int MODE>
 __global__ void __launch_bounds__(256, 4) column_sum_kernel(const __grid_constant__ ColumnParams p)
@@ -921,36 +978,34 @@ __global__ void __launch_bounds__(256, 4) column_sum_kernel(const __grid_constan
     __shared__ int off[kLinMaxExperts + 1], first[kLinMaxExperts + 1];
     constexpr int kAhead = MODE == kActWide ? 8 : 4;  // rows in flight per thread
     __shared__ float s[8][256];
+    pdl_launch_dependents();
     pdl_wait();
-    pdl_launch_dependents();  // (after the wait: see LinParams::early)
     load_offsets(p.experts, p.offsets, p.offsets64, p.tokens, off);
     const int n = max(p.experts, 1);
-    if (p.part) {
-        if (threadIdx.x < 32) {
-            const int lane = threadIdx.x;
-            int run = 0;
-            for (int i0 = 0; i0 < n; i0 += 32) {
-                const int c = i0 + lane < n ? (off[i0 + lane + 1] - off[i0 + lane] + p.chunk - 1) / p.chunk : 0;
-                int a = c;
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int run = 0;
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            const int c = i0 + lane < n ? (off[i0 + lane + 1] - off[i0 + lane] + p.chunk - 1) / p.chunk : 0;
+            int a = c;
 #pragma unroll
-                for (int d = 1; d < 32; d *= 2) {
-                    const int o = __shfl_up_sync(0xffffffffu, a, d);
-                    if (lane >= d) a += o;
-                }
-                if (i0 + lane < n) first[i0 + lane] = run + a - c;
-                run += __shfl_sync(0xffffffffu, a, 31);
+            for (int d = 1; d < 32; d *= 2) {
+                const int o = __shfl_up_sync(0xffffffffu, a, d);
+                if (lane >= d) a += o;
             }
-            if (lane == 0) first[n] = run;
+            if (i0 + lane < n) first[i0 + lane] = run + a - c;
+            run += __shfl_sync(0xffffffffu, a, 31);
         }
-        __syncthreads();
-        if (blockIdx.x == 0 && blockIdx.y == 0)
-            for (int i = threadIdx.x; i <= n; i += 256) p.first[i] = first[i];
+        if (lane == 0) first[n] = run;
     }
+    __syncthreads();
+    if (blockIdx.x == 0 && blockIdx.y == 0)
+        for (int i = threadIdx.x; i <= n; i += 256) p.first[i] = first[i];
     const int cx = 1 << p.cx_log, tx = threadIdx.x & (cx - 1), ty = threadIdx.x >> p.cx_log, ny = 256 >> p.cx_log;
     const int col = 8 * (blockIdx.x * cx + tx), m = min(8, p.N - col);
-    for (int c = blockIdx.y; c < (p.part ? first[n] : n); c += gridDim.y) {
-        const int e = p.part ? find_last(first, n, c) : c;
-        const int r0 = off[e] + (p.part ? (c - first[e]) * p.chunk : 0), r1 = p.part ? min(off[e + 1], r0 + p.chunk) : off[e + 1];
+    for (int c = blockIdx.y; c < first[n]; c += gridDim.y) {
+        const int e = find_last(first, n, c);
+        const int r0 = off[e] + (c - first[e]) * p.chunk, r1 = min(off[e + 1], r0 + p.chunk);
         float sum[8] = {};
         if (m > 0)
             for (int r = r0 + ty; r < r1; r += kAhead * ny) {
@@ -975,11 +1030,7 @@ __global__ void __launch_bounds__(256, 4) column_sum_kernel(const __grid_constan
             const int k = i & 7, x = i >> 3, j = 8 * (blockIdx.x * cx + x) + k;
             float a = 0.f;
             for (int y = 0; y < ny; ++y) a += s[k][(y << p.cx_log) + x];
-            if (j >= p.N) continue;
-            if (p.part)
-                p.part[(long long)c * p.N + j] = a;
-            else if (!p.accumulate || r0 < r1)
-                put_sum(p.out, (long long)e * p.N + j, p.out_dtype, p.accumulate, a);
+            if (j < p.N) p.part[(long long)c * p.N + j] = a;
         }
     }
 }

@@ -157,6 +157,7 @@ struct LinPlan {
     int M, N, kb;             // columns of the result, rows (weight gradient), 64-wide blocks of the sum
     int bt, split, stages, stage_bytes, pairs;
     bool few;                 // linear_rows_kernel
+    bool chunked;             // sums of several chunks
     bool pack_a, pack_b;      // operands that TMA cannot read
     long long part_rows, ldp;
     int sum_rows;             // rows of a partial sum of dbias
@@ -168,6 +169,11 @@ struct LinPlan {
 // MMAs (16 terms each) of equal signs, a few times less of mixed ones: 6e-6 of an fp32
 // result's (n = 64), 2e-4 of a 16-bit one's (n = 2048), 0.4 of fp16's rounding.
 constexpr int kChunkFp32 = 16, kChunk16 = 512;
+int lin_chunk(const wg_linear_problem& q) { return q.out_dtype == WG_FP32 ? kChunkFp32 : kChunk16; }
+
+// Rows up to which the weight gradient's product makes dbias itself (512 x 1024 to 1000 6.8 us against 12.7 with a
+// kernel before it, 2048 x 2560 to 4096 38.8 against 45.6; 4000 x 128 to 300 30 against 19).
+constexpr int kFewSums = 2048;
 
 // Rows up to which the forward product is linear_rows_kernel's: eight at a time; 16 of one
 // weight matrix below 64 MB (4096 x 4096 for 9 rows 9.7 us against 14.1 on the tensor-core tiles,
@@ -264,6 +270,8 @@ int lin_plan(const wg_linear_problem* p, int call, LinPlan* pl)
             if (t < best - 1e-9) best = t, pl->bt = bt, pl->split = s;
         }
     }
+    // Blocks of the longest sum (a part's, or an expert's that has every row).
+    pl->chunked = ((weight ? (q.tokens + 63) / 64 : pl->kb) + pl->split - 1) / pl->split > lin_chunk(q);
     pl->stage_bytes = wg::kLinABytes + (weight ? (pl->bt > 128 ? 16384 : 8192) : pl->bt * 64);
     pl->stages = std::min(wg::kLinMaxStages, wg::kLinRing / pl->stage_bytes);
 
@@ -368,15 +376,15 @@ int columns_launch(const wg::ColumnParams& c, const LinPlan& pl, cudaStream_t s)
     const bool vec = vec_rows(c.dy, c.ld, c.N, 2);
     const int groups = (c.N + 7) / 8;
     const long long cols = (groups + (1 << c.cx_log) - 1) >> c.cx_log;
-    const long long rows = c.part ? std::min(pl.sum_chunks, (4LL * num_sms() + cols - 1) / cols) : std::max(c.experts, 1);
+    const long long rows = std::min(pl.sum_chunks, (4LL * num_sms() + cols - 1) / cols);
     const auto kernel = vec ? wg::column_sum_kernel<wg::kActWide> : wg::column_sum_kernel<wg::kActShifted>;
     return launch("column_sum_kernel launch", kernel, dim3((unsigned)cols, (unsigned)std::max(1LL, rows)), dim3(256), s, c);
 }
 
-// w, or x of the weight gradient, is operand a (MMA rows); the other operand b.  sums: dbias's partial sums,
-// made before the product, which need not wait for them.
+// w, or x of the weight gradient, is operand a (MMA rows); the other operand b.  dbias: few, sums that the product
+// makes itself, or sums, partial sums made before it and what joins them.
 int lin_run(const LinPlan& pl, const void* offsets, LinOperand a, LinOperand b, const wg::LayerTail& tail, char* ws, cudaStream_t s,
-            const wg::ColumnParams* sums = nullptr, wg::SumParams* joined = nullptr)
+            const wg::FewSums* few = nullptr, const wg::ColumnParams* sums = nullptr, wg::SumParams* joined = nullptr)
 {
     const wg_linear_problem& q = pl.p;
     if (!pl.pack_a && !aligned16(a.p)) return set_err(WG_ERR_MISALIGNED, "x, w or dy with 16-byte strides must be 16-byte aligned");
@@ -397,10 +405,10 @@ int lin_run(const LinPlan& pl, const void* offsets, LinOperand a, LinOperand b, 
     if (st) return st;
     wg::LinParams g = {};
     g.t = tail;
-    g.early = sums != nullptr;
+    if (few) g.few = *few;
     g.experts = q.experts, g.offsets = offsets, g.offsets64 = q.offset_bits == 64, g.tokens = q.tokens;
     g.M = pl.M, g.N = pl.N, g.kb = pl.kb, g.bf16 = q.in_dtype == WG_BF16;
-    g.chunk = q.out_dtype == WG_FP32 ? kChunkFp32 : kChunk16;
+    g.chunk = lin_chunk(q);
     g.bt = pl.bt, g.stages = pl.stages, g.stage_bytes = pl.stage_bytes, g.split = pl.split, g.pairs = pl.pairs;
     const unsigned im = (unsigned)(pl.M + 255) / 256;
     g.by_bt = wg::fast_div((unsigned)pl.bt), g.by_im = wg::fast_div(im), g.by_8im = wg::fast_div(8 * im);
@@ -415,13 +423,10 @@ int lin_run(const LinPlan& pl, const void* offsets, LinOperand a, LinOperand b, 
         plan_join(&m, ne, pl.sum_chunks, pl.split > 1 ? wg::kJoinBlock : wg::kJoinThreads);
         if (m.units <= (pl.split > 1 ? 4 * num_sms() : 2 * pl.pairs)) g.sums = m, joined->part = nullptr;
     }
-    // Blocks of the longest sum (a part's, or an expert's that has every row).
-    const long long blocks = pl.call == WG_LINEAR_BWD_WEIGHT ? (q.tokens + 63) / 64 : pl.kb;
-    const bool chunked = (blocks + pl.split - 1) / pl.split > g.chunk;
     switch (pl.call) {
-        case WG_LINEAR_FORWARD: return chunked ? lin_launch<wg::kForward, true>(pl, g, a, b, s) : lin_launch<wg::kForward, false>(pl, g, a, b, s);
-        case WG_LINEAR_BWD_DATA: return chunked ? lin_launch<wg::kData, true>(pl, g, a, b, s) : lin_launch<wg::kData, false>(pl, g, a, b, s);
-        default: return chunked ? lin_launch<wg::kWeight, true>(pl, g, a, b, s) : lin_launch<wg::kWeight, false>(pl, g, a, b, s);
+        case WG_LINEAR_FORWARD: return pl.chunked ? lin_launch<wg::kForward, true>(pl, g, a, b, s) : lin_launch<wg::kForward, false>(pl, g, a, b, s);
+        case WG_LINEAR_BWD_DATA: return pl.chunked ? lin_launch<wg::kData, true>(pl, g, a, b, s) : lin_launch<wg::kData, false>(pl, g, a, b, s);
+        default: return pl.chunked ? lin_launch<wg::kWeight, true>(pl, g, a, b, s) : lin_launch<wg::kWeight, false>(pl, g, a, b, s);
     }
 }
 
@@ -659,23 +664,26 @@ int wg_linear_bwd_weight(const wg_linear_problem* p, const void* offsets, const 
     if (accumulate) g.res = dw, g.ldr = q.ld_weight;
     if (vec_rows(dw, q.ld_weight, q.in, oe, ne > 1 ? q.weight_stride : 0)) g.vec |= wg::kVecY | wg::kVecRes;
     if (pair_rows(dw, q.ld_weight, q.in, oe, ne > 1 ? q.weight_stride : 0)) g.vec |= wg::kPairY | wg::kPairRes;
+    if (!dbias) return lin_run(pl, offsets, {x, q.tokens, q.in, q.ld_in, 1, 0}, {dy, q.tokens, q.out, q.ld_out, 1, 0}, g, ws, s);
+    const bool vec = vec_rows(dy, q.ld_out, q.out, ie);
+    // Few rows: within the product, 64 columns and every row of an expert per CTA.
+    wg::FewSums few = {};
+    few.across = (q.out + 63) / 64, few.units = ne * few.across;
+    if (q.tokens <= kFewSums && few.units <= 4 * num_sms()) {
+        few.dy = dy, few.ld = q.ld_out, few.out = dbias, few.dtype = q.in_dtype, few.out_dtype = q.bias_dtype;
+        few.accumulate = accumulate != 0, few.vec = vec;
+        return lin_run(pl, offsets, {x, q.tokens, q.in, q.ld_in, 1, 0}, {dy, q.tokens, q.out, q.ld_out, 1, 0}, g, ws, s, &few);
+    }
     wg::ColumnParams c = {};
     c.dy = dy, c.tokens = q.tokens, c.ld = q.ld_out, c.N = q.out, c.dtype = q.in_dtype;
     c.experts = q.experts, c.offsets64 = q.offset_bits == 64, c.offsets = offsets, c.chunk = pl.sum_rows;
     c.part = reinterpret_cast<float*>(ws + pl.off_sum), c.first = reinterpret_cast<int*>(ws + pl.off_first);
-    c.out = dbias, c.out_dtype = q.bias_dtype, c.accumulate = accumulate != 0;
-    // Few rows: 64 columns and every row of an expert per block (1000 x 2048 with the product 12.2 us against 14.7 with
-    // parts; rows that start anywhere, 300 x 1515 11.1 against 13.4, but 700 x 2047 20.3 against 17.0).
-    const bool once = q.tokens <= (vec_rows(dy, q.ld_out, q.out, ie) ? 1024 : 512) && ne * ((q.out + 63LL) / 64) <= 4LL * num_sms();
-    if (once) c.part = nullptr;
     const int groups = (q.out + 7) / 8;
-    c.cx_log = std::min(once ? 3 : 5, log2_floor(groups) + ((groups & (groups - 1)) ? 1 : 0));
+    c.cx_log = std::min(5, log2_floor(groups) + ((groups & (groups - 1)) ? 1 : 0));
     wg::SumParams m = {};
-    if (!once) m.part = c.part;
-    m.out = dbias, m.dim = q.out, m.dtype = q.bias_dtype, m.accumulate = accumulate != 0, m.first = c.first;
-    st = lin_run(pl, offsets, {x, q.tokens, q.in, q.ld_in, 1, 0}, {dy, q.tokens, q.out, q.ld_out, 1, 0}, g, ws, s, dbias ? &c : nullptr,
-                 dbias ? &m : nullptr);
-    return st || !dbias || !m.part ? st : join_columns(m, ne, pl.sum_chunks, s);
+    m.part = c.part, m.out = dbias, m.dim = q.out, m.dtype = q.bias_dtype, m.accumulate = accumulate != 0, m.first = c.first;
+    st = lin_run(pl, offsets, {x, q.tokens, q.in, q.ld_in, 1, 0}, {dy, q.tokens, q.out, q.ld_out, 1, 0}, g, ws, s, nullptr, &c, &m);
+    return st || !m.part ? st : join_columns(m, ne, pl.sum_chunks, s);
 }
 
 int wg_activation_workspace_size(const wg_activation_problem* p, size_t* bytes)
