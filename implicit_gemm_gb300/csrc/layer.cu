@@ -344,15 +344,21 @@ int check_registers()
     return set_err(WG_ERR_CUDA, "linear_product_kernel was built with " + std::to_string(st) + " registers a thread, fewer than it hands out");
 }
 
-template <int KIND, bool CHUNKED>
-int lin_launch(const LinPlan& pl, const wg::LinParams& g, const LinOperand& a, const LinOperand& b, cudaStream_t s)
+// The kernels of a call, and what has to hold before they are launched.
+struct LinKernels {
+    void (*product)(CUtensorMap, CUtensorMap, wg::LinParams);
+    void (*join)(wg::LinParams);
+    int (*check)();
+};
+template <int KIND>
+LinKernels lin_kernels(bool chunked)
 {
-    CUtensorMap ma, mb;
-    int st = lin_map(&ma, a.p, g.bf16, a.cols, a.rows, a.batch, a.ld, a.bs, KIND == wg::kForward ? 128 : 64);
-    if (!st) st = lin_map(&mb, b.p, g.bf16, b.cols, b.rows, 1, b.ld, 0, KIND == wg::kWeight ? 64 : pl.bt / 2);
-    if (!st && CHUNKED) st = check_registers<KIND>();
-    if (!st) st = wg::ensure_smem(wg::linear_product_kernel<KIND, CHUNKED>, wg::kLinSmem);
-    if (st) return st;
+    if (chunked) return {wg::linear_product_kernel<KIND, true>, wg::linear_join_kernel<KIND>, check_registers<KIND>};
+    return {wg::linear_product_kernel<KIND, false>, wg::linear_join_kernel<KIND>, [] { return (int)WG_OK; }};
+}
+
+int product_launch(const LinPlan& pl, const LinKernels& k, const CUtensorMap& ma, const CUtensorMap& mb, const wg::LinParams& g, cudaStream_t s)
+{
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     unsigned na = 0;
@@ -362,13 +368,13 @@ int lin_launch(const LinPlan& pl, const wg::LinParams& g, const LinOperand& a, c
     ++na;
     wg::pdl_config(&cfg, attr, &na, s);
     cfg.gridDim = dim3((unsigned)(2 * g.pairs));
-    cfg.blockDim = dim3(wg::lin_threads(CHUNKED));
+    cfg.blockDim = dim3(wg::lin_threads(pl.chunked));
     cfg.dynamicSmemBytes = wg::kLinSmem;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, wg::linear_product_kernel<KIND, CHUNKED>, ma, mb, g);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k.product, ma, mb, g);
     if (e != cudaSuccess) return cuda_fail("linear_product_kernel launch", e);
     if (pl.split == 1) return WG_OK;
-    return launch("linear_join_kernel launch", wg::linear_join_kernel<KIND>,
-                  dim3((unsigned)(g.join_blocks + (g.sums.part ? g.sums.units : 0))), dim3(wg::kJoinBlock), s, g);
+    return launch("linear_join_kernel launch", k.join, dim3((unsigned)(g.join_blocks + (g.sums.part ? g.sums.units : 0))),
+                  dim3(wg::kJoinBlock), s, g);
 }
 
 int columns_launch(const wg::ColumnParams& c, const LinPlan& pl, cudaStream_t s)
@@ -389,25 +395,34 @@ int lin_run(const LinPlan& pl, const void* offsets, LinOperand a, LinOperand b, 
     const wg_linear_problem& q = pl.p;
     if (!pl.pack_a && !aligned16(a.p)) return set_err(WG_ERR_MISALIGNED, "x, w or dy with 16-byte strides must be 16-byte aligned");
     if (!pl.pack_b && !aligned16(b.p)) return set_err(WG_ERR_MISALIGNED, "x, w or dy with 16-byte strides must be 16-byte aligned");
-    int st = WG_OK;
+    wg::PackParams ka = {}, kb = {};
     if (q.tokens > 0) {
-        wg::PackParams ka = {}, kb = {};
         if (pl.pack_a) ka = lin_pack(&a, ws + pl.off_a);
         if (pl.pack_b) kb = lin_pack(&b, ws + pl.off_b);
-        const long long segments = (long long)ka.segments * ka.batch + kb.segments;
-        if (segments > 0)
-            st = launch("linear_pack_kernel launch", wg::linear_pack_kernel, dim3((unsigned)std::min<long long>((segments + 7) / 8, 8LL * num_sms())),
-                        dim3(256), s, ka, kb, offsets, (int)(q.offset_bits == 64), q.tokens);
     } else {
         a.p = b.p = ws, a.ld = b.ld = 8LL * (kMaxFeatures / 8), a.rows = b.rows = 1, a.batch = 1, a.bs = a.ld;  // (never read)
     }
+    // Whatever may fail comes before the first launch.
+    const LinKernels kernels = pl.call == WG_LINEAR_FORWARD    ? lin_kernels<wg::kForward>(pl.chunked)
+                               : pl.call == WG_LINEAR_BWD_DATA ? lin_kernels<wg::kData>(pl.chunked)
+                                                               : lin_kernels<wg::kWeight>(pl.chunked);
+    const int bf16 = q.in_dtype == WG_BF16;
+    CUtensorMap ma, mb;
+    int st = lin_map(&ma, a.p, bf16, a.cols, a.rows, a.batch, a.ld, a.bs, pl.call == WG_LINEAR_FORWARD ? 128 : 64);
+    if (!st) st = lin_map(&mb, b.p, bf16, b.cols, b.rows, 1, b.ld, 0, pl.call == WG_LINEAR_BWD_WEIGHT ? 64 : pl.bt / 2);
+    if (!st) st = kernels.check();
+    if (!st) st = wg::ensure_smem(kernels.product, wg::kLinSmem);
+    const long long segments = (long long)ka.segments * ka.batch + kb.segments;
+    if (!st && segments > 0)
+        st = launch("linear_pack_kernel launch", wg::linear_pack_kernel, dim3((unsigned)std::min<long long>((segments + 7) / 8, 8LL * num_sms())),
+                    dim3(256), s, ka, kb, offsets, (int)(q.offset_bits == 64), q.tokens);
     if (!st && sums) st = columns_launch(*sums, pl, s);
     if (st) return st;
     wg::LinParams g = {};
     g.t = tail;
     if (few) g.few = *few;
     g.experts = q.experts, g.offsets = offsets, g.offsets64 = q.offset_bits == 64, g.tokens = q.tokens;
-    g.M = pl.M, g.N = pl.N, g.kb = pl.kb, g.bf16 = q.in_dtype == WG_BF16;
+    g.M = pl.M, g.N = pl.N, g.kb = pl.kb, g.bf16 = bf16;
     g.chunk = lin_chunk(q);
     g.bt = pl.bt, g.stages = pl.stages, g.stage_bytes = pl.stage_bytes, g.split = pl.split, g.pairs = pl.pairs;
     const unsigned im = (unsigned)(pl.M + 255) / 256;
@@ -423,11 +438,7 @@ int lin_run(const LinPlan& pl, const void* offsets, LinOperand a, LinOperand b, 
         plan_join(&m, ne, pl.sum_chunks, pl.split > 1 ? wg::kJoinBlock : wg::kJoinThreads);
         if (m.units <= (pl.split > 1 ? 4 * num_sms() : 2 * pl.pairs)) g.sums = m, joined->part = nullptr;
     }
-    switch (pl.call) {
-        case WG_LINEAR_FORWARD: return pl.chunked ? lin_launch<wg::kForward, true>(pl, g, a, b, s) : lin_launch<wg::kForward, false>(pl, g, a, b, s);
-        case WG_LINEAR_BWD_DATA: return pl.chunked ? lin_launch<wg::kData, true>(pl, g, a, b, s) : lin_launch<wg::kData, false>(pl, g, a, b, s);
-        default: return pl.chunked ? lin_launch<wg::kWeight, true>(pl, g, a, b, s) : lin_launch<wg::kWeight, false>(pl, g, a, b, s);
-    }
+    return product_launch(pl, kernels, ma, mb, g, s);
 }
 
 template <int XR, int FG, int VEC>

@@ -540,7 +540,8 @@ WG_API int wg_linear_plan_string(const wg_linear_problem* p, wg_linear_call call
  * the same strides; else no output may overlap another tensor of the call.
  * accumulate: dw and dbias are added to what is there (in fp32, then rounded).
  * With tokens = 0 nothing is written but the weight gradient's zeros.
- * Returns WG_OK or an error status; nothing is launched on an error. */
+ * Returns WG_OK or an error status; nothing is launched on an error, but for a launch of CUDA's that
+ * itself fails behind others of the call (WG_ERR_CUDA; the results may then be written in part). */
 WG_API int wg_linear(const wg_linear_problem* p, const void* offsets, const void* x, const void* w, const void* bias,
                      const void* residual, void* y, void* z, void* workspace, size_t ws_bytes, void* stream);
 WG_API int wg_linear_bwd_data(const wg_linear_problem* p, const void* offsets, const void* dy, const void* w,
@@ -580,7 +581,7 @@ WG_API int wg_activation_workspace_size(const wg_activation_problem* p, size_t* 
  * anywhere are fetched in the aligned 16 bytes around them); workspace (needed with dbias
  * only) 16 bytes, one for each call whose work may overlap.  y may be x or residual, and dx may be x or dy, where
  * their types and strides are the same; else no output may overlap another tensor.
- * Returns WG_OK or an error status; nothing is launched on an error. */
+ * Returns WG_OK or an error status; nothing is launched on an error (but see above for launches that fail). */
 WG_API int wg_activation(const wg_activation_problem* p, const void* x, const void* bias, const void* residual, void* y,
                          void* stream);
 WG_API int wg_activation_bwd(const wg_activation_problem* p, const void* dy, const void* x, const void* bias, void* dx,

@@ -197,3 +197,22 @@ def test_convenience_calls_refuse_what_does_not_fit():
         binding.linear_bwd_weight(x.bfloat16(), torch.zeros(5, 72).bfloat16())
     with pytest.raises(ValueError):
         binding.linear_bwd_weight(x.bfloat16(), torch.zeros(4, 72).bfloat16(), accumulate=True)
+
+
+def no_gpu():
+    """Whether no CUDA device is there: then a call that passes validation reaches the driver's refusal and nothing else."""
+    torch = pytest.importorskip("torch")
+    return not torch.cuda.is_available()
+
+
+@pytest.mark.parametrize("sp,f", [
+    (lin(in_=65), lambda sp, kw: binding.wg_linear(sp, A, 2 * A, 3 * A, **kw)),
+    (lin(out=71), lambda sp, kw: binding.wg_linear_bwd_data(sp, A, 2 * A, 3 * A, **kw)),
+    (lin(tokens=5000), lambda sp, kw: binding.wg_linear_bwd_weight(sp, A, 2 * A, 3 * A, dbias=4 * A, accumulate=True, **kw)),
+    (lin(tokens=5000, in_=65), lambda sp, kw: binding.wg_linear_bwd_weight(sp, A, 2 * A, 3 * A, dbias=4 * A, **kw))])
+def test_what_may_fail_comes_before_the_first_launch(sp, f):
+    """Without a driver the tensor maps cannot be made: the call ends there, with no launch tried before."""
+    if not no_gpu():
+        pytest.skip("would launch with the addresses of nothing")
+    refused(5, f, sp, {"workspace": 15 * A, "ws_bytes": 1 << 40, "stream": 0})
+    assert "launch" not in binding.wg_last_error() and "cuTensorMapEncodeTiled" in binding.wg_last_error()
