@@ -54,6 +54,18 @@ struct Tensor {
     }
 };
 
+// Whether two tensors whose rows are one stride apart lie side by side in it, as columns of one buffer do.
+bool side_by_side(const Tensor& a, const Tensor& b)
+{
+    const Tensor& r = a.rows > 1 ? a : b;
+    const long long row = r.ld * r.es;
+    for (const Tensor* t : {&a, &b})
+        if ((t->rows > 1 && t->ld * t->es != row) || (t->count > 1 && t->stride * t->es % row)) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    const long long d = y >= x ? (long long)((y - x) % (uintptr_t)row) : (row - (long long)((x - y) % (uintptr_t)row)) % row;
+    return d >= a.cols * a.es && d + b.cols * b.es <= row;
+}
+
 // The first `outputs` of n tensors are written: none of them may share bytes with another one, but for pairs that
 // are the same elements (same address, type and strides) where `same` allows it.
 int check_tensors(const Tensor* t, int n, int outputs, int same_a, int same_b, int same_c = -1)
@@ -66,7 +78,7 @@ int check_tensors(const Tensor* t, int n, int outputs, int same_a, int same_b, i
             const Tensor &a = t[i], &b = t[j];
             const long long na = a.bytes(), nb = b.bytes();
             const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-            if (!na || !nb || x >= y + (uintptr_t)nb || y >= x + (uintptr_t)na) continue;
+            if (!na || !nb || x >= y + (uintptr_t)nb || y >= x + (uintptr_t)na || side_by_side(a, b)) continue;
             const bool equal = x == y && a.es == b.es && a.ld == b.ld && a.rows == b.rows && a.cols == b.cols;
             if (i == same_a && (j == same_b || j == same_c) && equal) continue;
             return set_err(WG_ERR_INVALID_ARGUMENT, std::string(a.name) + " overlaps " + b.name);

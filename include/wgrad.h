@@ -537,7 +537,8 @@ WG_API int wg_linear_plan_string(const wg_linear_problem* p, wg_linear_call call
  * them); every other tensor only its elements' (16-byte aligned rows are faster);
  * workspace 16 bytes, its contents of no use before or after a call: calls whose work may
  * overlap on the GPU, replayed graphs among them, need one each.  residual may be y (or dx) itself, with
- * the same strides; else no output may overlap another tensor of the call.
+ * the same strides; else no output may overlap another tensor of the call (columns of one buffer, side by
+ * side with one stride, do not).
  * accumulate: dw and dbias are added to what is there (in fp32, then rounded).
  * With tokens = 0 nothing is written but the weight gradient's zeros.
  * Returns WG_OK or an error status; nothing is launched on an error, but for a launch of CUDA's that
@@ -580,7 +581,8 @@ WG_API int wg_activation_workspace_size(const wg_activation_problem* p, size_t* 
 /* The two calls on `stream`.  Tensors need only their elements' alignment (rows that start
  * anywhere are fetched in the aligned 16 bytes around them); workspace (needed with dbias
  * only) 16 bytes, one for each call whose work may overlap.  y may be x or residual, and dx may be x or dy, where
- * their types and strides are the same; else no output may overlap another tensor.
+ * their types and strides are the same; else no output may overlap another tensor (columns of one buffer
+ * do not).
  * Returns WG_OK or an error status; nothing is launched on an error (but see above for launches that fail). */
 WG_API int wg_activation(const wg_activation_problem* p, const void* x, const void* bias, const void* residual, void* y,
                          void* stream);

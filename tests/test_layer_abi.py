@@ -216,3 +216,28 @@ def test_what_may_fail_comes_before_the_first_launch(sp, f):
         pytest.skip("would launch with the addresses of nothing")
     refused(5, f, sp, {"workspace": 15 * A, "ws_bytes": 1 << 40, "stream": 0})
     assert "launch" not in binding.wg_last_error() and "cuTensorMapEncodeTiled" in binding.wg_last_error()
+
+
+def test_columns_of_one_buffer_are_apart():
+    """x, y, z and residual side by side in the rows of one buffer share no bytes; shifted by an element they do."""
+    big = {"workspace": 15 * A, "ws_bytes": 1 << 40, "stream": 0}
+    x, y, z, w = 64 * 2, 72 * 2, 72 * 2, 2 * A
+    row = x + y + z
+    for tokens in (2, 20, 300):
+        sp = lin(tokens=tokens, ld_in=row // 2, ld_out=row // 2, ld_z=row // 2, ld_residual=row // 2)
+        f, d, g = binding.wg_linear, binding.wg_linear_bwd_data, binding.wg_linear_bwd_weight
+        apart = [lambda: f(sp, A, w, A + x, z=A + x + y, **big), lambda: f(sp, A + row - x, w, A, z=A + y, **big),
+                 lambda: f(sp, A + y, w, A, residual=A + y + x, **big), lambda: d(sp, A, w, A + y, **big),
+                 lambda: binding.wg_activation(act(tokens=tokens, ld_x=200, ld_y=200), A, A + 256, stream=0),
+                 lambda: binding.wg_activation(act(tokens=tokens, ld_x=200, ld_y=100, out_dtype="fp32"), A, A + 144, stream=0),
+                 lambda: g(lin(tokens=tokens, ld_weight=100), w, 3 * A, A, dbias=A + 128 + 72 * 200, **big)]
+        if no_gpu():
+            for call in apart:
+                refused(5, call)  # (what a call comes to that passes validation here)
+        for call in (lambda: f(sp, A, w, A + x - 2, z=A + x + y, **big), lambda: f(sp, A, w, A + x, z=A + x + y - 2, **big),
+                     lambda: f(sp, A, w, A + x + 2, z=A + x + y, **big), lambda: f(sp, A, w, A + x + z + 2, **big),
+                     lambda: f({**sp, "ld_out": row // 2 + 8}, A, w, A + x, **big), lambda: d(sp, A, w, A + y - 2, **big),
+                     lambda: f({**sp, "ld_out": 72}, A, w, A + x, **big),
+                     lambda: binding.wg_activation(act(tokens=tokens, ld_x=200, ld_y=100, out_dtype="fp32"), A, A + 148, stream=0),
+                     lambda: g(lin(tokens=tokens, ld_weight=100), w, 3 * A, A, dbias=A + 128, **big)):
+            refused(1, call)

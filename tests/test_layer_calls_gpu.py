@@ -124,3 +124,38 @@ def test_bias_sums_of_few_rows(tokens, inf, out, counts, dt, bdt):
     close(acc, wb + start.double(), berr + 2.0 ** -23 * (wb.abs() + start.double().abs()), bdt, "dbias added")
     for e, c in enumerate(counts or []):
         assert c or torch.equal(acc[e], start[e])
+
+
+@pytest.mark.parametrize("tokens,inf,out,pad,dt", [(5, 64, 72, 0, "bf16"), (90, 136, 72, 8, "bf16"), (700, 264, 520, 8, "fp16"),
+                                                   (13, 65, 71, 1, "fp16"), (300, 129, 333, 3, "bf16")])
+def test_columns_of_one_buffer(tokens, inf, out, pad, dt):
+    """x | y | z | residual as columns of one buffer: each call writes its own and nothing beside them."""
+    cols = {"x": inf, "y": out, "z": out, "res": out, "dx": inf}
+    at, o = {}, pad
+    for k, c in cols.items():
+        at[k], o = slice(o, o + c), o + c + pad
+    start = randn(1, tokens, o, dt=dt)
+    buf, w, bias = start.clone(), randn(2, out, inf, size=inf ** -0.5, dt=dt), randn(3, out)
+    v = {k: buf[:, s] for k, s in at.items()}
+    kw = dict(activation="silu", dropout=0.2, seed=3, offset=4)
+    sp = {"tokens": tokens, "in": inf, "out": out, "ld_in": o, "ld_out": o, "ld_z": o, "ld_residual": o, "in_dtype": dt,
+          "out_dtype": dt, **kw}
+    x, res = start[:, at["x"]].contiguous(), start[:, at["res"]].contiguous()
+    wy, wz = binding.linear(x, w, bias, res, keep_z=True, **kw)
+    binding.wg_linear(sp, v["x"], w, v["y"], bias, v["res"], v["z"], None, space(sp, "forward"))
+    want = start.clone()
+    want[:, at["y"]], want[:, at["z"]] = wy, wz
+    assert torch.equal(buf, want)
+    wdx = binding.linear_bwd_data(wy, w, x, **kw)
+    binding.wg_linear_bwd_data(sp, v["y"], w, v["dx"], v["x"], None, None, space(sp, "bwd_data"))
+    want[:, at["dx"]] = wdx
+    assert torch.equal(buf, want)
+    sa = {"tokens": tokens, "dim": out, "ld_x": o, "ld_y": o, "ld_residual": o, "ld_dx": o, "in_dtype": dt, "out_dtype": dt, **kw}
+    wa = binding.activation(wz, bias, res, **kw)
+    binding.wg_activation(sa, v["z"], v["y"], bias, v["res"])
+    want[:, at["y"]] = wa
+    assert torch.equal(buf, want)
+    wd = binding.activation_bwd(res, wz, bias, **kw)
+    binding.wg_activation_bwd(sa, v["res"], v["z"], v["y"], bias)
+    want[:, at["y"]] = wd
+    assert torch.equal(buf, want)
