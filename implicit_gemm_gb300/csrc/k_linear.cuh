@@ -162,6 +162,26 @@ __device__ __forceinline__ int list_used(const int* off, int n, short* used)
     return c;
 }
 
+// The passes over experts' rows, `most` rows at a time: expert and first row of each.  The first warp; the block
+// synchronises after it.
+__device__ __forceinline__ int list_passes(const int* off, int n, int most, short* expert, int* row)
+{
+    const int lane = threadIdx.x & 31;
+    int run = 0;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const int i = i0 + lane, c = i < n ? (off[i + 1] - off[i] + most - 1) / most : 0;
+        int a = c;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int o = __shfl_up_sync(0xffffffffu, a, d);
+            if (lane >= d) a += o;
+        }
+        for (int k = 0; k < c; ++k) expert[run + a - c + k] = (short)i, row[run + a - c + k] = off[i] + most * k;
+        run += __shfl_sync(0xffffffffu, a, 31);
+    }
+    return run;
+}
+
 // The last i with first[i] <= v, i < n (first ascending, first[0] <= v): empty experts have the
 // same first as the one after them, and the one that holds v is the last of those.
 __device__ __forceinline__ int find_last(const int* first, int n, int v)
@@ -707,8 +727,8 @@ __global__ void __launch_bounds__(kJoinBlock) linear_join_kernel(const __grid_co
 }
 
 // ---------------------------------------------------------------- few rows
-// The forward product of at most 8 XR rows per expert and pass: every byte of the weights is
-// read once, and that is what bounds it (one row of 8192 to 8192 24 us, 5.6 TB/s; of 4096 to 4096 9 us, of
+// The forward product of at most 8 XR rows of an expert per pass: a pass reads every byte of its expert's
+// weights once, and that is what bounds it (one row of 8192 to 8192 24 us, 5.6 TB/s; of 4096 to 4096 9 us, of
 // which 3 to 4 are the launch, the first loads and the warps' sums).  A CTA has 8 FG columns of the result (rows of w) of one
 // expert; its eight warps take 32 of the sum each in turn, so that a row of w is read in 512
 // bytes at a time, straight to registers: MMAs of 16 rows of x by 8 of w by 16, of which a
@@ -716,7 +736,10 @@ __global__ void __launch_bounds__(kJoinBlock) linear_join_kernel(const __grid_co
 // one for both operands).  One batch of loads is in flight while the one before is multiplied;
 // x's come with them (loaded where they were needed, each waited for L2: 4096 x 4096 for one
 // row 14 us).  The warps' sums meet in shared memory, in the order of the warps.
+// Passes of one expert are different CTAs' (64 rows of one of 8 experts'
+// 2047 x 2048 24 us; one after another 82).
 constexpr int kRowsThreads = 256;
+constexpr int kRowsMost = 64;  // rows in all, and so passes
 struct RowsParams {
     LayerTail t;
     int experts, offsets64;
@@ -807,102 +830,106 @@ __global__ void __launch_bounds__(kRowsThreads, 2) linear_rows_kernel(const __gr
         RowsRaw<VEC> w[kAhead][FG], x[kAhead][XR];
     };
     __shared__ int off[kLinMaxExperts + 1];
-    __shared__ short used[kLinMaxExperts];  // experts that have rows
-    __shared__ int count;
+    __shared__ short pass_expert[kRowsMost];
+    __shared__ int pass_row[kRowsMost], count;
     __shared__ float sums[8][8 * XR][8 * FG + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tig = lane & 3;
     pdl_launch_dependents();
     pdl_wait();
-    load_offsets(p.experts, p.offsets, p.offsets64, p.tokens, off);
-    const int n = max(p.experts, 1);
-    if (warp == 0) {
-        const int c = list_used(off, n, used);
-        if (lane == 0) count = c;
+    if (p.experts == 0) {
+        const int i = threadIdx.x, c = ((int)p.tokens + 8 * XR - 1) / (8 * XR);
+        if (i < c) pass_expert[i] = 0, pass_row[i] = 8 * XR * i;
+        if (i == 0) count = c;
     }
-    __syncthreads();
+    load_offsets(p.experts, p.offsets, p.offsets64, p.tokens, off);
+    if (p.experts) {
+        if (warp == 0) {
+            const int c = list_passes(off, p.experts, 8 * XR, pass_expert, pass_row);
+            if (lane == 0) count = c;
+        }
+        __syncthreads();
+    }
     const unsigned long long offset = layer_offset(p.t);
     const int per = (p.M + 8 * FG - 1) / (8 * FG);
     const int total = count * per;
     for (int item = blockIdx.x; item < total; item += gridDim.x) {
-        const int ei = item / per, e = used[ei], j0 = 8 * FG * (item - ei * per);
+        const int pass = item / per, e = pass_expert[pass], r0 = pass_row[pass], j0 = 8 * FG * (item - pass * per);
         const unsigned short* w = static_cast<const unsigned short*>(p.w) + e * p.wstride;
         const unsigned short* wrow[FG];
 #pragma unroll
         for (int f = 0; f < FG; ++f) wrow[f] = j0 + 8 * f + g < p.M ? w + (j0 + 8 * f + g) * p.ldw : nullptr;
-        for (int r0 = off[e]; r0 < off[e + 1]; r0 += 8 * XR) {
-            const int rows = min(8 * XR, off[e + 1] - r0);
-            const unsigned short* xrow[XR];
+        const int rows = min(8 * XR, off[e + 1] - r0);
+        const unsigned short* xrow[XR];
 #pragma unroll
-            for (int m = 0; m < XR; ++m)
-                xrow[m] = 8 * m + g < rows ? static_cast<const unsigned short*>(p.x) + (r0 + 8 * m + g) * p.ldx : nullptr;
-            float d[FG][4] = {};
-            const auto load = [&](Batch& c, int k) {
+        for (int m = 0; m < XR; ++m)
+            xrow[m] = 8 * m + g < rows ? static_cast<const unsigned short*>(p.x) + (r0 + 8 * m + g) * p.ldx : nullptr;
+        float d[FG][4] = {};
+        const auto load = [&](Batch& c, int k) {
 #pragma unroll
-                for (int u = 0; u < kAhead; ++u) {
+            for (int u = 0; u < kAhead; ++u) {
 #pragma unroll
-                    for (int f = 0; f < FG; ++f) c.w[u][f] = rows_load<VEC>(wrow[f], k + 256 * u + 8 * tig, p.K, true);
+                for (int f = 0; f < FG; ++f) c.w[u][f] = rows_load<VEC>(wrow[f], k + 256 * u + 8 * tig, p.K, true);
 #pragma unroll
-                    for (int m = 0; m < XR; ++m) c.x[u][m] = rows_load<VEC>(xrow[m], k + 256 * u + 8 * tig, p.K, false);
-                }
-            };
-            const auto multiply = [&](const Batch& c, int k) {
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u) {
-                    const int at = k + 256 * u + 8 * tig;
-                    const uint4 x0 = rows_take<VEC>(c.x[u][0], xrow[0], at, p.K);
-                    const uint4 x1 = XR > 1 ? rows_take<VEC>(c.x[u][XR - 1], xrow[XR - 1], at, p.K) : make_uint4(0u, 0u, 0u, 0u);
-                    const uint32_t lo[4] = {x0.x, x1.x, x0.y, x1.y}, hi[4] = {x0.z, x1.z, x0.w, x1.w};
-#pragma unroll
-                    for (int f = 0; f < FG; ++f) {
-                        const uint4 v = rows_take<VEC>(c.w[u][f], wrow[f], at, p.K);
-                        mma16816<BF16>(d[f], lo, v.x, v.y);
-                        mma16816<BF16>(d[f], hi, v.z, v.w);
-                    }
-                }
-            };
-            // The warp's sums so far, to its own place in shared memory: every 64 MMAs (they add with
-            // truncation, see above).
-            bool begun = false;
-            const auto put = [&]() {
-#pragma unroll
-                for (int f = 0; f < FG; ++f)
-#pragma unroll
-                    for (int i = 0; i < 2 * XR; ++i) {
-                        float& s = sums[warp][g + 8 * (i >> 1)][8 * f + 2 * tig + (i & 1)];
-                        s = begun ? s + d[f][i] : d[f][i];
-                        d[f][i] = 0.f;
-                    }
-                begun = true;
-            };
-            constexpr int kStep = 256 * kAhead, kPut = 64 / (2 * kAhead) / 2 * 2 * kStep;
-            Batch b0, b1;
-            int k = 32 * warp, next = k + kPut;
-            if (k < p.K) load(b0, k);
-            while (k < p.K) {
-                if (k >= next) put(), next += kPut;
-                if (k + kStep < p.K) load(b1, k + kStep);
-                multiply(b0, k);
-                if ((k += kStep) >= p.K) break;
-                if (k + kStep < p.K) load(b0, k + kStep);
-                multiply(b1, k);
-                k += kStep;
+                for (int m = 0; m < XR; ++m) c.x[u][m] = rows_load<VEC>(xrow[m], k + 256 * u + 8 * tig, p.K, false);
             }
-            put();
-            __syncthreads();
-            for (int i = threadIdx.x; i < rows * FG; i += kRowsThreads) {
-                const int r = i / FG, f = i - r * FG, j = j0 + 8 * f, nc = min(8, p.M - j);
-                if (nc <= 0) continue;
-                TailRead<kForward> rd;
-                tail_read<kForward>(p.t, e, r0 + r, j, nc, rd);
-                float v[8] = {};
+        };
+        const auto multiply = [&](const Batch& c, int k) {
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
+            for (int u = 0; u < kAhead; ++u) {
+                const int at = k + 256 * u + 8 * tig;
+                const uint4 x0 = rows_take<VEC>(c.x[u][0], xrow[0], at, p.K);
+                const uint4 x1 = XR > 1 ? rows_take<VEC>(c.x[u][XR - 1], xrow[XR - 1], at, p.K) : make_uint4(0u, 0u, 0u, 0u);
+                const uint32_t lo[4] = {x0.x, x1.x, x0.y, x1.y}, hi[4] = {x0.z, x1.z, x0.w, x1.w};
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) v[c] += sums[q][r][8 * f + c];
-                tail_write<kForward>(p.t, offset, e, r0 + r, j, nc, rd, v);
+                for (int f = 0; f < FG; ++f) {
+                    const uint4 v = rows_take<VEC>(c.w[u][f], wrow[f], at, p.K);
+                    mma16816<BF16>(d[f], lo, v.x, v.y);
+                    mma16816<BF16>(d[f], hi, v.z, v.w);
+                }
             }
-            __syncthreads();
+        };
+        // The warp's sums so far, to its own place in shared memory: every 64 MMAs (they add with
+        // truncation, see above).
+        bool begun = false;
+        const auto put = [&]() {
+#pragma unroll
+            for (int f = 0; f < FG; ++f)
+#pragma unroll
+                for (int i = 0; i < 2 * XR; ++i) {
+                    float& s = sums[warp][g + 8 * (i >> 1)][8 * f + 2 * tig + (i & 1)];
+                    s = begun ? s + d[f][i] : d[f][i];
+                    d[f][i] = 0.f;
+                }
+            begun = true;
+        };
+        constexpr int kStep = 256 * kAhead, kPut = 64 / (2 * kAhead) / 2 * 2 * kStep;
+        Batch b0, b1;
+        int k = 32 * warp, next = k + kPut;
+        if (k < p.K) load(b0, k);
+        while (k < p.K) {
+            if (k >= next) put(), next += kPut;
+            if (k + kStep < p.K) load(b1, k + kStep);
+            multiply(b0, k);
+            if ((k += kStep) >= p.K) break;
+            if (k + kStep < p.K) load(b0, k + kStep);
+            multiply(b1, k);
+            k += kStep;
         }
+        put();
+        __syncthreads();
+        for (int i = threadIdx.x; i < rows * FG; i += kRowsThreads) {
+            const int r = i / FG, f = i - r * FG, j = j0 + 8 * f, nc = min(8, p.M - j);
+            if (nc <= 0) continue;
+            TailRead<kForward> rd;
+            tail_read<kForward>(p.t, e, r0 + r, j, nc, rd);
+            float v[8] = {};
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+#pragma unroll
+                for (int c = 0; c < 8; ++c) v[c] += sums[q][r][8 * f + c];
+            tail_write<kForward>(p.t, offset, e, r0 + r, j, nc, rd, v);
+        }
+        __syncthreads();
     }
 }
 

@@ -189,11 +189,12 @@ constexpr int kFewSums = 2048;
 
 // Rows up to which the forward product is linear_rows_kernel's: eight at a time; 16 of one
 // weight matrix below 64 MB (4096 x 4096 for 9 rows 9.7 us against 14.1 on the tensor-core tiles,
-// 4096 x 16384 for 16 rows 31 against 25; 32 experts' 2048 x 1024 for 32 rows 24 against 26).  Where the tiles
+// 4096 x 16384 for 16 rows 31 against 25), and 16 of experts.  Where the tiles
 // would need a copy of the weights, 16 of any matrix (12 rows of 8191 x 7168 61 against 75, of 8190 x 8192 39
-// against 84) and 64 of experts with eight each at most on average (20 rows of 4 experts' 3918 x 3840 42
-// against 80, 64 of 16 experts' 2047 x 2048 49 against 78, of 8 experts' 999 x 4000 42 against 46).
-constexpr int kFewRows = 16, kFewCopied = 64;
+// against 84) and 64 of experts with eight each at most on average, which are not known here (20 rows of 4 experts'
+// 3918 x 3840, 5 each, 40 against 80; 64 of 16 experts' 2047 x 2048, 4 each, 49 against 78; of 8 experts' 26 against
+// 45, but if one expert has them all 24 against 18).
+constexpr int kFewRows = 16, kFewCopied = wg::kRowsMost;
 bool few_rows(const wg_linear_problem& q)
 {
     const bool copied = q.ld_in % 8 || q.ld_weight % 8 || (q.experts > 1 && q.weight_stride % 8);
@@ -456,7 +457,8 @@ int lin_run(const LinPlan& pl, const void* offsets, LinOperand a, LinOperand b, 
 template <int XR, int FG, int VEC>
 int rows_launch(const wg::RowsParams& g, bool bf16, cudaStream_t s)
 {
-    const long long items = (long long)std::max(1, std::min<int>(std::max(g.experts, 1), (int)g.tokens)) * ((g.M + 8 * FG - 1) / (8 * FG));
+    const long long passes = std::max(1LL, std::min(g.tokens, std::max(g.experts, 1) + g.tokens / (8 * XR)));  // at most
+    const long long items = passes * ((g.M + 8 * FG - 1) / (8 * FG));
     // (What an SM holds: 4 rows of 16 experts' 1024 x 4096 12.0 us against 12.6 with four times that.)
     const dim3 grid((unsigned)std::min<long long>(items, 2LL * num_sms()));
     return launch("linear_rows_kernel launch", bf16 ? wg::linear_rows_kernel<XR, FG, true, VEC> : wg::linear_rows_kernel<XR, FG, false, VEC>,
@@ -475,6 +477,7 @@ int rows_run(const LinPlan& pl, const void* offsets, const void* x, const void* 
     const bool bf16 = q.in_dtype == WG_BF16, one = q.tokens <= 8 || q.experts > 1;
     const long long used = std::min<long long>(std::max(q.experts, 1), q.tokens);
     const auto many = [&](int columns) { return 2 * ((q.out + columns - 1) / columns) * used >= 3LL * num_sms(); };  // CTAs
+    // Sixteen rows per pass of one weight matrix only (64 of 8 experts', 8 each, 33 us against 26).
     // 32 columns of the result per CTA where those are enough CTAs (8192 x 8192 23.5 us against 24.7
     // with 16, 4096 x 16384 25.1 against 27.4, 8000 rows of 999 9.4 against 11.3), else 16 (4096 x 4096 9.2
     // against 11.7).

@@ -6,7 +6,7 @@ from implicit_gemm_gb300 import binding, build
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from layer_oracle import DT, close, weight  # noqa: E402
+from layer_oracle import DT, close, forward, weight  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -159,3 +159,22 @@ def test_columns_of_one_buffer(tokens, inf, out, pad, dt):
     binding.wg_activation_bwd(sa, v["res"], v["z"], v["y"], bias)
     want[:, at["y"]] = wd
     assert torch.equal(buf, want)
+
+
+@pytest.mark.parametrize("counts,inf,out", [([1] * 64, 261, 40), ([9] * 7, 130, 77), ([64] + [0] * 7, 333, 600), ([0] * 1000 + [33, 0, 31], 65, 24),
+                                            ([16], 264, 72), ([9, 7], 1024, 264), ([0] * 500 + [16], 72, 40), ([8, 0, 8], 4096, 72),
+                                            ([17, 0, 30, 16], 2050, 99), ([0] * 9, 261, 40)])
+def test_few_rows_in_passes(counts, inf, out):
+    """As many passes as there may be, experts of one row more or less than a pass takes."""
+    n = len(counts)
+    off = offsets_of(counts, 0)
+    rows = sum(counts) or 7
+    x, w, bias = randn(1, rows, inf, dt="bf16"), randn(2, n, out, inf, size=inf ** -0.5, dt="bf16"), randn(3, n, out)
+    sp = {"tokens": rows, "in": inf, "out": out, "experts": n}
+    assert "linear_rows" in binding.wg_linear_plan_string(sp)
+    y = torch.full((rows, out), 7.0, dtype=DT["bf16"], device="cuda")
+    binding.linear(x, w, bias, activation="silu", dropout=0.2, seed=3, offset=4, offsets=off, out=y)
+    _, (want, err) = forward(x, w, bias, None, "silu", 0.2, 3, 4, off.tolist())
+    used = slice(0, sum(counts))
+    close(y[used], want[used], err[used], "bf16")
+    assert bool((y[used.stop:] == 7).all())
