@@ -161,9 +161,9 @@ def test_columns_of_one_buffer(tokens, inf, out, pad, dt):
     assert torch.equal(buf, want)
 
 
-@pytest.mark.parametrize("counts,inf,out", [([1] * 64, 261, 40), ([9] * 7, 130, 77), ([64] + [0] * 7, 333, 600), ([0] * 1000 + [33, 0, 31], 65, 24),
+@pytest.mark.parametrize("counts,inf,out", [([1] * 64, 261, 40), ([9] * 7 + [0], 130, 77), ([64] + [0] * 7, 333, 600), ([0] * 1000 + [33, 0, 31], 65, 24),
                                             ([16], 264, 72), ([9, 7], 1024, 264), ([0] * 500 + [16], 72, 40), ([8, 0, 8], 4096, 72),
-                                            ([17, 0, 30, 16], 2050, 99), ([0] * 9, 261, 40)])
+                                            ([17, 0, 30, 16, 0, 0, 0, 0], 2050, 99), ([0] * 9, 261, 40)])
 def test_few_rows_in_passes(counts, inf, out):
     """As many passes as there may be, experts of one row more or less than a pass takes."""
     n = len(counts)
