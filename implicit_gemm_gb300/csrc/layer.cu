@@ -169,7 +169,7 @@ struct LinPlan {
     int M, N, kb;             // columns of the result, rows (weight gradient), 64-wide blocks of the sum
     int bt, split, stages, stage_bytes, pairs;
     bool few;                 // linear_rows_kernel
-    bool chunked;             // sums of several chunks
+    long long chunks;         // of the longest sum (a part's, or an expert's that has every row)
     bool pack_a, pack_b;      // operands that TMA cannot read
     long long part_rows, ldp;
     int sum_rows;             // rows of a partial sum of dbias
@@ -283,8 +283,8 @@ int lin_plan(const wg_linear_problem* p, int call, LinPlan* pl)
             if (t < best - 1e-9) best = t, pl->bt = bt, pl->split = s;
         }
     }
-    // Blocks of the longest sum (a part's, or an expert's that has every row).
-    pl->chunked = ((weight ? (q.tokens + 63) / 64 : pl->kb) + pl->split - 1) / pl->split > lin_chunk(q);
+    const long long blocks = ((weight ? (q.tokens + 63) / 64 : pl->kb) + pl->split - 1) / pl->split;
+    pl->chunks = (blocks + lin_chunk(q) - 1) / lin_chunk(q);
     pl->stage_bytes = wg::kLinABytes + (weight ? (pl->bt > 128 ? 16384 : 8192) : pl->bt * 64);
     pl->stages = std::min(wg::kLinMaxStages, wg::kLinRing / pl->stage_bytes);
 
@@ -381,7 +381,7 @@ int product_launch(const LinPlan& pl, const LinKernels& k, const CUtensorMap& ma
     ++na;
     wg::pdl_config(&cfg, attr, &na, s);
     cfg.gridDim = dim3((unsigned)(2 * g.pairs));
-    cfg.blockDim = dim3(wg::lin_threads(pl.chunked));
+    cfg.blockDim = dim3(wg::lin_threads(pl.chunks > 1));
     cfg.dynamicSmemBytes = wg::kLinSmem;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, k.product, ma, mb, g);
     if (e != cudaSuccess) return cuda_fail("linear_product_kernel launch", e);
@@ -416,9 +416,9 @@ int lin_run(const LinPlan& pl, const void* offsets, LinOperand a, LinOperand b, 
         a.p = b.p = ws, a.ld = b.ld = 8LL * (kMaxFeatures / 8), a.rows = b.rows = 1, a.batch = 1, a.bs = a.ld;  // (never read)
     }
     // Whatever may fail comes before the first launch.
-    const LinKernels kernels = pl.call == WG_LINEAR_FORWARD    ? lin_kernels<wg::kForward>(pl.chunked)
-                               : pl.call == WG_LINEAR_BWD_DATA ? lin_kernels<wg::kData>(pl.chunked)
-                                                               : lin_kernels<wg::kWeight>(pl.chunked);
+    const LinKernels kernels = pl.call == WG_LINEAR_FORWARD    ? lin_kernels<wg::kForward>(pl.chunks > 1)
+                               : pl.call == WG_LINEAR_BWD_DATA ? lin_kernels<wg::kData>(pl.chunks > 1)
+                                                               : lin_kernels<wg::kWeight>(pl.chunks > 1);
     const int bf16 = q.in_dtype == WG_BF16;
     CUtensorMap ma, mb;
     int st = lin_map(&ma, a.p, bf16, a.cols, a.rows, a.batch, a.ld, a.bs, pl.call == WG_LINEAR_FORWARD ? 128 : 64);
@@ -464,27 +464,40 @@ int rows_launch(const wg::RowsParams& g, bool bf16, cudaStream_t s)
     return launch("linear_rows_kernel launch", bf16 ? wg::linear_rows_kernel<XR, FG, true, VEC> : wg::linear_rows_kernel<XR, FG, false, VEC>,
                   grid, dim3(wg::kRowsThreads), s, g);
 }
-int rows_run(const LinPlan& pl, const void* offsets, const void* x, const void* w, const wg::LayerTail& tail, cudaStream_t s)
+// Rows of a pass by eight, columns of a block by eight, elements of an access.
+struct RowsShape {
+    int xr, fg, vec;
+};
+RowsShape rows_shape(const wg_linear_problem& q, const void* x, const void* w)
 {
-    const wg_linear_problem& q = pl.p;
-    wg::RowsParams g = {};
-    g.t = tail, g.experts = q.experts, g.offsets64 = q.offset_bits == 64, g.offsets = offsets, g.tokens = q.tokens;
-    g.x = x, g.w = w, g.ldx = q.ld_in, g.ldw = q.ld_weight, g.wstride = q.weight_stride, g.K = q.in, g.M = q.out;
     const auto rows_of = [&](int v) {
         return q.in % v == 0 && q.ld_in % v == 0 && q.ld_weight % v == 0 && (q.experts <= 1 || q.weight_stride % v == 0) &&
                aligned_to(x, 2 * v) && aligned_to(w, 2 * v);
     };
-    const bool bf16 = q.in_dtype == WG_BF16, one = q.tokens <= 8 || q.experts > 1;
+    const bool one = q.tokens <= 8 || q.experts > 1;
     const long long used = std::min<long long>(std::max(q.experts, 1), q.tokens);
     const auto many = [&](int columns) { return 2 * ((q.out + columns - 1) / columns) * used >= 3LL * num_sms(); };  // CTAs
     // Sixteen rows per pass of one weight matrix only (64 of 8 experts', 8 each, 33 us against 26).
     // 32 columns of the result per CTA where those are enough CTAs (8192 x 8192 23.5 us against 24.7
     // with 16, 4096 x 16384 25.1 against 27.4, 8000 rows of 999 9.4 against 11.3), else 16 (4096 x 4096 9.2
     // against 11.7).
-    if (rows_of(8)) return !one ? rows_launch<2, 2, 8>(g, bf16, s) : many(32) ? rows_launch<1, 4, 8>(g, bf16, s) : rows_launch<1, 2, 8>(g, bf16, s);
-    if (rows_of(2)) return one ? rows_launch<1, 2, 2>(g, bf16, s) : rows_launch<2, 2, 2>(g, bf16, s);
-    if (!one) return rows_launch<2, 2, 1>(g, bf16, s);
-    return many(32) ? rows_launch<1, 4, 1>(g, bf16, s) : many(16) ? rows_launch<1, 2, 1>(g, bf16, s) : rows_launch<1, 1, 1>(g, bf16, s);
+    if (rows_of(8)) return {one ? 1 : 2, one && many(32) ? 4 : 2, 8};
+    if (rows_of(2)) return {one ? 1 : 2, 2, 2};
+    return {one ? 1 : 2, !one ? 2 : many(32) ? 4 : many(16) ? 2 : 1, 1};
+}
+
+int rows_run(const LinPlan& pl, const void* offsets, const void* x, const void* w, const wg::LayerTail& tail, cudaStream_t s)
+{
+    const wg_linear_problem& q = pl.p;
+    wg::RowsParams g = {};
+    g.t = tail, g.experts = q.experts, g.offsets64 = q.offset_bits == 64, g.offsets = offsets, g.tokens = q.tokens;
+    g.x = x, g.w = w, g.ldx = q.ld_in, g.ldw = q.ld_weight, g.wstride = q.weight_stride, g.K = q.in, g.M = q.out;
+    const bool bf16 = q.in_dtype == WG_BF16;
+    const RowsShape h = rows_shape(q, x, w);
+    if (h.vec == 8) return h.xr == 2 ? rows_launch<2, 2, 8>(g, bf16, s) : h.fg == 4 ? rows_launch<1, 4, 8>(g, bf16, s) : rows_launch<1, 2, 8>(g, bf16, s);
+    if (h.vec == 2) return h.xr == 2 ? rows_launch<2, 2, 2>(g, bf16, s) : rows_launch<1, 2, 2>(g, bf16, s);
+    if (h.xr == 2) return rows_launch<2, 2, 1>(g, bf16, s);
+    return h.fg == 4 ? rows_launch<1, 4, 1>(g, bf16, s) : h.fg == 2 ? rows_launch<1, 2, 1>(g, bf16, s) : rows_launch<1, 1, 1>(g, bf16, s);
 }
 
 int lin_offsets(const LinPlan& pl, const void* offsets)
@@ -585,12 +598,13 @@ int wg_linear_plan_string(const wg_linear_problem* p, wg_linear_call call, char*
     const int st = lin_plan(p, call, &pl);
     if (st) return st;
     if (pl.few) {
-        snprintf(buf, n, "kernel=linear_rows call=forward ws=%zu", pl.bytes);
+        const RowsShape h = rows_shape(pl.p, nullptr, nullptr);  // (for bases on 16 bytes)
+        snprintf(buf, n, "kernel=linear_rows call=forward rows=%d columns=%d access=%d ws=%zu", 8 * h.xr, 8 * h.fg, h.vec, pl.bytes);
         return WG_OK;
     }
     static const char* const kNames[3] = {"forward", "bwd_data", "bwd_weight"};
-    snprintf(buf, n, "kernel=linear_product call=%s columns=%d rows=%d split=%d stages=%d pairs=%d pack=%d%d smem=%d ws=%zu",
-             kNames[pl.call], 256, pl.bt, pl.split, pl.stages, pl.pairs, pl.pack_a, pl.pack_b, wg::kLinSmem, pl.bytes);
+    snprintf(buf, n, "kernel=linear_product call=%s columns=%d rows=%d split=%d chunks=%lld stages=%d pairs=%d pack=%d%d smem=%d ws=%zu",
+             kNames[pl.call], 256, pl.bt, pl.split, pl.chunks, pl.stages, pl.pairs, pl.pack_a, pl.pack_b, wg::kLinSmem, pl.bytes);
     return WG_OK;
 }
 

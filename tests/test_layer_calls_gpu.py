@@ -6,7 +6,7 @@ from implicit_gemm_gb300 import binding, build
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from layer_oracle import DT, close, forward, weight  # noqa: E402
+from layer_oracle import DT, HALF, close, data, forward, weight  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -178,3 +178,117 @@ def test_few_rows_in_passes(counts, inf, out):
     used = slice(0, sum(counts))
     close(y[used], want[used], err[used], "bf16")
     assert bool((y[used.stop:] == 7).all())
+
+
+def plan_of(sp, call="forward"):
+    return dict(v.split("=") for v in binding.wg_linear_plan_string(sp, call).split())
+
+
+# Every shape of the few-rows kernel, with more blocks' worth of columns than the GPU holds blocks, and sums longer than the
+# 64 MMAs after which a warp puts its sums away.
+ROWS = [(1, 8456, 9800, "8 32 8"), (8, 8456, 5000, "8 16 8"), (13, 6400, 5000, "16 16 8"), (13, 10248, 3200, "16 16 8"), (3, 8458, 5000, "8 16 2"),
+        (12, 8458, 5000, "16 16 2"), (8, 8457, 9801, "8 32 1"), (5, 8457, 4901, "8 16 1"), (2, 8457, 2500, "8 8 1"),
+        (16, 8457, 5001, "16 16 1"), (9, 264, 9801, "16 16 8"), (1, 257, 9801, "8 32 1"), (2, 200, 8200, "8 32 8")]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("tokens,inf,out,shape", ROWS)
+def test_every_shape_of_few_rows(tokens, inf, out, shape, dt):
+    sp = {"tokens": tokens, "in": inf, "out": out, "in_dtype": dt, "out_dtype": "fp32"}
+    p = plan_of(sp)
+    assert p["kernel"] == "linear_rows" and " ".join((p["rows"], p["columns"], p["access"])) == shape
+    x, w = randn(1, tokens, inf, dt=dt), randn(2, out, inf, size=inf ** -0.5, dt=dt)
+    bias, y = randn(3, out), torch.full((tokens, out), float("nan"), device="cuda")
+    binding.linear(x, w, bias, out=y)
+    _, (want, err) = forward(x, w[None], bias[None])
+    close(y, want, err, "fp32")
+
+
+def test_the_shapes_are_all_there():
+    assert {s for *_, s in ROWS} == {f"{8 * xr} {8 * fg} {v}" for v in (8, 2, 1) for xr, fg in ((1, 1), (1, 2), (1, 4), (2, 2))
+                                     if not (fg == 1 and v > 1) and not (fg == 4 and v == 2)}
+
+
+@pytest.mark.parametrize("counts,inf,out", [([40] * 6, 264, 2600), ([3, 0, 8, 5], 520, 8200), ([1, 2, 0, 4], 1025, 4901)])
+def test_wide_results_of_experts(counts, inf, out):
+    """Experts' few rows by 32 columns a block, and tiles of rows for more."""
+    off, n = offsets_of(counts), len(counts)
+    x, w = randn(1, sum(counts), inf, dt="fp16"), randn(2, n, out, inf, size=inf ** -0.5, dt="fp16")
+    y = binding.linear(x, w, activation="gelu", offsets=off)
+    _, (want, err) = forward(x, w, activation="gelu", offsets=off.tolist())
+    close(y, want, err, "fp16")
+
+
+LONG = [("forward", 2600, 1100, 2600, None), ("forward", 2600, 3100, 2600, None), ("bwd_data", 2600, 2600, 1100, None),
+        ("bwd_data", 2570, 2600, 3130, None), ("bwd_weight", 1100, 2570, 2570, None), ("bwd_weight", 3500, 2568, 2600, None),
+        ("bwd_weight", 7100, 1032, 2056, [1030, 40, 0, 2100, 1024, 1025, 1, 1800]),
+        ("forward", 1800, 2100, 2056, [500, 0, 3, 257, 700, 256]), ("bwd_data", 1800, 2056, 2100, [500, 0, 3, 257, 700, 256])]
+
+
+@pytest.mark.parametrize("call,tokens,inf,out,counts", LONG)
+def test_sums_of_several_chunks_over_more_tiles_than_pairs(call, tokens, inf, out, counts):
+    """fp32 results, whose sums are added up 1024 terms at a time: the buffers of sums and the totals in registers go on
+    from one tile of a pair to the next."""
+    n, off = len(counts) if counts else 1, offsets_of(counts, 4) if counts else None
+    sp = {"tokens": tokens, "in": inf, "out": out, "experts": n if counts else 0, "out_dtype": "fp32"}
+    p = plan_of(sp, call)
+    m, rows = (out, tokens) if call == "forward" else (inf, tokens) if call == "bwd_data" else (inf, n * out)
+    assert p["split"] == "1" and int(p["chunks"]) > 1
+    assert -(-m // 256) * -(-rows // int(p["rows"])) > int(p["pairs"])
+    offs, used = off.tolist() if counts else None, slice(4, 4 + sum(counts)) if counts else slice(0, tokens)
+    x, w, dy = randn(1, tokens, inf, dt="bf16"), randn(2, n, out, inf, size=inf ** -0.5, dt="bf16"), randn(3, tokens, out, dt="bf16")
+    ws = space(sp, call)
+    if call == "forward":
+        y = torch.full((tokens, out), 7.0, device="cuda")
+        binding.wg_linear(sp, x, w, y, offsets=off, workspace=ws)
+        _, (want, err) = forward(x, w, offsets=offs)
+    elif call == "bwd_data":
+        y = torch.full((tokens, inf), 7.0, device="cuda")
+        binding.wg_linear_bwd_data(sp, dy, w, y, offsets=off, workspace=ws)
+        want, err = data(dy, w, offsets=offs)
+    else:
+        y, db = torch.full((n, out, inf), float("nan"), device="cuda"), torch.full((n, out), float("nan"), device="cuda")
+        binding.wg_linear_bwd_weight(sp, x, dy, y, db, offsets=off, workspace=ws)
+        (want, err), (wb, berr) = weight(x, dy, offs, n)
+        close(db, wb, berr, "fp32", "dbias")
+        close(y, want, err, "fp32")
+        return
+    close(y[used], want[used], err[used], "fp32")
+    assert bool((y[:used.start] == 7).all()) and bool((y[used.stop:] == 7).all())
+
+
+@pytest.mark.parametrize("call,tokens,inf,out", [("forward", 1400, 40008, 4100), ("bwd_data", 1400, 4100, 33000),
+                                                 ("bwd_weight", 70000, 2300, 2570)])
+def test_16_bit_results_of_several_chunks(call, tokens, inf, out):
+    """More than 32768 terms to a 16-bit result in whole sums, over more tiles than pairs."""
+    sp = {"tokens": tokens, "in": inf, "out": out, "in_dtype": "fp16", "out_dtype": "fp16"}
+    p = plan_of(sp, call)
+    assert p["split"] == "1" and int(p["chunks"]) > 1
+    ws, size = space(sp, call), {"forward": inf, "bwd_data": out, "bwd_weight": tokens}[call] ** -0.5
+    if call == "bwd_weight":
+        x, dy, y = randn(1, tokens, inf, size=size, dt="fp16"), randn(3, tokens, out, dt="fp16"), torch.empty(1, out, inf, dtype=DT["fp16"], device="cuda")
+        binding.wg_linear_bwd_weight(sp, x, dy, y, workspace=ws)
+        (want, err), _ = weight(x, dy)
+    elif call == "forward":
+        x, w, y = randn(1, tokens, inf, dt="fp16"), randn(2, out, inf, size=size, dt="fp16"), torch.empty(tokens, out, dtype=DT["fp16"], device="cuda")
+        binding.wg_linear(sp, x, w, y, workspace=ws)
+        _, (want, err) = forward(x, w[None])
+    else:
+        dy, w, y = randn(1, tokens, out, dt="fp16"), randn(2, out, inf, size=size, dt="fp16"), torch.empty(tokens, inf, dtype=DT["fp16"], device="cuda")
+        binding.wg_linear_bwd_data(sp, dy, w, y, workspace=ws)
+        want, err = data(dy, w[None])
+    close(y, want, err, "fp16")
+
+
+@pytest.mark.parametrize("tokens,terms,out", [(9, 32768, 264), (1400, 32768, 4100), (1400, 40008, 4100), (700, 1000, 264)])
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+def test_16_bit_sums_of_equal_signs(tokens, terms, out, dt):
+    """What truncation takes of a 16-bit result's sum is at most 2e-4 of it, beside its rounding."""
+    a, b = 1 + 2.0 ** -5, 1 + 2.0 ** -6
+    x, w = torch.full((tokens, terms), a, dtype=DT[dt], device="cuda"), torch.full((out, terms), b, dtype=DT[dt], device="cuda")
+    want = a * b * terms
+    assert want < 65504
+    y = binding.linear(x, w)
+    assert float((y.double() / want - 1).abs().max()) <= 2e-4 + HALF[dt] * (1 + 2e-4)
+    y = binding.linear_bwd_data(x, w.t().contiguous())
+    assert float((y.double() / want - 1).abs().max()) <= 2e-4 + HALF[dt] * (1 + 2e-4)
