@@ -534,7 +534,8 @@ WG_API int wg_linear_plan_string(const wg_linear_problem* p, wg_linear_call call
 /* The three calls on `stream`.  x, w and dy need 16-byte aligned bases where their
  * ld (and, with several experts, weight_stride) is a multiple of 8 elements, else
  * only their elements' alignment (such rows are fetched in the aligned 16 bytes around
- * them); every other tensor only its elements' (16-byte aligned rows are faster);
+ * them; and so may x and w always where wg_linear_plan_string names linear_rows); every other tensor
+ * only its elements' (16-byte aligned rows are faster);
  * workspace 16 bytes, its contents of no use before or after a call: calls whose work may
  * overlap on the GPU, replayed graphs among them, need one each.  residual may be y (or dx) itself, with
  * the same strides; else no output may overlap another tensor of the call (columns of one buffer, side by

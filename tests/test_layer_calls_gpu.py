@@ -6,7 +6,7 @@ from implicit_gemm_gb300 import binding, build
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from layer_oracle import DT, HALF, close, data, forward, weight  # noqa: E402
+from layer_oracle import DT, HALF, close, data, forward, keep_mask, weight  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -292,3 +292,54 @@ def test_16_bit_sums_of_equal_signs(tokens, terms, out, dt):
     assert float((y.double() / want - 1).abs().max()) <= 2e-4 + HALF[dt] * (1 + 2e-4)
     y = binding.linear_bwd_data(x, w.t().contiguous())
     assert float((y.double() / want - 1).abs().max()) <= 2e-4 + HALF[dt] * (1 + 2e-4)
+
+
+@pytest.mark.parametrize("xat,wat", [(0, 0), (1, 0), (0, 2), (2, 6), (4, 3)])
+@pytest.mark.parametrize("tokens,inf,out,counts", [(1, 512, 72, None), (12, 264, 72, None), (11, 64, 40, [3, 0, 8])])
+def test_few_rows_of_aligned_strides_and_other_bases(tokens, inf, out, counts, xat, wat):
+    """Strides of whole 16 bytes from a base that is on none: taken by the few-rows kernel, as the header says."""
+    n, dt = len(counts) if counts else 1, "bf16"
+    xb, wb = torch.full((tokens * inf + 16,), float("nan"), dtype=DT[dt], device="cuda"), torch.full((n * out * inf + 16,), float("nan"), dtype=DT[dt], device="cuda")
+    x, w = xb[xat:xat + tokens * inf].view(tokens, inf), wb[wat:wat + n * out * inf].view(n, out, inf)
+    x.copy_(randn(1, tokens, inf, dt=dt))
+    w.copy_(randn(2, n, out, inf, size=inf ** -0.5, dt=dt))
+    off = offsets_of(counts) if counts else None
+    sp = {"tokens": tokens, "in": inf, "out": out, "experts": n if counts else 0, "out_dtype": "fp32"}
+    assert plan_of(sp)["kernel"] == "linear_rows"
+    y = torch.empty(tokens, out, device="cuda")
+    binding.wg_linear(sp, x, w, y, offsets=off, workspace=space(sp, "forward"))
+    _, (want, err) = forward(x, w, offsets=off.tolist() if counts else None)
+    close(y, want, err, "fp32")
+
+
+@pytest.mark.parametrize("kind", ["few", "tiles", "cut", "data", "activation", "gradient"])
+def test_a_mask_of_a_counter_at_every_replay(kind):
+    """Captured calls whose counter lies in device memory draw the mask of offset + counter, past 2^32 too."""
+    t, a, b = (5, 72, 40) if kind == "few" else (20, 4096, 264) if kind == "cut" else (300, 136, 264)
+    counter = torch.zeros(1, dtype=torch.int64, device="cuda")
+    x, w = torch.ones(t, a, dtype=DT["bf16"], device="cuda"), torch.full((b, a), 1 / a, dtype=DT["bf16"], device="cuda")
+    dims = (t, a) if kind in ("data", "activation", "gradient") else (t, b)
+    y = torch.empty(dims, dtype=DT["bf16"], device="cuda")
+    kw = {"dropout": 0.5, "seed": 11, "offset": (1 << 32) - 3, "counter": counter}
+    if kind in ("activation", "gradient"):
+        sp = {"tokens": t, "dim": a, **kw}
+        call = binding.PreparedActivation(sp, x, y) if kind == "activation" else binding.PreparedActivationBwd(sp, x, None, y)
+    elif kind == "data":
+        sp = {"tokens": t, "in": a, "out": b, **kw}
+        call = binding.PreparedLinearBwdData(sp, torch.ones(t, b, dtype=DT["bf16"], device="cuda"), w, y, workspace=space(sp, "bwd_data"))
+    else:
+        sp = {"tokens": t, "in": a, "out": b, **kw}
+        assert (plan_of(sp)["kernel"] == "linear_rows") == (kind == "few") and (plan_of(sp).get("split", "1") != "1") == (kind == "cut")
+        call = binding.PreparedLinear(sp, x, w, y, workspace=space(sp, "forward"))
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(torch.cuda.current_stream().cuda_stream)
+        counter += 2
+    counter.zero_()
+    for i in range(4):
+        g.replay()
+        torch.cuda.synchronize()
+        mask, _ = keep_mask(11, (1 << 32) - 3 + 2 * i, *dims, 0.5)
+        assert torch.equal((y != 0).cpu(), mask)
