@@ -27,11 +27,12 @@
 // NaN), by a warp of their own in each CTA, which then hands the block to the MMA warp.
 //
 // What bounds it: of long sums the MMAs, at the rate of a large library product (a block of 64
-// of a 256 x 256 tile 0.31 us on 76 pairs; the bare product of 8192 x 4096 to 16384 544 us alone; with gelu_tanh and z, on inputs
-// that change from call to call, 680 at the power cap); of few rows the weights' bytes (24 rows of 4096 to 16384 25 us, 5.4 TB/s); of sums below some 16 to 60 blocks the epilogue's
-// instructions (15 a result, 24 with silu, 30 with dropout, 44 with gelu and dropout), experts' weight
-// gradients among them (64 of 4096 x 2048, 256 rows each, to bf16 337 us, 353 with dbias, where their 1.3 GB are 190); of
-// small problems some 7 us from launch to end.
+// of a 256 x 256 tile 0.31 us on 76 pairs; the bare product of 8192 x 4096 to 16384 544 us alone; with
+// gelu_tanh and z, on inputs that change from call to call, 680 at the power cap); of few rows the
+// weights' bytes (24 rows of 4096 to 16384 25 us, 5.4 TB/s); of sums below some 16 to 60 blocks the
+// epilogue's instructions (15 a result, 24 with silu, 30 with dropout, 44 with gelu and dropout), experts'
+// weight gradients among them (64 of 4096 x 2048, 16384 rows in all, to bf16 337 us, 353 with dbias, where
+// their 1.3 GB are 190); of small problems some 7 us from launch to end.
 //
 // Where there are fewer tiles than pairs the sum is cut into `split` parts, whose fp32
 // sums go through the workspace to linear_join_kernel, in the order of the parts.
@@ -472,6 +473,7 @@ __global__ void __launch_bounds__(lin_threads(CHUNKED), 1)
             }
             __syncwarp();
         } else if (warp == 1) {
+            if (!p.experts) pdl_wait();  // (the waits below are bounded, and the kernel before may take longer)
             if (rank == 0) {
                 const uint32_t sbase = smem_u32(smem);
                 const uint64_t ad = make_sdesc(sbase, kAmn ? 8192u : 16u, 1024u, 2u, 0u);
@@ -516,6 +518,7 @@ __global__ void __launch_bounds__(lin_threads(CHUNKED), 1)
             }
         } else if (warp == 2) {
             if (KIND == kWeight) {
+                if (!p.experts) pdl_wait();
                 // Rows of an expert's last block that are the next one's become zeros.  (A row is
                 // one line of 128 bytes per 64 columns, whatever the swizzle does within it.)
                 const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0u);

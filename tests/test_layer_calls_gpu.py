@@ -343,3 +343,48 @@ def test_a_mask_of_a_counter_at_every_replay(kind):
         torch.cuda.synchronize()
         mask, _ = keep_mask(11, (1 << 32) - 3 + 2 * i, *dims, 0.5)
         assert torch.equal((y != 0).cpu(), mask)
+
+
+@pytest.mark.parametrize("kind", ["forward", "bwd_data", "bwd_weight"])
+def test_products_behind_calls_that_take_long(kind):
+    """Weight gradients on one CTA each, seconds in all, that let the next kernel start early: a product that has started
+    waits for them however long they take (its bounded waits are for its own copies and products only)."""
+    n, width = 64, 1 << 20
+    conv = {"ndim": 1, "G": 1, "N": n, "C": 8, "K": 8, "in": [width], "filt": [1]}
+    assert "grid=(1,1,1)" in binding.wg_plan_string(conv, 1, "direct")
+    cx, cy = (torch.ones(n * width * 8, dtype=DT["bf16"], device="cuda") for _ in range(2))
+    cw = torch.empty(64, device="cuda")
+
+    def run():
+        binding.wg_conv_bwd_weight(conv, cx, cy, cw, 1, "direct")
+    t, a, b = 300, 264, 136
+    x, w, dy = randn(1, t, a, dt="bf16"), randn(2, b, a, size=a ** -0.5, dt="bf16"), randn(3, t, b, dt="bf16")
+    sp = {"tokens": t, "in": a, "out": b, "out_dtype": "fp32"}
+    shape = {"forward": (t, b), "bwd_data": (t, a), "bwd_weight": (b, a)}[kind]
+    y, db, ws = torch.empty(shape, device="cuda"), torch.empty(b, device="cuda"), space(sp, kind)
+    call = {"forward": lambda: binding.PreparedLinear(sp, x, w, y, workspace=ws), "bwd_data": lambda: binding.PreparedLinearBwdData(sp, dy, w, y, workspace=ws),
+            "bwd_weight": lambda: binding.PreparedLinearBwdWeight(sp, x, dy, y, db, workspace=ws)}[kind]()
+    ends = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    run()
+    ends[0].record()
+    run()
+    ends[1].record()
+    torch.cuda.synchronize()
+    count = int(2600 / ends[0].elapsed_time(ends[1])) + 1
+    ends[0].record()
+    for _ in range(count):
+        run()
+    call(torch.cuda.current_stream().cuda_stream)
+    ends[1].record()
+    torch.cuda.synchronize()
+    assert ends[0].elapsed_time(ends[1]) > 2200
+    binding.wg_check_status()
+    if kind == "forward":
+        _, (want, err) = forward(x, w[None])
+    elif kind == "bwd_data":
+        want, err = data(dy, w[None])
+    else:
+        (want, err), (wb, berr) = weight(x, dy)
+        want, err = want[0], err[0]
+        close(db, wb[0], berr[0], "fp32", "dbias")
+    close(y, want, err, "fp32")
